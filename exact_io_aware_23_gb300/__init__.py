@@ -9,6 +9,7 @@ fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Tuple
 
@@ -16,7 +17,8 @@ import torch
 
 __all__ = ["forward", "forward_splitkv", "backward", "backward_noalloc", "backward_workspace_size",
            "backward_fused_workspace_size", "check_device_status", "set_fault_injection",
-           "set_wait_limit_ms", "FaError", "LIB_PATH", "lib"]
+           "set_wait_limit_ms", "FaError", "LIB_PATH", "lib", "rotary", "rotary_backward",
+           "rotary_frequencies", "append_paged", "forward_paged", "forward_paged_workspace_size"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa.so")
 
@@ -28,6 +30,22 @@ _DTYPES = {torch.bfloat16: FA_BF16, torch.float32: FA_FP32, torch.float16: FA_FP
 class FaDropout(ctypes.Structure):
     """fa_dropout: dropout probability, generator key and counter offset."""
     _fields_ = [("p", ctypes.c_float), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint32)]
+
+
+class FaScoreMod(ctypes.Structure):
+    """fa_score_mod: cap of the scores, distance slopes and prefix lengths (device pointers)."""
+    _fields_ = [("softcap", ctypes.c_float), ("alibi_slopes", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p)]
+
+
+class FaPagedCache(ctypes.Structure):
+    """fa_paged_cache: where a paged cache's keys and values lie."""
+    _fields_ = [("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int),
+                ("kv_lens", ctypes.c_void_p)]
 
 
 class FaError(RuntimeError):
@@ -101,6 +119,18 @@ def _load() -> ctypes.CDLL:
     L.fa_backward_noalloc.restype = i
     L.fa_backward_noalloc_max_workspace.argtypes = []
     L.fa_backward_noalloc_max_workspace.restype = sz
+    st3, i64 = ctypes.c_int64 * 3, ctypes.c_int64
+    L.fa_rotary.argtypes = [vp, st3, vp, st3, i, i, i, i, vp, i64, vp, i, i, f, i, vp]
+    L.fa_rotary.restype = i
+    L.fa_rotary_backward.argtypes = L.fa_rotary.argtypes
+    L.fa_rotary_backward.restype = i
+    cp, mp = ctypes.POINTER(FaPagedCache), ctypes.POINTER(FaScoreMod)
+    L.fa_append_paged.argtypes = [cp, vp, st3, vp, st3, vp, st3, vp, i, i, i, i, i, vp, vp, i, i, f, i, vp]
+    L.fa_append_paged.restype = i
+    L.fa_forward_paged_workspace_size.argtypes = [i, i, i, i, i]
+    L.fa_forward_paged_workspace_size.restype = sz
+    L.fa_forward_paged.argtypes = [vp, cp, vp, vp, i, i, i, i, i, f, vp, mp, i, vp, sz, vp]
+    L.fa_forward_paged.restype = i
     return L
 
 
@@ -396,3 +426,287 @@ def backward_noalloc(q, k, v, o, lse, do, *, causal: bool = False, scale: Option
 
 def noalloc_max_workspace() -> int:
     return int(lib.fa_backward_noalloc_max_workspace())
+
+
+# ---- rotary positions and the paged cache ----------------------------------------------------------
+
+_STRIDES = ctypes.c_int64 * 3
+
+
+def _here(name: str, t: torch.Tensor) -> None:
+    """The library launches on the current device: its tensors have to be there."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _keep(stream, *tensors) -> None:
+    """Memory allocated here is not reused before a call on another stream has read it."""
+    if stream is not None and stream != torch.cuda.current_stream():
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _heads_last(name: str, t: torch.Tensor, dtype, shape) -> "ctypes.Array":
+    """Strides (batch, head, token) of a [B, heads, N, d] tensor whose last axis adjoins."""
+    _here(name, t)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {list(shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the values of a head must adjoin in {name}")
+    return _STRIDES(t.stride(0), t.stride(1), t.stride(2))
+
+
+def _int32(name: str, t: torch.Tensor, shape) -> None:
+    _here(name, t)
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
+
+
+def _frequencies(inv_freq: Optional[torch.Tensor]) -> int:
+    """The rotated values of a head (0: none)."""
+    if inv_freq is None:
+        return 0
+    _here("inv_freq", inv_freq)
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 [rotary_dim / 2] tensor")
+    return 2 * inv_freq.numel()
+
+
+def _written(name: str, t: torch.Tensor) -> None:
+    if any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride())):
+        raise ValueError(f"{name} is written: its elements must not share memory")
+
+
+def _span(t: torch.Tensor) -> Tuple[int, int]:
+    """The bytes a tensor lies in."""
+    last = sum((n - 1) * st for n, st in zip(t.shape, t.stride())) if t.numel() else -1
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def _apart(a: str, x: torch.Tensor, b: str, y: torch.Tensor, same: bool) -> None:
+    """x may be y itself (``same``); otherwise the two must not share memory."""
+    if same and x.data_ptr() == y.data_ptr() and x.stride() == y.stride():
+        return
+    (x0, x1), (y0, y1) = _span(x), _span(y)
+    if x0 < y1 and y0 < x1:
+        raise ValueError(f"{a} and {b} overlap")
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, factor: float = 1.0,
+                       method: str = "linear", trained_len: Optional[int] = None,
+                       fast: float = 32.0, slow: float = 1.0, device="cuda") -> Tuple[torch.Tensor, float]:
+    """inv_freq (float64 [rotary_dim / 2], radians per position) and mscale for ``rotary``:
+    base ** (-2 p / rotary_dim), stretched for contexts ``factor`` times longer by one of
+      "linear"  every frequency divided by the factor (positions interpolated);
+      "ntk"     the base raised by factor ** (rotary_dim / (rotary_dim - 2)): the slowest pair is
+                divided by the factor, the fastest kept;
+      "ramp"    pairs that turn more than ``fast`` times in ``trained_len`` positions kept, those
+                that turn less than ``slow`` times divided by the factor, a linear ramp between,
+                and mscale = 0.1 ln(factor) + 1."""
+    if rotary_dim <= 0 or rotary_dim % 2 != 0:
+        raise ValueError("rotary_dim must be positive and even")
+    if not base > 0.0 or not factor >= 1.0:
+        raise ValueError("base must be positive and factor at least 1")
+    p = torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim
+    mscale = 1.0
+    if method == "ntk":
+        if rotary_dim > 2:
+            base = base * factor ** (rotary_dim / (rotary_dim - 2))
+        inv = base ** -p
+    elif method == "linear":
+        inv = base ** -p / factor
+    elif method == "ramp":
+        if trained_len is None or trained_len <= 0 or not fast > slow:
+            raise ValueError("the ramp needs trained_len > 0 and fast > slow")
+        inv = base ** -p
+        keep = ((trained_len * inv / (2.0 * math.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
+        inv = inv * keep + inv / factor * (1.0 - keep)
+        mscale = 0.1 * math.log(factor) + 1.0
+    else:
+        raise ValueError(f"unknown method {method!r}")
+    return inv.to(device), mscale
+
+
+def _rotary(fn, where, x, positions, inv_freq, interleaved, mscale, out, stream):
+    if x.dim() not in (3, 4):
+        raise ValueError("x must be [B, H, N, d] or [H, N, d]")
+    x4 = x if x.dim() == 4 else x.unsqueeze(0)
+    B, H, N, d = x4.shape
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    xs = _heads_last("x", x4, x.dtype, x4.shape)
+    rot = _frequencies(inv_freq)
+    per_batch = positions.dim() == 2
+    _int32("positions", positions, (B, N) if per_batch else (N,))
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        _keep(stream, out)
+    else:
+        if out.shape != x.shape:
+            raise ValueError("out must have x's shape")
+        _written("out", out)
+        _apart("x", x, "out", out, True)
+    y4 = out if out.dim() == 4 else out.unsqueeze(0)
+    ys = _heads_last("out", y4, x.dtype, x4.shape)
+    st = fn(x.data_ptr(), xs, out.data_ptr(), ys, B, H, N, d, positions.data_ptr(), N if per_batch else 0,
+            inv_freq.data_ptr(), rot, int(bool(interleaved)), float(mscale), _DTYPES[x.dtype], _stream(stream))
+    if st != FA_OK:
+        raise FaError(st, where)
+    return out
+
+
+def rotary(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *, interleaved: bool = False,
+           mscale: float = 1.0, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """fa_rotary: x with the first 2 * inv_freq.numel() values of every head turned by their
+    positions.  x: [B, H, N, d] or packed [H, total, d], any strides whose last axis adjoins (a
+    projection's [B, N, H, d] seen as [B, H, N, d], say); positions: int32 [N] or [B, N]; inv_freq:
+    float64, from ``rotary_frequencies``; out: a new contiguous tensor, or given (x itself for a
+    rotation in place).  bf16, fp16 or fp32."""
+    return _rotary(lib.fa_rotary, "fa_rotary", x, positions, inv_freq, interleaved, mscale, out, stream)
+
+
+def rotary_backward(dy: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *,
+                    interleaved: bool = False, mscale: float = 1.0,
+                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """fa_rotary_backward: the gradient of ``rotary``'s input, given that of its output."""
+    return _rotary(lib.fa_rotary_backward, "fa_rotary_backward", dy, positions, inv_freq, interleaved,
+                   mscale, out, stream)
+
+
+def _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, dtype) -> FaPagedCache:
+    """Checks a paged cache ([n_pages, Hkv, page_size, d], any strides) and says where it lies."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _here(name, t)
+        if t.dim() != 4 or t.dtype != dtype or t.shape[1] != Hkv or t.shape[3] != d:
+            raise ValueError(f"{name} must be {dtype} [n_pages, {Hkv}, page_size, {d}]")
+        if t.stride(3) != 1:
+            raise ValueError(f"the values of a head must adjoin in {name}")
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    _here("block_table", block_table)
+    if (block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B
+            or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
+        raise ValueError(f"block_table must be int32 [{B}, max_pages], a row's entries adjoining")
+    _int32("kv_lens", kv_lens, (B,))
+    n_pages, _, page_size, _ = k_cache.shape
+    s0, s1, s2, _ = k_cache.stride()
+    width = block_table.shape[1]
+    return FaPagedCache(k_cache.data_ptr(), v_cache.data_ptr(), s0, s1, s2, n_pages, page_size,
+                        block_table.data_ptr(), max(block_table.stride(0), width), width, kv_lens.data_ptr())
+
+
+def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 block_table: torch.Tensor, kv_lens: torch.Tensor, *, q: Optional[torch.Tensor] = None,
+                 q_lens: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None,
+                 interleaved: bool = False, mscale: float = 1.0, q_out: Optional[torch.Tensor] = None,
+                 stream=None) -> Optional[torch.Tensor]:
+    """fa_append_paged: writes new tokens k, v [B, Hkv, T, d] into the pages, keys rotated when
+    inv_freq is given, and returns the rotated queries [B, H, T, d] when q is.  kv_lens (int32 [B])
+    counts the new tokens already; q_lens (int32 [B]) says how many of the T are real (default all).
+    k_cache, v_cache: [n_pages, Hkv, page_size, d], any strides whose last axis adjoins;
+    block_table: int32 [B, max_pages]."""
+    if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("k must be bf16 or fp16 [B, Hkv, T, d]")
+    B, Hkv, T, d = k.shape
+    ks = _heads_last("k", k, k.dtype, k.shape)
+    vs = _heads_last("v", v, k.dtype, k.shape)
+    cache = _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, k.dtype)
+    _written("k_cache", k_cache)
+    rot = _frequencies(inv_freq)
+    if q_lens is not None:
+        _int32("q_lens", q_lens, (B,))
+    H, qs = Hkv, None
+    if q is not None:
+        H = q.shape[1] if q.dim() == 4 else 0
+        if Hkv == 0 or H % Hkv != 0 or H == 0:
+            raise ValueError("k, v must be [B, Hkv, T, d] with Hkv dividing the query heads")
+        qs = _heads_last("q", q, k.dtype, (B, H, T, d))
+        if q_out is None:
+            q_out = torch.empty((B, H, T, d), dtype=q.dtype, device=q.device)
+            _keep(stream, q_out)
+        else:
+            if q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
+                raise ValueError("q_out must be contiguous, of q's shape and type")
+            _here("q_out", q_out)
+            _apart("q", q, "q_out", q_out, True)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    st = lib.fa_append_paged(ctypes.byref(cache), k.data_ptr(), ks, v.data_ptr(), vs,
+                             None if q is None else q.data_ptr(), _STRIDES() if qs is None else qs,
+                             None if q_out is None else q_out.data_ptr(), B, H, Hkv, T, d,
+                             None if q_lens is None else q_lens.data_ptr(),
+                             None if inv_freq is None else inv_freq.data_ptr(), rot,
+                             int(bool(interleaved)), float(mscale), _DTYPES[k.dtype], _stream(stream))
+    if st != FA_OK:
+        raise FaError(st, "fa_append_paged")
+    return q_out
+
+
+def forward_paged_workspace_size(B: int, H: int, Hkv: int, T: int, d: int) -> int:
+    return int(lib.fa_forward_paged_workspace_size(B, H, Hkv, T, d))
+
+
+def _score_mod(softcap, alibi_slopes, prefix_lens, H, n_seqs) -> FaScoreMod:
+    """Checks the score arguments; slopes fp32 [H], prefix lengths int32 [n_seqs]."""
+    if alibi_slopes is not None:
+        _here("alibi_slopes", alibi_slopes)
+        if (alibi_slopes.dtype != torch.float32 or tuple(alibi_slopes.shape) != (H,)
+                or not alibi_slopes.is_contiguous()):
+            raise ValueError(f"alibi_slopes must be a contiguous float32 [{H}] tensor")
+    if prefix_lens is not None:
+        _int32("prefix_lens", prefix_lens, (n_seqs,))
+    return FaScoreMod(float(softcap), None if alibi_slopes is None else alibi_slopes.data_ptr(),
+                      None if prefix_lens is None else prefix_lens.data_ptr())
+
+
+def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                  kv_lens: torch.Tensor, *, scale: Optional[float] = None,
+                  q_lens: Optional[torch.Tensor] = None, softcap: float = 0.0,
+                  alibi_slopes: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
+                  lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """O, LSE of T new tokens per sequence over a paged cache that holds them (fa_forward_paged).
+    q: [B, H, T, d] contiguous, bf16 or fp16; the cache, block_table, kv_lens and q_lens as in
+    ``append_paged``.  Token t of a sequence's n new ones sees the keys up to its own place
+    kv_lens - n + t; scores capped by softcap * tanh(. / softcap) when softcap > 0 and lowered by
+    alibi_slopes[h] (fp32 [H]) times the distance."""
+    _here("q", q)
+    if q.dim() != 4 or q.dtype not in (torch.bfloat16, torch.float16) or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 or fp16 [B, H, T, d] tensor")
+    B, H, T, d = q.shape
+    Hkv = k_cache.shape[1] if k_cache.dim() == 4 else 0
+    if Hkv == 0 or H % Hkv != 0:
+        raise ValueError("k_cache must be [n_pages, Hkv, page_size, d] with Hkv dividing the query heads")
+    cache = _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, q.dtype)
+    if q_lens is not None:
+        _int32("q_lens", q_lens, (B,))
+    mod = _score_mod(softcap, alibi_slopes, None, H, B)
+    scale = 1.0 / d ** 0.5 if scale is None else float(scale)
+    if o is None:
+        o = torch.empty((B, H, T, d), dtype=q.dtype, device=q.device)
+        _keep(stream, o)
+    else:
+        if o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous():
+            raise ValueError("o must be contiguous, of q's shape and type")
+        _here("o", o)
+        _apart("q", q, "o", o, False)
+    if lse is None:
+        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
+        _keep(stream, lse)
+    else:
+        if tuple(lse.shape) != (B, H, T) or lse.dtype != torch.float32 or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous float32 [B, H, T]")
+        _here("lse", lse)
+    if workspace is None:
+        need = forward_paged_workspace_size(B, H, Hkv, T, d)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        _keep(stream, workspace)
+    st = lib.fa_forward_paged(q.data_ptr(), ctypes.byref(cache), o.data_ptr(), lse.data_ptr(), B, H, Hkv, T, d,
+                              scale, None if q_lens is None else q_lens.data_ptr(), ctypes.byref(mod),
+                              _DTYPES[q.dtype], workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), _stream(stream))
+    if st != FA_OK:
+        raise FaError(st, "fa_forward_paged")
+    return o, lse

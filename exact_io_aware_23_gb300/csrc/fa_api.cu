@@ -7,6 +7,7 @@
 #include <atomic>
 
 #include "fa_internal.cuh"
+#include "fa_paged.cuh"
 #include "fa_sm103.cuh"
 
 namespace {
@@ -19,13 +20,7 @@ fa::SymbolCache g_err_cache;
 std::atomic<int> g_inject{0};
 std::atomic<uint32_t> g_wait_limit_ms{2000};
 
-// The error word of the current context (looked up once per context).
-fa_status device_error_word(int** out) {
-  void* p = nullptr;
-  if (fa::symbol_address(g_err_cache, (const void*)&g_fa_error_word, &p) != cudaSuccess) return FA_ERR_CUDA;
-  *out = static_cast<int*>(p);
-  return FA_OK;
-}
+using fa::device_error_word;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -63,6 +58,18 @@ fa::DebugKnobs knobs() {
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 }  // namespace
+
+namespace fa {
+
+// The error word of the current context (looked up once per context).
+fa_status device_error_word(int** out) {
+  void* p = nullptr;
+  if (symbol_address(g_err_cache, (const void*)&g_fa_error_word, &p) != cudaSuccess) return FA_ERR_CUDA;
+  *out = static_cast<int*>(p);
+  return FA_OK;
+}
+
+}  // namespace fa
 
 extern "C" {
 

@@ -1,0 +1,186 @@
+// C-ABI layer of the rotary, cache-write and paged-attention calls: argument checks and launches.
+// See include/fa.h for the contract.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "fa_paged.cuh"
+#include "fa_sm103.cuh"
+
+namespace {
+
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Sizes every call here shares.  Tokens and heads stay below 2^31 in all, so that a grid and the
+// row numbers fit.
+fa_status check_sizes(int B, int H, int Hkv, int N, int d) {
+  if (B < 0 || H < 0 || N < 0 || Hkv < 0 || (H > 0 && Hkv == 0)) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (H > 65535 || Hkv > 65535 || B > 65535) return FA_ERR_UNSUPPORTED;
+  if (H > 0 && (Hkv > H || H % Hkv != 0)) return FA_ERR_UNSUPPORTED;
+  if ((int64_t)B * (H > 0 ? H : 1) * N > 0x7fffffff) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+// 16-byte accesses: every stride that is stepped over keeps the alignment.
+bool strides_ok(const int64_t* s, int B, int H, int N, int size) {
+  if (s == nullptr) return false;
+  const int64_t unit = 16 / size;
+  return (B <= 1 || s[0] % unit == 0) && (H <= 1 || s[1] % unit == 0) && (N <= 1 || s[2] % unit == 0);
+}
+
+fa::Strides strides(const int64_t* s) { return fa::Strides{s[0], s[1], s[2]}; }
+
+fa_status check_rotation(const double* inv_freq, int rotary_dim, float mscale, int d) {
+  if (rotary_dim < 0) return FA_ERR_INVALID_ARG;
+  if (rotary_dim > d || rotary_dim % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if (rotary_dim > 0 && (inv_freq == nullptr || !aligned(inv_freq, 8) || !isfinite(mscale))) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+fa_status check_cache(const fa_paged_cache* c, int Hkv) {
+  if (c == nullptr) return FA_ERR_INVALID_ARG;
+  if (c->n_pages < 0 || c->max_pages < 0 || c->page_size <= 0) return FA_ERR_INVALID_ARG;
+  if (c->page_size % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if (!c->k_cache || !c->v_cache || !c->block_table || !c->kv_lens) return FA_ERR_INVALID_ARG;
+  if (!aligned(c->k_cache, 16) || !aligned(c->v_cache, 16) || !aligned(c->block_table, 4) || !aligned(c->kv_lens, 4))
+    return FA_ERR_INVALID_ARG;
+  if (c->token_stride % 8 != 0 || (c->n_pages > 1 && c->page_stride % 8 != 0) || (Hkv > 1 && c->head_stride % 8 != 0))
+    return FA_ERR_INVALID_ARG;
+  if (c->table_stride < c->max_pages) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+fa::PagedCache cache_args(const fa_paged_cache* c) {
+  fa::PagedCache p{};
+  p.k = c->k_cache;
+  p.v = c->v_cache;
+  p.page_stride = c->page_stride;
+  p.head_stride = c->head_stride;
+  p.token_stride = c->token_stride;
+  p.n_pages = c->n_pages;
+  p.page_size = c->page_size;
+  p.table = c->block_table;
+  p.table_stride = c->table_stride;
+  p.max_pages = c->max_pages;
+  p.kv_lens = c->kv_lens;
+  return p;
+}
+
+fa_status rotary_impl(const void* x, const int64_t* xs, void* y, const int64_t* ys, int B, int H, int N, int d,
+                      const int32_t* positions, int64_t position_stride, const double* inv_freq,
+                      int rotary_dim, int interleaved, float mscale, float sign, fa_dtype dtype, void* stream) {
+  fa_status st = check_sizes(B, H, H, N, d);
+  if (st != FA_OK) return st;
+  if (dtype != FA_BF16 && dtype != FA_FP16 && dtype != FA_FP32) return FA_ERR_UNSUPPORTED;
+  st = check_rotation(inv_freq, rotary_dim, mscale, d);
+  if (st != FA_OK) return st;
+  if (B == 0 || H == 0 || N == 0) return FA_OK;
+  const int size = dtype == FA_FP32 ? 4 : 2;
+  if (!x || !y || !positions || !aligned(x, 16) || !aligned(y, 16) || !aligned(positions, 4)) return FA_ERR_INVALID_ARG;
+  if (!strides_ok(xs, B, H, N, size) || !strides_ok(ys, B, H, N, size) || position_stride < 0) return FA_ERR_INVALID_ARG;
+  fa::RotaryArgs a{};
+  a.x = x;
+  a.y = y;
+  a.xs = strides(xs);
+  a.ys = strides(ys);
+  a.B = B; a.H = H; a.N = N; a.d = d;
+  a.positions = positions;
+  a.pos_stride = position_stride;
+  a.rot = fa::Rotation{inv_freq, rotary_dim, interleaved != 0, mscale, sign};
+  return fa::launch_rotary(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_rotary(const void* x, const int64_t x_strides[3], void* y, const int64_t y_strides[3], int B, int H,
+                    int N, int d, const int32_t* positions, int64_t position_stride, const double* inv_freq,
+                    int rotary_dim, int interleaved, float mscale, fa_dtype dtype, void* stream) {
+  return rotary_impl(x, x_strides, y, y_strides, B, H, N, d, positions, position_stride, inv_freq, rotary_dim,
+                     interleaved, mscale, 1.f, dtype, stream);
+}
+
+fa_status fa_rotary_backward(const void* dy, const int64_t dy_strides[3], void* dx, const int64_t dx_strides[3],
+                             int B, int H, int N, int d, const int32_t* positions, int64_t position_stride,
+                             const double* inv_freq, int rotary_dim, int interleaved, float mscale,
+                             fa_dtype dtype, void* stream) {
+  return rotary_impl(dy, dy_strides, dx, dx_strides, B, H, N, d, positions, position_stride, inv_freq,
+                     rotary_dim, interleaved, mscale, -1.f, dtype, stream);
+}
+
+fa_status fa_append_paged(const fa_paged_cache* cache, const void* k, const int64_t k_strides[3], const void* v,
+                          const int64_t v_strides[3], const void* q, const int64_t q_strides[3], void* q_out,
+                          int B, int H, int Hkv, int T, int d, const int32_t* q_lens, const double* inv_freq,
+                          int rotary_dim, int interleaved, float mscale, fa_dtype dtype, void* stream) {
+  fa_status st = check_sizes(B, H, Hkv, T, d);
+  if (st != FA_OK) return st;
+  if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
+  st = check_rotation(inv_freq, rotary_dim, mscale, d);
+  if (st != FA_OK) return st;
+  st = check_cache(cache, Hkv);
+  if (st != FA_OK) return st;
+  if (B == 0 || H == 0 || T == 0) return FA_OK;
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_lens, 4)) return FA_ERR_INVALID_ARG;
+  if (!strides_ok(k_strides, B, Hkv, T, 2) || !strides_ok(v_strides, B, Hkv, T, 2)) return FA_ERR_INVALID_ARG;
+  if (q != nullptr && (!q_out || !aligned(q, 16) || !aligned(q_out, 16) || !strides_ok(q_strides, B, H, T, 2)))
+    return FA_ERR_INVALID_ARG;
+  fa::AppendArgs a{};
+  a.cache = cache_args(cache);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out = q_out;
+  if (q != nullptr) a.qs = strides(q_strides);
+  a.ks = strides(k_strides);
+  a.vs = strides(v_strides);
+  a.B = B; a.H = H; a.Hkv = Hkv; a.T = T; a.d = d;
+  a.q_lens = q_lens;
+  a.rot = fa::Rotation{inv_freq, rotary_dim, interleaved != 0, mscale, 1.f};
+  if (fa::device_error_word(&a.err) != FA_OK) return FA_ERR_CUDA;
+  return fa::launch_append(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_forward_paged_workspace_size(int B, int H, int Hkv, int T, int d) {
+  if (check_sizes(B, H, Hkv, T, d) != FA_OK || B == 0 || H == 0 || T == 0) return 0;
+  return (fa::paged_workspace(d) + 255) / 256 * 256;
+}
+
+fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, float* lse, int B, int H, int Hkv,
+                           int T, int d, float scale, const int32_t* q_lens, const fa_score_mod* score,
+                           fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  fa_status st = check_sizes(B, H, Hkv, T, d);
+  if (st != FA_OK) return st;
+  if (!isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+  if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
+  if (score != nullptr) {
+    if (!isfinite(score->softcap) || score->softcap < 0.f || !aligned(score->alibi_slopes, 4)) return FA_ERR_INVALID_ARG;
+    if (score->prefix_lens != nullptr) return FA_ERR_UNSUPPORTED;
+  }
+  st = check_cache(cache, Hkv);
+  if (st != FA_OK) return st;
+  if (B == 0 || H == 0 || T == 0) return FA_OK;
+  if (!q || !o || !lse || !workspace || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(q_lens, 4))
+    return FA_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256) || workspace_bytes < fa_forward_paged_workspace_size(B, H, Hkv, T, d))
+    return FA_ERR_INVALID_ARG;
+  fa::PagedArgs a{};
+  a.cache = cache_args(cache);
+  a.q = q;
+  a.o = o;
+  a.lse = lse;
+  a.B = B; a.H = H; a.Hkv = Hkv; a.T = T; a.d = d;
+  a.q_lens = q_lens;
+  a.scale = scale;
+  a.softcap = score != nullptr ? score->softcap : 0.f;
+  a.slopes = score != nullptr ? score->alibi_slopes : nullptr;
+  a.ctas = fa::paged_ctas(d);
+  const size_t parts = fa::paged_parts(a.ctas);
+  a.o_part = static_cast<float*>(workspace);
+  a.ml_part = reinterpret_cast<float2*>(a.o_part + parts * d);
+  if (fa::device_error_word(&a.err) != FA_OK) return FA_ERR_CUDA;
+  return fa::launch_paged(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -340,6 +340,111 @@ fa_status fa_backward_fused(const void* q, const void* k, const void* v, const v
                             const uint8_t* block_mask, fa_dtype dtype, const int32_t* kv_lens,
                             void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Scores that are capped, biased by distance, or see a prefix.  With u_ij = scale * (q_i . k_j):
+ *     s_ij = (softcap > 0 ? softcap * tanh(u_ij / softcap) : u_ij) - slope_h * |i - j|
+ *     allowed(i, j) = (!causal || j <= i || j < prefix_lens[b])
+ *                  && (kv_lens == NULL || j < kv_lens[b])
+ * i and j count within the sequence (within the document, for packed sequences: the document mask
+ * and these scores go together).  The bias is linear in the distance, one slope per query head;
+ * slopes are constants and get no gradient.
+ */
+typedef struct {
+  float softcap;               /* 0: no cap; otherwise finite and > 0 */
+  const float* alibi_slopes;   /* nullable; device fp32 [H], finite */
+  const int32_t* prefix_lens;  /* nullable; device int32 [B] (packed: [n_seqs]): the first keys of a
+                                  sequence, seen by all its queries in spite of `causal`; values
+                                  below 0 count as 0, values past the end as the whole sequence */
+} fa_score_mod;
+
+/*
+ * Rotary positions.  The first rotary_dim values of every head are turned in pairs (a, b) by the
+ * angle w = position * inv_freq[p] of their pair p:
+ *     (a, b) -> mscale * (a cos w - b sin w, a sin w + b cos w)
+ * Pairs are (2p, 2p + 1) when `interleaved`, else (p, p + rotary_dim / 2).  The other values are
+ * copied.  fa_rotary_backward is its gradient: the rotation by -w, times mscale.  Angles keep
+ * their accuracy at any int32 position (64-bit fixed-point turns).
+ *   x, y            : [B, H, N, d], d in {64, 128}, the d values of a head adjacent; strides of
+ *                     the other axes in elements {batch, head, token}, multiples of 16 bytes; base
+ *                     addresses 16-byte aligned.  y may be x (with the same strides); otherwise
+ *                     they must not overlap.
+ *   positions       : device int32 [N] (position_stride 0) or one list of N per batch,
+ *                     position_stride elements apart
+ *   inv_freq        : device fp64 [rotary_dim / 2], radians per position (finite, below 2^52)
+ *   rotary_dim      : a multiple of 16, at most d (FA_ERR_UNSUPPORTED otherwise); 0 copies
+ *   dtype           : FA_BF16, FA_FP16 or FA_FP32; the rotation runs in fp32, rounded once
+ */
+fa_status fa_rotary(const void* x, const int64_t x_strides[3], void* y, const int64_t y_strides[3],
+                    int B, int H, int N, int d, const int32_t* positions, int64_t position_stride,
+                    const double* inv_freq, int rotary_dim, int interleaved, float mscale,
+                    fa_dtype dtype, void* stream);
+fa_status fa_rotary_backward(const void* dy, const int64_t dy_strides[3], void* dx,
+                             const int64_t dx_strides[3], int B, int H, int N, int d,
+                             const int32_t* positions, int64_t position_stride,
+                             const double* inv_freq, int rotary_dim, int interleaved, float mscale,
+                             fa_dtype dtype, void* stream);
+
+/*
+ * A key/value cache in pages.  Token p of sequence b lies in page block_table[b][p / page_size],
+ * slot p % page_size; its key of head g is at
+ *     k_cache + page * page_stride + g * head_stride + slot * token_stride   (elements)
+ * and its value at the same place from v_cache.  Any order of the page, head and slot axes fits.
+ * Sequences may share pages that are only read.
+ */
+typedef struct {
+  void* k_cache;               /* bf16 or fp16, 16-byte aligned; the d values of a head adjacent */
+  void* v_cache;
+  int64_t page_stride;         /* elements; multiples of 8 */
+  int64_t head_stride;
+  int64_t token_stride;
+  int n_pages;                 /* pages that exist */
+  int page_size;               /* tokens of a page: a multiple of 16 */
+  const int32_t* block_table;  /* device int32, row b at b * table_stride */
+  int64_t table_stride;        /* >= max_pages */
+  int max_pages;               /* entries of a row */
+  const int32_t* kv_lens;      /* device int32 [B]: tokens of each sequence, the new ones included */
+} fa_paged_cache;
+
+/*
+ * Writes T new tokens per sequence into the cache, their keys rotated (rotary_dim > 0), and with q
+ * given writes the rotated queries to q_out, in one launch.  kv_lens counts the new tokens already:
+ * token t of sequence b's n = q_lens ? q_lens[b] : T new tokens (n clamped to [0, T]) takes place
+ * kv_lens[b] - n + t.  Tokens t >= n, and places below 0, do not exist: nothing is stored for them
+ * and their rows of q_out are zero.
+ *   k, v   : [B, Hkv, T, d], q (nullable): [B, H, T, d], strided as in fa_rotary
+ *   q_out  : [B, H, T, d] contiguous; may be q when q is contiguous
+ * bf16 or fp16.  Hkv divides H.  The lengths and the table live on the device and are checked
+ * there: a length beyond max_pages * page_size, or an entry outside [0, n_pages), is not followed
+ * and fa_check_device_status then returns FA_ERR_INVALID_ARG.
+ */
+fa_status fa_append_paged(const fa_paged_cache* cache, const void* k, const int64_t k_strides[3],
+                          const void* v, const int64_t v_strides[3], const void* q,
+                          const int64_t q_strides[3], void* q_out, int B, int H, int Hkv, int T,
+                          int d, const int32_t* q_lens, const double* inv_freq, int rotary_dim,
+                          int interleaved, float mscale, fa_dtype dtype, void* stream);
+
+/*
+ * Attention of T new tokens per sequence (one when decoding, a few when drafted tokens are
+ * checked) over a paged cache that holds them already (fa_append_paged).  Query t stands at place
+ * i = kv_lens[b] - n + t (n as in fa_append_paged) and sees the keys j <= i; softcap and
+ * alibi_slopes as in fa_score_mod (score nullable; its prefix_lens must be null).
+ *   q, o   : [B, H, T, d] contiguous; lse: fp32 [B, H, T].  Query head h reads key head
+ *            h / (H / Hkv).  Rows without a key, or past a sequence's new tokens, get O = 0 and
+ *            LSE = -inf.
+ *   workspace : >= fa_forward_paged_workspace_size(...) bytes, 256-byte aligned, caller-owned,
+ *            contents on entry irrelevant; calls in flight at once need their own
+ * The cache is split over its length among all SMs and joined in a fixed order: the same bits on
+ * every call.  Nothing that a page holds behind a sequence's last token enters the result.  bf16 or
+ * fp16.  Lengths and table entries outside their contract as in fa_append_paged (such a sequence's
+ * result is then unspecified).  The work is sized for few new tokens: every 16 query rows of a
+ * group (H / Hkv * T) read the cache once more.
+ */
+size_t fa_forward_paged_workspace_size(int B, int H, int Hkv, int T, int d);
+fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, float* lse, int B,
+                           int H, int Hkv, int T, int d, float scale, const int32_t* q_lens,
+                           const fa_score_mod* score, fa_dtype dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
 /* ABI version of this header: major * 100 + minor. */
 int fa_version(void);
 

@@ -1,0 +1,90 @@
+"""Attention with capped and biased scores in 64 bits, head by head, and bounds on what a kernel may
+differ by that takes 16-bit operands, adds in 32 bits and rounds its probabilities (and dS) and its
+outputs once to the operands' type.
+
+A rounding to type t is off by at most half a step, u = finfo(t).eps / 2 relative to the value; one
+fp32 operation by v = 2^-24.  The bounds, for one row i with probabilities p, and e_ij the largest
+error of a score:
+
+  e_ij  : d products added in fp32, in any order, (d + 4) v scale sum_c |q_c k_c|; the cap
+          multiplies an error of 6 v (exponential, sum, reciprocal, product of 1 / (1 + exp 2x); their
+          own bound is 2^-22 each) by twice itself: 2^-20 cap in all; the bias 4 v slope |i - j|
+          more, 4 v |s_ij| for the conversion to base 2.
+  p     : relative error 2 (max_j e_ij + 2^-22) =: f_i  (numerator and normaliser)
+  O     : u |O| + (u + f_i) sum_j p_j |v_j|
+  LSE   : max_j e_ij + 2^-22 + 4 v (1 + |LSE|)
+  dV    : u |dV| + sum_i (u + f_i) p_ij |dO_i|
+  dS_ij : = p (dP - D) c, c = the cap's derivative.  dP adds d products: (d + 2) v sum |dO_c V_c|;
+          D is computed from the O it is given, (d + 2) v sum |dO_c O_c|; c by 2^-19 (its terms are
+          at most 1, each off by e_ij-independent roundings, and by 2 e_ij / cap through its argument);
+          then one rounding u:
+          (u + f_i + 2^-19 + 2 e_ij / cap) |dS| + p c (the errors of dP and D)
+  dQ,dK : u |.| + scale sum of the above times |K| or |Q|; products added in fp32 stay below
+          f's slack.
+Each is asserted element by element.
+"""
+import math
+
+import torch
+
+V = 2.0 ** -24
+
+
+def scores(q, k, allowed, dist, scale, cap, slope):
+    """(s, c, e): masked scores, the cap's derivative, the error bound of s."""
+    x = q @ k.T * scale
+    e = (q.shape[-1] + 4) * V * scale * (q.abs() @ k.abs().T)
+    c = torch.ones_like(x)
+    if cap > 0.0:
+        t = torch.tanh(x / cap)
+        x, c = cap * t, 1.0 - t * t
+        e = e + 2.0 ** -20 * cap
+    if slope != 0.0:
+        x = x - slope * dist
+        e = e + 4 * V * slope * dist
+    e = e + 4 * V * x.abs()
+    return x.masked_fill(~allowed, -math.inf), c, e.masked_fill(~allowed, 0.0)
+
+
+def softmax(s):
+    lse = torch.logsumexp(s, -1)
+    p = torch.exp(s - torch.where(torch.isinf(lse), torch.zeros_like(lse), lse)[:, None])
+    return p, lse
+
+
+def head_forward(q, k, v, allowed, dist, scale, cap, slope, u):
+    """O, LSE of one head and the bounds of both (64-bit inputs)."""
+    s, _, e = scores(q, k, allowed, dist, scale, cap, slope)
+    p, lse = softmax(s)
+    f = 2 * (e.amax(-1, keepdim=True) + 2.0 ** -22) if s.shape[-1] else torch.zeros_like(lse)[:, None]
+    o = p @ v
+    o_tol = u * o.abs() + (u + f) * (p @ v.abs())
+    lse_tol = f[:, 0] / 2 + 4 * V * (1 + lse.abs().nan_to_num(posinf=0.0))
+    return o, lse, o_tol, lse_tol
+
+
+def head_backward(q, k, v, do, o_given, allowed, dist, scale, cap, slope, u):
+    """dQ, dK, dV of one head for the O that the backward is given, and their bounds."""
+    s, c, e = scores(q, k, allowed, dist, scale, cap, slope)
+    p, _ = softmax(s)
+    f = 2 * (e.amax(-1, keepdim=True) + 2.0 ** -22)
+    d = q.shape[-1]
+    dp = do @ v.T
+    delta = (do * o_given).sum(-1, keepdim=True)
+    ds = p * (dp - delta) * c
+    dp_err = (d + 2) * V * (do.abs() @ v.abs().T + (do * o_given).abs().sum(-1, keepdim=True))
+    ds_tol = (u + f + 2.0 ** -19 + (2 * e / cap if cap > 0.0 else 0.0)) * ds.abs() + p * c * dp_err
+    dq, dk, dv = scale * ds @ k, scale * ds.T @ q, p.T @ do
+    return (dq, dk, dv, u * dq.abs() + scale * ds_tol @ k.abs(), u * dk.abs() + scale * ds_tol.T @ q.abs(),
+            u * dv.abs() + ((u + f) * p).T @ do.abs())
+
+
+def assert_within(name, got, ref, tol):
+    got = got.double()
+    assert torch.equal(torch.isinf(got), torch.isinf(ref)), f"{name}: infinities differ"
+    fine = ~torch.isinf(ref)
+    assert bool(torch.isfinite(got[fine]).all()), f"{name}: not finite"
+    over = ((got - ref).abs() - tol)[fine]
+    # gradients that vanish in exact arithmetic keep the rounding of their terms: the bound has it
+    worst = float(over.max()) if over.numel() else 0.0
+    assert worst <= 1e-30, (name, worst, float((got - ref).abs()[fine].max()))

@@ -1,0 +1,123 @@
+"""Host-side argument checks of the rotary and paged-cache calls: the documented status before any
+CUDA call (CPU only: no kernel runs)."""
+import ctypes
+
+import pytest
+import torch
+
+import exact_io_aware_23_gb300 as fa
+
+OK, INVALID, UNSUPPORTED = 0, 1, 2
+P = 0x10000                        # aligned, never dereferenced: every call below returns early
+S3 = ctypes.c_int64 * 3
+DENSE = S3(1 << 20, 1 << 13, 64)
+
+
+def rotary(fn, x=P, xs=DENSE, y=P, ys=DENSE, B=1, H=2, N=8, d=64, pos=P, ps=0, inv=P, rot=64, mscale=1.0, dtype=0):
+    return fn(x, xs, y, ys, B, H, N, d, pos, ps, inv, rot, 0, mscale, dtype, None)
+
+
+@pytest.mark.parametrize("fn", [fa.lib.fa_rotary, fa.lib.fa_rotary_backward])
+def test_rotary_argument_checks(fn):
+    assert rotary(fn, d=96) == UNSUPPORTED
+    assert rotary(fn, dtype=9) == UNSUPPORTED
+    assert rotary(fn, rot=24) == UNSUPPORTED
+    assert rotary(fn, rot=80) == UNSUPPORTED              # more than the head
+    assert rotary(fn, rot=-16) == INVALID
+    assert rotary(fn, B=-1) == INVALID
+    assert rotary(fn, B=65536) == UNSUPPORTED
+    assert rotary(fn, B=60000, H=60000, N=60000) == UNSUPPORTED
+    assert rotary(fn, inv=None) == INVALID
+    assert rotary(fn, mscale=float("nan")) == INVALID
+    assert rotary(fn, x=None) == INVALID
+    assert rotary(fn, y=P + 8) == INVALID
+    assert rotary(fn, pos=None) == INVALID
+    assert rotary(fn, ps=-1) == INVALID
+    assert rotary(fn, xs=S3(1 << 20, 1 << 13, 68)) == INVALID          # rows off the 16-byte grid
+    assert rotary(fn, ys=S3(1 << 20, 4, 64)) == INVALID
+    for empty in (dict(B=0), dict(H=0), dict(N=0)):
+        assert rotary(fn, x=None, pos=None, **empty) == OK
+
+
+def cache(**kw):
+    c = dict(k_cache=P, v_cache=P, page_stride=1 << 12, head_stride=1 << 10, token_stride=64, n_pages=4,
+             page_size=16, block_table=P, table_stride=3, max_pages=3, kv_lens=P)
+    c.update(kw)
+    return ctypes.byref(fa.FaPagedCache(*[c[n] for n, _ in fa.FaPagedCache._fields_]))
+
+
+BAD_CACHES = [(dict(k_cache=None), INVALID), (dict(v_cache=P + 8), INVALID), (dict(page_size=0), INVALID),
+              (dict(page_size=24), UNSUPPORTED), (dict(n_pages=-1), INVALID), (dict(token_stride=65), INVALID),
+              (dict(head_stride=4), INVALID), (dict(page_stride=4), INVALID), (dict(block_table=None), INVALID),
+              (dict(kv_lens=None), INVALID), (dict(table_stride=2), INVALID), (dict(max_pages=-1), INVALID)]
+
+
+def append(c=None, k=P, ks=DENSE, v=P, q=P, qs=DENSE, q_out=P, B=2, H=4, Hkv=2, T=1, d=64, inv=P, rot=64, dtype=0, q_lens=None):
+    return fa.lib.fa_append_paged(cache() if c is None else c, k, ks, v, DENSE, q, qs, q_out, B, H, Hkv, T, d, q_lens, inv,
+                                  rot, 0, 1.0, dtype, None)
+
+
+def test_append_argument_checks():
+    for kw, status in BAD_CACHES:
+        assert append(cache(**kw)) == status, kw
+    assert append(dtype=1) == UNSUPPORTED                 # the cache is 16 bits
+    assert append(Hkv=3) == UNSUPPORTED
+    assert append(Hkv=0) == INVALID
+    assert append(d=80) == UNSUPPORTED
+    assert append(rot=40) == UNSUPPORTED
+    assert append(inv=None) == INVALID
+    assert append(k=None) == INVALID
+    assert append(v=P + 2) == INVALID
+    assert append(q_out=None) == INVALID
+    assert append(q=P + 4) == INVALID
+    assert append(ks=S3(1 << 20, 12, 64)) == INVALID
+    assert append(q_lens=P + 1) == INVALID
+    assert append(T=0, k=None) == OK
+    assert append(B=0, k=None) == OK
+
+
+def paged(c=None, q=P, o=P, lse=P, B=2, H=4, Hkv=2, T=1, d=64, scale=0.125, mod=None, dtype=0, w=P, wsb=None):
+    wsb = fa.forward_paged_workspace_size(2, 4, 2, 1, 64) if wsb is None else wsb
+    return fa.lib.fa_forward_paged(q, cache() if c is None else c, o, lse, B, H, Hkv, T, d, scale, None,
+                                   None if mod is None else ctypes.byref(mod), dtype, w, wsb, None)
+
+
+def test_paged_attention_argument_checks():
+    for kw, status in BAD_CACHES:
+        assert paged(cache(**kw)) == status, kw
+    ws = fa.forward_paged_workspace_size(2, 4, 2, 1, 64)
+    assert ws % 256 == 0 and ws > 0
+    assert fa.forward_paged_workspace_size(2, 4, 2, 1, 128) > ws
+    assert fa.forward_paged_workspace_size(0, 4, 2, 1, 64) == 0
+    assert fa.forward_paged_workspace_size(2, 4, 3, 1, 64) == 0
+    assert paged(dtype=1) == UNSUPPORTED
+    assert paged(d=96) == UNSUPPORTED
+    assert paged(Hkv=3) == UNSUPPORTED
+    for bad in (0.0, -1.0, float("nan"), float("inf")):
+        assert paged(scale=bad) == INVALID
+    assert paged(q=None) == INVALID
+    assert paged(o=P + 8) == INVALID
+    assert paged(lse=None) == INVALID
+    assert paged(w=None) == INVALID
+    assert paged(w=P + 16) == INVALID
+    assert paged(wsb=ws - 256) == INVALID
+    for bad in (-1.0, float("nan"), float("inf")):
+        assert paged(mod=fa.FaScoreMod(bad, None, None)) == INVALID
+    assert paged(mod=fa.FaScoreMod(0.0, None, P)) == UNSUPPORTED       # no prefix over a cache
+    assert paged(mod=fa.FaScoreMod(0.0, P + 2, None)) == INVALID
+    assert paged(T=0, q=None) == OK
+    assert paged(B=0, q=None) == OK
+
+
+def test_host_tensors_are_refused():
+    x = torch.zeros(1, 2, 8, 64, dtype=torch.bfloat16)
+    pos = torch.arange(8, dtype=torch.int32)
+    inv, _ = fa.rotary_frequencies(64, device="cpu")
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        fa.rotary(x, pos, inv)
+    table, n = torch.zeros(1, 1, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    pages = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        fa.append_paged(x, x, pages, pages.clone(), table, n)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        fa.forward_paged(x, pages, pages.clone(), table, n)
