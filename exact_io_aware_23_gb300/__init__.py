@@ -125,6 +125,15 @@ def _load() -> ctypes.CDLL:
     L.fa_rotary_backward.argtypes = L.fa_rotary.argtypes
     L.fa_rotary_backward.restype = i
     cp, mp = ctypes.POINTER(FaPagedCache), ctypes.POINTER(FaScoreMod)
+    L.fa_forward_scored.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, i, i, vp, mp, vp]
+    L.fa_forward_scored.restype = i
+    L.fa_backward_scored.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, i, i, vp, mp, vp, sz, vp]
+    L.fa_backward_scored.restype = i
+    L.fa_forward_varlen_scored.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, mp, vp]
+    L.fa_forward_varlen_scored.restype = i
+    L.fa_backward_varlen_scored.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i,
+                                            mp, vp, sz, vp]
+    L.fa_backward_varlen_scored.restype = i
     L.fa_append_paged.argtypes = [cp, vp, st3, vp, st3, vp, st3, vp, i, i, i, i, i, vp, vp, i, i, f, i, vp]
     L.fa_append_paged.restype = i
     L.fa_forward_paged_workspace_size.argtypes = [i, i, i, i, i]
@@ -178,21 +187,42 @@ def _masks(block_mask, kv_lens, B, N, device):
     return block_mask, kv_lens
 
 
+def _scored(softcap, alibi_slopes, prefix_lens) -> bool:
+    """Whether any score modification is asked for."""
+    return softcap != 0.0 or alibi_slopes is not None or prefix_lens is not None
+
+
 def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = False,
             scale: Optional[float] = None, block_mask: Optional[torch.Tensor] = None,
             kv_lens: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
             lse: Optional[torch.Tensor] = None, stream=None, dropout_p: float = 0.0,
             seed: int = 0, offset: int = 0, balanced: bool = True,
-            workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+            workspace: Optional[torch.Tensor] = None, softcap: float = 0.0,
+            alibi_slopes: Optional[torch.Tensor] = None,
+            prefix_lens: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """O, LSE = attention forward (fa_forward; fa_forward_gqa when k, v have fewer heads;
     fa_forward_dropout when dropout_p > 0; with a block mask and 16-bit inputs,
     fa_forward_blocksparse unless balanced=False).  q: [B, H, N, d]; k, v: [B, Hkv, N, d];
-    bf16, fp16 or fp32 on CUDA."""
+    bf16, fp16 or fp32 on CUDA.  With softcap > 0 (scores capped by softcap * tanh(. / softcap)),
+    alibi_slopes (fp32 [H]: scores lowered by the slope times |i - j|) or prefix_lens (int32 [B]:
+    leading keys seen in spite of causal), fa_forward_scored: bf16 or fp16, no block mask or
+    dropout."""
     B, H, N, d, Hkv = _check_qkv(q, k, v)
     scale = 1.0 / d ** 0.5 if scale is None else float(scale)
     block_mask, kv_lens = _masks(block_mask, kv_lens, B, N, q.device)
     o = torch.empty_like(q) if o is None else o
     lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device) if lse is None else lse
+    if _scored(softcap, alibi_slopes, prefix_lens):
+        if block_mask is not None or dropout_p > 0.0:
+            raise ValueError("score modifications take no block mask and no dropout")
+        mod = _score_mod(q, softcap, alibi_slopes, prefix_lens, H, B)
+        _keep(stream, o, lse)
+        st = lib.fa_forward_scored(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Hkv, N, d, scale,
+                                   int(bool(causal)), _DTYPES[q.dtype], _ptr(kv_lens), ctypes.byref(mod),
+                                   _stream(stream))
+        if st != FA_OK:
+            raise FaError(st, "fa_forward_scored")
+        return o, lse
     if dropout_p > 0.0:
         drop = FaDropout(float(dropout_p), int(seed), int(offset))
         st = lib.fa_forward_dropout(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Hkv, N, d,
@@ -243,13 +273,26 @@ def _check_packed(q, k, v, cu_seqlens):
 
 
 def forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, *, causal: bool = False,
-                   scale: Optional[float] = None, stream=None):
+                   scale: Optional[float] = None, stream=None, softcap: float = 0.0,
+                   alibi_slopes: Optional[torch.Tensor] = None,
+                   prefix_lens: Optional[torch.Tensor] = None):
     """fa_forward_varlen: sequences packed along the token axis (q [H, total, d], k, v
-    [Hkv, total, d], offsets cu_seqlens); returns O [H, total, d] and LSE [H, total]."""
+    [Hkv, total, d], offsets cu_seqlens); returns O [H, total, d] and LSE [H, total].  softcap,
+    alibi_slopes and prefix_lens (int32 [n_seqs]) as in ``forward`` (fa_forward_varlen_scored);
+    distances and prefixes count within a sequence."""
     H, Hkv, T, d, S = _check_packed(q, k, v, cu_seqlens)
     scale = 1.0 / d ** 0.5 if scale is None else float(scale)
     o = torch.empty_like(q)
     lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+    if _scored(softcap, alibi_slopes, prefix_lens):
+        mod = _score_mod(q, softcap, alibi_slopes, prefix_lens, H, S)
+        _keep(stream, o, lse)
+        st = lib.fa_forward_varlen_scored(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens), S,
+                                          int(max_seqlen), T, H, Hkv, d, scale, int(bool(causal)),
+                                          _DTYPES[q.dtype], ctypes.byref(mod), _stream(stream))
+        if st != FA_OK:
+            raise FaError(st, "fa_forward_varlen_scored")
+        return o, lse
     st = lib.fa_forward_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens), S,
                                int(max_seqlen), T, H, Hkv, d, scale, int(bool(causal)),
                                _DTYPES[q.dtype], _stream(stream))
@@ -259,8 +302,11 @@ def forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, *, causal: bool = False
 
 
 def backward_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen: int, *, causal: bool = False,
-                    scale: Optional[float] = None, stream=None):
-    """fa_backward_varlen: dQ [H, total, d], dK, dV [Hkv, total, d] for packed sequences."""
+                    scale: Optional[float] = None, stream=None, softcap: float = 0.0,
+                    alibi_slopes: Optional[torch.Tensor] = None,
+                    prefix_lens: Optional[torch.Tensor] = None):
+    """fa_backward_varlen: dQ [H, total, d], dK, dV [Hkv, total, d] for packed sequences
+    (fa_backward_varlen_scored with the score arguments of ``forward_varlen``)."""
     H, Hkv, T, d, S = _check_packed(q, k, v, cu_seqlens)
     for name, t in (("o", o), ("do", do)):
         if t.shape != q.shape or t.dtype != q.dtype or not t.is_contiguous():
@@ -271,6 +317,16 @@ def backward_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen: int, *, causal:
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     need = backward_deterministic_workspace_size(1, H, T)
     workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    if _scored(softcap, alibi_slopes, prefix_lens):
+        mod = _score_mod(q, softcap, alibi_slopes, prefix_lens, H, S)
+        _keep(stream, dq, dk, dv, workspace)
+        st = lib.fa_backward_varlen_scored(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq),
+                                           _ptr(dk), _ptr(dv), _ptr(cu_seqlens), S, int(max_seqlen), T, H, Hkv,
+                                           d, scale, int(bool(causal)), _DTYPES[q.dtype], ctypes.byref(mod),
+                                           _ptr(workspace), workspace.numel(), _stream(stream))
+        if st != FA_OK:
+            raise FaError(st, "fa_backward_varlen_scored")
+        return dq, dk, dv
     st = lib.fa_backward_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq),
                                 _ptr(dk), _ptr(dv), _ptr(cu_seqlens), S, int(max_seqlen), T, H,
                                 Hkv, d, scale, int(bool(causal)), _DTYPES[q.dtype],
@@ -337,10 +393,13 @@ def backward_fused_workspace_size(B: int, H: int, N: int, d: int) -> int:
 def backward(q, k, v, o, lse, do, *, causal: bool = False, scale: Optional[float] = None,
              block_mask=None, kv_lens=None, dq=None, dk=None, dv=None, workspace=None,
              stream=None, deterministic: bool = False, fused: bool = False,
-             dropout_p: float = 0.0, seed: int = 0, offset: int = 0):
+             dropout_p: float = 0.0, seed: int = 0, offset: int = 0, softcap: float = 0.0,
+             alibi_slopes: Optional[torch.Tensor] = None,
+             prefix_lens: Optional[torch.Tensor] = None):
     """dQ, dK, dV = recompute-based attention backward (fa_backward; fa_backward_gqa when k, v
     have fewer heads than q; fa_backward_deterministic, bit-reproducible, when asked;
-    fa_backward_fused, the single-pass atomic-dQ variant, when asked)."""
+    fa_backward_fused, the single-pass atomic-dQ variant, when asked; fa_backward_scored,
+    bit-reproducible too, with the score arguments of ``forward``)."""
     B, H, N, d, Hkv = _check_qkv(q, k, v)
     for name, t in (("o", o), ("do", do)):
         if t.shape != q.shape or t.dtype != q.dtype or not t.is_contiguous():
@@ -360,6 +419,17 @@ def backward(q, k, v, o, lse, do, *, causal: bool = False, scale: Optional[float
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv))
+    if _scored(softcap, alibi_slopes, prefix_lens):
+        if block_mask is not None or dropout_p > 0.0 or fused:
+            raise ValueError("score modifications take no block mask, no dropout and no fused backward")
+        mod = _score_mod(q, softcap, alibi_slopes, prefix_lens, H, B)
+        _keep(stream, dq, dk, dv, workspace)
+        st = lib.fa_backward_scored(*args, B, H, Hkv, N, d, scale, int(bool(causal)), _DTYPES[q.dtype],
+                                    _ptr(kv_lens), ctypes.byref(mod), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(stream))
+        if st != FA_OK:
+            raise FaError(st, "fa_backward_scored")
+        return dq, dk, dv
     tail = (d, scale, int(bool(causal)), _ptr(block_mask), _DTYPES[q.dtype], _ptr(kv_lens),
             _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
     if dropout_p > 0.0:
@@ -648,8 +718,9 @@ def forward_paged_workspace_size(B: int, H: int, Hkv: int, T: int, d: int) -> in
     return int(lib.fa_forward_paged_workspace_size(B, H, Hkv, T, d))
 
 
-def _score_mod(softcap, alibi_slopes, prefix_lens, H, n_seqs) -> FaScoreMod:
+def _score_mod(q, softcap, alibi_slopes, prefix_lens, H, n_seqs) -> FaScoreMod:
     """Checks the score arguments; slopes fp32 [H], prefix lengths int32 [n_seqs]."""
+    _here("q", q)
     if alibi_slopes is not None:
         _here("alibi_slopes", alibi_slopes)
         if (alibi_slopes.dtype != torch.float32 or tuple(alibi_slopes.shape) != (H,)
@@ -672,7 +743,6 @@ def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     ``append_paged``.  Token t of a sequence's n new ones sees the keys up to its own place
     kv_lens - n + t; scores capped by softcap * tanh(. / softcap) when softcap > 0 and lowered by
     alibi_slopes[h] (fp32 [H]) times the distance."""
-    _here("q", q)
     if q.dim() != 4 or q.dtype not in (torch.bfloat16, torch.float16) or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 or fp16 [B, H, T, d] tensor")
     B, H, T, d = q.shape
@@ -682,7 +752,7 @@ def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     cache = _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, q.dtype)
     if q_lens is not None:
         _int32("q_lens", q_lens, (B,))
-    mod = _score_mod(softcap, alibi_slopes, None, H, B)
+    mod = _score_mod(q, softcap, alibi_slopes, None, H, B)
     scale = 1.0 / d ** 0.5 if scale is None else float(scale)
     if o is None:
         o = torch.empty((B, H, T, d), dtype=q.dtype, device=q.device)

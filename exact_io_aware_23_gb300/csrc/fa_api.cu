@@ -8,6 +8,7 @@
 
 #include "fa_internal.cuh"
 #include "fa_paged.cuh"
+#include "fa_score.cuh"
 #include "fa_sm103.cuh"
 
 namespace {
@@ -154,17 +155,34 @@ PlanLayout plan_layout(int B, int H, int N, int d) {
   return L;
 }
 
+// Checks the score arguments and turns them into the kernels' form; a prefix matters only under a
+// causal mask.
+fa_status make_scored(const fa_score_mod* m, float scale, int causal, fa::ScoreArgs* out) {
+  if (m != nullptr) {
+    if (!isfinite(m->softcap) || m->softcap < 0.f) return FA_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(m->alibi_slopes) | reinterpret_cast<uintptr_t>(m->prefix_lens)) & 3u) != 0)
+      return FA_ERR_INVALID_ARG;
+  }
+  if (!fa::make_score(m, scale, out)) return FA_ERR_UNSUPPORTED;
+  if (!causal) out->prefix = nullptr;
+  return FA_OK;
+}
+// Whether any modification is set; without one the plain kernels run.
+bool has_score(const fa::ScoreArgs& s) { return s.cap_log2 != 0.f || s.slopes != nullptr || s.prefix != nullptr; }
+
 fa_status forward_impl(const void* q, const void* k, const void* v, void* o, float* lse,
                        int B, int H, int Hkv, int N, int d, float scale, int causal,
                        const uint8_t* block_mask, fa_dtype dtype, const int32_t* kv_lens,
                        void* stream, Packing pk = {nullptr, 0}, fa::DropoutArgs drop = {},
-                       Balance bal = {nullptr, 0}) {
+                       Balance bal = {nullptr, 0}, const fa_score_mod* mod = nullptr) {
   fa_status st = check_common(B, H, N, d, scale, dtype);
   if (st != FA_OK) return st;
   st = check_heads(H, Hkv, dtype);
   if (st != FA_OK) return st;
-  if ((pk.cu_seqlens != nullptr || drop.enabled) && dtype == FA_FP32) return FA_ERR_UNSUPPORTED;
+  if ((pk.cu_seqlens != nullptr || drop.enabled || mod != nullptr) && dtype == FA_FP32) return FA_ERR_UNSUPPORTED;
   if (pk.cu_seqlens != nullptr && drop.enabled) return FA_ERR_UNSUPPORTED;
+  fa::ScoreArgs score;
+  if ((st = make_scored(mod, scale, causal, &score)) != FA_OK) return st;
   if (B == 0 || H == 0 || N == 0 || (pk.cu_seqlens != nullptr && pk.total == 0)) return FA_OK;
   if (block_mask != nullptr && N > kMaxBlockSparseN) return FA_ERR_UNSUPPORTED;
   if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
@@ -190,6 +208,8 @@ fa_status forward_impl(const void* q, const void* k, const void* v, void* o, flo
   a.next_unit = nullptr;
   a.pair_bits = nullptr;
   a.bit_words = 0;
+  a.scored = has_score(score);
+  a.score = score;
   if (device_error_word(&a.err) != FA_OK) return FA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (bal.workspace != nullptr && block_mask != nullptr && dtype != FA_FP32) {
@@ -370,7 +390,8 @@ fa_status backward_impl(const void* q, const void* k, const void* v, const void*
                         int B, int H, int Hkv, int N, int d, float scale, int causal,
                         const uint8_t* block_mask, fa_dtype dtype, const int32_t* kv_lens,
                         void* workspace, size_t workspace_bytes, void* stream,
-                        BwdPath path, Packing pk = {nullptr, 0}, fa::DropoutArgs drop = {}) {
+                        BwdPath path, Packing pk = {nullptr, 0}, fa::DropoutArgs drop = {},
+                        const fa_score_mod* mod = nullptr) {
   fa_status st = check_common(B, H, N, d, scale, dtype);
   if (st != FA_OK) return st;
   st = check_heads(H, Hkv, dtype);
@@ -378,6 +399,8 @@ fa_status backward_impl(const void* q, const void* k, const void* v, const void*
   if ((path != BwdPath::kAuto || pk.cu_seqlens != nullptr || drop.enabled) && dtype == FA_FP32)
     return FA_ERR_UNSUPPORTED;
   if (pk.cu_seqlens != nullptr && drop.enabled) return FA_ERR_UNSUPPORTED;
+  fa::ScoreArgs score;
+  if ((st = make_scored(mod, scale, causal, &score)) != FA_OK) return st;
   // 16-bit inputs run the two-pass backward unless the fused one was asked for; fp32 always runs
   // the CUDA-core backward, which adds dQ from several blocks into the fp32 dQ output itself.
   const bool fused = path == BwdPath::kFused;
@@ -420,6 +443,8 @@ fa_status backward_impl(const void* q, const void* k, const void* v, const void*
   a.rows = pk.cu_seqlens != nullptr ? pk.total : N;
   if (pk.cu_seqlens != nullptr) a.heads_fastest = 1;     // sequences of unequal length
   a.drop = drop;
+  a.scored = has_score(score);
+  a.score = score;
   if (device_error_word(&a.err) != FA_OK) return FA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (two_pass && block_mask != nullptr) {
@@ -554,6 +579,49 @@ fa_status fa_backward_varlen(const void* q, const void* k, const void* v, const 
   return backward_impl(q, k, v, o, dO, lse, dq, dk, dv, n_seqs, H, Hkv, max_seqlen, d, scale,
                        causal, nullptr, dtype, nullptr, workspace, workspace_bytes, stream,
                        BwdPath::kTwoPass, Packing{cu_seqlens, total});
+}
+
+fa_status fa_forward_scored(const void* q, const void* k, const void* v, void* o, float* lse,
+                            int B, int H, int Hkv, int N, int d, float scale, int causal,
+                            fa_dtype dtype, const int32_t* kv_lens, const fa_score_mod* score,
+                            void* stream) {
+  if (score == nullptr) return FA_ERR_INVALID_ARG;
+  return forward_impl(q, k, v, o, lse, B, H, Hkv, N, d, scale, causal, nullptr, dtype, kv_lens, stream,
+                      Packing{nullptr, 0}, fa::DropoutArgs{}, Balance{nullptr, 0}, score);
+}
+
+fa_status fa_backward_scored(const void* q, const void* k, const void* v, const void* o,
+                             const void* dO, const float* lse, void* dq, void* dk, void* dv,
+                             int B, int H, int Hkv, int N, int d, float scale, int causal,
+                             fa_dtype dtype, const int32_t* kv_lens, const fa_score_mod* score,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  if (score == nullptr) return FA_ERR_INVALID_ARG;
+  return backward_impl(q, k, v, o, dO, lse, dq, dk, dv, B, H, Hkv, N, d, scale, causal, nullptr, dtype,
+                       kv_lens, workspace, workspace_bytes, stream, BwdPath::kTwoPass, Packing{nullptr, 0},
+                       fa::DropoutArgs{}, score);
+}
+
+fa_status fa_forward_varlen_scored(const void* q, const void* k, const void* v, void* o, float* lse,
+                                   const int32_t* cu_seqlens, int n_seqs, int max_seqlen, int total,
+                                   int H, int Hkv, int d, float scale, int causal, fa_dtype dtype,
+                                   const fa_score_mod* score, void* stream) {
+  if (score == nullptr || n_seqs < 0 || max_seqlen < 0 || total < 0) return FA_ERR_INVALID_ARG;
+  if (n_seqs > 0 && total > 0 && cu_seqlens == nullptr) return FA_ERR_INVALID_ARG;
+  return forward_impl(q, k, v, o, lse, n_seqs, H, Hkv, max_seqlen, d, scale, causal, nullptr, dtype, nullptr,
+                      stream, Packing{cu_seqlens, total}, fa::DropoutArgs{}, Balance{nullptr, 0}, score);
+}
+
+fa_status fa_backward_varlen_scored(const void* q, const void* k, const void* v, const void* o,
+                                    const void* dO, const float* lse, void* dq, void* dk, void* dv,
+                                    const int32_t* cu_seqlens, int n_seqs, int max_seqlen, int total,
+                                    int H, int Hkv, int d, float scale, int causal, fa_dtype dtype,
+                                    const fa_score_mod* score, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  if (score == nullptr || n_seqs < 0 || max_seqlen < 0 || total < 0) return FA_ERR_INVALID_ARG;
+  if (n_seqs > 0 && total > 0 && cu_seqlens == nullptr) return FA_ERR_INVALID_ARG;
+  return backward_impl(q, k, v, o, dO, lse, dq, dk, dv, n_seqs, H, Hkv, max_seqlen, d, scale, causal, nullptr,
+                       dtype, nullptr, workspace, workspace_bytes, stream, BwdPath::kTwoPass,
+                       Packing{cu_seqlens, total}, fa::DropoutArgs{}, score);
 }
 
 fa_status fa_check_device_status(void* stream) {

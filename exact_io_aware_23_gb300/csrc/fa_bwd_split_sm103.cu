@@ -21,7 +21,7 @@ namespace {
 // Both passes run with BwdLayout<D>'s block, one CTA per SM: at d = 128 320 threads (10 warps,
 // three on some of the SM's four 16K-register partitions, so at most 16384 / 96 -> 168
 // registers a thread), at d = 64 576 (18 warps, at most 112).
-template <int D, bool F16, bool kDrop>
+template <int D, bool F16, bool kDrop, bool kScore>
 __global__ void __launch_bounds__(BwdLayout<D>::kThreads, 1)
 bwd_split_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -29,8 +29,8 @@ bwd_split_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   (void)n_q_units;
   // under a tile mask, a plan may reorder the units so that the longest start first
   const int x = a.perm != nullptr ? a.perm[blockIdx.x] : (int)blockIdx.x;
-  if (x < n_kv_units) dkdv::run<D, F16, kDrop>(x, tmQ, tmK, tmV, tmDO, a);
-  else dqp::run<D, F16, kDrop>(x - n_kv_units, tmQ, tmK, tmV, tmDO, a);
+  if (x < n_kv_units) dkdv::run<D, F16, kDrop, kScore>(x, tmQ, tmK, tmV, tmDO, a);
+  else dqp::run<D, F16, kDrop, kScore>(x - n_kv_units, tmQ, tmK, tmV, tmDO, a);
 }
 
 cudaError_t make_map(CUtensorMap* m, const void* base, int D, int N, int BH, bool f16) {
@@ -42,7 +42,7 @@ cudaError_t make_map(CUtensorMap* m, const void* base, int D, int N, int BH, boo
                            3, base, dims, strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int D, bool F16, bool kDrop>
+template <int D, bool F16, bool kDrop, bool kScore = false>
 cudaError_t launch(const BwdArgs& a, cudaStream_t s) {
   CUtensorMap mq, mk, mv, mdo;
   const int BH = a.B * a.H;            // query-side work units per tile row (Q, dO, dQ)
@@ -55,7 +55,7 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t s) {
   if ((e = make_map(&mk, a.k, D, a.rows, kv_slices, F16)) != cudaSuccess) return e;
   if ((e = make_map(&mv, a.v, D, a.rows, kv_slices, F16)) != cudaSuccess) return e;
   if ((e = make_map(&mdo, a.dO, D, a.rows, q_slices, F16)) != cudaSuccess) return e;
-  auto kern = bwd_split_sm103_kernel<D, F16, kDrop>;
+  auto kern = bwd_split_sm103_kernel<D, F16, kDrop, kScore>;
   // each pass keeps its barriers 256 bytes below its live-tile bitmap (one bit per tile)
   const int bitmap = a.block_mask != nullptr ? ((a.n_tiles + 127) / 128) * 16 : 0;
   int smem = max(dkdv::Cfg<D, F16>::kSmem, dqp::Cfg<D, F16>::kSmem);
@@ -72,6 +72,12 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_bwd_split_sm103(const BwdArgs& a, fa_dtype dt, cudaStream_t s) {
+  if (a.scored) {
+    // no tile mask or dropout with score modifications
+    if (a.drop.enabled || a.block_mask != nullptr) return cudaErrorInvalidValue;
+    if (dt == FA_FP16) return a.d == 64 ? launch<64, true, false, true>(a, s) : launch<128, true, false, true>(a, s);
+    return a.d == 64 ? launch<64, false, false, true>(a, s) : launch<128, false, false, true>(a, s);
+  }
   if (a.drop.enabled) {
     if (dt == FA_FP16) return a.d == 64 ? launch<64, true, true>(a, s) : launch<128, true, true>(a, s);
     return a.d == 64 ? launch<64, false, true>(a, s) : launch<128, false, true>(a, s);

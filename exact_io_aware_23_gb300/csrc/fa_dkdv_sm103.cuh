@@ -34,6 +34,7 @@
 
 #include "dropout_sm103.cuh"
 #include "fa_internal.cuh"
+#include "fa_score.cuh"
 #include "fa_sm103.cuh"
 #include "ptx_sm103.cuh"
 
@@ -81,6 +82,8 @@ struct Bars {             // at most 256 bytes (the live-tile bitmap follows)
   uint64_t p_ready;
   uint64_t ds_ready;
   uint64_t acc_done;
+  uint64_t tail;          // scored variant: a head's last Q and dO tile, before their rows behind
+                          // the sequence are cleared (phase = the head's number in its group)
   uint32_t tmem_base;
 };
 
@@ -90,8 +93,10 @@ enum : int { kNone = 0, kPartial = 1, kFull = 2 };
 
 // Query tiles of one key tile: [i_begin, i_end) bounded by the causal diagonal and the valid key
 // length; a tile mask removes more (then `bits` lists the live ones).
+template <bool kScore>
 struct Geo {
   int k0, N, kv_lim, causal, T;
+  int prefix;             // scored variant: keys every query sees in spite of `causal`
   const uint8_t* bm;
   int i_begin, i_end;
   const uint32_t* bits;
@@ -99,8 +104,8 @@ struct Geo {
     const int r0 = i * BM, r1 = min(r0 + BM, N) - 1;
     const int c0 = k0, c1 = k0 + BN - 1;
     if (bm != nullptr && bm[(size_t)i * T + k0 / BN] == 0) return kNone;
-    if (c0 >= kv_lim || (causal && c0 > r1)) return kNone;
-    if (c1 < kv_lim && (!causal || c1 <= r0)) return kFull;
+    if (c0 >= kv_lim || (causal && c0 > r1 && !(kScore && c0 < prefix))) return kNone;
+    if (c1 < kv_lim && (!causal || c1 <= r0 || (kScore && c1 < prefix))) return kFull;
     return kPartial;
   }
   __device__ int next(int i) const {
@@ -114,7 +119,7 @@ struct Geo {
   }
 };
 
-template <int D, bool F16, bool kDrop>
+template <int D, bool F16, bool kDrop, bool kScore>
 __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                     const CUtensorMap& tmV, const CUtensorMap& tmDO,
                                     const BwdArgs& a) {
@@ -152,7 +157,7 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
   const int bhq0 = (a.cu_seqlens != nullptr ? 0 : b * a.H) + hk * G;            // first query slice
   const uint32_t lim_ms = a.dbg.wait_limit_ms;
 
-  Geo g;
+  Geo<kScore> g;
   g.k0 = jt * BN;
   g.N = len;
   int kvl = len;
@@ -162,6 +167,10 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
   g.T = a.n_tiles;
   g.bm = a.block_mask;
   g.i_begin = a.causal ? jt : 0;
+  if constexpr (kScore) {
+    g.prefix = a.causal && a.score.prefix != nullptr ? min(max(a.score.prefix[b], 0), len) : 0;
+    if (g.k0 < g.prefix) g.i_begin = 0;
+  }
   g.i_end = g.k0 < g.kv_lim ? (len + BM - 1) / BM : 0;
 
   if (threadIdx.x == 0) {
@@ -184,6 +193,7 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
     ptx::mbar_init(ptx::smem_u32(&bars->p_ready), L::kComputeWarps);
     ptx::mbar_init(ptx::smem_u32(&bars->ds_ready), L::kComputeWarps);
     ptx::mbar_init(ptx::smem_u32(&bars->acc_done), 1);
+    if constexpr (kScore) ptx::mbar_init(ptx::smem_u32(&bars->tail), 1);
     ptx::fence_mbar_init();
   }
   if (warp == L::kMmaWarp) {
@@ -207,6 +217,8 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
   int n_live = 0;                                // live query tiles of one head
   for (int i = g.next(g.i_begin); i < g.i_end; i = g.next(i + 1)) ++n_live;
   const int total = n_live * G;                  // tiles this CTA visits
+  // scored variant: the last query tile reaches into the memory behind a packed sequence
+  const bool has_tail = kScore && a.cu_seqlens != nullptr && len % BM != 0 && row0 + len < a.rows;
 
   if (warp == L::kProducerWarp) {
     // ------------------------------- producer (whole warp) --------------------------------------
@@ -228,12 +240,14 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
       for (int i = g.next(g.i_begin); i < g.i_end && ok; i = g.next(i + 1), ++n) {
         const int bhq = bhq0 + hg;
         const int qs = n % C::kQSlots, os = n % C::kOSlots, vs = n & 1;
+        const bool tail = has_tail && i == g.i_end - 1;
         if (lane == 0) {
+          if (tail) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&bars->tail), 2 * C::kTile);
           ok = ptx::mbar_wait(ptx::smem_u32(&bars->q_empty[qs]), ((uint32_t)(n / C::kQSlots) & 1u) ^ 1u,
                               lim_ms, a.err);
           if (ok) {
-            const uint32_t qb = ptx::smem_u32(&bars->q_full[qs]);
-            ptx::mbar_arrive_expect_tx(qb, C::kTile);
+            const uint32_t qb = ptx::smem_u32(tail ? &bars->tail : &bars->q_full[qs]);
+            if (!tail) ptx::mbar_arrive_expect_tx(qb, C::kTile);
             for (int hh = 0; hh < D / 64; ++hh)
               ptx::tma_load_3d(sbase + C::kQ + qs * C::kTile + hh * 128 * 128, &tmQ, qb, hh * 64, row0 + i * BM, bhq);
             ++nq;
@@ -241,8 +255,8 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
                                 lim_ms, a.err);
           }
           if (ok) {
-            const uint32_t ob = ptx::smem_u32(&bars->o_full[os]);
-            ptx::mbar_arrive_expect_tx(ob, C::kTile);
+            const uint32_t ob = ptx::smem_u32(tail ? &bars->tail : &bars->o_full[os]);
+            if (!tail) ptx::mbar_arrive_expect_tx(ob, C::kTile);
             for (int hh = 0; hh < D / 64; ++hh)
               ptx::tma_load_3d(sbase + C::kO + os * C::kTile + hh * 128 * 128, &tmDO, ob, hh * 64, row0 + i * BM, bhq);
             ++no;
@@ -252,6 +266,18 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
+        if (kScore && tail) {
+          // rows behind the sequence multiply probabilities of 0: cleared before a product reads them
+          ok = ptx::mbar_wait(ptx::smem_u32(&bars->tail), (uint32_t)hg & 1u, lim_ms, a.err);
+          ok = __all_sync(0xffffffffu, ok);
+          zero_rows<D>(smem + C::kQ + qs * C::kTile, len - i * BM);
+          zero_rows<D>(smem + C::kO + os * C::kTile, len - i * BM);
+          if (lane == 0) {
+            ptx::mbar_arrive(ptx::smem_u32(&bars->q_full[qs]));
+            ptx::mbar_arrive(ptx::smem_u32(&bars->o_full[os]));
+          }
+          if (!ok) break;
+        }
         // -LSE as a log2-domain bias (-inf where P must vanish) and D for the tile's rows
         float* lse2 = reinterpret_cast<float*>(smem + C::kVec + vs * 1024);
         float* dl = lse2 + 128;
@@ -385,7 +411,10 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
     const uint32_t sq = (uint32_t)lane & 3u;         // this key within its 4-key dropout block
     DropTest dtest{};
     if constexpr (kDrop) dtest = drop_test(a.drop);
-    for (int hg = 0; hg < G && ok; ++hg)
+    for (int hg = 0; hg < G && ok; ++hg) {
+    float slope = 0.f;                               // of the head's distance bias, log2 domain
+    if constexpr (kScore)
+      if (a.score.slopes != nullptr) slope = __ldg(a.score.slopes + hk * G + hg) * kLog2e;
     for (int i = g.next(g.i_begin); i < g.i_end; i = g.next(i + 1), ++n) {
       const int vs = n & 1;
       // dropout: this key's drop flags over the warpgroup's queries, 16 per word (generated
@@ -417,6 +446,47 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
 #pragma unroll
         for (int hc = 0; hc < kNR; ++hc) ptx::tmem_ld32(tX + hc * 32, raw[hc]);
         ptx::tmem_wait_ld();
+        if constexpr (kScore) {
+#pragma unroll
+          for (int hc = 0; hc < kNR; ++hc) {
+            ptx::reg_fence(raw[hc]);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) p[hc * 32 + e] = __uint_as_float(raw[hc][e]);
+          }
+          uint32_t pk[kCols / 2];
+          const float base = slope * (float)(q0 - key);
+          const float2 m2 = a.score.cap_log2 == 0.f ? c2 : make_float2(a.score.cap_log2, a.score.cap_log2);
+          with_score(p, a.score, [&](auto cap, auto bias) {
+            constexpr int kCap = decltype(cap)::value;
+#pragma unroll
+            for (int col = 0; col < kCols; col += 2) {
+              float2 t = make_float2(p[col], p[col + 1]);
+              if constexpr (kCap != kCapNone) t = tanh_of<kCap>(t, a.score);
+              float2 x = ptx::fma2(t, m2, *reinterpret_cast<const float2*>(lse2 + col));
+              if constexpr (decltype(bias)::value != 0) {
+                x.x = biased(x.x, base, slope, col);
+                x.y = biased(x.y, base, slope, col + 1);
+              }
+              float2 v = make_float2(ptx::ex2(x.x), ptx::ex2(x.y)), w = v;
+              // what dS takes: P times the cap's derivative 1 - tanh^2
+              if constexpr (kCap != kCapNone)
+                w = ptx::mul2(v, ptx::fma2(make_float2(-t.x, -t.y), t, make_float2(1.f, 1.f)));
+              if (kind == kPartial) {
+                const bool seen = !g.causal || key < g.prefix;
+                const bool ok0 = key_ok && (seen || key <= q0 + col), ok1 = key_ok && (seen || key <= q0 + col + 1);
+                v.x = ok0 ? v.x : 0.f;
+                v.y = ok1 ? v.y : 0.f;
+                w.x = ok0 ? w.x : 0.f;
+                w.y = ok1 ? w.y : 0.f;
+              }
+              pk[col / 2] = ptx::pack2<F16>(v.x, v.y);
+              p[col] = w.x;
+              p[col + 1] = w.y;
+            }
+          });
+          ptx::tmem_st(tX, pk);
+          ptx::tmem_wait_st();
+        } else {
 #pragma unroll
         for (int hc = 0; hc < kNR; ++hc) {
           ptx::reg_fence(raw[hc]);
@@ -435,8 +505,9 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
             p[col + 1] = v1;
           }
         }
+        }
       }
-      {
+      if constexpr (!kScore) {
         uint32_t pk[kCols / 2];
 #pragma unroll
         for (int e = 0; e < kCols / 2; ++e) {
@@ -480,7 +551,13 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
               dpv = ptx::mul2(dpv, make_float2(a.drop.scale, a.drop.scale));
             }
             const float2 dd = ptx::sub2(dpv, *reinterpret_cast<const float2*>(dl + col));
-            const float2 ds = ptx::mul2(make_float2(p[col], p[col + 1]), dd);
+            float2 ds = ptx::mul2(make_float2(p[col], p[col + 1]), dd);
+            if constexpr (kScore) {
+              if (kind == kPartial) {                // masked: 0 whatever the key's value holds
+                ds.x = p[col] == 0.f ? 0.f : ds.x;
+                ds.y = p[col + 1] == 0.f ? 0.f : ds.y;
+              }
+            }
             p[col] = ds.x;
             p[col + 1] = ds.y;
           }
@@ -499,6 +576,7 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
         ptx::mbar_arrive(ptx::smem_u32(&bars->ds_ready));
         ptx::mbar_arrive(ptx::smem_u32(&bars->vec_empty[vs]));   // this tile's vectors are read
       }
+    }
     }
     // ------------------------------- epilogue: dV (first half of the warpgroups), dK (second) ---
     const bool have = ok && n > 0;

@@ -36,6 +36,7 @@
 
 #include "dropout_sm103.cuh"
 #include "fa_internal.cuh"
+#include "fa_score.cuh"
 #include "fa_sm103.cuh"
 #include "ptx_sm103.cuh"
 
@@ -73,6 +74,7 @@ struct Bars {             // at most 256 bytes (the live-tile bitmap follows)
   uint64_t dp_full;
   uint64_t ds_ready;
   uint64_t dq_done;
+  uint64_t tail;          // scored variant: the last K tile, before its rows behind the keys are cleared
   uint32_t tmem_base;
 };
 
@@ -82,16 +84,18 @@ enum : int { kNone = 0, kPartial = 1, kFull = 2 };
 
 // Key tiles of one query tile: [0, j_end) bounded by the causal diagonal and the valid key
 // length; a tile mask removes more (then `bits` lists the live ones).
+template <bool kScore>
 struct Geo {
   int i, q0, N, kv_lim, causal, T, j_end;
+  int prefix;             // scored variant: keys every query sees in spite of `causal`
   const uint8_t* bm;
   const uint32_t* bits;
   __device__ int kind(int j) const {
     const int r0 = q0, r1 = min(q0 + BM, N) - 1;
     const int c0 = j * BN, c1 = c0 + BN - 1;
     if (bm != nullptr && bm[(size_t)i * T + j] == 0) return kNone;
-    if (c0 >= kv_lim || (causal && c0 > r1)) return kNone;
-    if (c1 < kv_lim && (!causal || c1 <= r0)) return kFull;
+    if (c0 >= kv_lim || (causal && c0 > r1 && !(kScore && c0 < prefix))) return kNone;
+    if (c1 < kv_lim && (!causal || c1 <= r0 || (kScore && c1 < prefix))) return kFull;
     return kPartial;
   }
   __device__ int next(int j) const {
@@ -105,7 +109,7 @@ struct Geo {
   }
 };
 
-template <int D, bool F16, bool kDrop>
+template <int D, bool F16, bool kDrop, bool kScore>
 __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                     const CUtensorMap& tmV, const CUtensorMap& tmDO,
                                     const BwdArgs& a) {
@@ -131,7 +135,7 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
   const int b = bh / a.H, h = bh % a.H;
   const uint32_t lim_ms = a.dbg.wait_limit_ms;
 
-  Geo g;
+  Geo<kScore> g;
   g.i = a.causal ? n_qt - 1 - it : it;
   g.q0 = g.i * BM;
   int row0 = 0, len = a.N;                       // this slice's rows on the token axis
@@ -155,7 +159,14 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
   g.T = a.n_tiles;
   g.bm = a.block_mask;
   g.j_end = (kvl + BN - 1) / BN;
-  if (a.causal) g.j_end = min(g.j_end, g.i + 1);
+  bool has_tail = false;    // scored variant: the last key tile reaches into memory behind the keys
+  if constexpr (kScore) {
+    g.prefix = a.causal && a.score.prefix != nullptr ? min(max(a.score.prefix[b], 0), len) : 0;
+    if (a.causal) g.j_end = min(g.j_end, max(g.i + 1, (g.prefix + BN - 1) / BN));
+    has_tail = g.j_end * BN > kvl && (a.cu_seqlens != nullptr ? row0 + kvl < a.rows : kvl < a.N);
+  } else {
+    if (a.causal) g.j_end = min(g.j_end, g.i + 1);
+  }
 
   if (threadIdx.x == 0) {
     ptx::mbar_init(ptx::smem_u32(&bars->q_full), 1);
@@ -172,6 +183,7 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
     ptx::mbar_init(ptx::smem_u32(&bars->dp_full), 1);
     ptx::mbar_init(ptx::smem_u32(&bars->ds_ready), L::kComputeWarps);
     ptx::mbar_init(ptx::smem_u32(&bars->dq_done), 1);
+    if constexpr (kScore) ptx::mbar_init(ptx::smem_u32(&bars->tail), 1);
     ptx::fence_mbar_init();
   }
   if (warp == L::kMmaWarp) {
@@ -196,9 +208,9 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
 
   if (warp == L::kProducerWarp) {
     // ------------------------------- TMA producer -----------------------------------------------
+    bool ok = true;
+    int n = 0;
     if (lane == 0 && any) {
-      bool ok = true;
-      int n = 0;
       const uint32_t qb = ptx::smem_u32(&bars->q_full);
       ptx::mbar_arrive_expect_tx(qb, 2 * C::kTile);
       for (int hh = 0; hh < D / 64; ++hh) {
@@ -210,7 +222,8 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
         ok = ptx::mbar_wait(ptx::smem_u32(&bars->k_empty[kslot]), ((uint32_t)(n / C::kKSlots) & 1u) ^ 1u,
                             lim_ms, a.err);
         if (!ok) break;
-        const uint32_t kb = ptx::smem_u32(&bars->k_full[kslot]);
+        const bool tail = has_tail && j == g.j_end - 1;
+        const uint32_t kb = ptx::smem_u32(tail ? &bars->tail : &bars->k_full[kslot]);
         ptx::mbar_arrive_expect_tx(kb, C::kTile);
         for (int hh = 0; hh < D / 64; ++hh)
           ptx::tma_load_3d(sbase + C::kK + kslot * C::kTile + hh * 128 * 128, &tmK, kb, hh * 64, row0 + j * BN, ks);
@@ -222,8 +235,21 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
         for (int hh = 0; hh < D / 64; ++hh)
           ptx::tma_load_3d(sbase + C::kV + vslot * C::kTile + hh * 128 * 128, &tmV, vb, hh * 64, row0 + j * BN, ks);
       }
+    }
+    if constexpr (kScore) {
+      // The last K tile's rows behind the keys multiply dS of 0: cleared before a product that sums
+      // over keys reads the tile (S, which reads it first, is masked).
+      const int issued = __shfl_sync(0xffffffffu, ok ? n : 0, 0);
+      if (has_tail && issued > 0) {
+        const int slot = (issued - 1) % C::kKSlots;
+        ptx::mbar_wait(ptx::smem_u32(&bars->tail), 0, lim_ms, a.err);
+        zero_rows<D>(smem + C::kK + slot * C::kTile, kvl - (g.j_end - 1) * BN);
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->k_full[slot]));
+      }
+    }
+    if (lane == 0 && any) {
       // drain: copies in flight must land before shared memory is released
-      ptx::mbar_wait(qb, 0, lim_ms, a.err);
+      ptx::mbar_wait(ptx::smem_u32(&bars->q_full), 0, lim_ms, a.err);
       for (int m = max(0, n - C::kKSlots); m < n; ++m)
         ptx::mbar_wait(ptx::smem_u32(&bars->k_full[m % C::kKSlots]), (uint32_t)(m / C::kKSlots) & 1u,
                        lim_ms, a.err);
@@ -316,6 +342,9 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
     const float2 nl2 = make_float2(nl, nl);
     const float dd = q < g.N ? a.delta[row] : 0.f;
     const float2 dd2 = make_float2(dd, dd);
+    float slope = 0.f;                               // of the distance bias, log2 domain
+    if constexpr (kScore)
+      if (a.score.slopes != nullptr) slope = a.score.slopes[h] * kLog2e;
     bool ok = true;
     int n = 0;
     const uint32_t tq = (uint32_t)lane & 3u;         // this row within its 4-row dropout block
@@ -345,6 +374,40 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
 #pragma unroll
         for (int hc = 0; hc < kNR; ++hc) ptx::tmem_ld32(tmem + lane_off + sb + hc * 32, raw[hc]);
         ptx::tmem_wait_ld();
+        if constexpr (kScore) {
+#pragma unroll
+          for (int hc = 0; hc < kNR; ++hc) {
+            ptx::reg_fence(raw[hc]);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) p[hc * 32 + e] = __uint_as_float(raw[hc][e]);
+          }
+          const float base = slope * (float)(k0 - q);
+          const float2 m2 = a.score.cap_log2 == 0.f ? c2 : make_float2(a.score.cap_log2, a.score.cap_log2);
+          const int seen = !g.causal ? g.kv_lim : min(g.kv_lim, max(q + 1, g.prefix));   // keys of the row
+          with_score(p, a.score, [&](auto cap, auto bias) {
+            constexpr int kCap = decltype(cap)::value;
+#pragma unroll
+            for (int col = 0; col < kCols; col += 2) {
+              float2 t = make_float2(p[col], p[col + 1]);
+              if constexpr (kCap != kCapNone) t = tanh_of<kCap>(t, a.score);
+              float2 x = ptx::fma2(t, m2, nl2);
+              if constexpr (decltype(bias)::value != 0) {
+                x.x = biased(x.x, base, slope, col);
+                x.y = biased(x.y, base, slope, col + 1);
+              }
+              float2 v = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+              // P times the cap's derivative 1 - tanh^2
+              if constexpr (kCap != kCapNone)
+                v = ptx::mul2(v, ptx::fma2(make_float2(-t.x, -t.y), t, make_float2(1.f, 1.f)));
+              if (kind == kPartial) {
+                v.x = k0 + col < seen ? v.x : 0.f;
+                v.y = k0 + col + 1 < seen ? v.y : 0.f;
+              }
+              p[col] = v.x;
+              p[col + 1] = v.y;
+            }
+          });
+        } else {
 #pragma unroll
         for (int hc = 0; hc < kNR; ++hc) {
           ptx::reg_fence(raw[hc]);
@@ -362,6 +425,7 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
             p[col] = v0;
             p[col + 1] = v1;
           }
+        }
         }
       }
       ok = ptx::mbar_wait(ptx::smem_u32(&bars->dp_full), (uint32_t)n & 1u, lim_ms, a.err);
@@ -392,7 +456,13 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
               dpv = ptx::mul2(dpv, make_float2(a.drop.scale, a.drop.scale));
             }
             const float2 dpd = ptx::sub2(dpv, dd2);
-            const float2 ds = ptx::mul2(make_float2(p[col], p[col + 1]), dpd);
+            float2 ds = ptx::mul2(make_float2(p[col], p[col + 1]), dpd);
+            if constexpr (kScore) {
+              if (kind == kPartial) {                // masked: 0 whatever the key's value holds
+                ds.x = p[col] == 0.f ? 0.f : ds.x;
+                ds.y = p[col + 1] == 0.f ? 0.f : ds.y;
+              }
+            }
             p[col] = ds.x;
             p[col + 1] = ds.y;
           }

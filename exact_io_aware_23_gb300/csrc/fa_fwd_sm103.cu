@@ -28,6 +28,7 @@
 
 #include "dropout_sm103.cuh"
 #include "fa_internal.cuh"
+#include "fa_score.cuh"
 #include "fa_sm103.cuh"
 #include "ptx_sm103.cuh"
 
@@ -66,6 +67,7 @@ struct Bars {            // all mbarriers of one CTA (8 bytes each)
   uint64_t mma_done;
   uint64_t kv_full[8];
   uint64_t kv_empty[8];
+  uint64_t tail;         // scored variant: the last V tile, before its rows behind the keys are cleared
   uint32_t tmem_base;
   int merge_last;        // balanced block-sparse plan: this CTA merges its pair's ranges
 };
@@ -73,6 +75,7 @@ struct Bars {            // all mbarriers of one CTA (8 bytes each)
 static_assert(sizeof(Bars) <= 256, "the live-tile bitmap starts 256 bytes after the barriers");
 
 // Per-CTA tile geometry: which key tiles exist and how each Q tile must treat them.
+template <bool kScore>
 struct Geo {
   int bh;          // (b, h) slice
   int row0;        // first row of the slice on the token axis (packed sequences; else 0)
@@ -85,6 +88,8 @@ struct Geo {
   const uint8_t* bm;
   int T;
   int j_end;       // key tiles [0, j_end) may be live
+  int prefix;      // scored variant: keys every query sees in spite of `causal`
+  bool tail;       // scored variant: the last tile reaches past the keys into other memory
 
   __device__ int kind(int t, int j) const {
     const int r0 = q0 + t * BM;
@@ -92,8 +97,8 @@ struct Geo {
     const int r1 = min(r0 + BM, N) - 1;
     const int c0 = j * BN, c1 = c0 + BN - 1;
     if (bm != nullptr && bm[(size_t)(r0 / BM) * T + j] == 0) return kNone;
-    if (c0 >= kv_lim || (causal && c0 > r1)) return kNone;
-    if (c1 < kv_lim && (!causal || c1 <= r0)) return kFull;
+    if (c0 >= kv_lim || (causal && c0 > r1 && !(kScore && c0 < prefix))) return kNone;
+    if (c1 < kv_lim && (!causal || c1 <= r0 || (kScore && c1 < prefix))) return kFull;
     return kPartial;
   }
   __device__ bool live(int j) const { return kind(0, j) != kNone || kind(1, j) != kNone; }
@@ -113,7 +118,8 @@ struct Geo {
 
 // kPlan: the balanced block-sparse variant (a work plan, split pairs, the last range merging);
 // a separate instantiation, so the others carry none of its code.
-template <int D, bool F16, bool kDrop, bool kPlan>
+// kScore: scores capped, biased or with a prefix (fa_score.cuh); without a tile mask.
+template <int D, bool F16, bool kDrop, bool kPlan, bool kScore>
 __global__ void __launch_bounds__(kThreads, 1)
 fwd_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, FwdArgs a) {
@@ -149,7 +155,7 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const int slot = a.heads_fastest ? unit / BH : unit % n_pairs;
     const int pair = kPlan ? work.x : a.causal ? n_pairs - 1 - slot : slot;
     const int b = bh / a.H, h = bh % a.H;
-    Geo g;
+    Geo<kScore> g;
     g.bh = bh;
     g.split = split;
     g.q0 = pair * 2 * BM;
@@ -170,8 +176,15 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     g.bm = a.block_mask;
     g.T = a.n_tiles;
     int last_key = g.kv_lim;
-    if (a.causal) last_key = min(last_key, min(g.q0 + 2 * BM, g.N));
+    if constexpr (kScore) {
+      g.prefix = a.causal && a.score.prefix != nullptr ? min(max(a.score.prefix[b], 0), g.N) : 0;
+      if (a.causal) last_key = min(last_key, max(min(g.q0 + 2 * BM, g.N), g.prefix));
+    } else {
+      if (a.causal) last_key = min(last_key, min(g.q0 + 2 * BM, g.N));
+    }
     g.j_end = (last_key + BN - 1) / BN;
+    if constexpr (kScore)
+      g.tail = g.j_end * BN > g.kv_lim && (a.cu_seqlens != nullptr ? g.row0 + g.kv_lim < a.rows : g.kv_lim < a.Nk);
     g.j0 = 0;
     if (a.n_splits > 1) {
       g.j0 = min(split * a.tiles_per_split, g.j_end);
@@ -208,7 +221,7 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   if (a.cu_seqlens != nullptr) {
     // Packed sequences: the grid is sized for the longest one; tiles past this sequence's end
     // have nothing to do, and offsets outside the contract are reported, not followed.
-    const Geo g0 = make_geo(false);
+    const auto g0 = make_geo(false);
     if (g0.row0 < 0) {
       if (threadIdx.x == 0) atomicExch(a.err, kDevBadOffsets);
       return;
@@ -224,6 +237,7 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       ptx::mbar_init(ptx::smem_u32(&bars->pv_done[t]), 1);
     }
     ptx::mbar_init(ptx::smem_u32(&bars->mma_done), 1);
+    if constexpr (kScore) ptx::mbar_init(ptx::smem_u32(&bars->tail), 1);
     for (int s = 0; s < C::kSlots; ++s) {
       ptx::mbar_init(ptx::smem_u32(&bars->kv_full[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&bars->kv_empty[s]), 1);
@@ -235,7 +249,7 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     ptx::tmem_relinquish();
   }
   if (a.block_mask != nullptr) {   // live-tile bitmap, one ballot per 32 tiles, words spread over all warps
-    const Geo g = make_geo(false);
+    const auto g = make_geo(false);
     for (int w = warp; w < (g.j_end + 31) / 32; w += kThreads / 32) {
       const int j = w * 32 + lane;
       const uint32_t word = __ballot_sync(0xffffffffu, j < g.j_end && g.live(j));
@@ -249,7 +263,7 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 
   if (warp >= 8) {
     ptx::regs_dec<88>();
-    const Geo g = make_geo(true);
+    const auto g = make_geo(true);
     if (warp == 8 && lane == 0) {
       // ------------------------------- TMA producer -------------------------------------------
       ptx::tma_prefetch_desc(&tmQ);
@@ -278,23 +292,35 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (a.dbg.inject == 1 && m == 0) continue;
         ptx::mbar_wait(ptx::smem_u32(&bars->kv_full[m % C::kKSlots]), (m / C::kKSlots) & 1, lim_ms, a.err);
       }
-    } else if (warp == 10 && lane == 0) {
+    } else if (warp == 10 && (kScore || lane == 0)) {
       // ------------------------------- TMA producer of V ------------------------------------
       // K and V have rings of their own, each with its own producer thread, so a K tile (freed
       // as soon as both S products have read it) is refilled without queueing behind a V slot
       // (freed only after both PV products of the next key tile).
       int n = 0;                                   // V tiles issued
       bool ok = true;
-      for (int j = g.next(g.j0); j < g.j_end && ok; j = g.next(j + 1), ++n) {
+      for (int j = g.next(g.j0); lane == 0 && j < g.j_end && ok; j = g.next(j + 1), ++n) {
         const int slot = C::kKSlots + n % C::kVSlots;
         ok = ptx::mbar_wait(ptx::smem_u32(&bars->kv_empty[slot]), ((n / C::kVSlots) & 1) ^ 1, lim_ms, a.err);
         if (!ok) break;
-        const uint32_t fb = ptx::smem_u32(&bars->kv_full[slot]);
+        const bool tail = kScore && g.tail && j == g.j_end - 1;
+        const uint32_t fb = ptx::smem_u32(tail ? &bars->tail : &bars->kv_full[slot]);
         ptx::mbar_arrive_expect_tx(fb, C::kTileBytes);
         for (int hh = 0; hh < D / 64; ++hh)
           ptx::tma_load_3d(sKV + slot * C::kTileBytes + hh * BN * 128, &tmV, fb, hh * 64, g.row0 + j * BN, g.ks);
       }
-      for (int m = max(0, n - C::kVSlots); m < n; ++m)
+      if constexpr (kScore) {
+        // The last tile's rows behind the keys multiply probabilities of 0: cleared before the
+        // product may read the tile.
+        const int issued = __shfl_sync(0xffffffffu, ok ? n : 0, 0);
+        if (g.tail && issued > 0) {
+          const int slot = C::kKSlots + (issued - 1) % C::kVSlots;
+          ptx::mbar_wait(ptx::smem_u32(&bars->tail), 0, lim_ms, a.err);
+          zero_rows<D>(smem + C::kKVOff + slot * C::kTileBytes, g.kv_lim - (g.j_end - 1) * BN);
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->kv_full[slot]));
+        }
+      }
+      for (int m = max(0, n - C::kVSlots); lane == 0 && m < n; ++m)
         ptx::mbar_wait(ptx::smem_u32(&bars->kv_full[C::kKSlots + m % C::kVSlots]), (m / C::kVSlots) & 1, lim_ms, a.err);
     } else if (warp == 9 && lane == 0) {
       // ------------------------------- MMA issuer ---------------------------------------------
@@ -368,7 +394,7 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   } else {
     // ------------------------------- softmax warpgroups -----------------------------------------
     ptx::regs_inc<200>();
-    const Geo g = make_geo(true);
+    const auto g = make_geo(true);
     const int t = warp / 4;
     const int sub = warp % 4;
     const int r = sub * 32 + lane;                  // TMEM lane == row within the Q tile
@@ -378,7 +404,10 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const uint32_t tO = tmem + lane_off + 256 + t * D;
     const float c = a.scale * kLog2e;               // scores -> log2 domain
     int row_lim = g.kv_lim;
-    if (a.causal) row_lim = min(row_lim, i + 1);
+    if (a.causal) row_lim = min(row_lim, kScore ? max(i + 1, g.prefix) : i + 1);
+    float slope = 0.f;                              // of the distance bias, in the log2 domain
+    if constexpr (kScore)
+      if (a.score.slopes != nullptr) slope = a.score.slopes[g.bh % a.H] * kLog2e;
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     int idx = 0;
@@ -429,6 +458,7 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             for (int e = 0; e < 32; ++e) s[q4 * 32 + e] = __uint_as_float(raw[q4][e]);
           }
         }
+        if constexpr (kScore) score_row(s, a.score, c, slope * (float)(j * BN - i), slope);
         if (kind == kPartial) {
           const int lim = row_lim - j * BN;
 #pragma unroll
@@ -441,7 +471,7 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         for (int q = 8; q < BN / 2; ++q) m8[q & 7] = ptx::max3(m8[q & 7], s[2 * q], s[2 * q + 1]);
         const float mx = ptx::max3(ptx::max3(m8[0], m8[1], m8[2]), ptx::max3(m8[3], m8[4], m8[5]),
                                    fmaxf(m8[6], m8[7]));
-        const float m_cand = mx * c;
+        const float m_cand = kScore ? mx : mx * c;    // scored: already in the log2 domain
         const bool need = m_cand > m_run + kRescaleLog2;   // false when the row is still empty
         const float alpha = need ? ptx::ex2(m_run - m_cand) : 1.f;
         if (__any_sync(0xffffffffu, need) && idx > 0) {
@@ -471,7 +501,8 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         for (int half = 0; half < 2; ++half) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float2 x = ptx::fma2(make_float2(s[half * 64 + 2 * e], s[half * 64 + 2 * e + 1]), c2, nm2);
+            const float2 s2 = make_float2(s[half * 64 + 2 * e], s[half * 64 + 2 * e + 1]);
+            const float2 x = kScore ? ptx::add2(s2, nm2) : ptx::fma2(s2, c2, nm2);
             const float2 pp = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
             ls[e & 3] = ptx::add2(ls[e & 3], pp);      // the normaliser counts every allowed key
             if constexpr (kDrop) {                  // keys 4u + 2h, 4u + 2h + 1 of word half*4 + e/8
@@ -620,7 +651,7 @@ cudaError_t make_map(CUtensorMap* m, const void* base, int D, int N, int BH, boo
                            CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int D, bool F16, bool kDrop, bool kPlan>
+template <int D, bool F16, bool kDrop, bool kPlan, bool kScore = false>
 cudaError_t launch(const FwdArgs& a, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
   // token axis and slice count of the tensor maps: per (b, h) slice, or packed per head
@@ -630,7 +661,7 @@ cudaError_t launch(const FwdArgs& a, cudaStream_t s) {
   if ((e = make_map(&mq, a.q, D, a.rows, q_slices, F16)) != cudaSuccess) return e;
   if ((e = make_map(&mk, a.k, D, packed ? a.rows : a.Nk, kv_slices, F16)) != cudaSuccess) return e;
   if ((e = make_map(&mv, a.v, D, packed ? a.rows : a.Nk, kv_slices, F16)) != cudaSuccess) return e;
-  auto kern = fwd_sm103_kernel<D, F16, kDrop, kPlan>;
+  auto kern = fwd_sm103_kernel<D, F16, kDrop, kPlan, kScore>;
   // + the live-tile bitmap of a block-sparse mask (one bit per key tile)
   const int smem = Cfg<D, F16>::kSmem + (a.block_mask != nullptr ? ((a.n_tiles + 127) / 128) * 16 : 0);
   // The warp groups re-split the CTA's registers (4 warps down to 88, 8 warps up to 200 per
@@ -647,6 +678,12 @@ cudaError_t launch(const FwdArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_fwd_sm103(const FwdArgs& a, fa_dtype dt, cudaStream_t s) {
+  if (a.scored) {
+    // no tile mask, split-KV or dropout with score modifications
+    if (a.drop.enabled || a.block_mask != nullptr || a.n_splits != 1 || a.o_part != nullptr) return cudaErrorInvalidValue;
+    if (dt == FA_FP16) return a.d == 64 ? launch<64, true, false, false, true>(a, s) : launch<128, true, false, false, true>(a, s);
+    return a.d == 64 ? launch<64, false, false, false, true>(a, s) : launch<128, false, false, false, true>(a, s);
+  }
   if (a.drop.enabled) {
     if (a.plan != nullptr) return cudaErrorInvalidValue;     // no plan with dropout
     if (dt == FA_FP16) return a.d == 64 ? launch<64, true, true, false>(a, s) : launch<128, true, true, false>(a, s);

@@ -30,6 +30,16 @@ struct DropoutArgs {
   uint32_t rk0[10], rk1[10];   // the generator's key in each of its ten rounds (host-computed)
 };
 
+// Score modifications (fa_score_mod; see fa_score.cuh).  Zero-initialised: none.
+struct ScoreArgs {
+  float cap_log2;            // softcap * log2(e); 0: no cap
+  float c_exp;               // 2 * scale * log2(e) / softcap
+  float poly_limit;          // raw products up to this size may take the polynomial
+  float poly[7];             // tanh(scale s / softcap) = s * sum_i poly[i] s^(2i)
+  const float* slopes;       // [H] or null
+  const int32_t* prefix;     // [B] or null
+};
+
 struct FwdArgs {
   const void* q;
   const void* k;
@@ -76,6 +86,8 @@ struct FwdArgs {
   int* next_unit;
   const uint32_t* pair_bits;
   int bit_words;
+  int scored;                 // run the variant with score modifications
+  ScoreArgs score;
 };
 
 // The work plan of the balanced block-sparse forward (see FwdArgs::plan).
@@ -132,6 +144,8 @@ struct BwdArgs {
   // perm[x] runs without a plan (dK/dV units of key tile j at j*B*Hkv + slice, then dQ units).
   // Null: that order itself.
   const int* perm;
+  int scored;                 // run the variant with score modifications
+  ScoreArgs score;
 };
 
 // The unit order of the two-pass backward under a tile mask (see BwdArgs::order).

@@ -25,6 +25,7 @@
 #include <math.h>
 
 #include "fa_paged.cuh"
+#include "fa_score.cuh"
 #include "fa_sm103.cuh"
 #include "ptx_sm103.cuh"
 
@@ -237,9 +238,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const PagedArgs a) {
   // ---- the warp's products -----------------------------------------------------------------------
   const int r0 = lane / 4, c0 = (lane % 4) * 2;
   const float c_log2 = a.scale * kLog2e;
-  // cap * tanh(x / cap) = cap - 2 cap / (1 + exp(2 x / cap)), in the log2 domain
-  const float cap2 = a.softcap * kLog2e;
-  const float c_tanh = a.softcap > 0.f ? 2.f * a.scale * kLog2e / a.softcap : 0.f;
   float* const join = reinterpret_cast<float*>(smem + C::kJoin);
   float2* const stat = reinterpret_cast<float2*>(smem + C::kStat);
   int take = 0;                                         // ring slot of the next tile
@@ -276,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const PagedArgs a) {
       for (int e = 0; e < 2; ++e) {
         const int r = row0 + r0 + e * 8, t = r % a.T;
         limit[e] = r < rows && t < count ? seg.len - count + t + 1 : 0;
-        slope[e] = a.slopes != nullptr && r < rows ? a.slopes[hk * G + r / a.T] * kLog2e : 0.f;
+        slope[e] = a.score.slopes != nullptr && r < rows ? a.score.slopes[hk * G + r / a.T] * kLog2e : 0.f;
       }
 #pragma unroll 1
       for (int i = mine; i < n; i += kWarps) {
@@ -310,8 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const PagedArgs a) {
             const int key = key0 + h * 8 + c0 + (e & 1);
             const int lim = limit[e >> 1];
             float x = s[h][e];
-            if (a.softcap > 0.f) x = cap2 - __fdividef(2.f * cap2, 1.f + ptx::ex2(x * c_tanh));
-            else x *= c_log2;
+            x = a.score.cap_log2 != 0.f ? a.score.cap_log2 * tanh_one(x, a.score) : x * c_log2;
             x = fmaf(slope[e >> 1], (float)(key - (lim - 1)), x);
             s[h][e] = key < lim ? x : -INFINITY;
           }

@@ -67,8 +67,7 @@ struct PagedArgs {
   int B, H, Hkv, T, d;
   const int32_t* q_lens;
   float scale;
-  float softcap;             // 0: none
-  const float* slopes;       // [H] or null
+  ScoreArgs score;           // cap and slopes; no prefix
   // fp32 partial results, two slots per CTA: o_part [2 * ctas][16][d] un-normalised, ml_part
   // [2 * ctas][16] = {log2-domain maximum, normaliser}
   float* o_part;

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "fa_paged.cuh"
+#include "fa_score.cuh"
 #include "fa_sm103.cuh"
 
 namespace {
@@ -158,6 +159,8 @@ fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, 
     if (!isfinite(score->softcap) || score->softcap < 0.f || !aligned(score->alibi_slopes, 4)) return FA_ERR_INVALID_ARG;
     if (score->prefix_lens != nullptr) return FA_ERR_UNSUPPORTED;
   }
+  fa::ScoreArgs mods;
+  if (!fa::make_score(score, scale, &mods)) return FA_ERR_UNSUPPORTED;
   st = check_cache(cache, Hkv);
   if (st != FA_OK) return st;
   if (B == 0 || H == 0 || T == 0) return FA_OK;
@@ -173,8 +176,7 @@ fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, 
   a.B = B; a.H = H; a.Hkv = Hkv; a.T = T; a.d = d;
   a.q_lens = q_lens;
   a.scale = scale;
-  a.softcap = score != nullptr ? score->softcap : 0.f;
-  a.slopes = score != nullptr ? score->alibi_slopes : nullptr;
+  a.score = mods;
   a.ctas = fa::paged_ctas(d);
   const size_t parts = fa::paged_parts(a.ctas);
   a.o_part = static_cast<float*>(workspace);

@@ -358,6 +358,37 @@ typedef struct {
 } fa_score_mod;
 
 /*
+ * fa_forward_gqa / fa_backward_gqa (the two-pass backward) and fa_forward_varlen /
+ * fa_backward_varlen with scores as above: the same function and gradients,
+ *     dS = P * (dP - D) * (1 - tanh^2(u / softcap)),  dQ = scale * dS K,  dK = scale * dS^T Q.
+ * score must not be null; with nothing set in it the results are those of the plain calls.  bf16 or
+ * fp16; no block mask, no dropout.  Other arguments, workspaces, errors and ownership as in the
+ * plain calls.  With a modification set, keys and values behind a sequence's valid ones (kv_lens, or
+ * rows of no document or the next one) never reach a result, whatever they hold.
+ * FA_ERR_UNSUPPORTED when softcap or 1 / softcap is too large for fp32 (scale / softcap above
+ * about 1e38).
+ */
+fa_status fa_forward_scored(const void* q, const void* k, const void* v, void* o, float* lse,
+                            int B, int H, int Hkv, int N, int d, float scale, int causal,
+                            fa_dtype dtype, const int32_t* kv_lens, const fa_score_mod* score,
+                            void* stream);
+fa_status fa_backward_scored(const void* q, const void* k, const void* v, const void* o,
+                             const void* dO, const float* lse, void* dq, void* dk, void* dv,
+                             int B, int H, int Hkv, int N, int d, float scale, int causal,
+                             fa_dtype dtype, const int32_t* kv_lens, const fa_score_mod* score,
+                             void* workspace, size_t workspace_bytes, void* stream);
+fa_status fa_forward_varlen_scored(const void* q, const void* k, const void* v, void* o, float* lse,
+                                   const int32_t* cu_seqlens, int n_seqs, int max_seqlen, int total,
+                                   int H, int Hkv, int d, float scale, int causal, fa_dtype dtype,
+                                   const fa_score_mod* score, void* stream);
+fa_status fa_backward_varlen_scored(const void* q, const void* k, const void* v, const void* o,
+                                    const void* dO, const float* lse, void* dq, void* dk, void* dv,
+                                    const int32_t* cu_seqlens, int n_seqs, int max_seqlen, int total,
+                                    int H, int Hkv, int d, float scale, int causal, fa_dtype dtype,
+                                    const fa_score_mod* score, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
  * Rotary positions.  The first rotary_dim values of every head are turned in pairs (a, b) by the
  * angle w = position * inv_freq[p] of their pair p:
  *     (a, b) -> mscale * (a cos w - b sin w, a sin w + b cos w)

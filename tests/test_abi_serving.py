@@ -121,3 +121,39 @@ def test_host_tensors_are_refused():
         fa.append_paged(x, x, pages, pages.clone(), table, n)
     with pytest.raises(ValueError, match="CUDA tensor"):
         fa.forward_paged(x, pages, pages.clone(), table, n)
+
+
+def test_scored_argument_checks():
+    """The score arguments are checked with the plain calls' own checks, and before any launch."""
+    ws = fa.backward_deterministic_workspace_size(2, 8, 100)
+
+    def fwd(mod, dtype=0, H=8, Hkv=2, N=128, d=64, scale=0.125, q=P):
+        return fa.lib.fa_forward_scored(q, P, P, P, P, 2, H, Hkv, N, d, scale, 1, dtype, None, mod, None)
+
+    def bwd(mod, dtype=0, H=8, Hkv=2, N=100, d=64, scale=0.125, q=P, w=P, wsb=ws):
+        return fa.lib.fa_backward_scored(q, P, P, P, P, P, P, P, P, 2, H, Hkv, N, d, scale, 1, dtype, None, mod, w, wsb, None)
+
+    def fwd_v(mod, dtype=0, H=8, Hkv=2, N=100, d=64, scale=0.125, q=P):
+        return fa.lib.fa_forward_varlen_scored(q, P, P, P, P, P, 3, N, N, H, Hkv, d, scale, 1, dtype, mod, None)
+
+    def bwd_v(mod, dtype=0, H=8, Hkv=2, N=100, d=64, scale=0.125, q=P, w=P, wsb=ws):
+        return fa.lib.fa_backward_varlen_scored(q, P, P, P, P, P, P, P, P, P, 3, N, N, H, Hkv, d, scale, 1, dtype, mod, w,
+                                                wsb, None)
+    good = fa.FaScoreMod(30.0, P, P)
+    for call in (fwd, bwd, fwd_v, bwd_v):
+        assert call(None) == INVALID
+        for bad in (-1.0, float("nan"), float("inf")):
+            assert call(fa.FaScoreMod(bad, None, None)) == INVALID
+        assert call(fa.FaScoreMod(0.0, P + 2, None)) == INVALID
+        assert call(fa.FaScoreMod(0.0, None, P + 1)) == INVALID
+        assert call(fa.FaScoreMod(1e-41, None, None)) == UNSUPPORTED       # 1 / softcap beyond fp32
+        assert call(good, dtype=1) == UNSUPPORTED
+        assert call(good, d=96) == UNSUPPORTED
+        assert call(good, Hkv=3) == UNSUPPORTED
+        assert call(good, scale=0.0) == INVALID
+        assert call(good, q=None) == INVALID
+        assert call(good, N=0) == OK
+    for call in (bwd, bwd_v):
+        assert call(good, w=None) == INVALID
+        assert call(good, w=P + 16) == INVALID
+    assert bwd(good, wsb=ws - 4) == INVALID

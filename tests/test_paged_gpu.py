@@ -59,9 +59,8 @@ def _check(q, kc, vc, table, lens, o, lse, cap=0.0, slopes=None, q_lens=None, sc
             g = h // (H // Hkv)
             k, v = (c[pages, g].reshape(-1, d)[:n].double() for c in (kc, vc))
             ro, rl, ot, lt = head_forward(q[b, h].double(), k, v, allowed, dist, scale, cap,
-                                          0.0 if slopes is None else float(slopes[h]), u)
-            if q.dtype == torch.float16:
-                ot = ot + 2.0 ** -25
+                                          0.0 if slopes is None else float(slopes[h]), u,
+                                          2.0 ** -25 if q.dtype == torch.float16 else 0.0)
             assert_within(f"O {b} {h}", o[b, h], ro, ot)
             assert_within(f"LSE {b} {h}", lse[b, h], rl, lt)
 
