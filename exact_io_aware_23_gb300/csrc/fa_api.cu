@@ -465,7 +465,7 @@ fa_status backward_impl(const void* q, const void* k, const void* v, const void*
     if (fa::launch_backward_order(p, s) != cudaSuccess) return FA_ERR_CUDA;
     a.perm = p.perm;
   }
-  cudaError_t e = fa::launch_bwd_preprocess(a, dtype, s);
+  cudaError_t e = a.scored ? fa::launch_delta_sm103(a, dtype, s) : fa::launch_bwd_preprocess(a, dtype, s);
   if (e == cudaSuccess) {
     if (two_pass) {
       e = fa::launch_bwd_split_sm103(a, dtype, s);

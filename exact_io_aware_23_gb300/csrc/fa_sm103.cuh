@@ -27,6 +27,10 @@ cudaError_t launch_bwd_sm103(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
 // is added from several CTAs.
 cudaError_t launch_bwd_split_sm103(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
 
+// D = rowsum(P * dP) of the scored backward (tcgen05 + TMA), d in {64, 128}; takes the place of the
+// preprocess kernel there.
+cudaError_t launch_delta_sm103(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
+
 // Compute layout of the two-pass backward's CTAs (both passes, one launch): kWG compute
 // warpgroups, each over 128 / kWG columns of a 128 x 128 tile, then the producer warp and the
 // MMA-issuing warp.  At d = 64 the tensor work per tile is half that of d = 128 and the compute

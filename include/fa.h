@@ -360,7 +360,8 @@ typedef struct {
 /*
  * fa_forward_gqa / fa_backward_gqa (the two-pass backward) and fa_forward_varlen /
  * fa_backward_varlen with scores as above: the same function and gradients,
- *     dS = P * (dP - D) * (1 - tanh^2(u / softcap)),  dQ = scale * dS K,  dK = scale * dS^T Q.
+ *     dS = P * (dP - D) * (1 - tanh^2(u / softcap)),  dQ = scale * dS K,  dK = scale * dS^T Q,
+ * where D = rowsum(P * dP) is summed in fp32 from the recomputed P (not from O, which is not read).
  * score must not be null; with nothing set in it the results are those of the plain calls.  bf16 or
  * fp16; no block mask, no dropout.  Other arguments, workspaces, errors and ownership as in the
  * plain calls.  With a modification set, keys and values behind a sequence's valid ones (kv_lens, or

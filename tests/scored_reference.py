@@ -16,7 +16,8 @@ error of a score:
   LSE   : max_j e_ij + 2^-22 + 4 v (1 + |LSE|)
   dV    : u |dV| + sum_i (u + f_i) p_ij |dO_i|
   dS_ij : = p (dP - D) c, c = the cap's derivative.  dP adds d products: (d + 2) v sum |dO_c V_c|;
-          D is computed from the O it is given, (d + 2) v sum |dO_c O_c|; c = 1 - tanh^2 is off by
+          D = sum_j p dP takes that error and f_i of each term, and one v for each of its fp32
+          additions in turn; c = 1 - tanh^2 is off by
           2^-20 (twice the tanh's 2^-21, absolutely), and by 2 c e_ij / cap through its argument;
           then one rounding u:
           (u + f_i + 2 e_ij / cap) |dS| + p |dP - D| 2^-20 + p c (the errors of dP and D)
@@ -72,16 +73,18 @@ def head_forward(q, k, v, allowed, dist, scale, cap, slope, u, tiny=0.0):
     return o, lse, o_tol, lse_tol
 
 
-def head_backward(q, k, v, do, o_given, allowed, dist, scale, cap, slope, u, tiny=0.0):
-    """dQ, dK, dV of one head for the O that the backward is given, and their bounds."""
+def head_backward(q, k, v, do, allowed, dist, scale, cap, slope, u, tiny=0.0):
+    """dQ, dK, dV of one head and their bounds."""
     s, c, e = scores(q, k, allowed, dist, scale, cap, slope)
     p, _ = softmax(s)
     f = 2 * (e.amax(-1, keepdim=True) + 2.0 ** -22)
     d = q.shape[-1]
     dp = do @ v.T
-    delta = (do * o_given).sum(-1, keepdim=True)
+    delta = (p * dp).sum(-1, keepdim=True)
     ds = p * (dp - delta) * c
-    dp_err = (d + 2) * V * (do.abs() @ v.abs().T + (do * o_given).abs().sum(-1, keepdim=True))
+    dp_err = (d + 2) * V * (do.abs() @ v.abs().T)
+    # each of the 128-key tiles adds to two pairs of sums 32 times in turn
+    dp_err = dp_err + (p * ((f + 34 * V * max(1, s.shape[-1] // 128)) * dp.abs() + dp_err)).sum(-1, keepdim=True)
     ds_tol = (u + f + (2 * e / cap if cap > 0.0 else 0.0)) * ds.abs() + p * c * dp_err
     if cap > 0.0:
         ds_tol = ds_tol + p * (dp - delta).abs() * 2.0 ** -20

@@ -47,8 +47,7 @@ def _check_sequence(t, out, at, n, nk, prefix, causal, cap, slopes, scale, dtype
             ro, rl, ot, lt = head_forward(pick(q, h).double(), kk, vv, allowed, dist, scale, cap, slope, u, tiny)
             assert_within(f"O {b} {h}", pick(o, h), ro, ot)
             assert_within(f"LSE {b} {h}", pick(lse, h), rl, lt)
-            rq, rk, rv, qt, kt, vt = head_backward(pick(q, h).double(), kk, vv, pick(do, h).double(),
-                                                   pick(o, h).double(), allowed, dist, scale, cap, slope, u, tiny)
+            rq, rk, rv, qt, kt, vt = head_backward(pick(q, h).double(), kk, vv, pick(do, h).double(), allowed, dist, scale, cap, slope, u, tiny)
             # P is rebuilt from the fp32 LSE: its error is one of P's, relative
             assert_within(f"dQ {b} {h}", pick(dq, h), rq, qt)
             for i, x in enumerate((rk, rv, kt, vt)):
