@@ -136,7 +136,7 @@ def _load() -> ctypes.CDLL:
     L.fa_backward_varlen_scored.restype = i
     L.fa_append_paged.argtypes = [cp, vp, st3, vp, st3, vp, st3, vp, i, i, i, i, i, vp, vp, i, i, f, i, vp]
     L.fa_append_paged.restype = i
-    L.fa_forward_paged_workspace_size.argtypes = [i, i, i, i, i]
+    L.fa_forward_paged_workspace_size.argtypes = [i, i, i, i, i, i]
     L.fa_forward_paged_workspace_size.restype = sz
     L.fa_forward_paged.argtypes = [vp, cp, vp, vp, i, i, i, i, i, f, vp, mp, i, vp, sz, vp]
     L.fa_forward_paged.restype = i
@@ -215,11 +215,12 @@ def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool =
     if _scored(softcap, alibi_slopes, prefix_lens):
         if block_mask is not None or dropout_p > 0.0:
             raise ValueError("score modifications take no block mask and no dropout")
-        mod = _score_mod(q, softcap, alibi_slopes, prefix_lens, H, B)
-        _keep(stream, o, lse)
-        st = lib.fa_forward_scored(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Hkv, N, d, scale,
-                                   int(bool(causal)), _DTYPES[q.dtype], _ptr(kv_lens), ctypes.byref(mod),
-                                   _stream(stream))
+        dev = _current_device(q)
+        mod = _score_mod(dev, q, softcap, alibi_slopes, prefix_lens, H, B)
+        st = lib.fa_forward_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H,
+                                   Hkv, N, d, scale, 1 if causal else 0, _DTYPES[q.dtype],
+                                   None if kv_lens is None else kv_lens.data_ptr(), ctypes.byref(mod),
+                                   _handle(stream, dev, o, lse))
         if st != FA_OK:
             raise FaError(st, "fa_forward_scored")
         return o, lse
@@ -285,11 +286,12 @@ def forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, *, causal: bool = False
     o = torch.empty_like(q)
     lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
     if _scored(softcap, alibi_slopes, prefix_lens):
-        mod = _score_mod(q, softcap, alibi_slopes, prefix_lens, H, S)
-        _keep(stream, o, lse)
-        st = lib.fa_forward_varlen_scored(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens), S,
-                                          int(max_seqlen), T, H, Hkv, d, scale, int(bool(causal)),
-                                          _DTYPES[q.dtype], ctypes.byref(mod), _stream(stream))
+        dev = _current_device(q)
+        mod = _score_mod(dev, q, softcap, alibi_slopes, prefix_lens, H, S)
+        st = lib.fa_forward_varlen_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                          cu_seqlens.data_ptr(), S, max_seqlen, T, H, Hkv, d, scale,
+                                          1 if causal else 0, _DTYPES[q.dtype], ctypes.byref(mod),
+                                          _handle(stream, dev, o, lse))
         if st != FA_OK:
             raise FaError(st, "fa_forward_varlen_scored")
         return o, lse
@@ -318,12 +320,14 @@ def backward_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen: int, *, causal:
     need = backward_deterministic_workspace_size(1, H, T)
     workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     if _scored(softcap, alibi_slopes, prefix_lens):
-        mod = _score_mod(q, softcap, alibi_slopes, prefix_lens, H, S)
-        _keep(stream, dq, dk, dv, workspace)
-        st = lib.fa_backward_varlen_scored(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq),
-                                           _ptr(dk), _ptr(dv), _ptr(cu_seqlens), S, int(max_seqlen), T, H, Hkv,
-                                           d, scale, int(bool(causal)), _DTYPES[q.dtype], ctypes.byref(mod),
-                                           _ptr(workspace), workspace.numel(), _stream(stream))
+        dev = _current_device(q)
+        mod = _score_mod(dev, q, softcap, alibi_slopes, prefix_lens, H, S)
+        st = lib.fa_backward_varlen_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+                                           lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                           cu_seqlens.data_ptr(), S, max_seqlen, T, H, Hkv, d, scale,
+                                           1 if causal else 0, _DTYPES[q.dtype], ctypes.byref(mod),
+                                           workspace.data_ptr(), workspace.numel(),
+                                           _handle(stream, dev, dq, dk, dv, workspace))
         if st != FA_OK:
             raise FaError(st, "fa_backward_varlen_scored")
         return dq, dk, dv
@@ -418,18 +422,21 @@ def backward(q, k, v, o, lse, do, *, causal: bool = False, scale: Optional[float
             else backward_workspace_size(B, H, N, d))
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv))
     if _scored(softcap, alibi_slopes, prefix_lens):
         if block_mask is not None or dropout_p > 0.0 or fused:
             raise ValueError("score modifications take no block mask, no dropout and no fused backward")
-        mod = _score_mod(q, softcap, alibi_slopes, prefix_lens, H, B)
-        _keep(stream, dq, dk, dv, workspace)
-        st = lib.fa_backward_scored(*args, B, H, Hkv, N, d, scale, int(bool(causal)), _DTYPES[q.dtype],
-                                    _ptr(kv_lens), ctypes.byref(mod), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream))
+        dev = _current_device(q)
+        mod = _score_mod(dev, q, softcap, alibi_slopes, prefix_lens, H, B)
+        st = lib.fa_backward_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+                                    lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Hkv, N, d,
+                                    scale, 1 if causal else 0, _DTYPES[q.dtype],
+                                    None if kv_lens is None else kv_lens.data_ptr(), ctypes.byref(mod),
+                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                    _handle(stream, dev, dq, dk, dv, workspace))
         if st != FA_OK:
             raise FaError(st, "fa_backward_scored")
         return dq, dk, dv
+    args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv))
     tail = (d, scale, int(bool(causal)), _ptr(block_mask), _DTYPES[q.dtype], _ptr(kv_lens),
             _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
     if dropout_p > 0.0:
@@ -498,47 +505,61 @@ def noalloc_max_workspace() -> int:
     return int(lib.fa_backward_noalloc_max_workspace())
 
 
-# ---- rotary positions and the paged cache ----------------------------------------------------------
+# ---- rotary positions, the paged cache, score modifications ------------------------------------------
+#
+# These calls are made once per layer and token: their host time is most of a short call, so the
+# checks read each property of a tensor once, and names for a message are found only when one is
+# raised.
 
 _STRIDES = ctypes.c_int64 * 3
+_16_BIT = (torch.bfloat16, torch.float16)
 
 
-def _here(name: str, t: torch.Tensor) -> None:
-    """The library launches on the current device: its tensors have to be there."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _refuse_place(**tensors) -> None:
+    """The library launches on the current device: says which tensor is not there."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
-def _keep(stream, *tensors) -> None:
-    """Memory allocated here is not reused before a call on another stream has read it."""
-    if stream is not None and stream != torch.cuda.current_stream():
-        for t in tensors:
-            t.record_stream(stream)
+def _current_device(t: torch.Tensor) -> int:
+    """The current device's index, when t is there; -1 otherwise (tensors elsewhere give -1 too)."""
+    dev = t.get_device()
+    return dev if dev >= 0 and dev == torch._C._cuda_getDevice() else -1
 
 
-def _heads_last(name: str, t: torch.Tensor, dtype, shape) -> "ctypes.Array":
-    """Strides (batch, head, token) of a [B, heads, N, d] tensor whose last axis adjoins."""
-    _here(name, t)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {dtype} {list(shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"the values of a head must adjoin in {name}")
-    return _STRIDES(t.stride(0), t.stride(1), t.stride(2))
+def _handle(stream, dev: int, *allocated) -> int:
+    """The stream's handle.  Memory allocated here for a call on a stream that is not the current one
+    is not reused before that stream is done with it."""
+    current = torch._C._cuda_getCurrentRawStream(dev)
+    if stream is None or stream.cuda_stream == current:
+        return current
+    for t in allocated:
+        t.record_stream(stream)
+    return stream.cuda_stream
 
 
 def _int32(name: str, t: torch.Tensor, shape) -> None:
-    _here(name, t)
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
 
 
-def _frequencies(inv_freq: Optional[torch.Tensor]) -> int:
+def _strides(name: str, t: torch.Tensor) -> "ctypes.Array":
+    """Strides (batch, head, token) of a [B, heads, N, d] tensor whose last axis adjoins."""
+    b, h, n, last = t.stride()
+    if last != 1:
+        raise ValueError(f"the values of a head must adjoin in {name}")
+    return _STRIDES(b, h, n)
+
+
+def _rotated(inv_freq: Optional[torch.Tensor]) -> int:
     """The rotated values of a head (0: none)."""
     if inv_freq is None:
         return 0
-    _here("inv_freq", inv_freq)
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 [rotary_dim / 2] tensor")
     return 2 * inv_freq.numel()
@@ -600,28 +621,39 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, factor: float 
 
 
 def _rotary(fn, where, x, positions, inv_freq, interleaved, mscale, out, stream):
-    if x.dim() not in (3, 4):
+    dev = _current_device(x)
+    if dev < 0 or positions.get_device() != dev or inv_freq.get_device() != dev:
+        _refuse_place(x=x, positions=positions, inv_freq=inv_freq)
+    shape, dtype = x.shape, x.dtype
+    if len(shape) == 4:
+        B, H, N, d = shape
+        x4 = x
+    elif len(shape) == 3:
+        H, N, d = shape
+        B, x4 = 1, x.unsqueeze(0)
+    else:
         raise ValueError("x must be [B, H, N, d] or [H, N, d]")
-    x4 = x if x.dim() == 4 else x.unsqueeze(0)
-    B, H, N, d = x4.shape
-    if x.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {x.dtype}")
-    xs = _heads_last("x", x4, x.dtype, x4.shape)
-    rot = _frequencies(inv_freq)
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    xs = _strides("x", x4)
+    rot = _rotated(inv_freq)
     per_batch = positions.dim() == 2
     _int32("positions", positions, (B, N) if per_batch else (N,))
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        _keep(stream, out)
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+        ys = _STRIDES(H * N * d, N * d, d)
+        s = _handle(stream, dev, out)
     else:
-        if out.shape != x.shape:
-            raise ValueError("out must have x's shape")
+        _refuse_place(out=out)
+        if out.shape != shape or out.dtype != dtype:
+            raise ValueError("out must have x's shape and type")
         _written("out", out)
         _apart("x", x, "out", out, True)
-    y4 = out if out.dim() == 4 else out.unsqueeze(0)
-    ys = _heads_last("out", y4, x.dtype, x4.shape)
+        ys = _strides("out", out if len(shape) == 4 else out.unsqueeze(0))
+        s = _handle(stream, dev)
     st = fn(x.data_ptr(), xs, out.data_ptr(), ys, B, H, N, d, positions.data_ptr(), N if per_batch else 0,
-            inv_freq.data_ptr(), rot, int(bool(interleaved)), float(mscale), _DTYPES[x.dtype], _stream(stream))
+            inv_freq.data_ptr(), rot, 1 if interleaved else 0, mscale, code, s)
     if st != FA_OK:
         raise FaError(st, where)
     return out
@@ -647,24 +679,25 @@ def rotary_backward(dy: torch.Tensor, positions: torch.Tensor, inv_freq: torch.T
 
 def _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, dtype) -> FaPagedCache:
     """Checks a paged cache ([n_pages, Hkv, page_size, d], any strides) and says where it lies."""
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _here(name, t)
-        if t.dim() != 4 or t.dtype != dtype or t.shape[1] != Hkv or t.shape[3] != d:
-            raise ValueError(f"{name} must be {dtype} [n_pages, {Hkv}, page_size, {d}]")
-        if t.stride(3) != 1:
-            raise ValueError(f"the values of a head must adjoin in {name}")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or shape[1] != Hkv or shape[3] != d or k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise ValueError(f"k_cache and v_cache must be {dtype} [n_pages, {Hkv}, page_size, {d}]")
+    if strides[3] != 1:
+        raise ValueError("the values of a head must adjoin in k_cache")
+    if v_cache.shape != shape or v_cache.stride() != strides:
         raise ValueError("k_cache and v_cache must have the same shape and strides")
-    _here("block_table", block_table)
-    if (block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B
-            or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
-        raise ValueError(f"block_table must be int32 [{B}, max_pages], a row's entries adjoining")
-    _int32("kv_lens", kv_lens, (B,))
-    n_pages, _, page_size, _ = k_cache.shape
-    s0, s1, s2, _ = k_cache.stride()
-    width = block_table.shape[1]
-    return FaPagedCache(k_cache.data_ptr(), v_cache.data_ptr(), s0, s1, s2, n_pages, page_size,
-                        block_table.data_ptr(), max(block_table.stride(0), width), width, kv_lens.data_ptr())
+    tshape = block_table.shape
+    if block_table.dtype != torch.int32 or len(tshape) != 2 or tshape[0] != B:
+        raise ValueError(f"block_table must be int32 [{B}, max_pages]")
+    row, entry = block_table.stride()
+    width = tshape[1]
+    if width > 1 and entry != 1:
+        raise ValueError("the entries of a row must adjoin in block_table")
+    if kv_lens.dtype != torch.int32 or kv_lens.shape != (B,) or not kv_lens.is_contiguous():
+        raise ValueError(f"kv_lens must be a contiguous int32 [{B}] tensor")
+    return FaPagedCache(k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], shape[0],
+                        shape[2], block_table.data_ptr(), row if B > 1 and row > width else width, width,
+                        kv_lens.data_ptr())
 
 
 def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -677,58 +710,72 @@ def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     counts the new tokens already; q_lens (int32 [B]) says how many of the T are real (default all).
     k_cache, v_cache: [n_pages, Hkv, page_size, d], any strides whose last axis adjoins;
     block_table: int32 [B, max_pages]."""
-    if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float16):
+    dev = _current_device(k)
+    if (dev < 0 or v.get_device() != dev or k_cache.get_device() != dev or v_cache.get_device() != dev
+            or block_table.get_device() != dev or kv_lens.get_device() != dev
+            or (q is not None and q.get_device() != dev) or (q_lens is not None and q_lens.get_device() != dev)
+            or (inv_freq is not None and inv_freq.get_device() != dev)):
+        _refuse_place(k=k, v=v, k_cache=k_cache, v_cache=v_cache, block_table=block_table, kv_lens=kv_lens,
+                      q=q, q_lens=q_lens, inv_freq=inv_freq)
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 4 or dtype not in _16_BIT:
         raise ValueError("k must be bf16 or fp16 [B, Hkv, T, d]")
-    B, Hkv, T, d = k.shape
-    ks = _heads_last("k", k, k.dtype, k.shape)
-    vs = _heads_last("v", v, k.dtype, k.shape)
-    cache = _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, k.dtype)
-    _written("k_cache", k_cache)
-    rot = _frequencies(inv_freq)
+    if v.shape != shape or v.dtype != dtype:
+        raise ValueError("v must have k's shape and type")
+    B, Hkv, T, d = shape
+    cache = _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, dtype)
+    if 0 in k_cache.stride():
+        _written("k_cache", k_cache)
+    rot = _rotated(inv_freq)
     if q_lens is not None:
         _int32("q_lens", q_lens, (B,))
     H, qs = Hkv, None
+    s = None
     if q is not None:
-        H = q.shape[1] if q.dim() == 4 else 0
-        if Hkv == 0 or H % Hkv != 0 or H == 0:
-            raise ValueError("k, v must be [B, Hkv, T, d] with Hkv dividing the query heads")
-        qs = _heads_last("q", q, k.dtype, (B, H, T, d))
+        qshape = q.shape
+        H = qshape[1] if len(qshape) == 4 else 0
+        if Hkv == 0 or H == 0 or H % Hkv != 0 or qshape != (B, H, T, d) or q.dtype != dtype:
+            raise ValueError("q must be [B, H, T, d] of k's type, the key heads dividing H")
+        qs = _strides("q", q)
         if q_out is None:
-            q_out = torch.empty((B, H, T, d), dtype=q.dtype, device=q.device)
-            _keep(stream, q_out)
+            q_out = torch.empty(qshape, dtype=dtype, device=k.device)
+            s = _handle(stream, dev, q_out)
         else:
-            if q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
+            _refuse_place(q_out=q_out)
+            if q_out.shape != qshape or q_out.dtype != dtype or not q_out.is_contiguous():
                 raise ValueError("q_out must be contiguous, of q's shape and type")
-            _here("q_out", q_out)
             _apart("q", q, "q_out", q_out, True)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    st = lib.fa_append_paged(ctypes.byref(cache), k.data_ptr(), ks, v.data_ptr(), vs,
+    if s is None:
+        s = _handle(stream, dev)
+    st = lib.fa_append_paged(ctypes.byref(cache), k.data_ptr(), _strides("k", k), v.data_ptr(), _strides("v", v),
                              None if q is None else q.data_ptr(), _STRIDES() if qs is None else qs,
                              None if q_out is None else q_out.data_ptr(), B, H, Hkv, T, d,
                              None if q_lens is None else q_lens.data_ptr(),
                              None if inv_freq is None else inv_freq.data_ptr(), rot,
-                             int(bool(interleaved)), float(mscale), _DTYPES[k.dtype], _stream(stream))
+                             1 if interleaved else 0, mscale, _DTYPES[dtype], s)
     if st != FA_OK:
         raise FaError(st, "fa_append_paged")
     return q_out
 
 
-def forward_paged_workspace_size(B: int, H: int, Hkv: int, T: int, d: int) -> int:
-    return int(lib.fa_forward_paged_workspace_size(B, H, Hkv, T, d))
+def forward_paged_workspace_size(B: int, H: int, Hkv: int, T: int, d: int, max_keys: int) -> int:
+    """max_keys: entries of a block table's row times the page size."""
+    return int(lib.fa_forward_paged_workspace_size(B, H, Hkv, T, d, max_keys))
 
 
-def _score_mod(q, softcap, alibi_slopes, prefix_lens, H, n_seqs) -> FaScoreMod:
+def _score_mod(dev, q, softcap, alibi_slopes, prefix_lens, H, n_seqs) -> FaScoreMod:
     """Checks the score arguments; slopes fp32 [H], prefix lengths int32 [n_seqs]."""
-    _here("q", q)
-    if alibi_slopes is not None:
-        _here("alibi_slopes", alibi_slopes)
-        if (alibi_slopes.dtype != torch.float32 or tuple(alibi_slopes.shape) != (H,)
-                or not alibi_slopes.is_contiguous()):
-            raise ValueError(f"alibi_slopes must be a contiguous float32 [{H}] tensor")
+    if (dev < 0 or (alibi_slopes is not None and alibi_slopes.get_device() != dev)
+            or (prefix_lens is not None and prefix_lens.get_device() != dev)):
+        _refuse_place(q=q, alibi_slopes=alibi_slopes, prefix_lens=prefix_lens)
+    if alibi_slopes is not None and (alibi_slopes.dtype != torch.float32 or alibi_slopes.shape != (H,)
+                                     or not alibi_slopes.is_contiguous()):
+        raise ValueError(f"alibi_slopes must be a contiguous float32 [{H}] tensor")
     if prefix_lens is not None:
         _int32("prefix_lens", prefix_lens, (n_seqs,))
-    return FaScoreMod(float(softcap), None if alibi_slopes is None else alibi_slopes.data_ptr(),
+    return FaScoreMod(softcap, None if alibi_slopes is None else alibi_slopes.data_ptr(),
                       None if prefix_lens is None else prefix_lens.data_ptr())
 
 
@@ -743,40 +790,52 @@ def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     ``append_paged``.  Token t of a sequence's n new ones sees the keys up to its own place
     kv_lens - n + t; scores capped by softcap * tanh(. / softcap) when softcap > 0 and lowered by
     alibi_slopes[h] (fp32 [H]) times the distance."""
-    if q.dim() != 4 or q.dtype not in (torch.bfloat16, torch.float16) or not q.is_contiguous():
+    dev = _current_device(q)
+    if (dev < 0 or k_cache.get_device() != dev or v_cache.get_device() != dev
+            or block_table.get_device() != dev or kv_lens.get_device() != dev
+            or (q_lens is not None and q_lens.get_device() != dev)):
+        _refuse_place(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, kv_lens=kv_lens, q_lens=q_lens)
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 4 or dtype not in _16_BIT or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 or fp16 [B, H, T, d] tensor")
-    B, H, T, d = q.shape
+    B, H, T, d = shape
     Hkv = k_cache.shape[1] if k_cache.dim() == 4 else 0
     if Hkv == 0 or H % Hkv != 0:
         raise ValueError("k_cache must be [n_pages, Hkv, page_size, d] with Hkv dividing the query heads")
-    cache = _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, q.dtype)
+    cache = _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, dtype)
     if q_lens is not None:
         _int32("q_lens", q_lens, (B,))
-    mod = _score_mod(q, softcap, alibi_slopes, None, H, B)
-    scale = 1.0 / d ** 0.5 if scale is None else float(scale)
+    mod = _score_mod(dev, q, softcap, alibi_slopes, None, H, B)
+    device = q.device
+    mine = []
     if o is None:
-        o = torch.empty((B, H, T, d), dtype=q.dtype, device=q.device)
-        _keep(stream, o)
+        o = torch.empty_like(q)
+        mine.append(o)
     else:
-        if o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous():
+        _refuse_place(o=o)
+        if o.shape != shape or o.dtype != dtype or not o.is_contiguous():
             raise ValueError("o must be contiguous, of q's shape and type")
-        _here("o", o)
         _apart("q", q, "o", o, False)
     if lse is None:
-        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
-        _keep(stream, lse)
+        lse = torch.empty((B, H, T), dtype=torch.float32, device=device)
+        mine.append(lse)
     else:
-        if tuple(lse.shape) != (B, H, T) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        _refuse_place(lse=lse)
+        if lse.shape != (B, H, T) or lse.dtype != torch.float32 or not lse.is_contiguous():
             raise ValueError("lse must be contiguous float32 [B, H, T]")
-        _here("lse", lse)
     if workspace is None:
-        need = forward_paged_workspace_size(B, H, Hkv, T, d)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-        _keep(stream, workspace)
+        need = lib.fa_forward_paged_workspace_size(B, H, Hkv, T, d, min(cache.max_pages * cache.page_size, 0x7fffffff))
+        if need > 0:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=device)
+            mine.append(workspace)
+    else:
+        _refuse_place(workspace=workspace)
     st = lib.fa_forward_paged(q.data_ptr(), ctypes.byref(cache), o.data_ptr(), lse.data_ptr(), B, H, Hkv, T, d,
-                              scale, None if q_lens is None else q_lens.data_ptr(), ctypes.byref(mod),
-                              _DTYPES[q.dtype], workspace.data_ptr(),
-                              workspace.numel() * workspace.element_size(), _stream(stream))
+                              1.0 / d ** 0.5 if scale is None else scale,
+                              None if q_lens is None else q_lens.data_ptr(), ctypes.byref(mod), _DTYPES[dtype],
+                              None if workspace is None else workspace.data_ptr(),
+                              0 if workspace is None else workspace.numel() * workspace.element_size(),
+                              _handle(stream, dev, *mine))
     if st != FA_OK:
         raise FaError(st, "fa_forward_paged")
     return o, lse

@@ -24,6 +24,9 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <atomic>
+#include <chrono>
+
 #include "fa_paged.cuh"
 #include "fa_score.cuh"
 #include "fa_sm103.cuh"
@@ -32,29 +35,40 @@
 namespace fa {
 namespace {
 
-constexpr int kWarps = 4;
+#ifndef PAGED_W
+#define PAGED_W 4
+#define PAGED_K64 32
+#define PAGED_K128 16
+#endif
+constexpr int kWarps = PAGED_W;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 16;                  // query rows of a block: one mma's
-constexpr int kKeys = 16;                  // keys of a tile
+constexpr int kCtasPerSm = 8 / kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleLog2 = 8.0f;       // the running maximum is raised when a score exceeds it by more
 
 template <int D>
 struct Cfg {
+  static constexpr int kKeys = D == 128 ? PAGED_K128 : PAGED_K64;   // keys of a tile
+  static constexpr int kParts = kKeys / 16;                   // 16-key parts of a tile, each in one page
   static constexpr int kRowBytes = D * 2;
   static constexpr int kHalf = kKeys * kRowBytes;             // a tile's keys (or values)
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = D == 128 ? 5 : 10;           // 160 KB of tiles a CTA
+  static constexpr int kStages = 192 * 1024 / kCtasPerSm / (kWarps * kStage);   // 192 KB of tiles a CTA
   static constexpr int kRing = kStages * kStage;              // per warp
-  static constexpr int kPitch = D + 8;                        // floats of a row to be joined
-  static constexpr int kJoin = kWarps * kRing;
-  static constexpr int kStat = kJoin + kWarps * kRows * kPitch * 4;
-  static constexpr int kSmem = kStat + kWarps * kRows * 8;
+  static constexpr int kStat = kWarps * kRing;
+  static constexpr int kFrom = kStat + kWarps * kRows * 8;
+  static constexpr int kSmem = kFrom + kWarps * 4 + 16;         // and a flag
+  static_assert(kStage >= kRows * D * 4, "a warp's output to be joined fits the slot of its last tile");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
   const int n = there ? 16 : 0;            // 0: the 16 bytes are filled with zeros, nothing is read
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -70,7 +84,7 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
 }
 // c (16 x 8, fp32) += a (16 x 16) b (16 x 8)
 template <bool F16>
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma(float* c, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (F16)
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -81,153 +95,293 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Tiles of sequence b, per key head and row block.
+// ---- sharing the work ------------------------------------------------------------------------------
+//
+// A segment is one (sequence, key head, row block).  It counts kSegment units for what it costs
+// whatever its length (its queries, the join of the warps; about as long as the CTA takes for that
+// many tiles), then one per tile; unit numbers run over all segments, and each CTA takes an equal
+// range of them.
+constexpr int kSegment = 4;
+constexpr int kMinUnits = kSegment + kWarps;   // a smaller share costs more in joining than it saves
+
+__host__ __device__ inline int sharing_ctas(int units, int ctas) {
+  const int want = (units + kMinUnits - 1) / kMinUnits;
+  return want < 1 ? 1 : want > ctas ? ctas : want;
+}
+// CTA c's range begins at c * q + min(c, r) for units = n * q + r
+struct Shares {
+  int q, r;
+  __device__ Shares(int units, int n) : q(units / n), r(units % n) {}
+  __device__ int begin(int c) const { return c * q + min(c, r); }
+  __device__ int owner(int u) const { return u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q; }
+};
+
+template <int kKeys>
 __device__ __forceinline__ int tiles_of(const PagedArgs& a, int b, int* err) {
   if (new_tokens(a.q_lens, b, a.T) == 0) return 0;
   return (paged_len(a.cache, b, err) + kKeys - 1) / kKeys;
 }
+template <int kKeys>
+__device__ __forceinline__ int units_of(const PagedArgs& a, int heads, int b, int* err) {
+  const int n = b < a.B ? tiles_of<kKeys>(a, b, err) : 0;
+  return n > 0 ? (n + kSegment) * heads : 0;
+}
 
-// The tiles of all sequences, and where sequence `b` (or tile `at`) lies among them; every warp
-// reckons for itself.
-struct Place {
-  int b;              // sequence
-  int64_t before;     // tiles before it
-};
-__device__ __forceinline__ int64_t warp_total(int64_t x) {
+// A warp's reckoning of all sequences' units: the first 256 sequences' stay in registers (all their
+// lengths are read at once), further ones are read again.
+template <int kKeys>
+struct Reckoning {
+  int keep[8];
+  int total;
+  __device__ Reckoning(const PagedArgs& a, int heads, int* err) {
+    const int lane = threadIdx.x % 32;
+    int sum = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-__device__ int64_t all_tiles(const PagedArgs& a, int heads, int* err) {
-  const int lane = threadIdx.x % 32;
-  int64_t sum = 0;
-  for (int b = lane; b < a.B; b += 32) sum += tiles_of(a, b, err);
-  return warp_total(sum) * heads;
-}
-// The sequence that holds tile `at`, which is below the total.
-__device__ Place find_tile(const PagedArgs& a, int heads, int64_t at) {
-  const int lane = threadIdx.x % 32;
-  int64_t before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int64_t n = b0 + lane < a.B ? (int64_t)tiles_of(a, b0 + lane, nullptr) * heads : 0;
-    int64_t sum = n;                                   // inclusive scan
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += up;
+    for (int c = 0; c < 8; ++c) {
+      keep[c] = units_of<kKeys>(a, heads, c * 32 + lane, err);
+      sum += keep[c];
     }
-    const uint32_t past = __ballot_sync(0xffffffffu, before + sum > at);
-    if (past != 0u) {
-      const int l = __ffs(past) - 1;
-      Place p;
-      p.b = b0 + l;
-      p.before = before + __shfl_sync(0xffffffffu, sum - n, l);
-      return p;
-    }
-    before += __shfl_sync(0xffffffffu, sum, 31);
+    for (int b = 256 + lane; b < a.B; b += 32) sum += units_of<kKeys>(a, heads, b, err);
+    total = __reduce_add_sync(0xffffffffu, sum);
   }
-  return Place{a.B, before};
-}
+  // The sequence that holds unit u, and the units before it.
+  __device__ void find(const PagedArgs& a, int heads, int u, int* b, int* before) const {
+    const int lane = threadIdx.x % 32;
+    int done = 0;
+    auto chunk = [&](int n, int b0) {
+      int sum = n;                                     // inclusive scan
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, done + sum > u);
+      if (past != 0u) {
+        const int l = __ffs(past) - 1;
+        *b = b0 + l;
+        *before = done + __shfl_sync(0xffffffffu, sum - n, l);
+        return true;
+      }
+      done += __shfl_sync(0xffffffffu, sum, 31);
+      return false;
+    };
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (chunk(keep[c], c * 32)) return;
+    for (int b0 = 256; b0 < a.B; b0 += 32)
+      if (chunk(units_of<kKeys>(a, heads, b0 + lane, nullptr), b0)) return;
+  }
+};
 
-// CTAs that share `total` tiles: each gets at least kMinTiles (one per warp and then some: a share
-// too small costs more in joining than it saves), none more than the grid has.
-constexpr int kMinTiles = 8;
-__host__ __device__ inline int sharing_ctas(int64_t total, int ctas) {
-  const int64_t want = (total + kMinTiles - 1) / kMinTiles;
-  return want < 1 ? 1 : want > ctas ? ctas : (int)want;
-}
-__host__ __device__ inline int64_t share_begin(int64_t total, int n, int c) { return total * c / n; }
-
-// A (sequence, key head, row block) and a tile in it; advances over empty sequences.
+// A segment and a tile in it.  The next sequence's lengths are read ahead.
+template <int kKeys>
 struct Walk {
-  int b, hr, tile, tiles, len;
-  __device__ void enter(const PagedArgs& a) {          // at hr = 0 of b, or past the end
-    while (b < a.B) {
-      len = paged_len(a.cache, b, nullptr);
-      tiles = new_tokens(a.q_lens, b, a.T) == 0 ? 0 : (len + kKeys - 1) / kKeys;
-      if (tiles > 0) return;
-      ++b;
-    }
-    tiles = 1 << 30;
+  int b, hk, block, tile, tiles, len, count;
+  int ahead_len, ahead_q;                              // of sequence b + 1, as stored
+  __device__ void read_ahead(const PagedArgs& a) {
+    const int n = b + 1;
+    ahead_len = n < a.B ? a.cache.kv_lens[n] : 0;
+    ahead_q = n < a.B && a.q_lens != nullptr ? a.q_lens[n] : a.T;
   }
-  __device__ void next_segment(const PagedArgs& a, int heads) {
-    if (++hr == heads) {
-      hr = 0;
+  __device__ void take(const PagedArgs& a, int kv, int q) {
+    len = kv > paged_capacity(a.cache) ? 0 : max(kv, 0);
+    count = min(max(q, 0), a.T);
+    tiles = count == 0 ? 0 : (len + kKeys - 1) / kKeys;
+  }
+  __device__ void start(const PagedArgs& a, int seq) {
+    b = seq;
+    hk = block = tile = 0;
+    take(a, a.cache.kv_lens[b], a.q_lens != nullptr ? a.q_lens[b] : a.T);
+    read_ahead(a);
+  }
+  // to the next segment with tiles; past the last one, tiles is beyond any tile number
+  __device__ void next(const PagedArgs& a, int blocks) {
+    if (++block < blocks) return;
+    block = 0;
+    if (++hk < a.Hkv) return;
+    hk = 0;
+    do {
       ++b;
-      enter(a);
-    }
+      if (b >= a.B) {
+        tiles = 1 << 30;
+        return;
+      }
+      take(a, ahead_len, ahead_q);
+      read_ahead(a);
+    } while (tiles == 0);
   }
 };
+
+// O = 0 and LSE = -inf for rows [row, row + n)
+template <int D>
+__device__ __forceinline__ void no_keys(const PagedArgs& a, int64_t row, int n) {
+  for (int x = threadIdx.x; x < n * (D / 4); x += kThreads) {
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + row * D)[x] = make_uint2(0u, 0u);
+    if (x < n) a.lse[row + x] = -INFINITY;
+  }
+}
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads, 1) paged_kernel(const PagedArgs a) {
+__device__ __forceinline__ void write_row4(const PagedArgs& a, int64_t row, int c, float4 acc, float sum, float mx) {
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + row * D + c) =
+      make_uint2(ptx::pack2<F16>(acc.x * inv, acc.y * inv), ptx::pack2<F16>(acc.z * inv, acc.w * inv));
+  if (c == 0) a.lse[row] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// Announces this CTA's part of a segment that CTAs ca..cb share, and says whether all of them are
+// there; run by one warp.  Every part has a word of its own, set to the call's number: no atomic
+// that 38 CTAs contend for (counting them in one word by compare-and-swap took 18 us at the end of
+// B1 H32 Hkv8 with 32K keys).  Between its own store and its reads of the others each CTA has a
+// sequentially consistent fence, so the last of them sees all words set, or cleared by one that did;
+// should two see them, both join the parts, to the same bits.  Who joins clears the words, for a
+// captured call's next run under the same number.  Whatever else a fresh workspace holds is not the
+// number: it has 64 bits, starts at another place in every process, and is not used twice in one.
+// So no launch is spent on clearing the words first.  (By cudaMemsetAsync: 3 us of a call's 40.)
+__device__ __forceinline__ bool all_arrived(unsigned long long* words, int mine, int part0, int ca, int cb,
+                                            unsigned long long call) {
+  const int lane = threadIdx.x % 32;
+  if (lane == 0) asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(words + mine), "l"(call) : "memory");
+  __syncwarp();
+  asm volatile("fence.sc.gpu;" ::: "memory");
+  bool there = true;
+  for (int i = ca + lane; i <= cb; i += 32) {
+    unsigned long long w;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(w) : "l"(words + (i == ca ? part0 : 2 * i)) : "memory");
+    there = there && w == call;
+  }
+  there = __all_sync(0xffffffffu, there);
+  if (there) {
+    asm volatile("fence.acq_rel.gpu;" ::: "memory");
+    for (int i = ca + lane; i <= cb; i += 32)
+      asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(words + (i == ca ? part0 : 2 * i)), "l"(0ull) : "memory");
+  }
+  return there;
+}
+
+// kShared: CTAs share all segments' units.  Otherwise a CTA has one segment to itself (few short
+// ones: nothing to join, nothing to reckon).
+template <int D, bool F16, bool kShared>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const PagedArgs a) {
   using C = Cfg<D>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int kKeys = C::kKeys, kParts = C::kParts, kQuads = D / 4;
+  extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int G = a.H / a.Hkv, rows = G * a.T;
   const int blocks = (rows + kRows - 1) / kRows;       // row blocks of a key head
   const int heads = a.Hkv * blocks;
-  asm volatile("griddepcontrol.launch_dependents;");   // the joining kernel may be set up meanwhile
 
-  const int64_t total = all_tiles(a, heads, blockIdx.x == 0 && warp == 0 ? a.err : nullptr);
-  const int n_ctas = sharing_ctas(total, gridDim.x);
-  if ((int)blockIdx.x >= n_ctas || total == 0) return;
-  const int64_t begin = share_begin(total, n_ctas, blockIdx.x);
-  const int64_t end = share_begin(total, n_ctas, blockIdx.x + 1);
-  Walk seg;
-  {
-    const Place p = find_tile(a, heads, begin);
-    seg.b = p.b;
-    seg.hr = 0;
-    seg.enter(a);
-    const int64_t off = begin - p.before;
-    seg.hr = (int)(off / seg.tiles);
-    seg.tile = (int)(off % seg.tiles);
+  Walk<kKeys> seg;
+  int units = 0, n_ctas = 1, s0 = 0;                   // s0: the segment's first unit
+  int begin = 0, end = 0;                              // the CTA's units
+  if constexpr (kShared) {
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+      if (tiles_of<kKeys>(a, b, nullptr) == 0) no_keys<D>(a, (int64_t)b * a.H * a.T, a.H * a.T);
+    const Reckoning<kKeys> all(a, heads, blockIdx.x == 0 && warp == 0 ? a.err : nullptr);
+    units = all.total;
+    n_ctas = sharing_ctas(units, gridDim.x);
+    if ((int)blockIdx.x >= n_ctas || units == 0) return;
+    const Shares share(units, n_ctas);
+    begin = share.begin(blockIdx.x);
+    end = share.begin(blockIdx.x + 1);
+    int b, before;
+    all.find(a, heads, begin, &b, &before);
+    seg.start(a, b);
+    const int hr = (begin - before) / (seg.tiles + kSegment);
+    seg.hk = hr / blocks;
+    seg.block = hr % blocks;
+    s0 = before + hr * (seg.tiles + kSegment);
+    seg.tile = max(0, begin - s0 - kSegment);
+  } else {
+    const int hr = blockIdx.x % heads;
+    seg.start(a, blockIdx.x / heads);
+    seg.hk = hr / blocks;
+    seg.block = hr % blocks;
+    if (blockIdx.x % heads == 0 && threadIdx.x == 0) paged_len(a.cache, seg.b, a.err);
+    if (seg.tiles == 0) {
+      no_keys<D>(a, ((int64_t)seg.b * a.H + seg.hk * G) * a.T + seg.block * kRows, min(kRows, rows - seg.block * kRows));
+      return;
+    }
+    end = seg.tiles + kSegment;
   }
+  // tiles of the current segment up to this number are the CTA's
+  auto last_tile = [&](int first_unit, int tiles) { return min(tiles, end - first_unit - kSegment); };
 
-  // ---- the warp's copies: tiles begin + warp, begin + warp + 4, ... into its own ring -----------
+  // ---- the warp's copies: every fourth tile of the CTA's, into its own ring ----------------------
   const uint32_t ring = ptx::smem_u32(smem) + warp * C::kRing;
-  Walk load = seg;
-  int64_t at = begin;
+  Walk<kKeys> load = seg;
+  int load_s0 = s0;
+  bool more = true;
   auto step = [&](int n) {                              // n tiles on
-    at += n;
-    if (at >= end) return;
     int t = load.tile + n;
     while (t >= load.tiles) {
       t -= load.tiles;
-      load.next_segment(a, heads);
+      load_s0 += load.tiles + kSegment;
+      load.next(a, blocks);
+      if (load_s0 + kSegment >= end) break;
     }
     load.tile = t;
+    more = load_s0 + kSegment + t < end;
   };
-  auto page_of = [&]() {
-    if (at >= end) return 0;
-    return a.cache.table[load.b * a.cache.table_stride + load.tile * kKeys / a.cache.page_size];
+  // The next tile's parts of 16 keys: their pages, and their first rows in them.  parts / (parts of
+  // a page) by multiplication with the rounded-up reciprocal, exact for the sizes the host admits.
+  int page[kParts], first[kParts];
+  auto read_pages = [&]() {
+    if (!more) return;
+    const int32_t* row = a.cache.table + load.b * a.cache.table_stride;
+#pragma unroll
+    for (int x = 0; x < kParts; ++x) {
+      const uint32_t part = load.tile * kParts + x;
+      const uint32_t at = (uint32_t)(((uint64_t)part * a.parts_magic) >> 36);
+      first[x] = (int)(part - at * a.page_parts) * 16;
+      page[x] = x == 0 || (int)part * 16 < load.len ? row[at] : 0;
+    }
   };
-  step(warp);
-  int page = page_of();                                 // of the next tile to copy
+  more = s0 + kSegment + seg.tile < end;
+  if (more) step(warp);
+  read_pages();
+  // This lane's 16-byte pieces: column c of rows row, row + kStep, ...; in shared memory piece c of
+  // row r lies at r * kRowBytes + ((c ^ (r & 7)) << 4), so that eight rows' pieces fill all banks.
+  constexpr int kChunks = D / 8, kStep = 32 / kChunks;
+  const int lane_row = lane / kChunks, lane_col = lane % kChunks;
+  const uint32_t lane_off = lane_row * C::kRowBytes + ((lane_col ^ lane_row) << 4);
+  const uint16_t* const kbase = static_cast<const uint16_t*>(a.cache.k) + lane_col * 8;
+  const int64_t v_off = static_cast<const uint16_t*>(a.cache.v) - static_cast<const uint16_t*>(a.cache.k);
+  const int64_t row_step = kStep * a.cache.token_stride;
   int slot = 0;
   auto copy_tile = [&]() {
-    if (at < end) {
-      const bool good = (unsigned)page < (unsigned)a.cache.n_pages;
-      if (!good && lane == 0) atomicExch(a.err, kDevBadOffsets);      // reported, not followed
-      const int first = load.tile * kKeys % a.cache.page_size;
-      const int64_t base = (good ? (int64_t)page * a.cache.page_stride : 0) +
-                           (int64_t)(load.hr / blocks) * a.cache.head_stride;
-      const uint32_t dst = ring + slot * C::kStage;
-      constexpr int kChunks = D / 8, kStep = 32 / kChunks;     // 16-byte pieces of a row; rows a step
-      const int c = lane % kChunks;
-      const int n = good ? load.len - load.tile * kKeys : 0;   // keys of the tile that exist
+    if (more) {
+      const uint32_t dst = ring + slot * C::kStage + lane_off;
 #pragma unroll
-      for (int i = 0; i < kKeys / kStep; ++i) {
-        const int r = i * kStep + lane / kChunks;
-        const bool there = r < n;
-        const int64_t off = base + (there ? (int64_t)(first + r) * a.cache.token_stride : 0) + c * 8;
-        const uint32_t to = dst + r * C::kRowBytes + ((c ^ (r & 7)) << 4);
-        cp16(to, static_cast<const uint16_t*>(a.cache.k) + off, there);
-        cp16(to + C::kHalf, static_cast<const uint16_t*>(a.cache.v) + off, there);
+      for (int x = 0; x < kParts; ++x) {
+        int n = load.len - (load.tile * kParts + x) * 16;      // keys of the part that exist
+        if ((unsigned)page[x] >= (unsigned)a.cache.n_pages && n > 0) {
+          if (lane == 0) atomicExch(a.err, kDevBadOffsets);    // reported, not followed
+          n = 0;
+        }
+        const uint16_t* src = kbase;
+        if (n > 0)
+          src += page[x] * a.cache.page_stride + load.hk * a.cache.head_stride + (first[x] + lane_row) * a.cache.token_stride;
+        if (n >= 16) {
+#pragma unroll
+          for (int i = 0; i < 16 / kStep; ++i, src += row_step) {
+            const uint32_t to = (dst ^ (((i * kStep) & 7) << 4)) + (x * 16 + i * kStep) * C::kRowBytes;
+            cp16(to, src);
+            cp16(to + C::kHalf, src + v_off);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16 / kStep; ++i, src += row_step) {
+            const bool there = i * kStep + lane_row < n;
+            const uint16_t* from = there ? src : kbase;
+            const uint32_t to = (dst ^ (((i * kStep) & 7) << 4)) + (x * 16 + i * kStep) * C::kRowBytes;
+            cp16(to, from, there);
+            cp16(to + C::kHalf, from + v_off, there);
+          }
+        }
       }
       step(kWarps);
-      page = page_of();
+      read_pages();
     }
     cp_commit();
     slot = slot + 1 == C::kStages ? 0 : slot + 1;
@@ -238,18 +392,42 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const PagedArgs a) {
   // ---- the warp's products -----------------------------------------------------------------------
   const int r0 = lane / 4, c0 = (lane % 4) * 2;
   const float c_log2 = a.scale * kLog2e;
-  float* const join = reinterpret_cast<float*>(smem + C::kJoin);
   float2* const stat = reinterpret_cast<float2*>(smem + C::kStat);
+  int* const from = reinterpret_cast<int*>(smem + C::kFrom);   // where each warp's output to be joined lies
+  int* const flag = from + kWarps;
   int take = 0;                                         // ring slot of the next tile
   int turn = 0;                                         // the warp whose turn the segment's first tile is
+  bool first_seg = true;
+
+  // the segment's queries as mma operands; per row its slope and the keys it sees
+  uint32_t q[D / 16][4];
+  int limit[2], full;
+  float slope[2];
+  auto read_rows = [&]() {
+    const int row0 = seg.block * kRows, n_rows = min(kRows, rows - row0);
+    const int64_t qrow = ((int64_t)seg.b * a.H + seg.hk * G) * a.T + row0;
+    const uint32_t* qp = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + qrow * D + r0 * D + c0);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        q[i][e] = r0 + (e & 1) * 8 < n_rows ? __ldg(qp + ((e & 1) * 8 * D + i * 16 + (e >> 1) * 8) / 2) : 0u;
+    full = 0x7fffffff;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = row0 + r0 + e * 8;
+      const int h = a.T == 1 ? r : r / a.T, t = r - h * a.T;
+      limit[e] = r < rows && t < seg.count ? seg.len - seg.count + t + 1 : 0;
+      if (r < rows) full = min(full, limit[e]);
+      slope[e] = a.score.slopes != nullptr && r < rows ? __ldg(a.score.slopes + seg.hk * G + h) * kLog2e : 0.f;
+    }
+    full = __reduce_min_sync(0xffffffffu, full);        // keys that every row sees
+  };
+  read_rows();
+
 #pragma unroll 1
-  for (int64_t g = begin; g < end;) {
-    const int n = (int)min((int64_t)(seg.tiles - seg.tile), end - g);
-    const int block = seg.hr % blocks, hk = seg.hr / blocks;
-    const int row0 = block * kRows;                     // first row of the block in the group
-    const int n_rows = min(kRows, rows - row0);
-    const int count = new_tokens(a.q_lens, seg.b, a.T);
-    const int64_t qrow = ((int64_t)seg.b * a.H + hk * G) * a.T + row0;
+  while (s0 + kSegment < end) {
+    const int n = last_tile(s0, seg.tiles) - seg.tile;  // the CTA's tiles of the segment: at least one
     const int mine = (warp - turn + kWarps) % kWarps;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float o[D / 8][4];
@@ -257,94 +435,95 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const PagedArgs a) {
     for (int i = 0; i < D / 8; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    if (mine < n) {
-      // the block's queries as mma operands, and each row's place, slope
-      uint32_t q[D / 16][4];
-      const uint32_t* qp = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + qrow * D);
+#pragma unroll 1
+    for (int i = mine; i < n; i += kWarps) {
+      cp_wait<C::kStages - 2>();
+      __syncwarp();                                   // this tile is there, the last one read
+      copy_tile();                                    // into the last one's slot
+      const uint32_t ks = ring + take * C::kStage, vs = ks + C::kHalf;
+      take = take + 1 == C::kStages ? 0 : take + 1;
+      constexpr int kN = kKeys / 8;                     // groups of 8 keys
+      float s[kKeys / 2];                               // row r0: s[4 n], s[4 n + 1]; r0 + 8: the next two
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
+      for (int e = 0; e < kKeys / 2; ++e) s[e] = 0.f;
+      {
+        // matrices of a load: keys 0-7 and 8-15, two groups of 8 values each
+        const int key = (lane & 7) + ((lane >> 4) << 3), part = (lane >> 3) & 1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = r0 + (e & 1) * 8;
-          q[i][e] = r < n_rows ? __ldg(qp + (r * D + i * 16 + (e >> 1) * 8 + c0) / 2) : 0u;
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int x = 0; x < kParts; ++x) {
+            uint32_t b[4];
+            ldsm4(ks + (x * 16 + key) * C::kRowBytes + (((2 * k + part) ^ (key & 7)) << 4), b);
+            mma<F16>(&s[8 * x], q[k], b[0], b[1]);
+            mma<F16>(&s[8 * x + 4], q[k], b[2], b[3]);
+          }
+      }
+      // scores in the log2 domain
+      const int key0 = (seg.tile + i) * kKeys;
+      if (a.score.cap_log2 == 0.f) {
+#pragma unroll
+        for (int e = 0; e < kKeys / 2; ++e) s[e] *= c_log2;
+      } else if (poly_fits(s, a.score.poly_limit)) {
+#pragma unroll
+        for (int e = 0; e < kKeys / 2; e += 2) {
+          const float2 t = tanh_poly(make_float2(s[e], s[e + 1]), a.score);
+          s[e] = t.x * a.score.cap_log2;
+          s[e + 1] = t.y * a.score.cap_log2;
         }
-      int limit[2];                                     // keys that the row sees
-      float slope[2];
+      } else {
+#pragma unroll
+        for (int e = 0; e < kKeys / 2; ++e) s[e] = a.score.cap_log2 * tanh_one(s[e], a.score);
+      }
+      if (a.score.slopes != nullptr) {
+#pragma unroll
+        for (int e = 0; e < kKeys / 2; ++e)
+          s[e] = fmaf(slope[(e >> 1) & 1], (float)(key0 + (e >> 2) * 8 + c0 + (e & 1) - (limit[(e >> 1) & 1] - 1)), s[e]);
+      }
+      if (key0 + kKeys > full) {                        // some row does not see all of the tile
+#pragma unroll
+        for (int e = 0; e < kKeys / 2; ++e)
+          s[e] = key0 + (e >> 2) * 8 + c0 + (e & 1) < limit[(e >> 1) & 1] ? s[e] : -INFINITY;
+      }
+      uint32_t p[kParts][4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = row0 + r0 + e * 8, t = r % a.T;
-        limit[e] = r < rows && t < count ? seg.len - count + t + 1 : 0;
-        slope[e] = a.score.slopes != nullptr && r < rows ? a.score.slopes[hk * G + r / a.T] * kLog2e : 0.f;
+        float mx = fmaxf(s[2 * e], s[2 * e + 1]);
+#pragma unroll
+        for (int n8 = 1; n8 < kN; ++n8) mx = ptx::max3(mx, s[4 * n8 + 2 * e], s[4 * n8 + 2 * e + 1]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        if (mx > m[e] + kRescaleLog2) {                 // false while the row is empty
+          const float alpha = ptx::ex2(m[e] - mx);      // 0 at the row's first key
+          m[e] = mx;
+          l[e] *= alpha;
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) {
+            o[k][2 * e] *= alpha;
+            o[k][2 * e + 1] *= alpha;
+          }
+        }
+        const float sub = m[e] == -INFINITY ? 0.f : m[e];
+        float sum = 0.f;
+#pragma unroll
+        for (int n8 = 0; n8 < kN; ++n8) {
+          const float p0 = ptx::ex2(s[4 * n8 + 2 * e] - sub), p1 = ptx::ex2(s[4 * n8 + 2 * e + 1] - sub);
+          sum += p0 + p1;
+          p[n8 / 2][e + 2 * (n8 & 1)] = ptx::pack2<F16>(p0, p1);
+        }
+        l[e] += sum;
       }
-#pragma unroll 1
-      for (int i = mine; i < n; i += kWarps) {
-        cp_wait<C::kStages - 2>();
-        __syncwarp();                                   // this tile is there, the last one read
-        copy_tile();                                    // into the last one's slot
-        const uint32_t ks = ring + take * C::kStage, vs = ks + C::kHalf;
-        take = take + 1 == C::kStages ? 0 : take + 1;
-        float s[2][4];
+      {
+        const int key = lane & 15, part = lane >> 4;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[h][e] = 0.f;
-        {
-          // matrices of the load: keys 0-7 and 8-15, two groups of 8 values each
-          const int key = (lane & 7) + ((lane >> 4) << 3), part = (lane >> 3) & 1;
+        for (int x = 0; x < kParts; ++x)
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             uint32_t b[4];
-            ldsm4(ks + key * C::kRowBytes + (((2 * k + part) ^ (key & 7)) << 4), b);
-            mma<F16>(s[0], q[k], b[0], b[1]);
-            mma<F16>(s[1], q[k], b[2], b[3]);
+            ldsm4t(vs + (x * 16 + key) * C::kRowBytes + (((2 * k + part) ^ (key & 7)) << 4), b);
+            mma<F16>(o[2 * k], p[x], b[0], b[1]);
+            mma<F16>(o[2 * k + 1], p[x], b[2], b[3]);
           }
-        }
-        // scores in the log2 domain, masked
-        const int key0 = (seg.tile + i) * kKeys;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = key0 + h * 8 + c0 + (e & 1);
-            const int lim = limit[e >> 1];
-            float x = s[h][e];
-            x = a.score.cap_log2 != 0.f ? a.score.cap_log2 * tanh_one(x, a.score) : x * c_log2;
-            x = fmaf(slope[e >> 1], (float)(key - (lim - 1)), x);
-            s[h][e] = key < lim ? x : -INFINITY;
-          }
-        uint32_t p[4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[e], mx);
-          const float sub = mn == -INFINITY ? 0.f : mn;
-          const float alpha = ptx::ex2(m[e] - sub);       // 0 while the row is empty
-          m[e] = mn;
-          float p0 = ptx::ex2(s[0][2 * e] - sub), p1 = ptx::ex2(s[0][2 * e + 1] - sub);
-          float p2 = ptx::ex2(s[1][2 * e] - sub), p3 = ptx::ex2(s[1][2 * e + 1] - sub);
-          l[e] = l[e] * alpha + ((p0 + p1) + (p2 + p3));
-          p[e] = ptx::pack2<F16>(p0, p1);
-          p[e + 2] = ptx::pack2<F16>(p2, p3);
-          if (alpha != 1.f) {
-#pragma unroll
-            for (int k = 0; k < D / 8; ++k) {
-              o[k][2 * e] *= alpha;
-              o[k][2 * e + 1] *= alpha;
-            }
-          }
-        }
-        {
-          const int key = lane & 15, part = lane >> 4;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            uint32_t b[4];
-            ldsm4t(vs + key * C::kRowBytes + (((2 * k + part) ^ (key & 7)) << 4), b);
-            mma<F16>(o[2 * k], p, b[0], b[1]);
-            mma<F16>(o[2 * k + 1], p, b[2], b[3]);
-          }
-        }
       }
     }
     // ---- the segment's end: join the warps -------------------------------------------------------
@@ -357,164 +536,179 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const PagedArgs a) {
       stat[warp * kRows + r0] = make_float2(m[0], l[0]);
       stat[warp * kRows + r0 + 8] = make_float2(m[1], l[1]);
     }
+    // the un-normalised output goes to the slot of the warp's last tile, free until its next one:
+    // groups of 4 values, their place in a row of D turned by the row against bank conflicts
     if (mine < n) {
-      float* to = join + (warp * kRows + r0) * C::kPitch + c0;
+      const int last = take == 0 ? C::kStages - 1 : take - 1;
+      if (lane == 0) from[warp] = warp * C::kRing + last * C::kStage;
+      __syncwarp();                                     // all lanes have read the tile
+      uint8_t* const to = smem + warp * C::kRing + last * C::kStage + r0 * D * 4;
 #pragma unroll
       for (int k = 0; k < D / 8; ++k) {
-        *reinterpret_cast<float2*>(to + k * 8) = make_float2(o[k][0], o[k][1]);
-        *reinterpret_cast<float2*>(to + 8 * C::kPitch + k * 8) = make_float2(o[k][2], o[k][3]);
+        const int at4 = ((2 * k + (lane % 4) / 2) ^ r0) * 16 + (lane & 1) * 8;
+        *reinterpret_cast<float2*>(to + at4) = make_float2(o[k][0], o[k][1]);
+        *reinterpret_cast<float2*>(to + 8 * D * 4 + at4) = make_float2(o[k][2], o[k][3]);
       }
     }
-    __syncthreads();
-    {
-      const bool whole = n == seg.tiles;
-      const int64_t part = 2 * (int64_t)blockIdx.x + (g == begin ? 0 : 1);
-      constexpr int kQuads = D / 4;
-      for (int x = threadIdx.x; x < n_rows * kQuads; x += kThreads) {
-        const int r = x / kQuads, c = x % kQuads * 4;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, stat[w * kRows + r].x);
-        float sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (mx != -INFINITY) {
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float2 ml = stat[w * kRows + r];
-            if (ml.x == -INFINITY) continue;
-            const float f = ptx::ex2(ml.x - mx);
-            const float4 v = *reinterpret_cast<const float4*>(join + (w * kRows + r) * C::kPitch + c);
-            sum = fmaf(f, ml.y, sum);
-            acc.x = fmaf(f, v.x, acc.x);
-            acc.y = fmaf(f, v.y, acc.y);
-            acc.z = fmaf(f, v.z, acc.z);
-            acc.w = fmaf(f, v.w, acc.w);
-          }
-        }
-        if (whole) {
-          const float inv = sum > 0.f ? 1.f / sum : 0.f;
-          const uint2 w = make_uint2(ptx::pack2<F16>(acc.x * inv, acc.y * inv), ptx::pack2<F16>(acc.z * inv, acc.w * inv));
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + (qrow + r) * D + c) = w;
-          if (c == 0) a.lse[qrow + r] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
-        } else {
-          *reinterpret_cast<float4*>(a.o_part + (part * kRows + r) * D + c) = acc;
-          if (c == 0) a.ml_part[part * kRows + r] = make_float2(mx, sum);
-        }
-      }
-    }
-    __syncthreads();
+    // what the join needs of this segment; then on to the next one, whose queries travel meanwhile
+    const int row0 = seg.block * kRows, n_rows = min(kRows, rows - row0);
+    const int64_t qrow = ((int64_t)seg.b * a.H + seg.hk * G) * a.T + row0;
+    const bool whole = n == seg.tiles;
+    const int seg_s0 = s0, seg_tiles = seg.tiles;
     turn = (turn + n) % kWarps;
-    g += n;
+    s0 += seg.tiles + kSegment;
     seg.tile = 0;
-    if (g < end) seg.next_segment(a, heads);
-  }
-  cp_wait<0>();
-}
-
-// Joins the parts of every segment that several CTAs shared, in the order of the tiles, and writes
-// the rows of sequences without keys.  One CTA per (sequence, key head, row block).
-template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs a) {
-  const int G = a.H / a.Hkv, rows = G * a.T;
-  const int blocks = (rows + kRows - 1) / kRows, heads = a.Hkv * blocks;
-  const int b = blockIdx.x / heads, hr = blockIdx.x % heads;
-  const int block = hr % blocks, hk = hr / blocks;
-  const int row0 = block * kRows, n_rows = min(kRows, rows - row0);
-  const int64_t qrow = ((int64_t)b * a.H + hk * G) * a.T + row0;
-  const int tiles = tiles_of(a, b, nullptr);
-  constexpr int kQuads = D / 4;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (tiles == 0) {
+    if (s0 + kSegment < end) {
+      seg.next(a, blocks);
+      read_rows();
+    }
+    __syncthreads();
     for (int x = threadIdx.x; x < n_rows * kQuads; x += kThreads) {
       const int r = x / kQuads, c = x % kQuads * 4;
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + (qrow + r) * D + c) = make_uint2(0u, 0u);
-      if (c == 0) a.lse[qrow + r] = -INFINITY;
-    }
-    return;
-  }
-  const int lane = threadIdx.x % 32;
-  int64_t sum = 0, first = 0;                          // all tiles; those before this sequence
-  for (int i = lane; i < a.B; i += 32) {
-    const int64_t n = tiles_of(a, i, nullptr);
-    sum += n;
-    if (i < b) first += n;
-  }
-  const int64_t total = warp_total(sum) * heads;
-  const int64_t s0 = warp_total(first) * heads + (int64_t)hr * tiles, s1 = s0 + tiles;
-  const int n_ctas = sharing_ctas(total, a.ctas);
-  auto owner = [&](int64_t t) {                        // the CTA whose share holds tile t
-    int c = (int)(t * n_ctas / total);
-    while (share_begin(total, n_ctas, c + 1) <= t) ++c;
-    while (share_begin(total, n_ctas, c) > t) --c;
-    return c;
-  };
-  const int ca = owner(s0), cb = owner(s1 - 1);
-  if (ca == cb) return;                                // one CTA had it all and wrote it
-  // the first CTA may have begun inside an earlier segment: this one is then its last
-  const int64_t part0 = 2 * (int64_t)ca + (share_begin(total, n_ctas, ca) == s0 ? 0 : 1);
-  for (int x = threadIdx.x; x < n_rows * kQuads; x += kThreads) {
-    const int r = x / kQuads, c = x % kQuads * 4;
-    float mx = -INFINITY;
-    for (int i = ca; i <= cb; ++i)
-      mx = fmaxf(mx, __ldcg(&a.ml_part[(i == ca ? part0 : 2 * (int64_t)i) * kRows + r]).x);
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (mx != -INFINITY) {
-#pragma unroll 4
-      for (int i = ca; i <= cb; ++i) {
-        const int64_t p = (i == ca ? part0 : 2 * (int64_t)i) * kRows + r;
-        const float2 ml = __ldcg(&a.ml_part[p]);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.o_part + p * D + c));
-        const float f = ptx::ex2(ml.x - mx);           // 0 for a part without keys
-        l = fmaf(f, ml.y, l);
+      float2 ml[kWarps];
+      float mx = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        ml[w] = stat[w * kRows + r];
+        mx = fmaxf(mx, ml[w].x);
+      }
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (ml[w].x == -INFINITY) continue;             // no tile, or none that the row sees
+        const float f = ptx::ex2(ml[w].x - mx);
+        const float4 v = *reinterpret_cast<const float4*>(smem + from[w] + r * D * 4 + (((c >> 2) ^ (r & 7)) << 4));
+        sum = fmaf(f, ml[w].y, sum);
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);
         acc.z = fmaf(f, v.z, acc.z);
         acc.w = fmaf(f, v.w, acc.w);
       }
+      if (!kShared || whole) {
+        write_row4<D, F16>(a, qrow + r, c, acc, sum, mx);
+      } else {
+        const int64_t part = (2 * (int64_t)blockIdx.x + (first_seg ? 0 : 1)) * kRows + r;
+        __stcg(reinterpret_cast<float4*>(a.o_part + part * D + c), acc);
+        if (c == 0) __stcg(&a.ml_part[part], make_float2(mx, sum));
+      }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const uint2 w = make_uint2(ptx::pack2<F16>(acc.x * inv, acc.y * inv), ptx::pack2<F16>(acc.z * inv, acc.w * inv));
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + (qrow + r) * D + c) = w;
-    if (c == 0) a.lse[qrow + r] = l > 0.f ? (mx + log2f(l)) * kLn2 : -INFINITY;
+    const bool was_first = first_seg;
+    first_seg = false;
+    if (kShared && !whole) {
+      // One of several CTAs with tiles of this segment: the one that comes last joins their parts, in
+      // the order of the tiles.
+      const Shares share(units, n_ctas);
+      const int ca = share.owner(seg_s0 + kSegment), cb = share.owner(seg_s0 + kSegment + seg_tiles - 1);
+      // the first CTA may have begun inside an earlier segment: this one is then its second part
+      const int part0 = 2 * ca + (share.begin(ca) >= seg_s0 ? 0 : 1);
+      __threadfence();                                  // the parts, before the word that announces them
+      __syncthreads();
+      if (warp == 0) {
+        const bool last = all_arrived(a.arrivals, 2 * (int)blockIdx.x + (was_first ? 0 : 1), part0, ca, cb, a.call);
+        if (lane == 0) *flag = last ? 1 : 0;
+      }
+      __syncthreads();
+      if (*flag != 0) {
+        __threadfence();
+        for (int x = threadIdx.x; x < n_rows * kQuads; x += kThreads) {
+          const int r = x / kQuads, c = x % kQuads * 4;
+          // eight parts at a time, all their reads in flight together; past the last, weight 0
+          auto part_of = [&](int i) { return (int64_t)(i <= ca ? part0 : 2 * min(i, cb)) * kRows + r; };
+          float mx = -INFINITY;
+          for (int i0 = ca; i0 <= cb; i0 += 16) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __ldcg(&a.ml_part[part_of(i0 + i)].x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, v[i]);
+          }
+          float sum = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (mx != -INFINITY) {
+            for (int i0 = ca; i0 <= cb; i0 += 8) {
+              float2 ml[8];
+              float4 v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int64_t part = part_of(i0 + i);
+                ml[i] = __ldcg(&a.ml_part[part]);
+                v[i] = __ldcg(reinterpret_cast<const float4*>(a.o_part + part * D + c));
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float f = i0 + i <= cb ? ptx::ex2(ml[i].x - mx) : 0.f;    // 0 too for a part without keys
+                sum = fmaf(f, ml[i].y, sum);
+                acc.x = fmaf(f, v[i].x, acc.x);
+                acc.y = fmaf(f, v[i].y, acc.y);
+                acc.z = fmaf(f, v[i].z, acc.z);
+                acc.w = fmaf(f, v[i].w, acc.w);
+              }
+            }
+          }
+          write_row4<D, F16>(a, qrow + r, c, acc, sum, mx);
+        }
+      }
+    }
+    __syncthreads();                                    // the slots and statistics may be written again
   }
+  cp_wait<0>();
+}
+
+template <int D, bool F16, bool kShared>
+cudaError_t launch(const PagedArgs& a, int grid, cudaStream_t s) {
+  auto kern = paged_kernel<D, F16, kShared>;
+  static LaunchSetup setup;
+  const cudaError_t e = prepare_launch(setup, kern, Cfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, Cfg<D>::kSmem, s>>>(a);
+  return cudaGetLastError();
 }
 
 template <int D, bool F16>
 cudaError_t paged(const PagedArgs& a, cudaStream_t s) {
-  auto kern = paged_kernel<D, F16>;
-  static LaunchSetup setup;
-  cudaError_t e = prepare_launch(setup, kern, Cfg<D>::kSmem);
-  if (e != cudaSuccess) return e;
-  kern<<<a.ctas, kThreads, Cfg<D>::kSmem, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int rows = a.H / a.Hkv * a.T;
   const int64_t segments = (int64_t)a.B * a.Hkv * ((rows + kRows - 1) / kRows);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)segments);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, F16>, a);
+  if (!paged_shares(a.B, a.Hkv, rows, paged_capacity(a.cache), a.ctas)) return launch<D, F16, false>(a, (int)segments, s);
+  return launch<D, F16, true>(a, a.ctas, s);
 }
 
 }  // namespace
 
-int paged_ctas(int d) {
+int paged_ctas() {
   int sms = 0;
-  (void)d;
-  return sm_count(&sms) == cudaSuccess && sms > 0 ? sms : 152;   // GB300's when no device can be asked
+  if (sm_count(&sms) != cudaSuccess || sms <= 0) sms = 152;      // GB300's when no device can be asked
+  return sms * kCtasPerSm;
 }
 
-size_t paged_parts(int ctas) { return 2 * (size_t)ctas * kRows; }
+unsigned long long paged_call_number() {
+  static std::atomic<unsigned long long> next{
+      (unsigned long long)std::chrono::system_clock::now().time_since_epoch().count() * 0x9E3779B97F4A7C15ull};
+  const unsigned long long n = next.fetch_add(1, std::memory_order_relaxed);
+  return n != 0 ? n : paged_call_number();             // 0 is a cleared word
+}
 
-size_t paged_workspace(int d) {
-  const size_t parts = paged_parts(paged_ctas(d));
-  return parts * d * sizeof(float) + parts * sizeof(float2);
+// Whether CTAs share segments.  Few segments of at most 512 keys get a CTA each, at most two after one
+// another in an SM's places: nothing to reckon, nothing to join and no workspace.
+bool paged_shares(int B, int Hkv, int rows, int capacity, int ctas) {
+  const int64_t segments = (int64_t)B * Hkv * ((rows + kRows - 1) / kRows);
+  return capacity > 512 || segments > 2 * (int64_t)ctas;
+}
+
+// Whether the units of all segments can be counted in 31 bits.
+bool paged_counts(int B, int Hkv, int rows, int capacity) {
+  const int64_t segments = (int64_t)B * Hkv * ((rows + kRows - 1) / kRows);
+  return segments <= 0x7fffffff / ((int64_t)capacity / 16 + 1 + kSegment);
+}
+
+// The workspace: arrivals [2 * ctas], then two parts of 16 rows a CTA, their statistics and outputs.
+PagedWorkspace paged_workspace(int ctas, int d) {
+  PagedWorkspace w;
+  const size_t rows = 2 * (size_t)ctas * kRows;
+  w.ml = (2 * (size_t)ctas * sizeof(unsigned long long) + 255) / 256 * 256;
+  w.o = w.ml + rows * sizeof(float2);
+  w.total = (w.o + rows * d * sizeof(float) + 255) / 256 * 256;
+  return w;
 }
 
 cudaError_t launch_paged(const PagedArgs& a, fa_dtype dt, cudaStream_t s) {

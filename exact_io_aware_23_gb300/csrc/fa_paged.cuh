@@ -68,8 +68,14 @@ struct PagedArgs {
   const int32_t* q_lens;
   float scale;
   ScoreArgs score;           // cap and slopes; no prefix
-  // fp32 partial results, two slots per CTA: o_part [2 * ctas][16][d] un-normalised, ml_part
+  // page_size / 16, and 2^36 / that rounded up
+  uint32_t page_parts;
+  uint64_t parts_magic;
+  // arrivals [2 * ctas]: the words that announce the parts; fp32 partial results, two parts per CTA:
+  // o_part [2 * ctas][16][d] un-normalised, ml_part
   // [2 * ctas][16] = {log2-domain maximum, normaliser}
+  unsigned long long* arrivals;
+  unsigned long long call;   // the call's number
   float* o_part;
   float2* ml_part;
   int ctas;
@@ -100,9 +106,17 @@ cudaError_t launch_rotary(const RotaryArgs& a, fa_dtype dt, cudaStream_t s);
 cudaError_t launch_append(const AppendArgs& a, fa_dtype dt, cudaStream_t s);
 
 // CTAs of a paged attention call, and the bytes of its partial results.
-int paged_ctas(int d);
-size_t paged_parts(int ctas);              // rows of partial results
-size_t paged_workspace(int d);
+// Pages of up to 4096 tokens: part * (rounding of the reciprocal) stays below 2^36 for any part of
+// a sequence of 2^31 tokens, which the kernel's division by multiplication needs.
+constexpr int kMaxPageSize = 4096;
+int paged_ctas();
+unsigned long long paged_call_number();
+bool paged_shares(int B, int Hkv, int rows, int capacity, int ctas);
+bool paged_counts(int B, int Hkv, int rows, int capacity);
+struct PagedWorkspace {
+  size_t ml, o, total;       // byte offsets; arrivals at 0
+};
+PagedWorkspace paged_workspace(int ctas, int d);
 cudaError_t launch_paged(const PagedArgs& a, fa_dtype dt, cudaStream_t s);
 
 }  // namespace fa

@@ -42,7 +42,7 @@ fa_status check_rotation(const double* inv_freq, int rotary_dim, float mscale, i
 fa_status check_cache(const fa_paged_cache* c, int Hkv) {
   if (c == nullptr) return FA_ERR_INVALID_ARG;
   if (c->n_pages < 0 || c->max_pages < 0 || c->page_size <= 0) return FA_ERR_INVALID_ARG;
-  if (c->page_size % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if (c->page_size % 16 != 0 || c->page_size > fa::kMaxPageSize) return FA_ERR_UNSUPPORTED;
   if (!c->k_cache || !c->v_cache || !c->block_table || !c->kv_lens) return FA_ERR_INVALID_ARG;
   if (!aligned(c->k_cache, 16) || !aligned(c->v_cache, 16) || !aligned(c->block_table, 4) || !aligned(c->kv_lens, 4))
     return FA_ERR_INVALID_ARG;
@@ -143,9 +143,10 @@ fa_status fa_append_paged(const fa_paged_cache* cache, const void* k, const int6
   return fa::launch_append(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-size_t fa_forward_paged_workspace_size(int B, int H, int Hkv, int T, int d) {
-  if (check_sizes(B, H, Hkv, T, d) != FA_OK || B == 0 || H == 0 || T == 0) return 0;
-  return (fa::paged_workspace(d) + 255) / 256 * 256;
+size_t fa_forward_paged_workspace_size(int B, int H, int Hkv, int T, int d, int max_keys) {
+  if (check_sizes(B, H, Hkv, T, d) != FA_OK || B == 0 || H == 0 || T == 0 || max_keys <= 0) return 0;
+  const int ctas = fa::paged_ctas();
+  return fa::paged_shares(B, Hkv, H / Hkv * T, max_keys, ctas) ? fa::paged_workspace(ctas, d).total : 0;
 }
 
 fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, float* lse, int B, int H, int Hkv,
@@ -164,12 +165,12 @@ fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, 
   st = check_cache(cache, Hkv);
   if (st != FA_OK) return st;
   if (B == 0 || H == 0 || T == 0) return FA_OK;
-  if (!q || !o || !lse || !workspace || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(q_lens, 4))
-    return FA_ERR_INVALID_ARG;
-  if (!aligned(workspace, 256) || workspace_bytes < fa_forward_paged_workspace_size(B, H, Hkv, T, d))
+  if (!q || !o || !lse || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(q_lens, 4))
     return FA_ERR_INVALID_ARG;
   fa::PagedArgs a{};
   a.cache = cache_args(cache);
+  const size_t need = fa_forward_paged_workspace_size(B, H, Hkv, T, d, fa::paged_capacity(a.cache));
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
   a.q = q;
   a.o = o;
   a.lse = lse;
@@ -177,10 +178,15 @@ fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, 
   a.q_lens = q_lens;
   a.scale = scale;
   a.score = mods;
-  a.ctas = fa::paged_ctas(d);
-  const size_t parts = fa::paged_parts(a.ctas);
-  a.o_part = static_cast<float*>(workspace);
-  a.ml_part = reinterpret_cast<float2*>(a.o_part + parts * d);
+  if (!fa::paged_counts(B, Hkv, H / Hkv * T, fa::paged_capacity(a.cache))) return FA_ERR_UNSUPPORTED;
+  a.page_parts = cache->page_size / 16;
+  a.parts_magic = ((uint64_t(1) << 36) + a.page_parts - 1) / a.page_parts;
+  a.ctas = fa::paged_ctas();
+  const fa::PagedWorkspace w = fa::paged_workspace(a.ctas, d);
+  a.arrivals = static_cast<unsigned long long*>(workspace);
+  a.call = fa::paged_call_number();
+  a.ml_part = reinterpret_cast<float2*>(static_cast<char*>(workspace) + w.ml);
+  a.o_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.o);
   if (fa::device_error_word(&a.err) != FA_OK) return FA_ERR_CUDA;
   return fa::launch_paged(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -23,26 +23,40 @@
 
 #include "fa_paged.cuh"
 #include "fa_sm103.cuh"
+#include "ptx_sm103.cuh"
 
 namespace fa {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnit = 16;                  // values per unit, 8 pairs
+constexpr int kBatch = 4;                  // heads whose values a thread has in flight together
 
-// 8 consecutive values as fp32, and back (rounded to nearest)
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// 8 consecutive values as they lie in memory
+template <typename T> struct Raw8 { uint4 w[sizeof(T) / 2]; };
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const Raw8<T>& r) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = r.w[i];
+}
+// ... as fp32, and back (rounded to nearest)
+__device__ __forceinline__ void unpack(const Raw8<__nv_bfloat16>& r, float (&x)[8]) {
+  const uint32_t u[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(u[i] << 16);
     x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void load8(const __half* p, float (&x)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ void unpack(const Raw8<__half>& r, float (&x)[8]) {
+  const uint32_t u[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
@@ -50,39 +64,25 @@ __device__ __forceinline__ void load8(const __half* p, float (&x)[8]) {
     x[2 * i + 1] = f.y;
   }
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  uint32_t u[4];
+__device__ __forceinline__ void unpack(const Raw8<float>& r, float (&x)[8]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    u[i] = *reinterpret_cast<const uint32_t*>(&v);
+  for (int i = 0; i < 2; ++i) {
+    x[4 * i] = __uint_as_float(r.w[i].x);
+    x[4 * i + 1] = __uint_as_float(r.w[i].y);
+    x[4 * i + 2] = __uint_as_float(r.w[i].z);
+    x[4 * i + 3] = __uint_as_float(r.w[i].w);
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ void store8(__half* p, const float (&x)[8]) {
-  uint32_t u[4];
+__device__ __forceinline__ void pack(const float (&x)[8], Raw8<__nv_bfloat16>& r) {
+  r.w[0] = make_uint4(ptx::pack_bf16(x[0], x[1]), ptx::pack_bf16(x[2], x[3]), ptx::pack_bf16(x[4], x[5]), ptx::pack_bf16(x[6], x[7]));
+}
+__device__ __forceinline__ void pack(const float (&x)[8], Raw8<__half>& r) {
+  r.w[0] = make_uint4(ptx::pack_f16(x[0], x[1]), ptx::pack_f16(x[2], x[3]), ptx::pack_f16(x[4], x[5]), ptx::pack_f16(x[6], x[7]));
+}
+__device__ __forceinline__ void pack(const float (&x)[8], Raw8<float>& r) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 v = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-    u[i] = *reinterpret_cast<const uint32_t*>(&v);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-}
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-// 8 values moved unchanged, bit for bit
-template <typename T>
-__device__ __forceinline__ void move8(T* to, const T* from) {
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-    reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(from)[i];
+  for (int i = 0; i < 2; ++i)
+    r.w[i] = make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]), __float_as_uint(x[4 * i + 3]));
 }
 
 // f / (2 pi) turns as a 64-bit fraction of a turn: the 53-bit significand of f times 2^128/(2 pi),
@@ -152,6 +152,17 @@ __device__ __forceinline__ void turn8(float (&x)[8], float (&y)[8], bool interle
 }
 
 template <typename T>
+__device__ __forceinline__ void turn_raw(Raw8<T>& lo, Raw8<T>& hi, bool interleaved, const float (&c)[8],
+                                         const float (&s)[8]) {
+  float x[8], y[8];
+  unpack(lo, x);
+  unpack(hi, y);
+  turn8(x, y, interleaved, c, s);
+  pack(x, lo);
+  pack(y, hi);
+}
+
+template <typename T>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, const int heads_per_block) {
   const int units = a.d / kUnit;
   const int u = threadIdx.x % units;
@@ -171,19 +182,24 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, co
     T* y = static_cast<T*>(a.y) + b * a.ys.b + n * a.ys.n + h0 * a.ys.h;
     float c[8], s[8];
     if (t.turns) angles(frac, a.positions[b * a.pos_stride + n], a.rot, c, s);
-#pragma unroll 4
-    for (int h = h0; h < h1; ++h, x += a.xs.h, y += a.ys.h) {
-      if (t.turns) {
-        float lo[8], hi[8];
-        load8(x + t.lo, lo);
-        load8(x + t.hi, hi);
-        turn8(lo, hi, a.rot.interleaved, c, s);
-        store8(y + t.lo, lo);
-        store8(y + t.hi, hi);
-      } else {
-        move8(y + t.lo, x + t.lo);
-        move8(y + t.hi, x + t.hi);
-      }
+    // kBatch heads at a time: their reads are all in flight before the first is used
+    for (int h = h0; h < h1; h += kBatch) {
+      Raw8<T> lo[kBatch], hi[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (h + i < h1) {
+          lo[i] = load8(x + i * a.xs.h + t.lo);
+          hi[i] = load8(x + i * a.xs.h + t.hi);
+        }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (h + i < h1) {
+          if (t.turns) turn_raw(lo[i], hi[i], a.rot.interleaved, c, s);
+          store8(y + i * a.ys.h + t.lo, lo[i]);
+          store8(y + i * a.ys.h + t.hi, hi[i]);
+        }
+      x += kBatch * a.xs.h;
+      y += kBatch * a.ys.h;
     }
   }
 }
@@ -224,31 +240,32 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
     float c[8], s[8];
     if (turns && there) angles(frac, pos, a.rot, c, s);
     const int64_t row = (int64_t)page * a.cache.page_stride + (int64_t)slot * a.cache.token_stride;
-#pragma unroll 2
-    for (int h = h0; h < h1; ++h) {
-      const bool is_q = h < Hq, is_k = !is_q && h < Hq + a.Hkv;
-      const int g = is_q ? h : is_k ? h - Hq : h - Hq - a.Hkv;
-      const Strides st = is_q ? a.qs : is_k ? a.ks : a.vs;
-      const T* x = static_cast<const T*>(is_q ? a.q : is_k ? a.k : a.v) + b * st.b + g * st.h + n * st.n;
-      T* y = is_q ? static_cast<T*>(a.q_out) + (((int64_t)b * a.H + g) * a.T + n) * a.d
-                  : static_cast<T*>(is_k ? a.cache.k : a.cache.v) + row + g * a.cache.head_stride;
-      if (!is_q && page < 0) continue;
-      float lo[8], hi[8];
-      if (is_q && !there) {
+    for (int h = h0; h < h1; h += kBatch) {
+      Raw8<T> lo[kBatch], hi[kBatch];
+      T* to[kBatch];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) lo[i] = hi[i] = 0.f;
-        store8(y + t.lo, lo);
-        store8(y + t.hi, hi);
-      } else if (t.turns && (is_q || is_k)) {
-        load8(x + t.lo, lo);
-        load8(x + t.hi, hi);
-        turn8(lo, hi, a.rot.interleaved, c, s);
-        store8(y + t.lo, lo);
-        store8(y + t.hi, hi);
-      } else {
-        // values, and the part of a head that is not rotated; a unit keeps its own two groups
-        move8(y + t.lo, x + t.lo);
-        move8(y + t.hi, x + t.hi);
+      for (int i = 0; i < kBatch; ++i) {
+        const bool is_q = h + i < Hq, is_k = !is_q && h + i < Hq + a.Hkv;
+        const int g = is_q ? h + i : is_k ? h + i - Hq : h + i - Hq - a.Hkv;
+        const Strides st = is_q ? a.qs : is_k ? a.ks : a.vs;
+        to[i] = nullptr;
+        if (h + i >= h1 || (!is_q && page < 0)) continue;
+        to[i] = is_q ? static_cast<T*>(a.q_out) + (((int64_t)b * a.H + g) * a.T + n) * a.d
+                     : static_cast<T*>(is_k ? a.cache.k : a.cache.v) + row + g * a.cache.head_stride;
+        lo[i] = hi[i] = Raw8<T>{};                    // queries that do not exist: zero
+        if (there) {
+          const T* x = static_cast<const T*>(is_q ? a.q : is_k ? a.k : a.v) + b * st.b + g * st.h + n * st.n;
+          lo[i] = load8(x + t.lo);
+          hi[i] = load8(x + t.hi);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (to[i] == nullptr) continue;
+        // values are copied, and so is the part of a head that is not rotated
+        if (t.turns && there && h + i < Hq + a.Hkv) turn_raw(lo[i], hi[i], a.rot.interleaved, c, s);
+        store8(to[i] + t.lo, lo[i]);
+        store8(to[i] + t.hi, hi[i]);
       }
     }
   }

@@ -430,7 +430,7 @@ typedef struct {
   int64_t head_stride;
   int64_t token_stride;
   int n_pages;                 /* pages that exist */
-  int page_size;               /* tokens of a page: a multiple of 16 */
+  int page_size;               /* tokens of a page: a multiple of 16, at most 4096 */
   const int32_t* block_table;  /* device int32, row b at b * table_stride */
   int64_t table_stride;        /* >= max_pages */
   int max_pages;               /* entries of a row */
@@ -463,15 +463,16 @@ fa_status fa_append_paged(const fa_paged_cache* cache, const void* k, const int6
  *   q, o   : [B, H, T, d] contiguous; lse: fp32 [B, H, T].  Query head h reads key head
  *            h / (H / Hkv).  Rows without a key, or past a sequence's new tokens, get O = 0 and
  *            LSE = -inf.
- *   workspace : >= fa_forward_paged_workspace_size(...) bytes, 256-byte aligned, caller-owned,
- *            contents on entry irrelevant; calls in flight at once need their own
+ *   workspace : >= fa_forward_paged_workspace_size(..., max_pages * page_size) bytes, 256-byte
+ *            aligned, caller-owned, contents on entry irrelevant; calls in flight at once need their
+ *            own.  The size is 0 for a few short sequences, which need none (workspace may be null).
  * The cache is split over its length among all SMs and joined in a fixed order: the same bits on
  * every call.  Nothing that a page holds behind a sequence's last token enters the result.  bf16 or
  * fp16.  Lengths and table entries outside their contract as in fa_append_paged (such a sequence's
  * result is then unspecified).  The work is sized for few new tokens: every 16 query rows of a
  * group (H / Hkv * T) read the cache once more.
  */
-size_t fa_forward_paged_workspace_size(int B, int H, int Hkv, int T, int d);
+size_t fa_forward_paged_workspace_size(int B, int H, int Hkv, int T, int d, int max_keys);
 fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, float* lse, int B,
                            int H, int Hkv, int T, int d, float scale, const int32_t* q_lens,
                            const fa_score_mod* score, fa_dtype dtype, void* workspace,

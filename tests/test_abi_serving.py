@@ -47,7 +47,7 @@ def cache(**kw):
 
 
 BAD_CACHES = [(dict(k_cache=None), INVALID), (dict(v_cache=P + 8), INVALID), (dict(page_size=0), INVALID),
-              (dict(page_size=24), UNSUPPORTED), (dict(n_pages=-1), INVALID), (dict(token_stride=65), INVALID),
+              (dict(page_size=24), UNSUPPORTED), (dict(page_size=8192), UNSUPPORTED), (dict(n_pages=-1), INVALID), (dict(token_stride=65), INVALID),
               (dict(head_stride=4), INVALID), (dict(page_stride=4), INVALID), (dict(block_table=None), INVALID),
               (dict(kv_lens=None), INVALID), (dict(table_stride=2), INVALID), (dict(max_pages=-1), INVALID)]
 
@@ -77,19 +77,23 @@ def test_append_argument_checks():
 
 
 def paged(c=None, q=P, o=P, lse=P, B=2, H=4, Hkv=2, T=1, d=64, scale=0.125, mod=None, dtype=0, w=P, wsb=None):
-    wsb = fa.forward_paged_workspace_size(2, 4, 2, 1, 64) if wsb is None else wsb
-    return fa.lib.fa_forward_paged(q, cache() if c is None else c, o, lse, B, H, Hkv, T, d, scale, None,
+    wsb = fa.forward_paged_workspace_size(2, 4, 2, 1, 64, 1600) if wsb is None else wsb
+    return fa.lib.fa_forward_paged(q, cache(max_pages=100, table_stride=100) if c is None else c, o, lse, B, H, Hkv, T, d, scale, None,
                                    None if mod is None else ctypes.byref(mod), dtype, w, wsb, None)
 
 
 def test_paged_attention_argument_checks():
     for kw, status in BAD_CACHES:
         assert paged(cache(**kw)) == status, kw
-    ws = fa.forward_paged_workspace_size(2, 4, 2, 1, 64)
+    ws = fa.forward_paged_workspace_size(2, 4, 2, 1, 64, 1600)
     assert ws % 256 == 0 and ws > 0
-    assert fa.forward_paged_workspace_size(2, 4, 2, 1, 128) > ws
-    assert fa.forward_paged_workspace_size(0, 4, 2, 1, 64) == 0
-    assert fa.forward_paged_workspace_size(2, 4, 3, 1, 64) == 0
+    assert fa.forward_paged_workspace_size(2, 4, 2, 1, 128, 1600) > ws
+    assert fa.forward_paged_workspace_size(0, 4, 2, 1, 64, 1600) == 0
+    assert fa.forward_paged_workspace_size(2, 4, 3, 1, 64, 1600) == 0
+    assert fa.forward_paged_workspace_size(2, 4, 2, 1, 64, 512) == 0       # a CTA each: none needed
+    assert fa.forward_paged_workspace_size(9999, 4, 2, 1, 64, 512) == ws   # too many for that
+    many = cache(max_pages=1 << 20, table_stride=1 << 20, page_size=4096)
+    assert paged(many, B=60000, H=4, Hkv=4) == UNSUPPORTED                 # more tiles than 31 bits count
     assert paged(dtype=1) == UNSUPPORTED
     assert paged(d=96) == UNSUPPORTED
     assert paged(Hkv=3) == UNSUPPORTED

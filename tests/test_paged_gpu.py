@@ -159,6 +159,34 @@ def test_captured_call_follows_the_lengths():
         _check(q, kc, vc, table, new, *want)
 
 
+@pytest.mark.parametrize("fill", [0, 255, None])
+def test_workspaces_hold_anything(fill):
+    """What a workspace holds on entry does not matter; calls and two captured graphs may share one."""
+    lens = [5000, 300]
+    kc, vc, table, g = _cache(lens, 2, 16, 64, "bf16", 11)
+    q = torch.randn((2, 4, 1, 64), generator=g, device="cuda").to(torch.bfloat16)
+    n = _i32(lens)
+    want = fa.forward_paged(q, kc, vc, table, n)
+    need = fa.forward_paged_workspace_size(2, 4, 2, 1, 64, table.shape[1] * 16)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for i in range(5):
+        if i != 2:                                # once: what the last call left
+            ws.random_(0, 256) if fill is None else ws.fill_(fill)
+        got = fa.forward_paged(q, kc, vc, table, n, workspace=ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = fa.forward_paged(q, kc, vc, table, n, workspace=ws)
+        graphs.append((gr, out))
+    for _ in range(3):
+        for gr, out in graphs:
+            out[0].zero_()
+            gr.replay()
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
 def test_two_streams_at_once():
     lens = [4000, 1000]
     kc, vc, table, g = _cache(lens, 4, 64, 128, "bf16", 10)
@@ -317,7 +345,8 @@ def test_refusals():
     with pytest.raises(fa.FaError, match="INVALID_ARG"):
         fa.forward_paged(q, kc, vc, table, n, scale=0.0)
     with pytest.raises(fa.FaError, match="INVALID_ARG"):
-        fa.forward_paged(q, kc, vc, table, n, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+        wide = torch.zeros((2, 40), dtype=torch.int32, device="cuda")
+        fa.forward_paged(q, kc, vc, wide, n, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(fa.FaError, match="UNSUPPORTED"):
         fa.forward_paged(q, kc[:, :, :8], vc[:, :, :8], table, n)          # pages of 8 tokens
     with pytest.raises(ValueError, match="q_out"):
