@@ -9,12 +9,13 @@
 // rounded at the end, 1.4 without it.  So D is summed here from P and dP themselves, in fp32, as
 // they come out of the tensor cores: two products more than the backward's seven, no pass over O.
 //
-// One CTA = two 128-row query tiles of one (b, h) slice, 320 threads:
+// One CTA = two 128-row query tiles of one (b, h) slice, 384 threads:
 //   warp 8      TMA producer: Q_0, Q_1, dO_0, dO_1 once, then K_j, V_j in turn through one ring
 //   warp 9      MMA issuer (one thread): S_t = Q_t K_j^T, then dP_t = dO_t V_j^T, t = 0, 1
 //   warps 0-3   query tile 0, warps 4-7 query tile 1; a thread owns a row (a TMEM lane): 128 scores
 //               to registers, which frees S_t for the next key tile at once, P, then dP 32 columns
 //               at a time into the row's sum.
+//   warps 10, 11 only make up the third warpgroup, which gives registers to the other two.
 //   TMEM (512 columns): S_0, S_1, dP_0, dP_1, 128 each.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -29,7 +30,7 @@ namespace fa {
 namespace {
 
 constexpr int BM = 128, BN = 128;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -120,6 +121,8 @@ delta_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
+  if (warp >= 8) {
+    ptx::regs_dec<88>();
   if (warp == 8) {
     // ------------------------------- TMA producer -----------------------------------------------
     if (lane == 0 && tiles > 0) {
@@ -175,7 +178,9 @@ delta_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
       ptx::mma_commit(ptx::smem_u32(&bars->done));
       ptx::mbar_wait(ptx::smem_u32(&bars->done), 0, lim_ms, a.err);
     }
+  }
   } else {
+    ptx::regs_inc<200>();
     // ------------------------------- rows -------------------------------------------------------
     const int t = warp / 4, sub = warp % 4;
     const int i = q0 + t * BM + sub * 32 + lane;
@@ -219,24 +224,32 @@ delta_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         if (t == 1 && sub == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->empty[(2 * n) % C::kSlots]));
       }
       if (kind != kNone) {
-        const float base = slope * (float)(c0 - i);
-        with_score(p, a.score, [&](auto cap, auto bias) {
-          constexpr int kCap = decltype(cap)::value;
+        // what is masked, or no row, does not choose the form of the tanh for the others
+        const int lim = i < N ? seen - c0 : 0;
+        if (kind == kPartial || r1 - r0 < BM - 1) {
+#pragma unroll
+          for (int e = 0; e < BN; ++e) p[e] = e < lim ? p[e] : 0.f;
+        }
+        const int lo = c0 - (r0 + BM - 1), hi = lo + BM + BN - 2;              // of j - i in the tile
+        const Bias bi = make_bias(slope, c0 - i, lo, a.causal && prefix == 0 ? min(hi, 0) : hi);
+        with_score(p, a.score, bi, [&](auto cap, auto bias) {
+          constexpr int kCap = decltype(cap)::value, kBias = decltype(bias)::value;
+          const float first = kBias == kBiasLinear ? nl + bi.base : nl;
+          const float2 first2 = make_float2(first, first);
 #pragma unroll
           for (int col = 0; col < BN; col += 2) {
             float2 x = make_float2(p[col], p[col + 1]);
             if constexpr (kCap != kCapNone) x = tanh_of<kCap>(x, a.score);
-            x = ptx::fma2(x, m2, nl2);
-            if constexpr (decltype(bias)::value != 0) {
-              x.x = biased(x.x, base, slope, col);
-              x.y = biased(x.y, base, slope, col + 1);
+            x = ptx::fma2(x, m2, first2);
+            if constexpr (kBias != kBiasNone) {
+              x.x = biased<kBias>(x.x, bi, col);
+              x.y = biased<kBias>(x.y, bi, col + 1);
             }
             p[col] = ptx::ex2(x.x);
             p[col + 1] = ptx::ex2(x.y);
           }
         });
         if (kind == kPartial) {
-          const int lim = seen - c0;
 #pragma unroll
           for (int e = 0; e < BN; ++e) p[e] = e < lim ? p[e] : 0.f;
         }
@@ -298,7 +311,10 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t s) {
   if ((e = make_map(&mdo, a.dO, D, a.rows, q_slices, F16)) != cudaSuccess) return e;
   auto kern = delta_kernel<D, F16>;
   static LaunchSetup setup;
-  if ((e = prepare_launch(setup, kern, Cfg<D, F16>::kSmem)) != cudaSuccess) return e;
+  // The warp groups re-split the CTA's registers; that only completes if the launch holds them.
+  int regs = 0;
+  if ((e = prepare_launch(setup, kern, Cfg<D, F16>::kSmem, &regs)) != cudaSuccess) return e;
+  if (regs * kThreads < 128 * 88 + 256 * 200) return cudaErrorInvalidConfiguration;
   kern<<<dim3((a.N + 2 * BM - 1) / (2 * BM) * a.B * a.H), kThreads, Cfg<D, F16>::kSmem, s>>>(mq, mk, mv, mdo, a);
   return cudaGetLastError();
 }

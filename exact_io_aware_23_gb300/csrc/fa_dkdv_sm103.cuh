@@ -453,19 +453,26 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
 #pragma unroll
             for (int e = 0; e < 32; ++e) p[hc * 32 + e] = __uint_as_float(raw[hc][e]);
           }
+          if (kind == kPartial && !key_ok) {         // no key: does not choose the form of the tanh
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) p[e] = 0.f;
+          }
           uint32_t pk[kCols / 2];
-          const float base = slope * (float)(q0 - key);
+          const int lo = i * BM - (g.k0 + BN - 1), hi = lo + BM + BN - 2;      // of i - j in the tile
+          const Bias bi = make_bias(slope, q0 - key, a.causal && g.prefix == 0 ? max(lo, 0) : lo, hi);
           const float2 m2 = a.score.cap_log2 == 0.f ? c2 : make_float2(a.score.cap_log2, a.score.cap_log2);
-          with_score(p, a.score, [&](auto cap, auto bias) {
-            constexpr int kCap = decltype(cap)::value;
+          with_score(p, a.score, bi, [&](auto cap, auto bias) {
+            constexpr int kCap = decltype(cap)::value, kBias = decltype(bias)::value;
+            const float base = kBias == kBiasLinear ? bi.base : 0.f;
 #pragma unroll
             for (int col = 0; col < kCols; col += 2) {
               float2 t = make_float2(p[col], p[col + 1]);
               if constexpr (kCap != kCapNone) t = tanh_of<kCap>(t, a.score);
               float2 x = ptx::fma2(t, m2, *reinterpret_cast<const float2*>(lse2 + col));
-              if constexpr (decltype(bias)::value != 0) {
-                x.x = biased(x.x, base, slope, col);
-                x.y = biased(x.y, base, slope, col + 1);
+              if constexpr (kBias == kBiasLinear) x = ptx::add2(x, make_float2(base, base));
+              if constexpr (kBias != kBiasNone) {
+                x.x = biased<kBias>(x.x, bi, col);
+                x.y = biased<kBias>(x.y, bi, col + 1);
               }
               float2 v = make_float2(ptx::ex2(x.x), ptx::ex2(x.y)), w = v;
               // what dS takes: P times the cap's derivative 1 - tanh^2

@@ -381,19 +381,26 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
 #pragma unroll
             for (int e = 0; e < 32; ++e) p[hc * 32 + e] = __uint_as_float(raw[hc][e]);
           }
-          const float base = slope * (float)(k0 - q);
+          if (g.q0 + BM > g.N && q >= g.N) {         // no row: does not choose the form of the tanh
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) p[e] = 0.f;
+          }
+          const int lo = j * BN - (g.q0 + BM - 1), hi = lo + BM + BN - 2;      // of j - i in the tile
+          const Bias bi = make_bias(slope, k0 - q, lo, a.causal && g.prefix == 0 ? min(hi, 0) : hi);
           const float2 m2 = a.score.cap_log2 == 0.f ? c2 : make_float2(a.score.cap_log2, a.score.cap_log2);
           const int seen = !g.causal ? g.kv_lim : min(g.kv_lim, max(q + 1, g.prefix));   // keys of the row
-          with_score(p, a.score, [&](auto cap, auto bias) {
-            constexpr int kCap = decltype(cap)::value;
+          with_score(p, a.score, bi, [&](auto cap, auto bias) {
+            constexpr int kCap = decltype(cap)::value, kBias = decltype(bias)::value;
+            const float first = kBias == kBiasLinear ? nl + bi.base : nl;
+            const float2 first2 = make_float2(first, first);
 #pragma unroll
             for (int col = 0; col < kCols; col += 2) {
               float2 t = make_float2(p[col], p[col + 1]);
               if constexpr (kCap != kCapNone) t = tanh_of<kCap>(t, a.score);
-              float2 x = ptx::fma2(t, m2, nl2);
-              if constexpr (decltype(bias)::value != 0) {
-                x.x = biased(x.x, base, slope, col);
-                x.y = biased(x.y, base, slope, col + 1);
+              float2 x = ptx::fma2(t, m2, first2);
+              if constexpr (kBias != kBiasNone) {
+                x.x = biased<kBias>(x.x, bi, col);
+                x.y = biased<kBias>(x.y, bi, col + 1);
               }
               float2 v = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
               // P times the cap's derivative 1 - tanh^2

@@ -458,7 +458,23 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             for (int e = 0; e < 32; ++e) s[q4 * 32 + e] = __uint_as_float(raw[q4][e]);
           }
         }
-        if constexpr (kScore) score_row(s, a.score, c, slope * (float)(j * BN - i), slope);
+        // Scored: a tile that all rows see whole, of capped scores without a bias, keeps its raw
+        // products; the cap rises with its argument, so their maximum is capped alone, and the
+        // others on their way into the exponential.  Any other tile's scores are finished first.
+        bool raw_cap = false;
+        if constexpr (kScore) {
+          // what is masked, or no row, does not choose the form of the tanh for the others
+          if (a.score.cap_log2 != 0.f && (kind == kPartial || g.q0 + (t + 1) * BM > g.N)) {
+            const int lim = i < g.N ? row_lim - j * BN : 0;
+#pragma unroll
+            for (int e = 0; e < BN; ++e) s[e] = e < lim ? s[e] : 0.f;
+          }
+          raw_cap = kind == kFull && a.score.cap_log2 != 0.f && a.score.slopes == nullptr;
+          if (!raw_cap) {
+            const int lo = j * BN - (g.q0 + t * BM + BM - 1), hi = lo + BM + BN - 2;     // of j - i in the tile
+            score_row(s, a.score, c, make_bias(slope, j * BN - i, lo, a.causal && g.prefix == 0 ? min(hi, 0) : hi));
+          }
+        }
         if (kind == kPartial) {
           const int lim = row_lim - j * BN;
 #pragma unroll
@@ -471,7 +487,8 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         for (int q = 8; q < BN / 2; ++q) m8[q & 7] = ptx::max3(m8[q & 7], s[2 * q], s[2 * q + 1]);
         const float mx = ptx::max3(ptx::max3(m8[0], m8[1], m8[2]), ptx::max3(m8[3], m8[4], m8[5]),
                                    fmaxf(m8[6], m8[7]));
-        const float m_cand = kScore ? mx : mx * c;    // scored: already in the log2 domain
+        // scored: the log2 domain already, or still to be capped
+        const float m_cand = kScore ? (raw_cap ? a.score.cap_log2 * tanh_one(mx, a.score) : mx) : mx * c;
         const bool need = m_cand > m_run + kRescaleLog2;   // false when the row is still empty
         const float alpha = need ? ptx::ex2(m_run - m_cand) : 1.f;
         if (__any_sync(0xffffffffu, need) && idx > 0) {
@@ -497,23 +514,43 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const float2 c2 = make_float2(c, c), nm2 = make_float2(-msub, -msub);
         float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                         make_float2(0.f, 0.f)};
+        // to_log2: a pair of scores to its exponents
+        auto exponentials = [&](auto to_log2) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+          for (int half = 0; half < 2; ++half) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float2 s2 = make_float2(s[half * 64 + 2 * e], s[half * 64 + 2 * e + 1]);
-            const float2 x = kScore ? ptx::add2(s2, nm2) : ptx::fma2(s2, c2, nm2);
-            const float2 pp = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
-            ls[e & 3] = ptx::add2(ls[e & 3], pp);      // the normaliser counts every allowed key
-            if constexpr (kDrop) {                  // keys 4u + 2h, 4u + 2h + 1 of word half*4 + e/8
-              const uint32_t u = ((uint32_t)e >> 1) & 3u;
-              const uint32_t x = flags[half * 4 + e / 8] << (u ^ tq);
-              pk[e] = ptx::pack2<F16>(pp.x, pp.y) & ~row_pair_mask(x, e & 1);
+            for (int e = 0; e < 32; ++e) {
+              const float2 x = to_log2(make_float2(s[half * 64 + 2 * e], s[half * 64 + 2 * e + 1]));
+              const float2 pp = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+              ls[e & 3] = ptx::add2(ls[e & 3], pp);      // the normaliser counts every allowed key
+              if constexpr (kDrop) {                  // keys 4u + 2h, 4u + 2h + 1 of word half*4 + e/8
+                const uint32_t u = ((uint32_t)e >> 1) & 3u;
+                const uint32_t x = flags[half * 4 + e / 8] << (u ^ tq);
+                pk[e] = ptx::pack2<F16>(pp.x, pp.y) & ~row_pair_mask(x, e & 1);
+              } else {
+                pk[e] = ptx::pack2<F16>(pp.x, pp.y);
+              }
+            }
+            ptx::tmem_st32(tS + half * 32, pk);
+          }
+        };
+        if constexpr (kScore) {
+          if (!raw_cap) {
+            exponentials([&](float2 x) { return ptx::add2(x, nm2); });
+          } else {
+            float mn = fminf(s[0], s[1]);
+#pragma unroll
+            for (int e = 2; e < BN; e += 2) mn = -ptx::max3(-mn, -s[e], -s[e + 1]);
+            if (__all_sync(0xffffffffu, fmaxf(mx, -mn) <= a.score.poly_limit)) {
+              exponentials([&](float2 x) { return ptx::fma2(poly2(ptx::mul2(x, x), a.score.capped), x, nm2); });
             } else {
-              pk[e] = ptx::pack2<F16>(pp.x, pp.y);
+              const float2 k2 = make_float2(-2.f * a.score.cap_log2, -2.f * a.score.cap_log2);
+              const float2 n2 = make_float2(a.score.cap_log2 - msub, a.score.cap_log2 - msub);
+              exponentials([&](float2 x) { return ptx::fma2(logistic(x, a.score), k2, n2); });
             }
           }
-          ptx::tmem_st32(tS + half * 32, pk);
+        } else {
+          exponentials([&](float2 x) { return ptx::fma2(x, c2, nm2); });
         }
         const float2 lsum = ptx::add2(ptx::add2(ls[0], ls[1]), ptx::add2(ls[2], ls[3]));
         l_run += lsum.x + lsum.y;

@@ -35,7 +35,9 @@ struct ScoreArgs {
   float cap_log2;            // softcap * log2(e); 0: no cap
   float c_exp;               // 2 * scale * log2(e) / softcap
   float poly_limit;          // raw products up to this size may take the polynomial
-  float poly[7];             // tanh(scale s / softcap) = s * sum_i poly[i] s^(2i)
+  // tanh(scale s / softcap) = s * sum_i poly[i] s^(2i), and the same times cap_log2: each
+  // coefficient twice, as packed arithmetic takes it
+  uint64_t poly[5], capped[5];
   const float* slopes;       // [H] or null
   const int32_t* prefix;     // [B] or null
 };

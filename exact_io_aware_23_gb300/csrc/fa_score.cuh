@@ -5,25 +5,25 @@
 //
 // All in the log2 domain, as the softmax is.  The tanh is what costs: through the exponential,
 // 1 - 2 / (1 + exp 2x), it takes two more special-function operations a score beside the softmax's
-// one, and that unit (16 a clock on an SM) then sets the pace of the whole attention at a third of
-// its speed.  Scores far below the cap are the common case, so where no score of a warp's tile
-// exceeds the cap, tanh(x) = x P(x^2) on |x| <= 1 with P of degree 6 (minimax for the relative
-// error, found by exchange: 5.0e-8, less than fp32's own rounding), eight packed operations for two
-// scores on the multiply-add pipe; else the exponential form, for the whole tile.
+// one, and that unit (16 a clock on an SM) then sets the pace.  Scores well below the cap are the
+// common case, so where no score of a warp's tile exceeds 0.6 of the cap, tanh(x) = x P(x^2) with P
+// of degree 4 (minimax for the relative error on |x| <= 0.6, found by exchange: 7.4e-8, about one
+// rounding of fp32), six multiply-adds a score; else the exponential form, for the whole tile.
 #pragma once
 
 #include <cuda_runtime.h>
 #include <math.h>
+#include <string.h>
 
 #include "fa_internal.cuh"
 #include "ptx_sm103.cuh"
 
 namespace fa {
 
-// P's coefficients, ascending
-constexpr double kTanhPoly[7] = {0.9999999502407381,   -0.3333283915308157,  0.13325204075948163,
-                                 -0.05345702957318134, 0.02028998043217086,  -0.0062033791124837,
-                                 0.0010410226362182575};
+// P's coefficients, ascending, and its range
+constexpr double kTanhPoly[5] = {0.9999999268689601, -0.33332309974406416, 0.13310173658059513,
+                                 -0.052101480120587754, 0.01547542749521836};
+constexpr double kTanhRange = 0.6;
 
 // Fills the kernels' form of the score arguments for raw products q . k; false when the cap is out
 // of the range fp32 can hold them in.
@@ -33,38 +33,51 @@ inline bool make_score(const fa_score_mod* m, float scale, ScoreArgs* out) {
   out->slopes = m->alibi_slopes;
   out->prefix = m->prefix_lens;
   if (m->softcap > 0.f) {
-    const double r = (double)scale / (double)m->softcap;
-    out->cap_log2 = (float)((double)m->softcap * 1.4426950408889634);
+    const double r = (double)scale / (double)m->softcap, cap = (double)m->softcap * 1.4426950408889634;
+    out->cap_log2 = (float)cap;
     out->c_exp = (float)(2.0 * r * 1.4426950408889634);
     if (!isfinite(out->cap_log2) || !isfinite(out->c_exp) || !(out->cap_log2 > 0.f)) return false;
-    out->poly_limit = (float)(1.0 / r);
-    double p = r;
-    for (int i = 0; i < 7; ++i, p *= r * r) {
-      out->poly[i] = (float)(kTanhPoly[i] * p);
-      if (!isfinite(out->poly[i])) out->poly_limit = -1.f;      // a tiny cap: always the exponential
-    }
+    out->poly_limit = (float)(kTanhRange / r);
     if (!isfinite(out->poly_limit)) out->poly_limit = 3.4e38f;
+    double p = r;
+    for (int i = 0; i < 5; ++i, p *= r * r) {
+      const float a = (float)(kTanhPoly[i] * p), b = (float)(kTanhPoly[i] * p * cap);
+      if (!isfinite(a) || !isfinite(b)) out->poly_limit = -1.f;   // a tiny cap: always the exponential
+      uint32_t bits;
+      memcpy(&bits, &a, 4);
+      out->poly[i] = (uint64_t)bits << 32 | bits;
+      memcpy(&bits, &b, 4);
+      out->capped[i] = (uint64_t)bits << 32 | bits;
+    }
   }
   return true;
 }
 
-// tanh(scale s / cap) of two raw products, |scale s| <= cap
-__device__ __forceinline__ float2 tanh_poly(float2 s, const ScoreArgs& k) {
-  const float2 z = ptx::mul2(s, s);
-  float2 p = make_float2(k.poly[6], k.poly[6]);
+// P(z) for two values
+__device__ __forceinline__ float2 poly2(float2 z, const uint64_t (&c)[5]) {
+  uint64_t zz, p = c[4];
+  asm("mov.b64 %0, {%1, %2};" : "=l"(zz) : "f"(z.x), "f"(z.y));
 #pragma unroll
-  for (int i = 5; i >= 0; --i) p = ptx::fma2(p, z, make_float2(k.poly[i], k.poly[i]));
-  return ptx::mul2(p, s);
+  for (int i = 3; i >= 0; --i) asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(p), "l"(zz), "l"(c[i]));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+// tanh(scale s / cap) of two raw products within the polynomial's range
+__device__ __forceinline__ float2 tanh_poly(float2 s, const ScoreArgs& k) {
+  return ptx::mul2(poly2(ptx::mul2(s, s), k.poly), s);
 }
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// the same for any s: 1 - 2 / (1 + exp 2x); the exponential may overflow to infinity
+// 1 / (1 + exp 2x) for any s; the exponential may overflow to infinity.  tanh = 1 - 2 times this.
+__device__ __forceinline__ float2 logistic(float2 s, const ScoreArgs& k) {
+  return make_float2(rcp(1.f + ptx::ex2(s.x * k.c_exp)), rcp(1.f + ptx::ex2(s.y * k.c_exp)));
+}
 __device__ __forceinline__ float2 tanh_exp(float2 s, const ScoreArgs& k) {
-  const float r0 = rcp(1.f + ptx::ex2(s.x * k.c_exp)), r1 = rcp(1.f + ptx::ex2(s.y * k.c_exp));
-  return make_float2(fmaf(-2.f, r0, 1.f), fmaf(-2.f, r1, 1.f));
+  return ptx::fma2(logistic(s, k), make_float2(-2.f, -2.f), make_float2(1.f, 1.f));
 }
 // one score by the better form for it
 __device__ __forceinline__ float tanh_one(float s, const ScoreArgs& k) {
@@ -82,50 +95,63 @@ __device__ __forceinline__ bool poly_fits(const float (&s)[N], float limit) {
   return __all_sync(0xffffffffu, mx <= limit);
 }
 
-// The forms of one tile's scores: which tanh, and whether there is a bias.
+// The forms of one tile's scores: which tanh, and which bias.
 enum : int { kCapNone = 0, kCapPoly = 1, kCapExp = 2 };
+enum : int { kBiasNone = 0, kBiasLinear = 1, kBiasAbs = 2 };
 template <int kCap>
 __device__ __forceinline__ float2 tanh_of(float2 s, const ScoreArgs& k) {
   if constexpr (kCap == kCapPoly) return tanh_poly(s, k);
   else return tanh_exp(s, k);
 }
-// -slope |i - j| for score e of a row (or column) whose distances run on by one from `first`:
-// base = slope * first, step = slope
-__device__ __forceinline__ float biased(float x, float base, float step, int e) {
-  return x - fabsf(fmaf(step, (float)e, base));
+// The bias -slope |i - j| over one thread's row (or column) of a tile, whose distances run on by one:
+// at score e it is base + e * step where the tile lies on one side of the diagonal (or the other
+// side is masked), and -|base + e * step| where it crosses it.  `first` is j - i, or i - j, at the
+// first score; lo and hi bound it over the unmasked part of the whole tile.
+struct Bias {
+  float base, step;
+  bool crosses;
+};
+__device__ __forceinline__ Bias make_bias(float slope, int first, int lo, int hi) {
+  const float s = lo >= 0 ? -slope : slope;
+  return Bias{s * (float)first, s, lo < 0 && hi > 0};
+}
+template <int kBias>
+__device__ __forceinline__ float biased(float x, const Bias& b, int e) {
+  if constexpr (kBias == kBiasLinear) return fmaf(b.step, (float)e, x);        // the base is in x already
+  else return x - fabsf(fmaf(b.step, (float)e, b.base));
 }
 
-// Calls body(cap form, with or without bias) as compile-time constants, the same one in the warp.
+// Calls body(cap form, bias form) as compile-time constants, the same ones in the warp.
 template <int V> struct Const { static constexpr int value = V; };
 template <int N, typename Body>
-__device__ __forceinline__ void with_score(const float (&s)[N], const ScoreArgs& k, Body&& body) {
-  const bool bias = k.slopes != nullptr;
-  if (k.cap_log2 == 0.f) {
-    if (bias) body(Const<kCapNone>(), Const<1>());
-    else body(Const<kCapNone>(), Const<0>());
-  } else if (poly_fits(s, k.poly_limit)) {
-    if (bias) body(Const<kCapPoly>(), Const<1>());
-    else body(Const<kCapPoly>(), Const<0>());
-  } else {
-    if (bias) body(Const<kCapExp>(), Const<1>());
-    else body(Const<kCapExp>(), Const<0>());
-  }
+__device__ __forceinline__ void with_score(const float (&s)[N], const ScoreArgs& k, const Bias& b, Body&& body) {
+  auto with_cap = [&](auto cap) {
+    if (k.slopes == nullptr) body(cap, Const<kBiasNone>());
+    else if (!b.crosses) body(cap, Const<kBiasLinear>());
+    else body(cap, Const<kBiasAbs>());
+  };
+  if (k.cap_log2 == 0.f) with_cap(Const<kCapNone>());
+  else if (poly_fits(s, k.poly_limit)) with_cap(Const<kCapPoly>());
+  else with_cap(Const<kCapExp>());
 }
 
 // Scores s[0..N) of one row turned into the log2 domain in place.
 template <int N>
-__device__ __forceinline__ void score_row(float (&s)[N], const ScoreArgs& k, float c, float base, float step) {
-  with_score(s, k, [&](auto cap, auto bias) {
-    constexpr int kCap = decltype(cap)::value;
-    const float2 m2 = kCap == kCapNone ? make_float2(c, c) : make_float2(k.cap_log2, k.cap_log2);
+__device__ __forceinline__ void score_row(float (&s)[N], const ScoreArgs& k, float c, const Bias& b) {
+  with_score(s, k, b, [&](auto cap, auto bias) {
+    constexpr int kCap = decltype(cap)::value, kBias = decltype(bias)::value;
+    const float m = kCap == kCapNone ? c : kCap == kCapPoly ? 1.f : -2.f * k.cap_log2;
+    const float a = (kBias == kBiasLinear ? b.base : 0.f) + (kCap == kCapExp ? k.cap_log2 : 0.f);
+    const float2 m2 = make_float2(m, m), a2 = make_float2(a, a);
 #pragma unroll
     for (int e = 0; e < N; e += 2) {
       float2 x = make_float2(s[e], s[e + 1]);
-      if constexpr (kCap != kCapNone) x = tanh_of<kCap>(x, k);
-      x = ptx::mul2(x, m2);
-      if constexpr (decltype(bias)::value != 0) {
-        x.x = biased(x.x, base, step, e);
-        x.y = biased(x.y, base, step, e + 1);
+      if constexpr (kCap == kCapPoly) x = ptx::fma2(poly2(ptx::mul2(x, x), k.capped), x, a2);
+      else if constexpr (kCap == kCapExp) x = ptx::fma2(logistic(x, k), m2, a2);
+      else x = ptx::fma2(x, m2, a2);
+      if constexpr (kBias != kBiasNone) {
+        x.x = biased<kBias>(x.x, b, e);
+        x.y = biased<kBias>(x.y, b, e + 1);
       }
       s[e] = x.x;
       s[e + 1] = x.y;
