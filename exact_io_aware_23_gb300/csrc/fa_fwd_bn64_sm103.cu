@@ -24,6 +24,7 @@
 #include <math.h>
 
 #include "fa_internal.cuh"
+#include "fa_score.cuh"
 #include "fa_sm103.cuh"
 #include "ptx_sm103.cuh"
 
@@ -66,12 +67,14 @@ struct Bars {            // all mbarriers of one CTA (8 bytes each)
   uint64_t mma_done;
   uint64_t kv_full[8];
   uint64_t kv_empty[8];
+  uint64_t tail;         // scored variant: the last V tile, before its rows behind the keys are cleared
   uint32_t tmem_base;
 };
 
 static_assert(sizeof(Bars) <= 256, "the barrier area is 256 bytes");
 
 // This CTA's tile geometry: which key tiles exist and how each Q tile must treat them.
+template <bool kScore>
 struct Geo {
   int bh;          // (b, h) slice: Q/O slice index
   int ks;          // K/V slice index
@@ -79,19 +82,21 @@ struct Geo {
   int N, kv_lim;   // keys with index >= kv_lim are masked (padding and tail)
   int causal;
   int j_end;       // key tiles [0, j_end) may be live
+  int prefix;      // scored variant: keys every query sees in spite of `causal`
 
   __device__ int kind(int t, int j) const {
     const int r0 = q0 + t * BM;
     if (r0 >= N) return kNone;
     const int r1 = min(r0 + BM, N) - 1;
     const int c0 = j * BN, c1 = c0 + BN - 1;
-    if (c0 >= kv_lim || (causal && c0 > r1)) return kNone;
-    if (c1 < kv_lim && (!causal || c1 <= r0)) return kFull;
+    if (c0 >= kv_lim || (causal && c0 > r1 && !(kScore && c0 < prefix))) return kNone;
+    if (c1 < kv_lim && (!causal || c1 <= r0 || (kScore && c1 < prefix))) return kFull;
     return kPartial;
   }
 };
 
-template <bool F16>
+// kScore: scores capped, biased or with a prefix (fa_score.cuh).
+template <bool F16, bool kScore>
 __global__ void __launch_bounds__(kThreads, 2)
 fwd_bn64_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, FwdArgs a) {
@@ -114,7 +119,7 @@ fwd_bn64_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     const int slot = a.heads_fastest ? unit / BH : unit % n_pairs;
     const int pair = a.causal ? n_pairs - 1 - slot : slot;
     const int b = bh / a.H, h = bh % a.H;
-    Geo g;
+    Geo<kScore> g;
     g.bh = bh;
     g.q0 = pair * 2 * BM;
     g.N = a.N;
@@ -123,7 +128,12 @@ fwd_bn64_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     g.kv_lim = a.kv_lens != nullptr ? max(0, min(a.Nk, (int)a.kv_lens[b])) : a.Nk;
     g.causal = a.causal;
     int last_key = g.kv_lim;
-    if (a.causal) last_key = min(last_key, min(g.q0 + 2 * BM, g.N));
+    if constexpr (kScore) {
+      g.prefix = a.causal && a.score.prefix != nullptr ? min(max(a.score.prefix[b], 0), g.N) : 0;
+      if (a.causal) last_key = min(last_key, max(min(g.q0 + 2 * BM, g.N), g.prefix));
+    } else {
+      if (a.causal) last_key = min(last_key, min(g.q0 + 2 * BM, g.N));
+    }
     g.j_end = (last_key + BN - 1) / BN;
     return g;
   };
@@ -137,6 +147,7 @@ fwd_bn64_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
       ptx::mbar_init(ptx::smem_u32(&bars->pv_done[t]), 1);
     }
     ptx::mbar_init(ptx::smem_u32(&bars->mma_done), 1);
+    if constexpr (kScore) ptx::mbar_init(ptx::smem_u32(&bars->tail), 1);
     for (int s = 0; s < C::kSlots; ++s) {
       ptx::mbar_init(ptx::smem_u32(&bars->kv_full[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&bars->kv_empty[s]), 1);
@@ -154,7 +165,7 @@ fwd_bn64_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
 
   if (warp >= 8) {
     ptx::regs_dec<kRegsOther>();
-    const Geo g = make_geo();
+    const auto g = make_geo();
     if (warp == 8 && lane == 0) {
       // ------------------------------- TMA producer (Q, K) ------------------------------------
       ptx::tma_prefetch_desc(&tmQ);
@@ -181,19 +192,31 @@ fwd_bn64_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         if (a.dbg.inject == 1 && m == 0) continue;
         ptx::mbar_wait(ptx::smem_u32(&bars->kv_full[m % C::kKSlots]), (m / C::kKSlots) & 1, lim_ms, a.err);
       }
-    } else if (warp == 10 && lane == 0) {
+    } else if (warp == 10 && (kScore || lane == 0)) {
       // ------------------------------- TMA producer of V ------------------------------------
+      const bool has_tail = kScore && g.j_end * BN > g.kv_lim && g.kv_lim < a.Nk;
       int n = 0;                                   // V tiles issued
       bool ok = true;
-      for (int j = 0; j < g.j_end && ok; ++j, ++n) {
+      for (int j = 0; lane == 0 && j < g.j_end && ok; ++j, ++n) {
         const int slot = C::kKSlots + n % C::kVSlots;
         ok = ptx::mbar_wait(ptx::smem_u32(&bars->kv_empty[slot]), ((n / C::kVSlots) & 1) ^ 1, lim_ms, a.err);
         if (!ok) break;
-        const uint32_t fb = ptx::smem_u32(&bars->kv_full[slot]);
+        const uint32_t fb = ptx::smem_u32(has_tail && j == g.j_end - 1 ? &bars->tail : &bars->kv_full[slot]);
         ptx::mbar_arrive_expect_tx(fb, C::kTileBytes);
         ptx::tma_load_3d(sKV + slot * C::kTileBytes, &tmV, fb, 0, j * BN, g.ks);
       }
-      for (int m = max(0, n - C::kVSlots); m < n; ++m)
+      if constexpr (kScore) {
+        // The last tile's rows behind the keys multiply probabilities of 0: cleared before the
+        // product may read the tile.
+        const int issued = __shfl_sync(0xffffffffu, ok ? n : 0, 0);
+        if (has_tail && issued > 0) {
+          const int slot = C::kKSlots + (issued - 1) % C::kVSlots;
+          ptx::mbar_wait(ptx::smem_u32(&bars->tail), 0, lim_ms, a.err);
+          zero_rows<D, BN>(smem + C::kKVOff + slot * C::kTileBytes, g.kv_lim - (g.j_end - 1) * BN);
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->kv_full[slot]));
+        }
+      }
+      for (int m = max(0, n - C::kVSlots); lane == 0 && m < n; ++m)
         ptx::mbar_wait(ptx::smem_u32(&bars->kv_full[C::kKSlots + m % C::kVSlots]), (m / C::kVSlots) & 1, lim_ms, a.err);
     } else if (warp == 9 && lane == 0) {
       // ------------------------------- MMA issuer ---------------------------------------------
@@ -266,7 +289,7 @@ fwd_bn64_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   } else {
     // ------------------------------- softmax warpgroups -----------------------------------------
     ptx::regs_inc<kRegsSoftmax>();
-    const Geo g = make_geo();
+    const auto g = make_geo();
     const int t = warp / 4;
     const int sub = warp % 4;
     const int r = sub * 32 + lane;                  // TMEM lane == row within the Q tile
@@ -276,7 +299,11 @@ fwd_bn64_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     const uint32_t tO = tmem + lane_off + 128 + t * D;
     const float c = a.scale * kLog2e;               // scores -> log2 domain
     int row_lim = g.kv_lim;
-    if (a.causal) row_lim = min(row_lim, i + 1);
+    if (a.causal) row_lim = min(row_lim, kScore ? max(i + 1, g.prefix) : i + 1);
+    float slope = 0.f;                              // of the distance bias, in the log2 domain
+    if constexpr (kScore)
+      if (a.score.slopes != nullptr) slope = a.score.slopes[g.bh % a.H] * kLog2e;
+    const bool plain = !kScore || (a.score.cap_log2 == 0.f && a.score.slopes == nullptr);   // only a prefix
     // How this Q tile treats key tile j, as two thresholds (fewer live registers than the
     // geometry): full below j_full, partly masked below j_none, skipped from there on.
     int j_full = 0, j_none = 0;
@@ -316,6 +343,22 @@ fwd_bn64_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
             for (int e = 0; e < 32; ++e) s[q2 * 32 + e] = __uint_as_float(raw[q2][e]);
           }
         }
+        // Scored: as in fa_fwd_sm103.cu, a tile that all rows see whole, of capped scores without a
+        // bias, is capped on its way into the exponential; any other is finished first.
+        bool raw_cap = false;
+        if constexpr (kScore) {
+          // what is masked, or no row, does not choose the form of the tanh for the others
+          if (a.score.cap_log2 != 0.f && (kind == kPartial || g.q0 + (t + 1) * BM > g.N)) {
+            const int lim = i < g.N ? row_lim - j * BN : 0;
+#pragma unroll
+            for (int e = 0; e < BN; ++e) s[e] = e < lim ? s[e] : 0.f;
+          }
+          raw_cap = kind == kFull && a.score.cap_log2 != 0.f && a.score.slopes == nullptr;
+          if (!raw_cap && !plain) {
+            const int lo = j * BN - (g.q0 + t * BM + BM - 1), hi = lo + BM + BN - 2;     // of j - i in the tile
+            score_row(s, a.score, c, make_bias(slope, j * BN - i, lo, a.causal && g.prefix == 0 ? min(hi, 0) : hi));
+          }
+        }
         if (kind == kPartial) {
           const int lim = row_lim - j * BN;
 #pragma unroll
@@ -327,7 +370,7 @@ fwd_bn64_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
 #pragma unroll
         for (int q = 4; q < BN / 2; ++q) m4[q & 3] = ptx::max3(m4[q & 3], s[2 * q], s[2 * q + 1]);
         const float mx = fmaxf(ptx::max3(m4[0], m4[1], m4[2]), m4[3]);
-        const float m_cand = mx * c;
+        const float m_cand = !kScore || plain ? mx * c : raw_cap ? a.score.cap_log2 * tanh_one(mx, a.score) : mx;
         const bool need = m_cand > m_run + kRescaleLog2;   // false when the row is still empty
         const float alpha = need ? ptx::ex2(m_run - m_cand) : 1.f;
         if (need) {
@@ -338,12 +381,35 @@ fwd_bn64_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         // p = exp2(s*c - m) on column pairs; 2 independent packed partial sums
         const float2 c2 = make_float2(c, c), nm2 = make_float2(-msub, -msub);
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // to_log2: a pair of scores to its exponents
+        auto exponentials = [&](auto to_log2) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float2 x = ptx::fma2(make_float2(s[2 * e], s[2 * e + 1]), c2, nm2);
-          const float2 pp = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
-          ls[e & 1] = ptx::add2(ls[e & 1], pp);        // the normaliser counts every allowed key
-          pk[e] = ptx::pack2<F16>(pp.x, pp.y);
+          for (int e = 0; e < 32; ++e) {
+            const float2 x = to_log2(make_float2(s[2 * e], s[2 * e + 1]));
+            const float2 pp = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+            ls[e & 1] = ptx::add2(ls[e & 1], pp);        // the normaliser counts every allowed key
+            pk[e] = ptx::pack2<F16>(pp.x, pp.y);
+          }
+        };
+        if constexpr (kScore) {
+          if (plain) {
+            exponentials([&](float2 x) { return ptx::fma2(x, c2, nm2); });
+          } else if (!raw_cap) {
+            exponentials([&](float2 x) { return ptx::add2(x, nm2); });
+          } else {
+            float mn = fminf(s[0], s[1]);
+#pragma unroll
+            for (int e = 2; e < BN; e += 2) mn = -ptx::max3(-mn, -s[e], -s[e + 1]);
+            if (__all_sync(0xffffffffu, fmaxf(mx, -mn) <= a.score.poly_limit)) {
+              exponentials([&](float2 x) { return ptx::fma2(poly2(ptx::mul2(x, x), a.score.capped), x, nm2); });
+            } else {
+              const float2 k2 = make_float2(-2.f * a.score.cap_log2, -2.f * a.score.cap_log2);
+              const float2 n2 = make_float2(a.score.cap_log2 - msub, a.score.cap_log2 - msub);
+              exponentials([&](float2 x) { return ptx::fma2(logistic(x, a.score), k2, n2); });
+            }
+          }
+        } else {
+          exponentials([&](float2 x) { return ptx::fma2(x, c2, nm2); });
         }
         ptx::tmem_st32(tS, pk);
         const float2 lsum = ptx::add2(ls[0], ls[1]);
@@ -422,14 +488,14 @@ cudaError_t make_map(CUtensorMap* m, const void* base, int N, int BH, int rows, 
                            CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <bool F16>
+template <bool F16, bool kScore>
 cudaError_t launch(const FwdArgs& a, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
   cudaError_t e;
   if ((e = make_map(&mq, a.q, a.N, a.B * a.H, BM, F16)) != cudaSuccess) return e;
   if ((e = make_map(&mk, a.k, a.Nk, a.B * a.Hkv, BN, F16)) != cudaSuccess) return e;
   if ((e = make_map(&mv, a.v, a.Nk, a.B * a.Hkv, BN, F16)) != cudaSuccess) return e;
-  auto kern = fwd_bn64_sm103_kernel<F16>;
+  auto kern = fwd_bn64_sm103_kernel<F16, kScore>;
   const int smem = Cfg<F16>::kSmem;
   // The warp groups re-split the CTA's registers; that only completes if the launch holds at
   // least that many.
@@ -458,7 +524,8 @@ cudaError_t launch_fwd_bn64_sm103(const FwdArgs& a, fa_dtype dt, cudaStream_t s)
   if (a.d != 64 || a.drop.enabled || a.plan != nullptr || a.block_mask != nullptr || a.cu_seqlens != nullptr ||
       a.n_splits != 1 || a.o_part != nullptr || a.Nk != a.N || a.rows != a.N)
     return cudaErrorInvalidValue;
-  return dt == FA_FP16 ? launch<true>(a, s) : launch<false>(a, s);
+  if (a.scored) return dt == FA_FP16 ? launch<true, true>(a, s) : launch<false, true>(a, s);
+  return dt == FA_FP16 ? launch<true, false>(a, s) : launch<false, false>(a, s);
 }
 
 }  // namespace fa

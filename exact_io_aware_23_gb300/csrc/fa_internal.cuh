@@ -37,7 +37,7 @@ struct ScoreArgs {
   float poly_limit;          // raw products up to this size may take the polynomial
   // tanh(scale s / softcap) = s * sum_i poly[i] s^(2i), and the same times cap_log2: each
   // coefficient twice, as packed arithmetic takes it
-  uint64_t poly[5], capped[5];
+  uint64_t poly[4], capped[4];
   const float* slopes;       // [H] or null
   const int32_t* prefix;     // [B] or null
 };

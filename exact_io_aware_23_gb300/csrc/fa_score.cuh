@@ -6,9 +6,11 @@
 // All in the log2 domain, as the softmax is.  The tanh is what costs: through the exponential,
 // 1 - 2 / (1 + exp 2x), it takes two more special-function operations a score beside the softmax's
 // one, and that unit (16 a clock on an SM) then sets the pace.  Scores well below the cap are the
-// common case, so where no score of a warp's tile exceeds 0.6 of the cap, tanh(x) = x P(x^2) with P
-// of degree 4 (minimax for the relative error on |x| <= 0.6, found by exchange: 7.4e-8, about one
-// rounding of fp32), six multiply-adds a score; else the exponential form, for the whole tile.
+// common case, so where no score of a warp's tile exceeds 0.4 of the cap, tanh(x) = x P(x^2) with P
+// of degree 3 (minimax for the relative error on |x| <= 0.4, found by exchange: 9.9e-8, less than
+// two roundings of fp32), five multiply-adds a score; else the exponential form, for the whole tile.
+// (B1 H16 Hkv4 N8192 d128 causal, forward: each multiply-add costs 16 us of 290, the exponential
+// form 140.  Degree 4 would reach to 0.6 of the cap, degree 6 to the cap itself.)
 #pragma once
 
 #include <cuda_runtime.h>
@@ -21,9 +23,9 @@
 namespace fa {
 
 // P's coefficients, ascending, and its range
-constexpr double kTanhPoly[5] = {0.9999999268689601, -0.33332309974406416, 0.13310173658059513,
-                                 -0.052101480120587754, 0.01547542749521836};
-constexpr double kTanhRange = 0.6;
+constexpr double kTanhPoly[4] = {0.999999901900935, -0.3333136245895285, 0.13270976759047418,
+                                 -0.04755360362774448};
+constexpr double kTanhRange = 0.4;
 
 // Fills the kernels' form of the score arguments for raw products q . k; false when the cap is out
 // of the range fp32 can hold them in.
@@ -40,7 +42,7 @@ inline bool make_score(const fa_score_mod* m, float scale, ScoreArgs* out) {
     out->poly_limit = (float)(kTanhRange / r);
     if (!isfinite(out->poly_limit)) out->poly_limit = 3.4e38f;
     double p = r;
-    for (int i = 0; i < 5; ++i, p *= r * r) {
+    for (int i = 0; i < 4; ++i, p *= r * r) {
       const float a = (float)(kTanhPoly[i] * p), b = (float)(kTanhPoly[i] * p * cap);
       if (!isfinite(a) || !isfinite(b)) out->poly_limit = -1.f;   // a tiny cap: always the exponential
       uint32_t bits;
@@ -54,11 +56,11 @@ inline bool make_score(const fa_score_mod* m, float scale, ScoreArgs* out) {
 }
 
 // P(z) for two values
-__device__ __forceinline__ float2 poly2(float2 z, const uint64_t (&c)[5]) {
-  uint64_t zz, p = c[4];
+__device__ __forceinline__ float2 poly2(float2 z, const uint64_t (&c)[4]) {
+  uint64_t zz, p = c[3];
   asm("mov.b64 %0, {%1, %2};" : "=l"(zz) : "f"(z.x), "f"(z.y));
 #pragma unroll
-  for (int i = 3; i >= 0; --i) asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(p), "l"(zz), "l"(c[i]));
+  for (int i = 2; i >= 0; --i) asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(p), "l"(zz), "l"(c[i]));
   float2 r;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
   return r;
@@ -159,17 +161,17 @@ __device__ __forceinline__ void score_row(float (&s)[N], const ScoreArgs& k, flo
   });
 }
 
-// Rows [r0, 128) of a 128-row operand tile in shared memory (d / 64 halves of 128-byte rows; the
-// swizzle moves bytes within a row only) set to zero by one warp, before the tensor cores read
-// them: what the memory behind a sequence holds may be NaN, and 0 * NaN is not 0.
-template <int D>
+// Rows [r0, kRows) of an operand tile in shared memory (d / 64 halves of 128-byte rows; the swizzle
+// moves bytes within a row only) set to zero by one warp, before the tensor cores read them: what
+// the memory behind a sequence holds may be NaN, and 0 * NaN is not 0.
+template <int D, int kRows = 128>
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int r0) {
   const int lane = threadIdx.x % 32;
 #pragma unroll 1
-  for (int r = r0 + lane / 8; r < 128; r += 4)
+  for (int r = r0 + lane / 8; r < kRows; r += 4)
 #pragma unroll
     for (int hh = 0; hh < D / 64; ++hh)
-      *reinterpret_cast<uint4*>(tile + hh * 128 * 128 + r * 128 + (lane % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(tile + hh * kRows * 128 + r * 128 + (lane % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
   ptx::fence_proxy_async_smem();
   __syncwarp();
 }

