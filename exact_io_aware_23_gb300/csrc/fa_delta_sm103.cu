@@ -60,7 +60,7 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 256, "");
 
-template <int D, bool F16>
+template <int D, bool F16, int kMod>
 __global__ void __launch_bounds__(kThreads, 1)
 delta_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO, const BwdArgs a) {
@@ -187,12 +187,13 @@ delta_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     const uint32_t lane_off = (uint32_t)(sub * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::kS + t * 128, tP = tmem + lane_off + C::kDP + t * 128;
     const float c = a.scale * kLog2e;
-    const float2 m2 = a.score.cap_log2 == 0.f ? make_float2(c, c) : make_float2(a.score.cap_log2, a.score.cap_log2);
+    const float m = (kMod & kModCap) == 0 ? c : a.score.cap_log2;
+    const float2 m2 = make_float2(m, m);
     const size_t row = (size_t)qs * a.rows + row0 + i;
     const float L = i < N ? a.lse[row] : -INFINITY;
     const float nl = L == -INFINITY ? -INFINITY : -L * kLog2e;     // P vanishes on empty rows
     const float2 nl2 = make_float2(nl, nl);
-    const float slope = a.score.slopes != nullptr ? a.score.slopes[h] * kLog2e : 0.f;
+    const float slope = (kMod & kModBias) != 0 ? a.score.slopes[h] * kLog2e : 0.f;
     const int seen = a.causal ? min(kv_lim, max(i + 1, prefix)) : kv_lim;        // keys of the row
     const int r0 = q0 + t * BM, r1 = min(r0 + BM, N) - 1;
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -232,7 +233,7 @@ delta_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         }
         const int lo = c0 - (r0 + BM - 1), hi = lo + BM + BN - 2;              // of j - i in the tile
         const Bias bi = make_bias(slope, c0 - i, lo, a.causal && prefix == 0 ? min(hi, 0) : hi);
-        with_score(p, a.score, bi, [&](auto cap, auto bias) {
+        with_score<kMod>(p, a.score, bi, [&](auto cap, auto bias) {
           constexpr int kCap = decltype(cap)::value, kBias = decltype(bias)::value;
           const float first = kBias == kBiasLinear ? nl + bi.base : nl;
           const float2 first2 = make_float2(first, first);
@@ -299,7 +300,7 @@ cudaError_t make_map(CUtensorMap* m, const void* base, int D, int N, int BH, boo
                            strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int D, bool F16>
+template <int D, bool F16, int kMod>
 cudaError_t launch(const BwdArgs& a, cudaStream_t s) {
   CUtensorMap mq, mk, mv, mdo;
   const bool packed = a.cu_seqlens != nullptr;
@@ -309,7 +310,7 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t s) {
   if ((e = make_map(&mk, a.k, D, a.rows, kv_slices, F16)) != cudaSuccess) return e;
   if ((e = make_map(&mv, a.v, D, a.rows, kv_slices, F16)) != cudaSuccess) return e;
   if ((e = make_map(&mdo, a.dO, D, a.rows, q_slices, F16)) != cudaSuccess) return e;
-  auto kern = delta_kernel<D, F16>;
+  auto kern = delta_kernel<D, F16, kMod>;
   static LaunchSetup setup;
   // The warp groups re-split the CTA's registers; that only completes if the launch holds them.
   int regs = 0;
@@ -319,11 +320,21 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+template <int kMod>
+cudaError_t dispatch(const BwdArgs& a, fa_dtype dt, cudaStream_t s) {
+  if (dt == FA_FP16) return a.d == 64 ? launch<64, true, kMod>(a, s) : launch<128, true, kMod>(a, s);
+  return a.d == 64 ? launch<64, false, kMod>(a, s) : launch<128, false, kMod>(a, s);
+}
+
 }  // namespace
 
 cudaError_t launch_delta_sm103(const BwdArgs& a, fa_dtype dt, cudaStream_t s) {
-  if (dt == FA_FP16) return a.d == 64 ? launch<64, true>(a, s) : launch<128, true>(a, s);
-  return a.d == 64 ? launch<64, false>(a, s) : launch<128, false>(a, s);
+  switch (mod_of(a.score)) {
+    case kModCap: return dispatch<kModCap>(a, dt, s);
+    case kModBias: return dispatch<kModBias>(a, dt, s);
+    case kModBoth: return dispatch<kModBoth>(a, dt, s);
+    default: return dispatch<kModPrefix>(a, dt, s);
+  }
 }
 
 }  // namespace fa

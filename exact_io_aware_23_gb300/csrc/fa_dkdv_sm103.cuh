@@ -119,12 +119,13 @@ struct Geo {
   }
 };
 
-template <int D, bool F16, bool kDrop, bool kScore>
+template <int D, bool F16, bool kDrop, int kMod>
 __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                     const CUtensorMap& tmV, const CUtensorMap& tmDO,
                                     const BwdArgs& a) {
   using C = Cfg<D, F16>;
   using L = BwdLayout<D>;
+  constexpr bool kScore = kMod != kModNone;
   constexpr int kCols = L::kCols;                // query columns per compute warpgroup
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -414,7 +415,7 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
     for (int hg = 0; hg < G && ok; ++hg) {
     float slope = 0.f;                               // of the head's distance bias, log2 domain
     if constexpr (kScore)
-      if (a.score.slopes != nullptr) slope = __ldg(a.score.slopes + hk * G + hg) * kLog2e;
+      if ((kMod & kModBias) != 0) slope = __ldg(a.score.slopes + hk * G + hg) * kLog2e;
     for (int i = g.next(g.i_begin); i < g.i_end; i = g.next(i + 1), ++n) {
       const int vs = n & 1;
       // dropout: this key's drop flags over the warpgroup's queries, 16 per word (generated
@@ -460,8 +461,8 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
           uint32_t pk[kCols / 2];
           const int lo = i * BM - (g.k0 + BN - 1), hi = lo + BM + BN - 2;      // of i - j in the tile
           const Bias bi = make_bias(slope, q0 - key, a.causal && g.prefix == 0 ? max(lo, 0) : lo, hi);
-          const float2 m2 = a.score.cap_log2 == 0.f ? c2 : make_float2(a.score.cap_log2, a.score.cap_log2);
-          with_score(p, a.score, bi, [&](auto cap, auto bias) {
+          const float2 m2 = (kMod & kModCap) == 0 ? c2 : make_float2(a.score.cap_log2, a.score.cap_log2);
+          with_score<kMod>(p, a.score, bi, [&](auto cap, auto bias) {
             constexpr int kCap = decltype(cap)::value, kBias = decltype(bias)::value;
             const float base = kBias == kBiasLinear ? bi.base : 0.f;
 #pragma unroll

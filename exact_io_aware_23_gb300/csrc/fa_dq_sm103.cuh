@@ -109,12 +109,13 @@ struct Geo {
   }
 };
 
-template <int D, bool F16, bool kDrop, bool kScore>
+template <int D, bool F16, bool kDrop, int kMod>
 __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                     const CUtensorMap& tmV, const CUtensorMap& tmDO,
                                     const BwdArgs& a) {
   using C = Cfg<D, F16>;
   using L = BwdLayout<D>;
+  constexpr bool kScore = kMod != kModNone;
   constexpr int kCols = L::kCols;                // keys per compute warpgroup
   constexpr int kNR = kCols / 32;                // 32-column TMEM loads per operand
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -344,7 +345,7 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
     const float2 dd2 = make_float2(dd, dd);
     float slope = 0.f;                               // of the distance bias, log2 domain
     if constexpr (kScore)
-      if (a.score.slopes != nullptr) slope = a.score.slopes[h] * kLog2e;
+      if ((kMod & kModBias) != 0) slope = a.score.slopes[h] * kLog2e;
     bool ok = true;
     int n = 0;
     const uint32_t tq = (uint32_t)lane & 3u;         // this row within its 4-row dropout block
@@ -387,9 +388,9 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
           }
           const int lo = j * BN - (g.q0 + BM - 1), hi = lo + BM + BN - 2;      // of j - i in the tile
           const Bias bi = make_bias(slope, k0 - q, lo, a.causal && g.prefix == 0 ? min(hi, 0) : hi);
-          const float2 m2 = a.score.cap_log2 == 0.f ? c2 : make_float2(a.score.cap_log2, a.score.cap_log2);
+          const float2 m2 = (kMod & kModCap) == 0 ? c2 : make_float2(a.score.cap_log2, a.score.cap_log2);
           const int seen = !g.causal ? g.kv_lim : min(g.kv_lim, max(q + 1, g.prefix));   // keys of the row
-          with_score(p, a.score, bi, [&](auto cap, auto bias) {
+          with_score<kMod>(p, a.score, bi, [&](auto cap, auto bias) {
             constexpr int kCap = decltype(cap)::value, kBias = decltype(bias)::value;
             const float first = kBias == kBiasLinear ? nl + bi.base : nl;
             const float2 first2 = make_float2(first, first);

@@ -123,24 +123,39 @@ __device__ __forceinline__ float biased(float x, const Bias& b, int e) {
   else return x - fabsf(fmaf(b.step, (float)e, b.base));
 }
 
+// What a call modifies, as the backward's kernels are compiled for it: one kernel for all kinds keeps
+// every kind's registers live and spills (B1 H16 Hkv4 N8192 d128 causal with a prefix alone, dK, dV
+// and dQ: 799 us by the kernel of all kinds, PREFIXUS by its own, 684 without a modification).
+enum : int { kModNone = 0, kModCap = 1, kModBias = 2, kModBoth = 3, kModPrefix = 4 };
+__host__ inline int mod_of(const ScoreArgs& k) {
+  const int m = (k.cap_log2 != 0.f ? kModCap : 0) | (k.slopes != nullptr ? kModBias : 0);
+  return m != 0 ? m : kModPrefix;
+}
+
 // Calls body(cap form, bias form) as compile-time constants, the same ones in the warp.
 template <int V> struct Const { static constexpr int value = V; };
-template <int N, typename Body>
+template <int kMod, int N, typename Body>
 __device__ __forceinline__ void with_score(const float (&s)[N], const ScoreArgs& k, const Bias& b, Body&& body) {
   auto with_cap = [&](auto cap) {
-    if (k.slopes == nullptr) body(cap, Const<kBiasNone>());
-    else if (!b.crosses) body(cap, Const<kBiasLinear>());
-    else body(cap, Const<kBiasAbs>());
+    if constexpr ((kMod & kModBias) == 0) {
+      body(cap, Const<kBiasNone>());
+    } else {
+      if (!b.crosses) body(cap, Const<kBiasLinear>());
+      else body(cap, Const<kBiasAbs>());
+    }
   };
-  if (k.cap_log2 == 0.f) with_cap(Const<kCapNone>());
-  else if (poly_fits(s, k.poly_limit)) with_cap(Const<kCapPoly>());
-  else with_cap(Const<kCapExp>());
+  if constexpr ((kMod & kModCap) == 0) {
+    with_cap(Const<kCapNone>());
+  } else {
+    if (poly_fits(s, k.poly_limit)) with_cap(Const<kCapPoly>());
+    else with_cap(Const<kCapExp>());
+  }
 }
 
 // Scores s[0..N) of one row turned into the log2 domain in place.
 template <int N>
 __device__ __forceinline__ void score_row(float (&s)[N], const ScoreArgs& k, float c, const Bias& b) {
-  with_score(s, k, b, [&](auto cap, auto bias) {
+  auto body = [&](auto cap, auto bias) {
     constexpr int kCap = decltype(cap)::value, kBias = decltype(bias)::value;
     const float m = kCap == kCapNone ? c : kCap == kCapPoly ? 1.f : -2.f * k.cap_log2;
     const float a = (kBias == kBiasLinear ? b.base : 0.f) + (kCap == kCapExp ? k.cap_log2 : 0.f);
@@ -158,7 +173,10 @@ __device__ __forceinline__ void score_row(float (&s)[N], const ScoreArgs& k, flo
       s[e] = x.x;
       s[e + 1] = x.y;
     }
-  });
+  };
+  if (k.slopes == nullptr) with_score<kModCap>(s, k, b, body);
+  else if (k.cap_log2 == 0.f) with_score<kModBias>(s, k, b, body);
+  else with_score<kModBoth>(s, k, b, body);
 }
 
 // Rows [r0, kRows) of an operand tile in shared memory (d / 64 halves of 128-byte rows; the swizzle

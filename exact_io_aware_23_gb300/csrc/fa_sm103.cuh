@@ -27,6 +27,12 @@ cudaError_t launch_bwd_sm103(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
 // is added from several CTAs.
 cudaError_t launch_bwd_split_sm103(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
 
+// ... with score modifications, by kind (fa_score.cuh)
+cudaError_t launch_bwd_scored_cap(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_bwd_scored_bias(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_bwd_scored_both(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_bwd_scored_prefix(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
+
 // D = rowsum(P * dP) of the scored backward (tcgen05 + TMA), d in {64, 128}; takes the place of the
 // preprocess kernel there.
 cudaError_t launch_delta_sm103(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
