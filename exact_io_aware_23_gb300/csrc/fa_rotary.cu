@@ -28,7 +28,7 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kUnit = 16;                  // values per unit, 8 pairs
 constexpr int kBatch = 4;                  // heads whose values a thread has in flight together
 
@@ -180,17 +180,23 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, co
     const int64_t b = m / a.N, n = m % a.N;
     const T* x = static_cast<const T*>(a.x) + b * a.xs.b + n * a.xs.n + h0 * a.xs.h;
     T* y = static_cast<T*>(a.y) + b * a.ys.b + n * a.ys.n + h0 * a.ys.h;
-    float c[8], s[8];
-    if (t.turns) angles(frac, a.positions[b * a.pos_stride + n], a.rot, c, s);
-    // kBatch heads at a time: their reads are all in flight before the first is used
-    for (int h = h0; h < h1; h += kBatch) {
-      Raw8<T> lo[kBatch], hi[kBatch];
+    // kBatch heads at a time: their reads are all in flight before the first is used, the first
+    // ones' while the sines are computed
+    Raw8<T> lo[kBatch], hi[kBatch];
+    auto read = [&](int h) {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
         if (h + i < h1) {
           lo[i] = load8(x + i * a.xs.h + t.lo);
           hi[i] = load8(x + i * a.xs.h + t.hi);
         }
+      x += kBatch * a.xs.h;
+    };
+    read(h0);
+    float c[8], s[8];
+    if (t.turns) angles(frac, a.positions[b * a.pos_stride + n], a.rot, c, s);
+    for (int h = h0; h < h1; h += kBatch) {
+      if (h > h0) read(h);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
         if (h + i < h1) {
@@ -198,7 +204,6 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, co
           store8(y + i * a.ys.h + t.lo, lo[i]);
           store8(y + i * a.ys.h + t.hi, hi[i]);
         }
-      x += kBatch * a.xs.h;
       y += kBatch * a.ys.h;
     }
   }
@@ -237,9 +242,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
         page = -1;
       }
     }
+    const int64_t row = (int64_t)page * a.cache.page_stride + (int64_t)slot * a.cache.token_stride;
     float c[8], s[8];
     if (turns && there) angles(frac, pos, a.rot, c, s);
-    const int64_t row = (int64_t)page * a.cache.page_stride + (int64_t)slot * a.cache.token_stride;
     for (int h = h0; h < h1; h += kBatch) {
       Raw8<T> lo[kBatch], hi[kBatch];
       T* to[kBatch];
@@ -272,10 +277,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
 }
 
 // Heads a block walks over.  More of them share one computation of the sines; fewer give small
-// calls more blocks: halved until there are two blocks per SM.
+// calls more blocks: halved until there are eight blocks of 128 threads per SM, about two waves.
+// (Cache write of 4 ragged prompts of 4096 tokens, 48 heads: 63 us; with two or four per SM 70, with 32
+// per SM 84.)
 int heads_per_block(int64_t token_blocks, int heads, int sms) {
   int per = heads;
-  while (per > 1 && token_blocks * ((heads + per - 1) / per) < 2 * sms) per = (per + 1) / 2;
+  while (per > 1 && token_blocks * ((heads + per - 1) / per) < 8 * sms) per = (per + 1) / 2;
   return per;
 }
 
