@@ -59,7 +59,9 @@ struct Cfg {
   static constexpr int kRing = kStages * kStage;              // per warp
   static constexpr int kStat = kWarps * kRing;
   static constexpr int kFrom = kStat + kWarps * kRows * 8;
-  static constexpr int kSmem = kFrom + kWarps * 4 + 16;         // and a flag
+  static constexpr int kParted = kFrom + kWarps * 4 + 16;       // after a flag: statistics to be joined
+  static constexpr int kJoin = 64;                              // parts
+  static constexpr int kSmem = kParted + kJoin * kRows * 8;
   static_assert(kStage >= kRows * D * 4, "a warp's output to be joined fits the slot of its last tile");
 };
 
@@ -235,13 +237,17 @@ __device__ __forceinline__ void write_row4(const PagedArgs& a, int64_t row, int 
 // B1 H32 Hkv8 with 32K keys).  Between its own store and its reads of the others each CTA has a
 // sequentially consistent fence, so the last of them sees all words set, or cleared by one that did;
 // should two see them, both join the parts, to the same bits.  Who joins clears the words, for a
-// captured call's next run under the same number.  Whatever else a fresh workspace holds is not the
+// captured call's next run under the same number (another that reads them cleared has nothing to do).  Whatever else a fresh workspace holds is not the
 // number: it has 64 bits, starts at another place in every process, and is not used twice in one.
 // So no launch is spent on clearing the words first.  (By cudaMemsetAsync: 3 us of a call's 40.)
 __device__ __forceinline__ bool all_arrived(unsigned long long* words, int mine, int part0, int ca, int cb,
                                             unsigned long long call) {
   const int lane = threadIdx.x % 32;
-  if (lane == 0) asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(words + mine), "l"(call) : "memory");
+  if (lane == 0) {
+    // releases what the whole CTA wrote before its barrier
+    asm volatile("fence.acq_rel.gpu;" ::: "memory");
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(words + mine), "l"(call) : "memory");
+  }
   __syncwarp();
   asm volatile("fence.sc.gpu;" ::: "memory");
   bool there = true;
@@ -251,11 +257,7 @@ __device__ __forceinline__ bool all_arrived(unsigned long long* words, int mine,
     there = there && w == call;
   }
   there = __all_sync(0xffffffffu, there);
-  if (there) {
-    asm volatile("fence.acq_rel.gpu;" ::: "memory");
-    for (int i = ca + lane; i <= cb; i += 32)
-      asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(words + (i == ca ? part0 : 2 * i)), "l"(0ull) : "memory");
-  }
+  if (there) asm volatile("fence.acq_rel.gpu;" ::: "memory");     // the parts, for the CTA after its barrier
   return there;
 }
 
@@ -386,8 +388,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
     cp_commit();
     slot = slot + 1 == C::kStages ? 0 : slot + 1;
   };
-#pragma unroll 1
-  for (int i = 0; i < C::kStages - 1; ++i) copy_tile();
 
   // ---- the warp's products -----------------------------------------------------------------------
   const int r0 = lane / 4, c0 = (lane % 4) * 2;
@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
   float2* const stat = reinterpret_cast<float2*>(smem + C::kStat);
   int* const from = reinterpret_cast<int*>(smem + C::kFrom);   // where each warp's output to be joined lies
   int* const flag = from + kWarps;
+  float2* const joined = reinterpret_cast<float2*>(smem + C::kParted);
   int take = 0;                                         // ring slot of the next tile
   int turn = 0;                                         // the warp whose turn the segment's first tile is
   bool first_seg = true;
@@ -423,7 +424,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
     }
     full = __reduce_min_sync(0xffffffffu, full);        // keys that every row sees
   };
-  read_rows();
+  read_rows();                                          // before the copies fill the way to memory
+#pragma unroll 1
+  for (int i = 0; i < C::kStages - 1; ++i) copy_tile();
 
 #pragma unroll 1
   while (s0 + kSegment < end) {
@@ -602,7 +605,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
       const int ca = share.owner(seg_s0 + kSegment), cb = share.owner(seg_s0 + kSegment + seg_tiles - 1);
       // the first CTA may have begun inside an earlier segment: this one is then its second part
       const int part0 = 2 * ca + (share.begin(ca) >= seg_s0 ? 0 : 1);
-      __threadfence();                                  // the parts, before the word that announces them
       __syncthreads();
       if (warp == 0) {
         const bool last = all_arrived(a.arrivals, 2 * (int)blockIdx.x + (was_first ? 0 : 1), part0, ca, cb, a.call);
@@ -610,43 +612,69 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
       }
       __syncthreads();
       if (*flag != 0) {
-        __threadfence();
-        for (int x = threadIdx.x; x < n_rows * kQuads; x += kThreads) {
-          const int r = x / kQuads, c = x % kQuads * 4;
-          // eight parts at a time, all their reads in flight together; past the last, weight 0
-          auto part_of = [&](int i) { return (int64_t)(i <= ca ? part0 : 2 * min(i, cb)) * kRows + r; };
-          float mx = -INFINITY;
-          for (int i0 = ca; i0 <= cb; i0 += 16) {
-            float v[16];
+        for (int i = ca + threadIdx.x; i <= cb; i += kThreads) a.arrivals[i == ca ? part0 : 2 * i] = 0ull;
+        // Up to kJoin parts at a time: their statistics to shared memory, all in flight together, then
+        // their outputs, sixteen in flight, onto what the parts before came to.
+        auto part_of = [&](int i) { return (int64_t)(i == ca ? part0 : 2 * i) * kRows; };
+        constexpr int kItems = (kRows * kQuads + kThreads - 1) / kThreads;
+        float mx[kItems], sum[kItems];
+        float4 acc[kItems];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __ldcg(&a.ml_part[part_of(i0 + i)].x);
+        for (int y = 0; y < kItems; ++y) {
+          mx[y] = -INFINITY;
+          sum[y] = 0.f;
+          acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll 1
+        for (int i0 = ca; i0 <= cb; i0 += C::kJoin) {
+          const int np = min(C::kJoin, cb + 1 - i0);
+          // sixteen parts' outputs of item x; past the last part its own again, with weight 0
+          auto outputs = [&](int x, int i, float4 (&v)[16]) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, v[i]);
-          }
-          float sum = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (mx != -INFINITY) {
-            for (int i0 = ca; i0 <= cb; i0 += 8) {
-              float2 ml[8];
-              float4 v[8];
+            for (int k = 0; k < 16; ++k)
+              v[k] = __ldcg(reinterpret_cast<const float4*>(a.o_part + (part_of(i0 + min(i + k, np - 1)) + x / kQuads) * D +
+                                                            x % kQuads * 4));
+          };
+          float4 v[16];
+          if (threadIdx.x < n_rows * kQuads) outputs(threadIdx.x, 0, v);    // under way with the statistics
+          __syncthreads();
+          for (int x = threadIdx.x; x < np * kRows; x += kThreads)
+            joined[x] = __ldcg(&a.ml_part[part_of(i0 + x / kRows) + x % kRows]);
+          __syncthreads();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int64_t part = part_of(i0 + i);
-                ml[i] = __ldcg(&a.ml_part[part]);
-                v[i] = __ldcg(reinterpret_cast<const float4*>(a.o_part + part * D + c));
-              }
+          for (int y = 0; y < kItems; ++y) {
+            const int x = threadIdx.x + y * kThreads;
+            if (x >= n_rows * kQuads) break;
+            const int r = x / kQuads;
+            float m_new = mx[y];
+            for (int i = 0; i < np; ++i) m_new = fmaxf(m_new, joined[i * kRows + r].x);
+            if (m_new == -INFINITY) continue;           // no key of the row so far
+            const float keep = ptx::ex2(mx[y] - m_new);
+            mx[y] = m_new;
+            sum[y] *= keep;
+            acc[y].x *= keep;
+            acc[y].y *= keep;
+            acc[y].z *= keep;
+            acc[y].w *= keep;
+            for (int i = 0; i < np; i += 16) {
+              if (y > 0 || i > 0) outputs(x, i, v);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float f = i0 + i <= cb ? ptx::ex2(ml[i].x - mx) : 0.f;    // 0 too for a part without keys
-                sum = fmaf(f, ml[i].y, sum);
-                acc.x = fmaf(f, v[i].x, acc.x);
-                acc.y = fmaf(f, v[i].y, acc.y);
-                acc.z = fmaf(f, v[i].z, acc.z);
-                acc.w = fmaf(f, v[i].w, acc.w);
+              for (int k = 0; k < 16; ++k) {
+                const float2 ml = joined[min(i + k, np - 1) * kRows + r];
+                const float f = i + k < np ? ptx::ex2(ml.x - m_new) : 0.f;     // 0 too for a part without keys
+                sum[y] = fmaf(f, ml.y, sum[y]);
+                acc[y].x = fmaf(f, v[k].x, acc[y].x);
+                acc[y].y = fmaf(f, v[k].y, acc[y].y);
+                acc[y].z = fmaf(f, v[k].z, acc[y].z);
+                acc[y].w = fmaf(f, v[k].w, acc[y].w);
               }
             }
           }
-          write_row4<D, F16>(a, qrow + r, c, acc, sum, mx);
+        }
+#pragma unroll
+        for (int y = 0; y < kItems; ++y) {
+          const int x = threadIdx.x + y * kThreads;
+          if (x < n_rows * kQuads) write_row4<D, F16>(a, qrow + x / kQuads, x % kQuads * 4, acc[y], sum[y], mx[y]);
         }
       }
     }
