@@ -158,19 +158,22 @@ def _stream(stream) -> ctypes.c_void_p:
 def _check_qkv(q, k, v):
     """q: [B, H, N, d]; k, v: [B, Hkv, N, d] with Hkv dividing H (grouped-query attention when
     Hkv < H).  Returns (B, H, N, d, Hkv)."""
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor")
-        if t.dim() != 4:
-            raise ValueError(f"{name} must be [B, H, N, d]")
-    B, H, N, d = q.shape
-    Hkv = k.shape[1]
-    if k.shape != v.shape or k.shape[0] != B or k.shape[2:] != q.shape[2:] or H % Hkv != 0:
+    qshape, kshape, dtype = q.shape, k.shape, q.dtype
+    if not (q.is_cuda and k.is_cuda and v.is_cuda and q.is_contiguous() and k.is_contiguous()
+            and v.is_contiguous() and len(qshape) == len(kshape) == v.dim() == 4):
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous CUDA tensor")
+            if t.dim() != 4:
+                raise ValueError(f"{name} must be [B, H, N, d]")
+    B, H, N, d = qshape
+    Bk, Hkv, Nk, dk = kshape
+    if kshape != v.shape or Bk != B or Nk != N or dk != d or H % Hkv != 0:
         raise ValueError("k, v must be [B, Hkv, N, d] with Hkv dividing the query heads")
-    if not (q.dtype == k.dtype == v.dtype):
+    if not (dtype == k.dtype == v.dtype):
         raise ValueError("q, k, v must share a dtype")
-    if q.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {q.dtype}")
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
     return B, H, N, d, Hkv
 
 
@@ -209,7 +212,8 @@ def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool =
     dropout."""
     B, H, N, d, Hkv = _check_qkv(q, k, v)
     scale = 1.0 / d ** 0.5 if scale is None else float(scale)
-    block_mask, kv_lens = _masks(block_mask, kv_lens, B, N, q.device)
+    if block_mask is not None or kv_lens is not None:
+        block_mask, kv_lens = _masks(block_mask, kv_lens, B, N, q.device)
     o = torch.empty_like(q) if o is None else o
     lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device) if lse is None else lse
     if _scored(softcap, alibi_slopes, prefix_lens):
@@ -405,13 +409,16 @@ def backward(q, k, v, o, lse, do, *, causal: bool = False, scale: Optional[float
     fa_backward_fused, the single-pass atomic-dQ variant, when asked; fa_backward_scored,
     bit-reproducible too, with the score arguments of ``forward``)."""
     B, H, N, d, Hkv = _check_qkv(q, k, v)
-    for name, t in (("o", o), ("do", do)):
-        if t.shape != q.shape or t.dtype != q.dtype or not t.is_contiguous():
-            raise ValueError(f"{name} must match q")
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (B, H, N):
+    shape, dtype = q.shape, q.dtype
+    if o.shape != shape or o.dtype != dtype or not o.is_contiguous():
+        raise ValueError("o must match q")
+    if do.shape != shape or do.dtype != dtype or not do.is_contiguous():
+        raise ValueError("do must match q")
+    if lse.dtype != torch.float32 or lse.shape != (B, H, N):
         raise ValueError("lse must be fp32 [B, H, N]")
     scale = 1.0 / d ** 0.5 if scale is None else float(scale)
-    block_mask, kv_lens = _masks(block_mask, kv_lens, B, N, q.device)
+    if block_mask is not None or kv_lens is not None:
+        block_mask, kv_lens = _masks(block_mask, kv_lens, B, N, q.device)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv

@@ -465,10 +465,12 @@ fa_status backward_impl(const void* q, const void* k, const void* v, const void*
     if (fa::launch_backward_order(p, s) != cudaSuccess) return FA_ERR_CUDA;
     a.perm = p.perm;
   }
-  cudaError_t e = a.scored ? fa::launch_delta_sm103(a, dtype, s) : fa::launch_bwd_preprocess(a, dtype, s);
+  fa::BwdMaps maps;
+  if (two_pass && fa::make_bwd_maps(a, dtype, &maps) != cudaSuccess) return FA_ERR_CUDA;
+  cudaError_t e = a.scored ? fa::launch_delta_sm103(a, maps, dtype, s) : fa::launch_bwd_preprocess(a, dtype, s);
   if (e == cudaSuccess) {
     if (two_pass) {
-      e = fa::launch_bwd_split_sm103(a, dtype, s);
+      e = fa::launch_bwd_split_sm103(a, maps, dtype, s);
     } else {
       e = dtype == FA_FP32 ? fa::launch_bwd_simt(a, dtype, s) : fa::launch_bwd_sm103(a, dtype, s);
       if (e == cudaSuccess) e = fa::launch_bwd_dq_convert(a, dtype, s);

@@ -3,10 +3,10 @@
 
 namespace fa {
 
-cudaError_t launch_bwd_scored_bias(const BwdArgs& a, fa_dtype dt, cudaStream_t s) {
+cudaError_t launch_bwd_scored_bias(const BwdArgs& a, const BwdMaps& m, fa_dtype dt, cudaStream_t s) {
   if (dt == FA_FP16)
-    return a.d == 64 ? launch_bwd_split<64, true, false, kModBias>(a, s) : launch_bwd_split<128, true, false, kModBias>(a, s);
-  return a.d == 64 ? launch_bwd_split<64, false, false, kModBias>(a, s) : launch_bwd_split<128, false, false, kModBias>(a, s);
+    return a.d == 64 ? launch_bwd_split<64, true, false, kModBias>(a, m, s) : launch_bwd_split<128, true, false, kModBias>(a, m, s);
+  return a.d == 64 ? launch_bwd_split<64, false, false, kModBias>(a, m, s) : launch_bwd_split<128, false, false, kModBias>(a, m, s);
 }
 
 }  // namespace fa

@@ -3,10 +3,10 @@
 
 namespace fa {
 
-cudaError_t launch_bwd_scored_both(const BwdArgs& a, fa_dtype dt, cudaStream_t s) {
+cudaError_t launch_bwd_scored_both(const BwdArgs& a, const BwdMaps& m, fa_dtype dt, cudaStream_t s) {
   if (dt == FA_FP16)
-    return a.d == 64 ? launch_bwd_split<64, true, false, kModBoth>(a, s) : launch_bwd_split<128, true, false, kModBoth>(a, s);
-  return a.d == 64 ? launch_bwd_split<64, false, false, kModBoth>(a, s) : launch_bwd_split<128, false, false, kModBoth>(a, s);
+    return a.d == 64 ? launch_bwd_split<64, true, false, kModBoth>(a, m, s) : launch_bwd_split<128, true, false, kModBoth>(a, m, s);
+  return a.d == 64 ? launch_bwd_split<64, false, false, kModBoth>(a, m, s) : launch_bwd_split<128, false, false, kModBoth>(a, m, s);
 }
 
 }  // namespace fa

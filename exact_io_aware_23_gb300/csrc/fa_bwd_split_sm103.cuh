@@ -35,28 +35,11 @@ bwd_split_sm103_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   else dqp::run<D, F16, kDrop, kMod>(x - n_kv_units, tmQ, tmK, tmV, tmDO, a);
 }
 
-cudaError_t make_map(CUtensorMap* m, const void* base, int D, int N, int BH, bool f16) {
-  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)BH};
-  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)N * D * 2};
-  const cuuint32_t box[3] = {64, 128, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return encode_tensor_map(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                           3, base, dims, strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
 template <int D, bool F16, bool kDrop, int kMod>
-cudaError_t launch_bwd_split(const BwdArgs& a, cudaStream_t s) {
-  CUtensorMap mq, mk, mv, mdo;
+cudaError_t launch_bwd_split(const BwdArgs& a, const BwdMaps& m, cudaStream_t s) {
   const int BH = a.B * a.H;            // query-side work units per tile row (Q, dO, dQ)
   const int BHkv = a.B * a.Hkv;        // key/value-side work units per tile row (K, V, dK, dV)
-  // token axis and slice count of the tensor maps: per (b, h) slice, or packed per head
-  const bool packed = a.cu_seqlens != nullptr;
-  const int q_slices = packed ? a.H : BH, kv_slices = packed ? a.Hkv : BHkv;
   cudaError_t e;
-  if ((e = make_map(&mq, a.q, D, a.rows, q_slices, F16)) != cudaSuccess) return e;
-  if ((e = make_map(&mk, a.k, D, a.rows, kv_slices, F16)) != cudaSuccess) return e;
-  if ((e = make_map(&mv, a.v, D, a.rows, kv_slices, F16)) != cudaSuccess) return e;
-  if ((e = make_map(&mdo, a.dO, D, a.rows, q_slices, F16)) != cudaSuccess) return e;
   auto kern = bwd_split_sm103_kernel<D, F16, kDrop, kMod>;
   // each pass keeps its barriers 256 bytes below its live-tile bitmap (one bit per tile)
   const int bitmap = a.block_mask != nullptr ? ((a.n_tiles + 127) / 128) * 16 : 0;
@@ -67,7 +50,7 @@ cudaError_t launch_bwd_split(const BwdArgs& a, cudaStream_t s) {
   if ((e = prepare_launch(setup, kern, smem)) != cudaSuccess) return e;
   const int n_t = (a.N + 127) / 128;
   const int n_kv = n_t * BHkv, n_q = n_t * BH;
-  kern<<<dim3(n_kv + n_q), BwdLayout<D>::kThreads, smem, s>>>(mq, mk, mv, mdo, a, n_kv, n_q);
+  kern<<<dim3(n_kv + n_q), BwdLayout<D>::kThreads, smem, s>>>(m.q, m.k, m.v, m.dO, a, n_kv, n_q);
   return cudaGetLastError();
 }
 

@@ -291,49 +291,33 @@ delta_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
   if (warp == 9) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
-cudaError_t make_map(CUtensorMap* m, const void* base, int D, int N, int BH, bool f16) {
-  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)BH};
-  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)N * D * 2};
-  const cuuint32_t box[3] = {64, 128, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return encode_tensor_map(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims,
-                           strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
 template <int D, bool F16, int kMod>
-cudaError_t launch(const BwdArgs& a, cudaStream_t s) {
-  CUtensorMap mq, mk, mv, mdo;
-  const bool packed = a.cu_seqlens != nullptr;
-  const int q_slices = packed ? a.H : a.B * a.H, kv_slices = packed ? a.Hkv : a.B * a.Hkv;
+cudaError_t launch(const BwdArgs& a, const BwdMaps& m, cudaStream_t s) {
   cudaError_t e;
-  if ((e = make_map(&mq, a.q, D, a.rows, q_slices, F16)) != cudaSuccess) return e;
-  if ((e = make_map(&mk, a.k, D, a.rows, kv_slices, F16)) != cudaSuccess) return e;
-  if ((e = make_map(&mv, a.v, D, a.rows, kv_slices, F16)) != cudaSuccess) return e;
-  if ((e = make_map(&mdo, a.dO, D, a.rows, q_slices, F16)) != cudaSuccess) return e;
   auto kern = delta_kernel<D, F16, kMod>;
   static LaunchSetup setup;
   // The warp groups re-split the CTA's registers; that only completes if the launch holds them.
   int regs = 0;
   if ((e = prepare_launch(setup, kern, Cfg<D, F16>::kSmem, &regs)) != cudaSuccess) return e;
   if (regs * kThreads < 128 * 88 + 256 * 200) return cudaErrorInvalidConfiguration;
-  kern<<<dim3((a.N + 2 * BM - 1) / (2 * BM) * a.B * a.H), kThreads, Cfg<D, F16>::kSmem, s>>>(mq, mk, mv, mdo, a);
+  kern<<<dim3((a.N + 2 * BM - 1) / (2 * BM) * a.B * a.H), kThreads, Cfg<D, F16>::kSmem, s>>>(m.q, m.k, m.v, m.dO, a);
   return cudaGetLastError();
 }
 
 template <int kMod>
-cudaError_t dispatch(const BwdArgs& a, fa_dtype dt, cudaStream_t s) {
-  if (dt == FA_FP16) return a.d == 64 ? launch<64, true, kMod>(a, s) : launch<128, true, kMod>(a, s);
-  return a.d == 64 ? launch<64, false, kMod>(a, s) : launch<128, false, kMod>(a, s);
+cudaError_t dispatch(const BwdArgs& a, const BwdMaps& m, fa_dtype dt, cudaStream_t s) {
+  if (dt == FA_FP16) return a.d == 64 ? launch<64, true, kMod>(a, m, s) : launch<128, true, kMod>(a, m, s);
+  return a.d == 64 ? launch<64, false, kMod>(a, m, s) : launch<128, false, kMod>(a, m, s);
 }
 
 }  // namespace
 
-cudaError_t launch_delta_sm103(const BwdArgs& a, fa_dtype dt, cudaStream_t s) {
+cudaError_t launch_delta_sm103(const BwdArgs& a, const BwdMaps& m, fa_dtype dt, cudaStream_t s) {
   switch (mod_of(a.score)) {
-    case kModCap: return dispatch<kModCap>(a, dt, s);
-    case kModBias: return dispatch<kModBias>(a, dt, s);
-    case kModBoth: return dispatch<kModBoth>(a, dt, s);
-    default: return dispatch<kModPrefix>(a, dt, s);
+    case kModCap: return dispatch<kModCap>(a, m, dt, s);
+    case kModBias: return dispatch<kModBias>(a, m, dt, s);
+    case kModBoth: return dispatch<kModBoth>(a, m, dt, s);
+    default: return dispatch<kModPrefix>(a, m, dt, s);
   }
 }
 

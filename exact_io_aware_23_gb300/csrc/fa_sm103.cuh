@@ -22,20 +22,27 @@ cudaError_t launch_fwd_bn64_sm103(const FwdArgs& a, fa_dtype dt, cudaStream_t s)
 // preprocess and the dQ conversion kernels.
 cudaError_t launch_bwd_sm103(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
 
+// The tensor maps of one backward call: Q, K, V, dO in boxes of 64 columns and 128 rows.  Each costs
+// the host about a microsecond to encode, so the calls' kernels share them.
+struct BwdMaps {
+  CUtensorMap q, k, v, dO;
+};
+cudaError_t make_bwd_maps(const BwdArgs& a, fa_dtype dt, BwdMaps* m);
+
 // bf16 / fp16 deterministic backward, both tensor-core passes in one launch (tcgen05 + TMA),
 // d in {64, 128}: key-stationary CTAs write dK and dV, query-stationary CTAs write dQ; no result
 // is added from several CTAs.
-cudaError_t launch_bwd_split_sm103(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_bwd_split_sm103(const BwdArgs& a, const BwdMaps& m, fa_dtype dt, cudaStream_t s);
 
 // ... with score modifications, by kind (fa_score.cuh)
-cudaError_t launch_bwd_scored_cap(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
-cudaError_t launch_bwd_scored_bias(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
-cudaError_t launch_bwd_scored_both(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
-cudaError_t launch_bwd_scored_prefix(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_bwd_scored_cap(const BwdArgs& a, const BwdMaps& m, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_bwd_scored_bias(const BwdArgs& a, const BwdMaps& m, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_bwd_scored_both(const BwdArgs& a, const BwdMaps& m, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_bwd_scored_prefix(const BwdArgs& a, const BwdMaps& m, fa_dtype dt, cudaStream_t s);
 
 // D = rowsum(P * dP) of the scored backward (tcgen05 + TMA), d in {64, 128}; takes the place of the
 // preprocess kernel there.
-cudaError_t launch_delta_sm103(const BwdArgs& a, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_delta_sm103(const BwdArgs& a, const BwdMaps& m, fa_dtype dt, cudaStream_t s);
 
 // Compute layout of the two-pass backward's CTAs (both passes, one launch): kWG compute
 // warpgroups, each over 128 / kWG columns of a 128 x 128 tile, then the producer warp and the
