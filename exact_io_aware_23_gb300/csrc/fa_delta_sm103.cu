@@ -233,14 +233,14 @@ delta_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         }
         const int lo = c0 - (r0 + BM - 1), hi = lo + BM + BN - 2;              // of j - i in the tile
         const Bias bi = make_bias(slope, c0 - i, lo, a.causal && prefix == 0 ? min(hi, 0) : hi);
-        with_score<kMod>(p, a.score, bi, [&](auto cap, auto bias) {
+        with_score<kMod>(p, a.score, F16 ? a.score.poly_limit : a.score.low_limit, bi, [&](auto cap, auto bias) {
           constexpr int kCap = decltype(cap)::value, kBias = decltype(bias)::value;
           const float first = kBias == kBiasLinear ? nl + bi.base : nl;
           const float2 first2 = make_float2(first, first);
 #pragma unroll
           for (int col = 0; col < BN; col += 2) {
             float2 x = make_float2(p[col], p[col + 1]);
-            if constexpr (kCap != kCapNone) x = tanh_of<kCap>(x, a.score);
+            if constexpr (kCap != kCapNone) x = tanh_of<kCap, F16>(x, a.score);
             x = ptx::fma2(x, m2, first2);
             if constexpr (kBias != kBiasNone) {
               x.x = biased<kBias>(x.x, bi, col);

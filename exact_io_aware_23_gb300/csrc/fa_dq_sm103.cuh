@@ -390,14 +390,14 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
           const Bias bi = make_bias(slope, k0 - q, lo, a.causal && g.prefix == 0 ? min(hi, 0) : hi);
           const float2 m2 = (kMod & kModCap) == 0 ? c2 : make_float2(a.score.cap_log2, a.score.cap_log2);
           const int seen = !g.causal ? g.kv_lim : min(g.kv_lim, max(q + 1, g.prefix));   // keys of the row
-          with_score<kMod>(p, a.score, bi, [&](auto cap, auto bias) {
+          with_score<kMod>(p, a.score, F16 ? a.score.poly_limit : a.score.low_limit, bi, [&](auto cap, auto bias) {
             constexpr int kCap = decltype(cap)::value, kBias = decltype(bias)::value;
             const float first = kBias == kBiasLinear ? nl + bi.base : nl;
             const float2 first2 = make_float2(first, first);
 #pragma unroll
             for (int col = 0; col < kCols; col += 2) {
               float2 t = make_float2(p[col], p[col + 1]);
-              if constexpr (kCap != kCapNone) t = tanh_of<kCap>(t, a.score);
+              if constexpr (kCap != kCapNone) t = tanh_of<kCap, F16>(t, a.score);
               float2 x = ptx::fma2(t, m2, first2);
               if constexpr (kBias != kBiasNone) {
                 x.x = biased<kBias>(x.x, bi, col);

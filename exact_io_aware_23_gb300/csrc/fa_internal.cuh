@@ -38,6 +38,9 @@ struct ScoreArgs {
   // tanh(scale s / softcap) = s * sum_i poly[i] s^(2i), and the same times cap_log2: each
   // coefficient twice, as packed arithmetic takes it
   uint64_t poly[4], capped[4];
+  // ... and of degree 2, for the bf16 backward
+  float low_limit;
+  uint64_t poly_low[3];
   const float* slopes;       // [H] or null
   const int32_t* prefix;     // [B] or null
 };

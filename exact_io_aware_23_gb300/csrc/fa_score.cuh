@@ -26,6 +26,10 @@ namespace fa {
 constexpr double kTanhPoly[4] = {0.999999901900935, -0.3333136245895285, 0.13270976759047418,
                                  -0.04755360362774448};
 constexpr double kTanhRange = 0.4;
+// The bf16 backward rebuilds P to round it, and dS, to 8 bits (2^-9 on average 1.7e-3): there degree 2
+// does, off by 6.3e-6 of a score, for scores up to 40, 2.5e-4 of P.  (fp16 keeps degree 3.)
+constexpr double kTanhLow[3] = {0.999993753137338, -0.33262579481744287, 0.12127786695232969};
+constexpr double kLowMost = 40.0;
 
 // Fills the kernels' form of the score arguments for raw products q . k; false when the cap is out
 // of the range fp32 can hold them in.
@@ -41,26 +45,31 @@ inline bool make_score(const fa_score_mod* m, float scale, ScoreArgs* out) {
     if (!isfinite(out->cap_log2) || !isfinite(out->c_exp) || !(out->cap_log2 > 0.f)) return false;
     out->poly_limit = (float)(kTanhRange / r);
     if (!isfinite(out->poly_limit)) out->poly_limit = 3.4e38f;
+    out->low_limit = (float)fmin((double)out->poly_limit, kLowMost / (double)scale);
+    auto twice = [&](double v) {
+      const float f = (float)v;
+      if (!isfinite(f)) out->poly_limit = out->low_limit = -1.f;    // a tiny cap: always the exponential
+      uint32_t bits;
+      memcpy(&bits, &f, 4);
+      return (uint64_t)bits << 32 | bits;
+    };
     double p = r;
     for (int i = 0; i < 4; ++i, p *= r * r) {
-      const float a = (float)(kTanhPoly[i] * p), b = (float)(kTanhPoly[i] * p * cap);
-      if (!isfinite(a) || !isfinite(b)) out->poly_limit = -1.f;   // a tiny cap: always the exponential
-      uint32_t bits;
-      memcpy(&bits, &a, 4);
-      out->poly[i] = (uint64_t)bits << 32 | bits;
-      memcpy(&bits, &b, 4);
-      out->capped[i] = (uint64_t)bits << 32 | bits;
+      out->poly[i] = twice(kTanhPoly[i] * p);
+      out->capped[i] = twice(kTanhPoly[i] * p * cap);
+      if (i < 3) out->poly_low[i] = twice(kTanhLow[i] * p);
     }
   }
   return true;
 }
 
 // P(z) for two values
-__device__ __forceinline__ float2 poly2(float2 z, const uint64_t (&c)[4]) {
-  uint64_t zz, p = c[3];
+template <int N>
+__device__ __forceinline__ float2 poly2(float2 z, const uint64_t (&c)[N]) {
+  uint64_t zz, p = c[N - 1];
   asm("mov.b64 %0, {%1, %2};" : "=l"(zz) : "f"(z.x), "f"(z.y));
 #pragma unroll
-  for (int i = 2; i >= 0; --i) asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(p), "l"(zz), "l"(c[i]));
+  for (int i = N - 2; i >= 0; --i) asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(p), "l"(zz), "l"(c[i]));
   float2 r;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
   return r;
@@ -100,10 +109,12 @@ __device__ __forceinline__ bool poly_fits(const float (&s)[N], float limit) {
 // The forms of one tile's scores: which tanh, and which bias.
 enum : int { kCapNone = 0, kCapPoly = 1, kCapExp = 2 };
 enum : int { kBiasNone = 0, kBiasLinear = 1, kBiasAbs = 2 };
-template <int kCap>
+// ... as the backward takes it, by the degree that its operands' type F16 asks for
+template <int kCap, bool F16>
 __device__ __forceinline__ float2 tanh_of(float2 s, const ScoreArgs& k) {
-  if constexpr (kCap == kCapPoly) return tanh_poly(s, k);
-  else return tanh_exp(s, k);
+  if constexpr (kCap == kCapExp) return tanh_exp(s, k);
+  else if constexpr (F16) return tanh_poly(s, k);
+  else return ptx::mul2(poly2(ptx::mul2(s, s), k.poly_low), s);
 }
 // The bias -slope |i - j| over one thread's row (or column) of a tile, whose distances run on by one:
 // at score e it is base + e * step where the tile lies on one side of the diagonal (or the other
@@ -135,7 +146,8 @@ __host__ inline int mod_of(const ScoreArgs& k) {
 // Calls body(cap form, bias form) as compile-time constants, the same ones in the warp.
 template <int V> struct Const { static constexpr int value = V; };
 template <int kMod, int N, typename Body>
-__device__ __forceinline__ void with_score(const float (&s)[N], const ScoreArgs& k, const Bias& b, Body&& body) {
+__device__ __forceinline__ void with_score(const float (&s)[N], const ScoreArgs& k, float limit, const Bias& b,
+                                           Body&& body) {
   auto with_cap = [&](auto cap) {
     if constexpr ((kMod & kModBias) == 0) {
       body(cap, Const<kBiasNone>());
@@ -147,7 +159,7 @@ __device__ __forceinline__ void with_score(const float (&s)[N], const ScoreArgs&
   if constexpr ((kMod & kModCap) == 0) {
     with_cap(Const<kCapNone>());
   } else {
-    if (poly_fits(s, k.poly_limit)) with_cap(Const<kCapPoly>());
+    if (poly_fits(s, limit)) with_cap(Const<kCapPoly>());
     else with_cap(Const<kCapExp>());
   }
 }
@@ -174,9 +186,9 @@ __device__ __forceinline__ void score_row(float (&s)[N], const ScoreArgs& k, flo
       s[e + 1] = x.y;
     }
   };
-  if (k.slopes == nullptr) with_score<kModCap>(s, k, b, body);
-  else if (k.cap_log2 == 0.f) with_score<kModBias>(s, k, b, body);
-  else with_score<kModBoth>(s, k, b, body);
+  if (k.slopes == nullptr) with_score<kModCap>(s, k, k.poly_limit, b, body);
+  else if (k.cap_log2 == 0.f) with_score<kModBias>(s, k, k.poly_limit, b, body);
+  else with_score<kModBoth>(s, k, k.poly_limit, b, body);
 }
 
 // Rows [r0, kRows) of an operand tile in shared memory (d / 64 halves of 128-byte rows; the swizzle

@@ -9,7 +9,8 @@ error of a score:
   e_ij  : d products added in fp32, in any order, (d + 4) v scale sum_c |q_c k_c|.  The cap by its
           polynomial, where no score of the head exceeds 0.4 of the cap, is off by 6 2^-24 of itself
           (its own 9.9e-8, Horner's steps, the scaled coefficients, the product with cap): 2^-21 |s|;
-          by the exponential, errors of 2^-22 in 1 / (1 + exp 2x) times 2 cap: 2^-20 cap in all.  The
+          by the exponential, errors of 2^-22 in 1 / (1 + exp 2x) times 2 cap: 2^-20 cap in all.
+          The bf16 backward's polynomial is off by 6.3e-6 of the score itself: 2^-17 |s| in all.  The
           bias 4 v slope |i - j| more, 4 v |s_ij| for the conversion to base 2.
   p     : relative error 2 (max_j e_ij + 2^-22) =: f_i  (numerator and normaliser)
   O     : u |O| + (u + f_i) sum_j p_j |v_j|
@@ -18,7 +19,7 @@ error of a score:
   dS_ij : = p (dP - D) c, c = the cap's derivative.  dP adds d products: (d + 2) v sum |dO_c V_c|;
           D = sum_j p dP takes that error and f_i of each term, and one v for each of its fp32
           additions in turn; c = 1 - tanh^2 is off by
-          2^-20 (twice the tanh's 2^-21, absolutely), and by 2 c e_ij / cap through its argument;
+          twice the tanh's error, absolutely, and by 2 c e_ij / cap through its argument;
           then one rounding u:
           (u + f_i + 2 e_ij / cap) |dS| + p |dP - D| 2^-20 + p c (the errors of dP and D)
   dQ,dK : u |.| + scale sum of the above times |K| or |Q|; products added in fp32 stay below
@@ -39,7 +40,7 @@ import torch
 V = 2.0 ** -24
 
 
-def scores(q, k, allowed, dist, scale, cap, slope):
+def scores(q, k, allowed, dist, scale, cap, slope, poly=2.0 ** -21):
     """(s, c, e): masked scores, the cap's derivative, the error bound of s."""
     x = q @ k.T * scale
     e = (q.shape[-1] + 4) * V * scale * (q.abs() @ k.abs().T)
@@ -48,7 +49,7 @@ def scores(q, k, allowed, dist, scale, cap, slope):
         t = torch.tanh(x / cap)
         fits = x.numel() == 0 or float(x.abs().max()) <= 0.4 * cap
         x, c = cap * t, 1.0 - t * t
-        e = e + (2.0 ** -21 * x.abs() if fits else 2.0 ** -20 * cap)
+        e = e + poly * x.abs() + (0.0 if fits else 2.0 ** -20 * cap)
     if slope != 0.0:
         x = x - slope * dist
         e = e + 4 * V * slope * dist
@@ -75,7 +76,9 @@ def head_forward(q, k, v, allowed, dist, scale, cap, slope, u, tiny=0.0):
 
 def head_backward(q, k, v, do, allowed, dist, scale, cap, slope, u, tiny=0.0):
     """dQ, dK, dV of one head and their bounds."""
-    s, c, e = scores(q, k, allowed, dist, scale, cap, slope)
+    # bf16 (u = 2^-8) or finer; the derivative 1 - tanh^2 takes twice the tanh's error
+    poly = 2.0 ** -17 if u > 2.0 ** -10 else 2.0 ** -21
+    s, c, e = scores(q, k, allowed, dist, scale, cap, slope, poly)
     p, _ = softmax(s)
     f = 2 * (e.amax(-1, keepdim=True) + 2.0 ** -22)
     d = q.shape[-1]
@@ -87,7 +90,7 @@ def head_backward(q, k, v, do, allowed, dist, scale, cap, slope, u, tiny=0.0):
     dp_err = dp_err + (p * ((f + 34 * V * max(1, s.shape[-1] // 128)) * dp.abs() + dp_err)).sum(-1, keepdim=True)
     ds_tol = (u + f + (2 * e / cap if cap > 0.0 else 0.0)) * ds.abs() + p * c * dp_err
     if cap > 0.0:
-        ds_tol = ds_tol + p * (dp - delta).abs() * 2.0 ** -20
+        ds_tol = ds_tol + p * (dp - delta).abs() * 2 * max(poly, 2.0 ** -21)
     dq, dk, dv = scale * ds @ k, scale * ds.T @ q, p.T @ do
     a = allowed.double()
     return (dq, dk, dv, u * dq.abs() + scale * ds_tol @ k.abs() + tiny * (1 + scale * a @ k.abs()),

@@ -47,3 +47,7 @@ def test_tanh_polynomial():
     fine = ref != 0
     assert float(((t - ref)[fine] / ref[fine]).abs().max()) < 9.9e-8
     assert math.isclose(c[0], 1.0, abs_tol=9.9e-8)
+    body = re.search(r"kTanhLow\[3\] = \{(.*?)\};", text, re.S).group(1)       # the bf16 backward's
+    c = [float(v) for v in body.split(",")]
+    t = x * sum(a * x ** (2 * i) for i, a in enumerate(c))
+    assert float(((t - ref)[fine] / ref[fine]).abs().max()) < 6.3e-6
