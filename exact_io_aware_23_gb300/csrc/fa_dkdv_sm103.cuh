@@ -479,19 +479,22 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
               // what dS takes: P times the cap's derivative 1 - tanh^2
               if constexpr (kCap != kCapNone)
                 w = ptx::mul2(v, ptx::fma2(make_float2(-t.x, -t.y), t, make_float2(1.f, 1.f)));
-              if (kind == kPartial) {
-                const bool seen = !g.causal || key < g.prefix;
-                const bool ok0 = key_ok && (seen || key <= q0 + col), ok1 = key_ok && (seen || key <= q0 + col + 1);
-                v.x = ok0 ? v.x : 0.f;
-                v.y = ok1 ? v.y : 0.f;
-                w.x = ok0 ? w.x : 0.f;
-                w.y = ok1 ? w.y : 0.f;
-              }
               pk[col / 2] = ptx::pack2<F16>(v.x, v.y);
               p[col] = w.x;
               p[col + 1] = w.y;
             }
           });
+          // the masks in a loop of their own, which only the tiles that have some run
+          if (kind == kPartial) {
+            const bool seen = !g.causal || key < g.prefix;
+#pragma unroll
+            for (int col = 0; col < kCols; col += 2) {
+              const bool ok0 = key_ok && (seen || key <= q0 + col), ok1 = key_ok && (seen || key <= q0 + col + 1);
+              p[col] = ok0 ? p[col] : 0.f;
+              p[col + 1] = ok1 ? p[col + 1] : 0.f;
+              pk[col / 2] &= (ok0 ? 0xffffu : 0u) | (ok1 ? 0xffff0000u : 0u);
+            }
+          }
           ptx::tmem_st(tX, pk);
           ptx::tmem_wait_st();
         } else {
@@ -559,15 +562,16 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
               dpv = ptx::mul2(dpv, make_float2(a.drop.scale, a.drop.scale));
             }
             const float2 dd = ptx::sub2(dpv, *reinterpret_cast<const float2*>(dl + col));
-            float2 ds = ptx::mul2(make_float2(p[col], p[col + 1]), dd);
-            if constexpr (kScore) {
-              if (kind == kPartial) {                // masked: 0 whatever the key's value holds
-                ds.x = p[col] == 0.f ? 0.f : ds.x;
-                ds.y = p[col + 1] == 0.f ? 0.f : ds.y;
-              }
-            }
+            const float2 ds = ptx::mul2(make_float2(p[col], p[col + 1]), dd);
             p[col] = ds.x;
             p[col + 1] = ds.y;
+          }
+        }
+        if constexpr (kScore) {
+          if (kind == kPartial) {                    // masked: 0 whatever the key's value holds
+            const bool seen = !g.causal || key < g.prefix;
+#pragma unroll
+            for (int col = 0; col < kCols; ++col) p[col] = key_ok && (seen || key <= q0 + col) ? p[col] : 0.f;
           }
         }
       }

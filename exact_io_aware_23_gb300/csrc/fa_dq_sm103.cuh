@@ -370,6 +370,8 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
       if (!ok) break;
       ptx::tc_fence_after();
       float p[kCols];
+      int seen = 0;                                  // scored variant: keys of the row
+      if constexpr (kScore) seen = !g.causal ? g.kv_lim : min(g.kv_lim, max(q + 1, g.prefix));
       {
         uint32_t raw[kNR][32];
 #pragma unroll
@@ -389,7 +391,6 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
           const int lo = j * BN - (g.q0 + BM - 1), hi = lo + BM + BN - 2;      // of j - i in the tile
           const Bias bi = make_bias(slope, k0 - q, lo, a.causal && g.prefix == 0 ? min(hi, 0) : hi);
           const float2 m2 = (kMod & kModCap) == 0 ? c2 : make_float2(a.score.cap_log2, a.score.cap_log2);
-          const int seen = !g.causal ? g.kv_lim : min(g.kv_lim, max(q + 1, g.prefix));   // keys of the row
           with_score<kMod>(p, a.score, F16 ? a.score.poly_limit : a.score.low_limit, bi, [&](auto cap, auto bias) {
             constexpr int kCap = decltype(cap)::value, kBias = decltype(bias)::value;
             const float first = kBias == kBiasLinear ? nl + bi.base : nl;
@@ -407,14 +408,15 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
               // P times the cap's derivative 1 - tanh^2
               if constexpr (kCap != kCapNone)
                 v = ptx::mul2(v, ptx::fma2(make_float2(-t.x, -t.y), t, make_float2(1.f, 1.f)));
-              if (kind == kPartial) {
-                v.x = k0 + col < seen ? v.x : 0.f;
-                v.y = k0 + col + 1 < seen ? v.y : 0.f;
-              }
               p[col] = v.x;
               p[col + 1] = v.y;
             }
           });
+          // the masks in a loop of their own, which only the tiles that have some run
+          if (kind == kPartial) {
+#pragma unroll
+            for (int col = 0; col < kCols; ++col) p[col] = k0 + col < seen ? p[col] : 0.f;
+          }
         } else {
 #pragma unroll
         for (int hc = 0; hc < kNR; ++hc) {
@@ -464,15 +466,15 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
               dpv = ptx::mul2(dpv, make_float2(a.drop.scale, a.drop.scale));
             }
             const float2 dpd = ptx::sub2(dpv, dd2);
-            float2 ds = ptx::mul2(make_float2(p[col], p[col + 1]), dpd);
-            if constexpr (kScore) {
-              if (kind == kPartial) {                // masked: 0 whatever the key's value holds
-                ds.x = p[col] == 0.f ? 0.f : ds.x;
-                ds.y = p[col + 1] == 0.f ? 0.f : ds.y;
-              }
-            }
+            const float2 ds = ptx::mul2(make_float2(p[col], p[col + 1]), dpd);
             p[col] = ds.x;
             p[col + 1] = ds.y;
+          }
+        }
+        if constexpr (kScore) {
+          if (kind == kPartial) {                    // masked: 0 whatever the key's value holds
+#pragma unroll
+            for (int col = 0; col < kCols; ++col) p[col] = k0 + col < seen ? p[col] : 0.f;
           }
         }
       }
