@@ -56,6 +56,7 @@ struct Bars {
   uint64_t s_full[2], s_free[2];
   uint64_t dp_full[2], dp_free[2];
   uint64_t done;
+  uint64_t tail;           // the last V tile, before its rows behind the keys are cleared
   uint32_t tmem_base;
 };
 static_assert(sizeof(Bars) <= 256, "");
@@ -96,6 +97,7 @@ delta_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
   int last = kv_lim;
   if (a.causal) last = min(last, max(min(q0 + 2 * BM, N), prefix));
   const int tiles = (last + BN - 1) / BN;
+  const bool has_tail = tiles * BN > kv_lim && (a.cu_seqlens != nullptr ? row0 + kv_lim < a.rows : kv_lim < a.N);
 
   if (threadIdx.x == 0) {
     ptx::mbar_init(ptx::smem_u32(&bars->q_full), 1);
@@ -110,6 +112,7 @@ delta_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
       ptx::mbar_init(ptx::smem_u32(&bars->dp_free[t]), 4);
     }
     ptx::mbar_init(ptx::smem_u32(&bars->done), 1);
+    ptx::mbar_init(ptx::smem_u32(&bars->tail), 1);
     ptx::fence_mbar_init();
   }
   if (warp == 9) {
@@ -125,6 +128,7 @@ delta_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     ptx::regs_dec<88>();
   if (warp == 8) {
     // ------------------------------- TMA producer -----------------------------------------------
+    int m = 0;                                     // tiles issued: K_0, V_0, K_1, ...
     if (lane == 0 && tiles > 0) {
       const uint32_t qb = ptx::smem_u32(&bars->q_full);
       ptx::mbar_arrive_expect_tx(qb, 4 * C::kTile);
@@ -133,18 +137,26 @@ delta_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
           ptx::tma_load_3d(sbase + C::kQ + t * C::kTile + hh * 128 * 128, &tmQ, qb, hh * 64, row0 + q0 + t * BM, qs);
           ptx::tma_load_3d(sbase + C::kDO + t * C::kTile + hh * 128 * 128, &tmDO, qb, hh * 64, row0 + q0 + t * BM, qs);
         }
-      int m = 0;                                   // tiles issued: K_0, V_0, K_1, ...
       for (; m < 2 * tiles; ++m) {
         const int slot = m % C::kSlots;
         if (!ptx::mbar_wait(ptx::smem_u32(&bars->empty[slot]), ((uint32_t)(m / C::kSlots) & 1u) ^ 1u, lim_ms, a.err)) break;
-        const uint32_t fb = ptx::smem_u32(&bars->full[slot]);
+        const uint32_t fb = ptx::smem_u32(has_tail && m == 2 * tiles - 1 ? &bars->tail : &bars->full[slot]);
         ptx::mbar_arrive_expect_tx(fb, C::kTile);
         for (int hh = 0; hh < D / 64; ++hh)
           ptx::tma_load_3d(sbase + C::kRing + slot * C::kTile + hh * 128 * 128, (m & 1) ? &tmV : &tmK, fb, hh * 64,
                            row0 + (m >> 1) * BN, ks);
       }
+    }
+    if (has_tail && __shfl_sync(0xffffffffu, m, 0) == 2 * tiles) {
+      // the values behind the keys meet probabilities of 0, and 0 * NaN is not 0: cleared first
+      const int slot = (2 * tiles - 1) % C::kSlots;
+      ptx::mbar_wait(ptx::smem_u32(&bars->tail), 0, lim_ms, a.err);
+      zero_rows<D>(smem + C::kRing + slot * C::kTile, kv_lim - (tiles - 1) * BN);
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->full[slot]));
+    }
+    if (lane == 0 && tiles > 0) {
       // drain: copies in flight must land before shared memory is released
-      ptx::mbar_wait(qb, 0, lim_ms, a.err);
+      ptx::mbar_wait(ptx::smem_u32(&bars->q_full), 0, lim_ms, a.err);
       for (int i = max(0, m - C::kSlots); i < m; ++i)
         ptx::mbar_wait(ptx::smem_u32(&bars->full[i % C::kSlots]), (uint32_t)(i / C::kSlots) & 1u, lim_ms, a.err);
     }
@@ -264,10 +276,6 @@ delta_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
           ptx::tmem_ld32(tP + q4 * 32, raw);
           ptx::tmem_wait_ld();
           ptx::reg_fence(raw);
-          if (kind == kPartial) {                    // a masked key's value may be NaN: 0 all the same
-#pragma unroll
-            for (int e = 0; e < 32; ++e) raw[e] = p[q4 * 32 + e] == 0.f ? 0u : raw[e];
-          }
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
             sum[(e >> 1) & 1] = ptx::fma2(make_float2(p[q4 * 32 + e], p[q4 * 32 + e + 1]),
