@@ -262,14 +262,17 @@ def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool =
 
 def _check_packed(q, k, v, cu_seqlens):
     """q: [H, total, d]; k, v: [Hkv, total, d]; cu_seqlens: int32 [n_seqs + 1] on q's device."""
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if not t.is_cuda or not t.is_contiguous() or t.dim() != 3:
-            raise ValueError(f"{name} must be a contiguous CUDA tensor [heads, total, d]")
-    H, T, d = q.shape
-    Hkv = k.shape[0]
-    if k.shape != v.shape or k.shape[1:] != q.shape[1:] or H % Hkv != 0:
+    qshape, kshape, dtype = q.shape, k.shape, q.dtype
+    if not (q.is_cuda and k.is_cuda and v.is_cuda and q.is_contiguous() and k.is_contiguous()
+            and v.is_contiguous() and len(qshape) == len(kshape) == v.dim() == 3):
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            if not t.is_cuda or not t.is_contiguous() or t.dim() != 3:
+                raise ValueError(f"{name} must be a contiguous CUDA tensor [heads, total, d]")
+    H, T, d = qshape
+    Hkv, Tk, dk = kshape
+    if kshape != v.shape or Tk != T or dk != d or H % Hkv != 0:
         raise ValueError("k, v must be [Hkv, total, d] with Hkv dividing the query heads")
-    if not (q.dtype == k.dtype == v.dtype) or q.dtype not in _DTYPES:
+    if not (dtype == k.dtype == v.dtype) or dtype not in _DTYPES:
         raise ValueError("q, k, v must share a supported dtype")
     if (cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1
             or cu_seqlens.device != q.device or not cu_seqlens.is_contiguous()):

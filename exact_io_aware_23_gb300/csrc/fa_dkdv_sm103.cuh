@@ -484,7 +484,9 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
               p[col + 1] = w.y;
             }
           });
-          // the masks in a loop of their own, which only the tiles that have some run
+          // The masks in a loop of their own, which only the tiles that have some run: among the
+          // products above they cost every tile (dK, dV and dQ of B1 H16 Hkv4 N8192 d128 causal,
+          // softcap 50: 895 us with them there, 699 so).
           if (kind == kPartial) {
             const bool seen = !g.causal || key < g.prefix;
 #pragma unroll

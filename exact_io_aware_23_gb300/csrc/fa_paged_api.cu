@@ -43,7 +43,7 @@ fa_status check_cache(const fa_paged_cache* c, int Hkv) {
   if (c == nullptr) return FA_ERR_INVALID_ARG;
   if (c->n_pages < 0 || c->max_pages < 0 || c->page_size <= 0) return FA_ERR_INVALID_ARG;
   if (c->page_size % 16 != 0 || c->page_size > fa::kMaxPageSize) return FA_ERR_UNSUPPORTED;
-  if (!c->k_cache || !c->v_cache || !c->block_table || !c->kv_lens) return FA_ERR_INVALID_ARG;
+  if (!c->k_cache || !c->v_cache || (!c->block_table && c->max_pages > 0) || !c->kv_lens) return FA_ERR_INVALID_ARG;
   if (!aligned(c->k_cache, 16) || !aligned(c->v_cache, 16) || !aligned(c->block_table, 4) || !aligned(c->kv_lens, 4))
     return FA_ERR_INVALID_ARG;
   if (c->token_stride % 8 != 0 || (c->n_pages > 1 && c->page_stride % 8 != 0) || (Hkv > 1 && c->head_stride % 8 != 0))
@@ -120,9 +120,9 @@ fa_status fa_append_paged(const fa_paged_cache* cache, const void* k, const int6
   if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
   st = check_rotation(inv_freq, rotary_dim, mscale, d);
   if (st != FA_OK) return st;
+  if (B == 0 || H == 0 || T == 0) return FA_OK;
   st = check_cache(cache, Hkv);
   if (st != FA_OK) return st;
-  if (B == 0 || H == 0 || T == 0) return FA_OK;
   if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_lens, 4)) return FA_ERR_INVALID_ARG;
   if (!strides_ok(k_strides, B, Hkv, T, 2) || !strides_ok(v_strides, B, Hkv, T, 2)) return FA_ERR_INVALID_ARG;
   if (q != nullptr && (!q_out || !aligned(q, 16) || !aligned(q_out, 16) || !strides_ok(q_strides, B, H, T, 2)))
@@ -162,9 +162,9 @@ fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, 
   }
   fa::ScoreArgs mods;
   if (!fa::make_score(score, scale, &mods)) return FA_ERR_UNSUPPORTED;
+  if (B == 0 || H == 0 || T == 0) return FA_OK;
   st = check_cache(cache, Hkv);
   if (st != FA_OK) return st;
-  if (B == 0 || H == 0 || T == 0) return FA_OK;
   if (!q || !o || !lse || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(q_lens, 4))
     return FA_ERR_INVALID_ARG;
   fa::PagedArgs a{};

@@ -254,6 +254,23 @@ def test_append_without_queries_and_in_place():
     assert torch.equal(q, q2)
 
 
+def test_nothing_to_do():
+    """Empty batches, no new tokens, tables without entries."""
+    kc, vc, table, g = _cache([16], 2, 16, 64, "bf16", 1)
+    q = torch.zeros((0, 4, 1, 64), dtype=torch.bfloat16, device="cuda")
+    o, lse = fa.forward_paged(q, kc, vc, table[:0], _i32([]))
+    assert o.shape == q.shape and lse.shape == (0, 4, 1)
+    assert fa.append_paged(q[:, :2], q[:, 2:], kc, vc, table[:0], _i32([]), q=q).shape == q.shape
+    q = torch.zeros((1, 4, 0, 64), dtype=torch.bfloat16, device="cuda")
+    assert fa.forward_paged(q, kc, vc, table, _i32([16]))[0].shape == q.shape
+    q = torch.ones((1, 4, 1, 64), dtype=torch.bfloat16, device="cuda")
+    o, lse = fa.forward_paged(q, kc, vc, table[:, :0], _i32([0]))
+    assert not bool(o.any()) and bool(torch.isinf(lse).all())
+    assert fa.check_device_status() == 0
+    fa.forward_paged(q, kc, vc, table[:, :0], _i32([1]))
+    assert fa.check_device_status() == fa.FA_ERR_INVALID_ARG
+
+
 def test_a_decoder_reads_what_it_wrote():
     """Prompt, then tokens one by one and drafted together: every step's attention over the cache
     equals attention over all keys so far."""
