@@ -4,21 +4,26 @@
 //
 // What bounds it: the cache's bytes.  Each key and value is read once for all G = H / Hkv query
 // heads (and T new tokens) of its group; the two products are 4 * G * T flops a value, far below
-// the tensor cores' share even with the rows padded to the 16 of one mma.
+// the tensor cores' share even with the rows padded to the 16 of one mma.  (So the warps feed
+// mma.sync from shared memory themselves; a 128-row tile of the fifth-generation cores would be
+// nearly all padding.)  Measured: B2 H32 Hkv8 d128 with 100K and 128K keys, 0.95 GB: 160 us, 6.4 TB/s,
+// 0.96 of the copy rate; 64 sequences of 1 to 8192 keys, 1.0 GB: 160 us; 16 sequences of up to 4000
+// keys at d = 64, five drafted tokens: 37 us, 4.1 TB/s (there the warps' own work shows).
 //
-// Work.  The cache of every (sequence, key head, block of 16 query rows) is cut into tiles of 16
-// keys, numbered through, and the CTAs take equal consecutive shares of the whole (their number is
-// fixed by the device, the shares by the lengths, which live on the device).  A share may end
-// inside a sequence: its statistics (m, l) and un-normalised output then go to the workspace, and
-// a second kernel joins them in the order of the tiles.  So one long sequence fills the GPU like a
-// hundred short ones, unequal lengths leave nobody idle, and every result has one fixed order of
-// additions.
+// Work.  The cache of every (sequence, key head, block of 16 query rows), a segment, is cut into tiles
+// of 16 or 32 keys, numbered through, and the CTAs take equal consecutive shares of the whole (their
+// number is fixed by the device, the shares by the lengths, which live on the device).  A share may
+// end inside a segment: its statistics (m, l) and un-normalised output then go to the workspace, and
+// the CTA that finishes a segment last joins its parts, in the order of the tiles.  So one long
+// sequence fills the GPU like a hundred short ones, unequal lengths leave nobody idle, and every
+// result has one fixed order of additions.
 //
 // Inside a CTA the four warps take the tiles in turn.  A warp copies its own tiles into its own
-// ring in shared memory (16-byte cp.async, several tiles ahead, running on into the next sequence)
-// and waits for nobody until the end of a (sequence, head); there the warps' statistics are joined
-// in shared memory.  A tile lies in one page (pages are multiples of 16 tokens); rows behind the
-// last key are filled with zeros, so that nothing a page holds beyond the sequence enters.
+// ring in shared memory (16-byte cp.async, several tiles ahead, running on into the next segment)
+// and waits for nobody until the end of a segment; there the warps' statistics are joined in shared
+// memory.  16 keys lie in one page (pages are multiples of 16 tokens); rows behind the last key are
+// filled with zeros, so that nothing a page holds beyond the sequence enters.  P is rounded to the
+// values' type for its product, like theirs an error of half a step; l, m, O stay in fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -35,14 +40,16 @@
 namespace fa {
 namespace {
 
-#ifndef PAGED_W
-#define PAGED_W 4
-#define PAGED_K64 32
-#define PAGED_K128 16
-#endif
-constexpr int kWarps = PAGED_W;
+// Four warps a CTA and two CTAs an SM: eight warps hide each other's latencies, and two segments' ends
+// (queries, join) overlap.  (B64 H32 Hkv8 d128, 1 to 8192 keys: 163 us, against 181 with eight warps in
+// one CTA; B256 with 1 to 200 keys: 65 against 98.  Four CTAs of two warps: about the same there, but
+// twice the parts to join of a long cache, 182 us against 164 for B2 of 128K keys.)
+constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRows = 16;                  // query rows of a block: one mma's
+// Query rows of a block: one mma's.  A group of more rows (T new tokens of H / Hkv heads) takes several
+// blocks, each reading the cache (through L2) again; blocks of two mma's rows read it half as often but
+// hold twice the output in registers and spill (B8 H64 Hkv8 T7 d128, 4096 keys: 95 us against 74).
+constexpr int kRows = 16;
 constexpr int kCtasPerSm = 8 / kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -50,12 +57,12 @@ constexpr float kRescaleLog2 = 8.0f;       // the running maximum is raised when
 
 template <int D>
 struct Cfg {
-  static constexpr int kKeys = D == 128 ? PAGED_K128 : PAGED_K64;   // keys of a tile
+  static constexpr int kKeys = D == 128 ? 16 : 32;            // keys of a tile: 8 KB with the values
   static constexpr int kParts = kKeys / 16;                   // 16-key parts of a tile, each in one page
   static constexpr int kRowBytes = D * 2;
   static constexpr int kHalf = kKeys * kRowBytes;             // a tile's keys (or values)
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = 192 * 1024 / kCtasPerSm / (kWarps * kStage);   // 192 KB of tiles a CTA
+  static constexpr int kStages = 192 * 1024 / kCtasPerSm / (kWarps * kStage);   // 192 KB of tiles an SM
   static constexpr int kRing = kStages * kStage;              // per warp
   static constexpr int kStat = kWarps * kRing;
   static constexpr int kFrom = kStat + kWarps * kRows * 8;

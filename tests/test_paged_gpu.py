@@ -81,7 +81,8 @@ def _run(lens, H, Hkv, T, page, d, dtype, cap=0.0, alibi=False, q_lens=None, sca
 @pytest.mark.parametrize("lens,H,Hkv,T,page", [
     ([1], 1, 1, 1, 16), ([0], 4, 2, 1, 16), ([17], 8, 8, 1, 16), ([0, 1, 15, 16, 17, 0, 33, 0], 8, 2, 1, 16),
     ([500, 3, 1290], 4, 1, 1, 48), ([129, 64, 128], 16, 1, 1, 64), ([20, 9], 24, 1, 1, 32),
-    ([5000], 4, 2, 1, 256), ([37, 700], 6, 2, 3, 32), ([4, 2, 0, 260], 8, 1, 5, 16), ([100], 40, 1, 2, 16)])
+    ([5000], 4, 2, 1, 256), ([37, 700], 6, 2, 3, 32), ([4, 2, 0, 260], 8, 1, 5, 16), ([100], 40, 1, 2, 16),
+    ([3000, 0, 17], 17, 1, 1, 32), ([33, 2, 900], 8, 1, 7, 16), ([4000], 32, 1, 1, 64)])
 def test_lengths_heads_and_pages(dtype, d, lens, H, Hkv, T, page):
     _run(lens, H, Hkv, T, page, d, dtype, seed=sum(lens) + H)
 
@@ -95,6 +96,7 @@ def test_scores(cap, alibi, scale):
 
 def test_ragged_new_tokens():
     _run([40, 3, 900, 0, 7], 4, 2, 6, 16, 64, "bf16", q_lens=[6, 2, 0, 6, 9], alibi=True, seed=5)
+    _run([40, 3, 900, 0, 7, 2100], 16, 2, 5, 16, 128, "bf16", q_lens=[5, 2, 0, 5, 9, 3], cap=20.0, alibi=True, seed=6)
 
 
 def test_many_sequences():
