@@ -575,11 +575,6 @@ def _rotated(inv_freq: Optional[torch.Tensor]) -> int:
     return 2 * inv_freq.numel()
 
 
-def _written(name: str, t: torch.Tensor) -> None:
-    if any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride())):
-        raise ValueError(f"{name} is written: its elements must not share memory")
-
-
 def _span(t: torch.Tensor) -> Tuple[int, int]:
     """The bytes a tensor lies in."""
     last = sum((n - 1) * st for n, st in zip(t.shape, t.stride())) if t.numel() else -1
@@ -658,7 +653,6 @@ def _rotary(fn, where, x, positions, inv_freq, interleaved, mscale, out, stream)
         _refuse_place(out=out)
         if out.shape != shape or out.dtype != dtype:
             raise ValueError("out must have x's shape and type")
-        _written("out", out)
         _apart("x", x, "out", out, True)
         ys = _strides("out", out if len(shape) == 4 else out.unsqueeze(0))
         s = _handle(stream, dev)
@@ -734,8 +728,6 @@ def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
         raise ValueError("v must have k's shape and type")
     B, Hkv, T, d = shape
     cache = _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, dtype)
-    if 0 in k_cache.stride():
-        _written("k_cache", k_cache)
     rot = _rotated(inv_freq)
     if q_lens is not None:
         _int32("q_lens", q_lens, (B,))
@@ -755,6 +747,8 @@ def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
             if q_out.shape != qshape or q_out.dtype != dtype or not q_out.is_contiguous():
                 raise ValueError("q_out must be contiguous, of q's shape and type")
             _apart("q", q, "q_out", q_out, True)
+            _apart("k", k, "q_out", q_out, False)
+            _apart("v", v, "q_out", q_out, False)
     elif q_out is not None:
         raise ValueError("q_out without q")
     if s is None:

@@ -244,9 +244,10 @@ __device__ __forceinline__ void write_row4(const PagedArgs& a, int64_t row, int 
 // B1 H32 Hkv8 with 32K keys).  Between its own store and its reads of the others each CTA has a
 // sequentially consistent fence, so the last of them sees all words set, or cleared by one that did;
 // should two see them, both join the parts, to the same bits.  Who joins clears the words, for a
-// captured call's next run under the same number (another that reads them cleared has nothing to do).  Whatever else a fresh workspace holds is not the
-// number: it has 64 bits, starts at another place in every process, and is not used twice in one.
-// So no launch is spent on clearing the words first.  (By cudaMemsetAsync: 3 us of a call's 40.)
+// captured call's next run under the same number (another that reads them cleared has nothing left
+// to do).  Whatever else a fresh workspace holds is not the number: it has 64 bits, starts at another
+// place in every process, and is not used twice in one.  So no launch is spent on clearing the words
+// first.  (By cudaMemsetAsync: 3 us of a call's 40.)
 __device__ __forceinline__ bool all_arrived(unsigned long long* words, int mine, int part0, int ca, int cb,
                                             unsigned long long call) {
   const int lane = threadIdx.x % 32;

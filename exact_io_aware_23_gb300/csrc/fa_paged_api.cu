@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "fa_paged.cuh"
 #include "fa_score.cuh"
 #include "fa_sm103.cuh"
@@ -28,6 +30,20 @@ bool strides_ok(const int64_t* s, int B, int H, int N, int size) {
   if (s == nullptr) return false;
   const int64_t unit = 16 / size;
   return (B <= 1 || s[0] % unit == 0) && (H <= 1 || s[1] % unit == 0) && (N <= 1 || s[2] % unit == 0);
+}
+
+// Whether no two elements of a written tensor share memory: taken by growing stride, every axis steps
+// over all that the ones before it span.
+bool apart(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int d) {
+  struct Axis { int64_t n, s; } x[3] = {{n0, s0}, {n1, s1}, {n2, s2}};
+  std::sort(x, x + 3, [](const Axis& a, const Axis& b) { return a.s < b.s; });
+  int64_t span = d;
+  for (const Axis& a : x) {
+    if (a.n <= 1) continue;
+    if (a.s < span) return false;
+    span += (a.n - 1) * a.s;
+  }
+  return true;
 }
 
 fa::Strides strides(const int64_t* s) { return fa::Strides{s[0], s[1], s[2]}; }
@@ -80,6 +96,7 @@ fa_status rotary_impl(const void* x, const int64_t* xs, void* y, const int64_t* 
   const int size = dtype == FA_FP32 ? 4 : 2;
   if (!x || !y || !positions || !aligned(x, 16) || !aligned(y, 16) || !aligned(positions, 4)) return FA_ERR_INVALID_ARG;
   if (!strides_ok(xs, B, H, N, size) || !strides_ok(ys, B, H, N, size) || position_stride < 0) return FA_ERR_INVALID_ARG;
+  if (!apart(B, ys[0], H, ys[1], N, ys[2], d)) return FA_ERR_INVALID_ARG;
   fa::RotaryArgs a{};
   a.x = x;
   a.y = y;
@@ -123,6 +140,10 @@ fa_status fa_append_paged(const fa_paged_cache* cache, const void* k, const int6
   if (B == 0 || H == 0 || T == 0) return FA_OK;
   st = check_cache(cache, Hkv);
   if (st != FA_OK) return st;
+  // the pages are written
+  if (cache->k_cache == cache->v_cache || !apart(cache->n_pages, cache->page_stride, Hkv, cache->head_stride,
+                                                 cache->page_size, cache->token_stride, d))
+    return FA_ERR_INVALID_ARG;
   if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_lens, 4)) return FA_ERR_INVALID_ARG;
   if (!strides_ok(k_strides, B, Hkv, T, 2) || !strides_ok(v_strides, B, Hkv, T, 2)) return FA_ERR_INVALID_ARG;
   if (q != nullptr && (!q_out || !aligned(q, 16) || !aligned(q_out, 16) || !strides_ok(q_strides, B, H, T, 2)))
@@ -165,7 +186,7 @@ fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, 
   if (B == 0 || H == 0 || T == 0) return FA_OK;
   st = check_cache(cache, Hkv);
   if (st != FA_OK) return st;
-  if (!q || !o || !lse || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(q_lens, 4))
+  if (!q || !o || !lse || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(q_lens, 4))
     return FA_ERR_INVALID_ARG;
   fa::PagedArgs a{};
   a.cache = cache_args(cache);

@@ -21,6 +21,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "fa_paged.cuh"
 #include "fa_sm103.cuh"
 #include "ptx_sm103.cuh"
@@ -281,8 +283,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
 // (Cache write of 4 ragged prompts of 4096 tokens, 48 heads: 63 us; with two or four per SM 70, with 32
 // per SM 84.)
 int heads_per_block(int64_t token_blocks, int heads, int sms) {
+  const int least = (heads + 65534) / 65535;          // a grid's second axis
   int per = heads;
-  while (per > 1 && token_blocks * ((heads + per - 1) / per) < 8 * sms) per = (per + 1) / 2;
+  while (per > least && token_blocks * ((heads + per - 1) / per) < 8 * sms) per = std::max(least, (per + 1) / 2);
   return per;
 }
 

@@ -396,10 +396,11 @@ fa_status fa_backward_varlen_scored(const void* q, const void* k, const void* v,
  * Pairs are (2p, 2p + 1) when `interleaved`, else (p, p + rotary_dim / 2).  The other values are
  * copied.  fa_rotary_backward is its gradient: the rotation by -w, times mscale.  Angles keep
  * their accuracy at any int32 position (64-bit fixed-point turns).
- *   x, y            : [B, H, N, d], d in {64, 128}, the d values of a head adjacent; strides of
- *                     the other axes in elements {batch, head, token}, multiples of 16 bytes; base
- *                     addresses 16-byte aligned.  y may be x (with the same strides); otherwise
- *                     they must not overlap.
+ *   x, y            : [B, H, N, d], d in {64, 128}, B * H * N < 2^31, the d values of a head
+ *                     adjacent; strides of the other axes in elements {batch, head, token},
+ *                     multiples of 16 bytes; base addresses 16-byte aligned.  y may be x (with
+ *                     the same strides); otherwise they must not overlap, nor y's elements one
+ *                     another.
  *   positions       : device int32 [N] (position_stride 0) or one list of N per batch,
  *                     position_stride elements apart
  *   inv_freq        : device fp64 [rotary_dim / 2], radians per position (finite, below 2^52)
@@ -445,6 +446,7 @@ typedef struct {
  * and their rows of q_out are zero.
  *   k, v   : [B, Hkv, T, d], q (nullable): [B, H, T, d], strided as in fa_rotary
  *   q_out  : [B, H, T, d] contiguous; may be q when q is contiguous
+ *   the cache's keys and values must not share memory, and no two slots either
  * bf16 or fp16.  Hkv divides H.  The lengths and the table live on the device and are checked
  * there: a length beyond max_pages * page_size, or an entry outside [0, n_pages), is not followed
  * and fa_check_device_status then returns FA_ERR_INVALID_ARG.

@@ -35,6 +35,8 @@ def test_rotary_argument_checks(fn):
     assert rotary(fn, ps=-1) == INVALID
     assert rotary(fn, xs=S3(1 << 20, 1 << 13, 68)) == INVALID          # rows off the 16-byte grid
     assert rotary(fn, ys=S3(1 << 20, 4, 64)) == INVALID
+    assert rotary(fn, ys=S3(0, 32, 64)) == INVALID        # heads that overlap
+    assert rotary(fn, B=2, ys=S3(0, 1 << 13, 64)) == INVALID
     for empty in (dict(B=0), dict(H=0), dict(N=0)):
         assert rotary(fn, x=None, pos=None, **empty) == OK
 
@@ -61,7 +63,11 @@ def test_append_argument_checks():
     for kw, status in BAD_CACHES:
         assert append(cache(**kw)) == status, kw
     assert append(dtype=1) == UNSUPPORTED                 # the cache is 16 bits
+    assert append() == INVALID                            # keys and values in one place
+    assert append(cache(v_cache=P + 4096, page_stride=0)) == INVALID
+    assert append(cache(v_cache=P + 4096, token_stride=32)) == INVALID
     assert append(Hkv=3) == UNSUPPORTED
+    assert append(B=0, c=cache(kv_lens=None)) == OK
     assert append(Hkv=0) == INVALID
     assert append(d=80) == UNSUPPORTED
     assert append(rot=40) == UNSUPPORTED

@@ -370,8 +370,12 @@ def test_refusals():
         fa.forward_paged(q, kc[:, :, :8], vc[:, :, :8], table, n)          # pages of 8 tokens
     with pytest.raises(ValueError, match="q_out"):
         fa.append_paged(q[:, :2], q[:, 2:], kc, vc, table, n, q_out=q)
-    with pytest.raises(ValueError, match="share memory"):
+    with pytest.raises(ValueError, match="overlap"):
+        fa.append_paged(q[:, :2].contiguous(), q[:, 2:], kc, vc, table, n, q=q.clone(), q_out=q)
+    with pytest.raises(fa.FaError, match="INVALID_ARG"):                   # pages that share memory
         fa.append_paged(q[:, :2], q[:, 2:], kc[:1].expand(5, 2, 16, 64), vc[:1].expand(5, 2, 16, 64), table, n)
+    with pytest.raises(fa.FaError, match="INVALID_ARG"):                   # keys and values in one place
+        fa.append_paged(q[:, :2], q[:, 2:], kc, kc, table, n)
     with pytest.raises(fa.FaError, match="UNSUPPORTED"):
         fa.append_paged(q[:, :2], q[:, 2:], kc, vc, table, n,
                         inv_freq=torch.ones(40, dtype=torch.float64, device="cuda"))

@@ -157,8 +157,9 @@ def test_refusals():
     with pytest.raises(ValueError, match="overlap"):
         buf = _x(1, 2, 9, 64, "bf16")
         fa.rotary(buf[:, :, :8], pos, inv_freq, out=buf[:, :, 1:])
-    with pytest.raises(ValueError, match="share memory"):
-        fa.rotary(x, pos, inv_freq, out=x[:, :1].expand(1, 2, 8, 64))
+    for shared in (x[:, :1].clone().expand(1, 2, 8, 64), torch.zeros_like(x).as_strided((1, 2, 8, 64), (1024, 512, 32, 1))):
+        with pytest.raises(fa.FaError, match="INVALID_ARG"):          # written elements that share memory
+            fa.rotary(x, pos, inv_freq, out=shared)
     with pytest.raises(ValueError, match="dtype"):
         fa.rotary(x.double(), pos, inv_freq)
     with pytest.raises(fa.FaError, match="UNSUPPORTED"):
