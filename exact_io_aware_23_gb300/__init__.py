@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -140,6 +141,10 @@ def _load() -> ctypes.CDLL:
     L.fa_forward_paged_workspace_size.restype = sz
     L.fa_forward_paged.argtypes = [vp, cp, vp, vp, i, i, i, i, i, f, vp, mp, i, vp, sz, vp]
     L.fa_forward_paged.restype = i
+    for packed in (L.fa_forward_scored_packed, L.fa_backward_scored_packed, L.fa_rotary_packed,
+                   L.fa_rotary_backward_packed, L.fa_append_paged_packed, L.fa_forward_paged_packed):
+        packed.argtypes = [ctypes.c_char_p]
+        packed.restype = i
     return L
 
 
@@ -186,7 +191,7 @@ def _masks(block_mask, kv_lens, B, N, device):
     if kv_lens is not None:
         if kv_lens.dtype != torch.int32 or tuple(kv_lens.shape) != (B,):
             raise ValueError(f"kv_lens must be int32 [{B}]")
-        kv_lens = kv_lens.to(device).contiguous()
+        kv_lens = (kv_lens if kv_lens.device == device else kv_lens.to(device)).contiguous()
     return block_mask, kv_lens
 
 
@@ -219,12 +224,11 @@ def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool =
     if _scored(softcap, alibi_slopes, prefix_lens):
         if block_mask is not None or dropout_p > 0.0:
             raise ValueError("score modifications take no block mask and no dropout")
-        dev = _current_device(q)
-        mod = _score_mod(dev, q, softcap, alibi_slopes, prefix_lens, H, B)
-        st = lib.fa_forward_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H,
-                                   Hkv, N, d, scale, 1 if causal else 0, _DTYPES[q.dtype],
-                                   None if kv_lens is None else kv_lens.data_ptr(), ctypes.byref(mod),
-                                   _handle(stream, dev, o, lse))
+        dev, slopes, prefix = _score_args(q, k, v, None, None, None, alibi_slopes, prefix_lens, H, B)
+        st = lib.fa_forward_scored_packed(_SCORED.pack(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), 0, 0, 0, 0,
+            0 if kv_lens is None else kv_lens.data_ptr(), 0, slopes, prefix, 0, 0, _handle(stream, dev, o, lse),
+            B, H, Hkv, N, 0, d, 1 if causal else 0, _DTYPES[q.dtype], scale, softcap))
         if st != FA_OK:
             raise FaError(st, "fa_forward_scored")
         return o, lse
@@ -293,12 +297,11 @@ def forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, *, causal: bool = False
     o = torch.empty_like(q)
     lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
     if _scored(softcap, alibi_slopes, prefix_lens):
-        dev = _current_device(q)
-        mod = _score_mod(dev, q, softcap, alibi_slopes, prefix_lens, H, S)
-        st = lib.fa_forward_varlen_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                          cu_seqlens.data_ptr(), S, max_seqlen, T, H, Hkv, d, scale,
-                                          1 if causal else 0, _DTYPES[q.dtype], ctypes.byref(mod),
-                                          _handle(stream, dev, o, lse))
+        dev, slopes, prefix = _score_args(q, k, v, None, None, None, alibi_slopes, prefix_lens, H, S)
+        st = lib.fa_forward_scored_packed(_SCORED.pack(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), 0, 0, 0, 0, 0,
+            cu_seqlens.data_ptr(), slopes, prefix, 0, 0, _handle(stream, dev, o, lse),
+            S, H, Hkv, int(max_seqlen), T, d, 1 if causal else 0, _DTYPES[q.dtype], scale, softcap))
         if st != FA_OK:
             raise FaError(st, "fa_forward_varlen_scored")
         return o, lse
@@ -327,14 +330,12 @@ def backward_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen: int, *, causal:
     need = backward_deterministic_workspace_size(1, H, T)
     workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     if _scored(softcap, alibi_slopes, prefix_lens):
-        dev = _current_device(q)
-        mod = _score_mod(dev, q, softcap, alibi_slopes, prefix_lens, H, S)
-        st = lib.fa_backward_varlen_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
-                                           lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                                           cu_seqlens.data_ptr(), S, max_seqlen, T, H, Hkv, d, scale,
-                                           1 if causal else 0, _DTYPES[q.dtype], ctypes.byref(mod),
-                                           workspace.data_ptr(), workspace.numel(),
-                                           _handle(stream, dev, dq, dk, dv, workspace))
+        dev, slopes, prefix = _score_args(q, k, v, o, lse, do, alibi_slopes, prefix_lens, H, S)
+        st = lib.fa_backward_scored_packed(_SCORED.pack(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
+            dk.data_ptr(), dv.data_ptr(), 0, cu_seqlens.data_ptr(), slopes, prefix, workspace.data_ptr(),
+            workspace.numel(), _handle(stream, dev, dq, dk, dv, workspace),
+            S, H, Hkv, int(max_seqlen), T, d, 1 if causal else 0, _DTYPES[q.dtype], scale, softcap))
         if st != FA_OK:
             raise FaError(st, "fa_backward_varlen_scored")
         return dq, dk, dv
@@ -435,14 +436,13 @@ def backward(q, k, v, o, lse, do, *, causal: bool = False, scale: Optional[float
     if _scored(softcap, alibi_slopes, prefix_lens):
         if block_mask is not None or dropout_p > 0.0 or fused:
             raise ValueError("score modifications take no block mask, no dropout and no fused backward")
-        dev = _current_device(q)
-        mod = _score_mod(dev, q, softcap, alibi_slopes, prefix_lens, H, B)
-        st = lib.fa_backward_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
-                                    lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Hkv, N, d,
-                                    scale, 1 if causal else 0, _DTYPES[q.dtype],
-                                    None if kv_lens is None else kv_lens.data_ptr(), ctypes.byref(mod),
-                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                    _handle(stream, dev, dq, dk, dv, workspace))
+        dev, slopes, prefix = _score_args(q, k, v, o, lse, do, alibi_slopes, prefix_lens, H, B)
+        st = lib.fa_backward_scored_packed(_SCORED.pack(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
+            dk.data_ptr(), dv.data_ptr(), 0 if kv_lens is None else kv_lens.data_ptr(), 0, slopes, prefix,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _handle(stream, dev, dq, dk, dv, workspace),
+            B, H, Hkv, N, 0, d, 1 if causal else 0, _DTYPES[q.dtype], scale, softcap))
         if st != FA_OK:
             raise FaError(st, "fa_backward_scored")
         return dq, dk, dv
@@ -518,10 +518,15 @@ def noalloc_max_workspace() -> int:
 # ---- rotary positions, the paged cache, score modifications ------------------------------------------
 #
 # These calls are made once per layer and token: their host time is most of a short call, so the
-# checks read each property of a tensor once, and names for a message are found only when one is
-# raised.
+# checks read each property of a tensor once, names for a message are found only when one is
+# raised, and the arguments cross as one packed structure (one token over a short cache: 15.3 us a
+# call, with an argument each 17.6; its write into the cache 12.7 and 16.9).
 
-_STRIDES = ctypes.c_int64 * 3
+_CACHE_FORMAT = "PPqqqiiPqiP"                                     # fa_paged_cache
+_SCORED = struct.Struct("14PNP8iff")                              # fa_scored_call
+_ROTARY = struct.Struct("PPPPP7q7if")                             # fa_rotary_call
+_APPEND = struct.Struct(_CACHE_FORMAT + "7P9q8if0q")              # fa_append_paged_call
+_PAGED = struct.Struct(_CACHE_FORMAT + "6PNP6iff")                # fa_forward_paged_call
 _16_BIT = (torch.bfloat16, torch.float16)
 
 
@@ -549,7 +554,8 @@ def _handle(stream, dev: int, *allocated) -> int:
     if stream is None or stream.cuda_stream == current:
         return current
     for t in allocated:
-        t.record_stream(stream)
+        if t is not None:
+            t.record_stream(stream)
     return stream.cuda_stream
 
 
@@ -558,12 +564,12 @@ def _int32(name: str, t: torch.Tensor, shape) -> None:
         raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
 
 
-def _strides(name: str, t: torch.Tensor) -> "ctypes.Array":
+def _strides(name: str, t: torch.Tensor) -> Tuple[int, int, int]:
     """Strides (batch, head, token) of a [B, heads, N, d] tensor whose last axis adjoins."""
     b, h, n, last = t.stride()
     if last != 1:
         raise ValueError(f"the values of a head must adjoin in {name}")
-    return _STRIDES(b, h, n)
+    return b, h, n
 
 
 def _rotated(inv_freq: Optional[torch.Tensor]) -> int:
@@ -647,7 +653,7 @@ def _rotary(fn, where, x, positions, inv_freq, interleaved, mscale, out, stream)
     _int32("positions", positions, (B, N) if per_batch else (N,))
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=x.device)
-        ys = _STRIDES(H * N * d, N * d, d)
+        ys = (H * N * d, N * d, d)
         s = _handle(stream, dev, out)
     else:
         _refuse_place(out=out)
@@ -656,8 +662,8 @@ def _rotary(fn, where, x, positions, inv_freq, interleaved, mscale, out, stream)
         _apart("x", x, "out", out, True)
         ys = _strides("out", out if len(shape) == 4 else out.unsqueeze(0))
         s = _handle(stream, dev)
-    st = fn(x.data_ptr(), xs, out.data_ptr(), ys, B, H, N, d, positions.data_ptr(), N if per_batch else 0,
-            inv_freq.data_ptr(), rot, 1 if interleaved else 0, mscale, code, s)
+    st = fn(_ROTARY.pack(x.data_ptr(), out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), s, *xs, *ys,
+                         N if per_batch else 0, B, H, N, d, rot, 1 if interleaved else 0, code, mscale))
     if st != FA_OK:
         raise FaError(st, where)
     return out
@@ -670,19 +676,19 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *, 
     projection's [B, N, H, d] seen as [B, H, N, d], say); positions: int32 [N] or [B, N]; inv_freq:
     float64, from ``rotary_frequencies``; out: a new contiguous tensor, or given (x itself for a
     rotation in place).  bf16, fp16 or fp32."""
-    return _rotary(lib.fa_rotary, "fa_rotary", x, positions, inv_freq, interleaved, mscale, out, stream)
+    return _rotary(lib.fa_rotary_packed, "fa_rotary", x, positions, inv_freq, interleaved, mscale, out, stream)
 
 
 def rotary_backward(dy: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *,
                     interleaved: bool = False, mscale: float = 1.0,
                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """fa_rotary_backward: the gradient of ``rotary``'s input, given that of its output."""
-    return _rotary(lib.fa_rotary_backward, "fa_rotary_backward", dy, positions, inv_freq, interleaved,
+    return _rotary(lib.fa_rotary_backward_packed, "fa_rotary_backward", dy, positions, inv_freq, interleaved,
                    mscale, out, stream)
 
 
-def _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, dtype) -> FaPagedCache:
-    """Checks a paged cache ([n_pages, Hkv, page_size, d], any strides) and says where it lies."""
+def _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, dtype) -> tuple:
+    """Checks a paged cache ([n_pages, Hkv, page_size, d], any strides) and gives fa_paged_cache's fields."""
     shape, strides = k_cache.shape, k_cache.stride()
     if len(shape) != 4 or shape[1] != Hkv or shape[3] != d or k_cache.dtype != dtype or v_cache.dtype != dtype:
         raise ValueError(f"k_cache and v_cache must be {dtype} [n_pages, {Hkv}, page_size, {d}]")
@@ -699,9 +705,8 @@ def _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, dtype) -> FaPagedC
         raise ValueError("the entries of a row must adjoin in block_table")
     if kv_lens.dtype != torch.int32 or kv_lens.shape != (B,) or not kv_lens.is_contiguous():
         raise ValueError(f"kv_lens must be a contiguous int32 [{B}] tensor")
-    return FaPagedCache(k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], shape[0],
-                        shape[2], block_table.data_ptr(), row if B > 1 and row > width else width, width,
-                        kv_lens.data_ptr())
+    return (k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], shape[0], shape[2],
+            block_table.data_ptr(), row if B > 1 and row > width else width, width, kv_lens.data_ptr())
 
 
 def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -731,7 +736,7 @@ def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     rot = _rotated(inv_freq)
     if q_lens is not None:
         _int32("q_lens", q_lens, (B,))
-    H, qs = Hkv, None
+    H, qs = Hkv, (0, 0, 0)
     s = None
     if q is not None:
         qshape = q.shape
@@ -753,12 +758,10 @@ def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
         raise ValueError("q_out without q")
     if s is None:
         s = _handle(stream, dev)
-    st = lib.fa_append_paged(ctypes.byref(cache), k.data_ptr(), _strides("k", k), v.data_ptr(), _strides("v", v),
-                             None if q is None else q.data_ptr(), _STRIDES() if qs is None else qs,
-                             None if q_out is None else q_out.data_ptr(), B, H, Hkv, T, d,
-                             None if q_lens is None else q_lens.data_ptr(),
-                             None if inv_freq is None else inv_freq.data_ptr(), rot,
-                             1 if interleaved else 0, mscale, _DTYPES[dtype], s)
+    st = lib.fa_append_paged_packed(_APPEND.pack(
+        *cache, k.data_ptr(), v.data_ptr(), 0 if q is None else q.data_ptr(), 0 if q_out is None else q_out.data_ptr(),
+        0 if q_lens is None else q_lens.data_ptr(), 0 if inv_freq is None else inv_freq.data_ptr(), s,
+        *_strides("k", k), *_strides("v", v), *qs, B, H, Hkv, T, d, rot, 1 if interleaved else 0, _DTYPES[dtype], mscale))
     if st != FA_OK:
         raise FaError(st, "fa_append_paged")
     return q_out
@@ -769,18 +772,28 @@ def forward_paged_workspace_size(B: int, H: int, Hkv: int, T: int, d: int, max_k
     return int(lib.fa_forward_paged_workspace_size(B, H, Hkv, T, d, max_keys))
 
 
-def _score_mod(dev, q, softcap, alibi_slopes, prefix_lens, H, n_seqs) -> FaScoreMod:
-    """Checks the score arguments; slopes fp32 [H], prefix lengths int32 [n_seqs]."""
-    if (dev < 0 or (alibi_slopes is not None and alibi_slopes.get_device() != dev)
-            or (prefix_lens is not None and prefix_lens.get_device() != dev)):
-        _refuse_place(q=q, alibi_slopes=alibi_slopes, prefix_lens=prefix_lens)
-    if alibi_slopes is not None and (alibi_slopes.dtype != torch.float32 or alibi_slopes.shape != (H,)
-                                     or not alibi_slopes.is_contiguous()):
+def _check_slopes(alibi_slopes, H) -> None:
+    if alibi_slopes.dtype != torch.float32 or alibi_slopes.shape != (H,) or not alibi_slopes.is_contiguous():
         raise ValueError(f"alibi_slopes must be a contiguous float32 [{H}] tensor")
+
+
+def _score_args(q, k, v, o, lse, do, alibi_slopes, prefix_lens, H, n_seqs) -> Tuple[int, int, int]:
+    """Checks the score arguments (slopes fp32 [H], prefix lengths int32 [n_seqs]) and where the
+    tensors are; the current device, and the two addresses (0: not given)."""
+    dev = _current_device(q)
+    if (dev < 0 or k.get_device() != dev or v.get_device() != dev
+            or (do is not None and not (o.get_device() == lse.get_device() == do.get_device() == dev))
+            or (alibi_slopes is not None and alibi_slopes.get_device() != dev)
+            or (prefix_lens is not None and prefix_lens.get_device() != dev)):
+        _refuse_place(q=q, k=k, v=v, o=o, lse=lse, do=do, alibi_slopes=alibi_slopes, prefix_lens=prefix_lens)
+    slopes = prefix = 0
+    if alibi_slopes is not None:
+        _check_slopes(alibi_slopes, H)
+        slopes = alibi_slopes.data_ptr()
     if prefix_lens is not None:
         _int32("prefix_lens", prefix_lens, (n_seqs,))
-    return FaScoreMod(softcap, None if alibi_slopes is None else alibi_slopes.data_ptr(),
-                      None if prefix_lens is None else prefix_lens.data_ptr())
+        prefix = prefix_lens.data_ptr()
+    return dev, slopes, prefix
 
 
 def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -797,8 +810,10 @@ def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     dev = _current_device(q)
     if (dev < 0 or k_cache.get_device() != dev or v_cache.get_device() != dev
             or block_table.get_device() != dev or kv_lens.get_device() != dev
-            or (q_lens is not None and q_lens.get_device() != dev)):
-        _refuse_place(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, kv_lens=kv_lens, q_lens=q_lens)
+            or (q_lens is not None and q_lens.get_device() != dev)
+            or (alibi_slopes is not None and alibi_slopes.get_device() != dev)):
+        _refuse_place(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, kv_lens=kv_lens, q_lens=q_lens,
+                      alibi_slopes=alibi_slopes)
     shape, dtype = q.shape, q.dtype
     if len(shape) != 4 or dtype not in _16_BIT or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 or fp16 [B, H, T, d] tensor")
@@ -809,37 +824,36 @@ def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     cache = _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, dtype)
     if q_lens is not None:
         _int32("q_lens", q_lens, (B,))
-    mod = _score_mod(dev, q, softcap, alibi_slopes, None, H, B)
+    if alibi_slopes is not None:
+        _check_slopes(alibi_slopes, H)
     device = q.device
-    mine = []
     if o is None:
-        o = torch.empty_like(q)
-        mine.append(o)
+        o = o_new = torch.empty_like(q)
     else:
+        o_new = None
         _refuse_place(o=o)
         if o.shape != shape or o.dtype != dtype or not o.is_contiguous():
             raise ValueError("o must be contiguous, of q's shape and type")
         _apart("q", q, "o", o, False)
     if lse is None:
-        lse = torch.empty((B, H, T), dtype=torch.float32, device=device)
-        mine.append(lse)
+        lse = lse_new = torch.empty((B, H, T), dtype=torch.float32, device=device)
     else:
+        lse_new = None
         _refuse_place(lse=lse)
         if lse.shape != (B, H, T) or lse.dtype != torch.float32 or not lse.is_contiguous():
             raise ValueError("lse must be contiguous float32 [B, H, T]")
+    ws_new = None
     if workspace is None:
-        need = lib.fa_forward_paged_workspace_size(B, H, Hkv, T, d, min(cache.max_pages * cache.page_size, 0x7fffffff))
+        need = lib.fa_forward_paged_workspace_size(B, H, Hkv, T, d, min(cache[6] * cache[9], 0x7fffffff))
         if need > 0:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=device)
-            mine.append(workspace)
+            workspace = ws_new = torch.empty((need,), dtype=torch.uint8, device=device)
     else:
         _refuse_place(workspace=workspace)
-    st = lib.fa_forward_paged(q.data_ptr(), ctypes.byref(cache), o.data_ptr(), lse.data_ptr(), B, H, Hkv, T, d,
-                              1.0 / d ** 0.5 if scale is None else scale,
-                              None if q_lens is None else q_lens.data_ptr(), ctypes.byref(mod), _DTYPES[dtype],
-                              None if workspace is None else workspace.data_ptr(),
-                              0 if workspace is None else workspace.numel() * workspace.element_size(),
-                              _handle(stream, dev, *mine))
+    st = lib.fa_forward_paged_packed(_PAGED.pack(
+        *cache, q.data_ptr(), o.data_ptr(), lse.data_ptr(), 0 if q_lens is None else q_lens.data_ptr(),
+        0 if alibi_slopes is None else alibi_slopes.data_ptr(), 0 if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _handle(stream, dev, o_new, lse_new, ws_new),
+        B, H, Hkv, T, d, _DTYPES[dtype], 1.0 / d ** 0.5 if scale is None else scale, softcap))
     if st != FA_OK:
         raise FaError(st, "fa_forward_paged")
     return o, lse

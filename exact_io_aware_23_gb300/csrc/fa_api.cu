@@ -626,6 +626,29 @@ fa_status fa_backward_varlen_scored(const void* q, const void* k, const void* v,
                        Packing{cu_seqlens, total}, fa::DropoutArgs{}, score);
 }
 
+fa_status fa_forward_scored_packed(const fa_scored_call* c) {
+  if (c == nullptr || (c->cu_seqlens != nullptr && c->kv_lens != nullptr)) return FA_ERR_INVALID_ARG;
+  const fa_score_mod mod{c->softcap, c->alibi_slopes, c->prefix_lens};
+  const fa_dtype dt = static_cast<fa_dtype>(c->dtype);
+  if (c->cu_seqlens != nullptr)
+    return fa_forward_varlen_scored(c->q, c->k, c->v, c->o, c->lse, c->cu_seqlens, c->B, c->N, c->total, c->H, c->Hkv,
+                                    c->d, c->scale, c->causal, dt, &mod, c->stream);
+  return fa_forward_scored(c->q, c->k, c->v, c->o, c->lse, c->B, c->H, c->Hkv, c->N, c->d, c->scale, c->causal, dt,
+                           c->kv_lens, &mod, c->stream);
+}
+
+fa_status fa_backward_scored_packed(const fa_scored_call* c) {
+  if (c == nullptr || (c->cu_seqlens != nullptr && c->kv_lens != nullptr)) return FA_ERR_INVALID_ARG;
+  const fa_score_mod mod{c->softcap, c->alibi_slopes, c->prefix_lens};
+  const fa_dtype dt = static_cast<fa_dtype>(c->dtype);
+  if (c->cu_seqlens != nullptr)
+    return fa_backward_varlen_scored(c->q, c->k, c->v, c->o, c->dO, c->lse, c->dq, c->dk, c->dv, c->cu_seqlens, c->B,
+                                     c->N, c->total, c->H, c->Hkv, c->d, c->scale, c->causal, dt, &mod, c->workspace,
+                                     c->workspace_bytes, c->stream);
+  return fa_backward_scored(c->q, c->k, c->v, c->o, c->dO, c->lse, c->dq, c->dk, c->dv, c->B, c->H, c->Hkv, c->N,
+                            c->d, c->scale, c->causal, dt, c->kv_lens, &mod, c->workspace, c->workspace_bytes, c->stream);
+}
+
 fa_status fa_check_device_status(void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(s) != cudaSuccess) return FA_ERR_CUDA;

@@ -212,4 +212,31 @@ fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, 
   return fa::launch_paged(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+fa_status fa_rotary_packed(const fa_rotary_call* c) {
+  if (c == nullptr) return FA_ERR_INVALID_ARG;
+  return fa_rotary(c->x, c->x_strides, c->y, c->y_strides, c->B, c->H, c->N, c->d, c->positions, c->position_stride,
+                   c->inv_freq, c->rotary_dim, c->interleaved, c->mscale, static_cast<fa_dtype>(c->dtype), c->stream);
+}
+
+fa_status fa_rotary_backward_packed(const fa_rotary_call* c) {
+  if (c == nullptr) return FA_ERR_INVALID_ARG;
+  return fa_rotary_backward(c->x, c->x_strides, c->y, c->y_strides, c->B, c->H, c->N, c->d, c->positions,
+                            c->position_stride, c->inv_freq, c->rotary_dim, c->interleaved, c->mscale,
+                            static_cast<fa_dtype>(c->dtype), c->stream);
+}
+
+fa_status fa_append_paged_packed(const fa_append_paged_call* c) {
+  if (c == nullptr) return FA_ERR_INVALID_ARG;
+  return fa_append_paged(&c->cache, c->k, c->k_strides, c->v, c->v_strides, c->q, c->q_strides, c->q_out, c->B, c->H,
+                         c->Hkv, c->T, c->d, c->q_lens, c->inv_freq, c->rotary_dim, c->interleaved, c->mscale,
+                         static_cast<fa_dtype>(c->dtype), c->stream);
+}
+
+fa_status fa_forward_paged_packed(const fa_forward_paged_call* c) {
+  if (c == nullptr) return FA_ERR_INVALID_ARG;
+  const fa_score_mod mod{c->softcap, c->alibi_slopes, nullptr};
+  return fa_forward_paged(c->q, &c->cache, c->o, c->lse, c->B, c->H, c->Hkv, c->T, c->d, c->scale, c->q_lens, &mod,
+                          static_cast<fa_dtype>(c->dtype), c->workspace, c->workspace_bytes, c->stream);
+}
+
 }  // extern "C"

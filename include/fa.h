@@ -480,6 +480,68 @@ fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, 
                            const fa_score_mod* score, fa_dtype dtype, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/*
+ * These calls with their arguments in one structure, fields as the parameters above.  For callers
+ * behind a foreign-function interface, which converts one argument then instead of up to 21.
+ */
+typedef struct {
+  const void *q, *k, *v;
+  void* o;                     /* read by the backward */
+  float* lse;                  /* read by the backward */
+  const void* dO;
+  void *dq, *dk, *dv;
+  const int32_t* kv_lens;      /* nullable; not with cu_seqlens */
+  const int32_t* cu_seqlens;   /* null for the batched calls, else their packed forms with B = n_seqs, */
+  const float* alibi_slopes;   /*   N = max_seqlen and `total` */
+  const int32_t* prefix_lens;
+  void* workspace;             /* backward */
+  size_t workspace_bytes;
+  void* stream;
+  int B, H, Hkv, N, total, d, causal, dtype;
+  float scale, softcap;
+} fa_scored_call;
+typedef struct {
+  const void* x;
+  void* y;
+  const int32_t* positions;
+  const double* inv_freq;
+  void* stream;
+  int64_t x_strides[3], y_strides[3];
+  int64_t position_stride;
+  int B, H, N, d, rotary_dim, interleaved, dtype;
+  float mscale;
+} fa_rotary_call;
+typedef struct {
+  fa_paged_cache cache;
+  const void *k, *v, *q;
+  void* q_out;
+  const int32_t* q_lens;
+  const double* inv_freq;
+  void* stream;
+  int64_t k_strides[3], v_strides[3], q_strides[3];
+  int B, H, Hkv, T, d, rotary_dim, interleaved, dtype;
+  float mscale;
+} fa_append_paged_call;
+typedef struct {
+  fa_paged_cache cache;
+  const void* q;
+  void* o;
+  float* lse;
+  const int32_t* q_lens;
+  const float* alibi_slopes;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+  int B, H, Hkv, T, d, dtype;
+  float scale, softcap;
+} fa_forward_paged_call;
+fa_status fa_forward_scored_packed(const fa_scored_call* call);
+fa_status fa_backward_scored_packed(const fa_scored_call* call);
+fa_status fa_rotary_packed(const fa_rotary_call* call);
+fa_status fa_rotary_backward_packed(const fa_rotary_call* call);
+fa_status fa_append_paged_packed(const fa_append_paged_call* call);
+fa_status fa_forward_paged_packed(const fa_forward_paged_call* call);
+
 /* ABI version of this header: major * 100 + minor. */
 int fa_version(void);
 

@@ -1,6 +1,8 @@
 """Host-side argument checks of the rotary and paged-cache calls: the documented status before any
 CUDA call (CPU only: no kernel runs)."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -167,3 +169,63 @@ def test_scored_argument_checks():
         assert call(good, w=None) == INVALID
         assert call(good, w=P + 16) == INVALID
     assert bwd(good, wsb=ws - 4) == INVALID
+
+
+def test_packed_calls():
+    """One structure in place of the arguments: the same checks, and the layouts of the header."""
+    for fn in (fa.lib.fa_forward_scored_packed, fa.lib.fa_backward_scored_packed, fa.lib.fa_rotary_packed,
+               fa.lib.fa_rotary_backward_packed, fa.lib.fa_append_paged_packed, fa.lib.fa_forward_paged_packed):
+        assert fn(None) == INVALID
+    header = open(os.path.join(os.path.dirname(fa.LIB_PATH), os.pardir, "include", "fa.h")).read()
+    size = {"int": 4, "float": 4, "fa_paged_cache": ctypes.sizeof(fa.FaPagedCache)}      # others: 8
+    for name, packed in (("fa_scored_call", fa._SCORED), ("fa_rotary_call", fa._ROTARY),
+                         ("fa_append_paged_call", fa._APPEND), ("fa_forward_paged_call", fa._PAGED)):
+        body = re.search(r"typedef struct \{([^{}]*)\} " + name + ";", header).group(1)
+        total = 0
+        for field in re.sub(r"/\*.*?\*/", "", body, flags=re.S).split(";")[:-1]:
+            kind = field.split()[1 if field.split()[0] == "const" else 0]
+            for one in field.split(","):
+                n = int((re.findall(r"\[(\d+)\]", one) or [1])[0])
+                total += n * (8 if "*" in one else size.get(kind, 8))
+        assert packed.size == (total + 7) // 8 * 8, name
+
+    rot = dict(x=P, y=P, pos=P, inv=P, xs=(1 << 16, 1 << 13, 64), ys=(1 << 16, 1 << 13, 64), B=1, H=2, N=8, d=64, rot=0)
+    def rotary_packed(**kw):
+        c = dict(rot, **kw)
+        return fa.lib.fa_rotary_packed(fa._ROTARY.pack(c["x"], c["y"], c["pos"], c["inv"], 0, *c["xs"], *c["ys"], 0,
+                                                       c["B"], c["H"], c["N"], c["d"], c["rot"], 0, 0, 1.0))
+    assert rotary_packed(N=0) == OK
+    assert rotary_packed(x=0) == INVALID
+    assert rotary_packed(d=80) == UNSUPPORTED
+    assert rotary_packed(rot=40) == UNSUPPORTED
+    assert rotary_packed(ys=(0, 32, 64)) == INVALID
+
+    def scored_packed(fn, q=P, kv_lens=0, cu=0, B=1, N=64, d=64, scale=0.1, softcap=30.0, ws=1 << 20):
+        return fn(fa._SCORED.pack(q, P, P, P, P, P, P, P, P, kv_lens, cu, 0, 0, P, ws, 0, B, 2, 2, N, 128, d, 1, 0,
+                                  scale, softcap))
+    for fn in (fa.lib.fa_forward_scored_packed, fa.lib.fa_backward_scored_packed):
+        assert scored_packed(fn, N=0) == OK
+        assert scored_packed(fn, cu=P, B=0) == OK
+        assert scored_packed(fn, cu=P, kv_lens=P) == INVALID
+        assert scored_packed(fn, q=0) == INVALID
+        assert scored_packed(fn, softcap=-1.0) == INVALID
+        assert scored_packed(fn, scale=0.0) == INVALID
+        assert scored_packed(fn, d=80) == UNSUPPORTED
+    assert scored_packed(fa.lib.fa_backward_scored_packed, ws=0) == INVALID
+
+    c = (P, P + 4096, 4096, 1024, 64, 4, 16, P, 8, 8, P)
+    def append_packed(B=1, d=64, k=P, q=0):
+        return fa.lib.fa_append_paged_packed(fa._APPEND.pack(*c, k, P, q, 0, 0, 0, 0, *(1 << 16, 1 << 13, 64) * 3,
+                                                             B, 2, 2, 1, d, 0, 0, 0, 1.0))
+    assert append_packed(B=0) == OK
+    assert append_packed(k=0) == INVALID
+    assert append_packed(q=P) == INVALID                  # queries without a place for them
+    assert append_packed(d=80) == UNSUPPORTED
+
+    def paged_packed(B=1, d=64, q=P, scale=0.1, softcap=0.0):
+        return fa.lib.fa_forward_paged_packed(fa._PAGED.pack(*c, q, P, P, 0, 0, 0, 0, 0, B, 2, 2, 1, d, 0, scale, softcap))
+    assert paged_packed(B=0) == OK
+    assert paged_packed(q=0) == INVALID
+    assert paged_packed(scale=0.0) == INVALID
+    assert paged_packed(softcap=float("inf")) == INVALID
+    assert paged_packed(d=80) == UNSUPPORTED
