@@ -9,6 +9,7 @@ fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import struct
@@ -519,8 +520,9 @@ def noalloc_max_workspace() -> int:
 #
 # These calls are made once per layer and token: their host time is most of a short call, so the
 # checks read each property of a tensor once, names for a message are found only when one is
-# raised, and the arguments cross as one packed structure (one token over a short cache: 15.3 us a
-# call, with an argument each 17.6; its write into the cache 12.7 and 16.9).
+# raised, and the arguments cross as one packed structure (one token over a short cache: 13.7 us a
+# call, 18 with an argument each and the workspace's size asked for every time; its write into the
+# cache 12.9 and 17.7).
 
 _CACHE_FORMAT = "PPqqqiiPqiP"                                     # fa_paged_cache
 _SCORED = struct.Struct("14PNP8iff")                              # fa_scored_call
@@ -528,6 +530,9 @@ _ROTARY = struct.Struct("PPPPP7q7if")                             # fa_rotary_ca
 _APPEND = struct.Struct(_CACHE_FORMAT + "7P9q8if0q")              # fa_append_paged_call
 _PAGED = struct.Struct(_CACHE_FORMAT + "6PNP6iff")                # fa_forward_paged_call
 _16_BIT = (torch.bfloat16, torch.float16)
+
+
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _refuse_place(**tensors) -> None:
@@ -544,13 +549,13 @@ def _refuse_place(**tensors) -> None:
 def _current_device(t: torch.Tensor) -> int:
     """The current device's index, when t is there; -1 otherwise (tensors elsewhere give -1 too)."""
     dev = t.get_device()
-    return dev if dev >= 0 and dev == torch._C._cuda_getDevice() else -1
+    return dev if dev >= 0 and dev == _device() else -1
 
 
 def _handle(stream, dev: int, *allocated) -> int:
     """The stream's handle.  Memory allocated here for a call on a stream that is not the current one
     is not reused before that stream is done with it."""
-    current = torch._C._cuda_getCurrentRawStream(dev)
+    current = _raw_stream(dev)
     if stream is None or stream.cuda_stream == current:
         return current
     for t in allocated:
@@ -745,7 +750,7 @@ def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
             raise ValueError("q must be [B, H, T, d] of k's type, the key heads dividing H")
         qs = _strides("q", q)
         if q_out is None:
-            q_out = torch.empty(qshape, dtype=dtype, device=k.device)
+            q_out = torch.empty(qshape, dtype=dtype, device=q.device)
             s = _handle(stream, dev, q_out)
         else:
             _refuse_place(q_out=q_out)
@@ -770,6 +775,13 @@ def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
 def forward_paged_workspace_size(B: int, H: int, Hkv: int, T: int, d: int, max_keys: int) -> int:
     """max_keys: entries of a block table's row times the page size."""
     return int(lib.fa_forward_paged_workspace_size(B, H, Hkv, T, d, max_keys))
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_workspace_size(dev, *sizes) -> int:
+    """forward_paged_workspace_size, which the device and the sizes determine: one call into the library
+    for each of them."""
+    return lib.fa_forward_paged_workspace_size(*sizes)
 
 
 def _check_slopes(alibi_slopes, H) -> None:
@@ -826,7 +838,6 @@ def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         _int32("q_lens", q_lens, (B,))
     if alibi_slopes is not None:
         _check_slopes(alibi_slopes, H)
-    device = q.device
     if o is None:
         o = o_new = torch.empty_like(q)
     else:
@@ -836,7 +847,7 @@ def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
             raise ValueError("o must be contiguous, of q's shape and type")
         _apart("q", q, "o", o, False)
     if lse is None:
-        lse = lse_new = torch.empty((B, H, T), dtype=torch.float32, device=device)
+        lse = lse_new = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
     else:
         lse_new = None
         _refuse_place(lse=lse)
@@ -844,9 +855,9 @@ def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
             raise ValueError("lse must be contiguous float32 [B, H, T]")
     ws_new = None
     if workspace is None:
-        need = lib.fa_forward_paged_workspace_size(B, H, Hkv, T, d, min(cache[6] * cache[9], 0x7fffffff))
+        need = _paged_workspace_size(dev, B, H, Hkv, T, d, min(cache[6] * cache[9], 0x7fffffff))
         if need > 0:
-            workspace = ws_new = torch.empty((need,), dtype=torch.uint8, device=device)
+            workspace = ws_new = torch.empty((need,), dtype=torch.uint8, device=q.device)
     else:
         _refuse_place(workspace=workspace)
     st = lib.fa_forward_paged_packed(_PAGED.pack(

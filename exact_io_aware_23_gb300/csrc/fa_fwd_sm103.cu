@@ -722,7 +722,7 @@ cudaError_t launch_fwd_sm103(const FwdArgs& a, fa_dtype dt, cudaStream_t s) {
     // no tile mask, split-KV or dropout with score modifications
     if (a.drop.enabled || a.block_mask != nullptr || a.n_splits != 1 || a.o_part != nullptr) return cudaErrorInvalidValue;
     // d = 64: as the plain forward, but where one CTA per SM holds the whole problem the larger key
-    // tiles are ahead (B4 H16 N511: 20 us against 23; B8 H12 N1024, 384 CTAs: 54 against 50)
+    // tiles are ahead (B4 H16 N511: 20 us against 23; B8 H12 N1024, 384 CTAs: 54 against 48)
     int sms = 0;
     const cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
