@@ -196,11 +196,6 @@ def _masks(block_mask, kv_lens, B, N, device):
     return block_mask, kv_lens
 
 
-def _scored(softcap, alibi_slopes, prefix_lens) -> bool:
-    """Whether any score modification is asked for."""
-    return softcap != 0.0 or alibi_slopes is not None or prefix_lens is not None
-
-
 def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = False,
             scale: Optional[float] = None, block_mask: Optional[torch.Tensor] = None,
             kv_lens: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
@@ -216,23 +211,16 @@ def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool =
     alibi_slopes (fp32 [H]: scores lowered by the slope times |i - j|) or prefix_lens (int32 [B]:
     leading keys seen in spite of causal), fa_forward_scored: bf16 or fp16, no block mask or
     dropout."""
+    if softcap != 0.0 or alibi_slopes is not None or prefix_lens is not None:
+        if block_mask is not None or dropout_p > 0.0:
+            raise ValueError("score modifications take no block mask and no dropout")
+        return _forward_scored(q, k, v, causal, scale, kv_lens, o, lse, stream, softcap, alibi_slopes, prefix_lens)
     B, H, N, d, Hkv = _check_qkv(q, k, v)
     scale = 1.0 / d ** 0.5 if scale is None else float(scale)
     if block_mask is not None or kv_lens is not None:
         block_mask, kv_lens = _masks(block_mask, kv_lens, B, N, q.device)
     o = torch.empty_like(q) if o is None else o
     lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device) if lse is None else lse
-    if _scored(softcap, alibi_slopes, prefix_lens):
-        if block_mask is not None or dropout_p > 0.0:
-            raise ValueError("score modifications take no block mask and no dropout")
-        dev, slopes, prefix = _score_args(q, k, v, None, None, None, alibi_slopes, prefix_lens, H, B)
-        st = lib.fa_forward_scored_packed(_SCORED.pack(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), 0, 0, 0, 0,
-            0 if kv_lens is None else kv_lens.data_ptr(), 0, slopes, prefix, 0, 0, _handle(stream, dev, o, lse),
-            B, H, Hkv, N, 0, d, 1 if causal else 0, _DTYPES[q.dtype], scale, softcap))
-        if st != FA_OK:
-            raise FaError(st, "fa_forward_scored")
-        return o, lse
     if dropout_p > 0.0:
         drop = FaDropout(float(dropout_p), int(seed), int(offset))
         st = lib.fa_forward_dropout(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Hkv, N, d,
@@ -297,7 +285,7 @@ def forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, *, causal: bool = False
     scale = 1.0 / d ** 0.5 if scale is None else float(scale)
     o = torch.empty_like(q)
     lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
-    if _scored(softcap, alibi_slopes, prefix_lens):
+    if softcap != 0.0 or alibi_slopes is not None or prefix_lens is not None:
         dev, slopes, prefix = _score_args(q, k, v, None, None, None, alibi_slopes, prefix_lens, H, S)
         st = lib.fa_forward_scored_packed(_SCORED.pack(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), 0, 0, 0, 0, 0,
@@ -330,7 +318,9 @@ def backward_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen: int, *, causal:
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     need = backward_deterministic_workspace_size(1, H, T)
     workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    if _scored(softcap, alibi_slopes, prefix_lens):
+    if softcap != 0.0 or alibi_slopes is not None or prefix_lens is not None:
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
         dev, slopes, prefix = _score_args(q, k, v, o, lse, do, alibi_slopes, prefix_lens, H, S)
         st = lib.fa_backward_scored_packed(_SCORED.pack(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
@@ -413,6 +403,11 @@ def backward(q, k, v, o, lse, do, *, causal: bool = False, scale: Optional[float
     have fewer heads than q; fa_backward_deterministic, bit-reproducible, when asked;
     fa_backward_fused, the single-pass atomic-dQ variant, when asked; fa_backward_scored,
     bit-reproducible too, with the score arguments of ``forward``)."""
+    if softcap != 0.0 or alibi_slopes is not None or prefix_lens is not None:
+        if block_mask is not None or dropout_p > 0.0 or fused:
+            raise ValueError("score modifications take no block mask, no dropout and no fused backward")
+        return _backward_scored(q, k, v, o, lse, do, causal, scale, kv_lens, dq, dk, dv, workspace, stream, softcap,
+                                alibi_slopes, prefix_lens)
     B, H, N, d, Hkv = _check_qkv(q, k, v)
     shape, dtype = q.shape, q.dtype
     if o.shape != shape or o.dtype != dtype or not o.is_contiguous():
@@ -434,19 +429,6 @@ def backward(q, k, v, o, lse, do, *, causal: bool = False, scale: Optional[float
             else backward_workspace_size(B, H, N, d))
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    if _scored(softcap, alibi_slopes, prefix_lens):
-        if block_mask is not None or dropout_p > 0.0 or fused:
-            raise ValueError("score modifications take no block mask, no dropout and no fused backward")
-        dev, slopes, prefix = _score_args(q, k, v, o, lse, do, alibi_slopes, prefix_lens, H, B)
-        st = lib.fa_backward_scored_packed(_SCORED.pack(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
-            dk.data_ptr(), dv.data_ptr(), 0 if kv_lens is None else kv_lens.data_ptr(), 0, slopes, prefix,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            _handle(stream, dev, dq, dk, dv, workspace),
-            B, H, Hkv, N, 0, d, 1 if causal else 0, _DTYPES[q.dtype], scale, softcap))
-        if st != FA_OK:
-            raise FaError(st, "fa_backward_scored")
-        return dq, dk, dv
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv))
     tail = (d, scale, int(bool(causal)), _ptr(block_mask), _DTYPES[q.dtype], _ptr(kv_lens),
             _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
@@ -530,9 +512,8 @@ _ROTARY = struct.Struct("PPPPP7q7if")                             # fa_rotary_ca
 _APPEND = struct.Struct(_CACHE_FORMAT + "7P9q8if0q")              # fa_append_paged_call
 _PAGED = struct.Struct(_CACHE_FORMAT + "6PNP6iff")                # fa_forward_paged_call
 _16_BIT = (torch.bfloat16, torch.float16)
-
-
-_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# of PyTorch's module for CUDA, without the wrappers around them (absent from builds without CUDA)
+_device, _raw_stream = (getattr(torch._C, name, None) for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
 
 
 def _refuse_place(**tensors) -> None:
@@ -553,14 +534,17 @@ def _current_device(t: torch.Tensor) -> int:
 
 
 def _handle(stream, dev: int, *allocated) -> int:
-    """The stream's handle.  Memory allocated here for a call on a stream that is not the current one
-    is not reused before that stream is done with it."""
+    """The stream's handle.  Memory allocated here (None: given by the caller) belongs to the current
+    stream: for a call on another one, that stream first waits for what the current one still does
+    with it, and it is not reused before that stream is done with it."""
     current = _raw_stream(dev)
     if stream is None or stream.cuda_stream == current:
         return current
-    for t in allocated:
-        if t is not None:
-            t.record_stream(stream)
+    mine = [t for t in allocated if t is not None]
+    if mine:
+        stream.wait_stream(torch.cuda.current_stream(dev))
+    for t in mine:
+        t.record_stream(stream)
     return stream.cuda_stream
 
 
@@ -806,6 +790,90 @@ def _score_args(q, k, v, o, lse, do, alibi_slopes, prefix_lens, H, n_seqs) -> Tu
         _int32("prefix_lens", prefix_lens, (n_seqs,))
         prefix = prefix_lens.data_ptr()
     return dev, slopes, prefix
+
+
+def _given(name: str, t: torch.Tensor, shape, dtype) -> None:
+    """Checks an output that the caller gives."""
+    _refuse_place(**{name: t})
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor")
+
+
+def _kv_lens(kv_lens, B, dev, q) -> torch.Tensor:
+    if kv_lens.get_device() != dev or kv_lens.dtype != torch.int32 or kv_lens.shape != (B,) or not kv_lens.is_contiguous():
+        kv_lens = _masks(None, kv_lens, B, 0, q.device)[1]
+    return kv_lens
+
+
+@functools.lru_cache(maxsize=1024)
+def _backward_workspace_size(B, H, N, d) -> int:
+    """backward_workspace_size, which the sizes determine: one call into the library for each of them."""
+    return max(lib.fa_backward_workspace_size(B, H, N, d), 256)
+
+
+def _forward_scored(q, k, v, causal, scale, kv_lens, o, lse, stream, softcap, alibi_slopes, prefix_lens):
+    B, H, N, d, Hkv = _check_qkv(q, k, v)
+    dev, slopes, prefix = _score_args(q, k, v, None, None, None, alibi_slopes, prefix_lens, H, B)
+    dtype = q.dtype
+    if kv_lens is not None:
+        kv_lens = _kv_lens(kv_lens, B, dev, q)
+    o_new = lse_new = None
+    if o is None:
+        o = o_new = torch.empty_like(q)
+    else:
+        _given("o", o, q.shape, dtype)
+    if lse is None:
+        lse = lse_new = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+    else:
+        _given("lse", lse, (B, H, N), torch.float32)
+    st = lib.fa_forward_scored_packed(_SCORED.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), 0, 0, 0, 0,
+        0 if kv_lens is None else kv_lens.data_ptr(), 0, slopes, prefix, 0, 0, _handle(stream, dev, o_new, lse_new),
+        B, H, Hkv, N, 0, d, 1 if causal else 0, _DTYPES[dtype], 1.0 / d ** 0.5 if scale is None else scale, softcap))
+    if st != FA_OK:
+        raise FaError(st, "fa_forward_scored")
+    return o, lse
+
+
+def _backward_scored(q, k, v, o, lse, do, causal, scale, kv_lens, dq, dk, dv, workspace, stream, softcap,
+                     alibi_slopes, prefix_lens):
+    B, H, N, d, Hkv = _check_qkv(q, k, v)
+    dev, slopes, prefix = _score_args(q, k, v, o, lse, do, alibi_slopes, prefix_lens, H, B)
+    shape, dtype = q.shape, q.dtype
+    if o.shape != shape or o.dtype != dtype or not o.is_contiguous():
+        raise ValueError("o must match q")
+    if do.shape != shape or do.dtype != dtype or not do.is_contiguous():
+        raise ValueError("do must match q")
+    if lse.dtype != torch.float32 or lse.shape != (B, H, N) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [B, H, N]")
+    if kv_lens is not None:
+        kv_lens = _kv_lens(kv_lens, B, dev, q)
+    dq_new = dk_new = dv_new = ws_new = None
+    if dq is None:
+        dq = dq_new = torch.empty_like(q)
+    else:
+        _given("dq", dq, shape, dtype)
+    if dk is None:
+        dk = dk_new = torch.empty_like(k)
+    else:
+        _given("dk", dk, k.shape, dtype)
+    if dv is None:
+        dv = dv_new = torch.empty_like(v)
+    else:
+        _given("dv", dv, k.shape, dtype)
+    if workspace is None:
+        workspace = ws_new = torch.empty(_backward_workspace_size(B, H, N, d), dtype=torch.uint8, device=q.device)
+    else:
+        _refuse_place(workspace=workspace)
+    st = lib.fa_backward_scored_packed(_SCORED.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
+        dk.data_ptr(), dv.data_ptr(), 0 if kv_lens is None else kv_lens.data_ptr(), 0, slopes, prefix,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _handle(stream, dev, dq_new, dk_new, dv_new, ws_new),
+        B, H, Hkv, N, 0, d, 1 if causal else 0, _DTYPES[dtype], 1.0 / d ** 0.5 if scale is None else scale, softcap))
+    if st != FA_OK:
+        raise FaError(st, "fa_backward_scored")
+    return dq, dk, dv
 
 
 def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,

@@ -123,6 +123,26 @@ def test_empty_and_copy():
     assert torch.equal(fa.rotary(x, torch.arange(9, dtype=torch.int32, device="cuda"), none), x)
 
 
+def test_memory_the_current_stream_still_reads():
+    """The output of a call on another stream may lie in memory that was given back on the current
+    one, whose kernels still read it."""
+    inv_freq, _ = fa.rotary_frequencies(128)
+    x = _x(1, 8, 4096, 128, "bf16")
+    pos = torch.arange(4096, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    old = x.clone()
+    busy = torch.randn(4096, 4096, device="cuda")
+    for _ in range(20):
+        busy = (busy @ busy).clamp_(-1.0, 1.0)          # some milliseconds
+    kept = old.clone()
+    del old
+    y = fa.rotary(x, pos, inv_freq, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(kept, x)
+    assert torch.equal(y, fa.rotary(x, pos, inv_freq))
+
+
 def test_captured_and_on_another_stream():
     inv_freq, _ = fa.rotary_frequencies(128)
     x = _x(1, 8, 256, 128, "bf16")

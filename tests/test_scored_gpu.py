@@ -225,6 +225,18 @@ def test_refusals():
     o, lse = fa.forward(q, k, v, softcap=10.0)
     with pytest.raises(ValueError, match="fused"):
         fa.backward(q, k, v, o, lse, do, softcap=10.0, fused=True)
+    wide = torch.empty((*lse.shape[:2], 2 * lse.shape[2]), device="cuda")
+    with pytest.raises(ValueError, match="lse"):
+        fa.backward(q, k, v, o, wide[:, :, ::2], do, softcap=10.0)
+    with pytest.raises(ValueError, match="lse"):
+        fa.forward(q, k, v, softcap=10.0, lse=wide[:, :, ::2])
+    with pytest.raises(ValueError, match="o must be"):
+        fa.forward(q, k, v, softcap=10.0, o=o[:, :2])
+    for name in ("dq", "dk", "dv"):
+        with pytest.raises(ValueError, match=name):
+            fa.backward(q, k, v, o, lse, do, softcap=10.0, **{name: torch.empty_like(q).float()})
+    with pytest.raises(fa.FaError, match="INVALID_ARG"):
+        fa.backward(q, k, v, o, lse, do, softcap=10.0, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError, match="alibi_slopes"):
         fa.forward(q, k, v, alibi_slopes=_slopes(2))
     with pytest.raises(ValueError, match="alibi_slopes"):
