@@ -118,20 +118,20 @@ __device__ __forceinline__ float2 tanh_of(float2 s, const ScoreArgs& k) {
 }
 // The bias -slope |i - j| over one thread's row (or column) of a tile, whose distances run on by one:
 // at score e it is base + e * step where the tile lies on one side of the diagonal (or the other
-// side is masked), and -|base + e * step| where it crosses it.  `first` is j - i, or i - j, at the
+// side is masked), and -slope * |first + e| where it crosses it.  `first` is j - i, or i - j, at the
 // first score; lo and hi bound it over the unmasked part of the whole tile.
 struct Bias {
-  float base, step;
+  float base, step, first, minus_slope;
   bool crosses;
 };
 __device__ __forceinline__ Bias make_bias(float slope, int first, int lo, int hi) {
   const float s = lo >= 0 ? -slope : slope;
-  return Bias{s * (float)first, s, lo < 0 && hi > 0};
+  return Bias{s * (float)first, s, (float)first, -slope, lo < 0 && hi > 0};
 }
 template <int kBias>
 __device__ __forceinline__ float biased(float x, const Bias& b, int e) {
   if constexpr (kBias == kBiasLinear) return fmaf(b.step, (float)e, x);        // the base is in x already
-  else return x - fabsf(fmaf(b.step, (float)e, b.base));
+  else return fmaf(b.minus_slope, fabsf(b.first + (float)e), x);
 }
 
 // What a call modifies, as the backward's kernels are compiled for it: one kernel for all kinds keeps
