@@ -799,10 +799,15 @@ def _given(name: str, t: torch.Tensor, shape, dtype) -> None:
         raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor")
 
 
-def _kv_lens(kv_lens, B, dev, q) -> torch.Tensor:
+def _kv_lens(kv_lens, B, dev, q):
+    """The key lengths where and as the library takes them, and the copy made for that (or None), which
+    is memory allocated here like an output."""
+    if kv_lens is None:
+        return None, None
     if kv_lens.get_device() != dev or kv_lens.dtype != torch.int32 or kv_lens.shape != (B,) or not kv_lens.is_contiguous():
         kv_lens = _masks(None, kv_lens, B, 0, q.device)[1]
-    return kv_lens
+        return kv_lens, kv_lens
+    return kv_lens, None
 
 
 @functools.lru_cache(maxsize=1024)
@@ -815,8 +820,7 @@ def _forward_scored(q, k, v, causal, scale, kv_lens, o, lse, stream, softcap, al
     B, H, N, d, Hkv = _check_qkv(q, k, v)
     dev, slopes, prefix = _score_args(q, k, v, None, None, None, alibi_slopes, prefix_lens, H, B)
     dtype = q.dtype
-    if kv_lens is not None:
-        kv_lens = _kv_lens(kv_lens, B, dev, q)
+    kv_lens, kv_new = _kv_lens(kv_lens, B, dev, q)
     o_new = lse_new = None
     if o is None:
         o = o_new = torch.empty_like(q)
@@ -828,7 +832,7 @@ def _forward_scored(q, k, v, causal, scale, kv_lens, o, lse, stream, softcap, al
         _given("lse", lse, (B, H, N), torch.float32)
     st = lib.fa_forward_scored_packed(_SCORED.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), 0, 0, 0, 0,
-        0 if kv_lens is None else kv_lens.data_ptr(), 0, slopes, prefix, 0, 0, _handle(stream, dev, o_new, lse_new),
+        0 if kv_lens is None else kv_lens.data_ptr(), 0, slopes, prefix, 0, 0, _handle(stream, dev, o_new, lse_new, kv_new),
         B, H, Hkv, N, 0, d, 1 if causal else 0, _DTYPES[dtype], 1.0 / d ** 0.5 if scale is None else scale, softcap))
     if st != FA_OK:
         raise FaError(st, "fa_forward_scored")
@@ -846,8 +850,7 @@ def _backward_scored(q, k, v, o, lse, do, causal, scale, kv_lens, dq, dk, dv, wo
         raise ValueError("do must match q")
     if lse.dtype != torch.float32 or lse.shape != (B, H, N) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [B, H, N]")
-    if kv_lens is not None:
-        kv_lens = _kv_lens(kv_lens, B, dev, q)
+    kv_lens, kv_new = _kv_lens(kv_lens, B, dev, q)
     dq_new = dk_new = dv_new = ws_new = None
     if dq is None:
         dq = dq_new = torch.empty_like(q)
@@ -869,7 +872,7 @@ def _backward_scored(q, k, v, o, lse, do, causal, scale, kv_lens, dq, dk, dv, wo
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
         dk.data_ptr(), dv.data_ptr(), 0 if kv_lens is None else kv_lens.data_ptr(), 0, slopes, prefix,
         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _handle(stream, dev, dq_new, dk_new, dv_new, ws_new),
+        _handle(stream, dev, dq_new, dk_new, dv_new, ws_new, kv_new),
         B, H, Hkv, N, 0, d, 1 if causal else 0, _DTYPES[dtype], 1.0 / d ** 0.5 if scale is None else scale, softcap))
     if st != FA_OK:
         raise FaError(st, "fa_backward_scored")
