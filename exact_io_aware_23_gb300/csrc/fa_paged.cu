@@ -232,10 +232,10 @@ __device__ __forceinline__ void no_keys(const PagedArgs& a, int64_t row, int n) 
 
 template <int D, bool F16>
 __device__ __forceinline__ void write_row4(const PagedArgs& a, int64_t row, int c, float4 acc, float sum, float mx) {
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;        // 0: no key; NaN stays
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + row * D + c) =
       make_uint2(ptx::pack2<F16>(acc.x * inv, acc.y * inv), ptx::pack2<F16>(acc.z * inv, acc.w * inv));
-  if (c == 0) a.lse[row] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+  if (c == 0) a.lse[row] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // Announces this CTA's part of a segment that CTAs ca..cb share, and says whether all of them are
@@ -590,7 +590,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if (ml[w].x == -INFINITY) continue;             // no tile, or none that the row sees
+        // no tile, or none that the row sees.  By the sum, not the maximum: scores that are NaN leave
+        // that at -inf, and have to show in the result.
+        if (ml[w].y == 0.f) continue;
         const float f = ptx::ex2(ml[w].x - mx);
         const float4 v = *reinterpret_cast<const float4*>(smem + from[w] + r * D * 4 + (((c >> 2) ^ (r & 7)) << 4));
         sum = fmaf(f, ml[w].y, sum);
@@ -639,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
 #pragma unroll 1
         for (int i0 = ca; i0 <= cb; i0 += C::kJoin) {
           const int np = min(C::kJoin, cb + 1 - i0);
-          // sixteen parts' outputs of item x; past the last part its own again, with weight 0
+          // sixteen parts' outputs of item x; past the last part its own again, not used
           auto outputs = [&](int x, int i, float4 (&v)[16]) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
@@ -659,8 +661,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
             const int r = x / kQuads;
             float m_new = mx[y];
             for (int i = 0; i < np; ++i) m_new = fmaxf(m_new, joined[i * kRows + r].x);
-            if (m_new == -INFINITY) continue;           // no key of the row so far
-            const float keep = ptx::ex2(mx[y] - m_new);
+            // no key of the row so far, and none that is NaN, where the maximum is still -inf
+            const float keep = mx[y] == m_new ? 1.f : ptx::ex2(mx[y] - m_new);
             mx[y] = m_new;
             sum[y] *= keep;
             acc[y].x *= keep;
@@ -672,7 +674,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
                 const float2 ml = joined[min(i + k, np - 1) * kRows + r];
-                const float f = i + k < np ? ptx::ex2(ml.x - m_new) : 0.f;     // 0 too for a part without keys
+                if (i + k >= np || ml.y == 0.f) continue;     // no part, or no key of the row in it
+                const float f = ptx::ex2(ml.x - m_new);
                 sum[y] = fmaf(f, ml.y, sum[y]);
                 acc[y].x = fmaf(f, v[k].x, acc[y].x);
                 acc[y].y = fmaf(f, v[k].y, acc[y].y);
