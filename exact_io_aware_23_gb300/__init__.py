@@ -692,10 +692,14 @@ def _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, dtype) -> tuple:
     width = tshape[1]
     if width > 1 and entry != 1:
         raise ValueError("the entries of a row must adjoin in block_table")
+    if B <= 1 or width == 0:
+        row = width                                   # no other row to step to
+    elif row < width:
+        raise ValueError("the rows of block_table overlap (one row seen as many, say): they must lie apart")
     if kv_lens.dtype != torch.int32 or kv_lens.shape != (B,) or not kv_lens.is_contiguous():
         raise ValueError(f"kv_lens must be a contiguous int32 [{B}] tensor")
     return (k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], shape[0], shape[2],
-            block_table.data_ptr(), row if B > 1 and row > width else width, width, kv_lens.data_ptr())
+            block_table.data_ptr(), row, width, kv_lens.data_ptr())
 
 
 def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -707,7 +711,7 @@ def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     inv_freq is given, and returns the rotated queries [B, H, T, d] when q is.  kv_lens (int32 [B])
     counts the new tokens already; q_lens (int32 [B]) says how many of the T are real (default all).
     k_cache, v_cache: [n_pages, Hkv, page_size, d], any strides whose last axis adjoins;
-    block_table: int32 [B, max_pages]."""
+    block_table: int32 [B, max_pages], rows that lie apart."""
     dev = _current_device(k)
     if (dev < 0 or v.get_device() != dev or k_cache.get_device() != dev or v_cache.get_device() != dev
             or block_table.get_device() != dev or kv_lens.get_device() != dev
