@@ -132,12 +132,15 @@ fa_status fa_append_paged(const fa_paged_cache* cache, const void* k, const int6
                           const int64_t v_strides[3], const void* q, const int64_t q_strides[3], void* q_out,
                           int B, int H, int Hkv, int T, int d, const int32_t* q_lens, const double* inv_freq,
                           int rotary_dim, int interleaved, float mscale, fa_dtype dtype, void* stream) {
+  // without queries the number of their heads does not matter; with some there have to be heads
+  if (H < 0 || (q != nullptr && H == 0 && Hkv > 0)) return FA_ERR_INVALID_ARG;
+  if (q == nullptr) H = Hkv;
   fa_status st = check_sizes(B, H, Hkv, T, d);
   if (st != FA_OK) return st;
   if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
   st = check_rotation(inv_freq, rotary_dim, mscale, d);
   if (st != FA_OK) return st;
-  if (B == 0 || H == 0 || T == 0) return FA_OK;
+  if (B == 0 || Hkv == 0 || T == 0) return FA_OK;
   st = check_cache(cache, Hkv);
   if (st != FA_OK) return st;
   // the pages are written

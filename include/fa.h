@@ -447,9 +447,9 @@ typedef struct {
  *   k, v   : [B, Hkv, T, d], q (nullable): [B, H, T, d], strided as in fa_rotary
  *   q_out  : [B, H, T, d] contiguous; may be q when q is contiguous
  *   the cache's keys and values must not share memory, and no two slots either
- * bf16 or fp16.  Hkv divides H.  The lengths and the table live on the device and are checked
- * there: a length beyond max_pages * page_size, or an entry outside [0, n_pages), is not followed
- * and fa_check_device_status then returns FA_ERR_INVALID_ARG.
+ * bf16 or fp16.  Hkv divides H, which is not looked at when q is null.  The lengths and the table
+ * live on the device and are checked there: a length beyond max_pages * page_size, or an entry
+ * outside [0, n_pages), is not followed and fa_check_device_status then returns FA_ERR_INVALID_ARG.
  */
 fa_status fa_append_paged(const fa_paged_cache* cache, const void* k, const int64_t k_strides[3],
                           const void* v, const int64_t v_strides[3], const void* q,
