@@ -454,9 +454,13 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
 #pragma unroll
             for (int e = 0; e < 32; ++e) p[hc * 32 + e] = __uint_as_float(raw[hc][e]);
           }
-          if (kind == kPartial && !key_ok) {         // no key: does not choose the form of the tanh
+          if ((kMod & kModCap) != 0 && kind == kPartial) {
+            // what is masked, or no key, does not choose the form of the tanh for the others
+            const int hidden = !key_ok ? kCols : !g.causal || key < g.prefix ? 0 : key - q0;   // leading queries
+            if (__any_sync(0xffffffffu, hidden > 0) && __any_sync(0xffffffffu, hidden < kCols)) {
 #pragma unroll
-            for (int e = 0; e < kCols; ++e) p[e] = 0.f;
+              for (int e = 0; e < kCols; ++e) p[e] = e < hidden ? 0.f : p[e];
+            }
           }
           uint32_t pk[kCols / 2];
           const int lo = i * BM - (g.k0 + BN - 1), hi = lo + BM + BN - 2;      // of i - j in the tile

@@ -384,9 +384,13 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
 #pragma unroll
             for (int e = 0; e < 32; ++e) p[hc * 32 + e] = __uint_as_float(raw[hc][e]);
           }
-          if (g.q0 + BM > g.N && q >= g.N) {         // no row: does not choose the form of the tanh
+          if ((kMod & kModCap) != 0 && (kind == kPartial || g.q0 + BM > g.N)) {
+            // what is masked, or no row, does not choose the form of the tanh for the others
+            const int lim = q < g.N ? seen - k0 : 0;
+            if (__any_sync(0xffffffffu, lim < kCols) && __any_sync(0xffffffffu, lim > 0)) {
 #pragma unroll
-            for (int e = 0; e < kCols; ++e) p[e] = 0.f;
+              for (int e = 0; e < kCols; ++e) p[e] = e < lim ? p[e] : 0.f;
+            }
           }
           const int lo = j * BN - (g.q0 + BM - 1), hi = lo + BM + BN - 2;      // of j - i in the tile
           const Bias bi = make_bias(slope, k0 - q, lo, a.causal && g.prefix == 0 ? min(hi, 0) : hi);
