@@ -247,17 +247,12 @@ delta_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         const Bias bi = make_bias(slope, c0 - i, lo, a.causal && prefix == 0 ? min(hi, 0) : hi);
         with_score<kMod>(p, a.score, F16 ? a.score.poly_limit : a.score.low_limit, bi, [&](auto cap, auto bias) {
           constexpr int kCap = decltype(cap)::value, kBias = decltype(bias)::value;
-          const float first = kBias == kBiasLinear ? nl + bi.base : nl;
-          const float2 first2 = make_float2(first, first);
 #pragma unroll
           for (int col = 0; col < BN; col += 2) {
             float2 x = make_float2(p[col], p[col + 1]);
             if constexpr (kCap != kCapNone) x = tanh_of<kCap, F16>(x, a.score);
-            x = ptx::fma2(x, m2, first2);
-            if constexpr (kBias != kBiasNone) {
-              x.x = biased<kBias>(x.x, bi, col);
-              x.y = biased<kBias>(x.y, bi, col + 1);
-            }
+            x = ptx::fma2(x, m2, nl2);
+            if constexpr (kBias != kBiasNone) x = biased<kBias>(x, bi, col);
             p[col] = ptx::ex2(x.x);
             p[col + 1] = ptx::ex2(x.y);
           }

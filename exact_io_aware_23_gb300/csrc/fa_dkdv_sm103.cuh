@@ -468,17 +468,12 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
           const float2 m2 = (kMod & kModCap) == 0 ? c2 : make_float2(a.score.cap_log2, a.score.cap_log2);
           with_score<kMod>(p, a.score, F16 ? a.score.poly_limit : a.score.low_limit, bi, [&](auto cap, auto bias) {
             constexpr int kCap = decltype(cap)::value, kBias = decltype(bias)::value;
-            const float base = kBias == kBiasLinear ? bi.base : 0.f;
 #pragma unroll
             for (int col = 0; col < kCols; col += 2) {
               float2 t = make_float2(p[col], p[col + 1]);
               if constexpr (kCap != kCapNone) t = tanh_of<kCap, F16>(t, a.score);
               float2 x = ptx::fma2(t, m2, *reinterpret_cast<const float2*>(lse2 + col));
-              if constexpr (kBias == kBiasLinear) x = ptx::add2(x, make_float2(base, base));
-              if constexpr (kBias != kBiasNone) {
-                x.x = biased<kBias>(x.x, bi, col);
-                x.y = biased<kBias>(x.y, bi, col + 1);
-              }
+              if constexpr (kBias != kBiasNone) x = biased<kBias>(x, bi, col);
               float2 v = make_float2(ptx::ex2(x.x), ptx::ex2(x.y)), w = v;
               // what dS takes: P times the cap's derivative 1 - tanh^2
               if constexpr (kCap != kCapNone)

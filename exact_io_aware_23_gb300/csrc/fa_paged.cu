@@ -487,12 +487,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
         for (int e = 0; e < kKeys / 2; ++e) s[e] = a.score.cap_log2 * tanh_one(s[e], a.score);
       }
       if (a.score.slopes != nullptr) {
-        float base[2];                                  // -slope * distance at the tile's first key of the lane
+        float ahead[2];                                 // minus the distance at the lane's first key, exact
 #pragma unroll
-        for (int e = 0; e < 2; ++e) base[e] = slope[e] * (float)(key0 + c0 - (limit[e] - 1));
+        for (int e = 0; e < 2; ++e) ahead[e] = (float)(key0 + c0 - (limit[e] - 1));
 #pragma unroll
         for (int e = 0; e < kKeys / 2; ++e)
-          s[e] = fmaf(slope[(e >> 1) & 1], (float)((e >> 2) * 8 + (e & 1)), s[e] + base[(e >> 1) & 1]);
+          s[e] = fmaf(slope[(e >> 1) & 1], ahead[(e >> 1) & 1] + (float)((e >> 2) * 8 + (e & 1)), s[e]);
       }
       if (key0 + kKeys > full) {                        // some row does not see all of the tile
 #pragma unroll

@@ -117,21 +117,29 @@ __device__ __forceinline__ float2 tanh_of(float2 s, const ScoreArgs& k) {
   else return ptx::mul2(poly2(ptx::mul2(s, s), k.poly_low), s);
 }
 // The bias -slope |i - j| over one thread's row (or column) of a tile, whose distances run on by one:
-// at score e it is base + e * step where the tile lies on one side of the diagonal (or the other
-// side is masked), and -slope * |first + e| where it crosses it.  `first` is j - i, or i - j, at the
-// first score; lo and hi bound it over the unmasked part of the whole tile.
+// at score e it is step * (first + e) where the tile lies on one side of the diagonal (or the other
+// side is masked), and step * |first + e| where it crosses it.  `first` is j - i, or i - j, at the
+// first score; lo and hi bound it over the unmasked part of the whole tile.  The distance is exact
+// before it meets the slope: step * first taken out of the row would round at up to 127 steps, and a
+// slope of 1000 move the scores next to the diagonal by 0.01.
 struct Bias {
-  float base, step, first, minus_slope;
+  float first, step;
   bool crosses;
 };
 __device__ __forceinline__ Bias make_bias(float slope, int first, int lo, int hi) {
-  const float s = lo >= 0 ? -slope : slope;
-  return Bias{s * (float)first, s, (float)first, -slope, lo < 0 && hi > 0};
+  return Bias{(float)first, lo < 0 && hi <= 0 ? slope : -slope, lo < 0 && hi > 0};
 }
+// Scores e and e + 1 (e even and a constant) with their bias.  The first 16 scores' distances are
+// single additions, the others' run on from them in pairs: one packed addition for two scores.
+// (Single additions throughout: forward of B1 H16 Hkv4 N8192 d128 causal with cap and bias 382 us
+// against 364, backward 1045 against 1030.)
 template <int kBias>
-__device__ __forceinline__ float biased(float x, const Bias& b, int e) {
-  if constexpr (kBias == kBiasLinear) return fmaf(b.step, (float)e, x);        // the base is in x already
-  else return fmaf(b.minus_slope, fabsf(b.first + (float)e), x);
+__device__ __forceinline__ float2 biased(float2 x, const Bias& b, int e) {
+  float2 d = make_float2(b.first + (float)(e & 14), b.first + (float)((e & 14) + 1));
+#pragma unroll
+  for (int i = 16; i <= e; i += 16) d = ptx::add2(d, make_float2(16.f, 16.f));
+  if constexpr (kBias == kBiasAbs) d = make_float2(fabsf(d.x), fabsf(d.y));
+  return ptx::fma2(d, make_float2(b.step, b.step), x);
 }
 
 // What a call modifies, as the backward's kernels are compiled for it: one kernel for all kinds keeps
@@ -170,18 +178,15 @@ __device__ __forceinline__ void score_row(float (&s)[N], const ScoreArgs& k, flo
   auto body = [&](auto cap, auto bias) {
     constexpr int kCap = decltype(cap)::value, kBias = decltype(bias)::value;
     const float m = kCap == kCapNone ? c : kCap == kCapPoly ? 1.f : -2.f * k.cap_log2;
-    const float a = (kBias == kBiasLinear ? b.base : 0.f) + (kCap == kCapExp ? k.cap_log2 : 0.f);
+    const float a = kCap == kCapExp ? k.cap_log2 : 0.f;
     const float2 m2 = make_float2(m, m), a2 = make_float2(a, a);
 #pragma unroll
     for (int e = 0; e < N; e += 2) {
       float2 x = make_float2(s[e], s[e + 1]);
-      if constexpr (kCap == kCapPoly) x = ptx::fma2(poly2(ptx::mul2(x, x), k.capped), x, a2);
+      if constexpr (kCap == kCapPoly) x = ptx::mul2(poly2(ptx::mul2(x, x), k.capped), x);
       else if constexpr (kCap == kCapExp) x = ptx::fma2(logistic(x, k), m2, a2);
-      else x = ptx::fma2(x, m2, a2);
-      if constexpr (kBias != kBiasNone) {
-        x.x = biased<kBias>(x.x, b, e);
-        x.y = biased<kBias>(x.y, b, e + 1);
-      }
+      else x = ptx::mul2(x, m2);
+      if constexpr (kBias != kBiasNone) x = biased<kBias>(x, b, e);
       s[e] = x.x;
       s[e + 1] = x.y;
     }
