@@ -803,6 +803,13 @@ def _given(name: str, t: torch.Tensor, shape, dtype) -> None:
         raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor")
 
 
+def _workspace_bytes(t: torch.Tensor) -> int:
+    """The bytes of a workspace that the caller gives: its elements adjoin, so its size is its memory's."""
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.numel() * t.element_size()
+
+
 def _kv_lens(kv_lens, B, dev, q):
     """The key lengths where and as the library takes them, and the copy made for that (or None), which
     is memory allocated here like an output."""
@@ -875,7 +882,7 @@ def _backward_scored(q, k, v, o, lse, do, causal, scale, kv_lens, dq, dk, dv, wo
     st = lib.fa_backward_scored_packed(_SCORED.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
         dk.data_ptr(), dv.data_ptr(), 0 if kv_lens is None else kv_lens.data_ptr(), 0, slopes, prefix,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        workspace.data_ptr(), _workspace_bytes(workspace),
         _handle(stream, dev, dq_new, dk_new, dv_new, ws_new, kv_new),
         B, H, Hkv, N, 0, d, 1 if causal else 0, _DTYPES[dtype], 1.0 / d ** 0.5 if scale is None else scale, softcap))
     if st != FA_OK:
@@ -938,7 +945,7 @@ def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     st = lib.fa_forward_paged_packed(_PAGED.pack(
         *cache, q.data_ptr(), o.data_ptr(), lse.data_ptr(), 0 if q_lens is None else q_lens.data_ptr(),
         0 if alibi_slopes is None else alibi_slopes.data_ptr(), 0 if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _handle(stream, dev, o_new, lse_new, ws_new),
+        0 if workspace is None else _workspace_bytes(workspace), _handle(stream, dev, o_new, lse_new, ws_new),
         B, H, Hkv, T, d, _DTYPES[dtype], 1.0 / d ** 0.5 if scale is None else scale, softcap))
     if st != FA_OK:
         raise FaError(st, "fa_forward_paged")

@@ -48,6 +48,15 @@ def test_keys_are_written_without_query_heads():
     assert append(c(), q=None, q_out=None, H=-1) == INVALID
 
 
+def test_a_workspace_counts_the_memory_it_has():
+    """One byte seen as many is no workspace of many bytes."""
+    w = torch.empty(64, dtype=torch.int32)
+    assert fa._workspace_bytes(w) == 256
+    for bad in (w[:1].expand(1 << 20), w[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            fa._workspace_bytes(bad)
+
+
 @pytest.mark.gpu
 def test_keys_without_queries_reach_the_cache():
     """The library's call with no query heads at all writes what the call with queries does."""
