@@ -79,8 +79,11 @@ struct Bars {             // at most 256 bytes (the live-tile bitmap follows)
   uint64_t vec_empty[2];
   uint64_t s_full[2];     // S^T(n) in TMEM: barrier n & 1, phase n >> 1
   uint64_t dp_full;
-  uint64_t p_ready;
-  uint64_t ds_ready;
+  // P^T(n) in TMEM: barrier n & 1, phase n >> 1.  With two S^T buffers a warp may be done with
+  // P^T(n + 1) before another is with P^T(n) (S^T(n + 1) and dP^T(n) wait for neither); on one
+  // barrier its second arrival would stand in for the other's first, and dV would be fed scores.
+  uint64_t p_ready[2];
+  uint64_t ds_ready;      // dS^T(n): no warp gets past dP^T(n + 1), which is issued after all arrived
   uint64_t acc_done;
   uint64_t tail;          // scored variant: a head's last Q and dO tile, before their rows behind
                           // the sequence are cleared (phase = the head's number in its group)
@@ -191,7 +194,8 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
     ptx::mbar_init(ptx::smem_u32(&bars->s_full[0]), 1);
     ptx::mbar_init(ptx::smem_u32(&bars->s_full[1]), 1);
     ptx::mbar_init(ptx::smem_u32(&bars->dp_full), 1);
-    ptx::mbar_init(ptx::smem_u32(&bars->p_ready), L::kComputeWarps);
+    ptx::mbar_init(ptx::smem_u32(&bars->p_ready[0]), L::kComputeWarps);
+    ptx::mbar_init(ptx::smem_u32(&bars->p_ready[1]), L::kComputeWarps);
     ptx::mbar_init(ptx::smem_u32(&bars->ds_ready), L::kComputeWarps);
     ptx::mbar_init(ptx::smem_u32(&bars->acc_done), 1);
     if constexpr (kScore) ptx::mbar_init(ptx::smem_u32(&bars->tail), 1);
@@ -367,7 +371,7 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
             ok = next_st();
             if (!ok) break;
           }
-          ok = ptx::mbar_wait(ptx::smem_u32(&bars->p_ready), (uint32_t)n & 1u, lim_ms, a.err);
+          ok = ptx::mbar_wait(ptx::smem_u32(&bars->p_ready[n & 1]), (uint32_t)(n >> 1) & 1u, lim_ms, a.err);
           if (!ok) break;
           ptx::tc_fence_after();
           acc_mma(C::kDV, C::x_col(n), sbase + C::kO + os * C::kTile, n == 0);
@@ -535,7 +539,7 @@ __device__ __forceinline__ void run(const int unit, const CUtensorMap& tmQ, cons
       }
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->p_ready));
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->p_ready[n & 1]));
       ok = ptx::mbar_wait(ptx::smem_u32(&bars->dp_full), (uint32_t)n & 1u, lim_ms, a.err);
       if (!ok) break;
       ptx::tc_fence_after();
