@@ -6,8 +6,8 @@
 // heads (and T new tokens) of its group; the two products are 4 * G * T flops a value, far below
 // the tensor cores' share even with the rows padded to the 16 of one mma.  (So the warps feed
 // mma.sync from shared memory themselves; a 128-row tile of the fifth-generation cores would be
-// nearly all padding.)  Measured: B2 H32 Hkv8 d128 with 100K and 128K keys, 0.95 GB: 160 us, 6.4 TB/s,
-// 0.96 of the copy rate; 64 sequences of 1 to 8192 keys, 1.0 GB: 160 us; 16 sequences of up to 4000
+// nearly all padding.)  Measured: B2 H32 Hkv8 d128 with 119K and 131K keys, 1.03 GB: 160 us, 6.4 TB/s,
+// 0.96 of the copy rate; 64 sequences of 1 to 8192 keys, 1.02 GB: 161 us; 16 sequences of up to 4000
 // keys at d = 64, five drafted tokens: 37 us, 4.1 TB/s (there the warps' own work shows).
 //
 // Work.  The cache of every (sequence, key head, block of 16 query rows), a segment, is cut into tiles

@@ -10,9 +10,12 @@
 // The angle.  t * inv_freq in 32 bits loses the angle of far positions (at t = 10^6 the product
 // is off by up to 0.03 rad), and 64-bit floating-point products run at a fiftieth of the 32-bit
 // rate here.  Only the fraction of a turn matters, so each thread turns its frequencies once into
-// 64-bit fixed point, F = inv_freq / (2 pi) * 2^64 mod 2^64; the product t * F then wraps modulo
-// one turn by itself, and its upper 32 bits are the angle to 2^-32 turns.  F is exact to 2^-63
-// turns a position, so a position of 2^31 still has an angle good to 2^-32 turns.
+// 64-bit fixed point, F = inv_freq / (2 pi) * 2^64 mod 2^64 (the long product with the digits of
+// 1 / (2 pi) is Payne and Hanek's reduction); the product t * F then wraps modulo one turn by itself,
+// and its upper 32 bits are the angle to 2^-32 turns.  F is exact to 2^-63 turns a position, so a
+// position of 2^31 still has an angle good to 2^-32 turns.  The sine takes it in fp32, whose 24 bits
+// move it by up to 2^-26 turns (pi 2^-25), as much as the rounding of the sine itself: 16-bit
+// results do not see that, fp32 ones have 1.3 times the error of sines taken in 64 bits.
 //
 // Layout.  A thread holds one unit of a token's heads: 8 pairs, the 16 values they occupy (two
 // 16-byte loads in either pairing of a 16-bit type), and walks over heads with the sines and

@@ -351,7 +351,7 @@ fa_status fa_backward_fused(const void* q, const void* k, const void* v, const v
  */
 typedef struct {
   float softcap;               /* 0: no cap; otherwise finite and > 0 */
-  const float* alibi_slopes;   /* nullable; device fp32 [H], finite */
+  const float* alibi_slopes;   /* nullable; device fp32 [H], finite, of either sign */
   const int32_t* prefix_lens;  /* nullable; device int32 [B] (packed: [n_seqs]): the first keys of a
                                   sequence, seen by all its queries in spite of `causal`; values
                                   below 0 count as 0, values past the end as the whole sequence */
@@ -469,10 +469,11 @@ fa_status fa_append_paged(const fa_paged_cache* cache, const void* k, const int6
  *            aligned, caller-owned, contents on entry irrelevant; calls in flight at once need their
  *            own.  The size is 0 for a few short sequences, which need none (workspace may be null).
  * The cache is split over its length among all SMs and joined in a fixed order: the same bits on
- * every call.  Nothing that a page holds behind a sequence's last token enters the result.  bf16 or
- * fp16.  Lengths and table entries outside their contract as in fa_append_paged (such a sequence's
- * result is then unspecified).  The work is sized for few new tokens: every 16 query rows of a
- * group (H / Hkv * T) read the cache once more.
+ * every call.  Nothing that a page holds behind a sequence's last token enters the result; NaN in a
+ * query, or in a key that it sees, makes its row of O and its LSE NaN.  bf16 or fp16.  Lengths and
+ * table entries outside their contract as in fa_append_paged (such a sequence's result is then
+ * unspecified).  The work is sized for few new tokens: every 16 query rows of a group (H / Hkv * T)
+ * read the cache once more.
  */
 size_t fa_forward_paged_workspace_size(int B, int H, int Hkv, int T, int d, int max_keys);
 fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, float* lse, int B,
@@ -482,7 +483,8 @@ fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, 
 
 /*
  * These calls with their arguments in one structure, fields as the parameters above.  For callers
- * behind a foreign-function interface, which converts one argument then instead of up to 21.
+ * behind a foreign-function interface, which converts one argument then instead of up to 21.  (It is
+ * the arguments that are packed: the sequences are where cu_seqlens is set.)
  */
 typedef struct {
   const void *q, *k, *v;

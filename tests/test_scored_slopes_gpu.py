@@ -1,5 +1,6 @@
-"""Distance biases on the GPU whose slopes are negative or of both signs, against 64-bit formulas.  The bounds of scored_reference.py take a slope by its size: `_signed_scores` gives a
-negative one that error too."""
+"""Distance biases on the GPU whose slopes are negative or of both signs, against 64-bit formulas.  The
+bounds of scored_reference.py take a slope by its size: `_signed_scores` gives a negative one that
+error too."""
 import pytest
 import torch
 
