@@ -20,7 +20,8 @@ import torch
 __all__ = ["forward", "forward_splitkv", "backward", "backward_noalloc", "backward_workspace_size",
            "backward_fused_workspace_size", "check_device_status", "set_fault_injection",
            "set_wait_limit_ms", "FaError", "LIB_PATH", "lib", "rotary", "rotary_backward",
-           "rotary_frequencies", "append_paged", "forward_paged", "forward_paged_workspace_size"]
+           "rotary_frequencies", "append_paged", "forward_paged", "forward_paged_workspace_size",
+           "select_pages", "select_pages_workspace_size", "assign_pages"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa.so")
 
@@ -48,6 +49,12 @@ class FaPagedCache(ctypes.Structure):
                 ("page_size", ctypes.c_int), ("block_table", ctypes.c_void_p),
                 ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int),
                 ("kv_lens", ctypes.c_void_p)]
+
+
+class FaPageStore(ctypes.Structure):
+    """fa_page_store: the pages' format, their scales and the bounds of their keys."""
+    _fields_ = [("format", ctypes.c_int), ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("k_bounds", ctypes.c_void_p), ("bound_scales", ctypes.c_void_p)]
 
 
 class FaError(RuntimeError):
@@ -142,7 +149,22 @@ def _load() -> ctypes.CDLL:
     L.fa_forward_paged_workspace_size.restype = sz
     L.fa_forward_paged.argtypes = [vp, cp, vp, vp, i, i, i, i, i, f, vp, mp, i, vp, sz, vp]
     L.fa_forward_paged.restype = i
-    for packed in (L.fa_forward_scored_packed, L.fa_backward_scored_packed, L.fa_rotary_packed,
+    fp = ctypes.POINTER(FaPageStore)
+    L.fa_append_paged_store.argtypes = [cp, fp, vp, st3, vp, st3, vp, st3, vp, i, i, i, i, i, vp, vp, i, i, f, i, vp]
+    L.fa_append_paged_store.restype = i
+    L.fa_forward_paged_store.argtypes = [vp, cp, fp, vp, i, vp, vp, i, i, i, i, i, f, vp, mp, i, vp, sz, vp]
+    L.fa_forward_paged_store.restype = i
+    L.fa_select_pages_workspace_size.argtypes = [i, i, i]
+    L.fa_select_pages_workspace_size.restype = sz
+    L.fa_select_pages.argtypes = [vp, cp, fp, vp, i, i, i, i, i, vp, i, i, i, i, vp, sz, vp]
+    L.fa_select_pages.restype = i
+    L.fa_assign_pages.argtypes = [vp, i64, i, i, i, vp, vp, vp, i, vp, vp, vp, vp, vp, vp, i, vp]
+    L.fa_assign_pages.restype = i
+    L.fa_append_paged_store_packed.argtypes = [ctypes.c_char_p, ctypes.c_char_p]
+    L.fa_append_paged_store_packed.restype = i
+    L.fa_forward_paged_store_packed.argtypes = [ctypes.c_char_p, ctypes.c_char_p, vp, i]
+    L.fa_forward_paged_store_packed.restype = i
+    for packed in (L.fa_select_pages_packed, L.fa_assign_pages_packed, L.fa_forward_scored_packed, L.fa_backward_scored_packed, L.fa_rotary_packed,
                    L.fa_rotary_backward_packed, L.fa_append_paged_packed, L.fa_forward_paged_packed):
         packed.argtypes = [ctypes.c_char_p]
         packed.restype = i
@@ -511,7 +533,11 @@ _SCORED = struct.Struct("14PNP8iff")                              # fa_scored_ca
 _ROTARY = struct.Struct("PPPPP7q7if")                             # fa_rotary_call
 _APPEND = struct.Struct(_CACHE_FORMAT + "7P9q8if0q")              # fa_append_paged_call
 _PAGED = struct.Struct(_CACHE_FORMAT + "6PNP6iff")                # fa_forward_paged_call
+_STORE = struct.Struct("iPPPP")                                   # fa_page_store
+_SELECT = struct.Struct(_CACHE_FORMAT + "iPPPP" + "4PNP9i0q")     # fa_select_pages_call
+_ASSIGN = struct.Struct("Pq10P5i0q")                              # fa_assign_pages_call
 _16_BIT = (torch.bfloat16, torch.float16)
+_PAGE_FORMATS = {torch.float8_e4m3fn: 1, torch.int8: 2}           # fa_page_format; 0: the queries' type
 # of PyTorch's module for CUDA, without the wrappers around them (absent from builds without CUDA)
 _device, _raw_stream = (getattr(torch._C, name, None) for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
 
@@ -685,6 +711,13 @@ def _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, dtype) -> tuple:
         raise ValueError("the values of a head must adjoin in k_cache")
     if v_cache.shape != shape or v_cache.stride() != strides:
         raise ValueError("k_cache and v_cache must have the same shape and strides")
+    table, row, width, lens = _table(block_table, kv_lens, B)
+    return (k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], shape[0], shape[2],
+            table, row, width, lens)
+
+
+def _table(block_table, kv_lens, B) -> Tuple[int, int, int, int]:
+    """Checks a block table and the lengths that go with it: its address, row stride and width, theirs."""
     tshape = block_table.shape
     if block_table.dtype != torch.int32 or len(tshape) != 2 or tshape[0] != B:
         raise ValueError(f"block_table must be int32 [{B}, max_pages]")
@@ -698,20 +731,64 @@ def _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, dtype) -> tuple:
         raise ValueError("the rows of block_table overlap (one row seen as many, say): they must lie apart")
     if kv_lens.dtype != torch.int32 or kv_lens.shape != (B,) or not kv_lens.is_contiguous():
         raise ValueError(f"kv_lens must be a contiguous int32 [{B}] tensor")
-    return (k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], shape[0], shape[2],
-            block_table.data_ptr(), row, width, kv_lens.data_ptr())
+    return block_table.data_ptr(), row, width, kv_lens.data_ptr()
+
+
+def _scales(name: str, t: Optional[torch.Tensor], dev: int, shape) -> int:
+    if t is None:
+        raise ValueError(f"8-bit pages (and bounds) need {name}")
+    if t.get_device() != dev:
+        _refuse_place(**{name: t})
+    if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 {list(shape)} tensor")
+    return t.data_ptr()
+
+
+def _bounds(k_bounds, bound_scales, dev: int, n_pages: int, Hkv: int, d: int) -> Tuple[int, int]:
+    if k_bounds.get_device() != dev:
+        _refuse_place(k_bounds=k_bounds)
+    if k_bounds.dtype != torch.int8 or k_bounds.shape != (n_pages, Hkv, 2, d) or not k_bounds.is_contiguous():
+        raise ValueError(f"k_bounds must be a contiguous int8 [{n_pages}, {Hkv}, 2, {d}] tensor")
+    return k_bounds.data_ptr(), _scales("bound_scales", bound_scales, dev, (n_pages, Hkv))
+
+
+def _store(k_cache, k_scales, v_scales, k_bounds, bound_scales, dtype, dev: int, Hkv: int, d: int):
+    """The type of the pages' elements, and fa_page_store's fields (None: 16-bit pages without bounds)."""
+    fmt = _PAGE_FORMATS.get(k_cache.dtype, 0)
+    if fmt == 0:
+        if k_scales is not None or v_scales is not None:
+            raise ValueError("16-bit pages have no scales")
+        if k_bounds is None and bound_scales is None:
+            return dtype, None
+        ks = vs = 0
+    else:
+        n_pages = k_cache.shape[0]
+        ks, vs = _scales("k_scales", k_scales, dev, (n_pages, Hkv)), _scales("v_scales", v_scales, dev, (n_pages, Hkv))
+        dtype = k_cache.dtype
+    kb = bs = 0
+    if k_bounds is not None:
+        kb, bs = _bounds(k_bounds, bound_scales, dev, k_cache.shape[0], Hkv, d)
+    elif bound_scales is not None:
+        raise ValueError("bound_scales without k_bounds")
+    return dtype, (fmt, ks, vs, kb, bs)
 
 
 def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                  block_table: torch.Tensor, kv_lens: torch.Tensor, *, q: Optional[torch.Tensor] = None,
                  q_lens: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None,
                  interleaved: bool = False, mscale: float = 1.0, q_out: Optional[torch.Tensor] = None,
+                 k_scales: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None,
+                 k_bounds: Optional[torch.Tensor] = None, bound_scales: Optional[torch.Tensor] = None,
                  stream=None) -> Optional[torch.Tensor]:
     """fa_append_paged: writes new tokens k, v [B, Hkv, T, d] into the pages, keys rotated when
     inv_freq is given, and returns the rotated queries [B, H, T, d] when q is.  kv_lens (int32 [B])
     counts the new tokens already; q_lens (int32 [B]) says how many of the T are real (default all).
     k_cache, v_cache: [n_pages, Hkv, page_size, d], any strides whose last axis adjoins;
-    block_table: int32 [B, max_pages], rows that lie apart."""
+    block_table: int32 [B, max_pages], rows that lie apart.
+    The pages are of k's type, or int8 or float8_e4m3fn with k_scales and v_scales (float32 [n_pages, Hkv],
+    a power of two for each page and head, written too; what they hold of pages without tokens does not
+    matter).  k_bounds (int8 [n_pages, Hkv, 2, d]) and bound_scales (float32 [n_pages, Hkv]): bounds of
+    each page's keys for ``select_pages``, kept when given (fa_append_paged_store)."""
     dev = _current_device(k)
     if (dev < 0 or v.get_device() != dev or k_cache.get_device() != dev or v_cache.get_device() != dev
             or block_table.get_device() != dev or kv_lens.get_device() != dev
@@ -725,7 +802,10 @@ def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     if v.shape != shape or v.dtype != dtype:
         raise ValueError("v must have k's shape and type")
     B, Hkv, T, d = shape
-    cache = _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, dtype)
+    pages, store = _store(k_cache, k_scales, v_scales, k_bounds, bound_scales, dtype, dev, Hkv, d)
+    cache = _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, pages)
+    if store is not None and store[0] and abs(store[1] - store[2]) < 4 * cache[5] * Hkv:
+        raise ValueError("k_scales and v_scales overlap")
     rot = _rotated(inv_freq)
     if q_lens is not None:
         _int32("q_lens", q_lens, (B,))
@@ -751,10 +831,11 @@ def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
         raise ValueError("q_out without q")
     if s is None:
         s = _handle(stream, dev)
-    st = lib.fa_append_paged_packed(_APPEND.pack(
+    call = _APPEND.pack(
         *cache, k.data_ptr(), v.data_ptr(), 0 if q is None else q.data_ptr(), 0 if q_out is None else q_out.data_ptr(),
         0 if q_lens is None else q_lens.data_ptr(), 0 if inv_freq is None else inv_freq.data_ptr(), s,
-        *_strides("k", k), *_strides("v", v), *qs, B, H, Hkv, T, d, rot, 1 if interleaved else 0, _DTYPES[dtype], mscale))
+        *_strides("k", k), *_strides("v", v), *qs, B, H, Hkv, T, d, rot, 1 if interleaved else 0, _DTYPES[dtype], mscale)
+    st = lib.fa_append_paged_packed(call) if store is None else lib.fa_append_paged_store_packed(call, _STORE.pack(*store))
     if st != FA_OK:
         raise FaError(st, "fa_append_paged")
     return q_out
@@ -895,12 +976,15 @@ def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                   q_lens: Optional[torch.Tensor] = None, softcap: float = 0.0,
                   alibi_slopes: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
                   lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                  stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+                  k_scales: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None,
+                  pages: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """O, LSE of T new tokens per sequence over a paged cache that holds them (fa_forward_paged).
     q: [B, H, T, d] contiguous, bf16 or fp16; the cache, block_table, kv_lens and q_lens as in
     ``append_paged``.  Token t of a sequence's n new ones sees the keys up to its own place
     kv_lens - n + t; scores capped by softcap * tanh(. / softcap) when softcap > 0 and lowered by
-    alibi_slopes[h] (fp32 [H]) times the distance."""
+    alibi_slopes[h] (fp32 [H]) times the distance.
+    k_scales, v_scales: of int8 or float8_e4m3fn pages.  pages (int32 [B, Hkv, n]): only these pages are seen,
+    by their number in the sequence, -1 for none (``select_pages``; fa_forward_paged_store)."""
     dev = _current_device(q)
     if (dev < 0 or k_cache.get_device() != dev or v_cache.get_device() != dev
             or block_table.get_device() != dev or kv_lens.get_device() != dev
@@ -915,7 +999,17 @@ def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     Hkv = k_cache.shape[1] if k_cache.dim() == 4 else 0
     if Hkv == 0 or H % Hkv != 0:
         raise ValueError("k_cache must be [n_pages, Hkv, page_size, d] with Hkv dividing the query heads")
-    cache = _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, dtype)
+    page_type, store = _store(k_cache, k_scales, v_scales, None, None, dtype, dev, Hkv, d)
+    cache = _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, page_type)
+    span = cache[6] * cache[9]
+    picks = 0
+    if pages is not None:
+        if pages.get_device() != dev:
+            _refuse_place(pages=pages)
+        picks = pages.shape[2] if pages.dim() == 3 else 0
+        if picks == 0 or pages.shape != (B, Hkv, picks) or pages.dtype != torch.int32 or not pages.is_contiguous():
+            raise ValueError(f"pages must be a contiguous int32 [{B}, {Hkv}, n] tensor, n > 0")
+        span = min(span, cache[6] * picks)
     if q_lens is not None:
         _int32("q_lens", q_lens, (B,))
     if alibi_slopes is not None:
@@ -937,16 +1031,124 @@ def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
             raise ValueError("lse must be contiguous float32 [B, H, T]")
     ws_new = None
     if workspace is None:
-        need = _paged_workspace_size(dev, B, H, Hkv, T, d, min(cache[6] * cache[9], 0x7fffffff))
+        need = _paged_workspace_size(dev, B, H, Hkv, T, d, min(span, 0x7fffffff))
         if need > 0:
             workspace = ws_new = torch.empty((need,), dtype=torch.uint8, device=q.device)
     else:
         _refuse_place(workspace=workspace)
-    st = lib.fa_forward_paged_packed(_PAGED.pack(
+    call = _PAGED.pack(
         *cache, q.data_ptr(), o.data_ptr(), lse.data_ptr(), 0 if q_lens is None else q_lens.data_ptr(),
         0 if alibi_slopes is None else alibi_slopes.data_ptr(), 0 if workspace is None else workspace.data_ptr(),
         0 if workspace is None else _workspace_bytes(workspace), _handle(stream, dev, o_new, lse_new, ws_new),
-        B, H, Hkv, T, d, _DTYPES[dtype], 1.0 / d ** 0.5 if scale is None else scale, softcap))
+        B, H, Hkv, T, d, _DTYPES[dtype], 1.0 / d ** 0.5 if scale is None else scale, softcap)
+    if store is None and pages is None:
+        st = lib.fa_forward_paged_packed(call)
+    else:
+        st = lib.fa_forward_paged_store_packed(call, None if store is None else _STORE.pack(*store),
+                                               None if pages is None else pages.data_ptr(), picks)
     if st != FA_OK:
         raise FaError(st, "fa_forward_paged")
     return o, lse
+
+
+def select_pages_workspace_size(B: int, Hkv: int, max_pages: int) -> int:
+    """max_pages: entries of a block table's row."""
+    return int(lib.fa_select_pages_workspace_size(B, Hkv, max_pages))
+
+
+def select_pages(q: torch.Tensor, k_bounds: torch.Tensor, bound_scales: torch.Tensor, block_table: torch.Tensor,
+                 kv_lens: torch.Tensor, n_select: int, page_size: int, *, q_lens: Optional[torch.Tensor] = None,
+                 first: int = 1, last: int = 1, pages: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """fa_select_pages: for each sequence and key head the n_select pages whose key bounds promise the
+    highest scores to its new tokens q [B, H, T, d] (contiguous, bf16 or fp16; rotated like the keys),
+    the first and the last ones among them: int32 [B, Hkv, n_select], ascending, -1 behind.  k_bounds and
+    bound_scales as ``append_paged`` keeps them; block_table, kv_lens and q_lens as there."""
+    dev = _current_device(q)
+    if (dev < 0 or block_table.get_device() != dev or kv_lens.get_device() != dev
+            or (q_lens is not None and q_lens.get_device() != dev)):
+        _refuse_place(q=q, block_table=block_table, kv_lens=kv_lens, q_lens=q_lens)
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 4 or dtype not in _16_BIT or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 or fp16 [B, H, T, d] tensor")
+    B, H, T, d = shape
+    n_pages, Hkv = k_bounds.shape[:2] if k_bounds.dim() == 4 else (0, 0)
+    if Hkv == 0 or H % Hkv != 0:
+        raise ValueError("k_bounds must be [n_pages, Hkv, 2, d] with Hkv dividing the query heads")
+    kb, bs = _bounds(k_bounds, bound_scales, dev, n_pages, Hkv, d)
+    table, row, width, lens = _table(block_table, kv_lens, B)
+    if q_lens is not None:
+        _int32("q_lens", q_lens, (B,))
+    if n_select <= 0:
+        raise ValueError("n_select must be positive")
+    pages_new = ws_new = None
+    if pages is None:
+        pages = pages_new = torch.empty((B, Hkv, n_select), dtype=torch.int32, device=q.device)
+        if H == 0 or T == 0:
+            pages.fill_(-1)                               # no new tokens: nothing is launched
+    else:
+        _given("pages", pages, (B, Hkv, n_select), torch.int32)
+    if workspace is None:
+        if width > n_select:
+            workspace = ws_new = torch.empty((B * Hkv * width * 4 + 255 & -256,), dtype=torch.uint8, device=q.device)
+    else:
+        _refuse_place(workspace=workspace)
+    st = lib.fa_select_pages_packed(_SELECT.pack(
+        0, 0, 0, 0, 0, n_pages, page_size, table, row, width, lens, 0, 0, 0, kb, bs, q.data_ptr(), pages.data_ptr(),
+        0 if q_lens is None else q_lens.data_ptr(), 0 if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else _workspace_bytes(workspace), _handle(stream, dev, pages_new, ws_new),
+        B, H, Hkv, T, d, n_select, first, last, _DTYPES[dtype]))
+    if st != FA_OK:
+        raise FaError(st, "fa_select_pages")
+    return pages
+
+
+def assign_pages(block_table: torch.Tensor, old_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
+                 free_state: torch.Tensor, page_size: int, max_new: int = 0, *, lens: Optional[torch.Tensor] = None,
+                 q_lens: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                 positions: Optional[torch.Tensor] = None, state: Optional[torch.Tensor] = None,
+                 stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """fa_assign_pages: takes the sequences from old_lens to new_lens tokens (int32 [B]); pages they need come
+    from free_pages (int32, a ring with a place for every page; free_state int32 [2]: its first entry and
+    their number) into block_table [B, max_pages], pages they no longer need go back.  Returns
+    (lens, q_lens, slots, positions, state): the lengths now and the new tokens of each sequence (``kv_lens`` and
+    ``q_lens`` of the paged calls), slots (int64) and positions (int32) [B, max_new] of the first max_new of
+    them, -1 where there is none, and the ring's state.  All may be given; lens may be old_lens or new_lens,
+    and state free_state.  When the free pages do not suffice nothing changes (lens are old_lens then) and
+    ``check_device_status`` tells."""
+    dev = _current_device(old_lens)
+    if (dev < 0 or block_table.get_device() != dev or new_lens.get_device() != dev or free_pages.get_device() != dev
+            or free_state.get_device() != dev):
+        _refuse_place(block_table=block_table, old_lens=old_lens, new_lens=new_lens, free_pages=free_pages,
+                      free_state=free_state)
+    B = old_lens.shape[0] if old_lens.dim() == 1 else -1
+    table, row, width, old = _table(block_table, old_lens, B)
+    _int32("new_lens", new_lens, (B,))
+    _int32("free_state", free_state, (2,))
+    n_free = free_pages.numel()
+    _int32("free_pages", free_pages, (n_free,))
+    if max_new < 0:
+        raise ValueError("max_new must not be negative")
+    mine, outs = [], []
+    for name, t, shape, dtype in (("lens", lens, (B,), torch.int32), ("q_lens", q_lens, (B,), torch.int32),
+                                  ("slots", slots, (B, max_new), torch.int64),
+                                  ("positions", positions, (B, max_new), torch.int32), ("state", state, (2,), torch.int32)):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=old_lens.device)
+            mine.append(t)
+        else:
+            _given(name, t, shape, dtype)
+            # written tensors lie apart from one another and from what is read, but for the ones named
+            for other, x in (("block_table", block_table), ("free_pages", free_pages), *outs):
+                _apart(name, t, other, x, False)
+            for other, x in (("old_lens", old_lens), ("new_lens", new_lens), ("free_state", free_state)):
+                _apart(name, t, other, x, (name, other) in (("lens", "old_lens"), ("lens", "new_lens"), ("state", "free_state")))
+        outs.append((name, t))
+    lens, q_lens, slots, positions, state = (t for _, t in outs)
+    st = lib.fa_assign_pages_packed(_ASSIGN.pack(
+        table, row, old, new_lens.data_ptr(), free_pages.data_ptr(), free_state.data_ptr(), state.data_ptr(), lens.data_ptr(),
+        q_lens.data_ptr(), slots.data_ptr(), positions.data_ptr(), _handle(stream, dev, *mine), B, width, page_size, n_free,
+        max_new))
+    if st != FA_OK:
+        raise FaError(st, "fa_assign_pages")
+    return lens, q_lens, slots, positions, state

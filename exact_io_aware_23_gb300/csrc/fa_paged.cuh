@@ -59,8 +59,27 @@ struct AppendArgs {
   int* err;
 };
 
+// Pages of 8 bits, or with key bounds (see fa_page_store), and how the write's work is cut up.
+struct StoreArgs {
+  int store;                 // fa_page_format
+  float* k_scales;           // [n_pages, Hkv]
+  float* v_scales;
+  int8_t* bounds;            // null, or [n_pages, Hkv, 2, d]
+  float* bound_scales;
+  int span;                  // pages that a sequence's new tokens reach at most
+  int heads, head_blocks;    // of the 2 * Hkv key and value heads: a team's, and the teams of a page
+  int64_t page_blocks;       // blocks of teams; those behind them turn queries
+  int q_heads, q_head_blocks;
+};
+
 struct PagedArgs {
   PagedCache cache;
+  int store;                 // fa_page_format; of 8-bit pages also the scales [n_pages, Hkv]
+  const float* k_scales;
+  const float* v_scales;
+  const int32_t* pages;      // null: all pages; else [B, Hkv, picks] chosen ones
+  int picks;
+  int f16;                   // queries and outputs are fp16 (8-bit pages)
   const void* q;             // [B, H, T, d]
   void* o;
   float* lse;
@@ -82,11 +101,47 @@ struct PagedArgs {
   int* err;
 };
 
+struct SelectArgs {
+  PagedCache cache;          // the table and the lengths; pages are not read
+  const void* q;             // [B, H, T, d]
+  const int8_t* bounds;      // [n_pages, Hkv, 2, d]
+  const float* bound_scales; // [n_pages, Hkv]
+  int B, H, Hkv, T, d;
+  const int32_t* q_lens;
+  int picks, first, last;
+  int32_t* pages;            // [B, Hkv, picks]
+  float* scores;             // workspace [B, Hkv, max_pages]
+  int* err;
+};
+
+struct AssignArgs {
+  int32_t* table;
+  int64_t table_stride;
+  int B, max_pages, page_size, T;
+  const int32_t* old_lens;
+  const int32_t* new_lens;
+  int32_t* free_pages;       // a ring of n_free
+  int n_free;
+  const int32_t* state;      // the ring's first page and their number
+  int32_t* state_out;
+  int32_t* lens;
+  int32_t* q_lens;
+  int64_t* slots;            // [B, T]
+  int32_t* positions;        // [B, T]
+  int* err;
+};
+
 // A sequence's valid keys and its new tokens.  A length beyond the table's pages breaks the
 // contract: the sequence then has no keys (the caller's error word tells).
 __host__ __device__ inline int paged_capacity(const PagedCache& c) {
   const int64_t cap = (int64_t)c.max_pages * c.page_size;
   return cap > 0x7ffffff0 ? 0x7ffffff0 : (int)cap;
+}
+// ... and the keys of a segment at most
+inline int paged_span(const PagedArgs& a) {
+  const int cap = paged_capacity(a.cache);
+  const int64_t chosen = (int64_t)a.picks * a.cache.page_size;
+  return a.pages != nullptr && chosen < cap ? (int)chosen : cap;
 }
 __device__ __forceinline__ int paged_len(const PagedCache& c, int b, int* err) {
   const int n = c.kv_lens[b];
@@ -104,6 +159,12 @@ __device__ __forceinline__ int new_tokens(const int32_t* q_lens, int b, int T) {
 
 cudaError_t launch_rotary(const RotaryArgs& a, fa_dtype dt, cudaStream_t s);
 cudaError_t launch_append(const AppendArgs& a, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_append_store(const AppendArgs& a, const StoreArgs& st, fa_dtype dt, cudaStream_t s);
+
+// Tables of at most this many pages are chosen from: their scores lie in a block's shared memory.
+constexpr int kMaxChoice = 49152;
+cudaError_t launch_select(const SelectArgs& a, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_assign(const AssignArgs& a, cudaStream_t s);
 
 // CTAs of a paged attention call, and the bytes of its partial results.
 // Pages of up to 4096 tokens: part * (rounding of the reciprocal) stays below 2^36 for any part of
@@ -118,5 +179,9 @@ struct PagedWorkspace {
 };
 PagedWorkspace paged_workspace(int ctas, int d);
 cudaError_t launch_paged(const PagedArgs& a, fa_dtype dt, cudaStream_t s);
+// ... of the pages' kinds, one file each
+cudaError_t launch_paged_picked(const PagedArgs& a, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_paged_e4m3(const PagedArgs& a, cudaStream_t s);
+cudaError_t launch_paged_int8(const PagedArgs& a, cudaStream_t s);
 
 }  // namespace fa

@@ -55,18 +55,38 @@ fa_status check_rotation(const double* inv_freq, int rotary_dim, float mscale, i
   return FA_OK;
 }
 
-fa_status check_cache(const fa_paged_cache* c, int Hkv) {
+// The table and the lengths of a cache.
+fa_status check_table(const fa_paged_cache* c) {
   if (c == nullptr) return FA_ERR_INVALID_ARG;
   if (c->n_pages < 0 || c->max_pages < 0 || c->page_size <= 0) return FA_ERR_INVALID_ARG;
   if (c->page_size % 16 != 0 || c->page_size > fa::kMaxPageSize) return FA_ERR_UNSUPPORTED;
-  if (!c->k_cache || !c->v_cache || (!c->block_table && c->max_pages > 0) || !c->kv_lens) return FA_ERR_INVALID_ARG;
-  if (!aligned(c->k_cache, 16) || !aligned(c->v_cache, 16) || !aligned(c->block_table, 4) || !aligned(c->kv_lens, 4))
-    return FA_ERR_INVALID_ARG;
-  if (c->token_stride % 8 != 0 || (c->n_pages > 1 && c->page_stride % 8 != 0) || (Hkv > 1 && c->head_stride % 8 != 0))
-    return FA_ERR_INVALID_ARG;
-  if (c->table_stride < c->max_pages) return FA_ERR_INVALID_ARG;
+  if ((!c->block_table && c->max_pages > 0) || !c->kv_lens) return FA_ERR_INVALID_ARG;
+  if (!aligned(c->block_table, 4) || !aligned(c->kv_lens, 4) || c->table_stride < c->max_pages) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
+
+// ... and its pages, of values of `size` bytes.
+fa_status check_cache(const fa_paged_cache* c, int Hkv, int size = 2) {
+  const fa_status st = check_table(c);
+  if (st != FA_OK) return st;
+  if (!c->k_cache || !c->v_cache || !aligned(c->k_cache, 16) || !aligned(c->v_cache, 16)) return FA_ERR_INVALID_ARG;
+  const int64_t unit = 16 / size;
+  if (c->token_stride % unit != 0 || (c->n_pages > 1 && c->page_stride % unit != 0) || (Hkv > 1 && c->head_stride % unit != 0))
+    return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+// The pages' format, their scales and bounds.  Null: 16-bit pages, nothing else.
+fa_status check_store(const fa_page_store* p, bool bounds) {
+  if (p == nullptr) return FA_OK;
+  if (p->format != FA_PAGES_16BIT && p->format != FA_PAGES_E4M3 && p->format != FA_PAGES_INT8) return FA_ERR_UNSUPPORTED;
+  const bool bits8 = p->format != FA_PAGES_16BIT;
+  if (bits8 && (!p->k_scales || !p->v_scales || !aligned(p->k_scales, 4) || !aligned(p->v_scales, 4))) return FA_ERR_INVALID_ARG;
+  if (bounds && (!p->k_bounds || !p->bound_scales || !aligned(p->k_bounds, 16) || !aligned(p->bound_scales, 4)))
+    return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+int value_bytes(const fa_page_store* p) { return p == nullptr || p->format == FA_PAGES_16BIT ? 2 : 1; }
 
 fa::PagedCache cache_args(const fa_paged_cache* c) {
   fa::PagedCache p{};
@@ -132,6 +152,15 @@ fa_status fa_append_paged(const fa_paged_cache* cache, const void* k, const int6
                           const int64_t v_strides[3], const void* q, const int64_t q_strides[3], void* q_out,
                           int B, int H, int Hkv, int T, int d, const int32_t* q_lens, const double* inv_freq,
                           int rotary_dim, int interleaved, float mscale, fa_dtype dtype, void* stream) {
+  return fa_append_paged_store(cache, nullptr, k, k_strides, v, v_strides, q, q_strides, q_out, B, H, Hkv, T, d, q_lens,
+                               inv_freq, rotary_dim, interleaved, mscale, dtype, stream);
+}
+
+fa_status fa_append_paged_store(const fa_paged_cache* cache, const fa_page_store* store, const void* k,
+                                const int64_t k_strides[3], const void* v, const int64_t v_strides[3], const void* q,
+                                const int64_t q_strides[3], void* q_out, int B, int H, int Hkv, int T, int d,
+                                const int32_t* q_lens, const double* inv_freq, int rotary_dim, int interleaved,
+                                float mscale, fa_dtype dtype, void* stream) {
   // without queries the number of their heads does not matter; with some there have to be heads
   if (H < 0 || (q != nullptr && H == 0 && Hkv > 0)) return FA_ERR_INVALID_ARG;
   if (q == nullptr) H = Hkv;
@@ -141,9 +170,13 @@ fa_status fa_append_paged(const fa_paged_cache* cache, const void* k, const int6
   st = check_rotation(inv_freq, rotary_dim, mscale, d);
   if (st != FA_OK) return st;
   if (B == 0 || Hkv == 0 || T == 0) return FA_OK;
-  st = check_cache(cache, Hkv);
+  const bool bounds = store != nullptr && store->k_bounds != nullptr;
+  st = check_store(store, bounds);
   if (st != FA_OK) return st;
-  // the pages are written
+  st = check_cache(cache, Hkv, value_bytes(store));
+  if (st != FA_OK) return st;
+  // the pages are written, and so are their scales
+  if (value_bytes(store) == 1 && store->k_scales == store->v_scales) return FA_ERR_INVALID_ARG;
   if (cache->k_cache == cache->v_cache || !apart(cache->n_pages, cache->page_stride, Hkv, cache->head_stride,
                                                  cache->page_size, cache->token_stride, d))
     return FA_ERR_INVALID_ARG;
@@ -164,6 +197,15 @@ fa_status fa_append_paged(const fa_paged_cache* cache, const void* k, const int6
   a.q_lens = q_lens;
   a.rot = fa::Rotation{inv_freq, rotary_dim, interleaved != 0, mscale, 1.f};
   if (fa::device_error_word(&a.err) != FA_OK) return FA_ERR_CUDA;
+  if (bounds || value_bytes(store) == 1) {
+    fa::StoreArgs p{};
+    p.store = store->format;
+    p.k_scales = store->k_scales;
+    p.v_scales = store->v_scales;
+    p.bounds = store->k_bounds;
+    p.bound_scales = store->bound_scales;
+    return fa::launch_append_store(a, p, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  }
   return fa::launch_append(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -176,6 +218,14 @@ size_t fa_forward_paged_workspace_size(int B, int H, int Hkv, int T, int d, int 
 fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, float* lse, int B, int H, int Hkv,
                            int T, int d, float scale, const int32_t* q_lens, const fa_score_mod* score,
                            fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  return fa_forward_paged_store(q, cache, nullptr, nullptr, 0, o, lse, B, H, Hkv, T, d, scale, q_lens, score, dtype,
+                                workspace, workspace_bytes, stream);
+}
+
+fa_status fa_forward_paged_store(const void* q, const fa_paged_cache* cache, const fa_page_store* store,
+                                 const int32_t* pages, int n_select, void* o, float* lse, int B, int H, int Hkv, int T,
+                                 int d, float scale, const int32_t* q_lens, const fa_score_mod* score, fa_dtype dtype,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
   fa_status st = check_sizes(B, H, Hkv, T, d);
   if (st != FA_OK) return st;
   if (!isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
@@ -187,13 +237,21 @@ fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, 
   fa::ScoreArgs mods;
   if (!fa::make_score(score, scale, &mods)) return FA_ERR_UNSUPPORTED;
   if (B == 0 || H == 0 || T == 0) return FA_OK;
-  st = check_cache(cache, Hkv);
+  st = check_store(store, false);
   if (st != FA_OK) return st;
+  st = check_cache(cache, Hkv, value_bytes(store));
+  if (st != FA_OK) return st;
+  if (pages != nullptr && (n_select <= 0 || !aligned(pages, 4))) return FA_ERR_INVALID_ARG;
   if (!q || !o || !lse || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(q_lens, 4))
     return FA_ERR_INVALID_ARG;
   fa::PagedArgs a{};
   a.cache = cache_args(cache);
-  const size_t need = fa_forward_paged_workspace_size(B, H, Hkv, T, d, fa::paged_capacity(a.cache));
+  a.pages = pages;
+  a.picks = n_select;
+  // (places behind all keys are a mark of keys that do not exist)
+  if (pages != nullptr && fa::paged_capacity(a.cache) >= 0x7f000000) return FA_ERR_UNSUPPORTED;
+  const int span = fa::paged_span(a);
+  const size_t need = fa_forward_paged_workspace_size(B, H, Hkv, T, d, span);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
   a.q = q;
   a.o = o;
@@ -202,7 +260,13 @@ fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, 
   a.q_lens = q_lens;
   a.scale = scale;
   a.score = mods;
-  if (!fa::paged_counts(B, Hkv, H / Hkv * T, fa::paged_capacity(a.cache))) return FA_ERR_UNSUPPORTED;
+  if (!fa::paged_counts(B, Hkv, H / Hkv * T, span)) return FA_ERR_UNSUPPORTED;
+  if (store != nullptr) {
+    a.store = store->format;
+    a.k_scales = store->k_scales;
+    a.v_scales = store->v_scales;
+  }
+  a.f16 = dtype == FA_FP16;
   a.page_parts = cache->page_size / 16;
   a.parts_magic = ((uint64_t(1) << 36) + a.page_parts - 1) / a.page_parts;
   a.ctas = fa::paged_ctas();
@@ -213,6 +277,108 @@ fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, 
   a.o_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.o);
   if (fa::device_error_word(&a.err) != FA_OK) return FA_ERR_CUDA;
   return fa::launch_paged(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_select_pages_workspace_size(int B, int Hkv, int max_pages) {
+  if (B <= 0 || Hkv <= 0 || max_pages <= 0) return 0;
+  return ((size_t)B * Hkv * max_pages * sizeof(float) + 255) / 256 * 256;
+}
+
+fa_status fa_select_pages(const void* q, const fa_paged_cache* cache, const fa_page_store* store, int32_t* pages, int B,
+                          int H, int Hkv, int T, int d, const int32_t* q_lens, int n_select, int first, int last,
+                          fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  fa_status st = check_sizes(B, H, Hkv, T, d);
+  if (st != FA_OK) return st;
+  if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
+  if (n_select < 0 || first < 0 || last < 0) return FA_ERR_INVALID_ARG;
+  if (B == 0 || H == 0 || T == 0 || n_select == 0) return FA_OK;
+  if (store == nullptr) return FA_ERR_INVALID_ARG;
+  st = check_table(cache);
+  if (st != FA_OK) return st;
+  if (cache->max_pages > fa::kMaxChoice) return FA_ERR_UNSUPPORTED;
+  if (!store->k_bounds || !store->bound_scales || !aligned(store->k_bounds, 16) || !aligned(store->bound_scales, 4) || !q ||
+      !pages || !aligned(q, 16) || !aligned(pages, 4) || !aligned(q_lens, 4))
+    return FA_ERR_INVALID_ARG;
+  if ((int64_t)B * Hkv * n_select > ((int64_t)1 << 40)) return FA_ERR_UNSUPPORTED;
+  if (cache->max_pages > n_select &&
+      (!workspace || !aligned(workspace, 256) || workspace_bytes < fa_select_pages_workspace_size(B, Hkv, cache->max_pages)))
+    return FA_ERR_INVALID_ARG;
+  fa::SelectArgs a{};
+  a.cache = cache_args(cache);
+  a.q = q;
+  a.bounds = store->k_bounds;
+  a.bound_scales = store->bound_scales;
+  a.B = B; a.H = H; a.Hkv = Hkv; a.T = T; a.d = d;
+  a.q_lens = q_lens;
+  a.picks = n_select;
+  a.first = first;
+  a.last = last;
+  a.pages = pages;
+  a.scores = static_cast<float*>(workspace);
+  if (fa::device_error_word(&a.err) != FA_OK) return FA_ERR_CUDA;
+  return fa::launch_select(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_assign_pages(int32_t* block_table, int64_t table_stride, int B, int max_pages, int page_size,
+                          const int32_t* old_lens, const int32_t* new_lens, int32_t* free_pages, int n_free,
+                          const int32_t* free_state, int32_t* free_state_out, int32_t* lens, int32_t* q_lens,
+                          int64_t* slots, int32_t* positions, int T, void* stream) {
+  if (B < 0 || max_pages < 0 || T < 0 || n_free < 0 || page_size <= 0 || table_stride < max_pages) return FA_ERR_INVALID_ARG;
+  if (page_size % 16 != 0 || page_size > fa::kMaxPageSize) return FA_ERR_UNSUPPORTED;
+  if (B > 65535 || (int64_t)B * T > 0x7fffffff) return FA_ERR_UNSUPPORTED;
+  if ((!block_table && B > 0 && max_pages > 0) || !free_pages || n_free == 0 || !free_state || !free_state_out)
+    return FA_ERR_INVALID_ARG;
+  if (B > 0 && (!old_lens || !new_lens || !lens || !q_lens || (T > 0 && (!slots || !positions)))) return FA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)block_table, (const void*)old_lens, (const void*)new_lens, (const void*)free_pages,
+                        (const void*)free_state, (const void*)free_state_out, (const void*)lens, (const void*)q_lens,
+                        (const void*)positions})
+    if (!aligned(p, 4)) return FA_ERR_INVALID_ARG;
+  if (!aligned(slots, 8)) return FA_ERR_INVALID_ARG;
+  fa::AssignArgs a{};
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.B = B; a.max_pages = max_pages; a.page_size = page_size; a.T = T;
+  a.old_lens = old_lens;
+  a.new_lens = new_lens;
+  a.free_pages = free_pages;
+  a.n_free = n_free;
+  a.state = free_state;
+  a.state_out = free_state_out;
+  a.lens = lens;
+  a.q_lens = q_lens;
+  a.slots = slots;
+  a.positions = positions;
+  if (fa::device_error_word(&a.err) != FA_OK) return FA_ERR_CUDA;
+  return fa::launch_assign(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_append_paged_store_packed(const fa_append_paged_call* c, const fa_page_store* store) {
+  if (c == nullptr) return FA_ERR_INVALID_ARG;
+  return fa_append_paged_store(&c->cache, store, c->k, c->k_strides, c->v, c->v_strides, c->q, c->q_strides, c->q_out,
+                               c->B, c->H, c->Hkv, c->T, c->d, c->q_lens, c->inv_freq, c->rotary_dim, c->interleaved,
+                               c->mscale, static_cast<fa_dtype>(c->dtype), c->stream);
+}
+
+fa_status fa_forward_paged_store_packed(const fa_forward_paged_call* c, const fa_page_store* store, const int32_t* pages,
+                                        int n_select) {
+  if (c == nullptr) return FA_ERR_INVALID_ARG;
+  const fa_score_mod mod{c->softcap, c->alibi_slopes, nullptr};
+  return fa_forward_paged_store(c->q, &c->cache, store, pages, n_select, c->o, c->lse, c->B, c->H, c->Hkv, c->T, c->d,
+                                c->scale, c->q_lens, &mod, static_cast<fa_dtype>(c->dtype), c->workspace,
+                                c->workspace_bytes, c->stream);
+}
+
+fa_status fa_select_pages_packed(const fa_select_pages_call* c) {
+  if (c == nullptr) return FA_ERR_INVALID_ARG;
+  return fa_select_pages(c->q, &c->cache, &c->store, c->pages, c->B, c->H, c->Hkv, c->T, c->d, c->q_lens, c->n_select,
+                         c->first, c->last, static_cast<fa_dtype>(c->dtype), c->workspace, c->workspace_bytes, c->stream);
+}
+
+fa_status fa_assign_pages_packed(const fa_assign_pages_call* c) {
+  if (c == nullptr) return FA_ERR_INVALID_ARG;
+  return fa_assign_pages(c->block_table, c->table_stride, c->B, c->max_pages, c->page_size, c->old_lens, c->new_lens,
+                         c->free_pages, c->n_free, c->free_state, c->free_state_out, c->lens, c->q_lens, c->slots,
+                         c->positions, c->T, c->stream);
 }
 
 fa_status fa_rotary_packed(const fa_rotary_call* c) {

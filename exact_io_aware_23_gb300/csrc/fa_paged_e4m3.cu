@@ -1,0 +1,12 @@
+// Attention over a cache of e4m3 pages, whole or chosen ones (fa_paged_kernel.cuh).
+#include "fa_paged_kernel.cuh"
+
+namespace fa {
+
+cudaError_t launch_paged_e4m3(const PagedArgs& a, cudaStream_t s) {
+  if (a.pages != nullptr)
+    return a.d == 64 ? paged<Cfg<64, FA_PAGES_E4M3, true, true>>(a, s) : paged<Cfg<128, FA_PAGES_E4M3, true, true>>(a, s);
+  return a.d == 64 ? paged<Cfg<64, FA_PAGES_E4M3, true, false>>(a, s) : paged<Cfg<128, FA_PAGES_E4M3, true, false>>(a, s);
+}
+
+}  // namespace fa

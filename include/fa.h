@@ -439,6 +439,24 @@ typedef struct {
 } fa_paged_cache;
 
 /*
+ * How the pages hold keys and values.  In 8-bit pages a value is its code times a scale of its page and
+ * head, one for the keys and one for the values:
+ *     FA_PAGES_E4M3   8-bit floats of 4 exponent and 3 mantissa bits, largest 448
+ *     FA_PAGES_INT8   whole numbers from -127 to 127
+ * The cache's strides then count bytes, multiples of 16.  Bounds of a page's keys, kept by the write of
+ * the keys and read by fa_select_pages, go with pages of any kind: for each of the d values of a key
+ * head the smallest and the largest one that the page's keys have, in whole numbers of a scale.
+ */
+typedef enum { FA_PAGES_16BIT = 0, FA_PAGES_E4M3 = 1, FA_PAGES_INT8 = 2 } fa_page_format;
+typedef struct {
+  int format;                  /* fa_page_format */
+  float* k_scales;             /* device fp32 [n_pages, Hkv]; null with FA_PAGES_16BIT */
+  float* v_scales;
+  int8_t* k_bounds;            /* nullable; device int8 [n_pages, Hkv, 2, d], 16-byte aligned: smallest, then largest */
+  float* bound_scales;         /* device fp32 [n_pages, Hkv], with k_bounds */
+} fa_page_store;
+
+/*
  * Writes T new tokens per sequence into the cache, their keys rotated (rotary_dim > 0), and with q
  * given writes the rotated queries to q_out, in one launch.  kv_lens counts the new tokens already:
  * token t of sequence b's n = q_lens ? q_lens[b] : T new tokens (n clamped to [0, T]) takes place
@@ -480,6 +498,100 @@ fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, 
                            int H, int Hkv, int T, int d, float scale, const int32_t* q_lens,
                            const fa_score_mod* score, fa_dtype dtype, void* workspace,
                            size_t workspace_bytes, void* stream);
+
+/*
+ * fa_append_paged into pages of any format (store null: 16 bits), with the bounds of the pages' keys kept
+ * where store->k_bounds is given.  Keys (rotated) and values go to 8 bits from fp32, rounded once to
+ * the nearest code, ties to the even one.  The scale of a page and head:
+ *     need = the smallest 2^e, e >= -100, for which largest code * 2^e reaches every new value
+ *     the page held tokens before (places below the first new one): max(its scale, need), and where that
+ *     grew the codes of those tokens are multiplied by old / new and rounded again; otherwise need
+ * Scales that a caller wrote itself may be any positive numbers.  Bounds grow in the same way (their
+ * scale with 127 as the largest code), lower ones rounded down and upper ones up; they bound the keys as
+ * they are before they go to 8 bits (16-bit pages: as stored).  A value that is not finite makes the scale
+ * of its page and head NaN, and the bounds' scale with it, until a write begins the page anew; the
+ * codes written there are 0.
+ * Several sequences must not write to one page.  Other arguments as in fa_append_paged; FA_ERR_INVALID_ARG
+ * also for k_scales == v_scales.
+ */
+fa_status fa_append_paged_store(const fa_paged_cache* cache, const fa_page_store* store,
+                                const void* k, const int64_t k_strides[3], const void* v,
+                                const int64_t v_strides[3], const void* q,
+                                const int64_t q_strides[3], void* q_out, int B, int H, int Hkv,
+                                int T, int d, const int32_t* q_lens, const double* inv_freq,
+                                int rotary_dim, int interleaved, float mscale, fa_dtype dtype,
+                                void* stream);
+
+/*
+ * fa_forward_paged over pages of any format (store null: 16 bits; its bounds are not looked at), and over
+ * chosen pages where `pages` is given:
+ *   pages  : nullable; device int32 [B, Hkv, n_select], n_select > 0: the pages, by their number in the
+ *            sequence, that the queries of a key head see.  The first min(n_select, pages of the
+ *            sequence) entries of a list count; entries that are no page of the sequence (-1) see
+ *            nothing.  Any order, each page once (one that is listed twice counts twice).
+ * Within the chosen pages query t sees the keys j <= i as before.  dtype is that of q and o (bf16 or
+ * fp16).  Products run on the codes as fp16 numbers, sums in fp32; P is rounded to fp16, at least to 2^-25 of
+ * the largest value scale among the pages.  Workspace: fa_forward_paged_workspace_size with
+ * max_keys = max_pages * page_size, or n_select * page_size where `pages` is given and that is less.
+ * Scales that are NaN show in the rows that see a key of their page.  Pages are chosen from tables of
+ * less than 0x7f000000 tokens (FA_ERR_UNSUPPORTED beyond).
+ */
+fa_status fa_forward_paged_store(const void* q, const fa_paged_cache* cache,
+                                 const fa_page_store* store, const int32_t* pages, int n_select,
+                                 void* o, float* lse, int B, int H, int Hkv, int T, int d,
+                                 float scale, const int32_t* q_lens, const fa_score_mod* score,
+                                 fa_dtype dtype, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * Chooses the pages that a sequence's new tokens attend to, by the bounds of their keys.  With q' a query
+ * row in whole numbers of the smallest 2^f, f >= -100, that keeps them within +-127, rounded to the
+ * nearest (ties to even), and lo, hi, s a page's bounds and their scale, the page's score is the largest of
+ *     2^f * s * sum_i max(q'_i lo_i, q'_i hi_i)
+ * over the existing new tokens and the query heads of the key head's group: what no key of the page exceeds
+ * in its product with q'.  The sum is a whole number, computed exactly.
+ *   pages  : [B, Hkv, n_select] the chosen pages' numbers in the sequence, ascending, -1 behind them:
+ *            the `first` first and the `last` last pages, then those with the highest scores; of
+ *            equal ones, and where first + last exceeds n_select, the lower numbers.  All pages
+ *            where a sequence has no more than n_select; none without new tokens.
+ *   cache  : the table and the lengths; keys and values are not looked at (they may be null)
+ *   store  : k_bounds and bound_scales, as fa_append_paged_store left them; nothing else is looked at
+ *   workspace : fa_select_pages_workspace_size(B, Hkv, max_pages) bytes, 256-byte aligned; none (it
+ *            may be null) when max_pages <= n_select
+ * A bounds' scale that is NaN counts above all scores; a query row that holds something not finite
+ * has no say next to others.  max_pages at most 49152 (FA_ERR_UNSUPPORTED).  Lengths and entries as in
+ * fa_append_paged.
+ */
+size_t fa_select_pages_workspace_size(int B, int Hkv, int max_pages);
+fa_status fa_select_pages(const void* q, const fa_paged_cache* cache, const fa_page_store* store,
+                          int32_t* pages, int B, int H, int Hkv, int T, int d,
+                          const int32_t* q_lens, int n_select, int first, int last, fa_dtype dtype,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Block tables and places of new tokens, from the lengths of the sequences.  Sequence b goes from old_lens[b]
+ * to new_lens[b] tokens: where it needs more pages they come from the free ones, where it needs
+ * fewer (0 tokens: none) the rest are given back.  Entries of its row behind its pages keep what they
+ * hold.
+ *   free_pages : device int32 [n_free], a ring of the pages that are free: free_state[1] of them, from
+ *                entry free_state[0] on.  Taken from there in the order of the sequences; given back
+ *                behind the last one in the order of the sequences, and not handed out again in the
+ *                same call.  n_free > 0 is the number of pages in all, so that every one has a place.
+ *   free_state_out, lens : the ring's state and the lengths after the call; may be free_state, and old_lens
+ *                or new_lens
+ *   q_lens     : [B] new tokens of each sequence, max(0, new - old)
+ *   slots      : [B, T] of the first T new tokens of each sequence, page * page_size + place in the page
+ *   positions  : [B, T] and their places in the sequence; -1 in both where there is no token
+ *   The outputs must not overlap one another, nor the inputs but as said.
+ * All or nothing: when the free pages do not suffice, or a length lies outside [0, max_pages * page_size],
+ * or the ring's state is none, the table and the ring stay as they are, lens = old_lens, q_lens = 0, slots
+ * and positions are -1, and fa_check_device_status returns FA_ERR_INVALID_ARG.
+ */
+fa_status fa_assign_pages(int32_t* block_table, int64_t table_stride, int B, int max_pages,
+                          int page_size, const int32_t* old_lens, const int32_t* new_lens,
+                          int32_t* free_pages, int n_free, const int32_t* free_state,
+                          int32_t* free_state_out, int32_t* lens, int32_t* q_lens, int64_t* slots,
+                          int32_t* positions, int T, void* stream);
 
 /*
  * These calls with their arguments in one structure, fields as the parameters above.  For callers
@@ -537,12 +649,41 @@ typedef struct {
   int B, H, Hkv, T, d, dtype;
   float scale, softcap;
 } fa_forward_paged_call;
+typedef struct {
+  fa_paged_cache cache;
+  fa_page_store store;
+  const void* q;
+  int32_t* pages;
+  const int32_t* q_lens;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+  int B, H, Hkv, T, d, n_select, first, last, dtype;
+} fa_select_pages_call;
+typedef struct {
+  int32_t* block_table;
+  int64_t table_stride;
+  const int32_t *old_lens, *new_lens;
+  int32_t* free_pages;
+  const int32_t* free_state;
+  int32_t *free_state_out, *lens, *q_lens;
+  int64_t* slots;
+  int32_t* positions;
+  void* stream;
+  int B, max_pages, page_size, n_free, T;
+} fa_assign_pages_call;
 fa_status fa_forward_scored_packed(const fa_scored_call* call);
 fa_status fa_backward_scored_packed(const fa_scored_call* call);
 fa_status fa_rotary_packed(const fa_rotary_call* call);
 fa_status fa_rotary_backward_packed(const fa_rotary_call* call);
 fa_status fa_append_paged_packed(const fa_append_paged_call* call);
 fa_status fa_forward_paged_packed(const fa_forward_paged_call* call);
+fa_status fa_append_paged_store_packed(const fa_append_paged_call* call, const fa_page_store* store);
+fa_status fa_forward_paged_store_packed(const fa_forward_paged_call* call,
+                                        const fa_page_store* store, const int32_t* pages,
+                                        int n_select);
+fa_status fa_select_pages_packed(const fa_select_pages_call* call);
+fa_status fa_assign_pages_packed(const fa_assign_pages_call* call);
 
 /* ABI version of this header: major * 100 + minor. */
 int fa_version(void);
