@@ -33,10 +33,12 @@ bool paged_counts(int B, int Hkv, int rows, int capacity) {
 }
 
 // The workspace: arrivals [2 * ctas], then two parts of 16 rows a CTA, their statistics and outputs.
+// Variants with more and smaller CTAs have as many rows of parts, and their arrivals fit too.
 PagedWorkspace paged_workspace(int ctas, int d) {
   PagedWorkspace w;
   const size_t rows = 2 * (size_t)ctas * kRows;
-  w.ml = (2 * (size_t)ctas * sizeof(unsigned long long) + 255) / 256 * 256;
+  static_assert(kFlipCtasPerSm * 8 == kCtasPerSm * kRows, "parts of 8 rows take the place of those of 16");
+  w.ml = (2 * (size_t)ctas * (kFlipCtasPerSm / kCtasPerSm) * sizeof(unsigned long long) + 255) / 256 * 256;
   w.o = w.ml + rows * sizeof(float2);
   w.total = (w.o + rows * d * sizeof(float) + 255) / 256 * 256;
   return w;

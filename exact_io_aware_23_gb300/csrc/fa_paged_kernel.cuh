@@ -65,6 +65,9 @@ constexpr int kThreads = 32 * kWarps;
 // hold twice the output in registers and spill (B8 H64 Hkv8 T7 d128, 4096 keys: 95 us against 74).
 constexpr int kRows = 16;
 constexpr int kCtasPerSm = 8 / kWarps;
+constexpr int kFlipCtasPerSm = 4;
+constexpr int kSegment = 4;
+constexpr int kFlipSegment = 12;           // (4: 10 % longer for 64 chosen pages of 64 keys; 24: the same for d = 64)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kUnitSlack = 16.0f;         // ... and the unit of the values' scales
@@ -72,15 +75,21 @@ constexpr int kNowhere = 0x7f000000;       // the place of keys that do not exis
 constexpr float kRescaleLog2 = 8.0f;       // the running maximum is raised when a score exceeds it by more
 
 // kStore: fa_page_format.  kF16_: the type of 16-bit pages and queries (8-bit pages: of the products).
-template <int D_, int kStore_, bool kF16_, bool kPick_>
+// kFlip_: keys are the rows of the products and queries their columns (see below).
+template <int D_, int kStore_, bool kF16_, bool kPick_, bool kFlip_ = false>
 struct Cfg {
   static constexpr int D = D_;
   static constexpr bool k8 = kStore_ != FA_PAGES_16BIT, kInt8 = kStore_ == FA_PAGES_INT8;
+  static constexpr bool kFlip = kFlip_;
+  static constexpr int kRows = kFlip ? 8 : 16;
+  static constexpr bool kDefer = k8;
+  static constexpr int kSegment = kFlip ? kFlipSegment : fa::kSegment;
+  static constexpr int kCtasPerSm = kFlip ? kFlipCtasPerSm : fa::kCtasPerSm;
   static constexpr bool kF16 = kF16_ || k8, kPick = kPick_;
   using Elem = std::conditional_t<k8, uint8_t, uint16_t>;
   static constexpr int kElem = sizeof(Elem);
   static constexpr int kRowBytes = D * kElem;
-  static constexpr int kKeys = 4096 / kRowBytes;              // keys of a tile: 8 KB with the values
+  static constexpr int kKeys = (kFlip ? 2048 : 4096) / kRowBytes;   // keys of a tile: 8 (4) KB with the values
   static constexpr int kParts = kKeys / 16;                   // 16-key parts of a tile, each in one page
   static constexpr int kHalf = kKeys * kRowBytes;             // a tile's keys (or values)
   static constexpr int kStage = 2 * kHalf;
@@ -91,7 +100,8 @@ struct Cfg {
   static constexpr int kParted = kFrom + kWarps * 4 + 16;       // after a flag: statistics to be joined
   static constexpr int kJoin = 64;                              // parts
   // what a tile's parts carry: {ks, vs, place of the first key, -}
-  static constexpr int kMeta = kParted + kJoin * kRows * 8;
+  static constexpr int kPending = kParted + kJoin * kRows * 8;  // the CTA's parts of segments
+  static constexpr int kMeta = kPending + 64;
   static constexpr int kMetaRing = k8 || kPick ? kStages * kParts * 16 : 0;     // per warp
   static constexpr int kSmem = kMeta + kWarps * kMetaRing;
   static constexpr int kChunks = kRowBytes / 16;              // 16-byte pieces of a row
@@ -130,6 +140,12 @@ __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
 __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+// an 8 x 8 matrix of 16-bit values, two adjacent ones of a row to a lane, as its transpose
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 // c (16 x 8, fp32) += a (16 x 16) b (16 x 8)
 template <bool F16>
@@ -171,10 +187,10 @@ __device__ __forceinline__ void codes(uint32_t x, uint32_t& lo, uint32_t& hi) {
 // whatever its length (its queries, the join of the warps; about as long as the CTA takes for that
 // many tiles), then one per tile; unit numbers run over all segments, and each CTA takes an equal
 // range of them.
-constexpr int kSegment = 4;
-constexpr int kMinUnits = kSegment + kWarps;   // a smaller share costs more in joining than it saves
 
+template <typename C>
 __host__ __device__ inline int sharing_ctas(int units, int ctas) {
+  constexpr int kMinUnits = C::kSegment + kWarps;   // a smaller share costs more in joining than it saves
   const int want = (units + kMinUnits - 1) / kMinUnits;
   return want < 1 ? 1 : want > ctas ? ctas : want;
 }
@@ -208,7 +224,7 @@ __device__ __forceinline__ int tiles_of(const PagedArgs& a, int b, int* err) {
 template <typename C>
 __device__ __forceinline__ int units_of(const PagedArgs& a, int heads, int b, int* err) {
   const int n = b < a.B ? tiles_of<C>(a, b, err) : 0;
-  return n > 0 ? (n + kSegment) * heads : 0;
+  return n > 0 ? (n + C::kSegment) * heads : 0;
 }
 
 // A warp's reckoning of all sequences' units: the first 256 sequences' stay in registers (all their
@@ -296,6 +312,10 @@ struct Walk {
   }
 };
 
+// The exponent (biased) by which a bf16 row of this largest value goes to fp16: it becomes that of 2^14;
+// infinities and NaN stay what they are.
+__device__ __forceinline__ int bf16_exponent(uint32_t bits) { return bits >= 0x7f800000u ? 141 : max((int)(bits >> 23), 15); }
+
 // O = 0 and LSE = -inf for rows [row, row + n)
 template <int D>
 __device__ __forceinline__ void no_keys(const PagedArgs& a, int64_t row, int n) {
@@ -315,8 +335,16 @@ __device__ __forceinline__ void write_row4(const PagedArgs& a, int64_t row, int 
   if (c == 0) a.lse[row] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-// Announces this CTA's part of a segment that CTAs ca..cb share, and says whether all of them are
-// there; run by one warp.  Every part has a word of its own, set to the call's number: no atomic
+// A CTA's part of a segment that others have tiles of too.
+struct Parted {
+  int64_t qrow;                                        // the segment's first query row
+  int n_rows;
+  int ca, cb;                                          // the CTAs that have tiles of it
+  int part0;                                           // the first one's part
+};
+
+// Announces this CTA's parts (bits of mine: first, second), and says for a segment that CTAs ca..cb
+// share whether all of its parts are there; run by one warp.  Every part has a word of its own, set to the call's number: no atomic
 // that 38 CTAs contend for (counting them in one word by compare-and-swap took 18 us at the end of
 // B1 H32 Hkv8 with 32K keys).  Between its own store and its reads of the others each CTA has a
 // sequentially consistent fence, so the last of them sees all words set, or cleared by one that did;
@@ -325,16 +353,19 @@ __device__ __forceinline__ void write_row4(const PagedArgs& a, int64_t row, int 
 // to do).  Whatever else a fresh workspace holds is not the number: it has 64 bits, starts at another
 // place in every process, and is not used twice in one.  So no launch is spent on clearing the words
 // first.  (By cudaMemsetAsync: 3 us of a call's 40.)
-__device__ __forceinline__ bool all_arrived(unsigned long long* words, int mine, int part0, int ca, int cb,
-                                            unsigned long long call) {
+__device__ __forceinline__ void announce(unsigned long long* words, int mine, unsigned long long call) {
   const int lane = threadIdx.x % 32;
   if (lane == 0) {
     // releases what the whole CTA wrote before its barrier
     asm volatile("fence.acq_rel.gpu;" ::: "memory");
-    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(words + mine), "l"(call) : "memory");
+    if ((mine & 1) != 0) asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(words), "l"(call) : "memory");
+    if ((mine & 2) != 0) asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(words + 1), "l"(call) : "memory");
   }
   __syncwarp();
   asm volatile("fence.sc.gpu;" ::: "memory");
+}
+__device__ __forceinline__ bool all_arrived(unsigned long long* words, int part0, int ca, int cb, unsigned long long call) {
+  const int lane = threadIdx.x % 32;
   bool there = true;
   for (int i = ca + lane; i <= cb; i += 32) {
     unsigned long long w;
@@ -349,9 +380,10 @@ __device__ __forceinline__ bool all_arrived(unsigned long long* words, int mine,
 // kShared: CTAs share all segments' units.  Otherwise a CTA has one segment to itself (few short
 // ones: nothing to join, nothing to reckon).
 template <typename C, bool kShared>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const PagedArgs a) {
   constexpr int D = C::D, kKeys = C::kKeys, kParts = C::kParts, kQuads = D / 4;
   constexpr bool F16 = C::kF16;
+  constexpr int kRows = C::kRows;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int G = a.H / a.Hkv, rows = G * a.T;
@@ -366,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
       if (tiles_of<C>(a, b, nullptr) == 0) no_keys<D>(a, (int64_t)b * a.H * a.T, a.H * a.T);
     const Reckoning<C> all(a, heads, blockIdx.x == 0 && warp == 0 ? a.err : nullptr);
     units = all.total;
-    n_ctas = sharing_ctas(units, gridDim.x);
+    n_ctas = sharing_ctas<C>(units, gridDim.x);
     if ((int)blockIdx.x >= n_ctas || units == 0) return;
     const Shares share(units, n_ctas);
     begin = share.begin(blockIdx.x);
@@ -374,11 +406,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
     int b, before;
     all.find(a, heads, begin, &b, &before);
     seg.start(a, b);
-    const int hr = (begin - before) / (seg.tiles + kSegment);
+    const int hr = (begin - before) / (seg.tiles + C::kSegment);
     seg.hk = hr / blocks;
     seg.block = hr % blocks;
-    s0 = before + hr * (seg.tiles + kSegment);
-    seg.tile = max(0, begin - s0 - kSegment);
+    s0 = before + hr * (seg.tiles + C::kSegment);
+    seg.tile = max(0, begin - s0 - C::kSegment);
   } else {
     const int hr = blockIdx.x % heads;
     seg.start(a, blockIdx.x / heads);
@@ -389,10 +421,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
       no_keys<D>(a, ((int64_t)seg.b * a.H + seg.hk * G) * a.T + seg.block * kRows, min(kRows, rows - seg.block * kRows));
       return;
     }
-    end = seg.tiles + kSegment;
+    end = seg.tiles + C::kSegment;
   }
   // tiles of the current segment up to this number are the CTA's
-  auto last_tile = [&](int first_unit, int tiles) { return min(tiles, end - first_unit - kSegment); };
+  auto last_tile = [&](int first_unit, int tiles) { return min(tiles, end - first_unit - C::kSegment); };
 
   // ---- the warp's copies: every fourth tile of the CTA's, into its own ring ----------------------
   const uint32_t ring = ptx::smem_u32(smem) + warp * C::kRing;
@@ -403,12 +435,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
     int t = load.tile + n;
     while (t >= load.tiles) {
       t -= load.tiles;
-      load_s0 += load.tiles + kSegment;
+      load_s0 += load.tiles + C::kSegment;
       load.next(a, blocks);
-      if (load_s0 + kSegment >= end) break;
+      if (load_s0 + C::kSegment >= end) break;
     }
     load.tile = t;
-    more = load_s0 + kSegment + t < end;
+    more = load_s0 + C::kSegment + t < end;
   };
   // The next tile's parts of 16 keys: their pages, and their first rows in them.
   int page[kParts], first[kParts];
@@ -444,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
       }
     }
   };
-  more = s0 + kSegment + seg.tile < end;
+  more = s0 + C::kSegment + seg.tile < end;
   if (more) step(warp);
   read_pages();
   // This lane's 16-byte pieces: column c of rows row, row + kStep, ...
@@ -516,12 +548,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
   int* const from = reinterpret_cast<int*>(smem + C::kFrom);   // where each warp's output to be joined lies
   int* const flag = from + kWarps;
   float2* const joined = reinterpret_cast<float2*>(smem + C::kParted);
+  Parted* const parted = reinterpret_cast<Parted*>(smem + C::kPending);
+  if (threadIdx.x == 0) *flag = 0;
   int take = 0;                                         // ring slot of the next tile
   int turn = 0;                                         // the warp whose turn the segment's first tile is
   bool first_seg = true;
 
   // the segment's queries as mma operands; per row its slope and the keys it sees
-  uint32_t q[D / 16][4];
+  constexpr bool kFlip = C::kFlip;
+  uint32_t q[D / 16][kFlip ? 2 : 4];
   int limit[2], full;
   float slope[2];
   float unit_q[2];                                      // 8-bit pages: what the operand's values count
@@ -535,6 +570,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           q[i][e] = r0 + (e & 1) * 8 < n_rows ? __ldg(qp + ((e & 1) * 8 * D + i * 16 + (e >> 1) * 8) / 2) : 0u;
+    } else if constexpr (kFlip) {
+      // the lane's values are row r0's, its scores those of rows c0 and c0 + 1
+      const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (qrow + r0) * D + 2 * c0;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint2 v = r0 < n_rows ? __ldg(reinterpret_cast<const uint2*>(qp + i * 16)) : make_uint2(0u, 0u);
+        q[i][0] = v.x;
+        q[i][1] = v.y;
+      }
     } else {
       // four adjacent codes of a key are a register: the products' columns 2 i, 2 i + 1 and 2 i + 8, 2 i + 9 of
       // lane i are values 4 i to 4 i + 3 of the 16
@@ -547,33 +591,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
           q[i][e] = v.x;
           q[i][e + 2] = v.y;
         }
-      unit_q[0] = unit_q[1] = 1.f;
-      if (!a.f16) {
-        // bf16: the row's largest exponent becomes that of 2^14 (infinities and NaN stay what they are)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t mx = 0;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-            for (int w = e; w < 4; w += 2) mx = max(mx, max(q[i][w] << 16 & 0x7fff0000u, q[i][w] & 0x7fff0000u));
-          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const int x = mx >= 0x7f800000u ? 141 : max((int)(mx >> 23), 15);
-          const float f = __uint_as_float((uint32_t)(268 - x) << 23);      // 2^(141 - x)
-          unit_q[e] = __uint_as_float((uint32_t)(x - 14) << 23);
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-            for (int w = e; w < 4; w += 2)
-              q[i][w] = ptx::pack_f16(__uint_as_float(q[i][w] << 16) * f, __uint_as_float(q[i][w] & 0xffff0000u) * f);
-        }
-      }
     }
     full = 0x7fffffff;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int r = row0 + r0 + e * 8;
+      const int r = row0 + (kFlip ? c0 + e : r0 + e * 8);
       const int h = a.T == 1 ? r : r / a.T, t = r - h * a.T;
       limit[e] = r < rows && t < seg.count ? seg.len - seg.count + t + 1 : 0;
       if (r < rows) full = min(full, limit[e]);
@@ -581,19 +603,169 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
     }
     full = __reduce_min_sync(0xffffffffu, full);        // keys that every row sees
   };
+  // 8-bit pages: bf16 queries as fp16 in units of their own (once they are there)
+  auto convert_rows = [&]() {
+    if constexpr (!C::k8) return;
+    unit_q[0] = unit_q[1] = 1.f;
+    if (a.f16) return;
+    if constexpr (kFlip) {
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) mx = max(mx, max(q[i][w] << 16 & 0x7fff0000u, q[i][w] & 0x7fff0000u));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int x = bf16_exponent(mx);
+      const float f = __uint_as_float((uint32_t)(268 - x) << 23), unit = __uint_as_float((uint32_t)(x - 14) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          q[i][w] = ptx::pack_f16(__uint_as_float(q[i][w] << 16) * f, __uint_as_float(q[i][w] & 0xffff0000u) * f);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) unit_q[e] = __shfl_sync(0xffffffffu, unit, 4 * (c0 + e));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int w = e; w < 4; w += 2) mx = max(mx, max(q[i][w] << 16 & 0x7fff0000u, q[i][w] & 0x7fff0000u));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int x = bf16_exponent(mx);
+        const float f = __uint_as_float((uint32_t)(268 - x) << 23);      // 2^(141 - x)
+        unit_q[e] = __uint_as_float((uint32_t)(x - 14) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int w = e; w < 4; w += 2)
+            q[i][w] = ptx::pack_f16(__uint_as_float(q[i][w] << 16) * f, __uint_as_float(q[i][w] & 0xffff0000u) * f);
+      }
+    }
+  };
+  // Who else has tiles of the segment, worked out while its first ones are on their way.
+  auto note_parted = [&](int k) {
+    if (!kShared || threadIdx.x != 0 || (seg.tile == 0 && last_tile(s0, seg.tiles) == seg.tiles)) return;
+    const Shares share(units, n_ctas);
+    const int ca = share.owner(s0 + C::kSegment), cb = share.owner(s0 + C::kSegment + seg.tiles - 1);
+    const int row0 = seg.block * kRows;
+    // the first CTA may have begun inside an earlier segment: this one is then its second part
+    parted[k] = Parted{((int64_t)seg.b * a.H + seg.hk * G) * a.T + row0, min(kRows, rows - row0), ca, cb,
+                       2 * ca + (share.begin(ca) >= s0 ? 0 : 1)};
+  };
   read_rows();                                          // before the copies fill the way to memory
 #pragma unroll 1
   for (int i = 0; i < C::kStages - 1; ++i) copy_tile();
+  convert_rows();
+  note_parted(0);
+
+  // Segments that other CTAs have tiles of too, the CTA's first one and its last: the CTA that comes last
+  // joins their parts, in the order of the tiles.  With 8-bit pages both are announced together, at the end:
+  // done where the first one ends, it held its CTA up by 9 us (B2 H32 Hkv8 d128 with 100K e4m3 keys).
+  // With 16-bit ones each is done with at its end, while twice the bytes are on their way: no CTA then
+  // has two segments to join at the end (B64, 1 to 8192 keys, 159 us against 163).
+  auto finish = [&](const int mine) {                   // bits: the first part, the second
+    if (warp == 0) {
+      announce(a.arrivals + 2 * blockIdx.x, mine, a.call);
+      int there = 0;
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        if ((mine >> k & 1) == 0) continue;
+        if (all_arrived(a.arrivals, parted[k].part0, parted[k].ca, parted[k].cb, a.call)) there |= 1 << k;
+      }
+      if (lane == 0) *flag = there;
+    }
+    __syncthreads();
+    const int last = *flag;
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      if ((last >> k & 1) == 0) continue;
+      const int n_rows = parted[k].n_rows;
+      const int64_t qrow = parted[k].qrow;
+      const int ca = parted[k].ca, cb = parted[k].cb, part0 = parted[k].part0;
+      for (int i = ca + threadIdx.x; i <= cb; i += kThreads) a.arrivals[i == ca ? part0 : 2 * i] = 0ull;
+      // Up to kJoin parts at a time: their statistics to shared memory, all in flight together, then
+      // their outputs, several in flight, onto what the parts before came to.
+      auto part_of = [&](int i) { return (int64_t)(i == ca ? part0 : 2 * i) * kRows; };
+      constexpr int kItems = (kRows * kQuads + kThreads - 1) / kThreads;
+      float mx[kItems], sum[kItems];
+      float4 acc[kItems];
+#pragma unroll
+      for (int y = 0; y < kItems; ++y) {
+        mx[y] = -INFINITY;
+        sum[y] = 0.f;
+        acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll 1
+      for (int i0 = ca; i0 <= cb; i0 += C::kJoin) {
+        const int np = min(C::kJoin, cb + 1 - i0);
+        // several parts' outputs of item x; past the last part its own again, not used
+        constexpr int kFlight = kFlip ? 8 : 16;
+        auto outputs = [&](int x, int i, float4 (&v)[kFlight]) {
+#pragma unroll
+          for (int k = 0; k < kFlight; ++k)
+            v[k] = __ldcg(reinterpret_cast<const float4*>(a.o_part + (part_of(i0 + min(i + k, np - 1)) + x / kQuads) * D +
+                                                          x % kQuads * 4));
+        };
+        float4 v[kFlight];
+        if (threadIdx.x < n_rows * kQuads) outputs(threadIdx.x, 0, v);    // under way with the statistics
+        __syncthreads();
+        for (int x = threadIdx.x; x < np * kRows; x += kThreads)
+          joined[x] = __ldcg(&a.ml_part[part_of(i0 + x / kRows) + x % kRows]);
+        __syncthreads();
+#pragma unroll
+        for (int y = 0; y < kItems; ++y) {
+          const int x = threadIdx.x + y * kThreads;
+          if (x >= n_rows * kQuads) break;
+          const int r = x / kQuads;
+          float m_new = mx[y];
+          for (int i = 0; i < np; ++i) m_new = fmaxf(m_new, joined[i * kRows + r].x);
+          // no key of the row so far, and none that is NaN, where the maximum is still -inf
+          const float keep = mx[y] == m_new ? 1.f : ptx::ex2(mx[y] - m_new);
+          mx[y] = m_new;
+          sum[y] *= keep;
+          acc[y].x *= keep;
+          acc[y].y *= keep;
+          acc[y].z *= keep;
+          acc[y].w *= keep;
+          for (int i = 0; i < np; i += kFlight) {
+            if (y > 0 || i > 0) outputs(x, i, v);
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) {
+              const float2 ml = joined[min(i + k, np - 1) * kRows + r];
+              if (i + k >= np || ml.y == 0.f) continue;     // no part, or no key of the row in it
+              const float f = ptx::ex2(ml.x - m_new);
+              sum[y] = fmaf(f, ml.y, sum[y]);
+              acc[y].x = fmaf(f, v[k].x, acc[y].x);
+              acc[y].y = fmaf(f, v[k].y, acc[y].y);
+              acc[y].z = fmaf(f, v[k].z, acc[y].z);
+              acc[y].w = fmaf(f, v[k].w, acc[y].w);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < kItems; ++y) {
+        const int x = threadIdx.x + y * kThreads;
+        if (x < n_rows * kQuads) write_row4<C>(a, qrow + x / kQuads, x % kQuads * 4, acc[y], sum[y], mx[y]);
+      }
+    }
+  };
 
 #pragma unroll 1
-  while (s0 + kSegment < end) {
+  while (s0 + C::kSegment < end) {
     const int n = last_tile(s0, seg.tiles) - seg.tile;  // the CTA's tiles of the segment: at least one
     const int mine = (warp - turn + kWarps) % kWarps;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float unit_v = 0.f;                                 // 8-bit pages: what the output counts
-    float o[D / 8][4];
+    float unit_v = 0.f, inv_unit_v = 0.f;               // 8-bit pages: what the output counts
+    // kFlip: o[j] are values 16 j + 2 r0 and the next one of rows c0 and c0 + 1
+    constexpr int kOut = kFlip ? D / 16 : D / 8;
+    float o[kOut][4];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int i = 0; i < kOut; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 #pragma unroll 1
@@ -609,10 +781,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
       }
       take = take + 1 == C::kStages ? 0 : take + 1;
       constexpr int kN = kKeys / 8;                     // groups of 8 keys
-      float s[kKeys / 2];                               // row r0: s[4 n], s[4 n + 1]; r0 + 8: the next two
+      constexpr int kScores = kFlip ? kKeys / 4 : kKeys / 2;
+      // row r0: s[4 n], s[4 n + 1] of key group n; r0 + 8: the next two.
+      // kFlip: s[2 n], s[2 n + 1]: key r0 of group n, rows c0 and c0 + 1
+      float s[kScores];
 #pragma unroll
-      for (int e = 0; e < kKeys / 2; ++e) s[e] = 0.f;
-      {
+      for (int e = 0; e < kScores; ++e) s[e] = 0.f;
+      // score e: its key's place in the tile without the lane's part, and which of the lane's two rows
+      auto key_of = [](int e) { return kFlip ? (e >> 1) * 8 : (e >> 2) * 8 + (e & 1); };
+      auto row_of = [](int e) { return kFlip ? e & 1 : (e >> 1) & 1; };
+      const int lane_key = kFlip ? r0 : c0;
+      if constexpr (kFlip) {
+        float odd[kScores];                             // the other half of the products, for shorter chains
+#pragma unroll
+        for (int e = 0; e < kScores; ++e) odd[e] = 0.f;
+        const int key = (lane & 7) + ((lane >> 4) << 3), part = (lane >> 3) & 1;
+#pragma unroll
+        for (int k = 0; k < kChunks / 2; ++k)
+#pragma unroll
+          for (int x = 0; x < kParts; ++x) {
+            uint32_t b[4];
+            ldsm4(ks + (x * 16 + key) * C::kRowBytes + (((2 * k + part) ^ C::turn(key)) << 4), b);
+            uint32_t lhs[4];
+            codes<C::kInt8, false>(b[0], lhs[0], lhs[2]);
+            codes<C::kInt8, false>(b[2], lhs[1], lhs[3]);
+            mma<F16>(&s[4 * x], lhs, q[2 * k][0], q[2 * k][1]);
+            codes<C::kInt8, false>(b[1], lhs[0], lhs[2]);
+            codes<C::kInt8, false>(b[3], lhs[1], lhs[3]);
+            mma<F16>(&odd[4 * x], lhs, q[2 * k + 1][0], q[2 * k + 1][1]);
+          }
+#pragma unroll
+        for (int e = 0; e < kScores; ++e) s[e] += odd[e];
+      } else {
         // matrices of a load: keys 0-7 and 8-15, two groups of 8 values each
         const int key = (lane & 7) + ((lane >> 4) << 3), part = (lane >> 3) & 1;
 #pragma unroll
@@ -645,39 +845,39 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
       if constexpr (C::k8) {
         const float c = a.score.cap_log2 == 0.f ? c_log2 : 1.f;
 #pragma unroll
-        for (int e = 0; e < kKeys / 2; ++e) s[e] *= meta[e >> 3].x * (unit_q[(e >> 1) & 1] * c);
+        for (int e = 0; e < kScores; ++e) s[e] *= meta[key_of(e) / 16].x * (unit_q[row_of(e)] * c);
       }
       if (a.score.cap_log2 == 0.f) {
         if constexpr (!C::k8) {
 #pragma unroll
-          for (int e = 0; e < kKeys / 2; ++e) s[e] *= c_log2;
+          for (int e = 0; e < kScores; ++e) s[e] *= c_log2;
         }
       } else if (poly_fits(s, a.score.poly_limit)) {
 #pragma unroll
-        for (int e = 0; e < kKeys / 2; e += 2) {
+        for (int e = 0; e < kScores; e += 2) {
           const float2 t = tanh_poly(make_float2(s[e], s[e + 1]), a.score);
           s[e] = t.x * a.score.cap_log2;
           s[e + 1] = t.y * a.score.cap_log2;
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < kKeys / 2; ++e) s[e] = a.score.cap_log2 * tanh_one(s[e], a.score);
+        for (int e = 0; e < kScores; ++e) s[e] = a.score.cap_log2 * tanh_one(s[e], a.score);
       }
       if (a.score.slopes != nullptr) {
 #pragma unroll
         for (int x = 0; x < kParts; ++x) {
           float ahead[2];                               // minus the distance at the lane's first key, exact
 #pragma unroll
-          for (int e = 0; e < 2; ++e) ahead[e] = (float)(key0[C::kPick ? x : 0] + c0 - (limit[e] - 1));
+          for (int e = 0; e < 2; ++e) ahead[e] = (float)(key0[C::kPick ? x : 0] + lane_key - (limit[e] - 1));
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            s[8 * x + e] = fmaf(slope[(e >> 1) & 1], ahead[(e >> 1) & 1] + (float)((C::kPick ? 0 : 16 * x) + (e >> 2) * 8 + (e & 1)), s[8 * x + e]);
+          for (int e = x * kScores / kParts; e < (x + 1) * kScores / kParts; ++e)
+            s[e] = fmaf(slope[row_of(e)], ahead[row_of(e)] + (float)(key_of(e) - (C::kPick ? 16 * x : 0)), s[e]);
         }
       }
       if (hidden) {
 #pragma unroll
-        for (int e = 0; e < kKeys / 2; ++e)
-          s[e] = key0[e >> 3] + ((e >> 2) & 1) * 8 + c0 + (e & 1) < limit[(e >> 1) & 1] ? s[e] : -INFINITY;
+        for (int e = 0; e < kScores; ++e)
+          s[e] = key0[key_of(e) / 16] + key_of(e) % 16 + lane_key < limit[row_of(e)] ? s[e] : -INFINITY;
       }
       float share[C::k8 ? kParts : 1];                  // vs in the output's unit
       if constexpr (C::k8) {
@@ -685,17 +885,67 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
 #pragma unroll
         for (int x = 1; x < kParts; ++x) top = fmaxf(top, meta[x].y);
         if (top > kUnitSlack * unit_v) {
-          const float down = unit_v / top;
-          unit_v = top;
+          const float up = fmaxf(top, 0x1p-120f), down = unit_v / up;
+          unit_v = up;
+          inv_unit_v = 1.f / up;
 #pragma unroll
-          for (int k = 0; k < D / 8; ++k)
+          for (int k = 0; k < kOut; ++k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[k][e] *= down;
         }
-        const float inv = unit_v > 0.f ? 1.f / unit_v : 0.f;
 #pragma unroll
-        for (int x = 0; x < kParts; ++x) share[x] = meta[x].y * inv;
+        for (int x = 0; x < kParts; ++x) share[x] = meta[x].y * inv_unit_v;
       }
+      if constexpr (kFlip) {
+        uint32_t p[kN];                                 // the keys of group n, transposed: right operands
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(s[e], s[2 + e]);
+#pragma unroll
+          for (int n8 = 2; n8 < kN; n8 += 2) mx = ptx::max3(mx, s[2 * n8 + e], s[2 * n8 + 2 + e]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+          if (mx > m[e] + kRescaleLog2) {               // false while the row is empty
+            const float alpha = ptx::ex2(m[e] - mx);    // 0 at the row's first key
+            m[e] = mx;
+            l[e] *= alpha;
+#pragma unroll
+            for (int k = 0; k < kOut; ++k) {
+              o[k][e] *= alpha;
+              o[k][2 + e] *= alpha;
+            }
+          }
+          const float sub = m[e] == -INFINITY ? 0.f : m[e];
+#pragma unroll
+          for (int n8 = 0; n8 < kN; ++n8) s[2 * n8 + e] = ptx::ex2(s[2 * n8 + e] - sub);
+#pragma unroll
+          for (int n8 = 0; n8 < kN; n8 += 2) l[e] += s[2 * n8 + e] + s[2 * n8 + 2 + e];
+        }
+#pragma unroll
+        for (int n8 = 0; n8 < kN; ++n8) {
+          // a scale that is NaN meets only the keys that the row sees
+          const float f = share[n8 / 2];
+          const float f0 = hidden && s[2 * n8] == 0.f ? 0.f : f, f1 = hidden && s[2 * n8 + 1] == 0.f ? 0.f : f;
+          p[n8] = transposed(ptx::pack2<F16>(s[2 * n8] * f0, s[2 * n8 + 1] * f1));
+        }
+        const int key = lane & 15, part = lane >> 4;
+#pragma unroll
+        for (int x = 0; x < kParts; ++x)
+#pragma unroll
+          for (int k = 0; k < kChunks / 2; ++k) {
+            uint32_t b[4];
+            ldsm4t(vs + (x * 16 + key) * C::kRowBytes + (((2 * k + part) ^ C::turn(key)) << 4), b);
+            // a register holds values 2 i, 2 i + 1 of two keys: the even ones are the product's upper rows, the
+            // odd ones its lower
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t lhs[4];
+              codes<C::kInt8, true>(b[2 * e], lhs[0], lhs[1]);
+              codes<C::kInt8, true>(b[2 * e + 1], lhs[2], lhs[3]);
+              mma<F16>(o[2 * k + e], lhs, p[2 * x], p[2 * x + 1]);
+            }
+          }
+      } else {
       uint32_t p[kParts][4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -756,15 +1006,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
           }
       }
     }
-    // ---- the segment's end: join the warps -------------------------------------------------------
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
     }
-    if (lane % 4 == 0) {
-      stat[warp * kRows + r0] = make_float2(m[0], l[0]);
-      stat[warp * kRows + r0 + 8] = make_float2(m[1], l[1]);
+    // ---- the segment's end: join the warps -------------------------------------------------------
+    if constexpr (kFlip) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
+        if (lane < 4) stat[warp * kRows + c0 + e] = make_float2(m[e], l[e]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      }
+      if (lane % 4 == 0) {
+        stat[warp * kRows + r0] = make_float2(m[0], l[0]);
+        stat[warp * kRows + r0 + 8] = make_float2(m[1], l[1]);
+      }
     }
     // the un-normalised output goes to the slot of the warp's last tile, free until its next one:
     // groups of 4 values, their place in a row of D turned by the row against bank conflicts
@@ -772,8 +1032,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
       const int last = take == 0 ? C::kStages - 1 : take - 1;
       if (lane == 0) from[warp] = warp * C::kRing + last * C::kStage;
       __syncwarp();                                     // all lanes have read the tile
-      uint8_t* const to = smem + warp * C::kRing + last * C::kStage + r0 * D * 4;
-      if constexpr (!C::k8) {
+      uint8_t* const to = smem + warp * C::kRing + last * C::kStage + (kFlip ? c0 : r0) * D * 4;
+      if constexpr (kFlip) {
+#pragma unroll
+        for (int j = 0; j < kOut; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float2*>(to + e * D * 4 + ((4 * j + r0 / 2) ^ (c0 + e)) * 16 + (r0 & 1) * 8) =
+                make_float2(o[j][e] * unit_v, o[j][2 + e] * unit_v);
+      } else if constexpr (!C::k8) {
 #pragma unroll
         for (int k = 0; k < D / 8; ++k) {
           const int at4 = ((2 * k + (lane % 4) / 2) ^ r0) * 16 + (lane & 1) * 8;
@@ -797,11 +1064,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
     const int row0 = seg.block * kRows, n_rows = min(kRows, rows - row0);
     const int64_t qrow = ((int64_t)seg.b * a.H + seg.hk * G) * a.T + row0;
     const bool whole = n == seg.tiles;
-    const int seg_s0 = s0, seg_tiles = seg.tiles;
     turn = (turn + n) % kWarps;
-    s0 += seg.tiles + kSegment;
+    s0 += seg.tiles + C::kSegment;
     seg.tile = 0;
-    if (s0 + kSegment < end) {
+    if (s0 + C::kSegment < end) {
       seg.next(a, blocks);
       read_rows();
     }
@@ -838,92 +1104,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_kernel(const Paged
         if (c == 0) __stcg(&a.ml_part[part], make_float2(mx, sum));
       }
     }
+    if (kShared && C::kDefer && !whole && threadIdx.x == 0) *flag |= first_seg ? 1 : 2;
     const bool was_first = first_seg;
     first_seg = false;
-    if (kShared && !whole) {
-      // One of several CTAs with tiles of this segment: the one that comes last joins their parts, in
-      // the order of the tiles.
-      const Shares share(units, n_ctas);
-      const int ca = share.owner(seg_s0 + kSegment), cb = share.owner(seg_s0 + kSegment + seg_tiles - 1);
-      // the first CTA may have begun inside an earlier segment: this one is then its second part
-      const int part0 = 2 * ca + (share.begin(ca) >= seg_s0 ? 0 : 1);
-      __syncthreads();
-      if (warp == 0) {
-        const bool last = all_arrived(a.arrivals, 2 * (int)blockIdx.x + (was_first ? 0 : 1), part0, ca, cb, a.call);
-        if (lane == 0) *flag = last ? 1 : 0;
-      }
-      __syncthreads();
-      if (*flag != 0) {
-        for (int i = ca + threadIdx.x; i <= cb; i += kThreads) a.arrivals[i == ca ? part0 : 2 * i] = 0ull;
-        // Up to kJoin parts at a time: their statistics to shared memory, all in flight together, then
-        // their outputs, sixteen in flight, onto what the parts before came to.
-        auto part_of = [&](int i) { return (int64_t)(i == ca ? part0 : 2 * i) * kRows; };
-        constexpr int kItems = (kRows * kQuads + kThreads - 1) / kThreads;
-        float mx[kItems], sum[kItems];
-        float4 acc[kItems];
-#pragma unroll
-        for (int y = 0; y < kItems; ++y) {
-          mx[y] = -INFINITY;
-          sum[y] = 0.f;
-          acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll 1
-        for (int i0 = ca; i0 <= cb; i0 += C::kJoin) {
-          const int np = min(C::kJoin, cb + 1 - i0);
-          // sixteen parts' outputs of item x; past the last part its own again, not used
-          auto outputs = [&](int x, int i, float4 (&v)[16]) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              v[k] = __ldcg(reinterpret_cast<const float4*>(a.o_part + (part_of(i0 + min(i + k, np - 1)) + x / kQuads) * D +
-                                                            x % kQuads * 4));
-          };
-          float4 v[16];
-          if (threadIdx.x < n_rows * kQuads) outputs(threadIdx.x, 0, v);    // under way with the statistics
-          __syncthreads();
-          for (int x = threadIdx.x; x < np * kRows; x += kThreads)
-            joined[x] = __ldcg(&a.ml_part[part_of(i0 + x / kRows) + x % kRows]);
-          __syncthreads();
-#pragma unroll
-          for (int y = 0; y < kItems; ++y) {
-            const int x = threadIdx.x + y * kThreads;
-            if (x >= n_rows * kQuads) break;
-            const int r = x / kQuads;
-            float m_new = mx[y];
-            for (int i = 0; i < np; ++i) m_new = fmaxf(m_new, joined[i * kRows + r].x);
-            // no key of the row so far, and none that is NaN, where the maximum is still -inf
-            const float keep = mx[y] == m_new ? 1.f : ptx::ex2(mx[y] - m_new);
-            mx[y] = m_new;
-            sum[y] *= keep;
-            acc[y].x *= keep;
-            acc[y].y *= keep;
-            acc[y].z *= keep;
-            acc[y].w *= keep;
-            for (int i = 0; i < np; i += 16) {
-              if (y > 0 || i > 0) outputs(x, i, v);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const float2 ml = joined[min(i + k, np - 1) * kRows + r];
-                if (i + k >= np || ml.y == 0.f) continue;     // no part, or no key of the row in it
-                const float f = ptx::ex2(ml.x - m_new);
-                sum[y] = fmaf(f, ml.y, sum[y]);
-                acc[y].x = fmaf(f, v[k].x, acc[y].x);
-                acc[y].y = fmaf(f, v[k].y, acc[y].y);
-                acc[y].z = fmaf(f, v[k].z, acc[y].z);
-                acc[y].w = fmaf(f, v[k].w, acc[y].w);
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (int y = 0; y < kItems; ++y) {
-          const int x = threadIdx.x + y * kThreads;
-          if (x < n_rows * kQuads) write_row4<C>(a, qrow + x / kQuads, x % kQuads * 4, acc[y], sum[y], mx[y]);
-        }
-      }
-    }
+    if (s0 + C::kSegment < end) convert_rows();
     __syncthreads();                                    // the slots and statistics may be written again
+    if constexpr (kShared && !C::kDefer)
+      if (!whole) finish(was_first ? 1 : 2);
+    if (s0 + C::kSegment < end) note_parted(1);
   }
   cp_wait<0>();
+  if constexpr (kShared && C::kDefer) {
+    const int mine = *flag;
+    __syncthreads();                                    // the word is written again
+    if (mine != 0) finish(mine);
+  }
 }
 
 template <typename C, bool kShared>
@@ -939,9 +1134,23 @@ cudaError_t launch(const PagedArgs& a, int grid, cudaStream_t s) {
 template <typename C>
 cudaError_t paged(const PagedArgs& a, cudaStream_t s) {
   const int rows = a.H / a.Hkv * a.T;
-  const int64_t segments = (int64_t)a.B * a.Hkv * ((rows + kRows - 1) / kRows);
+  const int64_t segments = (int64_t)a.B * a.Hkv * ((rows + C::kRows - 1) / C::kRows);
   if (!paged_shares(a.B, a.Hkv, rows, paged_span(a), a.ctas)) return launch<C, false>(a, (int)segments, s);
   return launch<C, true>(a, a.ctas, s);
+}
+
+// 8-bit pages: up to 8 rows of a group as columns of the products.
+template <int D, int kStore, bool kPick>
+cudaError_t paged8(const PagedArgs& a, cudaStream_t s) {
+  if (a.H / a.Hkv * a.T > 8) return paged<Cfg<D, kStore, true, kPick>>(a, s);
+  PagedArgs f = a;
+  f.ctas = a.ctas / kCtasPerSm * kFlipCtasPerSm;
+  return paged<Cfg<D, kStore, true, kPick, true>>(f, s);
+}
+template <int kStore>
+cudaError_t paged8(const PagedArgs& a, cudaStream_t s) {
+  if (a.pages != nullptr) return a.d == 64 ? paged8<64, kStore, true>(a, s) : paged8<128, kStore, true>(a, s);
+  return a.d == 64 ? paged8<64, kStore, false>(a, s) : paged8<128, kStore, false>(a, s);
 }
 
 }  // namespace
