@@ -22,6 +22,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fa_paged.cuh"
 #include "fa_rotate.cuh"
@@ -31,8 +32,9 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kHold = 2;                   // rows of 16 values that a thread keeps between the two passes
+constexpr int kThreads = 256;              // few tokens: eight warps
+constexpr int kHold = 2;                   // rows of 16 values that a lane of them holds
+constexpr int kPageRows = 4;               // ... and a thread of a block for many tokens
 
 template <typename T>
 __device__ __forceinline__ void round_values(float (&x)[8]) {
@@ -95,23 +97,24 @@ __device__ __forceinline__ bool page_work(const AppendArgs& a, int b, int p, Pag
   w->n = (int)min((int64_t)len, start + size) - w->first;
   w->kept = w->first - (int)start;
   w->page = a.cache.table[b * a.cache.table_stride + lead];
-  if ((uint64_t)w->page >= (uint64_t)a.cache.n_pages) {        // reported, not followed
-    atomicExch(a.err, kDevBadOffsets);
-    return false;
-  }
   return true;
 }
+// Whether the page exists (asked once the tokens' reads are on their way).
+__device__ __forceinline__ bool page_exists(const AppendArgs& a, const PageWork& w) {
+  if ((uint64_t)w.page < (uint64_t)a.cache.n_pages) return true;
+  atomicExch(a.err, kDevBadOffsets);                           // reported, not followed
+  return false;
+}
 
-template <typename T, int kStore, int kTeam>
-__device__ __forceinline__ void write_page(const AppendArgs& a, const StoreArgs& st, const PageWork& w, int b, int h0,
-                                           int h1, uint32_t* amax_smem, float (*bound_smem)[2][128]) {
+// One head of a page that gets a few tokens, by a warp: kHold rows of 16 values a lane.
+template <typename T, int kStore>
+__device__ __forceinline__ void write_rows(const AppendArgs& a, const StoreArgs& st, const PageWork& w, int b, int h) {
   constexpr bool k8 = kStore != FA_PAGES_16BIT;
-  const int lt = threadIdx.x % kTeam;
-  const int units = a.d / kUnit, rows = kTeam / units;
+  const int lt = threadIdx.x % 32;
+  const int units = a.d / kUnit, rows = 32 / units;
   const int u = lt % units, r = lt / units;
   const Unit t = unit_of(u, a.rot);
-  const bool turns = t.turns && h0 < a.Hkv;
-  const int iters = (w.n + rows - 1) / rows;
+  const bool turns = t.turns && h < a.Hkv;
   uint64_t frac[8];
   float c[kHold][8], s[kHold][8];
   if (turns) {
@@ -119,206 +122,477 @@ __device__ __forceinline__ void write_page(const AppendArgs& a, const StoreArgs&
     for (int i = 0; i < 8; ++i) frac[i] = turn_fraction(a.rot.inv_freq[8 * u + i]);
 #pragma unroll
     for (int i = 0; i < kHold; ++i)
-      if (i < iters) angles(frac, w.first + i * rows + r, a.rot, c[i], s[i]);
+      if (i * rows + r < w.n) angles(frac, w.first + i * rows + r, a.rot, c[i], s[i]);
   }
-#pragma unroll 1
-  for (int h = h0; h < h1; ++h) {
-    const bool is_k = h < a.Hkv;
-    const int g = is_k ? h : h - a.Hkv;
-    const Strides sd = is_k ? a.ks : a.vs;
-    const T* const src = static_cast<const T*>(is_k ? a.k : a.v) + b * sd.b + g * sd.h + (int64_t)(w.first - w.begin) * sd.n;
-    float* const scales = is_k ? st.k_scales : st.v_scales;
-    const int64_t place = w.page * a.Hkv + g;
-    float old = 0.f, old_unit = 0.f;
-    if (k8 && w.kept > 0) old = scales[place];
-    const bool bounds = is_k && st.bounds != nullptr;
-    if (bounds && w.kept > 0) old_unit = st.bound_scales[place];
+  const bool is_k = h < a.Hkv;
+  const int g = is_k ? h : h - a.Hkv;
+  const Strides sd = is_k ? a.ks : a.vs;
+  const T* const src = static_cast<const T*>(is_k ? a.k : a.v) + b * sd.b + g * sd.h + (int64_t)(w.first - w.begin) * sd.n;
+  float* const scales = is_k ? st.k_scales : st.v_scales;
+  const int64_t place = w.page * a.Hkv + g;
+  float old = 0.f, old_unit = 0.f;
+  if (k8 && w.kept > 0) old = scales[place];
+  const bool bounds = is_k && st.bounds != nullptr;
+  if (bounds && w.kept > 0) old_unit = st.bound_scales[place];
 
-    // a row's 16 values: read, turned
-    auto row = [&](int i, float (&x)[8], float (&y)[8], bool held) {
-      const T* p = src + (int64_t)(i * rows + r) * sd.n;
-      const Raw8<T> lo = load8(p + t.lo), hi = load8(p + t.hi);
-      unpack(lo, x);
-      unpack(hi, y);
-      if (turns && is_k) {
-        if (held) {
-          turn8(x, y, a.rot.interleaved, c[i < kHold ? i : 0], s[i < kHold ? i : 0]);
+  // a row's 16 values: read, turned
+  auto row = [&](int i, float (&x)[8], float (&y)[8]) {
+    const T* p = src + (int64_t)(i * rows + r) * sd.n;
+    const Raw8<T> lo = load8(p + t.lo), hi = load8(p + t.hi);
+    unpack(lo, x);
+    unpack(hi, y);
+    if (turns && is_k) {
+      turn8(x, y, a.rot.interleaved, c[i], s[i]);
+      if (!k8) {                                       // 16-bit pages: bounds of what is stored
+        round_values<T>(x);
+        round_values<T>(y);
+      }
+    }
+  };
+  float x[kHold][8], y[kHold][8];
+  uint32_t amax = 0;
+  float mn[2][8], mx[2][8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    mn[0][e] = mn[1][e] = INFINITY;
+    mx[0][e] = mx[1][e] = -INFINITY;
+  }
+  auto look = [&](const float (&x)[8], const float (&y)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = max(amax, max(abs_bits(x[e]), abs_bits(y[e])));
+    if (bounds) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        mn[0][e] = fminf(mn[0][e], x[e]);
+        mx[0][e] = fmaxf(mx[0][e], x[e]);
+        mn[1][e] = fminf(mn[1][e], y[e]);
+        mx[1][e] = fmaxf(mx[1][e], y[e]);
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    if (i * rows + r < w.n) {
+      row(i, x[i], y[i]);
+      look(x[i], y[i]);
+    }
+
+  // the team's largest value and bounds
+  if (k8 || bounds) {
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    if (bounds) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float& lo = mn[e / 8][e % 8];
+        float& hi = mx[e / 8][e % 8];
+        for (int o = 16; o >= units; o >>= 1) {
+          lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+          hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+      }
+    }
+    __syncwarp();
+  }
+  const bool finite = amax < 0x7f800000u;
+
+  // codes
+  typename StoredAs<T, kStore>::type* const dst =
+      static_cast<typename StoredAs<T, kStore>::type*>(is_k ? a.cache.k : a.cache.v) + w.page * a.cache.page_stride +
+      g * a.cache.head_stride;
+  float inv = 0.f, scale = 0.f;
+  if constexpr (k8) {
+    const float need = finite ? power_scale<kStore == FA_PAGES_INT8>(amax) : __uint_as_float(0x7fc00000u);
+    scale = old != old || need != need ? __uint_as_float(0x7fc00000u) : fmaxf(old, need);
+    inv = scale == scale ? 1.f / scale : 0.f;
+  }
+  auto store = [&](int i, float (&x)[8], float (&y)[8]) {
+    auto* p = dst + (int64_t)(w.kept + i * rows + r) * a.cache.token_stride;
+    if constexpr (k8) {
+      if (scale != scale) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
+      }
+      *reinterpret_cast<uint2*>(p + t.lo) = encode8<kStore>(x, inv);
+      *reinterpret_cast<uint2*>(p + t.hi) = encode8<kStore>(y, inv);
+    } else {
+      Raw8<T> lo, hi;
+      pack(x, lo);
+      pack(y, hi);
+      store8(p + t.lo, lo);
+      store8(p + t.hi, hi);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    if (i * rows + r < w.n) store(i, x[i], y[i]);
+  if constexpr (k8) {
+    if (w.kept > 0 && scale > old) {                  // (not where either is NaN)
+      const float ratio = old / scale;
+      for (int i = r; i < w.kept; i += rows) {
+        uint4* p = reinterpret_cast<uint4*>(dst + (int64_t)i * a.cache.token_stride + kUnit * u);
+        uint4 v = *p;
+        v.x = recode<kStore>(v.x, ratio);
+        v.y = recode<kStore>(v.y, ratio);
+        v.z = recode<kStore>(v.z, ratio);
+        v.w = recode<kStore>(v.w, ratio);
+        *p = v;
+      }
+    }
+    if (lt == 0) scales[place] = scale;
+  }
+  if (bounds && lt < units) {
+    const float need = finite ? power_scale<true>(amax) : __uint_as_float(0x7fc00000u);
+    const float unit = old_unit != old_unit || need != need ? __uint_as_float(0x7fc00000u) : fmaxf(old_unit, need);
+    const float by = unit == unit ? 1.f / unit : 0.f, ratio = w.kept > 0 && unit == unit ? old_unit / unit : 0.f;
+    int8_t* const q = st.bounds + place * 2 * a.d;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int at = half == 0 ? t.lo : t.hi;
+      int lo[8], hi[8];
+      uint2* const plo = reinterpret_cast<uint2*>(q + at);
+      uint2* const phi = reinterpret_cast<uint2*>(q + a.d + at);
+      const uint2 was_lo = w.kept > 0 ? *plo : make_uint2(0u, 0u), was_hi = w.kept > 0 ? *phi : make_uint2(0u, 0u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        lo[e] = down(mn[half][e], by);
+        hi[e] = -down(-mx[half][e], by);
+        if (w.kept > 0) {
+          lo[e] = min(lo[e], down((float)(int8_t)((e < 4 ? was_lo.x : was_lo.y) >> (8 * (e & 3))), ratio));
+          hi[e] = max(hi[e], -down(-(float)(int8_t)((e < 4 ? was_hi.x : was_hi.y) >> (8 * (e & 3))), ratio));
+        }
+      }
+      *plo = make_uint2(pack_s8(lo[0], lo[1], lo[2], lo[3]), pack_s8(lo[4], lo[5], lo[6], lo[7]));
+      *phi = make_uint2(pack_s8(hi[0], hi[1], hi[2], hi[3]), pack_s8(hi[4], hi[5], hi[6], hi[7]));
+    }
+    if (lt == 0) st.bound_scales[place] = unit;
+  }
+}
+
+// ---- many tokens: a block for each page and head -----------------------------------------------------
+
+// 16 values of a row as they lie in memory: pairs of 16-bit values, or fp32 where they are turned.
+template <typename T> struct Pair;
+template <> struct Pair<__nv_bfloat16> {
+  using type = __nv_bfloat162;
+  static __device__ __forceinline__ float2 values(uint32_t x) { return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)); }
+};
+template <> struct Pair<__half> {
+  using type = __half2;
+  static __device__ __forceinline__ float2 values(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
+};
+template <typename T>
+__device__ __forceinline__ uint32_t least(uint32_t a, uint32_t b) {
+  using P = typename Pair<T>::type;
+  const P r = __hmin2(*reinterpret_cast<P*>(&a), *reinterpret_cast<P*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) {
+  using P = typename Pair<T>::type;
+  const P r = __hmax2(*reinterpret_cast<P*>(&a), *reinterpret_cast<P*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// the fp32 bits of the larger of two 16-bit values without signs
+template <typename T>
+__device__ __forceinline__ uint32_t larger_bits(uint32_t x) {
+  const uint32_t m = max(x & 0xffffu, x >> 16);
+  return __float_as_uint(Pair<T>::values(m).x);
+}
+
+// Four values times inv (a power of two's inverse, products within +-127.5) to int8: adding 1.5 * 2^23 rounds
+// to a whole number, ties to even, whose low byte is the code.
+__device__ __forceinline__ uint32_t quick_s8(float a, float b, float c, float d, float inv) {
+  constexpr float kMagic = 12582912.f;
+  const uint32_t x = __float_as_uint(fmaf(a, inv, kMagic)), y = __float_as_uint(fmaf(b, inv, kMagic));
+  const uint32_t z = __float_as_uint(fmaf(c, inv, kMagic)), w = __float_as_uint(fmaf(d, inv, kMagic));
+  return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
+}
+template <int kStore>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
+  if constexpr (kStore == FA_PAGES_INT8) return quick_s8(a, b, c, d, inv);
+  else return pack_e4m3(a * inv, b * inv, c * inv, d * inv);
+}
+
+// kThr threads hold kRows rows of 16 values each: 128 threads 64 tokens of d = 128, or 128 of d = 64.  Several
+// blocks share an SM, so one's barrier and writes hide behind the others' reads.  Pages of more tokens than the
+// block holds are read twice.  kTurn: key heads are turned (value heads take the path of 16-bit values).
+template <typename T, int kStore, bool kTurn, bool kBounds, int kThr, int kRows>
+__device__ __forceinline__ void write_page(const AppendArgs& a, const StoreArgs& st, int b, int p, int h, uint32_t* smem) {
+  constexpr bool k8 = kStore != FA_PAGES_16BIT;
+  constexpr int kWarps = kThr / 32;
+  uint32_t* const amax_smem = smem;                        // [kWarps]
+  uint32_t* const bound_smem = smem + kWarps;              // [2][kWarps][d], or of pairs
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int units = a.d / kUnit, rows = kThr / units;
+  const int u = threadIdx.x % units, r = threadIdx.x / units;
+  const Unit t = kTurn ? unit_of(u, a.rot) : Unit{kUnit * u, kUnit * u + 8, false};
+  const bool is_k = h < a.Hkv;
+  const int g = is_k ? h : h - a.Hkv;
+  PageWork w;
+  if (!page_work(a, b, p, &w)) return;
+  const Strides sd = is_k ? a.ks : a.vs;
+  const T* const src = static_cast<const T*>(is_k ? a.k : a.v) + b * sd.b + g * sd.h + (int64_t)(w.first - w.begin) * sd.n;
+  const int64_t place = w.page * a.Hkv + g;
+  float* const scales = is_k ? st.k_scales : st.v_scales;
+  const bool bounds = kBounds && is_k;
+
+  // a row: eight pairs of 16-bit values, or 16 values in fp32
+  using Word = std::conditional_t<kTurn, float, uint32_t>;
+  constexpr int kWords = kTurn ? 16 : 8;
+  uint64_t frac[kTurn ? 8 : 1];
+  if constexpr (kTurn) {
+    if (t.turns) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) frac[i] = turn_fraction(a.rot.inv_freq[8 * u + i]);
+    }
+  }
+  auto read = [&](int i, Raw8<T>& lo, Raw8<T>& hi) {
+    const T* q = src + (int64_t)(i * rows + r) * sd.n;
+    lo = load8(q + t.lo);
+    hi = load8(q + t.hi);
+  };
+  auto take = [&](int i, const Raw8<T>& lo, const Raw8<T>& hi, Word (&x)[kWords]) {
+    if constexpr (kTurn) {
+      float p0[8], p1[8];
+      unpack(lo, p0);
+      unpack(hi, p1);
+      if (t.turns) {
+        float c[8], s[8];
+        angles(frac, w.first + i * rows + r, a.rot, c, s);
+        turn8(p0, p1, a.rot.interleaved, c, s);
+        if (!k8) {                                         // 16-bit pages: bounds of what is stored
+          round_values<T>(p0);
+          round_values<T>(p1);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] = p0[e];
+        x[8 + e] = p1[e];
+      }
+    } else {
+      const uint32_t v[8] = {lo.w[0].x, lo.w[0].y, lo.w[0].z, lo.w[0].w, hi.w[0].x, hi.w[0].y, hi.w[0].z, hi.w[0].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = v[e];
+    }
+  };
+  uint32_t amax = 0;
+  Word mn[kBounds ? kWords : 1], mx[kBounds ? kWords : 1];
+  bool any = false;
+  auto look = [&](const Word (&x)[kWords]) {
+#pragma unroll
+    for (int e = 0; e < kWords; ++e) {
+      if constexpr (kTurn) amax = max(amax, abs_bits(x[e]));
+      else amax = max_u16x2(amax, x[e] & 0x7fff7fffu);
+    }
+    if constexpr (kBounds) {
+      if (bounds) {
+#pragma unroll
+        for (int e = 0; e < kWords; ++e) {
+          if constexpr (kTurn) {
+            mn[e] = any ? fminf(mn[e], x[e]) : x[e];
+            mx[e] = any ? fmaxf(mx[e], x[e]) : x[e];
+          } else {
+            mn[e] = any ? least<T>(mn[e], x[e]) : x[e];
+            mx[e] = any ? most<T>(mx[e], x[e]) : x[e];
+          }
+        }
+        any = true;
+      }
+    }
+  };
+  Word x[kRows][kWords];
+  {
+    Raw8<T> lo[kRows], hi[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (i * rows + r < w.n) read(i, lo[i], hi[i]);
+    if (!page_exists(a, w)) return;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (i * rows + r < w.n) {
+        take(i, lo[i], hi[i], x[i]);
+        look(x[i]);
+      }
+  }
+  for (int i = kRows; i * rows + r < w.n; ++i) {
+    Raw8<T> lo, hi;
+    Word y[kWords];
+    read(i, lo, hi);
+    take(i, lo, hi, y);
+    look(y);
+  }
+  float old = 0.f, old_unit = 0.f;
+  if (k8 && w.kept > 0) old = scales[place];
+  if (bounds && w.kept > 0) old_unit = st.bound_scales[place];
+
+  // the page's largest value, and its bounds
+  if constexpr (!kTurn) amax = larger_bits<T>(amax);
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  if (lane == 0) amax_smem[warp] = amax;
+  if constexpr (kBounds) {
+    if (bounds) {
+      // threads without a row: +inf, -inf
+      const uint32_t inf = kTurn ? 0x7f800000u : std::is_same_v<T, __half> ? 0x7c007c00u : 0x7f807f80u;
+      const uint32_t sign = kTurn ? 0x80000000u : 0x80008000u;
+#pragma unroll
+      for (int e = 0; e < kWords; ++e) {
+        if constexpr (kTurn) {
+          mn[e] = any ? mn[e] : __uint_as_float(inf);
+          mx[e] = any ? mx[e] : __uint_as_float(inf | sign);
         } else {
-          float cc[8], ss[8];
-          angles(frac, w.first + i * rows + r, a.rot, cc, ss);
-          turn8(x, y, a.rot.interleaved, cc, ss);
+          mn[e] = any ? mn[e] : inf;
+          mx[e] = any ? mx[e] : inf | sign;
         }
-        if (!k8) {                                       // 16-bit pages: bounds of what is stored
-          round_values<T>(x);
-          round_values<T>(y);
-        }
-      }
-    };
-    float x[kHold][8], y[kHold][8];
-    uint32_t amax = 0;
-    float mn[2][8], mx[2][8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      mn[0][e] = mn[1][e] = INFINITY;
-      mx[0][e] = mx[1][e] = -INFINITY;
-    }
-    auto look = [&](const float (&x)[8], const float (&y)[8]) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = max(amax, max(abs_bits(x[e]), abs_bits(y[e])));
-      if (bounds) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          mn[0][e] = fminf(mn[0][e], x[e]);
-          mx[0][e] = fmaxf(mx[0][e], x[e]);
-          mn[1][e] = fminf(mn[1][e], y[e]);
-          mx[1][e] = fmaxf(mx[1][e], y[e]);
-        }
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < kHold; ++i)
-      if (i * rows + r < w.n) {
-        row(i, x[i], y[i], true);
-        look(x[i], y[i]);
-      }
-    for (int i = kHold; i < iters; ++i)
-      if (i * rows + r < w.n) {
-        float xx[8], yy[8];
-        row(i, xx, yy, false);
-        look(xx, yy);
-      }
-
-    // the team's largest value and bounds
-    if (k8 || bounds) {
-      amax = __reduce_max_sync(0xffffffffu, amax);
-      if (bounds) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float& lo = mn[e / 8][e % 8];
-          float& hi = mx[e / 8][e % 8];
-          for (int o = 16; o >= units; o >>= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        for (int o = 16; o >= units; o >>= 1) {
+          if constexpr (kTurn) {
+            mn[e] = fminf(mn[e], __shfl_xor_sync(0xffffffffu, mn[e], o));
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
+          } else {
+            mn[e] = least<T>(mn[e], __shfl_xor_sync(0xffffffffu, mn[e], o));
+            mx[e] = most<T>(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
           }
         }
       }
-      if constexpr (kTeam > 32) {
-        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-        if (lane == 0) amax_smem[warp] = amax;
-        if (bounds && lane < units) {
+      if (lane < units) {
+        const int words = kTurn ? a.d : a.d / 2;
+        uint32_t* const lo = bound_smem + warp * words;
+        uint32_t* const hi = lo + kWarps * words;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            bound_smem[warp][0][t.lo + e] = mn[0][e];
-            bound_smem[warp][0][t.hi + e] = mn[1][e];
-            bound_smem[warp][1][t.lo + e] = mx[0][e];
-            bound_smem[warp][1][t.hi + e] = mx[1][e];
-          }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kTeam / 32; ++i) amax = max(amax, amax_smem[i]);
-        if (bounds && lt < units) {
-#pragma unroll 1
-          for (int i = 1; i < kTeam / 32; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              mn[0][e] = fminf(mn[0][e], bound_smem[i][0][t.lo + e]);
-              mn[1][e] = fminf(mn[1][e], bound_smem[i][0][t.hi + e]);
-              mx[0][e] = fmaxf(mx[0][e], bound_smem[i][1][t.lo + e]);
-              mx[1][e] = fmaxf(mx[1][e], bound_smem[i][1][t.hi + e]);
-            }
+        for (int e = 0; e < kWords; ++e) {
+          const int at = kTurn ? (e < 8 ? t.lo + e : t.hi + e - 8) : 8 * u + e;
+          lo[at] = reinterpret_cast<const uint32_t&>(mn[e]);
+          hi[at] = reinterpret_cast<const uint32_t&>(mx[e]);
         }
       }
-      __syncwarp();
     }
-    const bool finite = amax < 0x7f800000u;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) amax = max(amax, amax_smem[i]);
+  const bool finite = amax < 0x7f800000u;
 
-    // codes
-    typename StoredAs<T, kStore>::type* const dst =
-        static_cast<typename StoredAs<T, kStore>::type*>(is_k ? a.cache.k : a.cache.v) + w.page * a.cache.page_stride +
-        g * a.cache.head_stride;
-    float inv = 0.f, scale = 0.f;
+  // codes
+  using Elem = typename StoredAs<T, kStore>::type;
+  Elem* const dst = static_cast<Elem*>(is_k ? a.cache.k : a.cache.v) + w.page * a.cache.page_stride + g * a.cache.head_stride;
+  float inv = 0.f, scale = 0.f;
+  if constexpr (k8) {
+    const float need = finite ? power_scale<kStore == FA_PAGES_INT8>(amax) : __uint_as_float(0x7fc00000u);
+    scale = old != old || need != need ? __uint_as_float(0x7fc00000u) : fmaxf(old, need);
+    inv = 1.f / scale;
+  }
+  auto store = [&](int i, const Word (&x)[kWords]) {
+    Elem* const q = dst + (int64_t)(w.kept + i * rows + r) * a.cache.token_stride;
     if constexpr (k8) {
-      const float need = finite ? power_scale<kStore == FA_PAGES_INT8>(amax) : __uint_as_float(0x7fc00000u);
-      scale = old != old || need != need ? __uint_as_float(0x7fc00000u) : fmaxf(old, need);
-      inv = scale == scale ? 1.f / scale : 0.f;
-    }
-    auto store = [&](int i, float (&x)[8], float (&y)[8]) {
-      auto* p = dst + (int64_t)(w.kept + i * rows + r) * a.cache.token_stride;
-      if constexpr (k8) {
-        if (scale != scale) {
+      uint32_t c[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (kTurn) {
+          c[e] = encode4<kStore>(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3], inv);
+        } else {
+          const float2 y = Pair<T>::values(x[2 * e]), z = Pair<T>::values(x[2 * e + 1]);
+          c[e] = encode4<kStore>(y.x, y.y, z.x, z.y, inv);
         }
-        *reinterpret_cast<uint2*>(p + t.lo) = encode8<kStore>(x, inv);
-        *reinterpret_cast<uint2*>(p + t.hi) = encode8<kStore>(y, inv);
+        if (scale != scale) c[e] = 0u;
+      }
+      if constexpr (kTurn) {
+        *reinterpret_cast<uint2*>(q + t.lo) = make_uint2(c[0], c[1]);
+        *reinterpret_cast<uint2*>(q + t.hi) = make_uint2(c[2], c[3]);
       } else {
-        Raw8<T> lo, hi;
-        pack(x, lo);
-        pack(y, hi);
-        store8(p + t.lo, lo);
-        store8(p + t.hi, hi);
+        *reinterpret_cast<uint4*>(q + t.lo) = make_uint4(c[0], c[1], c[2], c[3]);
       }
-    };
+    } else if constexpr (kTurn) {
+      float p0[8], p1[8];
 #pragma unroll
-    for (int i = 0; i < kHold; ++i)
-      if (i * rows + r < w.n) store(i, x[i], y[i]);
-    for (int i = kHold; i < iters; ++i)
-      if (i * rows + r < w.n) {
-        float xx[8], yy[8];
-        row(i, xx, yy, false);
-        store(i, xx, yy);
+      for (int e = 0; e < 8; ++e) {
+        p0[e] = x[e];
+        p1[e] = x[8 + e];
       }
-    if constexpr (k8) {
-      if (w.kept > 0 && scale > old) {                  // (not where either is NaN)
-        const float ratio = old / scale;
-        for (int i = r; i < w.kept; i += rows) {
-          uint4* p = reinterpret_cast<uint4*>(dst + (int64_t)i * a.cache.token_stride + kUnit * u);
-          uint4 v = *p;
-          v.x = recode<kStore>(v.x, ratio);
-          v.y = recode<kStore>(v.y, ratio);
-          v.z = recode<kStore>(v.z, ratio);
-          v.w = recode<kStore>(v.w, ratio);
-          *p = v;
-        }
-      }
-      if (lt == 0) scales[place] = scale;
+      Raw8<T> lo, hi;
+      pack(p0, lo);
+      pack(p1, hi);
+      store8(q + t.lo, lo);
+      store8(q + t.hi, hi);
+    } else {
+      *reinterpret_cast<uint4*>(q + t.lo) = make_uint4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<uint4*>(q + t.hi) = make_uint4(x[4], x[5], x[6], x[7]);
     }
-    if (bounds && lt < units) {
+  };
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    if (i * rows + r < w.n) store(i, x[i]);
+  for (int i = kRows; i * rows + r < w.n; ++i) {
+    Raw8<T> lo, hi;
+    Word y[kWords];
+    read(i, lo, hi);
+    take(i, lo, hi, y);
+    store(i, y);
+  }
+  if constexpr (k8) {
+    if (w.kept > 0 && scale > old) {                       // (not where either is NaN)
+      const float ratio = old / scale;
+      for (int i = r; i < w.kept; i += rows) {
+        uint4* q = reinterpret_cast<uint4*>(dst + (int64_t)i * a.cache.token_stride + kUnit * u);
+        uint4 v = *q;
+        v.x = recode<kStore>(v.x, ratio);
+        v.y = recode<kStore>(v.y, ratio);
+        v.z = recode<kStore>(v.z, ratio);
+        v.w = recode<kStore>(v.w, ratio);
+        *q = v;
+      }
+    }
+    if (threadIdx.x == 0) scales[place] = scale;
+  }
+  if constexpr (kBounds) {
+    if (bounds && threadIdx.x < a.d / 2) {                 // two of the d values to a thread
+      const int words = kTurn ? a.d : a.d / 2;
+      float lo[2], hi[2];
+#pragma unroll 1
+      for (int i = 0; i < kWarps; ++i) {
+        const uint32_t* const q = bound_smem + i * words;
+        float2 l, m;
+        if constexpr (kTurn) {
+          l = reinterpret_cast<const float2*>(q)[threadIdx.x];
+          m = reinterpret_cast<const float2*>(q + kWarps * words)[threadIdx.x];
+        } else {
+          l = Pair<T>::values(q[threadIdx.x]);
+          m = Pair<T>::values(q[kWarps * words + threadIdx.x]);
+        }
+        lo[0] = i == 0 ? l.x : fminf(lo[0], l.x);
+        lo[1] = i == 0 ? l.y : fminf(lo[1], l.y);
+        hi[0] = i == 0 ? m.x : fmaxf(hi[0], m.x);
+        hi[1] = i == 0 ? m.y : fmaxf(hi[1], m.y);
+      }
       const float need = finite ? power_scale<true>(amax) : __uint_as_float(0x7fc00000u);
       const float unit = old_unit != old_unit || need != need ? __uint_as_float(0x7fc00000u) : fmaxf(old_unit, need);
       const float by = unit == unit ? 1.f / unit : 0.f, ratio = w.kept > 0 && unit == unit ? old_unit / unit : 0.f;
-      int8_t* const q = st.bounds + place * 2 * a.d;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int at = half == 0 ? t.lo : t.hi;
-        int lo[8], hi[8];
-        uint2* const plo = reinterpret_cast<uint2*>(q + at);
-        uint2* const phi = reinterpret_cast<uint2*>(q + a.d + at);
-        const uint2 was_lo = w.kept > 0 ? *plo : make_uint2(0u, 0u), was_hi = w.kept > 0 ? *phi : make_uint2(0u, 0u);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          lo[e] = down(mn[half][e], by);
-          hi[e] = -down(-mx[half][e], by);
-          if (w.kept > 0) {
-            lo[e] = min(lo[e], down((float)(int8_t)((e < 4 ? was_lo.x : was_lo.y) >> (8 * (e & 3))), ratio));
-            hi[e] = max(hi[e], -down(-(float)(int8_t)((e < 4 ? was_hi.x : was_hi.y) >> (8 * (e & 3))), ratio));
-          }
-        }
-        *plo = make_uint2(pack_s8(lo[0], lo[1], lo[2], lo[3]), pack_s8(lo[4], lo[5], lo[6], lo[7]));
-        *phi = make_uint2(pack_s8(hi[0], hi[1], hi[2], hi[3]), pack_s8(hi[4], hi[5], hi[6], hi[7]));
+      char2* const q = reinterpret_cast<char2*>(st.bounds + place * 2 * a.d) + threadIdx.x;
+      int c[4] = {down(lo[0], by), down(lo[1], by), -down(-hi[0], by), -down(-hi[1], by)};
+      if (w.kept > 0) {
+        const char2 was_lo = q[0], was_hi = q[a.d / 2];
+        c[0] = min(c[0], down((float)was_lo.x, ratio));
+        c[1] = min(c[1], down((float)was_lo.y, ratio));
+        c[2] = max(c[2], -down(-(float)was_hi.x, ratio));
+        c[3] = max(c[3], -down(-(float)was_hi.y, ratio));
       }
-      if (lt == 0) st.bound_scales[place] = unit;
+      const uint32_t packed = pack_s8(c[0], c[1], c[2], c[3]);
+      q[0] = make_char2((signed char)packed, (signed char)(packed >> 8));
+      q[a.d / 2] = make_char2((signed char)(packed >> 16), (signed char)(packed >> 24));
+      if (threadIdx.x == 0) st.bound_scales[place] = unit;
     }
-    if constexpr (kTeam > 32) __syncthreads();           // the shared words are written again
   }
 }
 
 // Queries: turned and copied, as in the write into 16-bit pages.
-template <typename T>
+template <typename T, int kThr>
 __device__ __forceinline__ void turn_queries(const AppendArgs& a, const StoreArgs& st, int64_t block) {
   constexpr int kBatch = 4;
-  const int units = a.d / kUnit, per_block = kThreads / units;
+  const int units = a.d / kUnit, per_block = kThr / units;
   const int u = threadIdx.x % units;
   const Unit t = unit_of(u, a.rot);
   const int h0 = (int)(block % st.q_head_blocks) * st.q_heads, h1 = min(a.H, h0 + st.q_heads);
@@ -357,21 +631,45 @@ __device__ __forceinline__ void turn_queries(const AppendArgs& a, const StoreArg
   }
 }
 
-template <typename T, int kStore, int kTeam>
-__global__ void __launch_bounds__(kThreads) append_store_kernel(const AppendArgs a, const StoreArgs st) {
-  __shared__ uint32_t amax_smem[kThreads / 32];
-  __shared__ float bound_smem[kTeam > 32 ? kThreads / 32 : 1][2][128];
+template <typename T, int kStore>
+__global__ void __launch_bounds__(kThreads) append_rows_kernel(const AppendArgs a, const StoreArgs st) {
   if ((int64_t)blockIdx.x >= st.page_blocks) {
-    turn_queries<T>(a, st, (int64_t)blockIdx.x - st.page_blocks);
+    turn_queries<T, kThreads>(a, st, (int64_t)blockIdx.x - st.page_blocks);
     return;
   }
-  const int64_t team = (int64_t)blockIdx.x * (kThreads / kTeam) + threadIdx.x / kTeam;
-  const int64_t bp = team / st.head_blocks;
-  const int h0 = (int)(team % st.head_blocks) * st.heads, h1 = min(2 * a.Hkv, h0 + st.heads);
+  const int64_t team = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  const int64_t bp = team / (2 * a.Hkv);
   const int b = (int)(bp / st.span), p = (int)(bp % st.span);
   PageWork w;
-  if (b >= a.B || !page_work(a, b, p, &w)) return;
-  write_page<T, kStore, kTeam>(a, st, w, b, h0, h1, amax_smem, bound_smem);
+  if (b >= a.B || !page_work(a, b, p, &w) || !page_exists(a, w)) return;
+  write_rows<T, kStore>(a, st, w, b, (int)(team % (2 * a.Hkv)));
+}
+
+template <typename T, int kStore, bool kTurn, bool kBounds, int kThr>
+__global__ void __launch_bounds__(kThr, (kTurn ? 512 : kBounds ? 640 : 768) / kThr) append_page_kernel(const AppendArgs a, const StoreArgs st) {
+  constexpr int kWarps = kThr / 32;
+  __shared__ uint32_t smem[kWarps + (kBounds ? 2 * kWarps * (kTurn ? 128 : 64) : 0)];
+  if ((int64_t)blockIdx.x >= st.page_blocks) {
+    if constexpr (kTurn) turn_queries<T, kThr>(a, st, (int64_t)blockIdx.x - st.page_blocks);
+    else if (a.q != nullptr) turn_queries<T, kThr>(a, st, (int64_t)blockIdx.x - st.page_blocks);
+    return;
+  }
+  const int h = (int)(blockIdx.x % (2 * a.Hkv));
+  const int64_t bp = blockIdx.x / (2 * a.Hkv);
+  const int b = (int)(bp / st.span), p = (int)(bp % st.span);
+  if constexpr (kTurn) {
+    if (h < a.Hkv) {
+      write_page<T, kStore, true, kBounds, kThr, kPageRows>(a, st, b, p, h, smem);
+      return;
+    }
+  }
+  write_page<T, kStore, false, kBounds, kThr, kPageRows>(a, st, b, p, h, smem);
+}
+
+template <typename T, int kStore, bool kTurn, bool kBounds>
+void append_pages(const AppendArgs& a, const StoreArgs& st, unsigned grid, int threads, cudaStream_t s) {
+  if (threads == 128) append_page_kernel<T, kStore, kTurn, kBounds, 128><<<grid, 128, 0, s>>>(a, st);
+  else append_page_kernel<T, kStore, kTurn, kBounds, 512><<<grid, 512, 0, s>>>(a, st);
 }
 
 template <typename T, int kStore>
@@ -381,28 +679,31 @@ cudaError_t append_store(const AppendArgs& a, StoreArgs st, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int units = a.d / kUnit;
   st.span = (a.T + a.cache.page_size - 2) / a.cache.page_size + 1;
-  // a warp holds kHold * 32 / units tokens' rows
-  const bool warps = a.T <= kHold * 32 / units;
-  const int64_t pages = (int64_t)a.B * st.span;
-  st.heads = 2 * a.Hkv;
-  if (warps) st.heads = 1;
-  else
-    while (st.heads > 1 && pages * ((2 * a.Hkv + st.heads - 1) / st.heads) < 4 * sms) st.heads = (st.heads + 1) / 2;
-  st.head_blocks = (2 * a.Hkv + st.heads - 1) / st.heads;
-  const int per = warps ? kThreads / 32 : 1;
-  st.page_blocks = (pages * st.head_blocks + per - 1) / per;
+  const int64_t heads = (int64_t)a.B * st.span * 2 * a.Hkv;       // of all pages
+  const bool warps = a.T <= kHold * 32 / units;                   // a warp holds the rows of any page
+  // 128 threads where they hold all of a page's rows
+  const int threads = warps ? kThreads : std::min(a.cache.page_size, a.T) <= 128 / units * kPageRows ? 128 : 512;
+  st.page_blocks = warps ? (heads + kThreads / 32 - 1) / (kThreads / 32) : heads;
   int64_t q_blocks = 0;
   if (a.q != nullptr) {
-    const int64_t tokens = ((int64_t)a.B * a.T + kThreads / units - 1) / (kThreads / units);
+    const int64_t tokens = ((int64_t)a.B * a.T + threads / units - 1) / (threads / units);
     st.q_heads = a.H;
-    while (st.q_heads > 4 && tokens * ((a.H + st.q_heads - 1) / st.q_heads) < 4 * sms) st.q_heads = (st.q_heads + 1) / 2;
+    while (st.q_heads > 4 && tokens * ((a.H + st.q_heads - 1) / st.q_heads) < 1024 * (int64_t)sms / threads)
+      st.q_heads = (st.q_heads + 1) / 2;
     st.q_head_blocks = (a.H + st.q_heads - 1) / st.q_heads;
     q_blocks = tokens * st.q_head_blocks;
   }
-  const int64_t grid = st.page_blocks + q_blocks;
-  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  if (warps) append_store_kernel<T, kStore, 32><<<(unsigned)grid, kThreads, 0, s>>>(a, st);
-  else append_store_kernel<T, kStore, kThreads><<<(unsigned)grid, kThreads, 0, s>>>(a, st);
+  if (st.page_blocks + q_blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)(st.page_blocks + q_blocks);
+  if (warps) {
+    append_rows_kernel<T, kStore><<<grid, kThreads, 0, s>>>(a, st);
+  } else if (a.rot.rot > 0) {
+    if (st.bounds != nullptr) append_pages<T, kStore, true, true>(a, st, grid, threads, s);
+    else if constexpr (kStore != FA_PAGES_16BIT) append_pages<T, kStore, true, false>(a, st, grid, threads, s);
+  } else {
+    if (st.bounds != nullptr) append_pages<T, kStore, false, true>(a, st, grid, threads, s);
+    else if constexpr (kStore != FA_PAGES_16BIT) append_pages<T, kStore, false, false>(a, st, grid, threads, s);
+  }
   return cudaGetLastError();
 }
 

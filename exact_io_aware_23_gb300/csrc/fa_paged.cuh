@@ -67,8 +67,7 @@ struct StoreArgs {
   int8_t* bounds;            // null, or [n_pages, Hkv, 2, d]
   float* bound_scales;
   int span;                  // pages that a sequence's new tokens reach at most
-  int heads, head_blocks;    // of the 2 * Hkv key and value heads: a team's, and the teams of a page
-  int64_t page_blocks;       // blocks of teams; those behind them turn queries
+  int64_t page_blocks;       // blocks that write pages; those behind them turn queries
   int q_heads, q_head_blocks;
 };
 
