@@ -154,7 +154,7 @@ def _load() -> ctypes.CDLL:
     L.fa_append_paged_store.restype = i
     L.fa_forward_paged_store.argtypes = [vp, cp, fp, vp, i, vp, vp, i, i, i, i, i, f, vp, mp, i, vp, sz, vp]
     L.fa_forward_paged_store.restype = i
-    L.fa_select_pages_workspace_size.argtypes = [i, i, i]
+    L.fa_select_pages_workspace_size.argtypes = [i, i, i, i]
     L.fa_select_pages_workspace_size.restype = sz
     L.fa_select_pages.argtypes = [vp, cp, fp, vp, i, i, i, i, i, vp, i, i, i, i, vp, sz, vp]
     L.fa_select_pages.restype = i
@@ -1051,9 +1051,15 @@ def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     return o, lse
 
 
-def select_pages_workspace_size(B: int, Hkv: int, max_pages: int) -> int:
+def select_pages_workspace_size(B: int, Hkv: int, max_pages: int, n_select: int) -> int:
     """max_pages: entries of a block table's row."""
-    return int(lib.fa_select_pages_workspace_size(B, Hkv, max_pages))
+    return int(lib.fa_select_pages_workspace_size(B, Hkv, max_pages, n_select))
+
+
+@functools.lru_cache(maxsize=1024)
+def _select_workspace_size(dev, *sizes) -> int:
+    """select_pages_workspace_size, which the device and the sizes determine."""
+    return lib.fa_select_pages_workspace_size(*sizes)
 
 
 def select_pages(q: torch.Tensor, k_bounds: torch.Tensor, bound_scales: torch.Tensor, block_table: torch.Tensor,
@@ -1089,8 +1095,9 @@ def select_pages(q: torch.Tensor, k_bounds: torch.Tensor, bound_scales: torch.Te
     else:
         _given("pages", pages, (B, Hkv, n_select), torch.int32)
     if workspace is None:
-        if width > n_select:
-            workspace = ws_new = torch.empty((B * Hkv * width * 4 + 255 & -256,), dtype=torch.uint8, device=q.device)
+        need = _select_workspace_size(dev, B, Hkv, width, n_select)
+        if need > 0:
+            workspace = ws_new = torch.empty((need,), dtype=torch.uint8, device=q.device)
     else:
         _refuse_place(workspace=workspace)
     st = lib.fa_select_pages_packed(_SELECT.pack(

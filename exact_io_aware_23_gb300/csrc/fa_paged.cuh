@@ -109,7 +109,7 @@ struct SelectArgs {
   const int32_t* q_lens;
   int picks, first, last;
   int32_t* pages;            // [B, Hkv, picks]
-  float* scores;             // workspace [B, Hkv, max_pages]
+  float* scores;             // workspace [B, Hkv, max_pages], where select_scores_first
   int* err;
 };
 
@@ -162,6 +162,7 @@ cudaError_t launch_append_store(const AppendArgs& a, const StoreArgs& st, fa_dty
 
 // Tables of at most this many pages are chosen from: their scores lie in a block's shared memory.
 constexpr int kMaxChoice = 49152;
+bool select_scores_first(int B, int Hkv, int max_pages, int picks);
 cudaError_t launch_select(const SelectArgs& a, fa_dtype dt, cudaStream_t s);
 cudaError_t launch_assign(const AssignArgs& a, cudaStream_t s);
 

@@ -279,8 +279,8 @@ fa_status fa_forward_paged_store(const void* q, const fa_paged_cache* cache, con
   return fa::launch_paged(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-size_t fa_select_pages_workspace_size(int B, int Hkv, int max_pages) {
-  if (B <= 0 || Hkv <= 0 || max_pages <= 0) return 0;
+size_t fa_select_pages_workspace_size(int B, int Hkv, int max_pages, int n_select) {
+  if (B <= 0 || Hkv <= 0 || max_pages <= 0 || n_select <= 0 || !fa::select_scores_first(B, Hkv, max_pages, n_select)) return 0;
   return ((size_t)B * Hkv * max_pages * sizeof(float) + 255) / 256 * 256;
 }
 
@@ -299,10 +299,8 @@ fa_status fa_select_pages(const void* q, const fa_paged_cache* cache, const fa_p
   if (!store->k_bounds || !store->bound_scales || !aligned(store->k_bounds, 16) || !aligned(store->bound_scales, 4) || !q ||
       !pages || !aligned(q, 16) || !aligned(pages, 4) || !aligned(q_lens, 4))
     return FA_ERR_INVALID_ARG;
-  if ((int64_t)B * Hkv * n_select > ((int64_t)1 << 40)) return FA_ERR_UNSUPPORTED;
-  if (cache->max_pages > n_select &&
-      (!workspace || !aligned(workspace, 256) || workspace_bytes < fa_select_pages_workspace_size(B, Hkv, cache->max_pages)))
-    return FA_ERR_INVALID_ARG;
+  const size_t need = fa_select_pages_workspace_size(B, Hkv, cache->max_pages, n_select);
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
   fa::SelectArgs a{};
   a.cache = cache_args(cache);
   a.q = q;

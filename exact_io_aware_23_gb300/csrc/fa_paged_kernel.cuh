@@ -49,6 +49,7 @@
 #include "fa_paged.cuh"
 #include "fa_score.cuh"
 #include "fa_sm103.cuh"
+#include "fa_store.cuh"
 #include "ptx_sm103.cuh"
 
 namespace fa {
@@ -158,27 +159,6 @@ __device__ __forceinline__ void mma(float* c, const uint32_t (&a)[4], uint32_t b
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Four codes of a register (bytes 0 to 3) as two pairs of fp16: bytes 0, 1 and 2, 3, or 0, 2 and 1, 3.
-// int8: the byte with its sign turned becomes the low bits of 1024 + x + 128, from which 1152 is taken.
-template <bool kInt8, bool kApart>
-__device__ __forceinline__ void codes(uint32_t x, uint32_t& lo, uint32_t& hi) {
-  if constexpr (kInt8) {
-    x ^= 0x80808080u;
-    const __half2 bias = __half2half2(__ushort_as_half(0x6480));            // 1152
-    auto pair = [&](uint32_t sel) {
-      const uint32_t y = __byte_perm(x, 0x64646464u, sel);
-      const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&y), bias);
-      return *reinterpret_cast<const uint32_t*>(&h);
-    };
-    lo = pair(kApart ? 0x4240 : 0x4140);
-    hi = pair(kApart ? 0x4341 : 0x4342);
-  } else {
-    if constexpr (kApart) x = __byte_perm(x, 0u, 0x3120);
-    asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
-        : "=r"(lo), "=r"(hi) : "r"(x));
-  }
 }
 
 // ---- sharing the work ------------------------------------------------------------------------------

@@ -1,22 +1,27 @@
 // The choice of the pages that a sequence's next tokens attend to.
 //
 // For a query row q and a page whose keys lie between lo and hi in every one of the d values,
-//     q . k <= sum_i max(q_i lo_i, q_i hi_i)
-// for each of the page's keys.  With q in whole numbers of 2^f (8 bits, like lo and hi) the sum is
-//     I = sum_i min(q_i, 0) lo_i + max(q_i, 0) hi_i,
-// an inner product of 2 d whole numbers, below 2^24: exact in any order, so the choice does not depend on
-// how the work is cut up.  A page's score is the largest over the rows of its key head's group of
-// I * 2^f * (the bounds' scale); the first and the last pages, which are always chosen, and scores that are NaN
-// stand above all others, and of equal ones the lower page is chosen.
+//     q . k <= sum_i max(q_i lo_i, q_i hi_i) = 1/2 sum_i (q_i (hi_i + lo_i) + |q_i| (hi_i - lo_i))
+// for each of the page's keys.  With q in whole numbers of 2^f (8 bits, like lo and hi) all these are whole numbers,
+// the operands exact in fp16 and the sum, below 2^23, in fp32, in any order: the choice does not depend on how
+// the work is cut up.  A page's score is the largest over the rows of its key head's group of that times 2^f times
+// the bounds' scale; the first and the last pages, which are always chosen, and scores that are NaN stand
+// above all others, and of equal ones the lower page is chosen.
 //
-// Scores.  A warp takes eight pages at a time: their bounds are the right operand of mma.sync's 8-bit
-// whole-number form as they lie in memory, 16 rows' q the left one.  What bounds it: bytes, 2 d + 4 a page.
-// Choice.  A block for each (sequence, key head) finds the K-th largest score by its bits, eight at a time,
-// and lists the pages at or above it in their order.
+// Scores.  A warp takes 32 pages at a time, eight to a product, their bounds the right operand of mma.sync as
+// they lie in memory, 16 rows' q the left one.  What bounds it: bytes, 2 d + 4 a page, for few pages the chain
+// of reads: lengths, table entry, bounds.
+// Choice.  A block has a (sequence, key head): it keeps the scores in shared memory and narrows down the range
+// of the K-th largest one's bits, 1024 bins at a time.  The bins are laid over the range that the scores
+// have: by the bits from the top nearly all would meet in the few bins of their exponents.
+// Where there are fewer of them than SMs, and many pages, a kernel of its own scores the pages on all SMs first.
+// (A cluster of blocks for each instead, scores in the first one's shared memory: SCORETIMES.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
+
+#include <algorithm>
 
 #include "fa_paged.cuh"
 #include "fa_sm103.cuh"
@@ -26,16 +31,33 @@
 namespace fa {
 namespace {
 
-constexpr int kWarps = 4;
 constexpr int kRows = 16;
 constexpr int kGroup = 8;                  // pages of a warp's product
-constexpr int kPickThreads = 512;
+constexpr int kBins = 1024;
+constexpr int kScoreThreads = 128;         // of a block that only scores
+constexpr int kScoreCtas = 3;              // and such blocks on an SM
 
-// c (16 x 8, int32) += a (16 x 32) b (32 x 8)
-__device__ __forceinline__ void mma_s8(int (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+// c (16 x 8, fp32) += a (16 x 16) b (16 x 8)
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// hi + lo and hi - lo of four bounds each, as two pairs of fp16 (bytes 0, 1 and 2, 3): with their sign turned, the
+// bytes are the low bits of 1152 + x, and all sums are whole numbers below 2048, exact.
+__device__ __forceinline__ void sum_and_difference(uint32_t lo, uint32_t hi, uint32_t (&sum)[2], uint32_t (&diff)[2]) {
+  const __half2 twice = __half2half2(__ushort_as_half(0x6880));            // 2304
+  lo ^= 0x80808080u;
+  hi ^= 0x80808080u;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const uint32_t sel = e == 0 ? 0x4140 : 0x4342;
+    const uint32_t x = __byte_perm(hi, 0x64646464u, sel), y = __byte_perm(lo, 0x64646464u, sel);
+    const __half2 h = *reinterpret_cast<const __half2*>(&x), l = *reinterpret_cast<const __half2*>(&y);
+    const __half2 d = __hsub2(h, l), s = __hadd2(__hsub2(h, twice), l);
+    sum[e] = *reinterpret_cast<const uint32_t*>(&s);
+    diff[e] = *reinterpret_cast<const uint32_t*>(&d);
+  }
 }
 
 template <bool F16>
@@ -49,11 +71,11 @@ __device__ __forceinline__ int pages_of(const SelectArgs& a, int b) {
   return (paged_len(a.cache, b, nullptr) + a.cache.page_size - 1) / a.cache.page_size;
 }
 
-// 16 rows of queries as the left operand: products 4 j to 4 j + 3 of a lane's 64 bytes [64 i + 16 (lane % 4), + 16)
-// of a page's lower (then upper) bounds, and what their whole numbers count.
+// 16 rows of queries as left operands: product 4 i + w takes the values [64 i + 16 (lane % 4) + 4 w, + 4) of a lane
+// (columns 2 j, 2 j + 1, 2 j + 8, 2 j + 9 of lane j), whole numbers in fp16; and what these count.
 template <int D, bool F16>
 struct Queries {
-  uint32_t low[D / 32][4], high[D / 32][4];
+  uint32_t q[D / 16][4];
   float unit[2];                           // -1: no such row
   __device__ __forceinline__ void read(const SelectArgs& a, int b, int hk, int row0, int count) {
     const int lane = threadIdx.x % 32, G = a.H / a.Hkv, rows = G * a.T;
@@ -61,14 +83,14 @@ struct Queries {
     for (int e = 0; e < 2; ++e) {
       const int r = row0 + lane / 4 + e * 8, t = r % a.T;
       const bool there = r < rows && t < count;
-      const uint16_t* q = static_cast<const uint16_t*>(a.q) + (((int64_t)b * a.H + hk * G) * a.T + r) * D + lane % 4 * 16;
+      const uint16_t* p = static_cast<const uint16_t*>(a.q) + (((int64_t)b * a.H + hk * G) * a.T + r) * D + lane % 4 * 16;
       float x[D / 4];
       uint32_t amax = 0;
 #pragma unroll
       for (int i = 0; i < D / 64; ++i)
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          const uint4 v = there ? __ldg(reinterpret_cast<const uint4*>(q + i * 64) + w) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 v = there ? __ldg(reinterpret_cast<const uint4*>(p + i * 64) + w) : make_uint4(0u, 0u, 0u, 0u);
           const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -83,87 +105,12 @@ struct Queries {
       const float u = power_scale<true>(amax), inv = 1.f / u;
       unit[e] = !there ? -1.f : amax < 0x7f800000u ? u : __uint_as_float(0x7fc00000u);
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j)     // two products of 8 bytes of a lane's 16
+      for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          int c[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) c[y] = __float2int_rn(x[8 * j + 4 * k + y] * inv);
-          low[j][e + 2 * k] = pack_s8(min(c[0], 0), min(c[1], 0), min(c[2], 0), min(c[3], 0));
-          high[j][e + 2 * k] = pack_s8(max(c[0], 0), max(c[1], 0), max(c[2], 0), max(c[3], 0));
-        }
+        for (int k = 0; k < 2; ++k) q[j][e + 2 * k] = ptx::pack_f16(rintf(x[4 * j + 2 * k] * inv), rintf(x[4 * j + 2 * k + 1] * inv));
     }
   }
 };
-
-template <int D, bool F16>
-__global__ void __launch_bounds__(32 * kWarps) score_kernel(const SelectArgs a, const int chunks) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int slice = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-  const int b = slice / a.Hkv, hk = slice % a.Hkv;
-  const int n = pages_of(a, b);
-  if (n <= a.picks) return;                             // all of them
-  const int rows = a.H / a.Hkv * a.T, count = new_tokens(a.q_lens, b, a.T);
-  const int32_t* const table = a.cache.table + b * a.cache.table_stride;
-  float* const scores = a.scores + (int64_t)slice * a.cache.max_pages;
-  const int step = chunks * kWarps * kGroup;
-  for (int row0 = 0; row0 < rows; row0 += kRows) {
-    Queries<D, F16> q;
-    q.read(a, b, hk, row0, count);
-    for (int p0 = (chunk * kWarps + warp) * kGroup; p0 < n; p0 += step) {
-      const int p = p0 + lane / 4;
-      int page = p < n ? table[p] : -1;
-      if (p < n && (unsigned)page >= (unsigned)a.cache.n_pages) {
-        atomicExch(a.err, kDevBadOffsets);              // reported, not followed
-        page = -1;
-      }
-      const int64_t place = (int64_t)page * a.Hkv + hk;
-      uint4 v[D / 32];
-      const uint4* const src = reinterpret_cast<const uint4*>(a.bounds + place * 2 * D) + lane % 4;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) v[i] = page >= 0 ? __ldg(src + i * 4) : make_uint4(0u, 0u, 0u, 0u);
-      const float mine = page >= 0 ? __ldg(a.bound_scales + place) : 0.f;
-      int c[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        mma_s8(c, q.low[2 * i], v[i].x, v[i].y);
-        mma_s8(c, q.low[2 * i + 1], v[i].z, v[i].w);
-        mma_s8(c, q.high[2 * i], v[D / 64 + i].x, v[D / 64 + i].y);
-        mma_s8(c, q.high[2 * i + 1], v[D / 64 + i].z, v[D / 64 + i].w);
-      }
-      // the lane's columns are pages 2 (lane % 4) and the next; -inf: no such row
-      float best[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float s = __shfl_sync(0xffffffffu, mine, (2 * (lane % 4) + e) * 4);
-        best[e] = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const float x = __fmul_rn(__fmul_rn((float)c[2 * w + e], q.unit[w]), s);
-          // NaN: of the page, in every row; a row that is NaN itself has no say next to others
-          best[e] = q.unit[w] == -1.f ? best[e] : best[e] == -INFINITY ? x : fmaxf(best[e], x);
-        }
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          const float other = __shfl_xor_sync(0xffffffffu, best[e], o);
-          best[e] = best[e] == -INFINITY ? other : other == -INFINITY ? best[e] : fmaxf(best[e], other);
-        }
-      }
-      if (lane < 4) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int at = p0 + 2 * lane + e;
-          if (at >= n) break;
-          if (row0 > 0) {
-            const float before = scores[at];
-            best[e] = best[e] == -INFINITY ? before : before == -INFINITY ? best[e] : fmaxf(best[e], before);
-          }
-          scores[at] = best[e];
-        }
-      }
-    }
-  }
-}
 
 // Whole numbers in the order of the scores
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -171,122 +118,315 @@ __device__ __forceinline__ uint32_t order_of(float x) {
   return x != x ? 0xffffffffu : (u >> 31) != 0u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectArgs a) {
-  extern __shared__ uint32_t keys[];
-  __shared__ int hist[256];
-  __shared__ int sums[2][kPickThreads / 32];
-  __shared__ uint32_t digit_found;
-  __shared__ int want_left;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int b = blockIdx.x / a.Hkv;
-  if (blockIdx.x % a.Hkv == 0 && threadIdx.x == 0) paged_len(a.cache, b, a.err);
-  const int n = pages_of(a, b);
-  int32_t* const out = a.pages + (int64_t)blockIdx.x * a.picks;
-  if (n <= a.picks) {
-    for (int i = threadIdx.x; i < a.picks; i += kPickThreads) out[i] = i < n ? i : -1;
-    return;
-  }
-  const float* const scores = a.scores + (int64_t)blockIdx.x * a.cache.max_pages;
-  for (int i = threadIdx.x; i < n; i += kPickThreads)
-    keys[i] = i < a.first || i >= n - a.last ? 0xffffffffu : order_of(__ldcg(scores + i));
-  // the K-th largest key: its bits from the top, and how many of the keys equal to it are chosen
-  uint32_t prefix = 0, mask = 0;
-  int want = a.picks;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kPickThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kPickThreads)
-      if ((keys[i] & mask) == prefix) atomicAdd(&hist[(keys[i] >> shift) & 255u], 1);
-    __syncthreads();
-    if (warp == 0) {
-      // lane i holds digits 255 - 8 i down to 248 - 8 i
-      int mine[8], sum = 0;
+// Scores of pages [p32, n) in steps of `step`, 32 at a time, for rows [row0, row0 + 16): put(page, score).
+template <int D, bool F16, typename Put>
+__device__ __forceinline__ void score_pages(const SelectArgs& a, const Queries<D, F16>& q, int b, int hk, int n, int p32,
+                                            int step, Put&& put) {
+  const int lane = threadIdx.x % 32;
+  const int32_t* const table = a.cache.table + b * a.cache.table_stride;
+  // 32 pages' places, one to a lane, read ahead
+  auto places = [&](int p0) {
+    const int p = p0 + lane;
+    int page = p < n ? table[p] : -1;
+    if (p < n && (unsigned)page >= (unsigned)a.cache.n_pages) {
+      atomicExch(a.err, kDevBadOffsets);                 // reported, not followed
+      page = -1;
+    }
+    return page;
+  };
+  int next = places(p32);
+#pragma unroll 1
+  for (; p32 < n; p32 += step) {
+    const int lane_page = next;
+    uint4 v[4][D / 32];
+    float mine[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        mine[e] = hist[255 - 8 * lane - e];
-        sum += mine[e];
-      }
-      int up = sum;
+    for (int y = 0; y < 4; ++y) {
+      const int page = __shfl_sync(0xffffffffu, lane_page, y * kGroup + lane / 4);
+      const int64_t place = (int64_t)page * a.Hkv + hk;
+      const uint4* const src = reinterpret_cast<const uint4*>(a.bounds + place * 2 * D) + lane % 4;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, up, o);
-        if (lane >= o) up += x;
-      }
-      int before = up - sum;
-      if (before < want && up >= want) {
-        bool open = true;
+      for (int i = 0; i < D / 32; ++i) v[y][i] = page >= 0 ? __ldg(src + i * 4) : make_uint4(0u, 0u, 0u, 0u);
+      mine[y] = page >= 0 ? __ldg(a.bound_scales + place) : 0.f;
+    }
+    next = places(p32 + step);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (open && before + mine[e] >= want) {
-            digit_found = 255 - 8 * lane - e;
-            want_left = want - before;
-            open = false;
-          }
-          before += mine[e];
+    for (int y = 0; y < 4; ++y) {
+      const int p0 = p32 + y * kGroup;
+      if (p0 >= n) break;
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const uint32_t lo[4] = {v[y][i].x, v[y][i].y, v[y][i].z, v[y][i].w};
+        const uint4 up = v[y][D / 64 + i];
+        const uint32_t hi[4] = {up.x, up.y, up.z, up.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t sum[2], diff[2], size[4];
+          sum_and_difference(lo[w], hi[w], sum, diff);
+          mma(c, q.q[4 * i + w], sum[0], sum[1]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) size[k] = q.q[4 * i + w][k] & 0x7fff7fffu;
+          mma(c, size, diff[0], diff[1]);
         }
       }
-    }
-    __syncthreads();
-    prefix |= digit_found << shift;
-    mask |= 255u << shift;
-    want = want_left;
-    __syncthreads();
-  }
-  // in page order: keys above, and the first `want` of those equal
-  int above = 0, equal = 0;
-  for (int i0 = 0; i0 < n; i0 += kPickThreads) {
-    const int i = i0 + threadIdx.x;
-    const uint32_t key = i < n ? keys[i] : 0u;
-    const bool up = i < n && key > prefix, tie = i < n && key == prefix;
-    const uint32_t ups = __ballot_sync(0xffffffffu, up), ties = __ballot_sync(0xffffffffu, tie);
-    if (lane == 0) {
-      sums[0][warp] = __popc(ups);
-      sums[1][warp] = __popc(ties);
-    }
-    __syncthreads();
-    int u = above, t = equal;
-    for (int w = 0; w < kPickThreads / 32; ++w) {
-      if (w < warp) {
-        u += sums[0][w];
-        t += sums[1][w];
+      // the lane's columns are pages 2 (lane % 4) and the next.  The scale is positive, so it may wait until
+      // the largest is known; one that is NaN makes the score NaN, a row that is NaN has no say.
+      float best[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        best[e] = fmaxf(q.unit[0] == -1.f ? -INFINITY : 0.5f * c[e] * q.unit[0],
+                        q.unit[1] == -1.f ? -INFINITY : 0.5f * c[2 + e] * q.unit[1]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) best[e] = fmaxf(best[e], __shfl_xor_sync(0xffffffffu, best[e], o));
+        best[e] = __fmul_rn(best[e], __shfl_sync(0xffffffffu, mine[y], (2 * (lane % 4) + e) * 4));
       }
-      above += sums[0][w];
-      equal += sums[1][w];
+      if (lane < 4) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (p0 + 2 * lane + e < n) put(p0 + 2 * lane + e, best[e]);
+      }
     }
-    u += __popc(ups & ((1u << lane) - 1u));
-    t += __popc(ties & ((1u << lane) - 1u));
-    if (up) out[u + min(t, want)] = i;
-    else if (tie && t < want) out[u + t] = i;
-    __syncthreads();
   }
+}
+__device__ __forceinline__ float larger_score(float x, float y) { return x != x || y != y ? x + y : fmaxf(x, y); }
+
+// Scores on all SMs: warp W of the grid takes slice W % slices, so that neighbours read neighbouring heads' bounds.
+template <int D, bool F16>
+__global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const SelectArgs a, const int slots) {
+  const int warp = blockIdx.x * (kScoreThreads / 32) + threadIdx.x / 32, slices = a.B * a.Hkv;
+  const int slice = warp % slices, slot = warp / slices;
+  const int b = slice / a.Hkv, hk = slice % a.Hkv;
+  const int n = pages_of(a, b);
+  if (n <= a.picks || slot >= slots || slot * 32 >= n) return;   // all of them, or no page for this warp
+  const int rows = a.H / a.Hkv * a.T, count = new_tokens(a.q_lens, b, a.T);
+  float* const scores = a.scores + (int64_t)slice * a.cache.max_pages;
+  for (int row0 = 0; row0 < rows; row0 += kRows) {
+    Queries<D, F16> q;
+    q.read(a, b, hk, row0, count);
+    score_pages<D, F16>(a, q, b, hk, n, slot * 32, slots * 32,
+                        [&](int p, float x) { scores[p] = row0 > 0 ? larger_score(scores[p], x) : x; });
+  }
+}
+
+// kScored: score_kernel has been there.
+template <int D, bool F16, int kThr, bool kScored>
+__global__ void __launch_bounds__(kThr) select_kernel(const SelectArgs a) {
+  constexpr int kWarps = kThr / 32;
+  extern __shared__ __align__(16) uint32_t keys[];       // the pages' scores
+  __shared__ int hist[kBins];
+  __shared__ uint32_t ends[2][kWarps];
+  __shared__ int sums[2][kWarps];
+  __shared__ int found[3];                               // bin, keys in it, keys wanted of it
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int slice = blockIdx.x;
+  const int b = slice / a.Hkv, hk = slice % a.Hkv;
+  if (hk == 0 && threadIdx.x == 0) paged_len(a.cache, b, a.err);
+  const int n = pages_of(a, b);
+  int32_t* const out = a.pages + (int64_t)slice * a.picks;
+  if (n <= a.picks) {                                    // all of them
+    for (int i = threadIdx.x; i < a.picks; i += kThr) out[i] = i < n ? i : -1;
+    return;
+  }
+  if constexpr (kScored) {
+    const float* const scores = a.scores + (int64_t)slice * a.cache.max_pages;
+    for (int i = threadIdx.x; i < n; i += kThr) keys[i] = __float_as_uint(__ldcg(scores + i));
+  } else {
+    const int rows = a.H / a.Hkv * a.T, count = new_tokens(a.q_lens, b, a.T);
+    for (int row0 = 0; row0 < rows; row0 += kRows) {
+      Queries<D, F16> q;
+      q.read(a, b, hk, row0, count);
+      score_pages<D, F16>(a, q, b, hk, n, warp * 32, kWarps * 32, [&](int p, float x) {
+        keys[p] = __float_as_uint(row0 > 0 ? larger_score(__uint_as_float(keys[p]), x) : x);
+      });
+    }
+  }
+  __syncthreads();
+
+  // ---- the choice: pages that are always chosen, and the `want` highest of the others -----------------
+  auto forced = [&](int i) { return i < a.first || i >= n - a.last; };
+  const int64_t always = (int64_t)a.first + a.last;
+  int want = always < a.picks ? a.picks - (int)always : 0;
+  // the scores' range
+  uint32_t lo = 0xffffffffu, hi = 0u;
+  uint4* const keys4 = reinterpret_cast<uint4*>(keys);
+  const int n4 = (n + 3) / 4;
+  for (int i = threadIdx.x; i < n4; i += kThr) {
+    const uint4 v = keys4[i];
+    uint32_t key[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      key[e] = order_of(__uint_as_float(key[e]));
+      if (4 * i + e < n && !forced(4 * i + e)) {
+        lo = min(lo, key[e]);
+        hi = max(hi, key[e]);
+      }
+    }
+    keys4[i] = make_uint4(key[0], key[1], key[2], key[3]);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    ends[0][warp] = lo;
+    ends[1][warp] = hi;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    lo = min(lo, ends[0][w]);
+    hi = max(hi, ends[1][w]);
+  }
+  // [lo, hi] holds the K-th largest key: `want` of the keys in it are chosen, and all above
+  while (want > 0) {
+    const int bits = 32 - __clz(hi - lo), shift = max(0, bits - 10);
+    for (int i = threadIdx.x; i < kBins; i += kThr) hist[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n4; i += kThr) {
+      const uint4 v = keys4[i];
+      const uint32_t key[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (key[e] >= lo && key[e] <= hi && 4 * i + e < n && !forced(4 * i + e)) atomicAdd(&hist[(key[e] - lo) >> shift], 1);
+    }
+    __syncthreads();
+    // thread t holds bins from the top, kBins / kThr of them
+    constexpr int kPer = kBins / kThr;
+    int mine[kPer], sum = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      mine[e] = hist[kBins - 1 - kPer * threadIdx.x - e];
+      sum += mine[e];
+    }
+    int up = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += x;
+    }
+    if (lane == 31) sums[0][warp] = up;
+    __syncthreads();
+    int before = up - sum;
+    for (int w = 0; w < warp; ++w) before += sums[0][w];
+    if (before < want && before + sum >= want) {
+      bool open = true;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        if (open && before + mine[e] >= want) {
+          found[0] = kBins - 1 - kPer * (int)threadIdx.x - e;
+          found[1] = mine[e];
+          found[2] = want - before;
+          open = false;
+        }
+        before += mine[e];
+      }
+    }
+    __syncthreads();
+    const uint32_t at = lo + ((uint32_t)found[0] << shift);
+    hi = min(hi, at + ((1u << shift) - 1u));
+    lo = at;
+    want = found[2];
+    if (shift == 0 || found[1] == want) break;
+  }
+  // in page order, each warp a run of pages: keys above, and the first `want` of those in the range
+  const int run = ((n + kWarps - 1) / kWarps + 127) / 128 * 128, end = min(n, (warp + 1) * run);
+  // a lane's four pages: bits of those above, and of those in the range
+  auto look = [&](int i, uint32_t* ups, uint32_t* ties) {
+    const uint4 v = i < end ? keys4[i / 4] : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t key[4] = {v.x, v.y, v.z, v.w};
+    *ups = *ties = 0u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool there = i + e < end, sure = forced(i + e);
+      if (there && (sure || (want > 0 && key[e] > hi))) *ups |= 1u << e;
+      else if (there && want > 0 && key[e] >= lo) *ties |= 1u << e;
+    }
+  };
+  int above = 0, equal = 0;
+  for (int i0 = warp * run; i0 < end; i0 += 128) {
+    uint32_t ups, ties;
+    look(i0 + 4 * lane, &ups, &ties);
+    above += __popc(ups);
+    equal += __popc(ties);
+  }
+  above = __reduce_add_sync(0xffffffffu, above);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  __syncthreads();                                       // sums is read no more
+  if (lane == 0) {
+    sums[0][warp] = above;
+    sums[1][warp] = equal;
+  }
+  __syncthreads();
+  above = equal = 0;
+  for (int w = 0; w < warp; ++w) {
+    above += sums[0][w];
+    equal += sums[1][w];
+  }
+  for (int i0 = warp * run; i0 < end; i0 += 128) {
+    uint32_t ups, ties;
+    look(i0 + 4 * lane, &ups, &ties);
+    const int mine = __popc(ups) | __popc(ties) << 16;
+    int both = mine;                                     // two counts, the range's in the upper half
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, both, o);
+      if (lane >= o) both += x;
+    }
+    const int all = __shfl_sync(0xffffffffu, both, 31);
+    both -= mine;
+    int u = above + (both & 0xffff), t = equal + (both >> 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool up = (ups >> e & 1u) != 0u, tie = (ties >> e & 1u) != 0u;
+      const int at = u + min(t, want);
+      if ((up || (tie && t < want)) && at < a.picks) out[at] = i0 + 4 * lane + e;   // (more that are always chosen: the first ones)
+      u += up;
+      t += tie;
+    }
+    above += all & 0xffff;
+    equal += all >> 16;
+  }
+}
+
+template <int D, bool F16, int kThr, bool kScored>
+cudaError_t launch_one(const SelectArgs& a, cudaStream_t s) {
+  auto kern = select_kernel<D, F16, kThr, kScored>;
+  static LaunchSetup setup;
+  const int smem = a.cache.max_pages > a.picks ? (a.cache.max_pages + 3) / 4 * 16 : 0;
+  const cudaError_t e = prepare_launch(setup, kern, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(a.B * a.Hkv), kThr, smem, s>>>(a);
+  return cudaGetLastError();
+}
+template <int D, bool F16>
+cudaError_t launch_any(const SelectArgs& a, cudaStream_t s) {
+  if (!select_scores_first(a.B, a.Hkv, a.cache.max_pages, a.picks))
+    return a.cache.max_pages <= 512 ? launch_one<D, F16, 128, false>(a, s) : launch_one<D, F16, 256, false>(a, s);
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  // warps of a slice: all take the same number of pages, as many warps as the SMs hold
+  const int slices = a.B * a.Hkv, blocks = (a.cache.max_pages + 31) / 32;
+  const int most = std::max(1, sms * kScoreCtas * (kScoreThreads / 32) / slices), each = (blocks + most - 1) / most;
+  const int slots = (blocks + each - 1) / each;
+  const int grid = (slots * slices + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
+  score_kernel<D, F16><<<grid, kScoreThreads, 0, s>>>(a, slots);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_one<64, false, 1024, true>(a, s);              // (the queries' type and size do not matter)
 }
 
 }  // namespace
 
-cudaError_t launch_select(const SelectArgs& a, fa_dtype dt, cudaStream_t s) {
+// Whether the pages are scored by a kernel of its own: slices that leave SMs idle, each with more pages than a
+// block scores while another launch begins.
+bool select_scores_first(int B, int Hkv, int max_pages, int picks) {
   int sms = 0;
-  cudaError_t e = sm_count(&sms);
-  if (e != cudaSuccess) return e;
-  if (a.cache.max_pages > a.picks) {
-    const int64_t slices = (int64_t)a.B * a.Hkv;
-    const int chunks = (a.cache.max_pages + kWarps * kGroup - 1) / (kWarps * kGroup);
-    int64_t want = (16 * (int64_t)sms + slices - 1) / slices;
-    if (want > chunks) want = chunks;
-    const unsigned grid = (unsigned)(want * slices);
-    if (a.d == 64) {
-      if (dt == FA_FP16) score_kernel<64, true><<<grid, 32 * kWarps, 0, s>>>(a, (int)want);
-      else score_kernel<64, false><<<grid, 32 * kWarps, 0, s>>>(a, (int)want);
-    } else {
-      if (dt == FA_FP16) score_kernel<128, true><<<grid, 32 * kWarps, 0, s>>>(a, (int)want);
-      else score_kernel<128, false><<<grid, 32 * kWarps, 0, s>>>(a, (int)want);
-    }
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
-  static LaunchSetup setup;
-  const int smem = a.cache.max_pages > a.picks ? a.cache.max_pages * 4 : 0;
-  if ((e = prepare_launch(setup, pick_kernel, smem)) != cudaSuccess) return e;
-  pick_kernel<<<(unsigned)(a.B * a.Hkv), kPickThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  if (sm_count(&sms) != cudaSuccess || sms <= 0) sms = 152;        // GB300's when no device can be asked
+  return max_pages > picks && max_pages > 512 && (int64_t)B * Hkv < sms;
+}
+
+cudaError_t launch_select(const SelectArgs& a, fa_dtype dt, cudaStream_t s) {
+  if (a.d == 64) return dt == FA_FP16 ? launch_any<64, true>(a, s) : launch_any<64, false>(a, s);
+  return dt == FA_FP16 ? launch_any<128, true>(a, s) : launch_any<128, false>(a, s);
 }
 
 }  // namespace fa

@@ -556,13 +556,14 @@ fa_status fa_forward_paged_store(const void* q, const fa_paged_cache* cache,
  *            where a sequence has no more than n_select; none without new tokens.
  *   cache  : the table and the lengths; keys and values are not looked at (they may be null)
  *   store  : k_bounds and bound_scales, as fa_append_paged_store left them; nothing else is looked at
- *   workspace : fa_select_pages_workspace_size(B, Hkv, max_pages) bytes, 256-byte aligned; none (it
- *            may be null) when max_pages <= n_select
+ *   workspace : fa_select_pages_workspace_size(...) bytes, 256-byte aligned, contents on entry irrelevant; calls
+ *            in flight at once need their own.  The size is 0 for many sequences and for short ones,
+ *            which need none (workspace may be null).
  * A bounds' scale that is NaN counts above all scores; a query row that holds something not finite
  * has no say next to others.  max_pages at most 49152 (FA_ERR_UNSUPPORTED).  Lengths and entries as in
  * fa_append_paged.
  */
-size_t fa_select_pages_workspace_size(int B, int Hkv, int max_pages);
+size_t fa_select_pages_workspace_size(int B, int Hkv, int max_pages, int n_select);
 fa_status fa_select_pages(const void* q, const fa_paged_cache* cache, const fa_page_store* store,
                           int32_t* pages, int B, int H, int Hkv, int T, int d,
                           const int32_t* q_lens, int n_select, int first, int last, fa_dtype dtype,

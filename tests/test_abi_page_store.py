@@ -74,16 +74,21 @@ def test_forward_checks():
     assert forward(B=0, s=store(format=9)) == OK
 
 
-def select(c=None, s=None, q=P, pages=P, B=2, H=4, Hkv=2, T=1, d=64, n=4, first=1, last=1, dtype=0, w=P, wsb=None):
-    wsb = fa.select_pages_workspace_size(2, 2, 100) if wsb is None else wsb
+def select(c=None, s=None, q=P, pages=P, B=2, H=4, Hkv=2, T=1, d=64, n=4, first=1, last=1, dtype=0, w=P, wsb=1 << 20):
     return fa.lib.fa_select_pages(q, cache(max_pages=100, table_stride=100, k_cache=None, v_cache=None) if c is None else c,
-                                  store(k_bounds=P, bound_scales=P) if s is None else s, pages, B, H, Hkv, T, d, None, n, first, last, dtype, w, wsb,
-                                  None)
+                                  store(k_bounds=P, bound_scales=P) if s is None else s, pages, B, H, Hkv, T, d, None, n, first, last, dtype, w, wsb, None)
 
 
 def test_select_checks():
-    assert fa.select_pages_workspace_size(2, 2, 100) == 1792               # 1600 bytes, in steps of 256
-    assert fa.select_pages_workspace_size(0, 2, 100) == 0
+    assert fa.select_pages_workspace_size(2, 2, 1000, 10) == 16128         # 16000 bytes, in steps of 256
+    assert fa.select_pages_workspace_size(2, 2, 512, 10) == 0              # few pages,
+    assert fa.select_pages_workspace_size(200, 2, 1000, 10) == 0           # many sequences,
+    assert fa.select_pages_workspace_size(2, 2, 1000, 1000) == 0           # no choice
+    assert fa.select_pages_workspace_size(0, 2, 1000, 10) == 0
+    wide = cache(max_pages=1000, table_stride=1000, k_cache=None, v_cache=None)
+    assert select(wide, w=None) == INVALID
+    assert select(wide, w=P + 16) == INVALID
+    assert select(wide, wsb=16000) == INVALID
     for kw, status in BAD_CACHES:
         if "k_cache" not in kw and "v_cache" not in kw and not any("stride" in n and n != "table_stride" for n in kw):
             assert select(cache(**kw)) == status, kw
@@ -96,9 +101,6 @@ def test_select_checks():
     assert select(n=-1) == INVALID
     assert select(first=-1) == INVALID
     assert select(last=-2) == INVALID
-    assert select(w=None) == INVALID
-    assert select(w=P + 16) == INVALID
-    assert select(wsb=1536) == INVALID
     assert select(dtype=1) == UNSUPPORTED
     assert select(Hkv=3) == UNSUPPORTED
     assert select(cache(max_pages=49153, table_stride=49153)) == UNSUPPORTED

@@ -59,7 +59,8 @@ def _want(q, bounds, unit, table, lens, K, page, first, last, q_lens=None):
     ([1], 1, 1, 1, 16, 1, 1, 1), ([0, 5], 4, 2, 1, 16, 3, 0, 0), ([1000, 17, 160, 161], 4, 1, 1, 16, 10, 1, 1),
     ([900, 333], 8, 2, 3, 16, 7, 0, 0), ([5000], 8, 8, 1, 16, 100, 2, 3), ([2000, 700], 40, 2, 1, 16, 9, 1, 0),
     ([3000], 6, 1, 7, 32, 33, 0, 2), ([70000, 12], 2, 1, 1, 16, 200, 1, 1), ([600], 2, 2, 1, 16, 4, 3, 3),
-    ([640], 2, 2, 1, 16, 39, 0, 0), ([4096], 64, 2, 2, 256, 5, 1, 1)])
+    ([640], 2, 2, 1, 16, 39, 0, 0), ([4096], 64, 2, 2, 256, 5, 1, 1), ([160000, 5], 4, 1, 5, 16, 300, 1, 1), ([20000] * 3, 2, 2, 1, 16, 900, 0, 7),
+    ([786000], 1, 1, 1, 16, 1000, 500, 400), ([1600], 2, 1, 1, 16, 40, 60, 60)])
 def test_the_highest_scores_are_chosen(dtype, d, lens, H, Hkv, T, page, K, first, last):
     g = torch.Generator(device="cuda").manual_seed(sum(lens) + K)
     table, n = _table(lens, page, g)
@@ -121,7 +122,9 @@ def test_choice_in_a_graph_on_streams_and_with_given_memory():
     bounds, unit = _bounds(n, 2, 128, g)
     q = torch.randn((2, 8, 1, 128), generator=g, device="cuda").to(torch.bfloat16)
     nl = _i32(lens)
-    ws = torch.full((fa.select_pages_workspace_size(2, 2, 250),), 255, dtype=torch.uint8, device="cuda")
+    table = torch.cat((table, torch.full((2, 300), -1, dtype=torch.int32, device="cuda")), 1)     # room to grow
+    ws = torch.full((fa.select_pages_workspace_size(2, 2, 550, 20),), 255, dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 0
     out = torch.empty((2, 2, 20), dtype=torch.int32, device="cuda")
     fa.select_pages(q, bounds, unit, table, nl, 20, 16)
     gr = torch.cuda.CUDAGraph()
@@ -151,8 +154,7 @@ def test_choice_refusals():
                       ("pages", dict(pages=torch.zeros((1, 2, 5), dtype=torch.int32, device="cuda")))):
         with pytest.raises(ValueError, match=match):
             call(**kw)
-    for match, kw in (("INVALID_ARG", dict(first=-1)), ("UNSUPPORTED", dict(page=24)), ("INVALID_ARG", dict(page=0)),
-                      ("INVALID_ARG", dict(workspace=torch.zeros(32, dtype=torch.uint8, device="cuda")))):
+    for match, kw in (("INVALID_ARG", dict(first=-1)), ("UNSUPPORTED", dict(page=24)), ("INVALID_ARG", dict(page=0))):
         with pytest.raises(fa.FaError, match=match):
             call(**kw)
     with pytest.raises(fa.FaError, match="UNSUPPORTED"):
