@@ -160,11 +160,7 @@ def _load() -> ctypes.CDLL:
     L.fa_select_pages.restype = i
     L.fa_assign_pages.argtypes = [vp, i64, i, i, i, vp, vp, vp, i, vp, vp, vp, vp, vp, vp, i, vp]
     L.fa_assign_pages.restype = i
-    L.fa_append_paged_store_packed.argtypes = [ctypes.c_char_p, ctypes.c_char_p]
-    L.fa_append_paged_store_packed.restype = i
-    L.fa_forward_paged_store_packed.argtypes = [ctypes.c_char_p, ctypes.c_char_p, vp, i]
-    L.fa_forward_paged_store_packed.restype = i
-    for packed in (L.fa_select_pages_packed, L.fa_assign_pages_packed, L.fa_forward_scored_packed, L.fa_backward_scored_packed, L.fa_rotary_packed,
+    for packed in (L.fa_append_paged_store_packed, L.fa_forward_paged_store_packed, L.fa_select_pages_packed, L.fa_assign_pages_packed, L.fa_forward_scored_packed, L.fa_backward_scored_packed, L.fa_rotary_packed,
                    L.fa_rotary_backward_packed, L.fa_append_paged_packed, L.fa_forward_paged_packed):
         packed.argtypes = [ctypes.c_char_p]
         packed.restype = i
@@ -533,10 +529,13 @@ _SCORED = struct.Struct("14PNP8iff")                              # fa_scored_ca
 _ROTARY = struct.Struct("PPPPP7q7if")                             # fa_rotary_call
 _APPEND = struct.Struct(_CACHE_FORMAT + "7P9q8if0q")              # fa_append_paged_call
 _PAGED = struct.Struct(_CACHE_FORMAT + "6PNP6iff")                # fa_forward_paged_call
-_STORE = struct.Struct("iPPPP")                                   # fa_page_store
-_SELECT = struct.Struct(_CACHE_FORMAT + "iPPPP" + "4PNP9i0q")     # fa_select_pages_call
+_STORE_FORMAT = "iPPPP"                                           # fa_page_store
+_APPEND_STORE = struct.Struct(_CACHE_FORMAT + "7P9q8if0q" + _STORE_FORMAT)          # fa_append_paged_store_call
+_PAGED_STORE = struct.Struct(_CACHE_FORMAT + "6PNP6iff0q" + _STORE_FORMAT + "Pi0q")  # fa_forward_paged_store_call
+_SELECT = struct.Struct(_CACHE_FORMAT + _STORE_FORMAT + "4PNP9i0q")  # fa_select_pages_call
 _ASSIGN = struct.Struct("Pq10P5i0q")                              # fa_assign_pages_call
 _16_BIT = (torch.bfloat16, torch.float16)
+_PLAIN_STORE = (0, 0, 0, 0, 0)                                    # 16-bit pages
 _PAGE_FORMATS = {torch.float8_e4m3fn: 1, torch.int8: 2}           # fa_page_format; 0: the queries' type
 # of PyTorch's module for CUDA, without the wrappers around them (absent from builds without CUDA)
 _device, _raw_stream = (getattr(torch._C, name, None) for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
@@ -735,13 +734,12 @@ def _table(block_table, kv_lens, B) -> Tuple[int, int, int, int]:
 
 
 def _scales(name: str, t: Optional[torch.Tensor], dev: int, shape) -> int:
+    if t is not None and t.get_device() == dev and t.dtype is torch.float32 and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t is None:
         raise ValueError(f"8-bit pages (and bounds) need {name}")
-    if t.get_device() != dev:
-        _refuse_place(**{name: t})
-    if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 {list(shape)} tensor")
-    return t.data_ptr()
+    _refuse_place(**{name: t})
+    raise ValueError(f"{name} must be a contiguous float32 {list(shape)} tensor")
 
 
 def _bounds(k_bounds, bound_scales, dev: int, n_pages: int, Hkv: int, d: int) -> Tuple[int, int]:
@@ -754,6 +752,8 @@ def _bounds(k_bounds, bound_scales, dev: int, n_pages: int, Hkv: int, d: int) ->
 
 def _store(k_cache, k_scales, v_scales, k_bounds, bound_scales, dtype, dev: int, Hkv: int, d: int):
     """The type of the pages' elements, and fa_page_store's fields (None: 16-bit pages without bounds)."""
+    if k_scales is None and v_scales is None and k_bounds is None and bound_scales is None and k_cache.dtype is dtype:
+        return dtype, None
     fmt = _PAGE_FORMATS.get(k_cache.dtype, 0)
     if fmt == 0:
         if k_scales is not None or v_scales is not None:
@@ -762,8 +762,8 @@ def _store(k_cache, k_scales, v_scales, k_bounds, bound_scales, dtype, dev: int,
             return dtype, None
         ks = vs = 0
     else:
-        n_pages = k_cache.shape[0]
-        ks, vs = _scales("k_scales", k_scales, dev, (n_pages, Hkv)), _scales("v_scales", v_scales, dev, (n_pages, Hkv))
+        shape = (k_cache.shape[0], Hkv)
+        ks, vs = _scales("k_scales", k_scales, dev, shape), _scales("v_scales", v_scales, dev, shape)
         dtype = k_cache.dtype
     kb = bs = 0
     if k_bounds is not None:
@@ -831,11 +831,14 @@ def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
         raise ValueError("q_out without q")
     if s is None:
         s = _handle(stream, dev)
-    call = _APPEND.pack(
+    call = (
         *cache, k.data_ptr(), v.data_ptr(), 0 if q is None else q.data_ptr(), 0 if q_out is None else q_out.data_ptr(),
         0 if q_lens is None else q_lens.data_ptr(), 0 if inv_freq is None else inv_freq.data_ptr(), s,
         *_strides("k", k), *_strides("v", v), *qs, B, H, Hkv, T, d, rot, 1 if interleaved else 0, _DTYPES[dtype], mscale)
-    st = lib.fa_append_paged_packed(call) if store is None else lib.fa_append_paged_store_packed(call, _STORE.pack(*store))
+    if store is None:
+        st = lib.fa_append_paged_packed(_APPEND.pack(*call))
+    else:
+        st = lib.fa_append_paged_store_packed(_APPEND_STORE.pack(*call, *store))
     if st != FA_OK:
         raise FaError(st, "fa_append_paged")
     return q_out
@@ -1036,16 +1039,16 @@ def forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
             workspace = ws_new = torch.empty((need,), dtype=torch.uint8, device=q.device)
     else:
         _refuse_place(workspace=workspace)
-    call = _PAGED.pack(
+    call = (
         *cache, q.data_ptr(), o.data_ptr(), lse.data_ptr(), 0 if q_lens is None else q_lens.data_ptr(),
         0 if alibi_slopes is None else alibi_slopes.data_ptr(), 0 if workspace is None else workspace.data_ptr(),
         0 if workspace is None else _workspace_bytes(workspace), _handle(stream, dev, o_new, lse_new, ws_new),
         B, H, Hkv, T, d, _DTYPES[dtype], 1.0 / d ** 0.5 if scale is None else scale, softcap)
     if store is None and pages is None:
-        st = lib.fa_forward_paged_packed(call)
+        st = lib.fa_forward_paged_packed(_PAGED.pack(*call))
     else:
-        st = lib.fa_forward_paged_store_packed(call, None if store is None else _STORE.pack(*store),
-                                               None if pages is None else pages.data_ptr(), picks)
+        st = lib.fa_forward_paged_store_packed(_PAGED_STORE.pack(*call, *(_PLAIN_STORE if store is None else store),
+                                                                 0 if pages is None else pages.data_ptr(), picks))
     if st != FA_OK:
         raise FaError(st, "fa_forward_paged")
     return o, lse
@@ -1110,6 +1113,18 @@ def select_pages(q: torch.Tensor, k_bounds: torch.Tensor, bound_scales: torch.Te
     return pages
 
 
+def _check_assigned(given, B, max_new, **read) -> None:
+    """Outputs of ``assign_pages`` that the caller gives: they lie apart from one another and from what is read,
+    but for lens and state, which may be their inputs."""
+    for i, (name, t) in enumerate(given):
+        shape = (B, max_new) if name in ("slots", "positions") else (2,) if name == "state" else (B,)
+        _given(name, t, shape, torch.int64 if name == "slots" else torch.int32)
+        for other, x in given[:i]:
+            _apart(name, t, other, x, False)
+        for other, x in read.items():
+            _apart(name, t, other, x, (name, other) in (("lens", "old_lens"), ("lens", "new_lens"), ("state", "free_state")))
+
+
 def assign_pages(block_table: torch.Tensor, old_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
                  free_state: torch.Tensor, page_size: int, max_new: int = 0, *, lens: Optional[torch.Tensor] = None,
                  q_lens: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
@@ -1136,22 +1151,27 @@ def assign_pages(block_table: torch.Tensor, old_lens: torch.Tensor, new_lens: to
     _int32("free_pages", free_pages, (n_free,))
     if max_new < 0:
         raise ValueError("max_new must not be negative")
-    mine, outs = [], []
-    for name, t, shape, dtype in (("lens", lens, (B,), torch.int32), ("q_lens", q_lens, (B,), torch.int32),
-                                  ("slots", slots, (B, max_new), torch.int64),
-                                  ("positions", positions, (B, max_new), torch.int32), ("state", state, (2,), torch.int32)):
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=old_lens.device)
-            mine.append(t)
-        else:
-            _given(name, t, shape, dtype)
-            # written tensors lie apart from one another and from what is read, but for the ones named
-            for other, x in (("block_table", block_table), ("free_pages", free_pages), *outs):
-                _apart(name, t, other, x, False)
-            for other, x in (("old_lens", old_lens), ("new_lens", new_lens), ("free_state", free_state)):
-                _apart(name, t, other, x, (name, other) in (("lens", "old_lens"), ("lens", "new_lens"), ("state", "free_state")))
-        outs.append((name, t))
-    lens, q_lens, slots, positions, state = (t for _, t in outs)
+    given = [(n, t) for n, t in (("lens", lens), ("q_lens", q_lens), ("slots", slots), ("positions", positions), ("state", state))
+             if t is not None]
+    if given:
+        _check_assigned(given, B, max_new, block_table=block_table, free_pages=free_pages, old_lens=old_lens, new_lens=new_lens,
+                        free_state=free_state)
+    mine = []
+    if slots is None:
+        slots = torch.empty((B, max_new), dtype=torch.int64, device=old_lens.device)
+        mine.append(slots)
+    if positions is None:
+        positions = torch.empty((B, max_new), dtype=torch.int32, device=old_lens.device)
+        mine.append(positions)
+    if lens is None:
+        lens = torch.empty_like(old_lens)
+        mine.append(lens)
+    if q_lens is None:
+        q_lens = torch.empty_like(old_lens)
+        mine.append(q_lens)
+    if state is None:
+        state = torch.empty_like(free_state)
+        mine.append(state)
     st = lib.fa_assign_pages_packed(_ASSIGN.pack(
         table, row, old, new_lens.data_ptr(), free_pages.data_ptr(), free_state.data_ptr(), state.data_ptr(), lens.data_ptr(),
         q_lens.data_ptr(), slots.data_ptr(), positions.data_ptr(), _handle(stream, dev, *mine), B, width, page_size, n_free,

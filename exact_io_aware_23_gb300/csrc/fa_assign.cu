@@ -11,8 +11,10 @@
 // alone, whether the table has it already or not.
 //
 // What bounds it: the latency of a launch and of three reads one after another (lengths, state, ring), then the
-// bytes of the slots.  One cluster of blocks; each sums up all lengths for itself, and only what may be the
-// caller's own input (lengths, ring state) is written behind a barrier of the cluster.
+// bytes of the slots.  Few tokens: one block does it all.  Many: their places come first, from a kernel with a
+// block for every 1024 tokens of a sequence, each of which sums up the lengths for itself; it writes nothing that
+// may be the caller's own input.  (40 sequences of up to 4096 tokens, in one kernel, a cluster of 8 blocks with a
+// barrier before the lengths are written: 27 us; in two: 12.)
 #include <cuda_runtime.h>
 
 #include "fa_paged.cuh"
@@ -22,16 +24,15 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCtas = 8;                // of a cluster
+constexpr int kPlaceThreads = 256;         // of a block for tokens' places, each of
+constexpr int kPlaceTokens = 1024;         // so many tokens
 
-__device__ __forceinline__ uint32_t cluster_ctas() {
-  uint32_t n;
-  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
-  return n;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+// The pages of n tokens, by multiplication with the page size's rounded-up reciprocal: exact for n below 2^31 and
+// pages of up to 4096 tokens (2^43 / page, the error below n / 2^43 of a page).
+__device__ __forceinline__ int whole_pages(const AssignArgs& a, int n) { return (int)__umul64hi((uint64_t)(uint32_t)n << 21, a.page_magic); }
+__device__ __forceinline__ int pages_for(const AssignArgs& a, int n) {
+  const int w = whole_pages(a, n);
+  return w + (n - w * a.page_size > 0 ? 1 : 0);
 }
 
 struct Change {
@@ -41,53 +42,95 @@ __device__ __forceinline__ Change change_of(const AssignArgs& a, int b) {
   Change c;
   c.old = a.old_lens[b];
   c.now = a.new_lens[b];
-  // sums in 64 bits: lengths reach to 2^31 - 1
-  c.held = (int)(((int64_t)c.old + a.page_size - 1) / a.page_size);
-  c.want = (int)(((int64_t)c.now + a.page_size - 1) / a.page_size);
+  c.held = pages_for(a, max(c.old, 0));
+  c.want = pages_for(a, max(c.now, 0));
   return c;
 }
 
-// The block's sum of x.
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* words) {
+// What the whole call comes to; the same in every block.
+struct Totals {
+  int64_t grow, less, grow_before;         // the last: of the sequences before `upto`
+  bool ok;
+};
+template <int kThr>
+__device__ __forceinline__ Totals totals_of(const AssignArgs& a, int first, int count, int upto, int64_t (*words)[kThr / 32]) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t cap = (int64_t)a.max_pages * a.page_size;
+  // growth (with a large number for a length that is none), releases, growth before
+  int64_t x[3] = {0, 0, 0};
+  for (int b = threadIdx.x; b < a.B; b += kThr) {
+    const Change c = change_of(a, b);
+    const int grow = max(c.want - c.held, 0);
+    x[0] += c.old < 0 || c.now < 0 || c.old > cap || c.now > cap ? (int64_t)1 << 40 : grow;
+    x[1] += max(c.held - c.want, 0);
+    x[2] += b < upto ? grow : 0;
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  for (int k = 0; k < 3; ++k) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x[k] += __shfl_xor_sync(0xffffffffu, x[k], o);
+    if (lane == 0) words[k][warp] = x[k];
+  }
   __syncthreads();
-  if (lane == 0) words[warp] = x;
-  __syncthreads();
-  int64_t sum = 0;
-  for (int i = 0; i < kWarps; ++i) sum += words[i];
-  return sum;
+  Totals t{0, 0, 0, false};
+  for (int i = 0; i < kThr / 32; ++i) {
+    t.grow += words[0][i];
+    t.less += words[1][i];
+    t.grow_before += words[2][i];
+  }
+  // pages given back must not reach those handed out
+  t.ok = first >= 0 && first < a.n_free && count >= 0 && t.grow <= count && count + t.less <= a.n_free;
+  return t;
 }
 
-__global__ void __launch_bounds__(kThreads) assign_kernel(const AssignArgs a) {
-  __shared__ int64_t words[kWarps];
-  __shared__ int scan[2][kWarps];
-  __shared__ int olds[kThreads], news[kThreads], grown[kThreads], given[kThreads];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int cta = blockIdx.x, ctas = (int)cluster_ctas();
-  const int first = a.state[0], count = a.state[1];
-  const int64_t cap = (int64_t)a.max_pages * a.page_size;
-
-  // whether all of it can be done
-  int64_t grow = 0, less = 0, bad = 0;
-  for (int b = threadIdx.x; b < a.B; b += kThreads) {
-    const Change c = change_of(a, b);
-    bad += c.old < 0 || c.now < 0 || c.old > cap || c.now > cap;
-    grow += max(c.want - c.held, 0);
-    less += max(c.held - c.want, 0);
+// entry i of the ring, i below 3 n
+__device__ __forceinline__ int32_t* ring(const AssignArgs& a, int64_t i) {
+  i -= i >= a.n_free ? a.n_free : 0;
+  return a.free_pages + (i >= a.n_free ? i - a.n_free : i);
+}
+// Token t of sequence b: its place, and its slot; the sequence's first new page is the ring's entry `from`.
+__device__ __forceinline__ void place(const AssignArgs& a, const Change& c, int b, int t, int64_t from, bool ok) {
+  const int64_t at = (int64_t)b * a.T + t;
+  int64_t slot = -1;
+  int pos = -1;
+  if (ok && t < c.now - c.old) {
+    pos = c.old + t;
+    const int j = whole_pages(a, pos);
+    const int page = j < c.held ? a.table[(int64_t)b * a.table_stride + j] : *ring(a, from + (j - c.held));
+    slot = (int64_t)page * a.page_size + (pos - j * a.page_size);
   }
-  grow = block_sum(grow, words);
-  less = block_sum(less, words);
-  bad = block_sum(bad, words);
-  const bool ok = bad == 0 && first >= 0 && first < a.n_free && count >= 0 && grow <= count && count - grow + less <= a.n_free &&
-                  count + less <= a.n_free;
-  if (!ok && cta == 0 && threadIdx.x == 0) atomicExch(a.err, kDevBadOffsets);
-  const int64_t all = (int64_t)cta * kThreads + threadIdx.x, threads = (int64_t)ctas * kThreads;
-  auto ring = [&](int64_t i) {                             // i below 3 n
-    i -= i >= a.n_free ? a.n_free : 0;
-    return a.free_pages + (i >= a.n_free ? i - a.n_free : i);
-  };
+  a.slots[at] = slot;
+  a.positions[at] = pos;
+}
+
+// Block x: tokens from x % chunks * kPlaceTokens on of `per` sequences (one, unless there are thousands).
+__global__ void __launch_bounds__(kPlaceThreads) place_kernel(const AssignArgs a, const int chunks, const int per) {
+  __shared__ int64_t words[3][kPlaceThreads / 32];
+  const int b0 = blockIdx.x / chunks * per, t0 = blockIdx.x % chunks * kPlaceTokens;
+  const int first = a.state[0], count = a.state[1];
+  const Totals all = totals_of<kPlaceThreads>(a, first, count, b0, words);
+  const int end = min(a.T, t0 + kPlaceTokens);
+  int64_t from = (int64_t)first + all.grow_before;
+  for (int b = b0; b < min(a.B, b0 + per); ++b) {
+    const Change c = change_of(a, b);
+#pragma unroll 4
+    for (int t = t0 + threadIdx.x; t < end; t += kPlaceThreads) place(a, c, b, t, from, all.ok);
+    from += max(c.want - c.held, 0);
+  }
+}
+
+// Tables, ring, lengths and state; places too where `places`.
+__global__ void __launch_bounds__(kThreads) assign_kernel(const AssignArgs a, const int places) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ int64_t words[3][kWarps];
+  __shared__ int scan[2][kWarps];
+  __shared__ Change changes[kThreads];
+  __shared__ int grown[kThreads], given[kThreads];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int first = a.state[0], count = a.state[1];
+  const Totals all = totals_of<kThreads>(a, first, count, 0, words);
+  const bool ok = all.ok;
+  if (!ok && threadIdx.x == 0) atomicExch(a.err, kDevBadOffsets);
 
   int G = 0, R = 0;                                        // of the sequences before the chunk
   for (int b0 = 0; b0 < a.B; b0 += kThreads) {
@@ -104,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) assign_kernel(const AssignArgs a) {
         down += y;
       }
     }
-    __syncthreads();                                       // the chunk before is done with
+    if (b0 > 0) __syncthreads();                           // the chunk before is done with
     if (lane == 31) {
       scan[0][warp] = up;
       scan[1][warp] = down;
@@ -119,71 +162,63 @@ __global__ void __launch_bounds__(kThreads) assign_kernel(const AssignArgs a) {
       G += scan[0][w];
       R += scan[1][w];
     }
-    olds[threadIdx.x] = c.old;
-    news[threadIdx.x] = c.now;
-    grown[threadIdx.x] = base_up + up - up0;
-    given[threadIdx.x] = base_down + down - down0;
-    __syncthreads();
-
-    // pages: a warp takes a sequence
-    if (ok)
-      for (int i = cta * kWarps + warp; i < nb; i += ctas * kWarps) {
-        int32_t* const row = a.table + (int64_t)(b0 + i) * a.table_stride;
-        const int held = (int)(((int64_t)olds[i] + a.page_size - 1) / a.page_size);
-        const int want = (int)(((int64_t)news[i] + a.page_size - 1) / a.page_size);
-        for (int j = held + lane; j < want; j += 32) row[j] = *ring((int64_t)first + grown[i] + (j - held));
-        for (int j = want + lane; j < held; j += 32) *ring((int64_t)first + count + given[i] + (j - want)) = row[j];
-      }
-    // places of the new tokens
-    const int64_t tokens = (int64_t)nb * a.T;
-    for (int64_t x = all; x < tokens; x += threads) {
-      const int i = (int)(x / a.T), t = (int)(x - (int64_t)i * a.T);
-      const int64_t at = (int64_t)(b0 + i) * a.T + t;
-      const int pos = olds[i] + t;
-      int64_t slot = -1;
-      if (ok && t < news[i] - olds[i]) {
-        const int held = (int)(((int64_t)olds[i] + a.page_size - 1) / a.page_size), j = pos / a.page_size;
-        const int page = j < held ? a.table[(int64_t)(b0 + i) * a.table_stride + j]
-                                  : *ring((int64_t)first + grown[i] + (j - held));
-        slot = (int64_t)page * a.page_size + (pos - j * a.page_size);
-      }
-      a.slots[at] = slot;
-      a.positions[at] = slot < 0 ? -1 : pos;
+    const int before = base_up + up - up0, behind = base_down + down - down0;
+    changes[threadIdx.x] = c;
+    grown[threadIdx.x] = before;
+    given[threadIdx.x] = behind;
+    if (b < a.B) a.q_lens[b] = ok ? max(c.now - c.old, 0) : 0;
+    // a page or two more, or less: the sequence's own thread
+    const bool few = abs(c.want - c.held) <= 2;
+    if (few) {
+      int32_t* const row = a.table + (int64_t)b * a.table_stride;
+      for (int j = c.held; j < c.want; ++j) row[j] = *ring(a, (int64_t)first + before + (j - c.held));
+      for (int j = c.want; j < c.held; ++j) *ring(a, (int64_t)first + count + behind + (j - c.want)) = row[j];
     }
-    for (int64_t i = all; i < nb; i += threads) a.q_lens[b0 + i] = ok ? max(news[i] - olds[i], 0) : 0;
+    // many: a warp takes the sequence
+    __syncthreads();
+    if (ok)
+      for (int i = warp; i < nb; i += kWarps) {
+        const Change d = changes[i];
+        if (abs(d.want - d.held) <= 2) continue;
+        int32_t* const row = a.table + (int64_t)(b0 + i) * a.table_stride;
+        for (int j = d.held + lane; j < d.want; j += 32) row[j] = *ring(a, (int64_t)first + grown[i] + (j - d.held));
+        for (int j = d.want + lane; j < d.held; j += 32) *ring(a, (int64_t)first + count + given[i] + (j - d.want)) = row[j];
+      }
+    if (places)
+      for (int x = threadIdx.x; x < nb * a.T; x += kThreads) {
+        const int i = a.T == 1 ? x : x / a.T;
+        place(a, changes[i], b0 + i, x - i * a.T, (int64_t)first + grown[i], ok);
+      }
   }
   // lengths and state may be written over those that were read
-  if (ctas > 1) cluster_sync();
-  else __syncthreads();
-  for (int64_t b = all; b < a.B; b += threads) {
+  __syncthreads();
+  for (int b = threadIdx.x; b < a.B; b += kThreads) {
     const int n = ok ? a.new_lens[b] : a.old_lens[b];
     a.lens[b] = n;
   }
-  if (all == 0) {
-    int64_t f = (int64_t)first + (ok ? grow : 0);
+  if (threadIdx.x == 0) {
+    const int64_t f = (int64_t)first + (ok ? all.grow : 0);
     a.state_out[0] = (int)(ok && f >= a.n_free ? f - a.n_free : f);
-    a.state_out[1] = ok ? (int)(count - grow + less) : count;
+    a.state_out[1] = ok ? (int)(count - all.grow + all.less) : count;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_assign(const AssignArgs& a, cudaStream_t s) {
-  // a block for every 2048 tokens' places
-  const int64_t work = (int64_t)a.B * a.T;
-  int ctas = 1;
-  while (ctas < kMaxCtas && ctas * (int64_t)2048 < work) ctas *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, assign_kernel, a);
+cudaError_t launch_assign(const AssignArgs& args, cudaStream_t s) {
+  AssignArgs a = args;
+  a.page_magic = ((uint64_t(1) << 43) + a.page_size - 1) / a.page_size;
+  // the tokens that one block places in the time of another launch
+  const bool places = (int64_t)a.B * a.T <= 4 * kThreads;
+  if (!places) {
+    const int chunks = (a.T + kPlaceTokens - 1) / kPlaceTokens;
+    const int per = (a.B + 4095) / 4096, groups = (a.B + per - 1) / per;       // (each block reads all lengths)
+    place_kernel<<<(unsigned)((int64_t)groups * chunks), kPlaceThreads, 0, s>>>(a, chunks, per);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  assign_kernel<<<1, kThreads, 0, s>>>(a, places);
+  return cudaGetLastError();
 }
 
 }  // namespace fa

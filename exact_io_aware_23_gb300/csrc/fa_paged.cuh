@@ -117,6 +117,7 @@ struct AssignArgs {
   int32_t* table;
   int64_t table_stride;
   int B, max_pages, page_size, T;
+  uint64_t page_magic;       // 2^43 / page_size, rounded up
   const int32_t* old_lens;
   const int32_t* new_lens;
   int32_t* free_pages;       // a ring of n_free

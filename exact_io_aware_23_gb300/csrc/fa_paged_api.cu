@@ -350,18 +350,19 @@ fa_status fa_assign_pages(int32_t* block_table, int64_t table_stride, int B, int
   return fa::launch_assign(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-fa_status fa_append_paged_store_packed(const fa_append_paged_call* c, const fa_page_store* store) {
-  if (c == nullptr) return FA_ERR_INVALID_ARG;
-  return fa_append_paged_store(&c->cache, store, c->k, c->k_strides, c->v, c->v_strides, c->q, c->q_strides, c->q_out,
+fa_status fa_append_paged_store_packed(const fa_append_paged_store_call* call) {
+  if (call == nullptr) return FA_ERR_INVALID_ARG;
+  const fa_append_paged_call* c = &call->call;
+  return fa_append_paged_store(&c->cache, &call->store, c->k, c->k_strides, c->v, c->v_strides, c->q, c->q_strides, c->q_out,
                                c->B, c->H, c->Hkv, c->T, c->d, c->q_lens, c->inv_freq, c->rotary_dim, c->interleaved,
                                c->mscale, static_cast<fa_dtype>(c->dtype), c->stream);
 }
 
-fa_status fa_forward_paged_store_packed(const fa_forward_paged_call* c, const fa_page_store* store, const int32_t* pages,
-                                        int n_select) {
-  if (c == nullptr) return FA_ERR_INVALID_ARG;
+fa_status fa_forward_paged_store_packed(const fa_forward_paged_store_call* call) {
+  if (call == nullptr) return FA_ERR_INVALID_ARG;
+  const fa_forward_paged_call* c = &call->call;
   const fa_score_mod mod{c->softcap, c->alibi_slopes, nullptr};
-  return fa_forward_paged_store(c->q, &c->cache, store, pages, n_select, c->o, c->lse, c->B, c->H, c->Hkv, c->T, c->d,
+  return fa_forward_paged_store(c->q, &c->cache, &call->store, call->pages, call->n_select, c->o, c->lse, c->B, c->H, c->Hkv, c->T, c->d,
                                 c->scale, c->q_lens, &mod, static_cast<fa_dtype>(c->dtype), c->workspace,
                                 c->workspace_bytes, c->stream);
 }

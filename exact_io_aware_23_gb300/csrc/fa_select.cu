@@ -15,7 +15,8 @@
 // of the K-th largest one's bits, 1024 bins at a time.  The bins are laid over the range that the scores
 // have: by the bits from the top nearly all would meet in the few bins of their exponents.
 // Where there are fewer of them than SMs, and many pages, a kernel of its own scores the pages on all SMs first.
-// (A cluster of blocks for each instead, scores in the first one's shared memory: SCORETIMES.)
+// (A cluster of 4 or 8 blocks for each instead, scores in the first one's shared memory: 32 and 36 us for two
+// sequences of 8192 pages and 8 key heads, in two kernels 23; clusters of 8 do not all find their SMs at once.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

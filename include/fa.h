@@ -651,6 +651,16 @@ typedef struct {
   float scale, softcap;
 } fa_forward_paged_call;
 typedef struct {
+  fa_append_paged_call call;
+  fa_page_store store;
+} fa_append_paged_store_call;
+typedef struct {
+  fa_forward_paged_call call;
+  fa_page_store store;
+  const int32_t* pages;
+  int n_select;
+} fa_forward_paged_store_call;
+typedef struct {
   fa_paged_cache cache;
   fa_page_store store;
   const void* q;
@@ -679,10 +689,8 @@ fa_status fa_rotary_packed(const fa_rotary_call* call);
 fa_status fa_rotary_backward_packed(const fa_rotary_call* call);
 fa_status fa_append_paged_packed(const fa_append_paged_call* call);
 fa_status fa_forward_paged_packed(const fa_forward_paged_call* call);
-fa_status fa_append_paged_store_packed(const fa_append_paged_call* call, const fa_page_store* store);
-fa_status fa_forward_paged_store_packed(const fa_forward_paged_call* call,
-                                        const fa_page_store* store, const int32_t* pages,
-                                        int n_select);
+fa_status fa_append_paged_store_packed(const fa_append_paged_store_call* call);
+fa_status fa_forward_paged_store_packed(const fa_forward_paged_store_call* call);
 fa_status fa_select_pages_packed(const fa_select_pages_call* call);
 fa_status fa_assign_pages_packed(const fa_assign_pages_call* call);
 

@@ -124,18 +124,19 @@ def test_assign_checks():
 def test_packed_layouts():
     for fn in (fa.lib.fa_select_pages_packed, fa.lib.fa_assign_pages_packed):
         assert fn(None) == INVALID
-    assert fa.lib.fa_append_paged_store_packed(None, None) == INVALID
-    assert fa.lib.fa_forward_paged_store_packed(None, None, None, 0) == INVALID
+    assert fa.lib.fa_append_paged_store_packed(None) == INVALID
+    assert fa.lib.fa_forward_paged_store_packed(None) == INVALID
     header = open(os.path.join(os.path.dirname(fa.LIB_PATH), os.pardir, "include", "fa.h")).read()
-    size = {"int": 4, "float": 4, "fa_paged_cache": ctypes.sizeof(fa.FaPagedCache), "fa_page_store": ctypes.sizeof(fa.FaPageStore)}
-    for name, packed in (("fa_select_pages_call", fa._SELECT), ("fa_assign_pages_call", fa._ASSIGN)):
+    size = {"int": 4, "float": 4, "fa_paged_cache": ctypes.sizeof(fa.FaPagedCache), "fa_page_store": ctypes.sizeof(fa.FaPageStore),
+            "fa_append_paged_call": fa._APPEND.size, "fa_forward_paged_call": fa._PAGED.size}
+    for name, packed in (("fa_select_pages_call", fa._SELECT), ("fa_assign_pages_call", fa._ASSIGN),
+                         ("fa_append_paged_store_call", fa._APPEND_STORE), ("fa_forward_paged_store_call", fa._PAGED_STORE)):
         body = re.search(r"typedef struct \{([^{}]*)\} " + name + ";", header).group(1)
         total = 0
         for field in re.sub(r"/\*.*?\*/", "", body, flags=re.S).split(";")[:-1]:
             kind = field.split()[1 if field.split()[0] == "const" else 0]
             total += sum(8 if "*" in one else size.get(kind, 8) for one in field.split(","))
         assert packed.size == (total + 7) // 8 * 8, name
-    assert fa._STORE.size == ctypes.sizeof(fa.FaPageStore)
 
 
 def test_host_tensors_are_refused():
