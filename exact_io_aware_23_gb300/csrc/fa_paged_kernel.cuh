@@ -357,6 +357,19 @@ __device__ __forceinline__ bool all_arrived(unsigned long long* words, int part0
   return there;
 }
 
+// The same for 8-bit pages, whose CTAs announce their parts at the end alone: a word for each segment counts them,
+// {the call's number, the count}.  Each CTA sees to the number before its first tile is there (by one
+// compare-and-swap from whatever the word holds, unless another CTA was first), so that the end takes one
+// fence and one addition, and the one that brings the count to all parts joins them and clears the word.
+__device__ __forceinline__ void open_count(unsigned long long* word, unsigned long long call) {
+  unsigned long long w;
+  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(w) : "l"(word) : "memory");
+  if ((w ^ (call << 16)) >> 16 != 0) atomicCAS(word, w, call << 16);
+}
+__device__ __forceinline__ bool count_part(unsigned long long* word, int parts) {
+  return (int)(atomicAdd(word, 1ull) & 0xffffu) == parts - 1;
+}
+
 // kShared: CTAs share all segments' units.  Otherwise a CTA has one segment to itself (few short
 // ones: nothing to join, nothing to reckon).
 template <typename C, bool kShared>
@@ -633,8 +646,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
     const int ca = share.owner(s0 + C::kSegment), cb = share.owner(s0 + C::kSegment + seg.tiles - 1);
     const int row0 = seg.block * kRows;
     // the first CTA may have begun inside an earlier segment: this one is then its second part
-    parted[k] = Parted{((int64_t)seg.b * a.H + seg.hk * G) * a.T + row0, min(kRows, rows - row0), ca, cb,
-                       2 * ca + (share.begin(ca) >= s0 ? 0 : 1)};
+    const int part0 = 2 * ca + (share.begin(ca) >= s0 ? 0 : 1);
+    parted[k] = Parted{((int64_t)seg.b * a.H + seg.hk * G) * a.T + row0, min(kRows, rows - row0), ca, cb, part0};
+    if (C::kDefer) open_count(a.arrivals + part0, a.call);
   };
   read_rows();                                          // before the copies fill the way to memory
 #pragma unroll 1
@@ -648,7 +662,17 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
   // With 16-bit ones each is done with at its end, while twice the bytes are on their way: no CTA then
   // has two segments to join at the end (B64, 1 to 8192 keys, 159 us against 163).
   auto finish = [&](const int mine) {                   // bits: the first part, the second
-    if (warp == 0) {
+    if (C::kDefer) {
+      if (threadIdx.x == 0) {
+        asm volatile("fence.acq_rel.gpu;" ::: "memory");  // releases what the whole CTA wrote before its barrier
+        int there = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if ((mine >> k & 1) != 0 && count_part(a.arrivals + parted[k].part0, parted[k].cb - parted[k].ca + 1)) there |= 1 << k;
+        if (there != 0) asm volatile("fence.acq_rel.gpu;" ::: "memory");     // the parts, for the CTA after its barrier
+        *flag = there;
+      }
+    } else if (warp == 0) {
       announce(a.arrivals + 2 * blockIdx.x, mine, a.call);
       int there = 0;
 #pragma unroll 1
@@ -666,7 +690,11 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
       const int n_rows = parted[k].n_rows;
       const int64_t qrow = parted[k].qrow;
       const int ca = parted[k].ca, cb = parted[k].cb, part0 = parted[k].part0;
-      for (int i = ca + threadIdx.x; i <= cb; i += kThreads) a.arrivals[i == ca ? part0 : 2 * i] = 0ull;
+      if (C::kDefer) {
+        if (threadIdx.x == 0) a.arrivals[part0] = 0ull;
+      } else {
+        for (int i = ca + threadIdx.x; i <= cb; i += kThreads) a.arrivals[i == ca ? part0 : 2 * i] = 0ull;
+      }
       // Up to kJoin parts at a time: their statistics to shared memory, all in flight together, then
       // their outputs, several in flight, onto what the parts before came to.
       auto part_of = [&](int i) { return (int64_t)(i == ca ? part0 : 2 * i) * kRows; };
@@ -683,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
       for (int i0 = ca; i0 <= cb; i0 += C::kJoin) {
         const int np = min(C::kJoin, cb + 1 - i0);
         // several parts' outputs of item x; past the last part its own again, not used
-        constexpr int kFlight = kFlip ? 8 : 16;
+        constexpr int kFlight = 16;
         auto outputs = [&](int x, int i, float4 (&v)[kFlight]) {
 #pragma unroll
           for (int k = 0; k < kFlight; ++k)
