@@ -37,8 +37,8 @@ bool paged_counts(int B, int Hkv, int rows, int capacity) {
 PagedWorkspace paged_workspace(int ctas, int d) {
   PagedWorkspace w;
   const size_t rows = 2 * (size_t)ctas * kRows;
-  static_assert(kFlipCtasPerSm * 8 == kCtasPerSm * kRows, "parts of 8 rows take the place of those of 16");
-  w.ml = (2 * (size_t)ctas * (kFlipCtasPerSm / kCtasPerSm) * sizeof(unsigned long long) + 255) / 256 * 256;
+  static_assert(flip_ctas(64) * 8 <= kCtasPerSm * kRows && flip_ctas(128) * 8 <= kCtasPerSm * kRows, "parts of 8 rows take the place of those of 16");
+  w.ml = (2 * (size_t)ctas * 2 * sizeof(unsigned long long) + 255) / 256 * 256;
   w.o = w.ml + rows * sizeof(float2);
   w.total = (w.o + rows * d * sizeof(float) + 255) / 256 * 256;
   return w;

@@ -66,9 +66,10 @@ constexpr int kThreads = 32 * kWarps;
 // hold twice the output in registers and spill (B8 H64 Hkv8 T7 d128, 4096 keys: 95 us against 74).
 constexpr int kRows = 16;
 constexpr int kCtasPerSm = 8 / kWarps;
-constexpr int kFlipCtasPerSm = 4;
-constexpr int kSegment = 4;
 constexpr int kFlipSegment = 12;           // (4: 10 % longer for 64 chosen pages of 64 keys; 24: the same for d = 64)
+// kFlip, d = 128: three CTAs an SM and tiles of 32 keys, at d = 64 four and the same (4 KB in place of 8).
+constexpr int flip_ctas(int d) { return d == 128 ? 3 : 4; }
+constexpr int kSegment = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kUnitSlack = 16.0f;         // ... and the unit of the values' scales
@@ -85,12 +86,12 @@ struct Cfg {
   static constexpr int kRows = kFlip ? 8 : 16;
   static constexpr bool kDefer = k8;
   static constexpr int kSegment = kFlip ? kFlipSegment : fa::kSegment;
-  static constexpr int kCtasPerSm = kFlip ? kFlipCtasPerSm : fa::kCtasPerSm;
+  static constexpr int kCtasPerSm = kFlip ? flip_ctas(D) : fa::kCtasPerSm;
   static constexpr bool kF16 = kF16_ || k8, kPick = kPick_;
   using Elem = std::conditional_t<k8, uint8_t, uint16_t>;
   static constexpr int kElem = sizeof(Elem);
   static constexpr int kRowBytes = D * kElem;
-  static constexpr int kKeys = (kFlip ? 2048 : 4096) / kRowBytes;   // keys of a tile: 8 (4) KB with the values
+  static constexpr int kKeys = (kFlip && D == 64 ? 2048 : 4096) / kRowBytes;   // keys of a tile: 8 (4) KB with the values
   static constexpr int kParts = kKeys / 16;                   // 16-key parts of a tile, each in one page
   static constexpr int kHalf = kKeys * kRowBytes;             // a tile's keys (or values)
   static constexpr int kStage = 2 * kHalf;
@@ -218,7 +219,7 @@ struct Reckoning {
     int sum = 0;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      keep[c] = units_of<C>(a, heads, c * 32 + lane, err);
+      keep[c] = c * 32 < a.B ? units_of<C>(a, heads, c * 32 + lane, err) : 0;
       sum += keep[c];
     }
     for (int b = 256 + lane; b < a.B; b += 32) sum += units_of<C>(a, heads, b, err);
@@ -247,7 +248,7 @@ struct Reckoning {
     };
 #pragma unroll
     for (int c = 0; c < 8; ++c)
-      if (chunk(keep[c], c * 32)) return;
+      if (c * 32 < a.B && chunk(keep[c], c * 32)) return;
     for (int b0 = 256; b0 < a.B; b0 += 32)
       if (chunk(units_of<C>(a, heads, b0 + lane, nullptr), b0)) return;
   }
@@ -1152,7 +1153,7 @@ template <int D, int kStore, bool kPick>
 cudaError_t paged8(const PagedArgs& a, cudaStream_t s) {
   if (a.H / a.Hkv * a.T > 8) return paged<Cfg<D, kStore, true, kPick>>(a, s);
   PagedArgs f = a;
-  f.ctas = a.ctas / kCtasPerSm * kFlipCtasPerSm;
+  f.ctas = a.ctas / kCtasPerSm * flip_ctas(D);
   return paged<Cfg<D, kStore, true, kPick, true>>(f, s);
 }
 template <int kStore>
