@@ -32,9 +32,7 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 256;              // few tokens: eight warps
-constexpr int kHold = 2;                   // rows of 16 values that a lane of them holds
-constexpr int kPageRows = 4;               // ... and a thread of a block for many tokens
+constexpr int kPageRows = 4;               // rows of 16 values that a thread holds
 
 template <typename T>
 __device__ __forceinline__ void round_values(float (&x)[8]) {
@@ -43,19 +41,6 @@ __device__ __forceinline__ void round_values(float (&x)[8]) {
   unpack(r, x);
 }
 
-// 16 codes of a row, as they lie in memory
-template <int kStore>
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
-  if constexpr (kStore == FA_PAGES_INT8) {
-    int i[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) i[e] = __float2int_rn(x[e] * inv);
-    return make_uint2(pack_s8(i[0], i[1], i[2], i[3]), pack_s8(i[4], i[5], i[6], i[7]));
-  } else {
-    return make_uint2(pack_e4m3(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
-                      pack_e4m3(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
-  }
-}
 // four codes times a power of two, rounded again
 template <int kStore>
 __device__ __forceinline__ uint32_t recode(uint32_t c, float ratio) {
@@ -106,170 +91,6 @@ __device__ __forceinline__ bool page_exists(const AppendArgs& a, const PageWork&
   return false;
 }
 
-// One head of a page that gets a few tokens, by a warp: kHold rows of 16 values a lane.
-template <typename T, int kStore>
-__device__ __forceinline__ void write_rows(const AppendArgs& a, const StoreArgs& st, const PageWork& w, int b, int h) {
-  constexpr bool k8 = kStore != FA_PAGES_16BIT;
-  const int lt = threadIdx.x % 32;
-  const int units = a.d / kUnit, rows = 32 / units;
-  const int u = lt % units, r = lt / units;
-  const Unit t = unit_of(u, a.rot);
-  const bool turns = t.turns && h < a.Hkv;
-  uint64_t frac[8];
-  float c[kHold][8], s[kHold][8];
-  if (turns) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) frac[i] = turn_fraction(a.rot.inv_freq[8 * u + i]);
-#pragma unroll
-    for (int i = 0; i < kHold; ++i)
-      if (i * rows + r < w.n) angles(frac, w.first + i * rows + r, a.rot, c[i], s[i]);
-  }
-  const bool is_k = h < a.Hkv;
-  const int g = is_k ? h : h - a.Hkv;
-  const Strides sd = is_k ? a.ks : a.vs;
-  const T* const src = static_cast<const T*>(is_k ? a.k : a.v) + b * sd.b + g * sd.h + (int64_t)(w.first - w.begin) * sd.n;
-  float* const scales = is_k ? st.k_scales : st.v_scales;
-  const int64_t place = w.page * a.Hkv + g;
-  float old = 0.f, old_unit = 0.f;
-  if (k8 && w.kept > 0) old = scales[place];
-  const bool bounds = is_k && st.bounds != nullptr;
-  if (bounds && w.kept > 0) old_unit = st.bound_scales[place];
-
-  // a row's 16 values: read, turned
-  auto row = [&](int i, float (&x)[8], float (&y)[8]) {
-    const T* p = src + (int64_t)(i * rows + r) * sd.n;
-    const Raw8<T> lo = load8(p + t.lo), hi = load8(p + t.hi);
-    unpack(lo, x);
-    unpack(hi, y);
-    if (turns && is_k) {
-      turn8(x, y, a.rot.interleaved, c[i], s[i]);
-      if (!k8) {                                       // 16-bit pages: bounds of what is stored
-        round_values<T>(x);
-        round_values<T>(y);
-      }
-    }
-  };
-  float x[kHold][8], y[kHold][8];
-  uint32_t amax = 0;
-  float mn[2][8], mx[2][8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    mn[0][e] = mn[1][e] = INFINITY;
-    mx[0][e] = mx[1][e] = -INFINITY;
-  }
-  auto look = [&](const float (&x)[8], const float (&y)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) amax = max(amax, max(abs_bits(x[e]), abs_bits(y[e])));
-    if (bounds) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        mn[0][e] = fminf(mn[0][e], x[e]);
-        mx[0][e] = fmaxf(mx[0][e], x[e]);
-        mn[1][e] = fminf(mn[1][e], y[e]);
-        mx[1][e] = fmaxf(mx[1][e], y[e]);
-      }
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < kHold; ++i)
-    if (i * rows + r < w.n) {
-      row(i, x[i], y[i]);
-      look(x[i], y[i]);
-    }
-
-  // the team's largest value and bounds
-  if (k8 || bounds) {
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    if (bounds) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float& lo = mn[e / 8][e % 8];
-        float& hi = mx[e / 8][e % 8];
-        for (int o = 16; o >= units; o >>= 1) {
-          lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-          hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        }
-      }
-    }
-    __syncwarp();
-  }
-  const bool finite = amax < 0x7f800000u;
-
-  // codes
-  typename StoredAs<T, kStore>::type* const dst =
-      static_cast<typename StoredAs<T, kStore>::type*>(is_k ? a.cache.k : a.cache.v) + w.page * a.cache.page_stride +
-      g * a.cache.head_stride;
-  float inv = 0.f, scale = 0.f;
-  if constexpr (k8) {
-    const float need = finite ? power_scale<kStore == FA_PAGES_INT8>(amax) : __uint_as_float(0x7fc00000u);
-    scale = old != old || need != need ? __uint_as_float(0x7fc00000u) : fmaxf(old, need);
-    inv = scale == scale ? 1.f / scale : 0.f;
-  }
-  auto store = [&](int i, float (&x)[8], float (&y)[8]) {
-    auto* p = dst + (int64_t)(w.kept + i * rows + r) * a.cache.token_stride;
-    if constexpr (k8) {
-      if (scale != scale) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
-      }
-      *reinterpret_cast<uint2*>(p + t.lo) = encode8<kStore>(x, inv);
-      *reinterpret_cast<uint2*>(p + t.hi) = encode8<kStore>(y, inv);
-    } else {
-      Raw8<T> lo, hi;
-      pack(x, lo);
-      pack(y, hi);
-      store8(p + t.lo, lo);
-      store8(p + t.hi, hi);
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < kHold; ++i)
-    if (i * rows + r < w.n) store(i, x[i], y[i]);
-  if constexpr (k8) {
-    if (w.kept > 0 && scale > old) {                  // (not where either is NaN)
-      const float ratio = old / scale;
-      for (int i = r; i < w.kept; i += rows) {
-        uint4* p = reinterpret_cast<uint4*>(dst + (int64_t)i * a.cache.token_stride + kUnit * u);
-        uint4 v = *p;
-        v.x = recode<kStore>(v.x, ratio);
-        v.y = recode<kStore>(v.y, ratio);
-        v.z = recode<kStore>(v.z, ratio);
-        v.w = recode<kStore>(v.w, ratio);
-        *p = v;
-      }
-    }
-    if (lt == 0) scales[place] = scale;
-  }
-  if (bounds && lt < units) {
-    const float need = finite ? power_scale<true>(amax) : __uint_as_float(0x7fc00000u);
-    const float unit = old_unit != old_unit || need != need ? __uint_as_float(0x7fc00000u) : fmaxf(old_unit, need);
-    const float by = unit == unit ? 1.f / unit : 0.f, ratio = w.kept > 0 && unit == unit ? old_unit / unit : 0.f;
-    int8_t* const q = st.bounds + place * 2 * a.d;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int at = half == 0 ? t.lo : t.hi;
-      int lo[8], hi[8];
-      uint2* const plo = reinterpret_cast<uint2*>(q + at);
-      uint2* const phi = reinterpret_cast<uint2*>(q + a.d + at);
-      const uint2 was_lo = w.kept > 0 ? *plo : make_uint2(0u, 0u), was_hi = w.kept > 0 ? *phi : make_uint2(0u, 0u);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        lo[e] = down(mn[half][e], by);
-        hi[e] = -down(-mx[half][e], by);
-        if (w.kept > 0) {
-          lo[e] = min(lo[e], down((float)(int8_t)((e < 4 ? was_lo.x : was_lo.y) >> (8 * (e & 3))), ratio));
-          hi[e] = max(hi[e], -down(-(float)(int8_t)((e < 4 ? was_hi.x : was_hi.y) >> (8 * (e & 3))), ratio));
-        }
-      }
-      *plo = make_uint2(pack_s8(lo[0], lo[1], lo[2], lo[3]), pack_s8(lo[4], lo[5], lo[6], lo[7]));
-      *phi = make_uint2(pack_s8(hi[0], hi[1], hi[2], hi[3]), pack_s8(hi[4], hi[5], hi[6], hi[7]));
-    }
-    if (lt == 0) st.bound_scales[place] = unit;
-  }
-}
-
-// ---- many tokens: a block for each page and head -----------------------------------------------------
-
 // 16 values of a row as they lie in memory: pairs of 16-bit values, or fp32 where they are turned.
 template <typename T> struct Pair;
 template <> struct Pair<__nv_bfloat16> {
@@ -318,18 +139,19 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, 
   else return pack_e4m3(a * inv, b * inv, c * inv, d * inv);
 }
 
-// kThr threads hold kRows rows of 16 values each: 128 threads 64 tokens of d = 128, or 128 of d = 64.  Several
-// blocks share an SM, so one's barrier and writes hide behind the others' reads.  Pages of more tokens than the
-// block holds are read twice.  kTurn: key heads are turned (value heads take the path of 16-bit values).
-template <typename T, int kStore, bool kTurn, bool kBounds, int kThr, int kRows>
+// A page and head, by a team of kTeam threads (a warp, or the block), each of which holds kPageRows rows of 16 values:
+// a warp 16 tokens of d = 128, or 32 of d = 64, 128 threads four times as many.  Several blocks share an SM, so
+// one's barrier and writes hide behind the others' reads.  Pages of more tokens than the team holds are read
+// twice.  kTurn: key heads are turned (value heads take the path of 16-bit values).
+template <typename T, int kStore, bool kTurn, bool kBounds, int kTeam>
 __device__ __forceinline__ void write_page(const AppendArgs& a, const StoreArgs& st, int b, int p, int h, uint32_t* smem) {
   constexpr bool k8 = kStore != FA_PAGES_16BIT;
-  constexpr int kWarps = kThr / 32;
-  uint32_t* const amax_smem = smem;                        // [kWarps]
-  uint32_t* const bound_smem = smem + kWarps;              // [2][kWarps][d], or of pairs
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int units = a.d / kUnit, rows = kThr / units;
-  const int u = threadIdx.x % units, r = threadIdx.x / units;
+  constexpr int kWarps = kTeam / 32, kRows = kPageRows;
+  uint32_t* const bound_smem = smem;                       // [2][kWarps][d], or of pairs
+  uint32_t* const amax_smem = smem + (kBounds ? 2 * kWarps * (kTurn ? 128 : 64) : 0);   // [kWarps]
+  const int mine = threadIdx.x % kTeam, warp = mine / 32, lane = mine % 32;
+  const int units = a.d / kUnit, rows = kTeam / units;
+  const int u = mine % units, r = mine / units;
   const Unit t = kTurn ? unit_of(u, a.rot) : Unit{kUnit * u, kUnit * u + 8, false};
   const bool is_k = h < a.Hkv;
   const int g = is_k ? h : h - a.Hkv;
@@ -472,7 +294,8 @@ __device__ __forceinline__ void write_page(const AppendArgs& a, const StoreArgs&
       }
     }
   }
-  __syncthreads();
+  if constexpr (kTeam > 32) __syncthreads();
+  else __syncwarp();
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) amax = max(amax, amax_smem[i]);
   const bool finite = amax < 0x7f800000u;
@@ -546,44 +369,46 @@ __device__ __forceinline__ void write_page(const AppendArgs& a, const StoreArgs&
         *q = v;
       }
     }
-    if (threadIdx.x == 0) scales[place] = scale;
+    if (mine == 0) scales[place] = scale;
   }
   if constexpr (kBounds) {
-    if (bounds && threadIdx.x < a.d / 2) {                 // two of the d values to a thread
+    if (bounds) {
       const int words = kTurn ? a.d : a.d / 2;
-      float lo[2], hi[2];
-#pragma unroll 1
-      for (int i = 0; i < kWarps; ++i) {
-        const uint32_t* const q = bound_smem + i * words;
-        float2 l, m;
-        if constexpr (kTurn) {
-          l = reinterpret_cast<const float2*>(q)[threadIdx.x];
-          m = reinterpret_cast<const float2*>(q + kWarps * words)[threadIdx.x];
-        } else {
-          l = Pair<T>::values(q[threadIdx.x]);
-          m = Pair<T>::values(q[kWarps * words + threadIdx.x]);
-        }
-        lo[0] = i == 0 ? l.x : fminf(lo[0], l.x);
-        lo[1] = i == 0 ? l.y : fminf(lo[1], l.y);
-        hi[0] = i == 0 ? m.x : fmaxf(hi[0], m.x);
-        hi[1] = i == 0 ? m.y : fmaxf(hi[1], m.y);
-      }
       const float need = finite ? power_scale<true>(amax) : __uint_as_float(0x7fc00000u);
       const float unit = old_unit != old_unit || need != need ? __uint_as_float(0x7fc00000u) : fmaxf(old_unit, need);
       const float by = unit == unit ? 1.f / unit : 0.f, ratio = w.kept > 0 && unit == unit ? old_unit / unit : 0.f;
-      char2* const q = reinterpret_cast<char2*>(st.bounds + place * 2 * a.d) + threadIdx.x;
-      int c[4] = {down(lo[0], by), down(lo[1], by), -down(-hi[0], by), -down(-hi[1], by)};
-      if (w.kept > 0) {
-        const char2 was_lo = q[0], was_hi = q[a.d / 2];
-        c[0] = min(c[0], down((float)was_lo.x, ratio));
-        c[1] = min(c[1], down((float)was_lo.y, ratio));
-        c[2] = max(c[2], -down(-(float)was_hi.x, ratio));
-        c[3] = max(c[3], -down(-(float)was_hi.y, ratio));
+      for (int x = mine; x < a.d / 2; x += kTeam) {        // two of the d values at a time
+        float lo[2], hi[2];
+#pragma unroll 1
+        for (int i = 0; i < kWarps; ++i) {
+          const uint32_t* const q = bound_smem + i * words;
+          float2 l, m;
+          if constexpr (kTurn) {
+            l = reinterpret_cast<const float2*>(q)[x];
+            m = reinterpret_cast<const float2*>(q + kWarps * words)[x];
+          } else {
+            l = Pair<T>::values(q[x]);
+            m = Pair<T>::values(q[kWarps * words + x]);
+          }
+          lo[0] = i == 0 ? l.x : fminf(lo[0], l.x);
+          lo[1] = i == 0 ? l.y : fminf(lo[1], l.y);
+          hi[0] = i == 0 ? m.x : fmaxf(hi[0], m.x);
+          hi[1] = i == 0 ? m.y : fmaxf(hi[1], m.y);
+        }
+        char2* const q = reinterpret_cast<char2*>(st.bounds + place * 2 * a.d) + x;
+        int c[4] = {down(lo[0], by), down(lo[1], by), -down(-hi[0], by), -down(-hi[1], by)};
+        if (w.kept > 0) {
+          const char2 was_lo = q[0], was_hi = q[a.d / 2];
+          c[0] = min(c[0], down((float)was_lo.x, ratio));
+          c[1] = min(c[1], down((float)was_lo.y, ratio));
+          c[2] = max(c[2], -down(-(float)was_hi.x, ratio));
+          c[3] = max(c[3], -down(-(float)was_hi.y, ratio));
+        }
+        const uint32_t packed = pack_s8(c[0], c[1], c[2], c[3]);
+        q[0] = make_char2((signed char)packed, (signed char)(packed >> 8));
+        q[a.d / 2] = make_char2((signed char)(packed >> 16), (signed char)(packed >> 24));
       }
-      const uint32_t packed = pack_s8(c[0], c[1], c[2], c[3]);
-      q[0] = make_char2((signed char)packed, (signed char)(packed >> 8));
-      q[a.d / 2] = make_char2((signed char)(packed >> 16), (signed char)(packed >> 24));
-      if (threadIdx.x == 0) st.bound_scales[place] = unit;
+      if (mine == 0) st.bound_scales[place] = unit;
     }
   }
 }
@@ -631,59 +456,44 @@ __device__ __forceinline__ void turn_queries(const AppendArgs& a, const StoreArg
   }
 }
 
-template <typename T, int kStore>
-__global__ void __launch_bounds__(kThreads) append_rows_kernel(const AppendArgs a, const StoreArgs st) {
+// kThr threads a block, teams of kTeam.  Turned keys, and bounds, take registers: fewer blocks on an SM.
+template <typename T, int kStore, bool kTurn, bool kBounds, int kTeam, int kThr>
+__global__ void __launch_bounds__(kThr, (kTurn && kBounds ? 384 : kTurn ? 512 : kBounds ? 640 : 768) / kThr)
+    append_store_kernel(const AppendArgs a, const StoreArgs st) {
+  constexpr int kWarps = kTeam / 32, kTeams = kThr / kTeam;
+  constexpr int kWords = kWarps + (kBounds ? 2 * kWarps * (kTurn ? 128 : 64) : 0);
+  __shared__ __align__(16) uint32_t smem[kTeams][(kWords + 3) / 4 * 4];
   if ((int64_t)blockIdx.x >= st.page_blocks) {
-    turn_queries<T, kThreads>(a, st, (int64_t)blockIdx.x - st.page_blocks);
+    turn_queries<T, kThr>(a, st, (int64_t)blockIdx.x - st.page_blocks);
     return;
   }
-  const int64_t team = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  const int64_t team = (int64_t)blockIdx.x * kTeams + threadIdx.x / kTeam;
+  const int h = (int)(team % (2 * a.Hkv));
   const int64_t bp = team / (2 * a.Hkv);
-  const int b = (int)(bp / st.span), p = (int)(bp % st.span);
-  PageWork w;
-  if (b >= a.B || !page_work(a, b, p, &w) || !page_exists(a, w)) return;
-  write_rows<T, kStore>(a, st, w, b, (int)(team % (2 * a.Hkv)));
-}
-
-template <typename T, int kStore, bool kTurn, bool kBounds, int kThr>
-__global__ void __launch_bounds__(kThr, (kTurn ? 512 : kBounds ? 640 : 768) / kThr) append_page_kernel(const AppendArgs a, const StoreArgs st) {
-  constexpr int kWarps = kThr / 32;
-  __shared__ uint32_t smem[kWarps + (kBounds ? 2 * kWarps * (kTurn ? 128 : 64) : 0)];
-  if ((int64_t)blockIdx.x >= st.page_blocks) {
-    if constexpr (kTurn) turn_queries<T, kThr>(a, st, (int64_t)blockIdx.x - st.page_blocks);
-    else if (a.q != nullptr) turn_queries<T, kThr>(a, st, (int64_t)blockIdx.x - st.page_blocks);
-    return;
-  }
-  const int h = (int)(blockIdx.x % (2 * a.Hkv));
-  const int64_t bp = blockIdx.x / (2 * a.Hkv);
-  const int b = (int)(bp / st.span), p = (int)(bp % st.span);
+  const int64_t b = bp / st.span;
+  const int p = (int)(bp - b * st.span);
+  if (b >= a.B) return;                                    // (teams behind the last one: warps)
+  uint32_t* const words = smem[threadIdx.x / kTeam];
   if constexpr (kTurn) {
     if (h < a.Hkv) {
-      write_page<T, kStore, true, kBounds, kThr, kPageRows>(a, st, b, p, h, smem);
+      write_page<T, kStore, true, kBounds, kTeam>(a, st, (int)b, p, h, words);
       return;
     }
   }
-  write_page<T, kStore, false, kBounds, kThr, kPageRows>(a, st, b, p, h, smem);
+  write_page<T, kStore, false, kBounds, kTeam>(a, st, (int)b, p, h, words);
 }
 
 template <typename T, int kStore, bool kTurn, bool kBounds>
-void append_pages(const AppendArgs& a, const StoreArgs& st, unsigned grid, int threads, cudaStream_t s) {
-  if (threads == 128) append_page_kernel<T, kStore, kTurn, kBounds, 128><<<grid, 128, 0, s>>>(a, st);
-  else append_page_kernel<T, kStore, kTurn, kBounds, 512><<<grid, 512, 0, s>>>(a, st);
-}
-
-template <typename T, int kStore>
-cudaError_t append_store(const AppendArgs& a, StoreArgs st, cudaStream_t s) {
-  int sms = 0;
-  const cudaError_t e = sm_count(&sms);
-  if (e != cudaSuccess) return e;
+cudaError_t append_store(const AppendArgs& a, StoreArgs st, int sms, cudaStream_t s) {
+  constexpr int kLarge = kTurn ? 256 : 512;                // a team of more tokens than 128 threads hold
   const int units = a.d / kUnit;
   st.span = (a.T + a.cache.page_size - 2) / a.cache.page_size + 1;
   const int64_t heads = (int64_t)a.B * st.span * 2 * a.Hkv;       // of all pages
-  const bool warps = a.T <= kHold * 32 / units;                   // a warp holds the rows of any page
-  // 128 threads where they hold all of a page's rows
-  const int threads = warps ? kThreads : std::min(a.cache.page_size, a.T) <= 128 / units * kPageRows ? 128 : 512;
-  st.page_blocks = warps ? (heads + kThreads / 32 - 1) / (kThreads / 32) : heads;
+  // the smallest team that holds the new tokens of any page
+  const int most = std::min(a.cache.page_size, a.T);
+  const int team = most <= 32 / units * kPageRows ? 32 : most <= 128 / units * kPageRows ? 128 : kLarge;
+  const int threads = std::max(team, 128);
+  st.page_blocks = (heads + threads / team - 1) / (threads / team);
   int64_t q_blocks = 0;
   if (a.q != nullptr) {
     const int64_t tokens = ((int64_t)a.B * a.T + threads / units - 1) / (threads / units);
@@ -695,16 +505,22 @@ cudaError_t append_store(const AppendArgs& a, StoreArgs st, cudaStream_t s) {
   }
   if (st.page_blocks + q_blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const unsigned grid = (unsigned)(st.page_blocks + q_blocks);
-  if (warps) {
-    append_rows_kernel<T, kStore><<<grid, kThreads, 0, s>>>(a, st);
-  } else if (a.rot.rot > 0) {
-    if (st.bounds != nullptr) append_pages<T, kStore, true, true>(a, st, grid, threads, s);
-    else if constexpr (kStore != FA_PAGES_16BIT) append_pages<T, kStore, true, false>(a, st, grid, threads, s);
-  } else {
-    if (st.bounds != nullptr) append_pages<T, kStore, false, true>(a, st, grid, threads, s);
-    else if constexpr (kStore != FA_PAGES_16BIT) append_pages<T, kStore, false, false>(a, st, grid, threads, s);
-  }
+  if (team == 32) append_store_kernel<T, kStore, kTurn, kBounds, 32, 128><<<grid, 128, 0, s>>>(a, st);
+  else if (team == 128) append_store_kernel<T, kStore, kTurn, kBounds, 128, 128><<<grid, 128, 0, s>>>(a, st);
+  else append_store_kernel<T, kStore, kTurn, kBounds, kLarge, kLarge><<<grid, kLarge, 0, s>>>(a, st);
   return cudaGetLastError();
+}
+
+template <typename T, int kStore>
+cudaError_t append_store(const AppendArgs& a, const StoreArgs& st, cudaStream_t s) {
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  if (st.bounds != nullptr)
+    return a.rot.rot > 0 ? append_store<T, kStore, true, true>(a, st, sms, s) : append_store<T, kStore, false, true>(a, st, sms, s);
+  if constexpr (kStore != FA_PAGES_16BIT)
+    return a.rot.rot > 0 ? append_store<T, kStore, true, false>(a, st, sms, s) : append_store<T, kStore, false, false>(a, st, sms, s);
+  return cudaErrorInvalidValue;                            // 16-bit pages without bounds: launch_append
 }
 
 template <typename T>
