@@ -16,7 +16,8 @@
 // have: by the bits from the top nearly all would meet in the few bins of their exponents.
 // Where there are fewer of them than SMs, and many pages, a kernel of its own scores the pages on all SMs first.
 // (A cluster of 4 or 8 blocks for each instead, scores in the first one's shared memory: 32 and 36 us for two
-// sequences of 8192 pages and 8 key heads, in two kernels 23; clusters of 8 do not all find their SMs at once.)
+// sequences of 8192 pages and 8 key heads, in two kernels 23; clusters of 8 do not all find their SMs at once.
+// The choice launched as a dependent of the scores: 28.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -412,17 +413,19 @@ cudaError_t launch_any(const SelectArgs& a, cudaStream_t s) {
   const int grid = (slots * slices + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
   score_kernel<D, F16><<<grid, kScoreThreads, 0, s>>>(a, slots);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_one<64, false, 1024, true>(a, s);              // (the queries' type and size do not matter)
+  // (the queries' type and size do not matter)
+  return a.cache.max_pages <= 2048 ? launch_one<64, false, 256, true>(a, s) : launch_one<64, false, 1024, true>(a, s);
 }
 
 }  // namespace
 
-// Whether the pages are scored by a kernel of its own: slices that leave SMs idle, each with more pages than a
-// block scores while another launch begins.
+// Whether the pages are scored by a kernel of its own: where slices are not many times the SMs, each with more pages
+// than a block scores while another launch begins (32 sequences of 1024 pages and 8 key heads: 36 us in one
+// kernel, 31 in two; 64 of up to 128 pages: 10 and 12).
 bool select_scores_first(int B, int Hkv, int max_pages, int picks) {
   int sms = 0;
   if (sm_count(&sms) != cudaSuccess || sms <= 0) sms = 152;        // GB300's when no device can be asked
-  return max_pages > picks && max_pages > 512 && (int64_t)B * Hkv < sms;
+  return max_pages > picks && max_pages > 512 && (int64_t)B * Hkv <= 4 * (int64_t)sms;
 }
 
 cudaError_t launch_select(const SelectArgs& a, fa_dtype dt, cudaStream_t s) {

@@ -82,7 +82,7 @@ def select(c=None, s=None, q=P, pages=P, B=2, H=4, Hkv=2, T=1, d=64, n=4, first=
 def test_select_checks():
     assert fa.select_pages_workspace_size(2, 2, 1000, 10) == 16128         # 16000 bytes, in steps of 256
     assert fa.select_pages_workspace_size(2, 2, 512, 10) == 0              # few pages,
-    assert fa.select_pages_workspace_size(200, 2, 1000, 10) == 0           # many sequences,
+    assert fa.select_pages_workspace_size(400, 2, 1000, 10) == 0           # many sequences,
     assert fa.select_pages_workspace_size(2, 2, 1000, 1000) == 0           # no choice
     assert fa.select_pages_workspace_size(0, 2, 1000, 10) == 0
     wide = cache(max_pages=1000, table_stride=1000, k_cache=None, v_cache=None)
