@@ -804,8 +804,10 @@ def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     B, Hkv, T, d = shape
     pages, store = _store(k_cache, k_scales, v_scales, k_bounds, bound_scales, dtype, dev, Hkv, d)
     cache = _cache(k_cache, v_cache, block_table, kv_lens, B, Hkv, d, pages)
-    if store is not None and store[0] and abs(store[1] - store[2]) < 4 * cache[5] * Hkv:
-        raise ValueError("k_scales and v_scales overlap")
+    if store is not None and store[0]:
+        size = 4 * cache[5] * Hkv
+        if abs(store[1] - store[2]) < size or (store[4] and min(abs(store[1] - store[4]), abs(store[2] - store[4])) < size):
+            raise ValueError("the scales overlap")
     rot = _rotated(inv_freq)
     if q_lens is not None:
         _int32("q_lens", q_lens, (B,))

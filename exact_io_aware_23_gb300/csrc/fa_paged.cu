@@ -27,9 +27,9 @@ bool paged_shares(int B, int Hkv, int rows, int capacity, int ctas) {
 }
 
 // Whether the units of all segments can be counted in 31 bits.
-bool paged_counts(int B, int Hkv, int rows, int capacity) {
+bool paged_counts(int B, int Hkv, int rows, int capacity, bool bits8) {
   const int64_t segments = (int64_t)B * Hkv * ((rows + kRows - 1) / kRows);
-  return segments <= 0x7fffffff / ((int64_t)capacity / 16 + 1 + kSegment);
+  return segments <= 0x7fffffff / ((int64_t)capacity / 16 + 1 + (bits8 ? kFlipSegment : kSegment));
 }
 
 // The workspace: arrivals [2 * ctas], then two parts of 16 rows a CTA, their statistics and outputs.

@@ -174,7 +174,7 @@ constexpr int kMaxPageSize = 4096;
 int paged_ctas();
 unsigned long long paged_call_number();
 bool paged_shares(int B, int Hkv, int rows, int capacity, int ctas);
-bool paged_counts(int B, int Hkv, int rows, int capacity);
+bool paged_counts(int B, int Hkv, int rows, int capacity, bool bits8);
 struct PagedWorkspace {
   size_t ml, o, total;       // byte offsets; arrivals at 0
 };

@@ -177,6 +177,8 @@ fa_status fa_append_paged_store(const fa_paged_cache* cache, const fa_page_store
   if (st != FA_OK) return st;
   // the pages are written, and so are their scales
   if (value_bytes(store) == 1 && store->k_scales == store->v_scales) return FA_ERR_INVALID_ARG;
+  if (value_bytes(store) == 1 && bounds && (store->bound_scales == store->k_scales || store->bound_scales == store->v_scales))
+    return FA_ERR_INVALID_ARG;
   if (cache->k_cache == cache->v_cache || !apart(cache->n_pages, cache->page_stride, Hkv, cache->head_stride,
                                                  cache->page_size, cache->token_stride, d))
     return FA_ERR_INVALID_ARG;
@@ -260,7 +262,7 @@ fa_status fa_forward_paged_store(const void* q, const fa_paged_cache* cache, con
   a.q_lens = q_lens;
   a.scale = scale;
   a.score = mods;
-  if (!fa::paged_counts(B, Hkv, H / Hkv * T, span)) return FA_ERR_UNSUPPORTED;
+  if (!fa::paged_counts(B, Hkv, H / Hkv * T, span, value_bytes(store) == 1)) return FA_ERR_UNSUPPORTED;
   if (store != nullptr) {
     a.store = store->format;
     a.k_scales = store->k_scales;

@@ -642,7 +642,8 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
   };
   // Who else has tiles of the segment, worked out while its first ones are on their way.
   auto note_parted = [&](int k) {
-    if (!kShared || threadIdx.x != 0 || (seg.tile == 0 && last_tile(s0, seg.tiles) == seg.tiles)) return;
+    const int last = last_tile(s0, seg.tiles);
+    if (!kShared || threadIdx.x != 0 || last <= seg.tile || (seg.tile == 0 && last == seg.tiles)) return;
     const Shares share(units, n_ctas);
     const int ca = share.owner(s0 + C::kSegment), cb = share.owner(s0 + C::kSegment + seg.tiles - 1);
     const int row0 = seg.block * kRows;
@@ -854,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
       if constexpr (C::k8) {
         const float c = a.score.cap_log2 == 0.f ? c_log2 : 1.f;
 #pragma unroll
-        for (int e = 0; e < kScores; ++e) s[e] *= meta[key_of(e) / 16].x * (unit_q[row_of(e)] * c);
+        for (int e = 0; e < kScores; ++e) s[e] *= meta[key_of(e) / 16].x * c * unit_q[row_of(e)];
       }
       if (a.score.cap_log2 == 0.f) {
         if constexpr (!C::k8) {
@@ -1124,6 +1125,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
   }
   cp_wait<0>();
   if constexpr (kShared && C::kDefer) {
+    __syncthreads();                                    // (a CTA may have had units, but no tile)
     const int mine = *flag;
     __syncthreads();                                    // the word is written again
     if (mine != 0) finish(mine);

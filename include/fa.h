@@ -512,7 +512,7 @@ fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, 
  * of its page and head NaN, and the bounds' scale with it, until a write begins the page anew; the
  * codes written there are 0.
  * Several sequences must not write to one page.  Other arguments as in fa_append_paged; FA_ERR_INVALID_ARG
- * also for k_scales == v_scales.
+ * also where two of the scales are in one place.
  */
 fa_status fa_append_paged_store(const fa_paged_cache* cache, const fa_page_store* store,
                                 const void* k, const int64_t k_strides[3], const void* v,

@@ -35,6 +35,7 @@ def test_append_checks():
     for kw, status in BAD_STORES + BAD_BOUNDS:
         assert append(s=store(**kw)) == status, kw
     assert append(s=store(v_scales=P)) == INVALID                          # one place for both scales
+    assert append(s=store(k_bounds=P, bound_scales=P)) == INVALID
     assert append(cache(v_cache=P + 4096, token_stride=72)) == INVALID     # rows of 8-bit values off the 16-byte grid
     assert append(cache(v_cache=P + 4096, head_stride=8)) == INVALID
     assert append(cache()) == INVALID                                      # keys and values in one place
@@ -66,6 +67,8 @@ def test_forward_checks():
     assert forward(pages=P + 2, n=4, w=None) == INVALID
     assert forward(pages=P, n=99, w=None) == INVALID                       # 1584 keys: a workspace is needed
     assert forward(pages=P, n=99, wsb=256) == INVALID
+    many = cache(max_pages=1 << 20, table_stride=1 << 20, page_size=4096)
+    assert forward(many, B=60000, H=4, Hkv=4) == UNSUPPORTED               # more tiles than 31 bits count
     long = cache(max_pages=1 << 19, table_stride=1 << 19, page_size=4096)
     assert forward(long, pages=P, n=4) == UNSUPPORTED                      # places that mark keys which do not exist
     assert forward(q=None) == INVALID

@@ -242,6 +242,51 @@ def test_same_bits_layouts_graphs_streams_and_workspaces():
         assert all(torch.equal(x[0], want[0]) for x in got)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("store", ["int8", "e4m3"])
+def test_short_sequences_in_wide_tables(store, d):
+    """Few tiles, shared by all blocks of a call that is sized for many: blocks whose share holds no tile, or one."""
+    for n in (1, 16, 33, 64, 65, 150, 160, 200, 330, 500):
+        for T, lens in ((1, [n]), (2, [n, 0, 1, n])):
+            kc, vc, ks, vs, table, g = _cache8(lens, 2, 16, d, "bf16", store, n)
+            wide = torch.full((len(lens), 70), -1, dtype=torch.int32, device="cuda")
+            wide[:, : table.shape[1]] = table
+            q = torch.randn((len(lens), 4, T, d), generator=g, device="cuda").to(torch.bfloat16)
+            ws = torch.randint(0, 256, (fa.forward_paged_workspace_size(len(lens), 4, 2, T, d, 70 * 16),), generator=g, device="cuda", dtype=torch.uint8)
+            for _ in range(2):                           # and with what the call left
+                o, lse = fa.forward_paged(q, kc, vc, wide, _i32(lens), k_scales=ks, v_scales=vs, workspace=ws)
+                _check(q, kc, vc, ks, vs, table, lens, o, lse)
+    assert fa.check_device_status() == 0
+
+
+def test_one_workspace_for_calls_of_different_kinds():
+    """16-bit, 8-bit and chosen pages in turn, captured and replayed in another order."""
+    lens = [3000, 700]
+    kc, vc, ks, vs, table, g = _cache8(lens, 2, 16, 128, "bf16", "int8", 12)
+    k16, v16 = ((c.float() * s.nan_to_num()[..., None, None]).to(torch.bfloat16) for c, s in ((kc, ks), (vc, vs)))
+    q = torch.randn((2, 8, 1, 128), generator=g, device="cuda").to(torch.bfloat16)
+    n = _i32(lens)
+    pages = torch.arange(40, dtype=torch.int32, device="cuda").expand(2, 2, 40).contiguous()
+    ws = torch.randint(0, 256, (fa.forward_paged_workspace_size(2, 8, 2, 1, 128, table.shape[1] * 16),), generator=g, device="cuda", dtype=torch.uint8)
+    calls = [lambda w: fa.forward_paged(q, k16, v16, table, n, workspace=w),
+             lambda w: fa.forward_paged(q, kc, vc, table, n, k_scales=ks, v_scales=vs, workspace=w),
+             lambda w: fa.forward_paged(q, kc, vc, table, n, k_scales=ks, v_scales=vs, pages=pages, workspace=w),
+             lambda w: fa.forward_paged(q, k16, v16, table, n, pages=pages, workspace=w)]
+    want = [c(None) for c in calls]
+    graphs = []
+    for c in calls:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = c(ws)
+        graphs.append((gr, out))
+    for order in ((0, 1, 2, 3), (3, 1, 0, 2), (1, 1, 3, 3), (2, 0, 2, 1)):
+        for i in order:
+            graphs[i][0].replay()
+            assert torch.equal(graphs[i][1][0], want[i][0]) and torch.equal(graphs[i][1][1], want[i][1])
+            got = calls[(i + 1) % 4](ws)
+            assert torch.equal(got[0], want[(i + 1) % 4][0])
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 2^32 bytes."""
     pages = (1 << 32) // (8 * 64 * 128) + 40
@@ -536,5 +581,7 @@ def test_refusals():
         fa.append_paged(q[:, :2], q[:, 2:], kc, vc, table, n, bound_scales=ks, **kw)
     with pytest.raises(ValueError, match="overlap"):
         fa.append_paged(q[:, :2], q[:, 2:], kc, vc, table, n, k_scales=ks, v_scales=ks)
+    with pytest.raises(ValueError, match="overlap"):
+        fa.append_paged(q[:, :2], q[:, 2:], kc, vc, table, n, k_bounds=kb, bound_scales=vs, **kw)
     with pytest.raises(fa.FaError, match="INVALID_ARG"):
         fa.append_paged(q[:, :2], q[:, 2:], kc, kc, table, n, **kw)
