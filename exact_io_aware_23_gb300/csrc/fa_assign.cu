@@ -11,10 +11,11 @@
 // alone, whether the table has it already or not.
 //
 // What bounds it: the latency of a launch and of three reads one after another (lengths, state, ring), then the
-// bytes of the slots.  Few tokens: one block does it all.  Many: their places come first, from a kernel with a
-// block for every 1024 tokens of a sequence, each of which sums up the lengths for itself; it writes nothing that
-// may be the caller's own input.  (40 sequences of up to 4096 tokens, in one kernel, a cluster of 8 blocks with a
-// barrier before the lengths are written: 27 us; in two: 12.)
+// bytes of the slots.  Few tokens: one block does it all.  Many: blocks of their own place 2048 tokens each, after
+// summing up the lengths for themselves, while the first one sees to the tables: nothing that it writes is
+// read by them, unless the caller has the lengths or the state written over its inputs, and then it runs
+// behind them as a second launch.  (40 sequences of up to 4096 tokens: 27 us by a cluster of 8 blocks with a
+// barrier before the lengths are written, 12 in two launches, 9 in one.)
 #include <cuda_runtime.h>
 
 #include "fa_paged.cuh"
@@ -24,8 +25,7 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kPlaceThreads = 256;         // of a block for tokens' places, each of
-constexpr int kPlaceTokens = 1024;         // so many tokens
+constexpr int kPlaceTokens = 2048;         // a block's that places tokens of a sequence
 
 // The pages of n tokens, by multiplication with the page size's rounded-up reciprocal: exact for n below 2^31 and
 // pages of up to 4096 tokens (2^43 / page, the error below n / 2^43 of a page).
@@ -103,26 +103,31 @@ __device__ __forceinline__ void place(const AssignArgs& a, const Change& c, int 
   a.positions[at] = pos;
 }
 
-// Block x: tokens from x % chunks * kPlaceTokens on of `per` sequences (one, unless there are thousands).
-__global__ void __launch_bounds__(kPlaceThreads) place_kernel(const AssignArgs a, const int chunks, const int per) {
-  __shared__ int64_t words[3][kPlaceThreads / 32];
-  const int b0 = blockIdx.x / chunks * per, t0 = blockIdx.x % chunks * kPlaceTokens;
+// Block x places the tokens from x % chunks * kPlaceTokens on of `per` sequences (one, unless there are thousands).
+__device__ __forceinline__ void place_tokens(const AssignArgs& a, int x, int chunks, int per, int64_t (*words)[kThreads / 32]) {
+  const int b0 = x / chunks * per, t0 = x % chunks * kPlaceTokens;
   const int first = a.state[0], count = a.state[1];
-  const Totals all = totals_of<kPlaceThreads>(a, first, count, b0, words);
+  const Totals all = totals_of<kThreads>(a, first, count, b0, words);
   const int end = min(a.T, t0 + kPlaceTokens);
   int64_t from = (int64_t)first + all.grow_before;
   for (int b = b0; b < min(a.B, b0 + per); ++b) {
     const Change c = change_of(a, b);
 #pragma unroll 4
-    for (int t = t0 + threadIdx.x; t < end; t += kPlaceThreads) place(a, c, b, t, from, all.ok);
+    for (int t = t0 + threadIdx.x; t < end; t += kThreads) place(a, c, b, t, from, all.ok);
     from += max(c.want - c.held, 0);
   }
 }
 
-// Tables, ring, lengths and state; places too where `places`.
-__global__ void __launch_bounds__(kThreads) assign_kernel(const AssignArgs a, const int places) {
+// Block 0 (of all launches' blocks, from `begin` on): tables, ring, lengths and state, and where `places` the tokens too.
+// The others place tokens.
+__global__ void __launch_bounds__(kThreads) assign_kernel(const AssignArgs a, const int begin, const bool places, const int chunks,
+                                                          const int per) {
   constexpr int kWarps = kThreads / 32;
   __shared__ int64_t words[3][kWarps];
+  if (begin + (int)blockIdx.x > 0) {
+    place_tokens(a, begin + (int)blockIdx.x - 1, chunks, per, words);
+    return;
+  }
   __shared__ int scan[2][kWarps];
   __shared__ Change changes[kThreads];
   __shared__ int grown[kThreads], given[kThreads];
@@ -208,16 +213,22 @@ __global__ void __launch_bounds__(kThreads) assign_kernel(const AssignArgs a, co
 cudaError_t launch_assign(const AssignArgs& args, cudaStream_t s) {
   AssignArgs a = args;
   a.page_magic = ((uint64_t(1) << 43) + a.page_size - 1) / a.page_size;
-  // the tokens that one block places in the time of another launch
-  const bool places = (int64_t)a.B * a.T <= 4 * kThreads;
-  if (!places) {
-    const int chunks = (a.T + kPlaceTokens - 1) / kPlaceTokens;
-    const int per = (a.B + 4095) / 4096, groups = (a.B + per - 1) / per;       // (each block reads all lengths)
-    place_kernel<<<(unsigned)((int64_t)groups * chunks), kPlaceThreads, 0, s>>>(a, chunks, per);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+  if ((int64_t)a.B * a.T <= 4 * kThreads) {                // one block places them too
+    assign_kernel<<<1, kThreads, 0, s>>>(a, 0, true, 1, 1);
+    return cudaGetLastError();
   }
-  assign_kernel<<<1, kThreads, 0, s>>>(a, places);
+  const int chunks = (a.T + kPlaceTokens - 1) / kPlaceTokens;
+  const int per = (a.B + 4095) / 4096, groups = (a.B + per - 1) / per;     // (each block reads all lengths)
+  const int64_t blocks = (int64_t)groups * chunks;
+  if (blocks >= 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if (a.lens != a.old_lens && a.lens != a.new_lens && a.state_out != a.state) {
+    assign_kernel<<<(unsigned)blocks + 1, kThreads, 0, s>>>(a, 0, false, chunks, per);
+    return cudaGetLastError();
+  }
+  assign_kernel<<<(unsigned)blocks, kThreads, 0, s>>>(a, 1, false, chunks, per);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  assign_kernel<<<1, kThreads, 0, s>>>(a, 0, false, chunks, per);
   return cudaGetLastError();
 }
 

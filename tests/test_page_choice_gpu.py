@@ -187,13 +187,14 @@ def test_pages_are_assigned(old, new, page, T):
     g = torch.Generator(device="cuda").manual_seed(sum(new) + T)
     width = max(-(-n // page) for n in old + new) + 2
     grow = sum(max(0, -(-y // page) + -x // page) for x, y in zip(old, new))
-    for extra in (0, 9):
+    for extra, over in ((0, False), (9, False), (9, True)):
         table, ring, state = _state(old, page, width, grow + extra, g)
-        t, r, s = _i32(table), _i32(ring), _i32(state)
-        lens, q_lens, slots, positions, state2 = fa.assign_pages(t, _i32(old), _i32(new), r, s, page, T)
+        t, r, s, n = _i32(table), _i32(ring), _i32(state), _i32(old)
+        outs = dict(lens=n, state=s) if over else {}       # written over the inputs
+        lens, q_lens, slots, positions, state2 = fa.assign_pages(t, n, _i32(new), r, s, page, T, **outs)
         assert fa.check_device_status() == 0
         want_slots, want_pos, want_state = assign(table, old, new, ring, state, page, T)
-        assert t.tolist() == table and r.tolist() == ring and state2.tolist() == want_state and s.tolist() == state
+        assert t.tolist() == table and r.tolist() == ring and state2.tolist() == want_state and (over or s.tolist() == state)
         assert lens.tolist() == new and q_lens.tolist() == [max(0, y - x) for x, y in zip(old, new)]
         assert slots.dtype == torch.int64 and slots.tolist() == want_slots and positions.tolist() == want_pos
 
