@@ -1095,8 +1095,6 @@ def select_pages(q: torch.Tensor, k_bounds: torch.Tensor, bound_scales: torch.Te
     pages_new = ws_new = None
     if pages is None:
         pages = pages_new = torch.empty((B, Hkv, n_select), dtype=torch.int32, device=q.device)
-        if H == 0 or T == 0:
-            pages.fill_(-1)                               # no new tokens: nothing is launched
     else:
         _given("pages", pages, (B, Hkv, n_select), torch.int32)
     if workspace is None:

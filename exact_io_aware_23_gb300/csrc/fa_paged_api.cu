@@ -293,13 +293,17 @@ fa_status fa_select_pages(const void* q, const fa_paged_cache* cache, const fa_p
   if (st != FA_OK) return st;
   if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
   if (n_select < 0 || first < 0 || last < 0) return FA_ERR_INVALID_ARG;
-  if (B == 0 || H == 0 || T == 0 || n_select == 0) return FA_OK;
+  if (B == 0 || Hkv == 0 || n_select == 0) return FA_OK;
+  if (!pages || !aligned(pages, 4)) return FA_ERR_INVALID_ARG;
+  if (H == 0 || T == 0)                                     // no new tokens: -1 everywhere
+    return cudaMemsetAsync(pages, 0xff, (size_t)B * Hkv * n_select * sizeof(int32_t), static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? FA_OK : FA_ERR_CUDA;
   if (store == nullptr) return FA_ERR_INVALID_ARG;
   st = check_table(cache);
   if (st != FA_OK) return st;
   if (cache->max_pages > fa::kMaxChoice) return FA_ERR_UNSUPPORTED;
   if (!store->k_bounds || !store->bound_scales || !aligned(store->k_bounds, 16) || !aligned(store->bound_scales, 4) || !q ||
-      !pages || !aligned(q, 16) || !aligned(pages, 4) || !aligned(q_lens, 4))
+      !aligned(q, 16) || !aligned(q_lens, 4))
     return FA_ERR_INVALID_ARG;
   const size_t need = fa_select_pages_workspace_size(B, Hkv, cache->max_pages, n_select);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return FA_ERR_INVALID_ARG;

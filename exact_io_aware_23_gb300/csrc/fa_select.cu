@@ -78,7 +78,7 @@ __device__ __forceinline__ int pages_of(const SelectArgs& a, int b) {
 template <int D, bool F16>
 struct Queries {
   uint32_t q[D / 16][4];
-  float unit[2];                           // -1: no such row
+  float unit[2];                           // -1: no such row, or one that holds something not finite
   __device__ __forceinline__ void read(const SelectArgs& a, int b, int hk, int row0, int count) {
     const int lane = threadIdx.x % 32, G = a.H / a.Hkv, rows = G * a.T;
 #pragma unroll
@@ -105,7 +105,7 @@ struct Queries {
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       const float u = power_scale<true>(amax), inv = 1.f / u;
-      unit[e] = !there ? -1.f : amax < 0x7f800000u ? u : __uint_as_float(0x7fc00000u);
+      unit[e] = there && amax < 0x7f800000u ? u : -1.f;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
 #pragma unroll
@@ -173,7 +173,7 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, const Queries<D
         }
       }
       // the lane's columns are pages 2 (lane % 4) and the next.  The scale is positive, so it may wait until
-      // the largest is known; one that is NaN makes the score NaN, a row that is NaN has no say.
+      // the largest is known; one that is NaN makes the score NaN.
       float best[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {

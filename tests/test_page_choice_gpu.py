@@ -97,6 +97,33 @@ def test_nan_bounds_come_first_and_nan_queries_have_no_say():
     assert 57 in got and 0 in got and 99 in got and len(set(got) - set(want[0, 0].tolist())) <= 1
 
 
+def test_nan_queries_have_no_say_next_to_other_blocks_of_rows():
+    """24 rows of a key head are scored 16 and 8 at a time: all of the first, or of the second ones, are NaN."""
+    g = torch.Generator(device="cuda").manual_seed(16)
+    for length in (1600, 12000):                          # scored by the block that chooses, and before it
+        table, n = _table([length], 16, g)
+        bounds, unit = _bounds(n, 1, 64, g)
+        q = torch.randn((1, 24, 1, 64), generator=g, device="cuda").to(torch.bfloat16)
+        for nan, rest in ((slice(0, 16), slice(16, 24)), (slice(16, 24), slice(0, 16))):
+            x = q.clone()
+            x[0, nan, 0, 5] = float("nan")
+            want = fa.select_pages(q[:, rest].contiguous(), bounds, unit, table, _i32([length]), 9, 16)
+            assert torch.equal(fa.select_pages(x, bounds, unit, table, _i32([length]), 9, 16), want)
+        q[..., 7] = float("inf")                          # none has a say: the lower numbers
+        got = fa.select_pages(q, bounds, unit, table, _i32([length]), 9, 16)[0, 0].tolist()
+        assert got == [*range(8), -(-length // 16) - 1]
+
+
+def test_given_lists_without_new_tokens_are_emptied():
+    g = torch.Generator(device="cuda").manual_seed(17)
+    table, n = _table([1600, 20], 16, g)
+    bounds, unit = _bounds(n, 2, 64, g)
+    pages = torch.full((2, 2, 5), 7, dtype=torch.int32, device="cuda")
+    q = torch.zeros((2, 4, 0, 64), dtype=torch.float16, device="cuda")
+    assert fa.select_pages(q, bounds, unit, table, _i32([1600, 20]), 5, 16, pages=pages) is pages
+    assert bool((pages == -1).all())
+
+
 def test_bounds_hold_for_every_key():
     """A page's score is no less than the product of the rounded query with any of its keys, so the page of the
     highest product of one query is always chosen when its score is alone above the others'."""
