@@ -109,7 +109,10 @@ struct SelectArgs {
   const int32_t* q_lens;
   int picks, first, last;
   int32_t* pages;            // [B, Hkv, picks]
-  float* scores;             // workspace [B, Hkv, max_pages], where select_scores_first
+  // workspace, where select_scores_first: scores [B, Hkv, max_pages] (rows of whole 16 bytes), and counts [B, Hkv]
+  float* scores;
+  unsigned long long* arrivals;
+  unsigned long long call;   // the number that the counts go with
   int* err;
 };
 
@@ -164,6 +167,7 @@ cudaError_t launch_append_store(const AppendArgs& a, const StoreArgs& st, fa_dty
 // Tables of at most this many pages are chosen from: their scores lie in a block's shared memory.
 constexpr int kMaxChoice = 49152;
 bool select_scores_first(int B, int Hkv, int max_pages, int picks);
+size_t select_workspace(int B, int Hkv, int max_pages, size_t* arrivals);    // bytes; the counts' place
 cudaError_t launch_select(const SelectArgs& a, fa_dtype dt, cudaStream_t s);
 cudaError_t launch_assign(const AssignArgs& a, cudaStream_t s);
 

@@ -283,7 +283,8 @@ fa_status fa_forward_paged_store(const void* q, const fa_paged_cache* cache, con
 
 size_t fa_select_pages_workspace_size(int B, int Hkv, int max_pages, int n_select) {
   if (B <= 0 || Hkv <= 0 || max_pages <= 0 || n_select <= 0 || !fa::select_scores_first(B, Hkv, max_pages, n_select)) return 0;
-  return ((size_t)B * Hkv * max_pages * sizeof(float) + 255) / 256 * 256;
+  size_t arrivals;
+  return fa::select_workspace(B, Hkv, max_pages, &arrivals);
 }
 
 fa_status fa_select_pages(const void* q, const fa_paged_cache* cache, const fa_page_store* store, int32_t* pages, int B,
@@ -318,7 +319,13 @@ fa_status fa_select_pages(const void* q, const fa_paged_cache* cache, const fa_p
   a.first = first;
   a.last = last;
   a.pages = pages;
-  a.scores = static_cast<float*>(workspace);
+  if (need > 0) {
+    size_t arrivals;
+    fa::select_workspace(B, Hkv, cache->max_pages, &arrivals);
+    a.scores = static_cast<float*>(workspace);
+    a.arrivals = reinterpret_cast<unsigned long long*>(static_cast<char*>(workspace) + arrivals);
+    a.call = fa::paged_call_number();
+  }
   if (fa::device_error_word(&a.err) != FA_OK) return FA_ERR_CUDA;
   return fa::launch_select(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

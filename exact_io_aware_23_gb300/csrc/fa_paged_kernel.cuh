@@ -46,6 +46,7 @@
 
 #include <type_traits>
 
+#include "fa_arrivals.cuh"
 #include "fa_paged.cuh"
 #include "fa_score.cuh"
 #include "fa_sm103.cuh"
@@ -358,18 +359,8 @@ __device__ __forceinline__ bool all_arrived(unsigned long long* words, int part0
   return there;
 }
 
-// The same for 8-bit pages, whose CTAs announce their parts at the end alone: a word for each segment counts them,
-// {the call's number, the count}.  Each CTA sees to the number before its first tile is there (by one
-// compare-and-swap from whatever the word holds, unless another CTA was first), so that the end takes one
-// fence and one addition, and the one that brings the count to all parts joins them and clears the word.
-__device__ __forceinline__ void open_count(unsigned long long* word, unsigned long long call) {
-  unsigned long long w;
-  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(w) : "l"(word) : "memory");
-  if ((w ^ (call << 16)) >> 16 != 0) atomicCAS(word, w, call << 16);
-}
-__device__ __forceinline__ bool count_part(unsigned long long* word, int parts) {
-  return (int)(atomicAdd(word, 1ull) & 0xffffu) == parts - 1;
-}
+// 8-bit pages, whose CTAs announce their parts at the end alone, count them instead, in the word of the
+// segment's first part (fa_arrivals.cuh).
 
 // kShared: CTAs share all segments' units.  Otherwise a CTA has one segment to itself (few short
 // ones: nothing to join, nothing to reckon).

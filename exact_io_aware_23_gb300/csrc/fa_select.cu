@@ -11,10 +11,14 @@
 // Scores.  A warp takes 32 pages at a time, eight to a product, their bounds the right operand of mma.sync as
 // they lie in memory, 16 rows' q the left one.  What bounds it: bytes, 2 d + 4 a page, for few pages the chain
 // of reads: lengths, table entry, bounds.
-// Choice.  A block has a (sequence, key head): it keeps the scores in shared memory and narrows down the range
+// Choice.  A block has a (sequence, key head), a slice: it keeps the scores in shared memory and narrows down the range
 // of the K-th largest one's bits, 1024 bins at a time.  The bins are laid over the range that the scores
-// have: by the bits from the top nearly all would meet in the few bins of their exponents.
+// have: by the bits from the top nearly all would meet in the few bins of their exponents.  What costs there
+// is not the bytes but instructions that come from cold caches: loops that are not unrolled, and queries converted once for
+// a block, took 64 sequences of up to 128 pages from 10.2 us to 8.6.
 // Where there are fewer of them than SMs, and many pages, a kernel of its own scores the pages on all SMs first.
+// Few slices: the block that comes last of those that score a slice chooses, in the same launch (two sequences of 8192 pages
+// and 8 key heads: 23.0 us in two launches, 22.5 in one; more slices would leave some SMs without a block).
 // (A cluster of 4 or 8 blocks for each instead, scores in the first one's shared memory: 32 and 36 us for two
 // sequences of 8192 pages and 8 key heads, in two kernels 23; clusters of 8 do not all find their SMs at once.
 // The choice launched as a dependent of the scores: 28.)
@@ -25,6 +29,7 @@
 
 #include <algorithm>
 
+#include "fa_arrivals.cuh"
 #include "fa_paged.cuh"
 #include "fa_sm103.cuh"
 #include "fa_store.cuh"
@@ -38,6 +43,7 @@ constexpr int kGroup = 8;                  // pages of a warp's product
 constexpr int kBins = 1024;
 constexpr int kScoreThreads = 128;         // of a block that only scores
 constexpr int kScoreCtas = 3;              // and such blocks on an SM
+constexpr int kJointThreads = 384;         // of a block that scores a share of the pages, one on an SM
 
 // c (16 x 8, fp32) += a (16 x 16) b (16 x 8)
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -68,17 +74,71 @@ __device__ __forceinline__ float2 halves(uint32_t x) {
   else return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
 }
 
+// A slice's scores in the workspace
+__host__ __device__ inline int64_t score_stride(int max_pages) { return ((int64_t)max_pages + 3) / 4 * 4; }
+
 __device__ __forceinline__ int pages_of(const SelectArgs& a, int b) {
   if (new_tokens(a.q_lens, b, a.T) == 0) return 0;
   return (paged_len(a.cache, b, nullptr) + a.cache.page_size - 1) / a.cache.page_size;
 }
 
-// 16 rows of queries as left operands: product 4 i + w takes the values [64 i + 16 (lane % 4) + 4 w, + 4) of a lane
+// 16 rows of queries in whole numbers, fp16, converted once for a block, a row to a warp, by little code: a kernel this
+// short runs from cold instruction caches, and a warp that converts all rows for itself takes 2 us for it.
+template <int D>
+struct Rows {
+  static constexpr int kStride = D + 4;    // (8 bytes more: neighbouring rows in different banks)
+  __align__(16) uint16_t q[kRows][kStride];
+  float unit[kRows];                       // -1: no such row, or one that holds something not finite
+};
+template <int D, bool F16, int kThr>
+__device__ __forceinline__ void read_rows(const SelectArgs& a, int b, int hk, int row0, int count, Rows<D>& out) {
+  constexpr int kOwn = D / 64;             // pairs of a lane
+  const int lane = threadIdx.x % 32, G = a.H / a.Hkv, rows = G * a.T;
+#pragma unroll 1
+  for (int i = threadIdx.x / 32; i < kRows; i += kThr / 32) {
+    const int r = row0 + i;
+    const bool there = r < rows && r % a.T < count;
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + (((int64_t)b * a.H + hk * G) * a.T + r) * D) +
+                        lane * kOwn;
+    float2 x[kOwn];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      x[k] = halves<F16>(there ? __ldg(p + k) : 0u);
+      amax = max(amax, max(__float_as_uint(x[k].x) & 0x7fffffffu, __float_as_uint(x[k].y) & 0x7fffffffu));
+    }
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    const float u = power_scale<true>(amax), inv = 1.f / u;
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      const float y = rintf(x[k].x * inv), z = rintf(x[k].y * inv);
+      reinterpret_cast<uint32_t*>(out.q[i])[lane * kOwn + k] = ptx::pack_f16(y, z);
+    }
+    if (lane == 0) out.unit[i] = there && amax < 0x7f800000u ? u : -1.f;
+  }
+}
+
+// 16 rows as left operands: product 4 i + w takes the values [64 i + 16 (lane % 4) + 4 w, + 4) of a lane
 // (columns 2 j, 2 j + 1, 2 j + 8, 2 j + 9 of lane j), whole numbers in fp16; and what these count.
 template <int D, bool F16>
 struct Queries {
   uint32_t q[D / 16][4];
   float unit[2];                           // -1: no such row, or one that holds something not finite
+  __device__ __forceinline__ void take(const Rows<D>& r) {
+    const int lane = threadIdx.x % 32;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = lane / 4 + e * 8;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        const uint2 x = *reinterpret_cast<const uint2*>(&r.q[row][j / 4 * 64 + lane % 4 * 16 + j % 4 * 4]);
+        q[j][e] = x.x;
+        q[j][e + 2] = x.y;
+      }
+      unit[e] = r.unit[row];
+    }
+  }
+  // ... or converted by the warp itself
   __device__ __forceinline__ void read(const SelectArgs& a, int b, int hk, int row0, int count) {
     const int lane = threadIdx.x % 32, G = a.H / a.Hkv, rows = G * a.T;
 #pragma unroll
@@ -114,10 +174,11 @@ struct Queries {
   }
 };
 
-// Whole numbers in the order of the scores
+// Whole numbers in the order of the scores; above all of them those of pages that are always chosen, below them of no page.
+constexpr uint32_t kForcedKey = 0xffffffffu, kNanKey = 0xfffffffeu, kNoKey = 0u;
 __device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t u = __float_as_uint(x);
-  return x != x ? 0xffffffffu : (u >> 31) != 0u ? ~u : u | 0x80000000u;
+  return x != x ? kNanKey : (u >> 31) != 0u ? ~u : u | 0x80000000u;
 }
 
 // Scores of pages [p32, n) in steps of `step`, 32 at a time, for rows [row0, row0 + 16): put(page, score).
@@ -193,6 +254,25 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, const Queries<D
 }
 __device__ __forceinline__ float larger_score(float x, float y) { return x != x || y != y ? x + y : fmaxf(x, y); }
 
+// Scores by block `part` of the `parts` of a slice, neighbouring pages in different blocks: put(page, score, whether these are
+// the first rows).
+template <int D, bool F16, int kThr, typename Put>
+__device__ __forceinline__ void score_slice(const SelectArgs& a, int b, int hk, int n, int part, int parts, Put&& put) {
+  __shared__ Rows<D> shared;
+  const int rows = a.H / a.Hkv * a.T, count = new_tokens(a.q_lens, b, a.T);
+  const int p0 = (threadIdx.x / 32 * parts + part) * 32, step = parts * kThr;
+#pragma unroll 1
+  for (int row0 = 0; row0 < rows; row0 += kRows) {
+    if (row0 > 0) __syncthreads();                         // the rows before are read no more
+    read_rows<D, F16, kThr>(a, b, hk, row0, count, shared);
+    __syncthreads();
+    if (p0 >= n) continue;
+    Queries<D, F16> q;
+    q.take(shared);
+    score_pages<D, F16>(a, q, b, hk, n, p0, step, [&](int p, float x) { put(p, x, row0 == 0); });
+  }
+}
+
 // Scores on all SMs: warp W of the grid takes slice W % slices, so that neighbours read neighbouring heads' bounds.
 template <int D, bool F16>
 __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const SelectArgs a, const int slots) {
@@ -202,7 +282,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const 
   const int n = pages_of(a, b);
   if (n <= a.picks || slot >= slots || slot * 32 >= n) return;   // all of them, or no page for this warp
   const int rows = a.H / a.Hkv * a.T, count = new_tokens(a.q_lens, b, a.T);
-  float* const scores = a.scores + (int64_t)slice * a.cache.max_pages;
+  float* const scores = a.scores + (int64_t)slice * score_stride(a.cache.max_pages);
   for (int row0 = 0; row0 < rows; row0 += kRows) {
     Queries<D, F16> q;
     q.read(a, b, hk, row0, count);
@@ -211,58 +291,37 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const 
   }
 }
 
-// kScored: score_kernel has been there.
-template <int D, bool F16, int kThr, bool kScored>
-__global__ void __launch_bounds__(kThr) select_kernel(const SelectArgs a) {
+// The choice among n pages, more than are wanted.  keys: the scores, a thread's own in fours (4 i to 4 i + 3 of i = its
+// number + k kThr).  Little code, for the caches of instructions are cold: one page a lane wherever there is no more
+// to it than a comparison.
+template <int kThr>
+__device__ __forceinline__ void choose(const SelectArgs& a, uint32_t* keys, int n, int32_t* out) {
   constexpr int kWarps = kThr / 32;
-  extern __shared__ __align__(16) uint32_t keys[];       // the pages' scores
-  __shared__ int hist[kBins];
+  constexpr int kPer = (kBins + kThr - 1) / kThr;        // bins of a thread
+  __shared__ int hist[kPer * kThr];
   __shared__ uint32_t ends[2][kWarps];
   __shared__ int sums[2][kWarps];
   __shared__ int found[3];                               // bin, keys in it, keys wanted of it
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int slice = blockIdx.x;
-  const int b = slice / a.Hkv, hk = slice % a.Hkv;
-  if (hk == 0 && threadIdx.x == 0) paged_len(a.cache, b, a.err);
-  const int n = pages_of(a, b);
-  int32_t* const out = a.pages + (int64_t)slice * a.picks;
-  if (n <= a.picks) {                                    // all of them
-    for (int i = threadIdx.x; i < a.picks; i += kThr) out[i] = i < n ? i : -1;
-    return;
-  }
-  if constexpr (kScored) {
-    const float* const scores = a.scores + (int64_t)slice * a.cache.max_pages;
-    for (int i = threadIdx.x; i < n; i += kThr) keys[i] = __float_as_uint(__ldcg(scores + i));
-  } else {
-    const int rows = a.H / a.Hkv * a.T, count = new_tokens(a.q_lens, b, a.T);
-    for (int row0 = 0; row0 < rows; row0 += kRows) {
-      Queries<D, F16> q;
-      q.read(a, b, hk, row0, count);
-      score_pages<D, F16>(a, q, b, hk, n, warp * 32, kWarps * 32, [&](int p, float x) {
-        keys[p] = __float_as_uint(row0 > 0 ? larger_score(__uint_as_float(keys[p]), x) : x);
-      });
-    }
-  }
-  __syncthreads();
-
-  // ---- the choice: pages that are always chosen, and the `want` highest of the others -----------------
-  auto forced = [&](int i) { return i < a.first || i >= n - a.last; };
+  // pages that are always chosen, and the `want` highest of the others
   const int64_t always = (int64_t)a.first + a.last;
   int want = always < a.picks ? a.picks - (int)always : 0;
   // the scores' range
   uint32_t lo = 0xffffffffu, hi = 0u;
   uint4* const keys4 = reinterpret_cast<uint4*>(keys);
   const int n4 = (n + 3) / 4;
+#pragma unroll 1
   for (int i = threadIdx.x; i < n4; i += kThr) {
     const uint4 v = keys4[i];
     uint32_t key[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
+      const int p = 4 * i + e;
       key[e] = order_of(__uint_as_float(key[e]));
-      if (4 * i + e < n && !forced(4 * i + e)) {
-        lo = min(lo, key[e]);
-        hi = max(hi, key[e]);
-      }
+      const bool own = p >= a.first && p < n - a.last;   // (n exceeds both)
+      lo = own ? min(lo, key[e]) : lo;
+      hi = own ? max(hi, key[e]) : hi;
+      key[e] = own ? key[e] : p < n ? kForcedKey : kNoKey;
     }
     keys4[i] = make_uint4(key[0], key[1], key[2], key[3]);
   }
@@ -272,31 +331,36 @@ __global__ void __launch_bounds__(kThr) select_kernel(const SelectArgs a) {
     ends[0][warp] = lo;
     ends[1][warp] = hi;
   }
-  __syncthreads();
 #pragma unroll
+  for (int e = 0; e < kPer; ++e) hist[e * kThr + threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll 4
   for (int w = 0; w < kWarps; ++w) {
     lo = min(lo, ends[0][w]);
     hi = max(hi, ends[1][w]);
   }
+  if (want == 0) {                                       // those that are always chosen alone
+    lo = kForcedKey;
+    hi = kNanKey;
+  }
   // [lo, hi] holds the K-th largest key: `want` of the keys in it are chosen, and all above
+#pragma unroll 1
   while (want > 0) {
     const int bits = 32 - __clz(hi - lo), shift = max(0, bits - 10);
-    for (int i = threadIdx.x; i < kBins; i += kThr) hist[i] = 0;
-    __syncthreads();
+#pragma unroll 1
     for (int i = threadIdx.x; i < n4; i += kThr) {
       const uint4 v = keys4[i];
       const uint32_t key[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (key[e] >= lo && key[e] <= hi && 4 * i + e < n && !forced(4 * i + e)) atomicAdd(&hist[(key[e] - lo) >> shift], 1);
+        if (key[e] - lo <= hi - lo) atomicAdd(&hist[(key[e] - lo) >> shift], 1);
     }
     __syncthreads();
-    // thread t holds bins from the top, kBins / kThr of them
-    constexpr int kPer = kBins / kThr;
+    // thread t holds kPer bins, from the top
     int mine[kPer], sum = 0;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
-      mine[e] = hist[kBins - 1 - kPer * threadIdx.x - e];
+      mine[e] = hist[kPer * kThr - 1 - kPer * threadIdx.x - e];
       sum += mine[e];
     }
     int up = sum;
@@ -308,13 +372,14 @@ __global__ void __launch_bounds__(kThr) select_kernel(const SelectArgs a) {
     if (lane == 31) sums[0][warp] = up;
     __syncthreads();
     int before = up - sum;
+#pragma unroll 4
     for (int w = 0; w < warp; ++w) before += sums[0][w];
     if (before < want && before + sum >= want) {
       bool open = true;
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
         if (open && before + mine[e] >= want) {
-          found[0] = kBins - 1 - kPer * (int)threadIdx.x - e;
+          found[0] = kPer * kThr - 1 - kPer * (int)threadIdx.x - e;
           found[1] = mine[e];
           found[2] = want - before;
           open = false;
@@ -322,6 +387,8 @@ __global__ void __launch_bounds__(kThr) select_kernel(const SelectArgs a) {
         before += mine[e];
       }
     }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) hist[e * kThr + threadIdx.x] = 0;     // (all have read their bins)
     __syncthreads();
     const uint32_t at = lo + ((uint32_t)found[0] << shift);
     hi = min(hi, at + ((1u << shift) - 1u));
@@ -330,25 +397,13 @@ __global__ void __launch_bounds__(kThr) select_kernel(const SelectArgs a) {
     if (shift == 0 || found[1] == want) break;
   }
   // in page order, each warp a run of pages: keys above, and the first `want` of those in the range
-  const int run = ((n + kWarps - 1) / kWarps + 127) / 128 * 128, end = min(n, (warp + 1) * run);
-  // a lane's four pages: bits of those above, and of those in the range
-  auto look = [&](int i, uint32_t* ups, uint32_t* ties) {
-    const uint4 v = i < end ? keys4[i / 4] : make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t key[4] = {v.x, v.y, v.z, v.w};
-    *ups = *ties = 0u;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const bool there = i + e < end, sure = forced(i + e);
-      if (there && (sure || (want > 0 && key[e] > hi))) *ups |= 1u << e;
-      else if (there && want > 0 && key[e] >= lo) *ties |= 1u << e;
-    }
-  };
+  const int run = ((n + kWarps - 1) / kWarps + 31) / 32 * 32, begin = warp * run + lane, end = min(n, (warp + 1) * run);
   int above = 0, equal = 0;
-  for (int i0 = warp * run; i0 < end; i0 += 128) {
-    uint32_t ups, ties;
-    look(i0 + 4 * lane, &ups, &ties);
-    above += __popc(ups);
-    equal += __popc(ties);
+#pragma unroll 4
+  for (int i = begin; i < end; i += 32) {
+    const uint32_t key = keys[i];
+    above += key > hi ? 1 : 0;
+    equal += key - lo <= hi - lo ? 1 : 0;
   }
   above = __reduce_add_sync(0xffffffffu, above);
   equal = __reduce_add_sync(0xffffffffu, equal);
@@ -359,34 +414,87 @@ __global__ void __launch_bounds__(kThr) select_kernel(const SelectArgs a) {
   }
   __syncthreads();
   above = equal = 0;
+#pragma unroll 4
   for (int w = 0; w < warp; ++w) {
     above += sums[0][w];
     equal += sums[1][w];
   }
-  for (int i0 = warp * run; i0 < end; i0 += 128) {
-    uint32_t ups, ties;
-    look(i0 + 4 * lane, &ups, &ties);
-    const int mine = __popc(ups) | __popc(ties) << 16;
-    int both = mine;                                     // two counts, the range's in the upper half
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, both, o);
-      if (lane >= o) both += x;
-    }
-    const int all = __shfl_sync(0xffffffffu, both, 31);
-    both -= mine;
-    int u = above + (both & 0xffff), t = equal + (both >> 16);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const bool up = (ups >> e & 1u) != 0u, tie = (ties >> e & 1u) != 0u;
-      const int at = u + min(t, want);
-      if ((up || (tie && t < want)) && at < a.picks) out[at] = i0 + 4 * lane + e;   // (more that are always chosen: the first ones)
-      u += up;
-      t += tie;
-    }
-    above += all & 0xffff;
-    equal += all >> 16;
+  const uint32_t lower = (1u << lane) - 1u;
+#pragma unroll 1
+  for (int i = begin; i - lane < end; i += 32) {
+    const uint32_t key = i < end ? keys[i] : kNoKey;
+    const bool up = key > hi, tie = key - lo <= hi - lo;
+    const uint32_t ups = __ballot_sync(0xffffffffu, up), ties = __ballot_sync(0xffffffffu, tie);
+    const int t = equal + __popc(ties & lower), at = above + __popc(ups & lower) + min(t, want);
+    if ((up || (tie && t < want)) && at < a.picks) out[at] = i;          // (more that are always chosen: the first ones)
+    above += __popc(ups);
+    equal += __popc(ties);
   }
+}
+
+// Scores from the workspace to each thread's own keys.
+template <int kThr>
+__device__ __forceinline__ void take_scores(const float* scores, uint32_t* keys, int n) {
+  const int n4 = (n + 3) / 4;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < n4; i += kThr) reinterpret_cast<uint4*>(keys)[i] = __ldcg(reinterpret_cast<const uint4*>(scores) + i);
+}
+
+// kScored: score_kernel has been there.
+template <int D, bool F16, int kThr, bool kScored>
+__global__ void __launch_bounds__(kThr, kThr == 128 ? 3 : 1) select_kernel(const SelectArgs a) {
+  extern __shared__ __align__(16) uint32_t keys[];       // the pages' scores
+  const int slice = blockIdx.x;
+  const int b = slice / a.Hkv, hk = slice % a.Hkv;
+  if (hk == 0 && threadIdx.x == 0) paged_len(a.cache, b, a.err);
+  const int n = pages_of(a, b);
+  int32_t* const out = a.pages + (int64_t)slice * a.picks;
+  if (n <= a.picks) {                                    // all of them
+    for (int i = threadIdx.x; i < a.picks; i += kThr) out[i] = i < n ? i : -1;
+    return;
+  }
+  if constexpr (kScored) {
+    take_scores<kThr>(a.scores + (int64_t)slice * score_stride(a.cache.max_pages), keys, n);
+  } else {
+    score_slice<D, F16, kThr>(a, b, hk, n, 0, 1, [&](int p, float x, bool first) {
+      keys[p] = __float_as_uint(first ? x : larger_score(__uint_as_float(keys[p]), x));
+    });
+    __syncthreads();
+  }
+  choose<kThr>(a, keys, n, out);
+}
+
+// Few slices: `parts` blocks score the pages of each, and the one that comes last chooses.
+template <int D, bool F16>
+__global__ void __launch_bounds__(kJointThreads) joint_kernel(const SelectArgs a, const int parts) {
+  extern __shared__ __align__(16) uint32_t keys[];       // the pages' scores
+  __shared__ bool last;
+  const int slices = a.B * a.Hkv, slice = blockIdx.x % slices, part = blockIdx.x / slices;
+  const int b = slice / a.Hkv, hk = slice % a.Hkv;
+  if (hk == 0 && part == 0 && threadIdx.x == 0) paged_len(a.cache, b, a.err);
+  const int n = pages_of(a, b);
+  int32_t* const out = a.pages + (int64_t)slice * a.picks;
+  if (n <= a.picks) {                                    // all of them
+    if (part == 0)
+      for (int i = threadIdx.x; i < a.picks; i += kJointThreads) out[i] = i < n ? i : -1;
+    return;
+  }
+  unsigned long long* const word = a.arrivals + slice;
+  if (threadIdx.x == 0) open_count(word, a.call);
+  float* const scores = a.scores + (int64_t)slice * score_stride(a.cache.max_pages);
+  score_slice<D, F16, kJointThreads>(a, b, hk, n, part, parts,
+                                     [&](int p, float x, bool first) { scores[p] = first ? x : larger_score(scores[p], x); });
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    asm volatile("fence.acq_rel.gpu;" ::: "memory");     // releases what the whole block wrote before its barrier
+    last = count_part(word, parts);
+    if (last) asm volatile("fence.acq_rel.gpu;" ::: "memory");       // the scores, for the block after its barrier
+  }
+  __syncthreads();
+  if (!last) return;
+  if (threadIdx.x == 0) *word = 0ull;                    // for a captured call's next run under the same number
+  take_scores<kJointThreads>(scores, keys, n);
+  choose<kJointThreads>(a, keys, n, out);
 }
 
 template <int D, bool F16, int kThr, bool kScored>
@@ -399,6 +507,9 @@ cudaError_t launch_one(const SelectArgs& a, cudaStream_t s) {
   kern<<<(unsigned)(a.B * a.Hkv), kThr, smem, s>>>(a);
   return cudaGetLastError();
 }
+// Few slices, of which each finds blocks on several SMs: they choose too.
+bool select_jointly(int slices, int sms) { return 4 * slices <= sms; }
+
 template <int D, bool F16>
 cudaError_t launch_any(const SelectArgs& a, cudaStream_t s) {
   if (!select_scores_first(a.B, a.Hkv, a.cache.max_pages, a.picks))
@@ -406,8 +517,17 @@ cudaError_t launch_any(const SelectArgs& a, cudaStream_t s) {
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
+  const int slices = a.B * a.Hkv;
+  if (select_jointly(slices, sms)) {
+    const int parts = std::min(sms / slices, (a.cache.max_pages + 31) / 32);
+    static LaunchSetup setup;
+    const int smem = (int)score_stride(a.cache.max_pages) * 4;
+    if ((e = prepare_launch(setup, joint_kernel<D, F16>, smem)) != cudaSuccess) return e;
+    joint_kernel<D, F16><<<slices * parts, kJointThreads, smem, s>>>(a, parts);
+    return cudaGetLastError();
+  }
   // warps of a slice: all take the same number of pages, as many warps as the SMs hold
-  const int slices = a.B * a.Hkv, blocks = (a.cache.max_pages + 31) / 32;
+  const int blocks = (a.cache.max_pages + 31) / 32;
   const int most = std::max(1, sms * kScoreCtas * (kScoreThreads / 32) / slices), each = (blocks + most - 1) / most;
   const int slots = (blocks + each - 1) / each;
   const int grid = (slots * slices + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
@@ -426,6 +546,11 @@ bool select_scores_first(int B, int Hkv, int max_pages, int picks) {
   int sms = 0;
   if (sm_count(&sms) != cudaSuccess || sms <= 0) sms = 152;        // GB300's when no device can be asked
   return max_pages > picks && max_pages > 512 && (int64_t)B * Hkv <= 4 * (int64_t)sms;
+}
+
+size_t select_workspace(int B, int Hkv, int max_pages, size_t* arrivals) {
+  *arrivals = (size_t)B * Hkv * score_stride(max_pages) * sizeof(float);
+  return (*arrivals + (size_t)B * Hkv * sizeof(unsigned long long) + 255) / 256 * 256;
 }
 
 cudaError_t launch_select(const SelectArgs& a, fa_dtype dt, cudaStream_t s) {
