@@ -28,6 +28,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fa_arrivals.cuh"
 #include "fa_paged.cuh"
@@ -90,12 +91,12 @@ struct Rows {
   __align__(16) uint16_t q[kRows][kStride];
   float unit[kRows];                       // -1: no such row, or one that holds something not finite
 };
-template <int D, bool F16, int kThr>
+template <int D, bool F16, int kThr, int kCount>
 __device__ __forceinline__ void read_rows(const SelectArgs& a, int b, int hk, int row0, int count, Rows<D>& out) {
   constexpr int kOwn = D / 64;             // pairs of a lane
   const int lane = threadIdx.x % 32, G = a.H / a.Hkv, rows = G * a.T;
 #pragma unroll 1
-  for (int i = threadIdx.x / 32; i < kRows; i += kThr / 32) {
+  for (int i = threadIdx.x / 32; i < kCount; i += kThr / 32) {
     const int r = row0 + i;
     const bool there = r < rows && r % a.T < count;
     const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + (((int64_t)b * a.H + hk * G) * a.T + r) * D) +
@@ -118,31 +119,33 @@ __device__ __forceinline__ void read_rows(const SelectArgs& a, int b, int hk, in
   }
 }
 
-// 16 rows as left operands: product 4 i + w takes the values [64 i + 16 (lane % 4) + 4 w, + 4) of a lane
-// (columns 2 j, 2 j + 1, 2 j + 8, 2 j + 9 of lane j), whole numbers in fp16; and what these count.
-template <int D, bool F16>
+// 16 rows as left operands, or 8 as right ones (kFlip): product 4 i + w takes the values [64 i + 16 (lane % 4) + 4 w, + 4) of
+// a lane (k-columns 2 j, 2 j + 1, 2 j + 8, 2 j + 9 of lane j).
+template <int D, bool F16, bool kFlip>
 struct Queries {
-  uint32_t q[D / 16][4];
-  float unit[2];                           // -1: no such row, or one that holds something not finite
+  static constexpr int kHalves = kFlip ? 1 : 2;            // rows of a lane: lane / 4, and that and 8 more
+  uint32_t q[D / 16][2 * kHalves];
+  float unit[2];                           // of the rows of the lane's sums.  -1: no such row, or one that holds something not finite
   __device__ __forceinline__ void take(const Rows<D>& r) {
     const int lane = threadIdx.x % 32;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < kHalves; ++e) {
       const int row = lane / 4 + e * 8;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
         const uint2 x = *reinterpret_cast<const uint2*>(&r.q[row][j / 4 * 64 + lane % 4 * 16 + j % 4 * 4]);
         q[j][e] = x.x;
-        q[j][e + 2] = x.y;
+        q[j][e + kHalves] = x.y;
       }
-      unit[e] = r.unit[row];
     }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) unit[e] = r.unit[kFlip ? lane % 4 * 2 + e : lane / 4 + e * 8];
   }
   // ... or converted by the warp itself
   __device__ __forceinline__ void read(const SelectArgs& a, int b, int hk, int row0, int count) {
     const int lane = threadIdx.x % 32, G = a.H / a.Hkv, rows = G * a.T;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < kHalves; ++e) {
       const int r = row0 + lane / 4 + e * 8, t = r % a.T;
       const bool there = r < rows && t < count;
       const uint16_t* p = static_cast<const uint16_t*>(a.q) + (((int64_t)b * a.H + hk * G) * a.T + r) * D + lane % 4 * 16;
@@ -169,7 +172,13 @@ struct Queries {
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) q[j][e + 2 * k] = ptx::pack_f16(rintf(x[4 * j + 2 * k] * inv), rintf(x[4 * j + 2 * k + 1] * inv));
+        for (int k = 0; k < 2; ++k)
+          q[j][e + kHalves * k] = ptx::pack_f16(rintf(x[4 * j + 2 * k] * inv), rintf(x[4 * j + 2 * k + 1] * inv));
+    }
+    if constexpr (kFlip) {
+      const float own = unit[0];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) unit[e] = __shfl_sync(0xffffffffu, own, 4 * (lane % 4 * 2 + e));
     }
   }
 };
@@ -182,8 +191,8 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 }
 
 // Scores of pages [p32, n) in steps of `step`, 32 at a time, for rows [row0, row0 + 16): put(page, score).
-template <int D, bool F16, typename Put>
-__device__ __forceinline__ void score_pages(const SelectArgs& a, const Queries<D, F16>& q, int b, int hk, int n, int p32,
+template <int D, bool F16, bool kFlip, typename Put>
+__device__ __forceinline__ void score_pages(const SelectArgs& a, const Queries<D, F16, kFlip>& q, int b, int hk, int n, int p32,
                                             int step, Put&& put) {
   const int lane = threadIdx.x % 32;
   const int32_t* const table = a.cache.table + b * a.cache.table_stride;
@@ -213,6 +222,44 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, const Queries<D
       mine[y] = page >= 0 ? __ldg(a.bound_scales + place) : 0.f;
     }
     next = places(p32 + step);
+    if constexpr (kFlip) {
+      // two groups' pages are the rows of a product, the queries its columns
+#pragma unroll
+      for (int y = 0; y < 4; y += 2) {
+        const int p = p32 + y * kGroup + lane / 4;
+        if (p32 + y * kGroup >= n) break;
+        float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t sum[4], diff[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint4 lo = v[y + e][i], hi = v[y + e][D / 64 + i];
+              const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
+              uint32_t s2[2], d2[2];
+              sum_and_difference(l[w], h[w], s2, d2);
+              sum[e] = s2[0];
+              sum[e + 2] = s2[1];
+              diff[e] = d2[0];
+              diff[e + 2] = d2[1];
+            }
+            const uint32_t q0 = q.q[4 * i + w][0], q1 = q.q[4 * i + w][1];
+            mma(c, sum, q0, q1);
+            mma(d, diff, q0 & 0x7fff7fffu, q1 & 0x7fff7fffu);
+          }
+        // the lane's sums: queries 2 (lane % 4) and the next, of pages lane / 4 and that and 8 more
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float best = fmaxf(q.unit[0] == -1.f ? -INFINITY : 0.5f * (c[2 * e] + d[2 * e]) * q.unit[0],
+                             q.unit[1] == -1.f ? -INFINITY : 0.5f * (c[2 * e + 1] + d[2 * e + 1]) * q.unit[1]);
+          best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
+          best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
+          if (lane % 4 == 0 && p + 8 * e < n) put(p + 8 * e, __fmul_rn(best, mine[y + e]));
+        }
+      }
+    } else {
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
       const int p0 = p32 + y * kGroup;
@@ -250,13 +297,14 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, const Queries<D
           if (p0 + 2 * lane + e < n) put(p0 + 2 * lane + e, best[e]);
       }
     }
+    }
   }
 }
 __device__ __forceinline__ float larger_score(float x, float y) { return x != x || y != y ? x + y : fmaxf(x, y); }
 
 // Scores by block `part` of the `parts` of a slice, neighbouring pages in different blocks: put(page, score, whether these are
 // the first rows).
-template <int D, bool F16, int kThr, typename Put>
+template <int D, bool F16, bool kFlip, int kThr, typename Put>
 __device__ __forceinline__ void score_slice(const SelectArgs& a, int b, int hk, int n, int part, int parts, Put&& put) {
   __shared__ Rows<D> shared;
   const int rows = a.H / a.Hkv * a.T, count = new_tokens(a.q_lens, b, a.T);
@@ -264,17 +312,17 @@ __device__ __forceinline__ void score_slice(const SelectArgs& a, int b, int hk, 
 #pragma unroll 1
   for (int row0 = 0; row0 < rows; row0 += kRows) {
     if (row0 > 0) __syncthreads();                         // the rows before are read no more
-    read_rows<D, F16, kThr>(a, b, hk, row0, count, shared);
+    read_rows<D, F16, kThr, kFlip ? 8 : kRows>(a, b, hk, row0, count, shared);
     __syncthreads();
     if (p0 >= n) continue;
-    Queries<D, F16> q;
+    Queries<D, F16, kFlip> q;
     q.take(shared);
-    score_pages<D, F16>(a, q, b, hk, n, p0, step, [&](int p, float x) { put(p, x, row0 == 0); });
+    score_pages<D, F16, kFlip>(a, q, b, hk, n, p0, step, [&](int p, float x) { put(p, x, row0 == 0); });
   }
 }
 
 // Scores on all SMs: warp W of the grid takes slice W % slices, so that neighbours read neighbouring heads' bounds.
-template <int D, bool F16>
+template <int D, bool F16, bool kFlip>
 __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const SelectArgs a, const int slots) {
   const int warp = blockIdx.x * (kScoreThreads / 32) + threadIdx.x / 32, slices = a.B * a.Hkv;
   const int slice = warp % slices, slot = warp / slices;
@@ -284,9 +332,9 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const 
   const int rows = a.H / a.Hkv * a.T, count = new_tokens(a.q_lens, b, a.T);
   float* const scores = a.scores + (int64_t)slice * score_stride(a.cache.max_pages);
   for (int row0 = 0; row0 < rows; row0 += kRows) {
-    Queries<D, F16> q;
+    Queries<D, F16, kFlip> q;
     q.read(a, b, hk, row0, count);
-    score_pages<D, F16>(a, q, b, hk, n, slot * 32, slots * 32,
+    score_pages<D, F16, kFlip>(a, q, b, hk, n, slot * 32, slots * 32,
                         [&](int p, float x) { scores[p] = row0 > 0 ? larger_score(scores[p], x) : x; });
   }
 }
@@ -441,7 +489,7 @@ __device__ __forceinline__ void take_scores(const float* scores, uint32_t* keys,
 }
 
 // kScored: score_kernel has been there.
-template <int D, bool F16, int kThr, bool kScored>
+template <int D, bool F16, bool kFlip, int kThr, bool kScored>
 __global__ void __launch_bounds__(kThr, kThr == 128 ? 3 : 1) select_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) uint32_t keys[];       // the pages' scores
   const int slice = blockIdx.x;
@@ -456,7 +504,7 @@ __global__ void __launch_bounds__(kThr, kThr == 128 ? 3 : 1) select_kernel(const
   if constexpr (kScored) {
     take_scores<kThr>(a.scores + (int64_t)slice * score_stride(a.cache.max_pages), keys, n);
   } else {
-    score_slice<D, F16, kThr>(a, b, hk, n, 0, 1, [&](int p, float x, bool first) {
+    score_slice<D, F16, kFlip, kThr>(a, b, hk, n, 0, 1, [&](int p, float x, bool first) {
       keys[p] = __float_as_uint(first ? x : larger_score(__uint_as_float(keys[p]), x));
     });
     __syncthreads();
@@ -465,7 +513,7 @@ __global__ void __launch_bounds__(kThr, kThr == 128 ? 3 : 1) select_kernel(const
 }
 
 // Few slices: `parts` blocks score the pages of each, and the one that comes last chooses.
-template <int D, bool F16>
+template <int D, bool F16, bool kFlip>
 __global__ void __launch_bounds__(kJointThreads) joint_kernel(const SelectArgs a, const int parts) {
   extern __shared__ __align__(16) uint32_t keys[];       // the pages' scores
   __shared__ bool last;
@@ -482,7 +530,7 @@ __global__ void __launch_bounds__(kJointThreads) joint_kernel(const SelectArgs a
   unsigned long long* const word = a.arrivals + slice;
   if (threadIdx.x == 0) open_count(word, a.call);
   float* const scores = a.scores + (int64_t)slice * score_stride(a.cache.max_pages);
-  score_slice<D, F16, kJointThreads>(a, b, hk, n, part, parts,
+  score_slice<D, F16, kFlip, kJointThreads>(a, b, hk, n, part, parts,
                                      [&](int p, float x, bool first) { scores[p] = first ? x : larger_score(scores[p], x); });
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -497,9 +545,9 @@ __global__ void __launch_bounds__(kJointThreads) joint_kernel(const SelectArgs a
   choose<kJointThreads>(a, keys, n, out);
 }
 
-template <int D, bool F16, int kThr, bool kScored>
+template <int D, bool F16, bool kFlip, int kThr, bool kScored>
 cudaError_t launch_one(const SelectArgs& a, cudaStream_t s) {
-  auto kern = select_kernel<D, F16, kThr, kScored>;
+  auto kern = select_kernel<D, F16, kFlip, kThr, kScored>;
   static LaunchSetup setup;
   const int smem = a.cache.max_pages > a.picks ? (a.cache.max_pages + 3) / 4 * 16 : 0;
   const cudaError_t e = prepare_launch(setup, kern, smem);
@@ -510,10 +558,10 @@ cudaError_t launch_one(const SelectArgs& a, cudaStream_t s) {
 // Few slices, of which each finds blocks on several SMs: they choose too.
 bool select_jointly(int slices, int sms) { return 4 * slices <= sms; }
 
-template <int D, bool F16>
+template <int D, bool F16, bool kFlip>
 cudaError_t launch_any(const SelectArgs& a, cudaStream_t s) {
   if (!select_scores_first(a.B, a.Hkv, a.cache.max_pages, a.picks))
-    return a.cache.max_pages <= 512 ? launch_one<D, F16, 128, false>(a, s) : launch_one<D, F16, 256, false>(a, s);
+    return a.cache.max_pages <= 512 ? launch_one<D, F16, kFlip, 128, false>(a, s) : launch_one<D, F16, kFlip, 256, false>(a, s);
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
@@ -522,8 +570,8 @@ cudaError_t launch_any(const SelectArgs& a, cudaStream_t s) {
     const int parts = std::min(sms / slices, (a.cache.max_pages + 31) / 32);
     static LaunchSetup setup;
     const int smem = (int)score_stride(a.cache.max_pages) * 4;
-    if ((e = prepare_launch(setup, joint_kernel<D, F16>, smem)) != cudaSuccess) return e;
-    joint_kernel<D, F16><<<slices * parts, kJointThreads, smem, s>>>(a, parts);
+    if ((e = prepare_launch(setup, joint_kernel<D, F16, kFlip>, smem)) != cudaSuccess) return e;
+    joint_kernel<D, F16, kFlip><<<slices * parts, kJointThreads, smem, s>>>(a, parts);
     return cudaGetLastError();
   }
   // warps of a slice: all take the same number of pages, as many warps as the SMs hold
@@ -531,10 +579,10 @@ cudaError_t launch_any(const SelectArgs& a, cudaStream_t s) {
   const int most = std::max(1, sms * kScoreCtas * (kScoreThreads / 32) / slices), each = (blocks + most - 1) / most;
   const int slots = (blocks + each - 1) / each;
   const int grid = (slots * slices + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
-  score_kernel<D, F16><<<grid, kScoreThreads, 0, s>>>(a, slots);
+  score_kernel<D, F16, kFlip><<<grid, kScoreThreads, 0, s>>>(a, slots);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // (the queries' type and size do not matter)
-  return a.cache.max_pages <= 2048 ? launch_one<64, false, 256, true>(a, s) : launch_one<64, false, 1024, true>(a, s);
+  return a.cache.max_pages <= 2048 ? launch_one<64, false, false, 256, true>(a, s) : launch_one<64, false, false, 1024, true>(a, s);
 }
 
 }  // namespace
@@ -554,8 +602,13 @@ size_t select_workspace(int B, int Hkv, int max_pages, size_t* arrivals) {
 }
 
 cudaError_t launch_select(const SelectArgs& a, fa_dtype dt, cudaStream_t s) {
-  if (a.d == 64) return dt == FA_FP16 ? launch_any<64, true>(a, s) : launch_any<64, false>(a, s);
-  return dt == FA_FP16 ? launch_any<128, true>(a, s) : launch_any<128, false>(a, s);
+  auto launch = [&](auto d, auto f16) {
+    constexpr int D = decltype(d)::value;
+    constexpr bool F16 = decltype(f16)::value;
+    return a.H / a.Hkv * a.T <= 8 ? launch_any<D, F16, true>(a, s) : launch_any<D, F16, false>(a, s);
+  };
+  auto typed = [&](auto d) { return dt == FA_FP16 ? launch(d, std::true_type{}) : launch(d, std::false_type{}); };
+  return a.d == 64 ? typed(std::integral_constant<int, 64>{}) : typed(std::integral_constant<int, 128>{});
 }
 
 }  // namespace fa
