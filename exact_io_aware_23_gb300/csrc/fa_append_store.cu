@@ -75,7 +75,7 @@ __device__ __forceinline__ bool page_work(const AppendArgs& a, int b, int p, Pag
   const int count = new_tokens(a.q_lens, b, a.T);
   const int len = paged_len(a.cache, b, a.err);
   w->begin = len - count;
-  const int size = a.cache.page_size, lead = max(w->begin, 0) / size + p;
+  const int size = a.cache.page_size, lead = (int)((uint32_t)max(w->begin, 0) / (uint32_t)size) + p;
   const int64_t start = (int64_t)lead * size;
   if (count == 0 || start >= len) return false;
   w->first = max(max(w->begin, 0), (int)start);
@@ -415,15 +415,16 @@ __device__ __forceinline__ void write_page(const AppendArgs& a, const StoreArgs&
 
 // Queries: turned and copied, as in the write into 16-bit pages.
 template <typename T, int kThr>
-__device__ __forceinline__ void turn_queries(const AppendArgs& a, const StoreArgs& st, int64_t block) {
+__device__ __forceinline__ void turn_queries(const AppendArgs& a, const StoreArgs& st, uint32_t block) {
   constexpr int kBatch = 4;
   const int units = a.d / kUnit, per_block = kThr / units;
   const int u = threadIdx.x % units;
   const Unit t = unit_of(u, a.rot);
-  const int h0 = (int)(block % st.q_head_blocks) * st.q_heads, h1 = min(a.H, h0 + st.q_heads);
-  const int64_t m = block / st.q_head_blocks * per_block + threadIdx.x / units;
-  if (m >= (int64_t)a.B * a.T) return;
-  const int b = (int)(m / a.T), n = (int)(m % a.T);
+  const uint32_t group = block / (uint32_t)st.q_head_blocks;
+  const int h0 = (int)(block - group * st.q_head_blocks) * st.q_heads, h1 = min(a.H, h0 + st.q_heads);
+  const uint32_t m = group * per_block + threadIdx.x / units;      // (B * T is below 2^31)
+  if (m >= (uint32_t)a.B * (uint32_t)a.T) return;
+  const int b = (int)(m / (uint32_t)a.T), n = (int)(m - (uint32_t)b * a.T);
   const int count = new_tokens(a.q_lens, b, a.T);
   const int pos = paged_len(a.cache, b, nullptr) - count + n;
   const bool there = n < count && pos >= 0;
@@ -464,15 +465,14 @@ __global__ void __launch_bounds__(kThr, (kTurn && kBounds ? 384 : kTurn ? 512 : 
   constexpr int kWords = kWarps + (kBounds ? 2 * kWarps * (kTurn ? 128 : 64) : 0);
   __shared__ __align__(16) uint32_t smem[kTeams][(kWords + 3) / 4 * 4];
   if ((int64_t)blockIdx.x >= st.page_blocks) {
-    turn_queries<T, kThr>(a, st, (int64_t)blockIdx.x - st.page_blocks);
+    turn_queries<T, kThr>(a, st, blockIdx.x - (uint32_t)st.page_blocks);
     return;
   }
-  const int64_t team = (int64_t)blockIdx.x * kTeams + threadIdx.x / kTeam;
-  const int h = (int)(team % (2 * a.Hkv));
-  const int64_t bp = team / (2 * a.Hkv);
-  const int64_t b = bp / st.span;
-  const int p = (int)(bp - b * st.span);
-  if (b >= a.B) return;                                    // (teams behind the last one: warps)
+  // (32 bits: a division in 64 is longer than a row's work)
+  const uint32_t team = blockIdx.x * kTeams + threadIdx.x / kTeam, heads = 2u * a.Hkv;
+  const uint32_t bp = team / heads, b = bp / (uint32_t)st.span;
+  const int h = (int)(team - bp * heads), p = (int)(bp - b * st.span);
+  if (b >= (uint32_t)a.B) return;                          // (teams behind the last one: warps)
   uint32_t* const words = smem[threadIdx.x / kTeam];
   if constexpr (kTurn) {
     if (h < a.Hkv) {
@@ -503,7 +503,7 @@ cudaError_t append_store(const AppendArgs& a, StoreArgs st, int sms, cudaStream_
     st.q_head_blocks = (a.H + st.q_heads - 1) / st.q_heads;
     q_blocks = tokens * st.q_head_blocks;
   }
-  if (st.page_blocks + q_blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if (heads > 0x7fffff00 || st.page_blocks + q_blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const unsigned grid = (unsigned)(st.page_blocks + q_blocks);
   if (team == 32) append_store_kernel<T, kStore, kTurn, kBounds, 32, 128><<<grid, 128, 0, s>>>(a, st);
   else if (team == 128) append_store_kernel<T, kStore, kTurn, kBounds, 128, 128><<<grid, 128, 0, s>>>(a, st);
