@@ -457,9 +457,11 @@ __device__ __forceinline__ void turn_queries(const AppendArgs& a, const StoreArg
   }
 }
 
-// kThr threads a block, teams of kTeam.  Turned keys, and bounds, take registers: fewer blocks on an SM.
+// kThr threads a block, teams of kTeam.  Turned keys take registers: fewer blocks on an SM.  Otherwise as many as there can be,
+// though 72 registers spill four words: 4 ragged prompts of up to 4096 tokens at d = 128, int8 and bounds, 21.3 us with five
+// blocks, 19.2 with six, 18.8 with seven; without bounds 16.7 with six and 15.2 with seven.
 template <typename T, int kStore, bool kTurn, bool kBounds, int kTeam, int kThr>
-__global__ void __launch_bounds__(kThr, (kTurn && kBounds ? 384 : kTurn ? 512 : kBounds ? 640 : 768) / kThr)
+__global__ void __launch_bounds__(kThr, (kTurn && kBounds ? 384 : kTurn ? 512 : kTeam == 32 && kBounds ? 640 : kTeam == 128 ? 896 : 768) / kThr)
     append_store_kernel(const AppendArgs a, const StoreArgs st) {
   constexpr int kWarps = kTeam / 32, kTeams = kThr / kTeam;
   constexpr int kWords = kWarps + (kBounds ? 2 * kWarps * (kTurn ? 128 : 64) : 0);
