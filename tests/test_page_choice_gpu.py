@@ -168,6 +168,49 @@ def test_choice_in_a_graph_on_streams_and_with_given_memory():
     assert all(torch.equal(x, out) for x in got)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,Hkv,T,long", [
+    (20, 8, 2, 1, 9600), (20, 8, 2, 4, 8300), (13, 3, 3, 17, 12000),     # scored on all SMs first: 8, 16 and more rows
+    (160, 4, 4, 1, 8400), (80, 16, 8, 6, 8200),                            # many slices: a block scores and chooses
+    (38, 2, 1, 1, 9000), (39, 2, 1, 1, 9000), (19, 12, 2, 2, 33000)])       # the most that are chosen from where they are scored
+def test_slices_of_many_numbers(d, B, H, Hkv, T, long):
+    g = torch.Generator(device="cuda").manual_seed(B + H + T)
+    lens = [long if b % 37 == 1 else 16 * (b % 40) + b % 7 for b in range(B)]
+    table, n = _table(lens, 16, g)
+    bounds, unit = _bounds(n, Hkv, d, g, ties=B % 2 == 1)
+    q = torch.randn((B, H, T, d), generator=g, device="cuda").to(torch.float16)
+    got = fa.select_pages(q, bounds, unit, table, _i32(lens), 11, 16)
+    assert torch.equal(got, _want(q, bounds, unit, table, lens, 11, 16, 1, 1))
+
+
+def test_captured_choices_share_a_workspace():
+    """Two captured calls and calls between them count in the same words."""
+    g = torch.Generator(device="cuda").manual_seed(18)
+    table, n = _table([12000, 9000], 16, g)
+    bounds, unit = _bounds(n, 2, 64, g)
+    q = [torch.randn((2, 8, T, 64), generator=g, device="cuda").to(torch.bfloat16) for T in (1, 5)]
+    nl = _i32([12000, 9000])
+    ws = torch.randint(0, 256, (fa.select_pages_workspace_size(2, 2, 750, 20),), generator=g, device="cuda", dtype=torch.uint8)
+    out = [torch.empty((2, 2, 20), dtype=torch.int32, device="cuda") for _ in q]
+    graphs = []
+    for x, y in zip(q, out):
+        fa.select_pages(x, bounds, unit, table, nl, 20, 16, pages=y, workspace=ws)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            fa.select_pages(x, bounds, unit, table, nl, 20, 16, pages=y, workspace=ws)
+    for lens in ([12000, 9000], [8200, 12], [11999, 8999], [12000, 9000]):
+        nl.copy_(_i32(lens))
+        want = [_want(x, bounds, unit, table, lens, 20, 16, 1, 1) for x in q]
+        for order in ((0, 1), (1, 0), (1, 1)):
+            for y in out:
+                y.fill_(-5)
+            for i in order:
+                graphs[i].replay()
+            for i in set(order):
+                assert torch.equal(out[i], want[i])
+            assert torch.equal(fa.select_pages(q[0], bounds, unit, table, nl, 20, 16, workspace=ws), want[0])
+
+
 def test_choice_refusals():
     g = torch.Generator(device="cuda").manual_seed(8)
     table, n = _table([400], 16, g)
