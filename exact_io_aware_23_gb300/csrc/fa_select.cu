@@ -8,9 +8,11 @@
 // the bounds' scale; the first and the last pages, which are always chosen, and scores that are NaN stand
 // above all others, and of equal ones the lower page is chosen.
 //
-// Scores.  A warp takes 32 pages at a time, eight to a product, their bounds the right operand of mma.sync as
-// they lie in memory, 16 rows' q the left one.  What bounds it: bytes, 2 d + 4 a page, for few pages the chain
-// of reads: lengths, table entry, bounds.
+// Scores.  A warp takes 32 pages at a time, their bounds operands of mma.sync as they lie in memory: eight pages the right
+// one and 16 rows' q the left one, or with up to 8 rows 16 pages the left one and the rows the right one, half the
+// products.  What bounds it: for many pages the rate of mma.sync, one of 16 x 8 x 16 in 17 cycles on a quarter of an SM
+// (64 sequences of 1024 pages, 8 key heads of 4 rows, d = 128, 136 MB: 40 us, with 16 rows' products 48), for
+// few pages the chain of reads: lengths, table entry, bounds.
 // Choice.  A block has a (sequence, key head), a slice: it keeps the scores in shared memory and narrows down the range
 // of the K-th largest one's bits, 1024 bins at a time.  The bins are laid over the range that the scores
 // have: by the bits from the top nearly all would meet in the few bins of their exponents.  What costs there
