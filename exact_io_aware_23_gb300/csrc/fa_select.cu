@@ -10,17 +10,18 @@
 //
 // Scores.  A warp takes 32 pages at a time, their bounds operands of mma.sync as they lie in memory: eight pages the right
 // one and 16 rows' q the left one, or with up to 8 rows 16 pages the left one and the rows the right one, half the
-// products.  What bounds it: for many pages the rate of mma.sync, one of 16 x 8 x 16 in 17 cycles on a quarter of an SM
-// (64 sequences of 1024 pages, 8 key heads of 4 rows, d = 128, 136 MB: 40 us, with 16 rows' products 48), for
-// few pages the chain of reads: lengths, table entry, bounds.
+// products.  What bounds it: for many pages the warps' own work, 12 instructions a product for sums and differences, and
+// DRAM: 64 sequences of 1024 pages, 8 key heads of 4 rows, d = 128, 136 MB, take 36 us with the choice, 3.7 TB/s, and 48
+// with products of 16 rows; for few pages the chain of reads: lengths, table entry, bounds.
 // Choice.  A block has a (sequence, key head), a slice: it keeps the scores in shared memory and narrows down the range
 // of the K-th largest one's bits, 1024 bins at a time.  The bins are laid over the range that the scores
 // have: by the bits from the top nearly all would meet in the few bins of their exponents.  What costs there
 // is not the bytes but instructions that come from cold caches: loops that are not unrolled, and queries converted once for
 // a block, took 64 sequences of up to 128 pages from 10.2 us to 8.6.
 // Where there are fewer of them than SMs, and many pages, a kernel of its own scores the pages on all SMs first.
-// Few slices: the block that comes last of those that score a slice chooses, in the same launch (two sequences of 8192 pages
-// and 8 key heads: 23.0 us in two launches, 22.5 in one; more slices would leave some SMs without a block).
+// Few slices: the block that comes last of those that score a slice chooses, in the same launch (two sequences of 8192
+// pages and 8 key heads: 23.0 us in two launches, 22.7 in one, one sequence of 1000 pages 10.6 and 9.1; more slices would
+// leave some SMs without a block).
 // (A cluster of 4 or 8 blocks for each instead, scores in the first one's shared memory: 32 and 36 us for two
 // sequences of 8192 pages and 8 key heads, in two kernels 23; clusters of 8 do not all find their SMs at once.
 // The choice launched as a dependent of the scores: 28.)
@@ -45,7 +46,7 @@ constexpr int kRows = 16;
 constexpr int kGroup = 8;                  // pages of a warp's product
 constexpr int kBins = 1024;
 constexpr int kScoreThreads = 128;         // of a block that only scores
-constexpr int kScoreCtas = 3;              // and such blocks on an SM
+constexpr int score_ctas(bool flip) { return flip ? 4 : 3; }     // and such blocks on an SM (flip: 64 sequences of 1024 pages 40 us with 3)
 constexpr int kJointThreads = 384;         // of a block that scores a share of the pages, one on an SM
 
 // c (16 x 8, fp32) += a (16 x 16) b (16 x 8)
@@ -325,7 +326,7 @@ __device__ __forceinline__ void score_slice(const SelectArgs& a, int b, int hk, 
 
 // Scores on all SMs: warp W of the grid takes slice W % slices, so that neighbours read neighbouring heads' bounds.
 template <int D, bool F16, bool kFlip>
-__global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const SelectArgs a, const int slots) {
+__global__ void __launch_bounds__(kScoreThreads, score_ctas(kFlip)) score_kernel(const SelectArgs a, const int slots) {
   const int warp = blockIdx.x * (kScoreThreads / 32) + threadIdx.x / 32, slices = a.B * a.Hkv;
   const int slice = warp % slices, slot = warp / slices;
   const int b = slice / a.Hkv, hk = slice % a.Hkv;
@@ -557,7 +558,8 @@ cudaError_t launch_one(const SelectArgs& a, cudaStream_t s) {
   kern<<<(unsigned)(a.B * a.Hkv), kThr, smem, s>>>(a);
   return cudaGetLastError();
 }
-// Few slices, of which each finds blocks on several SMs: they choose too.
+// Few slices, of which each finds blocks on several SMs: they choose too.  (64 slices of up to 4000 pages: 24 us in two
+// launches, 25.6 in one; 40 of up to 1250: 9.5 and 10.7.)
 bool select_jointly(int slices, int sms) { return 4 * slices <= sms; }
 
 template <int D, bool F16, bool kFlip>
@@ -578,7 +580,7 @@ cudaError_t launch_any(const SelectArgs& a, cudaStream_t s) {
   }
   // warps of a slice: all take the same number of pages, as many warps as the SMs hold
   const int blocks = (a.cache.max_pages + 31) / 32;
-  const int most = std::max(1, sms * kScoreCtas * (kScoreThreads / 32) / slices), each = (blocks + most - 1) / most;
+  const int most = std::max(1, sms * score_ctas(kFlip) * (kScoreThreads / 32) / slices), each = (blocks + most - 1) / most;
   const int slots = (blocks + each - 1) / each;
   const int grid = (slots * slices + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
   score_kernel<D, F16, kFlip><<<grid, kScoreThreads, 0, s>>>(a, slots);
@@ -589,9 +591,9 @@ cudaError_t launch_any(const SelectArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Whether the pages are scored by a kernel of its own: where slices are not many times the SMs, each with more pages
-// than a block scores while another launch begins (32 sequences of 1024 pages and 8 key heads: 36 us in one
-// kernel, 31 in two; 64 of up to 128 pages: 10 and 12).
+// Whether the pages are scored on all SMs before the choice: where slices are not many times the SMs, each with more pages
+// than a block scores while another launch begins (8 key heads of 4 rows, d = 128, 1024 pages: 32 sequences 28 us in one
+// kernel and 22 in two, 64 sequences 54 and 36).
 bool select_scores_first(int B, int Hkv, int max_pages, int picks) {
   int sms = 0;
   if (sm_count(&sms) != cudaSuccess || sms <= 0) sms = 152;        // GB300's when no device can be asked
