@@ -62,9 +62,12 @@ struct BwdLayout {
 // Per-kernel launch set-up made once per device and kept: the dynamic shared memory the kernel
 // is opted in to (raised when a launch asks for more) and its registers per thread, so that a
 // launch queries and sets nothing in the runtime once its device has seen the kernel (a short
-// call's host time is a visible part of its time).
+// call's host time is a visible part of its time).  The kernel's attribute and the amount kept here
+// change together, under the lock: a thread that asks for less never sets it below what another
+// one has been told that it holds.
 struct LaunchSetup {
   static constexpr int kDevices = 64;
+  std::mutex mu;
   std::atomic<int> smem[kDevices] = {};
   std::atomic<int> regs[kDevices] = {};
 };
@@ -92,12 +95,11 @@ cudaError_t prepare_launch(LaunchSetup& c, Kern kern, int smem, int* regs = null
   if (e != cudaSuccess) return e;
   const bool cached = dev >= 0 && dev < LaunchSetup::kDevices;
   if (!cached || c.smem[dev].load(std::memory_order_acquire) < smem) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (cached) {
-      int cur = c.smem[dev].load(std::memory_order_relaxed);
-      while (cur < smem && !c.smem[dev].compare_exchange_weak(cur, smem, std::memory_order_release)) {
-      }
+    const std::lock_guard<std::mutex> lock(c.mu);
+    if (!cached || c.smem[dev].load(std::memory_order_relaxed) < smem) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      if (cached) c.smem[dev].store(smem, std::memory_order_release);
     }
   }
   if (regs != nullptr) {
