@@ -875,10 +875,10 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
             s[e] = fmaf(slope[row_of(e)], ahead[row_of(e)] + (float)(key_of(e) - (C::kPick ? 16 * x : 0)), s[e]);
         }
       }
+      auto sees = [&](int e) { return key0[key_of(e) / 16] + key_of(e) % 16 + lane_key < limit[row_of(e)]; };
       if (hidden) {
 #pragma unroll
-        for (int e = 0; e < kScores; ++e)
-          s[e] = key0[key_of(e) / 16] + key_of(e) % 16 + lane_key < limit[row_of(e)] ? s[e] : -INFINITY;
+        for (int e = 0; e < kScores; ++e) s[e] = sees(e) ? s[e] : -INFINITY;
       }
       float share[C::k8 ? kParts : 1];                  // vs in the output's unit
       if constexpr (C::k8) {
@@ -924,9 +924,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
         }
 #pragma unroll
         for (int n8 = 0; n8 < kN; ++n8) {
-          // a scale that is NaN meets only the keys that the row sees
+          // a scale that is NaN meets the keys that the row sees, all of them, and no others
           const float f = share[n8 / 2];
-          const float f0 = hidden && s[2 * n8] == 0.f ? 0.f : f, f1 = hidden && s[2 * n8 + 1] == 0.f ? 0.f : f;
+          const float f0 = hidden && !sees(2 * n8) ? 0.f : f, f1 = hidden && !sees(2 * n8 + 1) ? 0.f : f;
           p[n8] = transposed(ptx::pack2<F16>(s[2 * n8] * f0, s[2 * n8 + 1] * f1));
         }
         const int key = lane & 15, part = lane >> 4;
@@ -972,9 +972,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
           const float p0 = ptx::ex2(s[4 * n8 + 2 * e] - sub), p1 = ptx::ex2(s[4 * n8 + 2 * e + 1] - sub);
           sum += p0 + p1;
           if constexpr (C::k8) {
-            // a scale that is NaN meets only the keys that the row sees
+            // a scale that is NaN meets the keys that the row sees, all of them, and no others
             const float f = share[n8 / 2];
-            const float f0 = hidden && p0 == 0.f ? 0.f : f, f1 = hidden && p1 == 0.f ? 0.f : f;
+            const float f0 = hidden && !sees(4 * n8 + 2 * e) ? 0.f : f, f1 = hidden && !sees(4 * n8 + 2 * e + 1) ? 0.f : f;
             p[n8 / 2][e + 2 * (n8 & 1)] = ptx::pack2<F16>(p0 * f0, p1 * f1);
           } else {
             p[n8 / 2][e + 2 * (n8 & 1)] = ptx::pack2<F16>(p0, p1);
