@@ -33,10 +33,12 @@
 // the codes become fp16 operands in registers, two to an instruction, and the products are those of fp16
 // pages: ks meets the scores of its 16 keys, vs the probabilities.  A bf16 query row is brought into
 // fp16's range by a power of two of its own, with its largest value at 2^14: values down to 2^-28 of it
-// keep all their bits, smaller ones an absolute error of 2^-39 of it.  Probabilities carry vs / u, where u is
-// the largest vs that the warp has met (raised, like the maximum, when a new one exceeds it by more than
-// 2^4), so that p vs / u stays below 2^12; what is rounded below fp16's normal range is off by
-// 2^-25 u at most.
+// keep all their bits, smaller ones an absolute error of 2^-39 of it.  The probabilities' products carry vs
+// too, and each row has a unit for them, 2^u with u a running maximum of s_ij + log2 vs_j, apart from the
+// running maximum of s_ij that goes with the sum l (both raised when a new value exceeds them by more than
+// 2^8).  So p vs / 2^u stays below 2^8, and what is rounded below fp16's normal range is off by
+// 2^-25 of the row's largest p vs at most: a page of large values that the row gives no weight takes nothing from the
+// others.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -73,7 +75,6 @@ constexpr int flip_ctas(int d) { return d == 128 ? 3 : 4; }
 constexpr int kSegment = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kUnitSlack = 16.0f;         // ... and the unit of the values' scales
 constexpr int kNowhere = 0x7f000000;       // the place of keys that do not exist: behind every row's
 constexpr float kRescaleLog2 = 8.0f;       // the running maximum is raised when a score exceeds it by more
 
@@ -761,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
     const int n = last_tile(s0, seg.tiles) - seg.tile;  // the CTA's tiles of the segment: at least one
     const int mine = (warp - turn + kWarps) % kWarps;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float unit_v = 0.f, inv_unit_v = 0.f;               // 8-bit pages: what the output counts
+    float u[2] = {-INFINITY, -INFINITY};                // 8-bit pages: what the output counts, a power of two's exponent
     // kFlip: o[j] are values 16 j + 2 r0 and the next one of rows c0 and c0 + 1
     constexpr int kOut = kFlip ? D / 16 : D / 8;
     float o[kOut][4];
@@ -880,23 +881,51 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
 #pragma unroll
         for (int e = 0; e < kScores; ++e) s[e] = sees(e) ? s[e] : -INFINITY;
       }
-      float share[C::k8 ? kParts : 1];                  // vs in the output's unit
-      if constexpr (C::k8) {
-        float top = meta[0].y;
+      // 8-bit pages: the largest of each row's scores with their values' scales raises the row's unit; then, of the
+      // keys of each part, by how much a probability counts in it
+      float gain[C::k8 ? kParts : 1][2];
+      auto raise_units = [&]() {
+        float w[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int x = 1; x < kParts; ++x) top = fmaxf(top, meta[x].y);
-        if (top > kUnitSlack * unit_v) {
-          const float up = fmaxf(top, 0x1p-120f), down = unit_v / up;
-          unit_v = up;
-          inv_unit_v = 1.f / up;
+        for (int x = 0; x < kParts; ++x) {
+          const float lg = __log2f(meta[x].y);          // (NaN raises nothing)
 #pragma unroll
-          for (int k = 0; k < kOut; ++k)
+          for (int e = 0; e < 2; ++e) {
+            float top = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[k][e] *= down;
+            for (int i = x * kScores / kParts; i < (x + 1) * kScores / kParts; ++i)
+              if (row_of(i) == e) top = fmaxf(top, s[i]);
+            w[e] = fmaxf(w[e], top + lg);
+          }
         }
+        if (!__any_sync(0xffffffffu, w[0] > u[0] + kRescaleLog2 || w[1] > u[1] + kRescaleLog2)) return;
 #pragma unroll
-        for (int x = 0; x < kParts; ++x) share[x] = meta[x].y * inv_unit_v;
-      }
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int d = kFlip ? 4 : 1; d < (kFlip ? 32 : 4); d <<= 1) w[e] = fmaxf(w[e], __shfl_xor_sync(0xffffffffu, w[e], d));
+          if (w[e] > u[e] + kRescaleLog2) {
+            const float beta = ptx::ex2(u[e] - w[e]);
+            u[e] = w[e];
+#pragma unroll
+            for (int k = 0; k < kOut; ++k)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) o[k][kFlip ? e + 2 * i : 2 * e + i] *= beta;
+          }
+        }
+      };
+      auto set_gains = [&]() {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // (far above where the largest score is one of values that are next to nothing)
+          const float r = u[e] == -INFINITY ? 0.f : ptx::ex2(fminf(m[e] - u[e], 100.f));
+#pragma unroll
+          for (int x = 0; x < kParts; ++x) {
+            const float f = meta[x].y * r;
+            gain[x][e] = f > 0x1p120f ? 0x1p120f : f;   // not infinite, for probabilities that are 0; NaN stays
+          }
+        }
+      };
+      if constexpr (C::k8) raise_units();
       if constexpr (kFlip) {
         uint32_t p[kN];                                 // the keys of group n, transposed: right operands
 #pragma unroll
@@ -910,11 +939,6 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
             const float alpha = ptx::ex2(m[e] - mx);    // 0 at the row's first key
             m[e] = mx;
             l[e] *= alpha;
-#pragma unroll
-            for (int k = 0; k < kOut; ++k) {
-              o[k][e] *= alpha;
-              o[k][2 + e] *= alpha;
-            }
           }
           const float sub = m[e] == -INFINITY ? 0.f : m[e];
 #pragma unroll
@@ -922,11 +946,12 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
 #pragma unroll
           for (int n8 = 0; n8 < kN; n8 += 2) l[e] += s[2 * n8 + e] + s[2 * n8 + 2 + e];
         }
+        set_gains();
 #pragma unroll
         for (int n8 = 0; n8 < kN; ++n8) {
           // a scale that is NaN meets the keys that the row sees, all of them, and no others
-          const float f = share[n8 / 2];
-          const float f0 = hidden && !sees(2 * n8) ? 0.f : f, f1 = hidden && !sees(2 * n8 + 1) ? 0.f : f;
+          const float* const f = gain[n8 / 2];
+          const float f0 = hidden && !sees(2 * n8) ? 0.f : f[0], f1 = hidden && !sees(2 * n8 + 1) ? 0.f : f[1];
           p[n8] = transposed(ptx::pack2<F16>(s[2 * n8] * f0, s[2 * n8 + 1] * f1));
         }
         const int key = lane & 15, part = lane >> 4;
@@ -959,10 +984,12 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
           const float alpha = ptx::ex2(m[e] - mx);      // 0 at the row's first key
           m[e] = mx;
           l[e] *= alpha;
+          if constexpr (!C::k8) {
 #pragma unroll
-          for (int k = 0; k < D / 8; ++k) {
-            o[k][2 * e] *= alpha;
-            o[k][2 * e + 1] *= alpha;
+            for (int k = 0; k < D / 8; ++k) {
+              o[k][2 * e] *= alpha;
+              o[k][2 * e + 1] *= alpha;
+            }
           }
         }
         const float sub = m[e] == -INFINITY ? 0.f : m[e];
@@ -972,15 +999,25 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
           const float p0 = ptx::ex2(s[4 * n8 + 2 * e] - sub), p1 = ptx::ex2(s[4 * n8 + 2 * e + 1] - sub);
           sum += p0 + p1;
           if constexpr (C::k8) {
-            // a scale that is NaN meets the keys that the row sees, all of them, and no others
-            const float f = share[n8 / 2];
-            const float f0 = hidden && !sees(4 * n8 + 2 * e) ? 0.f : f, f1 = hidden && !sees(4 * n8 + 2 * e + 1) ? 0.f : f;
-            p[n8 / 2][e + 2 * (n8 & 1)] = ptx::pack2<F16>(p0 * f0, p1 * f1);
+            s[4 * n8 + 2 * e] = p0;
+            s[4 * n8 + 2 * e + 1] = p1;
           } else {
             p[n8 / 2][e + 2 * (n8 & 1)] = ptx::pack2<F16>(p0, p1);
           }
         }
         l[e] += sum;
+      }
+      if constexpr (C::k8) {
+        set_gains();
+#pragma unroll
+        for (int n8 = 0; n8 < kN; ++n8)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // a scale that is NaN meets the keys that the row sees, all of them, and no others
+            const int i = 4 * n8 + 2 * e;
+            const float f = gain[n8 / 2][e], f0 = hidden && !sees(i) ? 0.f : f, f1 = hidden && !sees(i + 1) ? 0.f : f;
+            p[n8 / 2][e + 2 * (n8 & 1)] = ptx::pack2<F16>(s[i] * f0, s[i + 1] * f1);
+          }
       }
       {
         const int key = lane & 15, part = lane >> 4;
@@ -1030,6 +1067,12 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
     // the un-normalised output goes to the slot of the warp's last tile, free until its next one:
     // groups of 4 values, their place in a row of D turned by the row against bank conflicts
     if (mine < n) {
+      // 8-bit pages: a row's output, from its unit to the one that goes with its maximum
+      float unit_o[2] = {1.f, 1.f};
+      if constexpr (C::k8) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) unit_o[e] = m[e] == -INFINITY ? 1.f : ptx::ex2(u[e] - m[e]);
+      }
       const int last = take == 0 ? C::kStages - 1 : take - 1;
       if (lane == 0) from[warp] = warp * C::kRing + last * C::kStage;
       __syncwarp();                                     // all lanes have read the tile
@@ -1040,7 +1083,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             *reinterpret_cast<float2*>(to + e * D * 4 + ((4 * j + r0 / 2) ^ (c0 + e)) * 16 + (r0 & 1) * 8) =
-                make_float2(o[j][e] * unit_v, o[j][2 + e] * unit_v);
+                make_float2(o[j][e] * unit_o[e], o[j][2 + e] * unit_o[e]);
       } else if constexpr (!C::k8) {
 #pragma unroll
         for (int k = 0; k < D / 8; ++k) {
@@ -1056,8 +1099,8 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             *reinterpret_cast<float4*>(to + e * 8 * D * 4 + at4) =
-                make_float4(o[2 * j][2 * e] * unit_v, o[2 * j + 1][2 * e] * unit_v, o[2 * j][2 * e + 1] * unit_v,
-                            o[2 * j + 1][2 * e + 1] * unit_v);
+                make_float4(o[2 * j][2 * e] * unit_o[e], o[2 * j + 1][2 * e] * unit_o[e], o[2 * j][2 * e + 1] * unit_o[e],
+                            o[2 * j + 1][2 * e + 1] * unit_o[e]);
         }
       }
     }

@@ -530,9 +530,10 @@ fa_status fa_append_paged_store(const fa_paged_cache* cache, const fa_page_store
  *            sequence) entries of a list count; entries that are no page of the sequence (-1) see
  *            nothing.  Any order, each page once (one that is listed twice counts twice).
  * Within the chosen pages query t sees the keys j <= i as before.  dtype is that of q and o (bf16 or
- * fp16).  Products run on the codes as fp16 numbers, sums in fp32; P is rounded to fp16, at least to 2^-25 of
- * the largest value scale among the pages.  Workspace: fa_forward_paged_workspace_size with
- * max_keys = max_pages * page_size, or n_select * page_size where `pages` is given and that is less.
+ * fp16).  Products run on the codes as fp16 numbers, sums in fp32; P times the values' scales is rounded to
+ * fp16: each product to 2^-11 of itself, or to 2^-25 of its row's largest where that is more.  Workspace:
+ * fa_forward_paged_workspace_size with max_keys = max_pages * page_size, or n_select * page_size where
+ * `pages` is given and that is less.
  * Scales that are NaN show in the rows that see a key of their page.  Pages are chosen from tables of
  * less than 0x7f000000 tokens (FA_ERR_UNSUPPORTED beyond).
  */
