@@ -56,10 +56,18 @@ __device__ __forceinline__ uint32_t recode(uint32_t c, float ratio) {
   }
 }
 
-// x times a power of two, rounded down, also where the product is below fp32's range
-__device__ __forceinline__ int down(float x, float by) {
+// x / unit rounded down, exactly, for |x| up to 128 of any positive unit; by: 1 / unit, rounded.  What the
+// rounded product says is one too much or too little at most, and the signs of remainders, which their one rounding keeps, tell.
+__device__ __forceinline__ int down(float x, float unit, float by) {
   const int i = __float2int_rd(x * by);
-  return x < 0.f ? min(i, -1) : i;
+  return i + (fmaf(-(float)i, unit, x) < 0.f ? -1 : fmaf(-(float)(i + 1), unit, x) >= 0.f ? 1 : 0);
+}
+// A bound c, in whole numbers of `old`, in those of `unit`, rounded down in the same way.  unit is old or, where it grew, a
+// power of two, so that i * unit is exact.
+__device__ __forceinline__ int down_again(int c, float old, float unit, float ratio) {
+  if (old == unit) return c;
+  const int i = __float2int_rd((float)c * ratio);
+  return i + (fmaf((float)c, old, -((float)i * unit)) < 0.f ? -1 : fmaf((float)c, old, -((float)(i + 1) * unit)) >= 0.f ? 1 : 0);
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
@@ -396,13 +404,13 @@ __device__ __forceinline__ void write_page(const AppendArgs& a, const StoreArgs&
           hi[1] = i == 0 ? m.y : fmaxf(hi[1], m.y);
         }
         char2* const q = reinterpret_cast<char2*>(st.bounds + place * 2 * a.d) + x;
-        int c[4] = {down(lo[0], by), down(lo[1], by), -down(-hi[0], by), -down(-hi[1], by)};
+        int c[4] = {down(lo[0], unit, by), down(lo[1], unit, by), -down(-hi[0], unit, by), -down(-hi[1], unit, by)};
         if (w.kept > 0) {
           const char2 was_lo = q[0], was_hi = q[a.d / 2];
-          c[0] = min(c[0], down((float)was_lo.x, ratio));
-          c[1] = min(c[1], down((float)was_lo.y, ratio));
-          c[2] = max(c[2], -down(-(float)was_hi.x, ratio));
-          c[3] = max(c[3], -down(-(float)was_hi.y, ratio));
+          c[0] = min(c[0], down_again(was_lo.x, old_unit, unit, ratio));
+          c[1] = min(c[1], down_again(was_lo.y, old_unit, unit, ratio));
+          c[2] = max(c[2], -down_again(-was_hi.x, old_unit, unit, ratio));
+          c[3] = max(c[3], -down_again(-was_hi.y, old_unit, unit, ratio));
         }
         const uint32_t packed = pack_s8(c[0], c[1], c[2], c[3]);
         q[0] = make_char2((signed char)packed, (signed char)(packed >> 8));
