@@ -2,7 +2,9 @@
 //
 // For a query row q and a page whose keys lie between lo and hi in every one of the d values,
 //     q . k <= sum_i max(q_i lo_i, q_i hi_i) = 1/2 sum_i (q_i (hi_i + lo_i) + |q_i| (hi_i - lo_i))
-// for each of the page's keys.  With q in whole numbers of 2^f (8 bits, like lo and hi) all these are whole numbers,
+// for each of the page's keys.  (Bounds are those of the keys before they go to 8 bits.  Codes of int8 pages keep within
+// them, being rounded to the bounds' own whole numbers; one of an e4m3 page can lie outside by its rounding, 2^-4 of a
+// value.)  With q in whole numbers of 2^f (8 bits, like lo and hi) all these are whole numbers,
 // the operands exact in fp16 and the sum, below 2^23, in fp32, in any order: the choice does not depend on how
 // the work is cut up.  A page's score is the largest over the rows of its key head's group of that times 2^f times
 // the bounds' scale; the first and the last pages, which are always chosen, and scores that are NaN stand

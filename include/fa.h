@@ -506,11 +506,11 @@ fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, 
  *     need = the smallest 2^e, e >= -100, for which largest code * 2^e reaches every new value
  *     the page held tokens before (places below the first new one): max(its scale, need), and where that
  *     grew the codes of those tokens are multiplied by old / new and rounded again; otherwise need
- * Scales that a caller wrote itself may be any positive numbers.  Bounds grow in the same way (their
- * scale with 127 as the largest code), lower ones rounded down and upper ones up; they bound the keys as
- * they are before they go to 8 bits (16-bit pages: as stored).  A value that is not finite makes the scale
- * of its page and head NaN, and the bounds' scale with it, until a write begins the page anew; the
- * codes written there are 0.
+ * Scales that a caller wrote itself may be any positive numbers (values are then divided by them as products
+ * with the rounded reciprocal).  Bounds grow in the same way (their scale with 127 as the largest code), lower
+ * ones rounded down and upper ones up; they bound the keys as they are before they go to 8 bits (16-bit
+ * pages: as stored).  A value that is not finite makes the scale of its page and head NaN, and the bounds'
+ * scale with it, until a write begins the page anew; the codes written there are 0.
  * Several sequences must not write to one page.  Other arguments as in fa_append_paged; FA_ERR_INVALID_ARG
  * also where two of the scales are in one place.
  */
@@ -549,8 +549,11 @@ fa_status fa_forward_paged_store(const void* q, const fa_paged_cache* cache,
  * row in whole numbers of the smallest 2^f, f >= -100, that keeps them within +-127, rounded to the
  * nearest (ties to even), and lo, hi, s a page's bounds and their scale, the page's score is the largest of
  *     2^f * s * sum_i max(q'_i lo_i, q'_i hi_i)
- * over the existing new tokens and the query heads of the key head's group: what no key of the page exceeds
- * in its product with q'.  The sum is a whole number, computed exactly.
+ * over the existing new tokens and the query heads of the key head's group: what no key within the bounds exceeds
+ * in its product with q'.  The sum is a whole number, computed exactly, its products with 2^f and s in
+ * fp32.  Within the bounds are the page's keys before they went to 8 bits, and as they are held in 16-bit and
+ * int8 pages (under scales that the writes chose).  A key that an e4m3 page holds can lie outside by its
+ * rounding, up to 2^-4 of each value and 2^-9 of the page's scale.
  *   pages  : [B, Hkv, n_select] the chosen pages' numbers in the sequence, ascending, -1 behind them:
  *            the `first` first and the `last` last pages, then those with the highest scores; of
  *            equal ones, and where first + last exceeds n_select, the lower numbers.  All pages

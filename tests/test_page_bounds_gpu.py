@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import exact_io_aware_23_gb300 as fa
+from page_reference import STORES
 from test_paged_gpu import TYPES, _i32
 
 pytestmark = pytest.mark.gpu
@@ -83,3 +84,46 @@ def test_a_callers_scale_that_grows(turned):
     want = torch.stack((torch.floor(exact[:, :, 0]).clamp(max=0), torch.ceil(exact[:, :, 1]).clamp(min=0)), 2)
     want[:, :, 1, 7], want[:, :, 0, 9] = 127, -127
     assert torch.equal(kb[grew].double(), want[grew])
+
+
+@pytest.mark.parametrize("store", ["16", "int8", "e4m3"])
+@pytest.mark.parametrize("turned", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_keys_as_the_pages_hold_them(store, turned, d):
+    """Keys of 16-bit and int8 pages lie within their bounds as they are stored.  Those of e4m3 pages may lie outside by their
+    rounding: half a step, 2^-4 of the value, and where a code is below the normal range 2^-10 of the scale, each time that it
+    is rounded; scales at least double when they grow, so 2^-9 of the last one in all.  Then no key of a page that is not
+    chosen has a larger product with the rounded query than the scores of those that are, but for that."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    page, length, K = 16, 600, 9
+    n = -(-length // page)
+    kind = torch.bfloat16 if store == "16" else STORES[store]
+    kc, vc = (torch.zeros((n, 1, page, d), dtype=kind, device="cuda") for _ in range(2))
+    ks, vs = (None if store == "16" else torch.zeros((n, 1), device="cuda") for _ in range(2))
+    kb, bs = torch.zeros((n, 1, 2, d), dtype=torch.int8, device="cuda"), torch.zeros((n, 1), device="cuda")
+    table = torch.randperm(n, generator=g, device="cuda").to(torch.int32)[None]
+    k = (torch.randn((1, 1, length, d), generator=g, device="cuda") * torch.exp(torch.randn((1, 1, length, 1), generator=g, device="cuda"))).to(torch.bfloat16)
+    inv_freq = fa.rotary_frequencies(32)[0] if turned else None
+    cuts = [0, 1, 2, 9, 311, 312, 330, 331, 333, 340, 600]      # pages written in one go and token by token: scales that grow
+    for begin, end in zip(cuts, cuts[1:]):
+        fa.append_paged(k[:, :, begin:end], k[:, :, begin:end], kc, vc, table, _i32([end]), inv_freq=inv_freq, k_scales=ks, v_scales=vs,
+                        k_bounds=kb, bound_scales=bs)
+    at = table[0].long()
+    held = kc[at, 0].double() * (1.0 if ks is None else ks[at].double()[..., None])
+    there = (torch.arange(n * page, device="cuda") < length).reshape(n, page, 1)
+    lo, hi = (kb[at, 0, i].double() * bs[at].double() for i in (0, 1))
+    # the value before its rounding is within 1 / (1 - 2^-4) of the code's
+    excess = torch.zeros_like(held) if store != "e4m3" else 2.0 ** -4 / (1 - 2.0 ** -4) * held.abs() + 2.0 ** -9 * ks[at].double()[..., None]
+    outside = torch.maximum(lo[:, None] - held, held - hi[:, None]).masked_fill(~there, 0.0)
+    assert bool((outside <= excess).all())
+    assert bool((outside > 0.0).any()) == (store == "e4m3")
+    q = torch.randn((1, 1, 1, d), generator=g, device="cuda").to(torch.bfloat16)
+    pages = fa.select_pages(q, kb, bs, table, _i32([length]), K, page, first=0, last=0)[0, 0].long()
+    assert fa.check_device_status() == 0 and bool((pages >= 0).all())
+    unit = 2.0 ** np.ceil(np.log2(float(q.abs().max()) / 127.0))
+    rounded = torch.round(q[0, 0, 0].double() / unit)
+    scores = torch.maximum(rounded * lo, rounded * hi).sum(-1)
+    rest = torch.ones(n, dtype=torch.bool, device="cuda")
+    rest[pages] = False
+    products = ((held * rounded).sum(-1) - (excess * rounded.abs()).sum(-1)).masked_fill(~there[..., 0], -float("inf"))
+    assert float(products[rest].max()) <= float(scores[pages].min())
