@@ -497,7 +497,7 @@ template <typename T, int kStore, bool kTurn, bool kBounds>
 cudaError_t append_store(const AppendArgs& a, StoreArgs st, int sms, cudaStream_t s) {
   constexpr int kLarge = kTurn ? 256 : 512;                // a team of more tokens than 128 threads hold
   const int units = a.d / kUnit;
-  st.span = (a.T + a.cache.page_size - 2) / a.cache.page_size + 1;
+  st.span = (int)(((int64_t)a.T + a.cache.page_size - 2) / a.cache.page_size) + 1;
   const int64_t heads = (int64_t)a.B * st.span * 2 * a.Hkv;       // of all pages
   // the smallest team that holds the new tokens of any page
   const int most = std::min(a.cache.page_size, a.T);
