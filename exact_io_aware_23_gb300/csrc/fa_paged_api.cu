@@ -336,7 +336,7 @@ fa_status fa_assign_pages(int32_t* block_table, int64_t table_stride, int B, int
                           int64_t* slots, int32_t* positions, int T, void* stream) {
   if (B < 0 || max_pages < 0 || T < 0 || n_free < 0 || page_size <= 0 || table_stride < max_pages) return FA_ERR_INVALID_ARG;
   if (page_size % 16 != 0 || page_size > fa::kMaxPageSize) return FA_ERR_UNSUPPORTED;
-  if (B > 65535 || (int64_t)B * T > 0x7fffffff) return FA_ERR_UNSUPPORTED;
+  if (B > 65535 || (int64_t)B * T > 0x7fffffff - 4096) return FA_ERR_UNSUPPORTED;     // (the blocks' runs of tokens end behind T)
   if ((!block_table && B > 0 && max_pages > 0) || !free_pages || n_free == 0 || !free_state || !free_state_out)
     return FA_ERR_INVALID_ARG;
   if (B > 0 && (!old_lens || !new_lens || !lens || !q_lens || (T > 0 && (!slots || !positions)))) return FA_ERR_INVALID_ARG;

@@ -586,7 +586,8 @@ fa_status fa_select_pages(const void* q, const fa_paged_cache* cache, const fa_p
  *                or new_lens
  *   q_lens     : [B] new tokens of each sequence, max(0, new - old)
  *   slots      : [B, T] of the first T new tokens of each sequence, page * page_size + place in the page
- *   positions  : [B, T] and their places in the sequence; -1 in both where there is no token
+ *   positions  : [B, T] and their places in the sequence; -1 in both where there is no token.  B * T at most
+ *                2^31 - 4097 (FA_ERR_UNSUPPORTED)
  *   The outputs must not overlap one another, nor the inputs but as said.
  * All or nothing: when the free pages do not suffice, or a length lies outside [0, max_pages * page_size],
  * or the ring's state is none, the table and the ring stay as they are, lens = old_lens, q_lens = 0, slots

@@ -149,3 +149,9 @@ def test_host_tensors_are_refused():
         fa.select_pages(q, torch.zeros(2, 2, 2, 64, dtype=torch.int8), torch.zeros(2, 2), table, n, 1, 16)
     with pytest.raises(ValueError, match="CUDA tensor"):
         fa.assign_pages(table, n, n, n, n, 16)
+
+
+def test_assign_sizes_that_end_behind_31_bits():
+    for T in (2 ** 31 - 1, 2 ** 31 - 2047, 2 ** 31 - 4096):
+        assert assign(B=1, T=T) == UNSUPPORTED
+    assert assign(B=1, T=2 ** 31 - 4097, slots=None) == INVALID           # of a size that is looked at
