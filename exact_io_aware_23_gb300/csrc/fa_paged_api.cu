@@ -294,6 +294,7 @@ fa_status fa_select_pages(const void* q, const fa_paged_cache* cache, const fa_p
   if (st != FA_OK) return st;
   if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
   if (n_select < 0 || first < 0 || last < 0) return FA_ERR_INVALID_ARG;
+  if (n_select > 0x7fffffff - 4096) return FA_ERR_UNSUPPORTED;          // (threads' steps over a list end behind it)
   if (B == 0 || Hkv == 0 || n_select == 0) return FA_OK;
   if (!pages || !aligned(pages, 4)) return FA_ERR_INVALID_ARG;
   if (H == 0 || T == 0)                                     // no new tokens: -1 everywhere

@@ -564,8 +564,8 @@ fa_status fa_forward_paged_store(const void* q, const fa_paged_cache* cache,
  *            in flight at once need their own.  The size is 0 for many sequences and for short ones,
  *            which need none (workspace may be null).
  * A bounds' scale that is NaN counts above all scores; a query row that holds something not finite
- * has no say next to others.  max_pages at most 49152 (FA_ERR_UNSUPPORTED).  Lengths and entries as in
- * fa_append_paged.
+ * has no say next to others.  max_pages at most 49152, n_select at most 2^31 - 4097 (FA_ERR_UNSUPPORTED).
+ * Lengths and entries as in fa_append_paged.
  */
 size_t fa_select_pages_workspace_size(int B, int Hkv, int max_pages, int n_select);
 fa_status fa_select_pages(const void* q, const fa_paged_cache* cache, const fa_page_store* store,

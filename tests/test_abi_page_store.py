@@ -155,3 +155,9 @@ def test_assign_sizes_that_end_behind_31_bits():
     for T in (2 ** 31 - 1, 2 ** 31 - 2047, 2 ** 31 - 4096):
         assert assign(B=1, T=T) == UNSUPPORTED
     assert assign(B=1, T=2 ** 31 - 4097, slots=None) == INVALID           # of a size that is looked at
+
+
+def test_lists_that_end_behind_31_bits():
+    for n in (2 ** 31 - 1, 2 ** 31 - 4096):
+        assert select(n=n) == UNSUPPORTED
+    assert select(n=2 ** 31 - 4097, q=None) == INVALID                     # of a length that is looked at
