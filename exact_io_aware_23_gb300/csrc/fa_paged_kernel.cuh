@@ -197,7 +197,7 @@ __device__ __forceinline__ int entries_of(const PagedArgs& a, int len) {
 template <typename C>
 __device__ __forceinline__ int tiles_in(const PagedArgs& a, int len) {
   if constexpr (C::kPick) return (entries_of(a, len) * (int)a.page_parts + C::kParts - 1) / C::kParts;
-  else return (len + C::kKeys - 1) / C::kKeys;
+  else return (int)(((uint32_t)len + C::kKeys - 1) / C::kKeys);      // (a length may end within a tile of 2^31)
 }
 template <typename C>
 __device__ __forceinline__ int tiles_of(const PagedArgs& a, int b, int* err) {
@@ -842,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
 #pragma unroll
       for (int x = 0; x < kParts; ++x) {
         key0[x] = C::kPick ? __float_as_int(meta[x].z) : (seg.tile + i) * kKeys + x * 16;
-        hidden = hidden || key0[x] + 16 > full;
+        hidden = hidden || key0[x] > full - 16;
       }
       if constexpr (C::k8) {
         const float c = a.score.cap_log2 == 0.f ? c_log2 : 1.f;

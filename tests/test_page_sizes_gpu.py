@@ -48,3 +48,28 @@ def test_a_call_sized_for_many_tokens_writes_the_few_there_are(T):
 def test_more_sequences_than_blocks_place(B, T):
     choice.test_pages_are_assigned([(7 * i) % 90 for i in range(B)], [(11 * i) % 90 for i in range(B)], 16, T)
     choice.test_pages_are_assigned([(5 * i) % 40 for i in range(B)], [(5 * i) % 40 + i % (T + 2) for i in range(B)], 16, T)
+
+
+@pytest.mark.parametrize("kind,d,H,T", [("int8", 64, 4, 1), ("int8", 64, 24, 1), ("e4m3", 128, 4, 2), ("bf16", 64, 4, 1), ("bf16", 128, 4, 1)])
+def test_lengths_up_to_the_last_ones_of_31_bits(kind, d, H, T):
+    """2^31 - 16 keys and a few less, one page of 4096 named again and again: each of its keys counts as often as it is
+    seen.  A lane adds the sums of at most 2^31 / (32 * 608) = 110000 tiles in turn (152 SMs, 4 warps each at least):
+    2^-24 of the sum each time, 0.7 % in all."""
+    g = torch.Generator(device="cuda").manual_seed(d + H)
+    raw = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn, "bf16": torch.bfloat16}[kind]
+    kc, vc = ((torch.randint(-60, 61, (1, 1, 4096, d), generator=g, device="cuda") / (64 if kind == "bf16" else 1)).to(raw) for _ in range(2))
+    scales = {} if kind == "bf16" else dict(zip(("k_scales", "v_scales"), torch.full((2, 1, 1), 1 / 64, device="cuda")))
+    table = torch.zeros((1, 2 ** 31 // 4096), dtype=torch.int32, device="cuda")
+    q = torch.randn((1, H, T, d), generator=g, device="cuda").to(torch.bfloat16)
+    k, v = (c[0, 0].double() / (1 if kind == "bf16" else 64) for c in (kc, vc))
+    for length in (2 ** 31 - 16, 2 ** 31 - 17, 2 ** 31 - 64, 2 ** 31 - 2100):
+        o, lse = fa.forward_paged(q, kc, vc, table, _i32([length]), **scales)
+        assert fa.check_device_status() == 0
+        for t in range(T):
+            seen = length - T + t + 1
+            times = torch.where(torch.arange(4096, device="cuda") < seen % 4096, seen // 4096 + 1, seen // 4096).double()
+            x = q[0, :, t].double() @ k.T / d ** 0.5 + torch.log(times)
+            want = torch.logsumexp(x, -1)
+            p = torch.exp(x - want[:, None])
+            assert bool(((lse[0, :, t].double() - want).abs() <= 8e-3).all())
+            assert bool(((o[0, :, t].double() - p @ v).abs() <= 2.0 ** -8 * (p @ v).abs() + 0.02 * (p @ v.abs())).all())
