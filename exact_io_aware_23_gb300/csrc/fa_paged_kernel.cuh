@@ -44,6 +44,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 
 #include <type_traits>
@@ -762,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
     const int n = last_tile(s0, seg.tiles) - seg.tile;  // the CTA's tiles of the segment: at least one
     const int mine = (warp - turn + kWarps) % kWarps;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float u[2] = {-INFINITY, -INFINITY};                // 8-bit pages: what the output counts, a power of two's exponent
+    float u[2] = {-FLT_MAX, -FLT_MAX};                  // 8-bit pages: what the output counts, a power of two's exponent
     // kFlip: o[j] are values 16 j + 2 r0 and the next one of rows c0 and c0 + 1
     constexpr int kOut = kFlip ? D / 16 : D / 8;
     float o[kOut][4];
@@ -883,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
       }
       // 8-bit pages: the largest of each row's scores with their values' scales raises the row's unit; then, of the
       // keys of each part, by how much a probability counts in it
-      float gain[C::k8 ? kParts : 1][2];
+      float gain[C::k8 ? kParts : 1][2], top[2] = {-INFINITY, -INFINITY};
       auto raise_units = [&]() {
         float w[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -891,11 +892,12 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
           const float lg = __log2f(meta[x].y);          // (NaN raises nothing)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = -INFINITY;
+            float t = -INFINITY;
 #pragma unroll
             for (int i = x * kScores / kParts; i < (x + 1) * kScores / kParts; ++i)
-              if (row_of(i) == e) top = fmaxf(top, s[i]);
-            w[e] = fmaxf(w[e], top + lg);
+              if (row_of(i) == e) t = fmaxf(t, s[i]);
+            top[e] = fmaxf(top[e], t);
+            w[e] = fmaxf(w[e], t + lg);
           }
         }
         if (!__any_sync(0xffffffffu, w[0] > u[0] + kRescaleLog2 || w[1] > u[1] + kRescaleLog2)) return;
@@ -917,12 +919,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           // (far above where the largest score is one of values that are next to nothing)
-          const float r = u[e] == -INFINITY ? 0.f : ptx::ex2(fminf(m[e] - u[e], 100.f));
+          const float r = ptx::ex2(fminf(m[e] - u[e], 100.f));
 #pragma unroll
-          for (int x = 0; x < kParts; ++x) {
-            const float f = meta[x].y * r;
-            gain[x][e] = f > 0x1p120f ? 0x1p120f : f;   // not infinite, for probabilities that are 0; NaN stays
-          }
+          for (int x = 0; x < kParts; ++x) gain[x][e] = ptx::min_nan(meta[x].y * r, 0x1p120f);   // finite, for probabilities that are 0
         }
       };
       if constexpr (C::k8) raise_units();
@@ -930,9 +929,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
         uint32_t p[kN];                                 // the keys of group n, transposed: right operands
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(s[e], s[2 + e]);
-#pragma unroll
-          for (int n8 = 2; n8 < kN; n8 += 2) mx = ptx::max3(mx, s[2 * n8 + e], s[2 * n8 + 2 + e]);
+          float mx = top[e];
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
           if (mx > m[e] + kRescaleLog2) {               // false while the row is empty
@@ -975,9 +972,12 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
       uint32_t p[kParts][4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float mx = fmaxf(s[2 * e], s[2 * e + 1]);
+        float mx = top[e];
+        if constexpr (!C::k8) {
+          mx = fmaxf(s[2 * e], s[2 * e + 1]);
 #pragma unroll
-        for (int n8 = 1; n8 < kN; ++n8) mx = ptx::max3(mx, s[4 * n8 + 2 * e], s[4 * n8 + 2 * e + 1]);
+          for (int n8 = 1; n8 < kN; ++n8) mx = ptx::max3(mx, s[4 * n8 + 2 * e], s[4 * n8 + 2 * e + 1]);
+        }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         if (mx > m[e] + kRescaleLog2) {                 // false while the row is empty
