@@ -1,7 +1,7 @@
 // The write of new tokens into 8-bit pages, and into pages whose key bounds are kept.
 //
 // All new tokens of a page and head share what is computed for it, so the work goes by pages: a team (a
-// warp for a few new tokens, a block for many) takes one page of one sequence and walks over heads.
+// warp for a few new tokens, a block for many) takes one page of one sequence and one head, of its keys or values.
 //
 //     amax = max |x| over the page's new tokens,  need = the smallest 2^e, e >= -100, with amax <= largest 2^e
 //     scale' = max(scale, need) (need alone where the page held no token before)
@@ -466,8 +466,10 @@ __device__ __forceinline__ void turn_queries(const AppendArgs& a, const StoreArg
 }
 
 // kThr threads a block, teams of kTeam.  Turned keys take registers: fewer blocks on an SM.  Otherwise as many as there can be,
-// though 72 registers spill four words: 4 ragged prompts of up to 4096 tokens at d = 128, int8 and bounds, 21.3 us with five
-// blocks, 19.2 with six, 18.8 with seven; without bounds 16.7 with six and 15.2 with seven.
+// though 72 registers spill four words, and six where 8-bit pages have bounds: 4 ragged prompts of up to 4096 tokens at d = 128,
+// int8 and bounds, 21.5 us with five blocks, 19.5 with six, 19.1 with seven; without bounds 17.1 with six and 15.6 with seven;
+// e4m3 and bounds at d = 64 17.8, 16.3 and 15.6.  Most spilled, 24 words at 128 registers, are those of the warps that turn
+// keys for 8-bit pages without bounds (a decoding step): 64 tokens take 5.06 us, and 4.99 with 168 registers and none spilled.
 template <typename T, int kStore, bool kTurn, bool kBounds, int kTeam, int kThr>
 __global__ void __launch_bounds__(kThr, (kTurn && kBounds ? 384 : kTurn ? 512 : kTeam == 32 && kBounds ? 640 : kTeam == 128 ? 896 : 768) / kThr)
     append_store_kernel(const AppendArgs a, const StoreArgs st) {
