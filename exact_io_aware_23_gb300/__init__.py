@@ -788,7 +788,7 @@ def append_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     The pages are of k's type, or int8 or float8_e4m3fn with k_scales and v_scales (float32 [n_pages, Hkv],
     a power of two for each page and head, written too; what they hold of pages without tokens does not
     matter).  k_bounds (int8 [n_pages, Hkv, 2, d]) and bound_scales (float32 [n_pages, Hkv]): bounds of
-    each page's keys for ``select_pages``, kept when given (fa_append_paged_store)."""
+    each page's keys, before they go to 8 bits, for ``select_pages``, kept when given (fa_append_paged_store)."""
     dev = _current_device(k)
     if (dev < 0 or v.get_device() != dev or k_cache.get_device() != dev or v_cache.get_device() != dev
             or block_table.get_device() != dev or kv_lens.get_device() != dev
@@ -1073,8 +1073,8 @@ def select_pages(q: torch.Tensor, k_bounds: torch.Tensor, bound_scales: torch.Te
                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """fa_select_pages: for each sequence and key head the n_select pages whose key bounds promise the
     highest scores to its new tokens q [B, H, T, d] (contiguous, bf16 or fp16; rotated like the keys),
-    the first and the last ones among them: int32 [B, Hkv, n_select], ascending, -1 behind.  k_bounds and
-    bound_scales as ``append_paged`` keeps them; block_table, kv_lens and q_lens as there."""
+    the first and the last ones among them: int32 [B, Hkv, n_select], ascending, -1 behind.  (For this q goes to
+    whole numbers of 8 bits, row by row.)  k_bounds and bound_scales as ``append_paged`` keeps them; block_table, kv_lens and q_lens as there."""
     dev = _current_device(q)
     if (dev < 0 or block_table.get_device() != dev or kv_lens.get_device() != dev
             or (q_lens is not None and q_lens.get_device() != dev)):

@@ -919,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) paged_kernel(const Pa
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           // (far above where the largest score is one of values that are next to nothing)
-          const float r = ptx::ex2(fminf(m[e] - u[e], 100.f));
+          const float r = ptx::ex2(fminf(m[e] - u[e], 126.f));
 #pragma unroll
           for (int x = 0; x < kParts; ++x) gain[x][e] = ptx::min_nan(meta[x].y * r, 0x1p120f);   // finite, for probabilities that are 0
         }

@@ -490,8 +490,9 @@ fa_status fa_append_paged(const fa_paged_cache* cache, const void* k, const int6
  * every call.  Nothing that a page holds behind a sequence's last token enters the result; NaN in a
  * query, or in a key that it sees, makes its row of O and its LSE NaN.  bf16 or fp16.  Lengths and
  * table entries outside their contract as in fa_append_paged (such a sequence's result is then
- * unspecified).  The work is sized for few new tokens: every 16 query rows of a group (H / Hkv * T)
- * read the cache once more.
+ * unspecified).  Sums of P (up to 2^8) times values run in fp32 and are divided at the end: the largest
+ * |value| times the number of keys has to stay below 2^120.  The work is sized for few new tokens: every 16
+ * query rows of a group (H / Hkv * T) read the cache once more.
  */
 size_t fa_forward_paged_workspace_size(int B, int H, int Hkv, int T, int d, int max_keys);
 fa_status fa_forward_paged(const void* q, const fa_paged_cache* cache, void* o, float* lse, int B,

@@ -104,3 +104,21 @@ def test_values_of_no_size_at_the_heaviest_key(store, H):
         o, lse = fa.forward_paged(q, kc, vc, table, _i32([304]), k_scales=ks, v_scales=vs, alibi_slopes=torch.full((H,), slope, device="cuda"))
         _check(q, kc, vc, ks, vs, 304, o, lse, slope)
         assert slope < 1.0 or not bool(o.any())
+
+
+@pytest.mark.parametrize("store", ["int8", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,T", [(4, 1), (24, 1), (8, 5)])
+def test_the_smallest_and_the_largest_scales(store, d, H, T):
+    """All values as small as scales from 2^-100 on make them (and somewhat smaller), or as large as they may be: sums of P (up
+    to 2^8) times values run in fp32 before they are divided, so 2^8 times 1500 keys times 2^8 codes of scales up to 2^98
+    stays below 2^128.  (Scales of 2^114 do not.)"""
+    g = torch.Generator(device="cuda").manual_seed(d + H)
+    for shift in (2.0 ** -90, 2.0 ** -94, 2.0 ** -106, 2.0 ** 100):     # of scales around 2^-6
+        for length, slope in ((300, 0.0), (1500, 0.1), (33, 0.0)):
+            kc, vc, ks, vs, table, q = _inputs(store, d, "bf16", H, 1, T, length, g)
+            vs *= shift
+            o, lse = fa.forward_paged(q, kc, vc, table, _i32([length]), k_scales=ks, v_scales=vs,
+                                      alibi_slopes=torch.full((H,), slope, device="cuda") if slope else None)
+            assert fa.check_device_status() == 0
+            _check(q, kc, vc, ks, vs, length, o, lse, slope)
