@@ -73,3 +73,36 @@ def test_lengths_up_to_the_last_ones_of_31_bits(kind, d, H, T):
             p = torch.exp(x - want[:, None])
             assert bool(((lse[0, :, t].double() - want).abs() <= 8e-3).all())
             assert bool(((o[0, :, t].double() - p @ v).abs() <= 2.0 ** -8 * (p @ v).abs() + 0.02 * (p @ v.abs())).all())
+
+
+def test_choices_of_two_host_threads():
+    """Small and large tables chosen from at once, on streams of their own: each thread's kernels find the shared memory that
+    they ask for."""
+    import threading
+    g = torch.Generator(device="cuda").manual_seed(5)
+    work = []
+    for length in (16 * 600, 16 * 40000, 16 * 30, 16 * 9000):
+        table, n = choice._table([length], 16, g)
+        bounds, unit = choice._bounds(n, 1, 64, g)
+        q = torch.randn((1, 20, 1, 64), generator=g, device="cuda").to(torch.float16)      # 20 rows: kernels that few calls use
+        work.append((q, bounds, unit, table, _i32([length]), choice._want(q, bounds, unit, table, [length], 12, 16, 1, 1)))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(order):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for i in order * 30:
+                q, bounds, unit, table, lens, want = work[i]
+                try:
+                    if not torch.equal(fa.select_pages(q, bounds, unit, table, lens, 12, 16), want):
+                        wrong.append(i)
+                except fa.FaError as e:
+                    wrong.append(str(e))
+
+    threads = [threading.Thread(target=run, args=(order,)) for order in ([0, 2, 1, 3], [1, 3, 0, 2], [3, 0, 2, 1])]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == [] and fa.check_device_status() == 0
